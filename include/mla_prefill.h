@@ -562,6 +562,190 @@ mla_status_t mla_decode(void* out, float* lse, const void* q, const uint32_t* in
                         void* workspace, size_t workspace_bytes, int32_t* d_status,
                         mla_stream_t stream);
 
+/*
+ * The 8-bit latent cache.  The pages have no counterpart to it: their fp8
+ * paths take one scale for the whole cache.
+ *
+ * kv_cache:  [num_pages][page_size][576] e4m3 codes (512 latent, 64 rope), as
+ *            for MLA_E4M3 above
+ * kv_scales: [num_pages][page_size / scale_block] float32: slots
+ *            [i * scale_block, (i + 1) * scale_block) of a page share scale i,
+ *            real value = code * scale.  scale_block must divide page_size and
+ *            be 1 (a scale for each token) to 128.
+ * A scale is a power of two, the smallest s with |value| <= 448 s for the
+ * values of its block, between 2^-60 and 2^120.
+ *
+ * mla_latent_cache_write_q8: mla_latent_cache_write into that cache (same
+ * arguments, rows, rotations and errors; kv_inv_scale has no counterpart, the
+ * scales are found).  A call fills a block from some slot on:
+ *   - from its first slot: the block's scale is set from the new rows alone;
+ *   - from a later slot (the rows before are earlier tokens' of the sequence):
+ *     the scale grows if the new rows need it, never shrinks, and when it grows
+ *     the rows before are requantised, old code * old / new rounded to the
+ *     nearest e4m3 (exact but below e4m3's normal range).  An old scale that is
+ *     not a positive finite number is replaced and the rows before are left.
+ * Slots behind the new rows keep their codes and read as code * the new scale:
+ * they are rows to be written later.  Two sequences must not share a block that
+ * a call writes to.  A NaN value is stored as a NaN code and takes no part in
+ * the scale; an infinite one makes the scale 2^120 and is stored as 448.
+ * Host errors: MLA_ERR_ARG as mla_latent_cache_write, and for a null kv_scales
+ * or a scale_block that does not divide page_size or is outside 1..128.
+ */
+mla_status_t mla_latent_cache_write_q8(void* kv_cache, float* kv_scales, void* q, const void* kv_latent,
+                                       const float* kv_norm_gamma, const float* freqs_cis,
+                                       const uint32_t* input_row_offsets, const uint32_t* cache_lengths,
+                                       const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                                       int32_t max_pages_per_seq, int32_t scale_block, int32_t batch_size,
+                                       int32_t num_heads, int32_t total_q_tokens, int32_t max_seq_len,
+                                       float epsilon, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * mla_gather_latent out of the 8-bit cache: c_kv_buf [buffer_token_size][512]
+ * and k_rope_buf [buffer_token_size][64] receive code * scale as bf16 (exact
+ * for the scales that mla_latent_cache_write_q8 stores, within bf16's range;
+ * rounded to nearest even otherwise), ready for mla_upproject and
+ * mla_prefill_attention in bf16.  Other arguments, rows and errors as
+ * mla_gather_latent ("mla_prefill_decode_graph_bf16", Parameters: kv_input_fn).
+ */
+mla_status_t mla_gather_latent_q8(void* c_kv_buf, void* k_rope_buf, const void* kv_cache,
+                                  const float* kv_scales, const int32_t* page_table, int32_t num_pages,
+                                  int32_t page_size, int32_t max_pages_per_seq, int32_t scale_block,
+                                  const uint32_t* buffer_row_offsets, const uint32_t* cache_offsets,
+                                  const int32_t* buffer_lengths, int32_t chunk, int32_t batch_size,
+                                  uint32_t buffer_token_size, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * mla_prefill over the 8-bit cache: the same plan and chunk loop with
+ * mla_gather_latent_q8 in place of the gather and everything after it in bf16
+ * (q, w_k, w_uv and out are bf16).  Workspace: mla_prefill_workspace_bytes(...,
+ * MLA_BF16).  Errors as mla_prefill, and MLA_ERR_ARG for kv_scales or
+ * scale_block as above.  Follows "mla_prefill_decode_graph_bf16".
+ */
+mla_status_t mla_prefill_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                            const uint32_t* cache_lengths, const void* kv_cache, const float* kv_scales,
+                            const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                            int32_t max_pages_per_seq, int32_t scale_block, const void* w_k,
+                            const void* w_uv, int32_t batch_size, int32_t num_heads,
+                            int32_t total_q_tokens, int32_t max_prompt_len, uint32_t buffer_token_size,
+                            int32_t max_chunks, float scale, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, mla_stream_t stream);
+
+/*
+ * Partitions a sequence that mla_decode_q8 uses when num_partitions is 0, and
+ * the workspace it needs, as mla_decode_partitions and
+ * mla_decode_workspace_bytes are for mla_decode (no counterpart on the pages).
+ */
+int32_t mla_decode_q8_partitions(int32_t batch_size, int32_t num_heads, int32_t max_new_tokens,
+                                 int32_t max_keys);
+/* The pages size no buffer: no counterpart. */
+size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, int32_t num_partitions);
+
+/*
+ * mla_decode over the 8-bit cache (the decode branch of
+ * "mla_prefill_decode_graph_bf16"; its cache is bf16 there): the same
+ * definition with c_kv_j and k_rope_j = code * scale of their row.  kv_scales
+ * may hold any positive finite numbers.  Arguments, sparse lists, sinks and lse
+ * as in mla_decode; q, w_uk, w_uv and out are bf16.
+ * To give every token a list of its own, pass each token as a sequence of one
+ * (batch_size = total_q_tokens, input_row_offsets = 0, 1, 2, ...; in the sparse
+ * form cache_lengths and page_table are not used).
+ * Rounding: the projected query and the softmax weights are each held as the
+ * sum of two e4m3 values (within 2^-8, 0.4 of a bf16 rounding's mean error),
+ * partial results as fp16, the merged latent result as two bf16 terms; scores,
+ * sums and the merge run in fp32.
+ * Rows of out (and lse) of tokens outside every sequence, or of a sequence that
+ * is left out, are not written.
+ * max_seq_len bounds the contexts (dense form).
+ * Errors: host MLA_ERR_GEOMETRY, MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH
+ * as mla_decode, MLA_ERR_ARG for kv_scales or scale_block as above and for more
+ * than 16383 heads.  Device MLA_DEV_BAD_OFFSETS (input_row_offsets[b+1] >
+ * total_q_tokens, or a dense context longer than max_seq_len: sequence b left
+ * out), MLA_DEV_BAD_PAGE (a page id or listed row out of range: the result of
+ * the rows that see it is not meaningful), MLA_DEV_TIMEOUT.
+ */
+mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                           const uint32_t* cache_lengths, const void* kv_cache, const float* kv_scales,
+                           const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                           int32_t max_pages_per_seq, int32_t scale_block, const void* w_uk, const void* w_uv,
+                           int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                           int32_t max_new_tokens, int32_t max_seq_len, int32_t num_partitions, float scale,
+                           const int32_t* d_indices, int32_t indices_stride, const int32_t* topk_lengths,
+                           const float* attn_sink, void* workspace, size_t workspace_bytes,
+                           int32_t* d_status, mla_stream_t stream);
+
+/*
+ * A score of every block of keys for every new token, from small index keys:
+ * what picks the row lists of the sparse decode calls.  The pages take the
+ * lists ("mla_prefill_decode_graph_bf16", Args: d_indices, topk_lengths) and
+ * have no counterpart to making them.
+ *
+ * New token i of sequence b (row t = input_row_offsets[b] + i) sits at position
+ * P = cache_lengths[b] + i and sees keys j <= P.  Block x holds the positions
+ * [x * block, (x + 1) * block).
+ *   scores[t][x] = max over j in block x, j <= P, of
+ *                  s_j * sum_h index_w[t][h] * max(index_q[t][h] . k_j, 0)
+ * and -infinity for blocks without a visible key, up to scores_stride.  fp32
+ * accumulation.  NaN products give a NaN score.
+ *
+ * scores:       [total_q_tokens][scores_stride] float32, output;
+ *               scores_stride * block >= max_seq_len
+ * index_q:      [total_q_tokens][num_index_heads][128] bf16 or e4m3 (dtype)
+ * index_w:      [total_q_tokens][num_index_heads] float32, any sign (a scale of
+ *               index_q goes into it)
+ * index_cache:  [num_pages][page_size][128] in the same type, index keys of the
+ *               context under the same page ids as the latent cache (the new
+ *               tokens' included)
+ * index_scales: [num_pages * page_size] float32, the keys' scales s_j, or NULL
+ *               for 1
+ * block:        1, 2, 4, ... 128 keys
+ * max_new_tokens, max_seq_len: largest new-token count and context of any
+ *               sequence
+ * index_q and index_cache must be 16-byte aligned.
+ * Errors: host MLA_ERR_DTYPE, MLA_ERR_GEOMETRY (num_index_heads outside
+ * 1..128), MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS
+ * (input_row_offsets[b+1] > total_q_tokens or a context longer than
+ * max_seq_len: sequence b left out), MLA_DEV_BAD_PAGE (the block's score is not
+ * meaningful), MLA_DEV_TIMEOUT.  Rows of tokens outside every sequence are not
+ * written, nor are tokens past max_new_tokens of their sequence.
+ */
+mla_status_t mla_index_scores(float* scores, const void* index_q, const float* index_w, const void* index_cache,
+                              const float* index_scales, const uint32_t* input_row_offsets,
+                              const uint32_t* cache_lengths, const int32_t* page_table, int32_t num_pages,
+                              int32_t page_size, int32_t max_pages_per_seq, int32_t block, int32_t batch_size,
+                              int32_t num_index_heads, int32_t total_q_tokens, int32_t max_new_tokens,
+                              int32_t max_seq_len, int32_t scores_stride, int32_t dtype, int32_t* d_status,
+                              mla_stream_t stream);
+
+/*
+ * The best blocks of every new token, as physical cache rows: the d_indices
+ * and topk_lengths of mla_decode and mla_decode_q8 ("mla_prefill_decode_graph_bf16",
+ * Args: d_indices, indices_stride, topk_lengths), a list for each token.
+ *
+ * Token t sees nb = P / block + 1 blocks.  The last num_local of them are always
+ * chosen; the others by scores[t][x], larger first, equal ones lowest x first
+ * (NaN counts as -infinity, -0 equals 0), min(top_blocks, nb) blocks in all.
+ * indices[t] lists, in position order, page_table[b][j / page_size] * page_size
+ * + j % page_size of every chosen block's positions j <= P; counts[t] of them,
+ * the rest of the row -1.
+ *
+ * indices: [total_q_tokens][indices_stride] int32, output; indices_stride >=
+ *          top_blocks * block
+ * counts:  [total_q_tokens] int32, output
+ * scores:  [total_q_tokens][scores_stride] float32; scores_stride * block >=
+ *          max_seq_len
+ * num_local: 0 .. top_blocks
+ * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS (as
+ * above), MLA_DEV_BAD_PAGE (that entry is -1).  Rows of tokens outside every
+ * sequence are not written.
+ */
+mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* scores,
+                              const uint32_t* input_row_offsets, const uint32_t* cache_lengths,
+                              const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                              int32_t max_pages_per_seq, int32_t block, int32_t top_blocks, int32_t num_local,
+                              int32_t batch_size, int32_t total_q_tokens, int32_t max_seq_len,
+                              int32_t scores_stride, int32_t indices_stride, int32_t* d_status,
+                              mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,20 @@ SIGNATURES = {
     "mla_decode_workspace_bytes": (_Z, [_I, _I, _I]),
     "mla_decode": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I,
                         _F, _P, _I, _P, _P, _I, _P, _Z, _P, _P]),
+    "mla_latent_cache_write_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                       _I, _I, _F, _P, _P]),
+    "mla_gather_latent_q8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _U, _P,
+                                  _P]),
+    "mla_prefill_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _I,
+                            _U, _I, _F, _P, _Z, _P, _P]),
+    "mla_decode_q8_partitions": (_I, [_I, _I, _I, _I]),
+    "mla_decode_q8_workspace_bytes": (_Z, [_I, _I, _I]),
+    "mla_decode_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _I,
+                           _I, _I, _F, _P, _I, _P, _P, _P, _Z, _P, _P]),
+    "mla_index_scores": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                              _I, _I, _P, _P]),
+    "mla_index_select": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                              _P, _P]),
 }
 
 _lib = None
@@ -280,6 +294,84 @@ def mla_decode(out, lse, q, input_row_offsets, cache_lengths, kv_cache, page_tab
         num_partitions, scale,
         _ptr(d_indices), indices_stride, _ptr(topk_lengths), _ptr(attn_sink), dtype,
         _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
+
+
+def mla_latent_cache_write_q8(kv_cache, kv_scales, q, kv_latent, kv_norm_gamma, freqs_cis,
+                              input_row_offsets, cache_lengths, page_table, num_pages, page_size,
+                              max_pages_per_seq, scale_block, batch_size, num_heads, total_q_tokens,
+                              max_seq_len, epsilon, d_status=None, stream=None) -> int:
+    return load().mla_latent_cache_write_q8(
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(q), _ptr(kv_latent), _ptr(kv_norm_gamma),
+        _ptr(freqs_cis), _ptr(input_row_offsets), _ptr(cache_lengths), _ptr(page_table), num_pages,
+        page_size, max_pages_per_seq, scale_block, batch_size, num_heads, total_q_tokens,
+        max_seq_len, epsilon, _ptr(d_status), _stream(stream))
+
+
+def mla_gather_latent_q8(c_kv_buf, k_rope_buf, kv_cache, kv_scales, page_table, num_pages, page_size,
+                         max_pages_per_seq, scale_block, buffer_row_offsets, cache_offsets,
+                         buffer_lengths, chunk, batch_size, buffer_token_size, d_status=None,
+                         stream=None) -> int:
+    return load().mla_gather_latent_q8(
+        _ptr(c_kv_buf), _ptr(k_rope_buf), _ptr(kv_cache), _ptr(kv_scales), _ptr(page_table),
+        num_pages, page_size, max_pages_per_seq, scale_block, _ptr(buffer_row_offsets),
+        _ptr(cache_offsets), _ptr(buffer_lengths), chunk, batch_size, buffer_token_size,
+        _ptr(d_status), _stream(stream))
+
+
+def mla_prefill_q8(out, lse, q, input_row_offsets, cache_lengths, kv_cache, kv_scales, page_table,
+                   num_pages, page_size, max_pages_per_seq, scale_block, w_k, w_uv, batch_size,
+                   num_heads, total_q_tokens, max_prompt_len, buffer_token_size, max_chunks, scale,
+                   workspace=None, workspace_bytes=0, d_status=None, stream=None) -> int:
+    """mla_prefill over the 8-bit block-scaled cache; the workspace is mla_prefill's for bf16."""
+    return load().mla_prefill_q8(
+        _ptr(out), _ptr(lse), _ptr(q), _ptr(input_row_offsets), _ptr(cache_lengths),
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(page_table), num_pages, page_size, max_pages_per_seq,
+        scale_block, _ptr(w_k), _ptr(w_uv), batch_size, num_heads, total_q_tokens, max_prompt_len,
+        buffer_token_size, max_chunks, scale, _ptr(workspace), workspace_bytes, _ptr(d_status),
+        _stream(stream))
+
+
+def mla_decode_q8_partitions(batch_size, num_heads, max_new_tokens, max_keys) -> int:
+    return load().mla_decode_q8_partitions(batch_size, num_heads, max_new_tokens, max_keys)
+
+
+def mla_decode_q8_workspace_bytes(num_heads, total_q_tokens, num_partitions) -> int:
+    return load().mla_decode_q8_workspace_bytes(num_heads, total_q_tokens, num_partitions)
+
+
+def mla_decode_q8(out, lse, q, input_row_offsets, cache_lengths, kv_cache, kv_scales, page_table,
+                  num_pages, page_size, max_pages_per_seq, scale_block, w_uk, w_uv, batch_size,
+                  num_heads, total_q_tokens, max_new_tokens, max_seq_len, num_partitions, scale,
+                  d_indices=None, indices_stride=0, topk_lengths=None, attn_sink=None,
+                  workspace=None, workspace_bytes=0, d_status=None, stream=None) -> int:
+    return load().mla_decode_q8(
+        _ptr(out), _ptr(lse), _ptr(q), _ptr(input_row_offsets), _ptr(cache_lengths),
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(page_table), num_pages, page_size, max_pages_per_seq,
+        scale_block, _ptr(w_uk), _ptr(w_uv), batch_size, num_heads, total_q_tokens, max_new_tokens,
+        max_seq_len, num_partitions, scale, _ptr(d_indices), indices_stride, _ptr(topk_lengths),
+        _ptr(attn_sink), _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
+
+
+def mla_index_scores(scores, index_q, index_w, index_cache, index_scales, input_row_offsets,
+                     cache_lengths, page_table, num_pages, page_size, max_pages_per_seq, block,
+                     batch_size, num_index_heads, total_q_tokens, max_new_tokens, max_seq_len,
+                     scores_stride, dtype=MLA_BF16, d_status=None, stream=None) -> int:
+    return load().mla_index_scores(
+        _ptr(scores), _ptr(index_q), _ptr(index_w), _ptr(index_cache), _ptr(index_scales),
+        _ptr(input_row_offsets), _ptr(cache_lengths), _ptr(page_table), num_pages, page_size,
+        max_pages_per_seq, block, batch_size, num_index_heads, total_q_tokens, max_new_tokens,
+        max_seq_len, scores_stride, dtype, _ptr(d_status), _stream(stream))
+
+
+def mla_index_select(indices, counts, scores, input_row_offsets, cache_lengths, page_table,
+                     num_pages, page_size, max_pages_per_seq, block, top_blocks, num_local,
+                     batch_size, total_q_tokens, max_seq_len, scores_stride, indices_stride,
+                     d_status=None, stream=None) -> int:
+    return load().mla_index_select(
+        _ptr(indices), _ptr(counts), _ptr(scores), _ptr(input_row_offsets), _ptr(cache_lengths),
+        _ptr(page_table), num_pages, page_size, max_pages_per_seq, block, top_blocks, num_local,
+        batch_size, total_q_tokens, max_seq_len, scores_stride, indices_stride, _ptr(d_status),
+        _stream(stream))
 
 
 __all__ = [n for n in SIGNATURES] + ["load", "check", "status_string", "MLAError", "LIB_PATH"]

@@ -38,6 +38,14 @@ int elt_bytes(int32_t dtype) { return dtype == MLA_BF16 ? 2 : 1; }
 
 bool dtype_ok(int32_t dtype) { return dtype == MLA_BF16 || dtype == MLA_E4M3; }
 
+// Slots that share a scale: they divide a page, 128 at most.
+bool scale_block_ok(int32_t page_size, int32_t scale_block) {
+  return page_size >= 1 && scale_block >= 1 && scale_block <= 128 && page_size % scale_block == 0;
+}
+
+// Keys of a selection block: a power of two, 128 at most.
+bool index_block_ok(int32_t block) { return block >= 1 && block <= 128 && (block & (block - 1)) == 0; }
+
 mla_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_LAUNCH; }
 
 // Workspace layout of the fused entry point.
@@ -394,15 +402,17 @@ size_t mla_prefill_workspace_bytes(int32_t batch_size, int32_t num_heads, int32_
   return layout(batch_size, num_heads, total_q_tokens, max_chunks, buffer_token_size, dtype).total;
 }
 
-mla_status_t mla_prefill(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
-                         const uint32_t* cache_lengths, const void* kv_cache,
-                         const int32_t* page_table, int32_t num_pages, int32_t page_size,
-                         int32_t max_pages_per_seq, const void* w_k, const void* w_uv,
-                         int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
-                         int32_t max_prompt_len, uint32_t buffer_token_size, int32_t max_chunks,
-                         float scale, float q_scale, float ckv_scale, float w_scale,
-                         int32_t dtype, void* workspace, size_t workspace_bytes,
-                         int32_t* d_status, mla_stream_t stream_) {
+// kv_scales given: the 8-bit block-scaled cache, gathered as bf16 (dtype MLA_BF16).
+static mla_status_t prefill_impl(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                                 const uint32_t* cache_lengths, const void* kv_cache,
+                                 const float* kv_scales, int32_t scale_block,
+                                 const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                                 int32_t max_pages_per_seq, const void* w_k, const void* w_uv,
+                                 int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                                 int32_t max_prompt_len, uint32_t buffer_token_size, int32_t max_chunks,
+                                 float scale, float q_scale, float ckv_scale, float w_scale,
+                                 int32_t dtype, void* workspace, size_t workspace_bytes,
+                                 int32_t* d_status, mla_stream_t stream_) {
   if (!dtype_ok(dtype)) return MLA_ERR_DTYPE;
   if (num_heads < 1) return MLA_ERR_GEOMETRY;
   if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !page_table || !w_k ||
@@ -435,9 +445,14 @@ mla_status_t mla_prefill(void* out, float* lse, const void* q, const uint32_t* i
   // projection re-reads every A tile once per head tile, and the copy costs
   // about 1 % of a chunk.)
   for (int c = 0; c < max_chunks; ++c) {
-    st = mla_gather_latent(ws + L.ckv, ws + L.krope, kv_cache, page_table, num_pages, page_size,
-                           max_pages_per_seq, bro, co, bl, c, batch_size, buffer_token_size,
-                           dtype, d_status, stream_);
+    if (kv_scales != nullptr)
+      st = mla_gather_latent_q8(ws + L.ckv, ws + L.krope, kv_cache, kv_scales, page_table, num_pages, page_size,
+                                max_pages_per_seq, scale_block, bro, co, bl, c, batch_size, buffer_token_size,
+                                d_status, stream_);
+    else
+      st = mla_gather_latent(ws + L.ckv, ws + L.krope, kv_cache, page_table, num_pages, page_size,
+                             max_pages_per_seq, bro, co, bl, c, batch_size, buffer_token_size,
+                             dtype, d_status, stream_);
     if (st != MLA_OK) return st;
     st = mla_upproject(ws + L.knope, ws + L.v, ws + L.ckv, w_k, w_uv, bl, c, buffer_token_size,
                        num_heads, dtype, ckv_scale, w_scale, kv_inv, d_status, stream_);
@@ -449,6 +464,36 @@ mla_status_t mla_prefill(void* out, float* lse, const void* q, const uint32_t* i
     if (st != MLA_OK) return st;
   }
   return MLA_OK;
+}
+
+mla_status_t mla_prefill(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                         const uint32_t* cache_lengths, const void* kv_cache,
+                         const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                         int32_t max_pages_per_seq, const void* w_k, const void* w_uv,
+                         int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                         int32_t max_prompt_len, uint32_t buffer_token_size, int32_t max_chunks,
+                         float scale, float q_scale, float ckv_scale, float w_scale,
+                         int32_t dtype, void* workspace, size_t workspace_bytes,
+                         int32_t* d_status, mla_stream_t stream) {
+  return prefill_impl(out, lse, q, input_row_offsets, cache_lengths, kv_cache, nullptr, 0, page_table, num_pages,
+                      page_size, max_pages_per_seq, w_k, w_uv, batch_size, num_heads, total_q_tokens,
+                      max_prompt_len, buffer_token_size, max_chunks, scale, q_scale, ckv_scale, w_scale, dtype,
+                      workspace, workspace_bytes, d_status, stream);
+}
+
+mla_status_t mla_prefill_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                            const uint32_t* cache_lengths, const void* kv_cache, const float* kv_scales,
+                            const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                            int32_t max_pages_per_seq, int32_t scale_block, const void* w_k,
+                            const void* w_uv, int32_t batch_size, int32_t num_heads,
+                            int32_t total_q_tokens, int32_t max_prompt_len, uint32_t buffer_token_size,
+                            int32_t max_chunks, float scale, void* workspace, size_t workspace_bytes,
+                            int32_t* d_status, mla_stream_t stream) {
+  if (num_heads >= 1 && (!kv_scales || !scale_block_ok(page_size, scale_block))) return MLA_ERR_ARG;
+  return prefill_impl(out, lse, q, input_row_offsets, cache_lengths, kv_cache, kv_scales, scale_block, page_table,
+                      num_pages, page_size, max_pages_per_seq, w_k, w_uv, batch_size, num_heads, total_q_tokens,
+                      max_prompt_len, buffer_token_size, max_chunks, scale, 1.0f, 1.0f, 1.0f, MLA_BF16, workspace,
+                      workspace_bytes, d_status, stream);
 }
 
 int32_t mla_decode_partitions(int32_t batch_size, int32_t num_heads, int32_t max_new_tokens,
@@ -521,6 +566,227 @@ mla_status_t mla_decode(void* out, float* lse, const void* q, const uint32_t* in
   a.workspace = workspace;
   a.status = d_status;
   return from_cuda(mla::launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ 8-bit cache
+mla_status_t mla_latent_cache_write_q8(void* kv_cache, float* kv_scales, void* q, const void* kv_latent,
+                                       const float* kv_norm_gamma, const float* freqs_cis,
+                                       const uint32_t* input_row_offsets, const uint32_t* cache_lengths,
+                                       const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                                       int32_t max_pages_per_seq, int32_t scale_block, int32_t batch_size,
+                                       int32_t num_heads, int32_t total_q_tokens, int32_t max_seq_len,
+                                       float epsilon, int32_t* d_status, mla_stream_t stream) {
+  if (!kv_cache || !kv_scales || !kv_latent || !kv_norm_gamma || !freqs_cis || !input_row_offsets ||
+      !cache_lengths || !page_table || !aligned16(kv_cache) || !aligned16(kv_latent) ||
+      !aligned16(kv_norm_gamma) || !aligned16(freqs_cis) || (q && !aligned16(q)) || batch_size < 1 ||
+      total_q_tokens < 0 || (q && num_heads < 1) || num_pages < 1 || max_pages_per_seq < 1 || max_seq_len < 1 ||
+      !scale_block_ok(page_size, scale_block) || !(epsilon >= 0.0f))
+    return MLA_ERR_ARG;
+  mla::CacheWriteQ8Args a;
+  a.kv_cache = kv_cache;
+  a.kv_scales = kv_scales;
+  a.q = q;
+  a.kv_latent = kv_latent;
+  a.gamma = kv_norm_gamma;
+  a.freqs = freqs_cis;
+  a.iro = input_row_offsets;
+  a.cache_len = cache_lengths;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.scale_block = scale_block;
+  a.B = batch_size;
+  a.H = q ? num_heads : 0;
+  a.T = total_q_tokens;
+  a.max_seq_len = max_seq_len;
+  a.eps = epsilon;
+  a.status = d_status;
+  return from_cuda(mla::launch_cache_write_q8(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_gather_latent_q8(void* c_kv_buf, void* k_rope_buf, const void* kv_cache,
+                                  const float* kv_scales, const int32_t* page_table, int32_t num_pages,
+                                  int32_t page_size, int32_t max_pages_per_seq, int32_t scale_block,
+                                  const uint32_t* buffer_row_offsets, const uint32_t* cache_offsets,
+                                  const int32_t* buffer_lengths, int32_t chunk, int32_t batch_size,
+                                  uint32_t buffer_token_size, int32_t* d_status, mla_stream_t stream) {
+  if (!c_kv_buf || !k_rope_buf || !kv_cache || !kv_scales || !page_table || !buffer_row_offsets ||
+      !cache_offsets || !buffer_lengths || !aligned16(c_kv_buf) || !aligned16(k_rope_buf) ||
+      !aligned16(kv_cache) || num_pages < 1 || max_pages_per_seq < 1 || !scale_block_ok(page_size, scale_block) ||
+      chunk < 0 || batch_size < 1 || buffer_token_size == 0 || buffer_token_size > 0x7FFFFFFFu)
+    return MLA_ERR_ARG;
+  mla::GatherQ8Args a;
+  a.c_kv_buf = c_kv_buf;
+  a.k_rope_buf = k_rope_buf;
+  a.kv_cache = kv_cache;
+  a.kv_scales = kv_scales;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.scale_block = scale_block;
+  a.bro = buffer_row_offsets;
+  a.co = cache_offsets;
+  a.bl = buffer_lengths;
+  a.chunk = chunk;
+  a.B = batch_size;
+  a.S = buffer_token_size;
+  a.status = d_status;
+  return from_cuda(mla::launch_gather_q8(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t mla_decode_q8_partitions(int32_t batch_size, int32_t num_heads, int32_t max_new_tokens, int32_t max_keys) {
+  if (batch_size < 1 || num_heads < 1) return 1;
+  return mla::decode_q8_partitioning(batch_size, num_heads, max_new_tokens, max_keys).parts;
+}
+
+size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, int32_t num_partitions) {
+  if (num_heads < 1 || total_q_tokens < 0 || num_partitions < 1) return 0;
+  return mla::decode_q8_layout(total_q_tokens, num_heads, num_partitions).total;
+}
+
+mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                           const uint32_t* cache_lengths, const void* kv_cache, const float* kv_scales,
+                           const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                           int32_t max_pages_per_seq, int32_t scale_block, const void* w_uk, const void* w_uv,
+                           int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                           int32_t max_new_tokens, int32_t max_seq_len, int32_t num_partitions, float scale,
+                           const int32_t* d_indices, int32_t indices_stride, const int32_t* topk_lengths,
+                           const float* attn_sink, void* workspace, size_t workspace_bytes,
+                           int32_t* d_status, mla_stream_t stream) {
+  if (num_heads < 1) return MLA_ERR_GEOMETRY;
+  if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !kv_scales || !w_uk || !w_uv ||
+      !aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
+      batch_size < 1 || total_q_tokens < 0 || max_new_tokens < 0 || max_seq_len < 1 || num_partitions < 0 ||
+      num_pages < 1 || !scale_block_ok(page_size, scale_block) || !(scale > 0.0f))
+    return MLA_ERR_ARG;
+  if (d_indices == nullptr && (!page_table || max_pages_per_seq < 1)) return MLA_ERR_ARG;
+  if (d_indices != nullptr && indices_stride < 1) return MLA_ERR_ARG;
+  const long long rows = static_cast<long long>(total_q_tokens) * num_heads;
+  // Launch limits: 65535 heads (or a quarter of them for the query clusters).
+  if (rows >= (1ll << 31) / 4 || num_heads > 65535 / 4 ||
+      static_cast<long long>(max_new_tokens) * num_heads >= (1ll << 31) / 4 ||
+      static_cast<long long>(num_pages) * page_size >= (1ll << 31))
+    return MLA_ERR_ARG;
+  if (total_q_tokens == 0 || max_new_tokens == 0) return MLA_OK;
+  const int max_keys = d_indices != nullptr ? std::min(indices_stride, max_seq_len) : max_seq_len;
+  const mla::DecodePartitioning auto_parts =
+      mla::decode_q8_partitioning(batch_size, num_heads, max_new_tokens, max_keys);
+  const int parts = num_partitions > 0 ? num_partitions : auto_parts.parts;
+  const long long items = static_cast<long long>(batch_size) * parts *
+                          ((static_cast<long long>(max_new_tokens) * num_heads + 31) / 32);
+  if (items >= (1ll << 31)) return MLA_ERR_ARG;
+  const mla::DecodeQ8Layout L = mla::decode_q8_layout(total_q_tokens, num_heads, parts);
+  if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return MLA_ERR_WORKSPACE;
+  mla::DecodeQ8Args a;
+  a.out = out;
+  a.lse = lse;
+  a.q = q;
+  a.kv_cache = kv_cache;
+  a.kv_scales = kv_scales;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.scale_block = scale_block;
+  a.w_uk = w_uk;
+  a.w_uv = w_uv;
+  a.iro = input_row_offsets;
+  a.cache_len = cache_lengths;
+  a.B = batch_size;
+  a.H = num_heads;
+  a.T = total_q_tokens;
+  a.max_new = max_new_tokens;
+  a.max_seq = max_seq_len;
+  a.parts = parts;
+  a.part_keys = num_partitions > 0 ? 0 : auto_parts.part_keys;
+  a.scale = scale;
+  a.indices = d_indices;
+  a.indices_stride = indices_stride;
+  a.topk = topk_lengths;
+  a.sink = attn_sink;
+  a.workspace = workspace;
+  a.status = d_status;
+  return from_cuda(mla::launch_decode_q8(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ key selection
+mla_status_t mla_index_scores(float* scores, const void* index_q, const float* index_w, const void* index_cache,
+                              const float* index_scales, const uint32_t* input_row_offsets,
+                              const uint32_t* cache_lengths, const int32_t* page_table, int32_t num_pages,
+                              int32_t page_size, int32_t max_pages_per_seq, int32_t block, int32_t batch_size,
+                              int32_t num_index_heads, int32_t total_q_tokens, int32_t max_new_tokens,
+                              int32_t max_seq_len, int32_t scores_stride, int32_t dtype, int32_t* d_status,
+                              mla_stream_t stream) {
+  if (!dtype_ok(dtype)) return MLA_ERR_DTYPE;
+  if (num_index_heads < 1 || num_index_heads > 128) return MLA_ERR_GEOMETRY;
+  if (!scores || !index_q || !index_w || !index_cache || !input_row_offsets || !cache_lengths || !page_table ||
+      !aligned16(index_q) || !aligned16(index_cache) || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+      !index_block_ok(block) || batch_size < 1 || total_q_tokens < 0 || max_new_tokens < 0 || max_seq_len < 1 ||
+      scores_stride < 1 || static_cast<long long>(scores_stride) * block < max_seq_len ||
+      static_cast<long long>(num_pages) * page_size >= (1ll << 31) ||
+      static_cast<long long>(total_q_tokens) * num_index_heads >= (1ll << 31))
+    return MLA_ERR_ARG;
+  mla::IndexScoresArgs a;
+  a.scores = scores;
+  a.iq = index_q;
+  a.w = index_w;
+  a.keys = index_cache;
+  a.key_scales = index_scales;
+  a.iro = input_row_offsets;
+  a.cache_len = cache_lengths;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.block = block;
+  a.B = batch_size;
+  a.Hi = num_index_heads;
+  a.T = total_q_tokens;
+  a.max_new = max_new_tokens;
+  a.max_seq = max_seq_len;
+  a.stride = scores_stride;
+  a.dtype = dtype;
+  a.status = d_status;
+  return from_cuda(mla::launch_index_scores(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* scores,
+                              const uint32_t* input_row_offsets, const uint32_t* cache_lengths,
+                              const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                              int32_t max_pages_per_seq, int32_t block, int32_t top_blocks, int32_t num_local,
+                              int32_t batch_size, int32_t total_q_tokens, int32_t max_seq_len,
+                              int32_t scores_stride, int32_t indices_stride, int32_t* d_status,
+                              mla_stream_t stream) {
+  if (!indices || !counts || !scores || !input_row_offsets || !cache_lengths || !page_table || num_pages < 1 ||
+      page_size < 1 || max_pages_per_seq < 1 || !index_block_ok(block) || top_blocks < 1 || num_local < 0 ||
+      num_local > top_blocks || batch_size < 1 || total_q_tokens < 0 || total_q_tokens > (1 << 27) ||
+      max_seq_len < 1 || scores_stride < 1 || static_cast<long long>(scores_stride) * block < max_seq_len ||
+      static_cast<long long>(top_blocks) * block > indices_stride ||
+      static_cast<long long>(num_pages) * page_size >= (1ll << 31))
+    return MLA_ERR_ARG;
+  mla::IndexSelectArgs a;
+  a.rows = indices;
+  a.count = counts;
+  a.scores = scores;
+  a.iro = input_row_offsets;
+  a.cache_len = cache_lengths;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.block = block;
+  a.top = top_blocks;
+  a.local = num_local;
+  a.B = batch_size;
+  a.T = total_q_tokens;
+  a.max_seq = max_seq_len;
+  a.stride = scores_stride;
+  a.rows_stride = indices_stride;
+  a.status = d_status;
+  return from_cuda(mla::launch_index_select(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

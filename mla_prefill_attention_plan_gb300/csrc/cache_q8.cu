@@ -1,0 +1,334 @@
+// The 8-bit latent cache: e4m3 rows of 576 values with one float32 scale, a
+// power of two, for each block of scale_block consecutive slots of a page.
+// Writing (RMSNorm, RoPE, quantisation) and the gather of one plan chunk as
+// bf16 rows.
+//
+// A block's scale is the smallest power of two s with |value| <= 448 s for
+// every value of its rows.  Rows arrive over many calls, so the scale may have
+// to grow: the rows before are then requantised by the ratio of the scales.
+// The ratio is a power of two, so that changes their codes' exponents only and
+// is exact but for codes that leave e4m3's normal range.
+#include "kernels.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kWriteThreads = 256;
+constexpr int kWriteWarps = kWriteThreads / 32;
+
+// hi + lo += x, keeping the rounding error of the sum in lo.
+__device__ __forceinline__ void add_two(float& hi, float& lo, float x) {
+  const float s = hi + x;
+  const float b = s - hi;
+  lo += (hi - (s - b)) + (x - b);
+  hi = s;
+}
+
+// a c - b d with one rounding of each product's error taken back (the plain
+// form loses up to three roundings, which moves codes next to a border).
+__device__ __forceinline__ float diff_of_products(float a, float c, float b, float d) {
+  const float w = b * d;
+  const float e = fmaf(-b, d, w);
+  return fmaf(a, c, -w) + e;
+}
+__device__ __forceinline__ float2 rotate2(float re, float im, float c, float s) {
+  return make_float2(diff_of_products(re, c, im, s), diff_of_products(re, s, -im, c));
+}
+
+// One row's 576 values before quantisation, held by a warp: lane l has latent
+// values 8l..8l+7 and 256+8l..256+8l+7 and rope values 2l, 2l+1.
+struct RowValues {
+  float y[16];
+  float2 rope;
+};
+
+__device__ __forceinline__ RowValues row_values(const uint16_t* __restrict__ row, const float* __restrict__ gamma,
+                                                const float* __restrict__ freq, float eps) {
+  const int lane = threadIdx.x & 31;
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+  const uint4 b = __ldg(reinterpret_cast<const uint4*>(row) + 32 + lane);
+  const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(row + 512) + lane);
+  const float2 f = __ldg(reinterpret_cast<const float2*>(freq) + lane);
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  RowValues v;
+  // Sum of squares in two floats (a bf16 square is exact in fp32).
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v.y[2 * i] = bf16_lo(u[i]);
+    v.y[2 * i + 1] = bf16_hi(u[i]);
+    add_two(hi, lo, v.y[2 * i] * v.y[2 * i]);
+    add_two(hi, lo, v.y[2 * i + 1] * v.y[2 * i + 1]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const float oh = __shfl_xor_sync(0xffffffffu, hi, d), ol = __shfl_xor_sync(0xffffffffu, lo, d);
+    // Both lanes of a pair add the same two numbers in the same order.
+    const bool up = (lane & d) != 0;
+    float h = up ? oh : hi, l = up ? ol : lo;
+    add_two(h, l, up ? hi : oh);
+    hi = h;
+    lo = l + (up ? lo : ol);
+  }
+  // 1 / sqrt(mean + eps) as rh + rl: the hardware's approximation and one
+  // Newton step whose residual 1 - s rh^2 is formed in two floats.
+  float sh = hi * (1.0f / 512.0f), sl = lo * (1.0f / 512.0f);
+  add_two(sh, sl, eps);
+  const float rh = rsqrtf(sh);
+  const float th = rh * rh, tl = fmaf(rh, rh, -th);
+  const float res = fmaf(-sh, th, 1.0f) - fmaf(sh, tl, sl * th);
+  const float rl = 0.5f * rh * res;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + (i < 8 ? 0 : 256) + 8 * lane) + ((i & 4) >> 2));
+    const float gv[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float p = v.y[i + k] * gv[k];
+      const float e = fmaf(v.y[i + k], gv[k], -p);
+      // rh + rl is finite unless the row is all zero with eps 0 (then NaN, as x / 0).
+      v.y[i + k] = fmaf(p, rh, fmaf(p, rl, e * rh));
+    }
+  }
+  v.rope = rotate2(bf16_lo(r), bf16_hi(r), f.x, f.y);
+  return v;
+}
+
+__device__ __forceinline__ float row_amax(const RowValues& v) {
+  float m = fmaxf(fabsf(v.rope.x), fabsf(v.rope.y));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v.y[i]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m;
+}
+
+__device__ __forceinline__ void store_row(uint8_t* __restrict__ dst, const RowValues& v, float inv) {
+  const int lane = threadIdx.x & 31;
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = static_cast<uint32_t>(pack_e4m3(v.y[4 * i] * inv, v.y[4 * i + 1] * inv)) |
+           (static_cast<uint32_t>(pack_e4m3(v.y[4 * i + 2] * inv, v.y[4 * i + 3] * inv)) << 16);
+  reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
+  reinterpret_cast<uint2*>(dst + 256)[lane] = make_uint2(c[2], c[3]);
+  reinterpret_cast<uint16_t*>(dst + 512)[lane] = pack_e4m3(v.rope.x * inv, v.rope.y * inv);
+}
+
+// Four e4m3 codes times a power of two, back to e4m3.
+__device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
+  const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(static_cast<uint16_t>(c & 0xFFFFu)));
+  const float2 b = f16x2_to_float2(e4m3x2_to_f16x2(static_cast<uint16_t>(c >> 16)));
+  return static_cast<uint32_t>(pack_e4m3(a.x * ratio, a.y * ratio)) |
+         (static_cast<uint32_t>(pack_e4m3(b.x * ratio, b.y * ratio)) << 16);
+}
+
+// One CTA per new token (grid-stride).  All its threads rotate the token's
+// query heads; the CTA of the first new token of each touched block also
+// writes that block's new rows (one warp a row): first their largest value,
+// then, with the scale known, the codes (the rows are read again, from L1).
+// HBM-bound: per token 1152 bytes of latent read, 576 written, 256 of
+// frequencies, and 4 * 64 * H of queries read and written.
+__global__ void __launch_bounds__(kWriteThreads)
+    cache_write_q8_kernel(const CacheWriteQ8Args a) {
+  __shared__ float s_amax[kWriteWarps];
+  __shared__ int s_info[3];   // position (-1: skip), rows to write as leader, first slot of the block
+  __shared__ long long s_row; // cache row of the token (-1: no page)
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint16_t* latent = static_cast<const uint16_t*>(a.kv_latent);
+  uint8_t* cache = static_cast<uint8_t*>(a.kv_cache);
+
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (tid == 0) {
+      int lo = 0, hi = a.B;   // largest b with iro[b] <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.iro[mid] <= static_cast<uint32_t>(t)) lo = mid; else hi = mid;
+      }
+      const uint32_t first = a.iro[lo], end = a.iro[lo + 1];
+      int pos = -1, rows = 0, slot = 0;
+      long long row = -1;
+      if (first <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < end) {
+        const uint64_t p = static_cast<uint64_t>(a.cache_len[lo]) + (static_cast<uint32_t>(t) - first);
+        if (p < static_cast<uint64_t>(a.max_seq_len)) {
+          pos = static_cast<int>(p);
+          slot = pos % a.scale_block;
+          if (slot == 0 || static_cast<uint32_t>(t) == first) {
+            // This block's new rows: up to its end, the sequence's last new
+            // token, the last row of the call and the last position.
+            rows = a.scale_block - slot;
+            rows = static_cast<int>(min(static_cast<uint32_t>(rows), min(end, static_cast<uint32_t>(a.T)) - t));
+            rows = min(rows, a.max_seq_len - pos);
+            const int pidx = pos / a.page_size;
+            const int page = pidx < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + pidx] : -1;
+            if (page >= 0 && page < a.num_pages)
+              row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+            else
+              set_status(a.status, MLA_DEV_BAD_PAGE);
+          }
+        } else {
+          set_status(a.status, MLA_DEV_BAD_OFFSETS);
+        }
+      } else {
+        set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      }
+      s_info[0] = pos;
+      s_info[1] = row >= 0 ? rows : 0;
+      s_info[2] = slot;
+      s_row = row;
+    }
+    __syncthreads();
+    const int pos = s_info[0], rows = s_info[1], slot = s_info[2];
+    const long long row0 = s_row;
+    if (rows > 0) {
+      const uint16_t* src = latent + static_cast<size_t>(t) * 576;
+      RowValues v;
+      float m = 0.f;
+      for (int r = warp; r < rows; r += kWriteWarps) {
+        v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(pos + r) * 64, a.eps);
+        m = fmaxf(m, row_amax(v));
+      }
+      if ((tid & 31) == 0) s_amax[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWriteWarps; ++w) m = fmaxf(m, s_amax[w]);
+      float scale = pow2_scale(m);
+      float* sp = a.kv_scales + row0 / a.scale_block;
+      if (slot > 0) {
+        // Rows before, written by earlier calls under the block's scale.
+        const float was = *sp;
+        if (was > 0.f && was < __int_as_float(0x7f800000)) {
+          if (was >= scale) {
+            scale = was;
+          } else {
+            uint4* old = reinterpret_cast<uint4*>(cache + static_cast<size_t>(row0 - slot) * 576);
+            const float ratio = was / scale;
+            for (int i = tid; i < slot * 36; i += kWriteThreads) {
+              const uint4 c = old[i];
+              old[i] = make_uint4(requantise4(c.x, ratio), requantise4(c.y, ratio), requantise4(c.z, ratio),
+                                  requantise4(c.w, ratio));
+            }
+          }
+        }
+      }
+      __syncthreads();   // every thread has read the old scale
+      if (tid == 0) *sp = scale;
+      const float inv = 1.0f / scale;   // exact for a power of two
+      for (int r = warp; r < rows; r += kWriteWarps) {
+        if (rows > kWriteWarps)
+          v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(pos + r) * 64, a.eps);
+        store_row(cache + static_cast<size_t>(row0 + r) * 576, v, inv);
+      }
+    }
+    // q: piece m of head h holds rope values 8m .. 8m+7 (pairs 4m .. 4m+3).
+    if (a.q != nullptr && pos >= 0) {
+      const float4* fr = reinterpret_cast<const float4*>(a.freqs + static_cast<size_t>(pos) * 64);
+      uint16_t* qt = static_cast<uint16_t*>(a.q) + static_cast<size_t>(t) * a.H * 192 + 128;
+      for (int i = tid; i < 8 * a.H; i += kWriteThreads) {
+        const int h = i >> 3, m = i & 7;
+        uint4* pq = reinterpret_cast<uint4*>(qt + static_cast<size_t>(h) * 192) + m;
+        const uint4 x = *pq;
+        const float4 fa = __ldg(fr + 2 * m), fb = __ldg(fr + 2 * m + 1);
+        const float2 a0 = rotate2(bf16_lo(x.x), bf16_hi(x.x), fa.x, fa.y);
+        const float2 a1 = rotate2(bf16_lo(x.y), bf16_hi(x.y), fa.z, fa.w);
+        const float2 a2 = rotate2(bf16_lo(x.z), bf16_hi(x.z), fb.x, fb.y);
+        const float2 a3 = rotate2(bf16_lo(x.w), bf16_hi(x.w), fb.z, fb.w);
+        *pq = make_uint4(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y), pack_bf16(a2.x, a2.y), pack_bf16(a3.x, a3.y));
+      }
+    }
+    __syncthreads();   // the shared words are rewritten for the next token
+  }
+}
+
+// ------------------------------------------------------------------ gather
+// As the bf16 gather: each CTA owns 32 consecutive buffer rows, resolves their
+// addresses, then moves them in 16-byte pieces; a piece of 16 codes becomes 32
+// bytes of bf16 (code times scale in fp32, rounded once; exact for the powers
+// of two that the write stores).  HBM-bound: 576 bytes read and 1152 written a
+// row.
+constexpr int kGatherRows = 32;
+constexpr int kGatherThreads = 256;
+constexpr int kPieces = 36;   // 16-byte pieces of a row
+
+__device__ __forceinline__ uint2 dequant4(uint32_t c, float s) {
+  const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(static_cast<uint16_t>(c & 0xFFFFu)));
+  const float2 b = f16x2_to_float2(e4m3x2_to_f16x2(static_cast<uint16_t>(c >> 16)));
+  return make_uint2(pack_bf16(a.x * s, a.y * s), pack_bf16(b.x * s, b.y * s));
+}
+
+__global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const GatherQ8Args a) {
+  constexpr int kVecs = kGatherRows * kPieces;
+  constexpr int kPer = (kVecs + kGatherThreads - 1) / kGatherThreads;
+  __shared__ long long s_src[kGatherRows];   // cache row, or -1
+  __shared__ float s_scale[kGatherRows];
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int n = min(a.bl[a.chunk], static_cast<int>(a.S));
+  const int r0 = blockIdx.x * kGatherRows;
+  if (r0 >= n) return;
+  const uint32_t* bro = a.bro + static_cast<size_t>(a.chunk) * (a.B + 1);
+  const uint32_t* co = a.co + static_cast<size_t>(a.chunk) * a.B;
+  if (threadIdx.x < kGatherRows) {
+    const int r = r0 + threadIdx.x;
+    long long src = -1;
+    if (r < n) {
+      int lo = 0, hi = a.B;   // bro[lo] <= r < bro[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (bro[mid] <= static_cast<uint32_t>(r)) lo = mid; else hi = mid;
+      }
+      const uint32_t pos = co[lo] + (static_cast<uint32_t>(r) - bro[lo]);
+      const uint32_t pidx = pos / static_cast<uint32_t>(a.page_size);
+      const int page = pidx < static_cast<uint32_t>(a.max_pages)
+                           ? a.page_table[static_cast<size_t>(lo) * a.max_pages + pidx] : -1;
+      if (page >= 0 && page < a.num_pages) {
+        src = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+        s_scale[threadIdx.x] = __ldg(a.kv_scales + src / a.scale_block);
+      } else {
+        set_status(a.status, MLA_DEV_BAD_PAGE);
+      }
+    }
+    s_src[threadIdx.x] = src;
+  }
+  __syncthreads();
+  uint4 v[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int idx = threadIdx.x + k * kGatherThreads;
+    const int row = idx / kPieces, col = idx - row * kPieces;
+    const long long src = idx < kVecs ? s_src[row] : -1;
+    if (src >= 0)
+      v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv_cache) + src * 576) + col);
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int idx = threadIdx.x + k * kGatherThreads;
+    const int row = idx / kPieces, col = idx - row * kPieces;
+    if (idx >= kVecs || s_src[row] < 0) continue;
+    const float s = s_scale[row];
+    const uint2 p0 = dequant4(v[k].x, s), p1 = dequant4(v[k].y, s), p2 = dequant4(v[k].z, s), p3 = dequant4(v[k].w, s);
+    const size_t r = static_cast<size_t>(r0 + row);
+    uint4* dst = col < 32 ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c_kv_buf) + r * 512) + 2 * col
+                          : reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_rope_buf) + r * 64) + 2 * (col - 32);
+    dst[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
+    dst[1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write_q8(const CacheWriteQ8Args& a, cudaStream_t stream) {
+  if (a.T <= 0) return cudaSuccess;
+  const int grid = a.T < 16 * sm_count() ? a.T : 16 * sm_count();
+  return launch_pdl(cache_write_q8_kernel, dim3(grid), dim3(kWriteThreads), 0, stream, a);
+}
+
+cudaError_t launch_gather_q8(const GatherQ8Args& a, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((static_cast<uint64_t>(a.S) + kGatherRows - 1) / kGatherRows);
+  return launch_pdl(gather_q8_kernel, dim3(grid), dim3(kGatherThreads), 0, stream, a);
+}
+
+}  // namespace mla

@@ -1,0 +1,651 @@
+// Key selection for sparse decode: a cheap score for every block of keys and
+// new token, and the best blocks of every token as the list of physical cache
+// rows that the sparse decode calls take.
+//
+// Scores: with index queries q[t][h] and one index key k_j per cached token
+// (128 values each, kept in a paged cache of their own under the same page
+// table),
+//   score(t, i) = max over visible j in block i of s_j sum_h w[t][h] relu(q[t][h] . k_j).
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace mla {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Largest b with iro[b] <= t (t belongs to b when t < iro[b + 1]).
+__device__ __forceinline__ int sequence_of(const uint32_t* __restrict__ iro, int B, uint32_t t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(iro + mid) <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ============================================================ scores
+// Keys are the M side of the MMA (128 keys a tile, the heads of one token the
+// N side, K = 128), so a thread of the epilogue holds one key's products with
+// all heads in its own TMEM lane and the weighted sum needs no other thread.
+// One CTA per (sequence, group of its new tokens, range of positions): the
+// group's queries stay in shared memory, key tiles stream through a ring, and
+// two epilogue warpgroups take the (tile, token) units in turn, each with its
+// own TMEM buffer.  With one new token a sequence the call is bound by reading
+// the keys (256 or 128 bytes each, 64 heads: 64 flops a byte); with many it is
+// bound by the epilogue's two instructions a head and pair.
+constexpr int IT = 128;                             // keys of a tile
+constexpr int I_QMAX = 64 * 1024;                   // query bytes kept at most
+constexpr int I_RING = 128 * 1024;
+constexpr int kScoreThreads = 320;                  // producer, MMA, 2 x 4 epilogue warps
+constexpr int I_MAXG = 16;
+constexpr int I_AT_RING = I_QMAX;
+constexpr int I_AT_W = I_AT_RING + I_RING;          // weights [I_MAXG][128], at most 8 KB
+constexpr int I_AT_BAR = I_AT_W + I_MAXG * 128 * 4;
+constexpr int I_TOTAL = I_AT_BAR + 1024 + 1024;
+static_assert(I_TOTAL <= 227 * 1024, "shared memory");
+
+struct ScoreSmem {
+  uint64_t k_full[8], k_empty[8], q_full, d_full[2], d_free[2], drain;
+  uint32_t tmem;
+  int abort;
+  float part[2][4];
+};
+
+struct ScoreParams {
+  float* scores;
+  const float* w;
+  const uint8_t* keys;
+  const float* key_scales;
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages, block, B, Hi, NP, T, G, groups, splits, span, max_seq, stride, box;
+  int32_t* status;
+};
+
+__device__ __forceinline__ int score_row(const ScoreParams& p, int b, int pos) {
+  const int pi = pos / p.page_size;
+  const int page = pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
+  if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - pi * p.page_size);
+  set_status(p.status, MLA_DEV_BAD_PAGE);
+  return -1;
+}
+
+template <bool E8, bool DENSE>
+__global__ void __launch_bounds__(kScoreThreads, 1)
+    index_scores_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                        const ScoreParams p) {
+  constexpr int KB = E8 ? 1 : 2;                    // 128-byte blocks of a row
+  constexpr int ELT = E8 ? 1 : 2;
+  constexpr int STAGE = KB * IT * 128;
+  constexpr int STAGES = E8 ? 8 : 4;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  ScoreSmem* sh = reinterpret_cast<ScoreSmem*>(smem + I_AT_BAR);
+  float* sw = reinterpret_cast<float*>(smem + I_AT_W);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_enter();
+
+  const int sp = blockIdx.x % p.splits;
+  const int g = (blockIdx.x / p.splits) % p.groups;
+  const int b = blockIdx.x / p.splits / p.groups;
+  const uint32_t qa = p.iro[b], qe = p.iro[b + 1];
+  if (qe <= qa) return;
+  const uint64_t ctx = static_cast<uint64_t>(p.cache_len[b]) + (qe - qa);
+  if (qe > static_cast<uint32_t>(p.T) || ctx > static_cast<uint64_t>(p.max_seq)) {
+    if (threadIdx.x == 0) set_status(p.status, MLA_DEV_BAD_OFFSETS);
+    return;
+  }
+  const int n_new = static_cast<int>(qe - qa);
+  const int i0 = g * p.G;
+  if (i0 >= n_new) return;
+  const int ng = min(p.G, n_new - i0);
+  const int t0 = static_cast<int>(qa) + i0;
+  const int pos_first = static_cast<int>(p.cache_len[b]) + i0;   // position of the group's first token
+  const int pos_last = pos_first + ng - 1;
+  const long long tiles_all = (static_cast<long long>(p.stride) * p.block + IT - 1) / IT;
+  const long long tile0 = static_cast<long long>(sp) * p.span;
+  if (tile0 >= tiles_all) return;
+  const int tiles = static_cast<int>(min(static_cast<long long>(p.span), tiles_all - tile0));
+  const long long base0 = tile0 * IT;
+  const int n = base0 > pos_last ? 0 : static_cast<int>(min(static_cast<long long>(tiles), (pos_last - base0) / IT + 1));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&sh->k_full[s]), 1);
+      mbar_init(smem_u32(&sh->k_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh->q_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh->d_full[i]), 1);
+      mbar_init(smem_u32(&sh->d_free[i]), 4);
+    }
+    mbar_init(smem_u32(&sh->drain), 1);
+    sh->abort = timed_out_before(p.status) ? 1 : 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh->tmem), 256);
+    tmem_relinquish();
+  }
+  // The group's weights, heads past the last one zero.
+  for (int i = threadIdx.x; i < ng * p.NP; i += kScoreThreads) {
+    const int gi = i / p.NP, h = i - gi * p.NP;
+    sw[gi * 128 + h] = h < p.Hi ? __ldg(p.w + static_cast<long long>(t0 + gi) * p.Hi + h) : 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  volatile int* abort_flag = &sh->abort;
+  const bool dead = sh->abort != 0;                  // an earlier kernel timed out: no work
+
+  if (dead) {
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (n > 0 && elect_one()) {
+      const uint32_t qf = smem_u32(&sh->q_full);
+      mbar_expect_tx(qf, ng * KB * p.NP * 128);
+      for (int i = 0; i < ng; ++i)
+        for (int c = 0; c < KB; ++c)
+          tma_load_2d(smem_u32(smem + (i * KB + c) * p.NP * 128), &q_map, qf, c * (128 / ELT), (t0 + i) * p.Hi);
+    }
+    __syncwarp();
+    bool ok = true;
+    uint32_t issued = 0;
+    int pend = -1;
+    for (int j = 0; j < n && ok; ++j) {
+      const int pos0 = static_cast<int>(base0) + j * IT;
+      const uint32_t s = j % STAGES;
+      const uint32_t full = smem_u32(&sh->k_full[s]);
+      const uint32_t dst = smem_u32(smem + I_AT_RING + s * STAGE);
+      const int have = min(IT, pos_last + 1 - pos0);   // keys that some token sees
+      if constexpr (DENSE) {
+        const int boxes = (have + p.box - 1) / p.box;
+        int row = 0;
+        if (lane < boxes) {
+          row = score_row(p, b, pos0 + lane * p.box);
+          if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
+        }
+        if (j >= STAGES && !(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), ((j / STAGES) & 1) ^ 1, p.status, abort_flag)))
+          break;
+        if (lane == 0) mbar_expect_tx(full, boxes * p.box * 128 * KB);
+        __syncwarp();
+        if (lane < boxes)
+          for (int c = 0; c < KB; ++c)
+            tma_load_2d(dst + c * IT * 128 + lane * p.box * 128, &k_map, full, c * (128 / ELT), row);
+        __syncwarp();
+      } else {
+        int row[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          row[x] = 32 * x + lane < have ? score_row(p, b, pos0 + 32 * x + lane) : 0;
+          if (row[x] < 0) row[x] = 0;                    // reported
+        }
+        if (j >= STAGES) {
+          // The ring is full: what was copied has to be counted before waiting.
+          if (pend >= 0) {
+            cp_async_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
+            pend = -1;
+          }
+          if (!(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), ((j / STAGES) & 1) ^ 1, p.status, abort_flag))) break;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int r = 4 * i + (lane >> 3), ch = lane & 7;
+          const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
+#pragma unroll
+          for (int c = 0; c < KB; ++c)
+            cp_async16(dst + c * IT * 128 + r * 128 + ((ch ^ (r & 7)) << 4),
+                       p.keys + static_cast<size_t>(src) * (128 * KB) + c * 128 + ch * 16);
+        }
+        cp_async_commit();
+        if (pend >= 0) {
+          cp_async_wait<1>();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
+        }
+        pend = static_cast<int>(s);
+      }
+      ++issued;
+    }
+    if constexpr (!DENSE) {
+      cp_async_wait<0>();
+      fence_async_smem();
+      __syncwarp();
+      if (pend >= 0 && lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
+    }
+    volatile int never = 0;
+    if (n > 0) mbar_wait_warp(smem_u32(&sh->q_full), 0, p.status, &never);
+    for (uint32_t s = 0; s < STAGES; ++s)
+      if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / STAGES) & 1, p.status, &never);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (n > 0 && elect_one()) {
+      const uint32_t idesc = E8 ? idesc_e4m3(128, p.NP, false, false) : idesc_bf16(128, p.NP, false, false);
+      bool ok = mbar_wait(smem_u32(&sh->q_full), 0, p.status, abort_flag);
+      uint32_t u = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t s = j % STAGES;
+        if (!(ok = mbar_wait(smem_u32(&sh->k_full[s]), (j / STAGES) & 1, p.status, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + I_AT_RING + s * STAGE);
+        for (int i = 0; i < ng; ++i, ++u) {
+          if (u >= 2 && !(ok = mbar_wait(smem_u32(&sh->d_free[u & 1]), ((u >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + (u & 1) * 128;
+#pragma unroll
+          for (int c = 0; c < KB; ++c) {
+            const uint32_t q = smem_u32(smem + (i * KB + c) * p.NP * 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = sdesc(a + c * IT * 128 + kk * 32, 16, 1024), bd = sdesc(q + kk * 32, 16, 1024);
+              if (E8) mma_f8_ss(d, ad, bd, idesc, (c | kk) != 0);
+              else mma_f16_ss(d, ad, bd, idesc, (c | kk) != 0);
+            }
+          }
+          tc_commit(smem_u32(&sh->d_full[u & 1]));
+        }
+        tc_commit(smem_u32(&sh->k_empty[s]));
+      }
+      tc_commit(smem_u32(&sh->drain));
+      volatile int never = 0;
+      mbar_wait(smem_u32(&sh->drain), 0, p.status, &never);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ weighted sums
+    const int e = (warp - 2) >> 2;                   // epilogue warpgroup: units u with u & 1 == e
+    const int q4 = warp & 3;
+    const int key = q4 * 32 + lane;
+    const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * 128;
+    bool ok = true;
+    uint32_t u = 0, mine = 0;
+    for (int j = 0; j < n && ok; ++j) {
+      const int pos = static_cast<int>(base0) + j * IT + key;
+      float ks = 1.f;
+      if (p.key_scales != nullptr && pos <= pos_last) {
+        const int row = score_row(p, b, pos);
+        if (row >= 0) ks = __ldg(p.key_scales + row);
+      }
+      for (int i = 0; i < ng; ++i, ++u) {
+        if ((u & 1) != static_cast<uint32_t>(e)) continue;
+        ok = ok && mbar_wait_warp(smem_u32(&sh->d_full[e]), mine & 1, p.status, abort_flag);
+        ++mine;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (ok) {
+          tc_fence_after();
+          const float* w = sw + i * 128;
+          for (int c0 = 0; c0 < p.NP; c0 += 32) {
+            uint32_t x[32];
+            tmem_ld32(ta + c0, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 wv = *reinterpret_cast<const float4*>(w + c0 + c);
+              if (c0 + c + 4 <= p.Hi) {
+                acc[0] = fmaf(max_nan(__uint_as_float(x[c]), 0.f), wv.x, acc[0]);
+                acc[1] = fmaf(max_nan(__uint_as_float(x[c + 1]), 0.f), wv.y, acc[1]);
+                acc[2] = fmaf(max_nan(__uint_as_float(x[c + 2]), 0.f), wv.z, acc[2]);
+                acc[3] = fmaf(max_nan(__uint_as_float(x[c + 3]), 0.f), wv.w, acc[3]);
+              } else {
+                // Columns past the last head hold the next token's products.
+                if (c0 + c < p.Hi) acc[0] = fmaf(max_nan(__uint_as_float(x[c]), 0.f), wv.x, acc[0]);
+                if (c0 + c + 1 < p.Hi) acc[1] = fmaf(max_nan(__uint_as_float(x[c + 1]), 0.f), wv.y, acc[1]);
+                if (c0 + c + 2 < p.Hi) acc[2] = fmaf(max_nan(__uint_as_float(x[c + 2]), 0.f), wv.z, acc[2]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->d_free[e]));
+        }
+        float v = ((acc[0] + acc[1]) + (acc[2] + acc[3])) * ks;
+        if (pos > pos_first + i) v = -kInf;          // not visible to the token
+        float* dst = p.scores + static_cast<long long>(t0 + i) * p.stride;
+        if (p.block == 1) {
+          if (ok && pos < p.stride) dst[pos] = v;
+        } else {
+          const int in_warp = min(p.block, 32);
+          for (int d = 1; d < in_warp; d <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
+          if (p.block <= 32) {
+            if (ok && lane % p.block == 0 && pos / p.block < p.stride) dst[pos / p.block] = v;
+          } else {
+            // Blocks of 64 or 128 keys: two or four warps' maxima.  (A failed
+            // wait leaves this loop only at its end, so the barrier is met.)
+            if (lane == 0) sh->part[e][q4] = v;
+            asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
+            const int first = p.block == 64 ? (q4 & 2) : 0;
+            if (lane == 0 && q4 == first) {
+              float m = max_nan(sh->part[e][first], sh->part[e][first + 1]);
+              if (p.block == 128) m = max_nan(m, max_nan(sh->part[e][2], sh->part[e][3]));
+              if (ok && pos / p.block < p.stride) dst[pos / p.block] = m;
+            }
+            asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
+          }
+        }
+      }
+    }
+    // Blocks past the group's last key: -infinity.
+    const long long from = (base0 + static_cast<long long>(n) * IT) / p.block;
+    const long long to = min(static_cast<long long>(p.stride), (base0 + static_cast<long long>(tiles) * IT) / p.block);
+    const int tid = threadIdx.x - 64;
+    for (int i = 0; i < ng; ++i)
+      for (long long x = from + tid; x < to; x += 256) p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ============================================================ selection
+// A cluster of CTAs per token, each with a contiguous slice of the token's
+// block scores (kept in shared memory where it fits).  The k-th largest score
+// is found digit by digit (11, 11 and 10 bits of an order-preserving integer,
+// histograms summed over the cluster through distributed shared memory), then
+// the chosen blocks are written in position order: those above it, and as many
+// equal to it as are missing, lowest first.
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMaxCluster = 8;
+constexpr int kSelCacheFloats = 40 * 1024;           // slice kept in shared memory, 160 KB
+
+struct SelectSmem {
+  uint32_t hist[3][2048];
+  uint32_t scan[kSelWarps];
+  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  uint32_t total[2];           // chosen-for-sure and equal blocks of this CTA
+  uint32_t bin, need;
+  int seq, pos;
+};
+
+__device__ __forceinline__ uint32_t select_key(float s) {
+  if (s != s) s = -kInf;                             // NaN counts as -infinity
+  const uint32_t u = __float_as_uint(s + 0.0f);      // -0 becomes +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads)
+    index_select_kernel(const IndexSelectArgs a, int cached) {
+  extern __shared__ __align__(16) uint32_t cache[];
+  __shared__ SelectSmem sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t C = cluster_size(), rank = cluster_rank();
+  const int t = blockIdx.x / C;
+  pdl_enter();
+  if (tid == 0) {
+    int seq = -1, pos = 0;
+    if (!timed_out_before(a.status)) {
+      const int b = sequence_of(a.iro, a.B, t);
+      const uint32_t qa = a.iro[b], qe = a.iro[b + 1];
+      if (qa <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < qe) {
+        const uint64_t ctx = static_cast<uint64_t>(a.cache_len[b]) + (static_cast<uint32_t>(t) - qa);
+        if (ctx < static_cast<uint64_t>(a.max_seq) && qe <= static_cast<uint32_t>(a.T)) {
+          seq = b;
+          pos = static_cast<int>(ctx);
+        } else {
+          set_status(a.status, MLA_DEV_BAD_OFFSETS);
+        }
+      }
+    }
+    sh.seq = seq;
+    sh.pos = pos;
+  }
+  for (int i = tid; i < 3 * 2048; i += kSelThreads) (&sh.hist[0][0])[i] = 0u;
+  cluster_sync();
+  // The token's sequence is read from CTA 0, so that all CTAs agree.
+  const int seq = static_cast<int>(ld_cluster_u32(&sh.seq, 0)), pos = static_cast<int>(ld_cluster_u32(&sh.pos, 0));
+  if (seq < 0) {                                     // outside every sequence: left as it was
+    cluster_sync();
+    return;
+  }
+  const int nb = pos / a.block + 1;                  // visible blocks
+  const int k = min(a.top, nb);
+  const int slice = ((nb + static_cast<int>(C) - 1) / static_cast<int>(C) + 31) / 32 * 32;
+  const int lo = min(nb, static_cast<int>(rank) * slice), cnt = min(nb, lo + slice) - lo;
+  const float* src = a.scores + static_cast<long long>(t) * a.stride + lo;
+  const int local_from = nb - a.local - lo;          // slice index of the first always-chosen block
+  auto load = [&](int i) -> uint32_t { return i >= local_from ? 0xFFFFFFFFu : select_key(__ldg(src + i)); };
+  auto key = [&](int i) -> uint32_t { return cached ? cache[i] : load(i); };
+
+  uint32_t thr = 0u, need = 0u;
+  if (k < nb) {
+    need = k;
+    uint32_t mask = 0u;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      uint32_t* hist = sh.hist[pass];
+#pragma unroll 4
+      for (int i = tid; i < cnt; i += kSelThreads) {
+        uint32_t u;
+        if (pass == 0) {
+          u = load(i);
+          if (cached) cache[i] = u;
+        } else {
+          u = key(i);
+        }
+        if ((u & mask) == thr) atomicAdd(&hist[(u >> shift) & digits], 1u);
+      }
+      cluster_sync();
+      // Two digits a thread, from the largest down: the cluster's counts and
+      // how many keys have a larger digit.
+      const int d0 = 2047 - 2 * tid;
+      uint32_t c0 = 0, c1 = 0;
+      for (uint32_t r = 0; r < C; ++r) {
+        c0 += ld_cluster_u32(hist + d0, r);
+        c1 += ld_cluster_u32(hist + d0 - 1, r);
+      }
+      uint32_t incl = c0 + c1;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (lane == 31) sh.scan[warp] = incl;
+      __syncthreads();
+      uint32_t before = incl - c0 - c1;
+      for (int w = 0; w < warp; ++w) before += sh.scan[w];
+      if (before < need && need <= before + c0) {
+        sh.bin = d0;
+        sh.need = need - before;
+      } else if (before + c0 < need && need <= before + c0 + c1) {
+        sh.bin = d0 - 1;
+        sh.need = need - before - c0;
+      }
+      __syncthreads();
+      thr |= sh.bin << shift;
+      need = sh.need;
+      mask |= digits << shift;
+      __syncthreads();   // bin, need and scan are rewritten by the next pass
+    }
+  } else if (cached) {
+    for (int i = tid; i < cnt; i += kSelThreads) cache[i] = load(i);
+    __syncthreads();
+  }
+
+  // Chosen and equal blocks before each warp's part of the slice.
+  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int s0 = min(cnt, warp * seg), s1 = min(cnt, s0 + seg);
+  uint32_t gt = 0, eq = 0;
+  for (int i = s0; i < s1; i += 32) {
+    const uint32_t u = i + lane < s1 ? key(i + lane) : 0u;
+    const bool in = i + lane < s1;
+    gt += __popc(__ballot_sync(0xffffffffu, in && u > thr));
+    eq += __popc(__ballot_sync(0xffffffffu, in && u == thr));
+  }
+  if (lane == 0) {
+    sh.warp_gt[warp] = gt;
+    sh.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t x = 0, y = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      x += sh.warp_gt[w];
+      y += sh.warp_eq[w];
+    }
+    sh.total[0] = x;
+    sh.total[1] = y;
+  }
+  cluster_sync();
+  gt = eq = 0;
+  for (uint32_t r = 0; r < rank; ++r) {
+    gt += ld_cluster_u32(&sh.total[0], r);
+    eq += ld_cluster_u32(&sh.total[1], r);
+  }
+  for (int w = 0; w < warp; ++w) {
+    gt += sh.warp_gt[w];
+    eq += sh.warp_eq[w];
+  }
+
+  int32_t* out = a.rows + static_cast<long long>(t) * a.rows_stride;
+  const int32_t* table = a.page_table + static_cast<long long>(seq) * a.max_pages;
+  auto row_of = [&](int x) -> int32_t {
+    const int pi = x / a.page_size;
+    const int page = pi < a.max_pages ? __ldg(table + pi) : -1;
+    if (page >= 0 && page < a.num_pages) return page * a.page_size + (x - pi * a.page_size);
+    set_status(a.status, MLA_DEV_BAD_PAGE);
+    return -1;
+  };
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = s0; i < s1; i += 32) {
+    const bool in = i + lane < s1;
+    const uint32_t u = in ? key(i + lane) : 0u;
+    const uint32_t mg = __ballot_sync(0xffffffffu, in && u > thr), me = __ballot_sync(0xffffffffu, in && u == thr);
+    const uint32_t my_eq = eq + __popc(me & below);
+    const bool chosen = in && (u > thr || (u == thr && my_eq < need));
+    const uint32_t at = gt + __popc(mg & below) + min(my_eq, need);   // chosen blocks before
+    if (a.block == 1) {
+      if (chosen) out[at] = row_of(lo + i + lane);
+    } else {
+      uint32_t todo = __ballot_sync(0xffffffffu, chosen);
+      while (todo) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const long long o = static_cast<long long>(__shfl_sync(0xffffffffu, at, from)) * a.block;
+        const int first = (lo + i + from) * a.block;
+        for (int r = lane; r < a.block; r += 32) out[o + r] = first + r <= pos ? row_of(first + r) : -1;
+      }
+    }
+    // The last visible block may be cut by the token's position.
+    if (in && lo + i + lane == nb - 1)
+      a.count[t] = chosen ? (k - 1) * a.block + pos % a.block + 1 : k * a.block;
+    gt += __popc(mg);
+    eq += __popc(me);
+  }
+  for (long long x = static_cast<long long>(k) * a.block + rank * kSelThreads + tid; x < a.rows_stride; x += C * kSelThreads)
+    out[x] = -1;
+  cluster_sync();   // no CTA leaves while another may read its counts
+}
+
+}  // namespace
+
+cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
+  if (a.T == 0 || a.max_new == 0) return cudaSuccess;
+  const bool e8 = a.dtype == MLA_E4M3;
+  const int kb = e8 ? 1 : 2;
+  ScoreParams p;
+  p.scores = a.scores;
+  p.w = a.w;
+  p.keys = static_cast<const uint8_t*>(a.keys);
+  p.key_scales = a.key_scales;
+  p.iro = a.iro;
+  p.cache_len = a.cache_len;
+  p.page_table = a.page_table;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.block = a.block;
+  p.B = a.B;
+  p.Hi = a.Hi;
+  p.NP = (a.Hi + 15) / 16 * 16;
+  p.T = a.T;
+  p.max_seq = a.max_seq;
+  p.stride = a.stride;
+  p.status = a.status;
+  p.G = std::max(1, std::min({I_MAXG, a.max_new, I_QMAX / (p.NP * 128 * kb)}));
+  p.groups = (a.max_new + p.G - 1) / p.G;
+  int box = 1;
+  while (box < IT && a.page_size % (2 * box) == 0) box *= 2;
+  p.box = box;
+  // Ranges of positions: about two CTAs an SM, at least eight tiles each.
+  const long long tiles = (static_cast<long long>(a.stride) * a.block + IT - 1) / IT;
+  const long long pairs = static_cast<long long>(a.B) * p.groups;
+  long long span = (pairs * tiles + 2 * sm_count() - 1) / (2 * sm_count());
+  span = std::min(tiles, std::max(8ll, span));
+  p.span = static_cast<int>(span);
+  p.splits = static_cast<int>((tiles + span - 1) / span);
+  const long long items = pairs * p.splits;
+  if (items >= (1ll << 31)) return cudaErrorInvalidValue;
+  const CUtensorMapDataType dt = e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int cols = e8 ? 128 : 64;
+  const bool dense = box >= 8;
+  CUtensorMap q_map, k_map;
+  if (!encode_2d(&q_map, a.iq, dt, 128, static_cast<uint64_t>(a.T) * a.Hi, 128 * kb, cols, p.NP,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&k_map, a.keys, dt, 128, static_cast<uint64_t>(a.num_pages) * a.page_size, 128 * kb, cols,
+                 dense ? box : 8, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto go = [&](auto kernel) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I_TOTAL);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kScoreThreads), I_TOTAL, stream, q_map, k_map, p);
+  };
+  if (e8) return dense ? go(index_scores_kernel<true, true>) : go(index_scores_kernel<true, false>);
+  return dense ? go(index_scores_kernel<false, true>) : go(index_scores_kernel<false, false>);
+}
+
+cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream) {
+  if (a.T == 0) return cudaSuccess;
+  // One CTA a token, or, where the tokens leave SMs idle and the rows are
+  // long, up to eight (at least 4096 scores each).
+  int C = 1;
+  while (C < kSelMaxCluster && static_cast<long long>(a.T) * 2 * C <= sm_count() && a.stride / (2 * C) >= 4096) C *= 2;
+  const long long slice = ((static_cast<long long>(a.stride) + C - 1) / C + 31) / 32 * 32;
+  const int cached = slice <= kSelCacheFloats ? 1 : 0;
+  const size_t smem = cached ? static_cast<size_t>(slice) * 4 : 16;
+  cudaError_t e = cudaFuncSetAttribute(index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSelCacheFloats * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(C) * static_cast<unsigned>(a.T));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, index_select_kernel, a, cached);
+}
+
+}  // namespace mla

@@ -154,6 +154,99 @@ struct DecodePartitioning {
 DecodePartitioning decode_partitioning(int B, int H, int max_new, int max_keys);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
+// The 8-bit latent cache (cache_q8.cu): e4m3 rows, one power-of-two scale for
+// each block of scale_block slots of a page (scale_block divides page_size,
+// so cache row r has scale r / scale_block).
+struct CacheWriteQ8Args {
+  void* kv_cache;           // e4m3 [num_pages][page_size][576]
+  float* kv_scales;         // [num_pages * page_size / scale_block]
+  void* q;                  // bf16 [T][H][192] or null
+  const void* kv_latent;    // bf16 [T][576]
+  const float* gamma;       // [512]
+  const float* freqs;       // [max_seq_len][64]
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages, scale_block, B, H, T, max_seq_len;
+  float eps;
+  int32_t* status;
+};
+cudaError_t launch_cache_write_q8(const CacheWriteQ8Args& a, cudaStream_t stream);
+
+struct GatherQ8Args {
+  void* c_kv_buf;           // bf16 [S][512]
+  void* k_rope_buf;         // bf16 [S][64]
+  const void* kv_cache;
+  const float* kv_scales;
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages, scale_block;
+  const uint32_t* bro;
+  const uint32_t* co;
+  const int32_t* bl;
+  int chunk, B;
+  uint32_t S;
+  int32_t* status;
+};
+cudaError_t launch_gather_q8(const GatherQ8Args& a, cudaStream_t stream);
+
+// Absorbed MLA decode over the 8-bit cache (decode_q8.cu).
+struct DecodeQ8Args {
+  void* out;                  // [T][H][128] bf16
+  float* lse;                 // [T][H] or null
+  const void* q;              // [T][H][192] bf16
+  const void* kv_cache;       // e4m3 [num_pages][page_size][576]
+  const float* kv_scales;
+  const int32_t* page_table;  // [B][max_pages], or null with indices
+  int num_pages, page_size, max_pages, scale_block;
+  const void* w_uk;           // [H][512][128] bf16
+  const void* w_uv;           // [H][128][512] bf16
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  int B, H, T, max_new, max_seq, parts;
+  int part_keys;              // > 0: about this many keys a partition, at most `parts` of them
+  float scale;
+  const int32_t* indices;     // sparse: [B][indices_stride] physical cache rows, or null
+  int indices_stride;
+  const int32_t* topk;        // sparse: [B] or null
+  const float* sink;          // [B] or null
+  void* workspace;
+  int32_t* status;
+};
+struct DecodeQ8Layout {
+  size_t q8, q_scale, o_part, meta, total;
+};
+DecodeQ8Layout decode_q8_layout(int T, int H, int parts);
+DecodePartitioning decode_q8_partitioning(int B, int H, int max_new, int max_keys);
+cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream);
+
+// Key scores and block selection for sparse decode (index.cu).
+struct IndexScoresArgs {
+  float* scores;              // [T][stride]
+  const void* iq;             // [T][Hi][128]
+  const float* w;             // [T][Hi]
+  const void* keys;           // [num_pages][page_size][128]
+  const float* key_scales;    // [num_pages * page_size] or null
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages, block, B, Hi, T, max_new, max_seq, stride;
+  int dtype;
+  int32_t* status;
+};
+cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream);
+
+struct IndexSelectArgs {
+  int32_t* rows;              // [T][rows_stride]
+  int32_t* count;             // [T]
+  const float* scores;        // [T][stride]
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages, block, top, local, B, T, max_seq, stride, rows_stride;
+  int32_t* status;
+};
+cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream);
+
 // Self-test of the bounded waits (selftest.cu): one cluster of `cluster`
 // CTAs waiting on barriers nothing arrives at.
 cudaError_t launch_bounded_wait_selftest(int32_t* status, long long* elapsed_ns, uint64_t limit_ns,
