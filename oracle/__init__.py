@@ -24,3 +24,6 @@ def codes(t) -> np.ndarray:
     if t.dtype == torch.float8_e4m3fn:
         return t.view(torch.uint8).numpy()
     return t.numpy()
+
+
+from . import q8_oracle as q8  # noqa: E402,F401
