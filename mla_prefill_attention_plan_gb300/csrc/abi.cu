@@ -638,7 +638,7 @@ mla_status_t mla_gather_latent_q8(void* c_kv_buf, void* k_rope_buf, const void* 
 
 int32_t mla_decode_q8_partitions(int32_t batch_size, int32_t num_heads, int32_t max_new_tokens, int32_t max_keys) {
   if (batch_size < 1 || num_heads < 1) return 1;
-  return mla::decode_q8_partitioning(batch_size, num_heads, max_new_tokens, max_keys).parts;
+  return mla::decode_q8_pieces(batch_size, num_heads, max_new_tokens, max_keys);
 }
 
 size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, int32_t num_partitions) {
@@ -671,13 +671,15 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
     return MLA_ERR_ARG;
   if (total_q_tokens == 0 || max_new_tokens == 0) return MLA_OK;
   const int max_keys = d_indices != nullptr ? std::min(indices_stride, max_seq_len) : max_seq_len;
-  const mla::DecodePartitioning auto_parts =
-      mla::decode_q8_partitioning(batch_size, num_heads, max_new_tokens, max_keys);
-  const int parts = num_partitions > 0 ? num_partitions : auto_parts.parts;
-  const long long items = static_cast<long long>(batch_size) * parts *
-                          ((static_cast<long long>(max_new_tokens) * num_heads + 31) / 32);
-  if (items >= (1ll << 31)) return MLA_ERR_ARG;
-  const mla::DecodeQ8Layout L = mla::decode_q8_layout(total_q_tokens, num_heads, parts);
+  const int pieces = num_partitions > 0
+                         ? num_partitions
+                         : mla::decode_q8_pieces(batch_size, num_heads, max_new_tokens, max_keys);
+  // Units of the plan (one key tile of an item each, items of 32 rows or more) and CTAs.
+  const long long tiles = ((d_indices != nullptr ? indices_stride : max_seq_len) + 127ll) / 128;
+  const long long items = total_q_tokens + (rows + 31) / 32;
+  if (items * tiles >= (1ll << 31) || 8ll * pieces >= (1ll << 31) || 512 * (items + pieces) >= (1ll << 31))
+    return MLA_ERR_ARG;
+  const mla::DecodeQ8Layout L = mla::decode_q8_layout(total_q_tokens, num_heads, pieces);
   if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return MLA_ERR_WORKSPACE;
   mla::DecodeQ8Args a;
@@ -700,8 +702,7 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
   a.T = total_q_tokens;
   a.max_new = max_new_tokens;
   a.max_seq = max_seq_len;
-  a.parts = parts;
-  a.part_keys = num_partitions > 0 ? 0 : auto_parts.part_keys;
+  a.pieces = pieces;
   a.scale = scale;
   a.indices = d_indices;
   a.indices_stride = indices_stride;

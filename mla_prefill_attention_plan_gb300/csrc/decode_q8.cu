@@ -21,10 +21,20 @@
 //
 // Three launches:
 //   1. q8_query_kernel   u = w_uk[h] q per head (tcgen05, bf16), a power-of-two
-//      scale for each row, and the two terms: q8 [T*H][hi 576 | lo 576].
-//   2. q8_attn_kernel    one CTA per (sequence, row tile, key partition).
-//   3. q8_out_kernel     merges the partitions by LSE and multiplies by w_uv[h]
-//      (tcgen05, the latent result as two bf16 terms).
+//      scale for each row, and the two terms: q8 [T*H][hi 576 | lo 576].  Its
+//      first CTA also writes the plan: the batch's work as one line of units.
+//   2. q8_attn_kernel    one CTA per piece of that line (and row tile).
+//   3. q8_out_kernel     merges the pieces' results by LSE and multiplies by
+//      w_uv[h] (tcgen05, the latent result as two bf16 terms).
+//
+// The line: a sequence with n new tokens and L keys has ceil(n H / rows) row
+// tiles; `members` of them (a token's heads) make an item, and each item is
+// ceil(L / 128) units, one 128-key tile each.  The line of all items' units is
+// cut into `pieces` equal parts whatever the sequences' lengths, so every SM
+// gets the same number of tiles; the members of a piece walk it at the same
+// time on neighbouring CTAs and share its keys in L2.  A piece that ends inside
+// an item leaves a partial result in the slot (piece + item), which no other
+// (piece, item) pair has.
 #include <algorithm>
 #include <mutex>
 
@@ -36,17 +46,123 @@ namespace {
 constexpr float kLn2q = 0.693147180559945309f;
 constexpr float kInf = __builtin_huge_valf();
 
-// x as two e4m3 terms, for a pair of values given as packed f16: the codes of
-// the rounded values and of what that rounding left (the difference is exact).
-__device__ __forceinline__ uint16_t e4m3x2_from_f16x2(uint32_t v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+struct PlanEntry {     // a sequence with work, in batch order
+  int b, qa, n, cb;    // sequence, first token, new tokens, cached tokens (0 in the sparse form)
+  int L, tiles;        // keys, ceil(L / 128)
+  int units, items;    // units and items before it
+};
+struct PlanHead {
+  int entries, units;
+};
+struct PlanArgs {
+  PlanHead* head;
+  PlanEntry* entries;
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* topk;
+  int B, H, T, max_seq, indices_stride, sparse, item_rows;   // rows of an item: members * rows of a tile
+  int32_t* status;
+};
+constexpr int BK = 128;                     // keys of a tile
+
+// The plan, by 128 threads (tid) of one CTA: scans over the sequences, 128 at
+// a time.  A sequence is left out if it is empty, ends past the call's tokens,
+// begins before an earlier one ends, or (dense) is longer than max_seq; all but
+// the first are reported.  What is kept is disjoint and ascending, so there are
+// at most T entries.  `scr`: 4 x 4 ints.
+__device__ void q8_plan(const PlanArgs& a, int tid, int (*scr)[4]) {
+  const int warp = tid >> 5, lane = tid & 31;
+  int entries = 0, units = 0, items = 0;
+  uint32_t reach = 0;                       // end of the last sequence so far
+  for (int b0 = 0; b0 < a.B; b0 += 128) {
+    const int b = b0 + tid;
+    PlanEntry e;
+    e.b = b;
+    e.n = 0;
+    uint32_t qa = 0, qe = 0;
+    bool ok = false, some = false;
+    int u = 0, it = 0;
+    if (b < a.B) {
+      qa = __ldg(a.iro + b);
+      qe = __ldg(a.iro + b + 1);
+      const uint32_t cb = __ldg(a.cache_len + b);
+      some = qe != qa;
+      if (qe > qa && qe <= static_cast<uint32_t>(a.T)) {
+        const uint64_t ctx = static_cast<uint64_t>(cb) + (qe - qa);
+        e.qa = static_cast<int>(qa);
+        e.n = static_cast<int>(qe - qa);
+        e.cb = a.sparse ? 0 : static_cast<int>(cb);
+        if (a.sparse) {
+          const int k = a.topk != nullptr ? __ldg(a.topk + b) : a.indices_stride;
+          e.L = max(0, min(k, a.indices_stride));
+          ok = true;
+        } else {
+          e.L = static_cast<int>(ctx);
+          ok = ctx <= static_cast<uint64_t>(a.max_seq);
+        }
+        e.tiles = (e.L + BK - 1) / BK;
+      }
+    }
+    // Ends of the sequences before this one (of those that may be kept).
+    uint32_t end = ok ? qe : 0u;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end = max(end, o);
+    }
+    uint32_t before = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) before = 0u;
+    if (lane == 31) scr[0][warp] = static_cast<int>(end);
+    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+    before = max(before, reach);
+    for (int w = 0; w < warp; ++w) before = max(before, static_cast<uint32_t>(scr[0][w]));
+    if (some && (!ok || qa < before)) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+    ok = ok && qa >= before;
+    if (ok) {
+      it = static_cast<int>((static_cast<long long>(e.n) * a.H + a.item_rows - 1) / a.item_rows);
+      u = it * e.tiles;
+    }
+    int sc = ok ? 1 : 0, su = u, si = it;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sc, d), y = __shfl_up_sync(0xffffffffu, su, d);
+      const int z = __shfl_up_sync(0xffffffffu, si, d);
+      if (lane >= d) {
+        sc += x;
+        su += y;
+        si += z;
+      }
+    }
+    if (lane == 31) {
+      scr[1][warp] = sc;
+      scr[2][warp] = su;
+      scr[3][warp] = si;
+    }
+    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+    int at = entries + sc - (ok ? 1 : 0);
+    e.units = units + su - u;
+    e.items = items + si - it;
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) {
+        at += scr[1][w];
+        e.units += scr[2][w];
+        e.items += scr[3][w];
+      }
+      entries += scr[1][w];
+      units += scr[2][w];
+      items += scr[3][w];
+      reach = max(reach, static_cast<uint32_t>(scr[0][w]));
+    }
+    if (ok) {
+      reinterpret_cast<int4*>(a.entries + at)[0] = make_int4(e.b, e.qa, e.n, e.cb);
+      reinterpret_cast<int4*>(a.entries + at)[1] = make_int4(e.L, e.tiles, e.units, e.items);
+    }
+    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");   // scr is rewritten
+  }
+  if (tid == 0) {
+    a.head->entries = entries;
+    a.head->units = units;
+  }
 }
 
 // ============================================================ 1. queries
@@ -65,12 +181,13 @@ struct QuerySmem {
   uint32_t tmem;
   int abort;
   float amax[128];
+  int scr[4][4];
 };
 
 __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
     q8_query_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                     const uint16_t* __restrict__ q, uint8_t* __restrict__ q8, float* __restrict__ q_scale, int T,
-                    int H, int32_t* status) {
+                    int H, int32_t* status, const PlanArgs plan) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   QuerySmem* sh = reinterpret_cast<QuerySmem*>(smem + Q_SMEM_BAR);
@@ -134,6 +251,7 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
     }
     __syncwarp();
   } else if (work) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) q8_plan(plan, threadIdx.x - 64, sh->scr);
     ok = mbar_wait_warp(smem_u32(&sh->done), 0, status, abort_flag);
     if (ok) {
       tc_fence_after();
@@ -216,25 +334,29 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
 }
 
 // ============================================================ 2. attention
-constexpr int BK = 128;                     // keys of a tile
 constexpr int SLOT = BK * 128;              // one 128-column latent block of a tile, 16 KB
 constexpr int ROPE = BK * 64;               // its rope part, 8 KB
 constexpr float kShift = 5.0f;              // weights are kept around 2^5 of e4m3's 448
 constexpr float kGrow = 8.0f;               // and may grow to 2^8 before the reference moves
-constexpr uint32_t TM_S = 0, TM_O = 128;    // TMEM: scores 2 x 64 columns, O^T 4 x 64
-constexpr uint32_t TM_COLS = 512;
 
-// WIDE: 64 query rows, the two terms as two MMAs of N = 64.  Narrow: 32 query
-// rows, both terms side by side in one MMA of N = 64 (an MMA this small is
-// paced by its A operand, so the second term is free), the halves added when
-// they are read; the smaller query buffer leaves room for two more key slots.
+// A tile has 64 (WIDE) or 32 query rows.  The query operand holds both terms,
+// the first terms' rows above the second's, so one MMA of N = 128 or 64 gives
+// both products and the softmax adds them.  The weights' terms: 32 rows lie side
+// by side in one operand of N = 64 and O has two halves, added when it is read;
+// for 64 rows that would fill the whole TMEM with O, so there the terms are two
+// MMAs of N = 64 on the same accumulator.  (An MMA of M = 128 from shared
+// memory takes 40, 48, 64 clk at N = 32, 64, 128, measured: half of it at
+// N = 64 is its A operand's 128 bytes a clk.)  The smaller query buffer leaves
+// room for two more key slots.
 template <bool WIDE>
 struct Shape {
   static constexpr int ROWS = WIDE ? 64 : 32;
+  static constexpr int COLS = ROWS / 2;                   // rows of a softmax warpgroup
+  static constexpr int NQ = 2 * ROWS;                     // score columns of a tile
   static constexpr int SLOTS = WIDE ? 8 : 10;
   static constexpr int ROPES = WIDE ? 1 : 2;
-  static constexpr int QTERM = 4 * 8192 + 4096;           // 64 operand rows x 576
-  static constexpr int QBYTES = WIDE ? 2 * QTERM : QTERM;
+  static constexpr int QBLOCK = NQ * 128;                 // query operand, 128 columns
+  static constexpr int QBYTES = NQ * 576;
   static constexpr int PTERM = BK * 64;
   static constexpr int PBYTES = WIDE ? 2 * PTERM : PTERM;
   static constexpr int AT_ROPE = SLOTS * SLOT;
@@ -242,105 +364,163 @@ struct Shape {
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
   static constexpr int TOTAL = AT_BAR + 1920 + 1024;
-  static_assert(TOTAL <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x 64 columns
+  static constexpr uint32_t TM_COLS = 512;
+  static_assert(TOTAL <= 227 * 1024 && TM_O + 256 <= TM_COLS, "shared memory, TMEM");
 };
 
 struct AttnSmem {
   uint64_t k_full[10], k_empty[10];
   uint64_t r_full[2], r_empty[2];
-  uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+  uint64_t q_full, q_free, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem;
   int abort;
-  float2 rn[64];       // per query row: factor on the raw score, minus the reference (log2)
-  float f[64], d[64];  // a moved reference: factor on what was summed, step of the exponent
-  int lim[64];         // keys of the partition that the row sees
+  alignas(16) float rf[64];   // per query row: factor on the raw score,
+  alignas(16) float ry[64];   // minus the reference (log2 units),
+  alignas(16) float f[64];    // when that moves: factor on what was summed,
+  alignas(16) float d[64];    // and step of the exponent;
+  int top[64];                // largest weight of a row (order-preserving integers)
+  int lim[64];                // keys of the segment that the row sees
 };
 static_assert(sizeof(AttnSmem) <= 1920, "barrier block");
 
 struct Q8Params {
+  const PlanHead* head;
+  const PlanEntry* entries;
   const float* q_scale;
   const float* kv_scales;
   const uint8_t* kv_cache;
-  const uint32_t* iro;
-  const uint32_t* cache_len;
   const int32_t* page_table;
   const int32_t* indices;
-  const int32_t* topk;
-  __half* o_part;          // [parts][R][512], O / (sum of weights * smax)
-  float2* meta;            // [parts][R]: LSE in log2, smax (the partition's largest row scale)
+  __half* o_part;          // [slot][members][rows][512], O / (sum of weights * smax)
+  float2* meta;            // [slot][members][rows]: LSE in log2, smax (the segment's largest row scale)
   int indices_stride, num_pages, page_size, max_pages, scale_block;
-  int B, H, R, parts, part_keys, m_tiles, max_seq, box;
+  int H, R, T, pieces, members, box;
   float scale_log2;
   int32_t* status;
 };
 
-// A sequence's new tokens and keys; false where it is left out (reported once).
-struct SeqInfo {
-  int qa, n;           // first token, new tokens
-  int cb, L;           // cached tokens, keys
-};
-__device__ __forceinline__ bool q8_seq(const Q8Params& p, int b, SeqInfo& s) {
-  const uint32_t qa = p.iro[b], qe = p.iro[b + 1];
-  const uint32_t cb = p.cache_len[b];
-  if (qe <= qa) return false;
-  const uint64_t ctx = static_cast<uint64_t>(cb) + (qe - qa);
-  if (static_cast<uint64_t>(qe) * static_cast<uint32_t>(p.H) > static_cast<uint64_t>(p.R) ||
-      (p.indices == nullptr && ctx > static_cast<uint64_t>(p.max_seq))) {
-    set_status(p.status, MLA_DEV_BAD_OFFSETS);
-    return false;
-  }
-  s.qa = static_cast<int>(qa);
-  s.n = static_cast<int>(qe - qa);
-  s.cb = p.indices == nullptr ? static_cast<int>(cb) : 0;
-  if (p.indices != nullptr) {
-    const int k = p.topk != nullptr ? p.topk[b] : p.indices_stride;
-    s.L = max(0, min(k, p.indices_stride));
-  } else {
-    s.L = static_cast<int>(ctx);
-  }
-  return true;
+__device__ __forceinline__ PlanEntry load_entry(const PlanEntry* e) {
+  const int4 x = __ldg(reinterpret_cast<const int4*>(e)), y = __ldg(reinterpret_cast<const int4*>(e) + 1);
+  PlanEntry r;
+  r.b = x.x; r.qa = x.y; r.n = x.z; r.cb = x.w;
+  r.L = y.x; r.tiles = y.y; r.units = y.z; r.items = y.w;
+  return r;
 }
-__device__ __forceinline__ int q8_part_count(const Q8Params& p, int L) {
-  if (p.part_keys <= 0) return p.parts;
-  return max(1, min(p.parts, (L + p.part_keys - 1) / p.part_keys));
+// First unit of piece g, and the piece of unit u.
+__device__ __forceinline__ int piece_begin(int g, int pieces, int units) {
+  return static_cast<int>(static_cast<long long>(g) * units / pieces);
 }
-__device__ __forceinline__ int q8_part_size(int L, int count) {
-  const int per = L / count + (L % count != 0);
-  return per <= 0x7FFFFF00 ? (per + BK - 1) / BK * BK : 0x7FFFFF00;
+__device__ __forceinline__ int piece_of(int u, int pieces, int units) {
+  return static_cast<int>((static_cast<long long>(u + 1) * pieces - 1) / units);
 }
 
-// Cache row of key `pos` of sequence b, or -1 (reported).
-__device__ __forceinline__ int q8_row(const Q8Params& p, int b, int pos) {
+// One item's share of a piece.
+struct Segment {
+  int b, n;              // sequence, tiles to visit
+  int row0, nrows;       // first global query row of this CTA's tile, valid rows
+  int r0;                // first row of the tile within the sequence's rows
+  int cb;                // cached tokens
+  int key0, key1;        // keys (key1 before the tile's causal limit)
+  int slot;
+};
+
+// The segments of a piece in order.  Every role of the CTA walks them by itself.
+struct Walk {
+  int u, u1, e, entries, units;
+  PlanEntry pe;
+};
+__device__ __forceinline__ Walk walk_begin(const Q8Params& p, int piece) {
+  Walk w;
+  w.entries = __ldg(&p.head->entries);
+  w.units = __ldg(&p.head->units);
+  w.e = 0;
+  // No more pieces than units, so that none between two others is empty.
+  const int pieces = min(p.pieces, w.units);
+  w.u = w.u1 = 0;
+  if (piece >= pieces) return w;
+  w.u = piece_begin(piece, pieces, w.units);
+  w.u1 = piece_begin(piece + 1, pieces, w.units);
+  if (w.u < w.u1) {
+    // Last entry with units <= u that has any (a search over ascending numbers;
+    // entries without units share the next one's number and come before it).
+    int lo = 0, hi = w.entries;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(&p.entries[mid].units) <= w.u) lo = mid; else hi = mid;
+    }
+    w.e = lo;
+    w.pe = load_entry(p.entries + lo);
+  }
+  return w;
+}
+template <int ROWS>
+__device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member, int piece, Segment& s) {
+  while (w.u < w.u1) {
+    if (w.u >= w.pe.units + w.pe.tiles * static_cast<int>((static_cast<long long>(w.pe.n) * p.H + p.members * ROWS - 1) / (p.members * ROWS))) {
+      w.pe = load_entry(p.entries + ++w.e);          // units remain, so there is one
+      continue;
+    }
+    const int off = w.u - w.pe.units;
+    const int item = off / w.pe.tiles, tile = off - item * w.pe.tiles;
+    const int len = min(w.pe.tiles - tile, w.u1 - w.u);
+    w.u += len;
+    const long long rows = static_cast<long long>(w.pe.n) * p.H;
+    const long long r0 = (static_cast<long long>(item) * p.members + member) * ROWS;
+    if (r0 >= rows) continue;
+    s.b = w.pe.b;
+    s.r0 = static_cast<int>(r0);
+    s.nrows = static_cast<int>(min(static_cast<long long>(ROWS), rows - r0));
+    s.row0 = static_cast<int>(static_cast<long long>(w.pe.qa) * p.H + r0);
+    s.cb = w.pe.cb;
+    s.key0 = tile * BK;
+    s.key1 = min(w.pe.L, (tile + len) * BK);
+    if (p.indices == nullptr)   // causal: the tile's last token sees keys up to cb + i
+      s.key1 = min(s.key1, s.cb + (s.r0 + s.nrows - 1) / p.H + 1);
+    if (s.key1 <= s.key0) continue;
+    s.n = (s.key1 - s.key0 + BK - 1) / BK;
+    s.slot = (piece + w.pe.items + item) * p.members + member;
+    return true;
+  }
+  return false;
+}
+
+// Cache row of key `pos` of sequence b, in two steps, so that the table read can
+// be issued a tile or more before its value is looked at: the page id (or the
+// listed row), then the row or -1 (reported).
+__device__ __forceinline__ int q8_entry(const Q8Params& p, int b, int pos) {
+  if (p.indices != nullptr) return __ldg(p.indices + static_cast<long long>(b) * p.indices_stride + pos);
+  const int pi = pos / p.page_size;
+  return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
+}
+__device__ __forceinline__ int q8_row(const Q8Params& p, int pos, int entry) {
   int row = -1;
   if (p.indices != nullptr) {
-    row = p.indices[static_cast<long long>(b) * p.indices_stride + pos];
-    if (row < 0 || row >= p.num_pages * p.page_size) row = -1;
-  } else {
-    const int pi = pos / p.page_size;
-    const int page = pi < p.max_pages ? p.page_table[static_cast<long long>(b) * p.max_pages + pi] : -1;
-    if (page >= 0 && page < p.num_pages) row = page * p.page_size + (pos - pi * p.page_size);
+    if (entry >= 0 && entry < p.num_pages * p.page_size) row = entry;
+  } else if (entry >= 0 && entry < p.num_pages) {
+    row = entry * p.page_size + pos % p.page_size;
   }
   if (row < 0) set_status(p.status, MLA_DEV_BAD_PAGE);
   return row;
 }
 
-// Vote of the four softmax warps: whether any has a weight out of range, and
-// whether any wait of theirs failed.  Both are uniform over the 128 threads, so
-// that they leave their loop together.
-__device__ __forceinline__ void softmax_vote(bool bad, bool fail, bool& any_bad, bool& any_fail) {
+// Vote of a softmax warpgroup's four warps: whether any has a weight out of
+// range, and whether any wait of theirs failed.  Both are uniform over the 128
+// threads, so that they leave their loop together.
+__device__ __forceinline__ void softmax_vote(int bar, bool bad, bool fail, bool& any_bad, bool& any_fail) {
   const int lane = threadIdx.x & 31;
   const int mine = lane == 0 ? (bad ? 1 : 0) : (lane <= 5 ? (fail ? 1 : 0) : 0);
   int n;
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.popc.aligned.u32 %0, 1, 128, p;\n\t}"
+      "barrier.cta.red.popc.aligned.u32 %0, %2, 128, p;\n\t}"
       : "=r"(n)
-      : "r"(mine)
+      : "r"(mine), "r"(bar)
       : "memory");
   any_fail = n >= 5;
   any_bad = n % 5 != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync(int bar) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(bar) : "memory"); }
 
 // Order-preserving integer of a float (for the integer warp maximum) and back.
 __device__ __forceinline__ int float_order(float x) {
@@ -349,67 +529,59 @@ __device__ __forceinline__ int float_order(float x) {
 }
 __device__ __forceinline__ float order_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
-constexpr int kSparseProducers = 2;   // eight warps in all, so that a thread may have 255 registers
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_st32(addr, r); else tmem_st16(addr, r);
+}
+
+constexpr int kSparseProducers = 2;
+constexpr int kAttnThreads = 320;           // producer, MMA, 2 x 4 softmax warps; + 2 copying warps if not DENSE
 
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
 // multiple of 8) two warps copy the rows with cp.async.
 template <bool DENSE, bool WIDE>
-__global__ void __launch_bounds__(DENSE ? 192 : 192 + 32 * kSparseProducers, 1)
+__global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSparseProducers, 1)
     q8_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qr_map,
                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
                    const Q8Params p) {
   using C = Shape<WIDE>;
-  constexpr int ROWS = C::ROWS, SLOTS = C::SLOTS, ROPES = C::ROPES;
-  constexpr uint32_t IDESC_QK = idesc_e4m3(128, 64, false, false);
+  constexpr int ROWS = C::ROWS, COLS = C::COLS, SLOTS = C::SLOTS, ROPES = C::ROPES, NQ = C::NQ;
+  constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_COLS = C::TM_COLS;
+  constexpr uint32_t IDESC_QK = idesc_e4m3(128, NQ, false, false);
   constexpr uint32_t IDESC_PV = idesc_e4m3(128, 64, true, true);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   AttnSmem* sh = reinterpret_cast<AttnSmem*>(smem + C::AT_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int member = blockIdx.x % p.members, piece = blockIdx.x / p.members;
   int32_t* status = p.status;
   pdl_enter();
 
-  // The item: row tile m of sequence b, key partition k.  Row tiles are
-  // neighbours, so that they share their keys in L2.
-  const int m = blockIdx.x % p.m_tiles;
-  const int b = (blockIdx.x / p.m_tiles) % p.B;
-  const int k = blockIdx.x / p.m_tiles / p.B;
-  SeqInfo sq;
-  if (!q8_seq(p, b, sq)) return;
-  const long long rows_b = static_cast<long long>(sq.n) * p.H;
-  const long long r0 = static_cast<long long>(m) * ROWS;
-  if (r0 >= rows_b) return;
-  const int nrows = static_cast<int>(min(static_cast<long long>(ROWS), rows_b - r0));
-  const int row0 = static_cast<int>(static_cast<long long>(sq.qa) * p.H + r0);
-  const int count = q8_part_count(p, sq.L);
-  const int size = q8_part_size(sq.L, count);
-  if (k >= count || static_cast<long long>(k) * size >= sq.L) return;
-  const int key0 = k * size;
-  int key1 = min(sq.L, key0 + size);
-  if (p.indices == nullptr) {   // causal: the tile's last token sees keys up to cb + i
-    key1 = min(key1, sq.cb + static_cast<int>((r0 + nrows - 1) / p.H) + 1);
-    if (key1 <= key0) return;
-  }
-  const int n = (key1 - key0 + BK - 1) / BK;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(smem_u32(&sh->k_full[s]), DENSE ? 1 : kSparseProducers);
+      mbar_init(smem_u32(&sh->k_full[s]), DENSE ? 1 : 32 * kSparseProducers);
       mbar_init(smem_u32(&sh->k_empty[s]), 1);
     }
     for (int s = 0; s < ROPES; ++s) {
-      mbar_init(smem_u32(&sh->r_full[s]), DENSE ? 1 : kSparseProducers);
+      mbar_init(smem_u32(&sh->r_full[s]), DENSE ? 1 : 32 * kSparseProducers);
       mbar_init(smem_u32(&sh->r_empty[s]), 1);
     }
     mbar_init(smem_u32(&sh->q_full), 1);
+    mbar_init(smem_u32(&sh->q_free), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh->s_full[i]), 1);
-      mbar_init(smem_u32(&sh->s_free[i]), 4);
+      mbar_init(smem_u32(&sh->s_free[i]), 8);
     }
-    mbar_init(smem_u32(&sh->p_full), 4);
+    mbar_init(smem_u32(&sh->p_full), 8);
     mbar_init(smem_u32(&sh->pv_done), 1);
+    mbar_init(smem_u32(&sh->o_free), 8);
     mbar_init(smem_u32(&sh->drain), 1);
+    // An earlier kernel timed out: no work (and no plan to read).
     sh->abort = timed_out_before(status) ? 1 : 0;
     fence_mbar_init();
   }
@@ -422,452 +594,542 @@ __global__ void __launch_bounds__(DENSE ? 192 : 192 + 32 * kSparseProducers, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
   volatile int* abort_flag = &sh->abort;
+  const bool dead = sh->abort != 0;
+  __syncthreads();                                   // the flag may be raised from here on
+  Segment sg;
+  Walk wk;
+  if (!dead) wk = walk_begin(p, piece); else wk.u = wk.u1 = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ queries, and the keys' TMA loads
-    if (elect_one()) {
-      const uint32_t qf = smem_u32(&sh->q_full);
-      mbar_expect_tx(qf, C::QBYTES);
+    uint32_t seg = 0, issued = 0, r_issued = 0;
+    bool ok = true;
+    while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      auto load_q = [&]() -> bool {
+        if (seg > 0 && !mbar_wait_warp(smem_u32(&sh->q_free), (seg - 1) & 1, status, abort_flag)) return false;
+        if (elect_one()) {
+          const uint32_t qf = smem_u32(&sh->q_full);
+          mbar_expect_tx(qf, C::QBYTES);
 #pragma unroll
-      for (int term = 0; term < 2; ++term) {
-        // Wide: one buffer a term.  Narrow: the terms are rows 0..31 and 32..63 of one.
-        const uint32_t base = smem_u32(smem + C::AT_Q + (WIDE ? term * C::QTERM : 0));
+          for (int term = 0; term < 2; ++term) {
+            // The second term's rows follow the first's.
+            const uint32_t base = smem_u32(smem + C::AT_Q);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tma_load_2d(base + c * 8192 + (WIDE ? 0 : term * 4096), &q_map, qf, term * 576 + c * 128, row0);
-        tma_load_2d(base + 32768 + (WIDE ? 0 : term * 2048), &qr_map, qf, term * 576 + 512, row0);
+            for (int c = 0; c < 4; ++c)
+              tma_load_2d(base + c * C::QBLOCK + term * ROWS * 128, &q_map, qf, term * 576 + c * 128, sg.row0);
+            tma_load_2d(base + 4 * C::QBLOCK + term * ROWS * 64, &qr_map, qf, term * 576 + 512, sg.row0);
+          }
+        }
+        __syncwarp();
+        ++seg;
+        return true;
+      };
+      if constexpr (DENSE) {
+        const int nbox = BK / p.box;                      // runs of a tile, 16 at most
+        const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
+        // Lane l has run l % nbox of tile j0 + l / nbox; the next tiles' table
+        // entries are read while these are loaded.
+        auto entry_of = [&](int j0) -> int {
+          const int pos = sg.key0 + j0 * BK + lane * p.box;
+          return pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
+        };
+        int entry = entry_of(0), row = 0;
+        // A later segment's queries wait for the scores before them; its first
+        // keys need not.
+        const bool late = seg > 0;
+        if (!late) ok = load_q();
+        for (int j = 0; j < sg.n && ok; ++j) {
+          const int at = j % span;
+          if (at == 0) {
+            const int pos = sg.key0 + j * BK + lane * p.box;
+            row = pos < sg.key1 ? q8_row(p, pos, entry) : 0;
+            if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
+            entry = entry_of(j + span);
+          }
+          const int boxes = min(nbox, (sg.key1 - (sg.key0 + j * BK) + p.box - 1) / p.box);   // runs that hold a key
+#pragma unroll
+          for (int c = 0; c < 5; ++c) {
+            const uint32_t s = c < 4 ? issued % SLOTS : r_issued % ROPES;
+            const uint32_t turn = c < 4 ? issued / SLOTS : r_issued / ROPES;
+            const uint32_t empty = smem_u32(c < 4 ? &sh->k_empty[s] : &sh->r_empty[s]);
+            const uint32_t full = smem_u32(c < 4 ? &sh->k_full[s] : &sh->r_full[s]);
+            const uint32_t dst = smem_u32(smem + (c < 4 ? s * SLOT : C::AT_ROPE + s * ROPE));
+            constexpr int W[5] = {128, 128, 128, 128, 64};
+            if (turn > 0 && !(ok = mbar_wait_warp(empty, (turn & 1) ^ 1, status, abort_flag))) break;
+            if (elect_one()) mbar_expect_tx(full, boxes * p.box * W[c]);
+            for (int x = 0; x < boxes; ++x) {
+              const int r = __shfl_sync(0xffffffffu, row, at * nbox + x);
+              if (elect_one()) tma_load_2d(dst + x * p.box * W[c], c < 4 ? &k_map : &kr_map, full, c * 128, r);
+            }
+            if (c < 4) ++issued; else ++r_issued;
+          }
+          if (late && j == 0 && ok) ok = load_q();
+        }
+      } else {
+        ok = load_q();
       }
     }
-    __syncwarp();
-    uint32_t issued = 0, r_issued = 0;
+    // Every load lands before the CTA leaves.
+    volatile int never = 0;
     if constexpr (DENSE) {
-      const int nbox = BK / p.box;
-      bool ok = true;
-      for (int j = 0; j < n && ok; ++j) {
-        const int pos0 = key0 + j * BK;
-        const int boxes = min(nbox, (key1 - pos0 + p.box - 1) / p.box);   // runs that hold a key
-        int row = 0;
-        if (lane < boxes) {
-          row = q8_row(p, b, pos0 + lane * p.box);
-          if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
-        }
-        for (int c = 0; c < 5; ++c) {
-          const bool rope = c == 4;
-          const uint32_t u = rope ? r_issued : issued;
-          const uint32_t cap = rope ? ROPES : SLOTS;
-          const uint32_t s = u % cap;
-          uint64_t* empty = rope ? &sh->r_empty[s] : &sh->k_empty[s];
-          if (u >= cap && !(ok = mbar_wait_warp(smem_u32(empty), ((u / cap) & 1) ^ 1, status, abort_flag))) break;
-          const uint32_t full = smem_u32(rope ? &sh->r_full[s] : &sh->k_full[s]);
-          const int width = rope ? 64 : 128;
-          if (lane == 0) mbar_expect_tx(full, boxes * p.box * width);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = smem_u32(smem + (rope ? C::AT_ROPE + s * ROPE : s * SLOT)) + lane * p.box * width;
-            tma_load_2d(dst, rope ? &kr_map : &k_map, full, c * 128, row);
-          }
-          __syncwarp();
-          if (rope) ++r_issued; else ++issued;
-        }
-      }
-      // Every load lands before the CTA leaves.
-      volatile int never = 0;
       for (uint32_t s = 0; s < SLOTS; ++s)
         if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / SLOTS) & 1, status, &never);
       for (uint32_t s = 0; s < ROPES; ++s)
         if (r_issued > s) mbar_wait_warp(smem_u32(&sh->r_full[s]), ((r_issued - 1 - s) / ROPES) & 1, status, &never);
     }
-    volatile int never_q = 0;
-    mbar_wait_warp(smem_u32(&sh->q_full), 0, status, &never_q);
+    if (seg > 0) mbar_wait_warp(smem_u32(&sh->q_full), (seg - 1) & 1, status, &never);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
       const uint32_t q0 = smem_u32(smem + C::AT_Q);
       const uint32_t p0 = smem_u32(smem + C::AT_P);
-      auto issue_qk = [&](int j) -> bool {
-        const uint32_t sb = j & 1;
-        if (j >= 2 && !mbar_wait(smem_u32(&sh->s_free[sb]), ((j >> 1) & 1) ^ 1, status, abort_flag)) return false;
-        const uint32_t d = tmem + TM_S + sb * 64;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t u = 4 * j + c, s = u % SLOTS;
-          if (!mbar_wait(smem_u32(&sh->k_full[s]), (u / SLOTS) & 1, status, abort_flag)) return false;
-          tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * SLOT);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = sdesc(a + kk * 32, 16, 1024);
-            mma_f8_ss(d, ad, sdesc(q0 + c * 8192 + kk * 32, 16, 1024), IDESC_QK, (c | kk) != 0);
-            if (WIDE) mma_f8_ss(d, ad, sdesc(q0 + C::QTERM + c * 8192 + kk * 32, 16, 1024), IDESC_QK, 1);
-          }
-        }
-        const uint32_t rs = j % ROPES;
-        if (!mbar_wait(smem_u32(&sh->r_full[rs]), (j / ROPES) & 1, status, abort_flag)) return false;
+      // A block of a tile's scores: latent block c, or (c = 4) the rope part.
+      // `g`: the tile's number in the CTA.
+      auto qk_block = [&](uint32_t g, int c, bool last) {
+        const uint32_t d = tmem + TM_S + (g & 1) * NQ;
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + C::AT_ROPE + rs * ROPE);
+        if (!DENSE) fence_async_smem();              // the rows came by cp.async
+        if (c < 4) {
+          const uint32_t a = smem_u32(smem + ((4 * g + c) % SLOTS) * SLOT);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const uint64_t ad = sdesc(a + kk * 32, 16, 512, kSwizzle64);
-          mma_f8_ss(d, ad, sdesc(q0 + 32768 + kk * 32, 16, 512, kSwizzle64), IDESC_QK, 1);
-          if (WIDE) mma_f8_ss(d, ad, sdesc(q0 + C::QTERM + 32768 + kk * 32, 16, 512, kSwizzle64), IDESC_QK, 1);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_ss(d, sdesc(a + kk * 32, 16, 1024), sdesc(q0 + c * C::QBLOCK + kk * 32, 16, 1024), IDESC_QK,
+                      (c | kk) != 0);
+        } else {
+          const uint32_t a = smem_u32(smem + C::AT_ROPE + (g % ROPES) * ROPE);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+            mma_f8_ss(d, sdesc(a + kk * 32, 16, 512, kSwizzle64),
+                      sdesc(q0 + 4 * C::QBLOCK + kk * 32, 16, 512, kSwizzle64), IDESC_QK, 1);
+          tc_commit(smem_u32(&sh->s_full[g & 1]));
+          tc_commit(smem_u32(&sh->r_empty[g % ROPES]));
+          if (last) tc_commit(smem_u32(&sh->q_free));
         }
-        tc_commit(smem_u32(&sh->s_full[sb]));
-        tc_commit(smem_u32(&sh->r_empty[rs]));
-        return true;
       };
-      auto issue_pv = [&](int j) -> bool {
-        if (!mbar_wait(smem_u32(&sh->p_full), j & 1, status, abort_flag)) return false;
+      auto issue_pv = [&](uint32_t g, bool first) {
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const uint32_t s = (4 * j + c) % SLOTS;
+          const uint32_t s = (4 * g + c) % SLOTS;
           const uint32_t a = smem_u32(smem + s * SLOT);
           const uint32_t d = tmem + TM_O + c * 64;
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk) {
             // 32 keys a step: both operands MN-major, groups of 8 keys 1024 (keys) and 512 (weights) bytes apart.
             const uint64_t ad = sdesc(a + kk * 4096, 16, 1024);
-            mma_f8_ss(d, ad, sdesc(p0 + kk * 2048, 16, 512, kSwizzle64), IDESC_PV, (j | kk) != 0);
+            mma_f8_ss(d, ad, sdesc(p0 + kk * 2048, 16, 512, kSwizzle64), IDESC_PV, !first || kk != 0);
             if (WIDE) mma_f8_ss(d, ad, sdesc(p0 + C::PTERM + kk * 2048, 16, 512, kSwizzle64), IDESC_PV, 1);
           }
           tc_commit(smem_u32(&sh->k_empty[s]));
         }
         tc_commit(smem_u32(&sh->pv_done));
-        return true;
       };
-      bool ok = mbar_wait(smem_u32(&sh->q_full), 0, status, abort_flag);
-      if (ok) ok = issue_qk(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) ok = issue_qk(j + 1);
-        if (ok) ok = issue_pv(j);
+      uint32_t seg = 0, g0 = 0;                        // segments done, tiles before this segment
+      bool ok = true;
+      while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+        if (!(ok = mbar_wait(smem_u32(&sh->q_full), seg & 1, status, abort_flag))) break;
+        // Whichever is ready goes next, P V first (it frees key slots): waiting
+        // for the next tile's keys in front of a ready P V would keep the slots
+        // that those keys need.
+        int jq = 0, cq = 0, jp = 0;                    // next score tile and block, next P V
+        uint32_t idle = 0;
+        uint64_t since = 0;
+        while (ok && jp < sg.n) {
+          bool did = false;
+          if (jp < jq && mbar_test(smem_u32(&sh->p_full), (g0 + jp) & 1)) {
+            // O is free once the segment before has been read.
+            if (jp == 0 && seg > 0 && !(ok = mbar_wait(smem_u32(&sh->o_free), (seg - 1) & 1, status, abort_flag))) break;
+            issue_pv(g0 + jp, jp == 0);
+            ++jp;
+            did = true;
+          } else if (jq < sg.n) {
+            const uint32_t g = g0 + jq, u = 4 * g + cq;
+            const bool have = cq < 4 ? mbar_test(smem_u32(&sh->k_full[u % SLOTS]), (u / SLOTS) & 1)
+                                     : mbar_test(smem_u32(&sh->r_full[g % ROPES]), (g / ROPES) & 1);
+            if (have && (cq > 0 || g < 2 || mbar_test(smem_u32(&sh->s_free[g & 1]), ((g >> 1) & 1) ^ 1))) {
+              qk_block(g, cq, jq == sg.n - 1);
+              if (++cq == 5) {
+                cq = 0;
+                ++jq;
+              }
+              did = true;
+            }
+          }
+          if (did) {
+            idle = 0;
+          } else if ((++idle & 63u) == 0) {            // bounded, as every wait
+            if (*abort_flag) ok = false;
+            if (idle == 64) since = globaltimer();
+            if (ok && globaltimer() - since > kWaitLimitNs) {
+              set_status(status, MLA_DEV_TIMEOUT);
+              raise_abort(abort_flag);
+              ok = false;
+            }
+          }
+        }
+        g0 += sg.n;
+        ++seg;
       }
       tc_commit(smem_u32(&sh->drain));
       volatile int never = 0;
       mbar_wait(smem_u32(&sh->drain), 0, status, &never);
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     // ------------------------------------------------------------ softmax (thread = key), epilogue
+    // Two warpgroups, each with all 128 keys and half of the tile's query rows.
+    const int wg = (warp - 2) >> 2, bar = 1 + wg;
+    const int c0 = wg * COLS;                         // first query row of the group
     const int q4 = warp & 3;
     const int key = q4 * 32 + lane;
-    const int tid = threadIdx.x - 64;                 // 0..127
+    const int tid = (warp - 2 - 4 * wg) * 32 + lane;  // 0..127 in the group
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
     uint8_t* pbuf = smem + C::AT_P;
-    if (tid < ROWS) {
-      float rf = 0.f;
-      int lim = 0;
-      if (tid < nrows) {
-        rf = p.q_scale[row0 + tid] * p.scale_log2;
-        lim = key1 - key0;
-        if (p.indices == nullptr) lim = min(lim, sq.cb + static_cast<int>((r0 + tid) / p.H) + 1 - key0);
-      }
-      sh->rn[tid] = make_float2(rf, 0.f);
-      sh->lim[tid] = lim;
-    }
-    // Keys that every row of the tile sees.
-    int all = key1 - key0;
-    if (p.indices == nullptr) all = min(all, sq.cb + static_cast<int>(r0 / p.H) + 1 - key0);
-    softmax_sync();
-    bool seen = false;                                // this thread's row has a reference
-    float l[ROWS];
-#pragma unroll
-    for (int c = 0; c < ROWS; ++c) l[c] = 0.f;
-    float smax = 0.f;
-    // The scale of this thread's key, one tile ahead.
-    auto key_scale = [&](int j) -> float {
-      const int pos = key0 + j * BK + key;
-      if (j >= n || pos >= key1) return 1.f;
-      const int row = q8_row(p, b, pos);
-      return row < 0 ? 1.f : __ldg(p.kv_scales + row / p.scale_block);
-    };
-    float next = key_scale(0);
+    uint32_t seg = 0, g0 = 0;
     bool fail = false;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t sb = j & 1;
-      float ksc = next;
-      next = key_scale(j + 1);
-      const bool valid = key0 + j * BK + key < key1;
-      const bool broken = !(fabsf(ksc) < kInf);       // a scale that is no number: the key's scores are NaN
-      if (broken) ksc = 1.f;
-      if (valid) smax = fmaxf(smax, fabsf(ksc));
-      const float lsc = __log2f(fabsf(ksc));
-      float t[ROWS];
-      const bool got = mbar_wait_warp(smem_u32(&sh->s_full[sb]), (j >> 1) & 1, status, abort_flag);
-      fail |= !got;
-      if (got) {
-        tc_fence_after();
-        uint32_t raw[64];
-        tmem_ld32(tmem + lane_off + TM_S + sb * 64, *reinterpret_cast<uint32_t(*)[32]>(raw));
-        tmem_ld32(tmem + lane_off + TM_S + sb * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
-        tmem_ld_wait();
+    while (!fail && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      const int mine = min(COLS, sg.nrows - c0);      // rows of this group (none: it only keeps the pace)
+      const int span = sg.key1 - sg.key0;
+      bool seen = false;                              // this thread's row has a reference
+      if (tid < COLS) {
+        const int r = c0 + tid;
+        float rf = 0.f;
+        int lim = 0;
+        if (tid < mine) {
+          rf = p.q_scale[sg.row0 + r] * p.scale_log2;
+          lim = span;
+          if (p.indices == nullptr) lim = min(lim, sg.cb + (sg.r0 + r) / p.H + 1 - sg.key0);
+        }
+        sh->rf[r] = rf;
+        sh->ry[r] = 0.f;
+        sh->lim[r] = lim;
+        sh->top[r] = float_order(-kInf);
+      }
+      // Keys that every row of the tile sees.
+      int all = span;
+      if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
+      softmax_sync(bar);
+      float2 l[COLS / 2];
 #pragma unroll
-        for (int c = 0; c < ROWS; ++c)
-          t[c] = WIDE ? __uint_as_float(raw[c]) : __uint_as_float(raw[c]) + __uint_as_float(raw[c + 32]);
-        tc_fence_before();
+      for (int c = 0; c < COLS / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      float smax = 0.f;
+      // The scale of this thread's key is read one tile ahead, its table entry two.
+      auto key_entry = [&](int j) -> int {
+        const int pos = sg.key0 + j * BK + key;
+        return j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
+      };
+      auto key_scale = [&](int j, int entry) -> float {
+        const int pos = sg.key0 + j * BK + key;
+        if (j >= sg.n || pos >= sg.key1) return 1.f;
+        const int row = q8_row(p, pos, entry);
+        return row < 0 ? 1.f : __ldg(p.kv_scales + row / p.scale_block);
+      };
+      int entry = key_entry(1);
+      float next = key_scale(0, key_entry(0));
+      for (int j = 0; j < sg.n; ++j) {
+        const uint32_t g = g0 + j, sb = g & 1;
+        float ksc = next;
+        next = key_scale(j + 1, entry);
+        entry = key_entry(j + 2);
+        const bool valid = sg.key0 + j * BK + key < sg.key1;
+        const bool broken = !(fabsf(ksc) < kInf);     // a scale that is no number: the key's scores are NaN
+        if (broken) ksc = 1.f;
+        if (valid) smax = fmaxf(smax, fabsf(ksc));
+        const float lsc = __log2f(fabsf(ksc));
+        const float2 xs = broken ? make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)) : make_float2(ksc, ksc);
+        float2 t[COLS / 2];
+        const bool got = mbar_wait_warp(smem_u32(&sh->s_full[sb]), (g >> 1) & 1, status, abort_flag);
+        fail |= !got;
+        float mx = -kInf;
+        const bool masked = (j + 1) * BK > all;       // some row does not see every key of the tile
+        if (got && mine > 0) {
+          tc_fence_after();
+          uint32_t hi[COLS], lo[COLS];
+          tmem_ld_n<COLS>(tmem + lane_off + TM_S + sb * NQ + c0, hi);
+          tmem_ld_n<COLS>(tmem + lane_off + TM_S + sb * NQ + ROWS + c0, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < COLS; c += 4) {
+            const float4 rf = *reinterpret_cast<const float4*>(sh->rf + c0 + c);
+            const float4 ry = *reinterpret_cast<const float4*>(sh->ry + c0 + c);
+            const float2 a = __fadd2_rn(make_float2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1])),
+                                        make_float2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1])));
+            const float2 b = __fadd2_rn(make_float2(__uint_as_float(hi[c + 2]), __uint_as_float(hi[c + 3])),
+                                        make_float2(__uint_as_float(lo[c + 2]), __uint_as_float(lo[c + 3])));
+            t[c / 2] = __ffma2_rn(__fmul2_rn(a, xs), make_float2(rf.x, rf.y), make_float2(ry.x, ry.y));
+            t[c / 2 + 1] = __ffma2_rn(__fmul2_rn(b, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
+          }
+          tc_fence_before();
+        } else {
+#pragma unroll
+          for (int c = 0; c < COLS / 2; ++c) t[c] = make_float2(0.f, 0.f);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->s_free[sb]));
-      } else {
+        if (got && lane == 0) mbar_arrive(smem_u32(&sh->s_free[sb]));
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < ROWS; ++c) t[c] = 0.f;
-      }
-      const float xs = broken ? __int_as_float(0x7fc00000) : ksc;
-      float mx = -kInf;
-      const bool masked = (j + 1) * BK > all;         // some row does not see every key of the tile
-#pragma unroll
-      for (int c0 = 0; c0 < ROWS; c0 += 16) {
-        if (c0 < nrows) {
-#pragma unroll
-          for (int c = c0; c < c0 + 16; ++c) {
-            const float2 rn = sh->rn[c];
-            t[c] = fmaf(t[c] * xs, rn.x, rn.y);
-            if (masked) t[c] = j * BK + key < sh->lim[c] ? t[c] : -kInf;
-            mx = fmaxf(mx, t[c]);
+          for (int c = 0; c < COLS / 2; ++c) {
+            t[c].x = j * BK + key < sh->lim[c0 + 2 * c] ? t[c].x : -kInf;
+            t[c].y = j * BK + key < sh->lim[c0 + 2 * c + 1] ? t[c].y : -kInf;
           }
         }
-      }
-      bool any_bad, any_fail;
-      softmax_vote(__any_sync(0xffffffffu, mx + lsc > kGrow), fail, any_bad, any_fail);
-      if (any_fail) { fail = true; break; }
-      // The weights' buffer (and O, where the reference moves) is free once P V
-      // of the tile before is done.
-      const bool wait_pv = j > 0;
-      if (j == 0 || any_bad) {
-        // ---- move the reference of the rows that need it
-        if (wait_pv && !mbar_wait_warp(smem_u32(&sh->pv_done), (j - 1) & 1, status, abort_flag)) fail = true;
-        tc_fence_after();
-        float* wmax = reinterpret_cast<float*>(pbuf);  // [4][ROWS], in the free weights' buffer
 #pragma unroll
-        for (int c0 = 0; c0 < ROWS; c0 += 32) {
-          float mine = -kInf;
+        for (int c = 0; c < COLS / 2; ++c)
+          if (2 * c < mine) mx = fmax3(mx, t[c].x, 2 * c + 1 < mine ? t[c].y : -kInf);
+        bool any_bad, any_fail;
+        softmax_vote(bar, __any_sync(0xffffffffu, mx + lsc > kGrow), fail, any_bad, any_fail);
+        if (any_fail) {
+          fail = true;
+          break;
+        }
+        // The weights' buffer (and O, where the reference moves) is free once
+        // P V of the tile before is done.
+        if (g > 0 && !mbar_wait_warp(smem_u32(&sh->pv_done), (g - 1) & 1, status, abort_flag)) fail = true;
+        if (j == 0 || any_bad) {
+          // ---- move the reference of the rows that need it
+          tc_fence_after();
+          int own = 0;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float v = order_float(__reduce_max_sync(0xffffffffu, float_order(fmaxf(t[c0 + c] + lsc, -kInf))));
-            if (lane == c) mine = v;
+          for (int c = 0; c < COLS; ++c) {
+            const int v = __reduce_max_sync(0xffffffffu, float_order(fmaxf((c & 1 ? t[c / 2].y : t[c / 2].x) + lsc, -kInf)));
+            if (lane == c) own = v;
           }
-          wmax[q4 * ROWS + c0 + lane] = mine;
-        }
-        softmax_sync();
-        if (tid < ROWS) {
-          const float mm = fmaxf(fmaxf(wmax[tid], wmax[ROWS + tid]), fmaxf(wmax[2 * ROWS + tid], wmax[3 * ROWS + tid]));
-          float d = 0.f, f = 1.f;
-          if (mm > -kInf) {
-            if (!seen) {
-              d = kShift - mm;
-              seen = true;
-            } else if (mm > kShift) {
-              d = kShift - mm;
-              f = ex2(d);
-            }
-          }
-          sh->rn[tid].y += d;
-          sh->d[tid] = d;
-          sh->f[tid] = f;
-        }
-        softmax_sync();
-#pragma unroll
-        for (int c = 0; c < ROWS; ++c) {
-          t[c] += sh->d[c];
-          l[c] *= sh->f[c];
-        }
-        if (wait_pv && !fail) {
-#pragma unroll 1
-          for (int cb = 0; cb < 8; ++cb) {
-            uint32_t r[32];
-            const uint32_t ta = tmem + lane_off + TM_O + cb * 32;
-            tmem_ld32(ta, r);
-            tmem_ld_wait();
-            const float* f = sh->f + (WIDE ? (cb & 1) * 32 : 0);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f[i]);
-            tmem_st32(ta, r);
-          }
-          tmem_st_wait();
-        }
-      } else if (wait_pv && !mbar_wait_warp(smem_u32(&sh->pv_done), (j - 1) & 1, status, abort_flag)) {
-        fail = true;
-      }
-      // ---- weights: two e4m3 terms, key-major rows of 64 bytes (64-byte swizzle)
-      uint32_t hi[ROWS / 4], lo[ROWS / 4];
-#pragma unroll
-      for (int i = 0; i < ROWS / 4; ++i) hi[i] = lo[i] = 0u;
-#pragma unroll
-      for (int c0 = 0; c0 < ROWS; c0 += 16) {
-        if (c0 < nrows) {
-#pragma unroll
-          for (int c = c0; c < c0 + 16; c += 4) {
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] = ex2(t[c + i]);
-              l[c + i] += e[i];
-              e[i] *= ksc;
-            }
-            const uint32_t a = pack_f16(e[0], e[1]), bb = pack_f16(e[2], e[3]);
-            const uint16_t ha = e4m3x2_from_f16x2(a), hb = e4m3x2_from_f16x2(bb);
-            const uint16_t la = e4m3x2_from_f16x2(sub_f16x2(a, e4m3x2_to_f16x2(ha)));
-            const uint16_t lb = e4m3x2_from_f16x2(sub_f16x2(bb, e4m3x2_to_f16x2(hb)));
-            hi[c / 4] = static_cast<uint32_t>(ha) | (static_cast<uint32_t>(hb) << 16);
-            lo[c / 4] = static_cast<uint32_t>(la) | (static_cast<uint32_t>(lb) << 16);
-          }
-        }
-      }
-      const int sw = (key >> 1) & 3;
-      uint8_t* prow = pbuf + key * 64;
-      if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<uint4*>(prow + ((i ^ sw) << 4)) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-          *reinterpret_cast<uint4*>(prow + C::PTERM + ((i ^ sw) << 4)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          *reinterpret_cast<uint4*>(prow + ((i ^ sw) << 4)) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-          *reinterpret_cast<uint4*>(prow + (((2 + i) ^ sw) << 4)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        }
-      }
-      if (masked && j * BK + key >= all) {
-        // A key that some row does not see: its weight is 0 there, but 0 times
-        // a NaN code is NaN.  Rows past the partition become zeros (they may
-        // hold anything); in the others every NaN code does (a row that sees
-        // such a key has a NaN score, so its result is NaN all the same).
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint4* kr = reinterpret_cast<uint4*>(smem + ((4 * j + c) % SLOTS) * SLOT + key * 128);
-          for (int i = 0; i < 8; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) {
-              v = kr[i];
-              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-              for (int x = 0; x < 4; ++x) {
-                // Bytes equal to 0x7F after clearing the sign.
-                const uint32_t nan = ((w[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                w[x] &= ~((nan >> 7) * 0xFFu);
+          if (lane < COLS) atomicMax(&sh->top[c0 + lane], own);   // a maximum: the order does not matter
+          softmax_sync(bar);
+          if (tid < COLS) {
+            const float mm = order_float(sh->top[c0 + tid]);
+            sh->top[c0 + tid] = float_order(-kInf);
+            float d = 0.f, f = 1.f;
+            if (mm > -kInf) {
+              if (!seen) {
+                d = kShift - mm;
+                seen = true;
+              } else if (mm > kShift) {
+                d = kShift - mm;
+                f = ex2(d);
               }
             }
-            kr[i] = v;
+            sh->ry[c0 + tid] += d;
+            sh->d[c0 + tid] = d;
+            sh->f[c0 + tid] = f;
+          }
+          softmax_sync(bar);
+#pragma unroll
+          for (int c = 0; c < COLS; c += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(sh->d + c0 + c);
+            const float4 f = *reinterpret_cast<const float4*>(sh->f + c0 + c);
+            t[c / 2] = __fadd2_rn(t[c / 2], make_float2(d.x, d.y));
+            t[c / 2 + 1] = __fadd2_rn(t[c / 2 + 1], make_float2(d.z, d.w));
+            l[c / 2] = __fmul2_rn(l[c / 2], make_float2(f.x, f.y));
+            l[c / 2 + 1] = __fmul2_rn(l[c / 2 + 1], make_float2(f.z, f.w));
+          }
+          if (j > 0 && !fail) {
+#pragma unroll 1
+            for (int cb = 0; cb < (WIDE ? 4 : 8); ++cb) {
+              uint32_t r[COLS];
+              const uint32_t ta = tmem + lane_off + TM_O + cb * (WIDE ? 64 : 32) + c0;
+              tmem_ld_n<COLS>(ta, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < COLS; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh->f[c0 + i]);
+              tmem_st_n<COLS>(ta, r);
+            }
+            tmem_st_wait();
           }
         }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh->p_full));
-    }
-    // ------------------------------------------------------------ epilogue
-    if (!fail && !mbar_wait_warp(smem_u32(&sh->pv_done), (n - 1) & 1, status, abort_flag)) fail = true;
-    tc_fence_after();
-    bool any_bad, any_fail;
-    softmax_vote(false, fail, any_bad, any_fail);
-    if (!any_fail) {
-      // Sums over the keys: every thread's, through the key slots (all read by now).
-      float* ls = reinterpret_cast<float*>(smem);
+        // ---- weights: two e4m3 terms, key-major rows of 64 bytes (64-byte swizzle)
+        if (mine > 0) {
+          uint32_t hi[COLS / 4], lo[COLS / 4];
+          const float2 ks = make_float2(ksc, ksc);
+          // Rounds to four bits: y = x (2^20 + 1) has 24 bits, 20 of which
+          // y - (y - x) cancels.  (The product is an fma with zero so that it
+          // is not merged into the subtractions.)
+          const float2 split = make_float2(1048577.f, 1048577.f);
 #pragma unroll
-      for (int c = 0; c < ROWS; ++c) ls[key * ROWS + c] = l[c];
-      float* sm = reinterpret_cast<float*>(pbuf);
+          for (int c = 0; c < COLS; c += 4) {
+            uint16_t h[2], w[2];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-      if (lane == 0) sm[q4] = smax;
-      softmax_sync();
-      if (tid < ROWS) {
-        float sum = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < BK; ++i) sum += ls[i * ROWS + tid];
-        float s = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-        if (!(s > 0.f)) s = 1.f;
-        sh->f[tid] = sum == 0.f ? 0.f : 1.0f / (sum * s);
-        // Weights carry 2^-reference: log2 of the plain sum adds it back.
-        if (tid < nrows)
-          p.meta[static_cast<long long>(k) * p.R + row0 + tid] =
-              make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->rn[tid].y, s);
-      }
-      softmax_sync();
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[64];
-        tmem_ld32(tmem + lane_off + TM_O + c * 64, *reinterpret_cast<uint32_t(*)[32]>(o));
-        tmem_ld32(tmem + lane_off + TM_O + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
-        tmem_ld_wait();
-        __half* dst = p.o_part + (static_cast<long long>(k) * p.R + row0) * 512 + c * 128 + key;
+            for (int i = 0; i < 2; ++i) {
+              const float2 e = make_float2(ex2(t[c / 2 + i].x), ex2(t[c / 2 + i].y));
+              l[c / 2 + i] = __fadd2_rn(l[c / 2 + i], e);
+              const float2 x = __fmul2_rn(e, ks);
+              const float2 y = __ffma2_rn(x, split, make_float2(0.f, 0.f));
+              const float2 z = __fadd2_rn(y, make_float2(-x.x, -x.y));
+              const float2 a = __fadd2_rn(y, make_float2(-z.x, -z.y));
+              const float2 b = __fadd2_rn(x, make_float2(-a.x, -a.y));
+              h[i] = pack_e4m3(a.x, a.y);
+              w[i] = pack_e4m3(b.x, b.y);
+            }
+            hi[c / 4] = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
+            lo[c / 4] = static_cast<uint32_t>(w[0]) | (static_cast<uint32_t>(w[1]) << 16);
+          }
+          const int sw = (key >> 1) & 3;
+          uint8_t* prow = pbuf + key * 64;
+          if constexpr (WIDE) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          float v = __uint_as_float(o[r]);
-          if constexpr (!WIDE) v += __uint_as_float(o[32 + r]);
-          if (r < nrows) dst[static_cast<long long>(r) * 512] = __float2half_rn(sh->f[r] == 0.f ? 0.f : v * sh->f[r]);
+            for (int i = 0; i < 2; ++i) {
+              uint8_t* at = prow + (((2 * wg + i) ^ sw) << 4);
+              *reinterpret_cast<uint4*>(at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+              *reinterpret_cast<uint4*>(at + C::PTERM) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            }
+          } else {
+            *reinterpret_cast<uint4*>(prow + ((wg ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(prow + (((2 + wg) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
+        if (masked && j * BK + key >= all) {
+          // A key that some row does not see: its weight is 0 there, but 0 times
+          // a NaN code is NaN.  Rows past the segment become zeros (they may
+          // hold anything); in the others every NaN code does (a row that sees
+          // such a key has a NaN score, so its result is NaN all the same).
+          // Each group has two of the four latent blocks.
+#pragma unroll 1
+          for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
+            uint4* kr = reinterpret_cast<uint4*>(smem + ((4 * g + c) % SLOTS) * SLOT + key * 128);
+            for (int i = 0; i < 8; ++i) {
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (valid) {
+                v = kr[i];
+                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                for (int x = 0; x < 4; ++x) {
+                  // Bytes equal to 0x7F after clearing the sign.
+                  const uint32_t nan = ((w[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  w[x] &= ~((nan >> 7) * 0xFFu);
+                }
+              }
+              kr[i] = v;
+            }
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->p_full));
       }
+      g0 += sg.n;
+      // ---------------------------------------------------------- epilogue
+      if (!fail && !mbar_wait_warp(smem_u32(&sh->pv_done), (g0 - 1) & 1, status, abort_flag)) fail = true;
+      tc_fence_after();
+      bool any_bad, any_fail;
+      softmax_vote(bar, false, fail, any_bad, any_fail);
+      fail = any_fail;
+      if (!fail && mine > 0) {
+        // Sums over the keys: within each warp by shuffles, then over the four
+        // warps through the row arrays that the segment no longer needs.
+        float own = 0.f;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          float v = c & 1 ? l[c / 2].y : l[c / 2].x;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (lane == c) own = v;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
+        float* part = q4 == 0 ? sh->rf : (q4 == 1 ? sh->d : (q4 == 2 ? sh->f : reinterpret_cast<float*>(sh->top)));
+        if (lane < COLS) part[c0 + lane] = own;
+        if (lane == 0) sh->lim[c0 + q4] = __float_as_int(smax);
+        softmax_sync(bar);
+        if (tid < COLS) {
+          const int r = c0 + tid;
+          const float sum = (sh->rf[r] + sh->d[r]) + (sh->f[r] + __int_as_float(sh->top[r]));
+          float s = fmaxf(fmaxf(__int_as_float(sh->lim[c0]), __int_as_float(sh->lim[c0 + 1])),
+                          fmaxf(__int_as_float(sh->lim[c0 + 2]), __int_as_float(sh->lim[c0 + 3])));
+          if (!(s > 0.f)) s = 1.f;
+          sh->f[r] = sum == 0.f ? 0.f : 1.0f / (sum * s);
+          // Weights carry 2^-reference: log2 of the plain sum adds it back.
+          if (tid < mine)
+            p.meta[static_cast<long long>(sg.slot) * ROWS + r] =
+                make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->ry[r], s);
+        }
+        softmax_sync(bar);
+        __half* dst0 = p.o_part + (static_cast<long long>(sg.slot) * ROWS + c0) * 512 + key;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[COLS], o2[COLS];
+          const uint32_t ta = tmem + lane_off + TM_O + c * 64 + c0;
+          tmem_ld_n<COLS>(ta, o);
+          if constexpr (!WIDE) tmem_ld_n<COLS>(ta + 32, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < COLS; ++r) {
+            float v = __uint_as_float(o[r]);
+            if constexpr (!WIDE) v += __uint_as_float(o2[r]);
+            const float f = sh->f[c0 + r];
+            if (r < mine) dst0[r * 512 + c * 128] = __float2half_rn(f == 0.f ? 0.f : v * f);
+          }
+        }
+        tc_fence_before();
+      }
+      softmax_sync(bar);                              // the row arrays are rewritten by the next segment
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->o_free));
+      ++seg;
     }
   } else {
     // ------------------------------------------------------------ listed rows: cp.async
     if constexpr (!DENSE) {
       constexpr int RW = BK / kSparseProducers;       // this warp's keys [RW pw, RW pw + RW) of the tile
-      const int pw = warp - 6;
+      const int pw = warp - 10;
       uint32_t issued = 0, r_issued = 0;
-      uint32_t pend[4];                               // full barriers of the copies in flight
-      int npend = 0;
       bool ok = true;
-      auto landed = [&](uint32_t bar) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-      for (int j = 0; j < n && ok; ++j) {
-        int row[RW / 32];                             // key 32 x + lane
+      while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+        int row[RW / 32], next[RW / 32];              // key 32 x + lane: this tile's row, the next one's table entry
+        auto entries = [&](int j, int (&r)[RW / 32]) {
 #pragma unroll
-        for (int x = 0; x < RW / 32; ++x) {
-          const int pos = key0 + j * BK + pw * RW + 32 * x + lane;
-          row[x] = pos < key1 ? q8_row(p, b, pos) : 0;
-          if (row[x] < 0) row[x] = 0;                 // reported; the result of its rows is not meaningful
-        }
-        for (int c = 0; c < 5; ++c) {
-          const bool rope = c == 4;
-          const uint32_t u = rope ? r_issued : issued;
-          const uint32_t cap = rope ? ROPES : SLOTS;
-          const uint32_t s = u % cap;
-          if (u >= cap) {
-            const uint32_t empty = smem_u32(rope ? &sh->r_empty[s] : &sh->k_empty[s]);
-            const uint32_t parity = ((u / cap) & 1) ^ 1;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
-              // About to wait for the MMAs: they may be waiting for these copies.
-              cp_async_wait<0>();
-              for (int i = 0; i < npend; ++i) landed(pend[i]);
-              npend = 0;
-              if (!(ok = mbar_wait_warp(empty, parity, status, abort_flag))) break;
-            }
+          for (int x = 0; x < RW / 32; ++x) {
+            const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
+            r[x] = j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
           }
-          const uint32_t full = smem_u32(rope ? &sh->r_full[s] : &sh->k_full[s]);
-          if (!rope) {
-            const uint32_t dst = smem_u32(smem + s * SLOT) + pw * RW * 128;
+        };
+        entries(0, next);
+        for (int j = 0; j < sg.n && ok; ++j) {
 #pragma unroll
-            for (int i = 0; i < RW / 4; ++i) {        // four rows of 8 chunks an instruction
-              const int r = 4 * i + (lane >> 3), ch = lane & 7;
-              const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
-              cp_async16(dst + r * 128 + ((ch ^ (r & 7)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + c * 128 + ch * 16);
-            }
-          } else {
-            const uint32_t dst = smem_u32(smem + C::AT_ROPE + s * ROPE) + pw * RW * 64;
+          for (int x = 0; x < RW / 32; ++x) {
+            const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
+            row[x] = pos < sg.key1 ? q8_row(p, pos, next[x]) : 0;
+            if (row[x] < 0) row[x] = 0;               // reported; the result of its rows is not meaningful
+          }
+          entries(j + 1, next);                       // in flight while the tile is copied
 #pragma unroll
-            for (int i = 0; i < RW / 8; ++i) {        // eight rows of 4 chunks
-              const int r = 8 * i + (lane >> 2), ch = lane & 3;
-              const int src = __shfl_sync(0xffffffffu, row[i / 4], r & 31);
-              cp_async16(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + 512 + ch * 16);
+          for (int c = 0; c < 5; ++c) {
+            const uint32_t s = c < 4 ? issued % SLOTS : r_issued % ROPES;
+            const uint32_t turn = c < 4 ? issued / SLOTS : r_issued / ROPES;
+            const uint32_t empty = smem_u32(c < 4 ? &sh->k_empty[s] : &sh->r_empty[s]);
+            const uint32_t full = smem_u32(c < 4 ? &sh->k_full[s] : &sh->r_full[s]);
+            if (turn > 0 && !(ok = mbar_wait_warp(empty, (turn & 1) ^ 1, status, abort_flag))) break;
+            if (c < 4) {
+              const uint32_t dst = smem_u32(smem + s * SLOT) + pw * RW * 128;
+#pragma unroll
+              for (int i = 0; i < RW / 4; ++i) {      // four rows of 8 chunks an instruction
+                const int r = 4 * i + (lane >> 3), ch = lane & 7;
+                const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
+                cp_async16(dst + r * 128 + ((ch ^ (r & 7)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + c * 128 + ch * 16);
+              }
+            } else {
+              const uint32_t dst = smem_u32(smem + C::AT_ROPE + s * ROPE) + pw * RW * 64;
+#pragma unroll
+              for (int i = 0; i < RW / 8; ++i) {      // eight rows of 4 chunks
+                const int r = 8 * i + (lane >> 2), ch = lane & 3;
+                const int src = __shfl_sync(0xffffffffu, row[i / 4], r & 31);
+                cp_async16(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + 512 + ch * 16);
+              }
             }
+            cp_async_arrive(full);                    // counted as the copies land
+            if (c < 4) ++issued; else ++r_issued;
           }
-          cp_async_commit();
-          if (npend == 3) {
-            cp_async_wait<3>();
-            landed(pend[0]);
-            pend[0] = pend[1];
-            pend[1] = pend[2];
-            pend[2] = full;
-          } else {
-            pend[npend++] = full;
-          }
-          if (rope) ++r_issued; else ++issued;
         }
       }
+      // Every copy lands, and its arrival with it, before the CTA leaves.
+      cp_async_commit();
       cp_async_wait<0>();
-      for (int i = 0; i < npend; ++i) landed(pend[i]);
+      volatile int never = 0;
+      if (ok) {
+        for (uint32_t s = 0; s < SLOTS; ++s)
+          if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / SLOTS) & 1, status, &never);
+        for (uint32_t s = 0; s < ROPES; ++s)
+          if (r_issued > s) mbar_wait_warp(smem_u32(&sh->r_full[s]), ((r_issued - 1 - s) / ROPES) & 1, status, &never);
+      }
     }
   }
 
@@ -880,7 +1142,7 @@ __global__ void __launch_bounds__(DENSE ? 192 : 192 + 32 * kSparseProducers, 1)
 }
 
 // ============================================================ 3. merge and w_uv
-// One CTA per (head, NT tokens): the partitions' latent results are merged by
+// One CTA per (head, NT tokens): the segments' latent results are merged by
 // LSE in fp32 (with the attention sink in the denominator), split into two
 // bf16 terms (their sum within 2^-16) and multiplied by w_uv[h]: D^T [128
 // values, NT tokens] = w_uv[h] [128, 512] . o^T, so that few tokens make a
@@ -899,14 +1161,15 @@ struct OutSmem {
   uint64_t full, done;
   uint32_t tmem;
   int abort;
-  int used[32];      // partitions that hold keys of the token; -1: its rows are not written
+  int used[32];      // segments that hold keys of the token; -1: its rows are not written
+  int first[32];     // row of the first one's results (in slots), the others `step` apart
   float sink[32];    // log2 units
 };
 
 template <int NT>
 __global__ void __launch_bounds__(kOutThreads, 1)
     q8_out_kernel(const __grid_constant__ CUtensorMap w_map, const Q8Params p, const float* __restrict__ sink,
-                  __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T) {
+                  __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T, int rows) {
   using C = OutShape<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -930,23 +1193,33 @@ __global__ void __launch_bounds__(kOutThreads, 1)
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {
     const int i = threadIdx.x - 64, t = t0 + i;
-    int used = -1;
+    int used = -1, first = 0;
     float sk = -kInf;
     if (t < T) {
-      int lo = 0, hi = p.B;   // largest b with iro[b] <= t
+      const int entries = __ldg(&p.head->entries), units = __ldg(&p.head->units);
+      int lo = 0, hi = entries;   // last entry with qa <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(p.iro + mid) <= static_cast<uint32_t>(t)) lo = mid; else hi = mid;
+        if (__ldg(&p.entries[mid].qa) <= t) lo = mid; else hi = mid;
       }
-      SeqInfo s;
-      if (q8_seq(p, lo, s) && s.qa <= t && t < s.qa + s.n) {
-        const int count = q8_part_count(p, s.L);
-        const int size = q8_part_size(s.L, count);
-        const int keys = p.indices != nullptr ? s.L : min(s.L, s.cb + (t - s.qa) + 1);
-        used = size > 0 ? min(count, keys / size + (keys % size != 0)) : 0;
-        if (sink != nullptr) sk = __ldg(sink + lo) * 1.4426950408889634f;
+      if (entries > 0) {
+        const PlanEntry e = load_entry(p.entries + lo);
+        if (e.qa <= t && t < e.qa + e.n) {
+          const int keys = p.indices != nullptr ? e.L : min(e.L, e.cb + (t - e.qa) + 1);
+          const long long r = static_cast<long long>(t - e.qa) * p.H + h;
+          const int item = static_cast<int>(r / (p.members * rows)), in = static_cast<int>(r % (p.members * rows));
+          used = 0;
+          if (keys > 0) {
+            const int u = e.units + item * e.tiles;
+            const int pieces = min(p.pieces, units), g0 = piece_of(u, pieces, units);
+            used = piece_of(u + (keys + BK - 1) / BK - 1, pieces, units) - g0 + 1;
+            first = (g0 + e.items + item) * p.members * rows + in;
+          }
+          if (sink != nullptr) sk = __ldg(sink + e.b) * 1.4426950408889634f;
+        }
       }
     }
+    sh->first[i] = first;
     sh->used[i] = used;
     sh->sink[i] = sk;
   }
@@ -957,18 +1230,19 @@ __global__ void __launch_bounds__(kOutThreads, 1)
 
   for (int i = warp; i < NT; i += kOutThreads / 32) {
     const int used = sh->used[i];
+    const long long first = sh->first[i], step = static_cast<long long>(p.members) * rows;
     const long long grow = static_cast<long long>(t0 + i) * p.H + h;
     float o[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0.f;
     float mx = -kInf, tot = 0.f;
-    constexpr int KU = 4;                           // partitions loaded together
+    constexpr int KU = 4;                           // segments loaded together
     for (int k0 = 0; k0 < used; k0 += KU) {
       uint4 a[KU], c[KU];
       float2 mt[KU];
 #pragma unroll
       for (int x = 0; x < KU; ++x) {
-        const long long at = static_cast<long long>(k0 + x) * p.R + grow;
+        const long long at = first + (k0 + x) * step;
         const bool in = k0 + x < used;
         mt[x] = in ? __ldg(p.meta + at) : make_float2(-kInf, 0.f);
         const uint4* src = reinterpret_cast<const uint4*>(p.o_part + at * 512);
@@ -1084,28 +1358,31 @@ int run_rows(int page_size) {
 
 template <bool DENSE, bool WIDE>
 cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, const CUtensorMap& k_map,
-                        const CUtensorMap& kr_map, const Q8Params& p, long long items, cudaStream_t stream) {
+                        const CUtensorMap& kr_map, const Q8Params& p, long long ctas, cudaStream_t stream) {
   cudaError_t e = opt_in_smem(q8_attn_kernel<DENSE, WIDE>, Shape<WIDE>::TOTAL);
   if (e != cudaSuccess) return e;
-  const int threads = DENSE ? 192 : 192 + 32 * kSparseProducers;
-  return launch_pdl(q8_attn_kernel<DENSE, WIDE>, dim3(static_cast<unsigned>(items)), dim3(threads),
+  const int threads = DENSE ? kAttnThreads : kAttnThreads + 32 * kSparseProducers;
+  return launch_pdl(q8_attn_kernel<DENSE, WIDE>, dim3(static_cast<unsigned>(ctas)), dim3(threads),
                     Shape<WIDE>::TOTAL, stream, q_map, qr_map, k_map, kr_map, p);
 }
 
 template <int NT>
-cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const DecodeQ8Args& a, cudaStream_t stream) {
+cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const DecodeQ8Args& a, int rows,
+                       cudaStream_t stream) {
   cudaError_t e = opt_in_smem(q8_out_kernel<NT>, OutShape<NT>::TOTAL);
   if (e != cudaSuccess) return e;
   return launch_pdl(q8_out_kernel<NT>, dim3((a.T + NT - 1) / NT, a.H), dim3(kOutThreads), OutShape<NT>::TOTAL, stream,
-                    w_map, p, a.sink, static_cast<__nv_bfloat16*>(a.out), a.lse, a.T);
+                    w_map, p, a.sink, static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, rows);
 }
 
-// 64 query rows a tile where a sequence can fill more than 32.
-bool wide_rows(int H, int max_new) { return static_cast<long long>(H) * max_new > 32; }
+// Query rows of a tile: 64 where a sequence can fill more than 32.
+int tile_rows(int H, int max_new) { return static_cast<long long>(H) * max_new > 32 ? 64 : 32; }
+// Row tiles that walk a piece together: those of one token's heads, eight at most.
+int item_members(int H, int rows) { return std::min(8, (H + rows - 1) / rows); }
 
 }  // namespace
 
-DecodeQ8Layout decode_q8_layout(int T, int H, int parts) {
+DecodeQ8Layout decode_q8_layout(int T, int H, int pieces) {
   const size_t R = static_cast<size_t>(T) * H;
   DecodeQ8Layout L;
   size_t off = 0;
@@ -1114,38 +1391,45 @@ DecodeQ8Layout decode_q8_layout(int T, int H, int parts) {
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
+  L.head = take(sizeof(PlanHead));
+  L.entries = take(sizeof(PlanEntry) * static_cast<size_t>(T > 0 ? T : 1));
   L.q8 = take(R * 1152);
   L.q_scale = take(R * 4);
-  L.o_part = take(static_cast<size_t>(parts) * R * 512 * 2);
-  L.meta = take(static_cast<size_t>(parts) * R * 8);
+  // Slots: one for each piece and item.  Items: R / (rows of an item), and one
+  // more for every sequence whose rows do not fill their last one (T sequences
+  // at most).  For either number of rows, as max_new is not known here.
+  size_t slot_rows = 0;
+  for (int rows : {32, 64}) {
+    const size_t item = static_cast<size_t>(rows) * item_members(H, rows);
+    const size_t items = (R + item - 1) / item + (H % static_cast<int>(item) == 0 ? 0 : T);
+    slot_rows = std::max(slot_rows, (items + pieces) * item);
+  }
+  L.o_part = take(slot_rows * 512 * 2);
+  L.meta = take(slot_rows * 8);
   L.total = off;
   return L;
 }
 
-DecodePartitioning decode_q8_partitioning(int B, int H, int max_new, int max_keys) {
-  const long long sms = sm_count();
-  const int rows = wide_rows(H, max_new) ? 64 : 32;
-  const long long m_tiles = (static_cast<long long>(std::max(1, max_new)) * H + rows - 1) / rows;
-  const long long keys = std::max(1, max_keys);
-  long long pk = static_cast<long long>(B) * m_tiles * keys / sms;
-  pk = std::min<long long>(4096, std::max<long long>(256, (pk + BK - 1) / BK * BK));
-  DecodePartitioning d;
-  d.part_keys = static_cast<int>(pk);
-  d.parts = static_cast<int>(std::min<long long>(256, std::max(1ll, (keys + pk - 1) / pk)));
-  return d;
+int decode_q8_pieces(int B, int H, int max_new, int max_keys) {
+  // One piece (of `members` CTAs) for the SMs at a time, as long as there is a tile for each.
+  const int rows = tile_rows(H, std::max(1, max_new)), members = item_members(H, rows);
+  const long long item = static_cast<long long>(rows) * members;
+  const long long items = B * ((static_cast<long long>(std::max(1, max_new)) * H + item - 1) / item);
+  const long long tiles = (static_cast<long long>(std::max(1, max_keys)) + BK - 1) / BK;
+  return static_cast<int>(std::min<long long>(std::max(1, sm_count() / members), items * tiles));
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   const int H = a.H, T = a.T;
   const long long R = static_cast<long long>(T) * H;
   if (T == 0) return cudaSuccess;
-  const DecodeQ8Layout L = decode_q8_layout(T, H, a.parts);
+  const DecodeQ8Layout L = decode_q8_layout(T, H, a.pieces);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   uint8_t* q8 = ws + L.q8;
   float* q_scale = reinterpret_cast<float*>(ws + L.q_scale);
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const bool wide = wide_rows(H, a.max_new);
-  const int rows = wide ? 64 : 32;
+  const int rows = tile_rows(H, a.max_new), members = item_members(H, rows);
+  const bool wide = rows == 64;
 
   CUtensorMap qa_map, wuk_map;
   if (!encode_2d(&qa_map, a.q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
@@ -1153,21 +1437,34 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
       !encode_2d(&wuk_map, a.w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  PlanArgs plan;
+  plan.head = reinterpret_cast<PlanHead*>(ws + L.head);
+  plan.entries = reinterpret_cast<PlanEntry*>(ws + L.entries);
+  plan.iro = a.iro;
+  plan.cache_len = a.cache_len;
+  plan.topk = a.topk;
+  plan.B = a.B;
+  plan.H = H;
+  plan.T = T;
+  plan.max_seq = a.max_seq;
+  plan.indices_stride = a.indices_stride;
+  plan.sparse = a.indices != nullptr ? 1 : 0;
+  plan.item_rows = rows * members;
+  plan.status = a.status;
   cudaError_t e = opt_in_smem(q8_query_kernel, Q_SMEM_TOTAL);
   if (e != cudaSuccess) return e;
   e = launch_pdl(q8_query_kernel, dim3((T + 127) / 128, 4 * H), dim3(kQThreads), Q_SMEM_TOTAL, stream, qa_map, wuk_map,
-                 static_cast<const uint16_t*>(a.q), q8, q_scale, T, H, a.status);
+                 static_cast<const uint16_t*>(a.q), q8, q_scale, T, H, a.status, plan);
   if (e != cudaSuccess) return e;
 
   Q8Params p;
+  p.head = plan.head;
+  p.entries = plan.entries;
   p.q_scale = q_scale;
   p.kv_scales = a.kv_scales;
   p.kv_cache = static_cast<const uint8_t*>(a.kv_cache);
-  p.iro = a.iro;
-  p.cache_len = a.cache_len;
   p.page_table = a.page_table;
   p.indices = a.indices;
-  p.topk = a.topk;
   p.o_part = reinterpret_cast<__half*>(ws + L.o_part);
   p.meta = reinterpret_cast<float2*>(ws + L.meta);
   p.indices_stride = a.indices_stride;
@@ -1175,13 +1472,11 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.scale_block = a.scale_block;
-  p.B = a.B;
   p.H = H;
   p.R = static_cast<int>(R);
-  p.parts = a.parts;
-  p.part_keys = a.part_keys;
-  p.m_tiles = static_cast<int>((static_cast<long long>(a.max_new) * H + rows - 1) / rows);
-  p.max_seq = a.max_seq;
+  p.T = T;
+  p.pieces = a.pieces;
+  p.members = members;
   p.box = run_rows(a.page_size);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
@@ -1194,19 +1489,19 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
       !encode_2d(&k_map, a.kv_cache, u8, 576, cache_rows, 576, 128, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&kr_map, a.kv_cache, u8, 576, cache_rows, 576, 64, box, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  const long long items = static_cast<long long>(a.B) * a.parts * p.m_tiles;
+  const long long ctas = static_cast<long long>(a.pieces) * members;
   if (dense)
-    e = wide ? launch_attn<true, true>(q_map, qr_map, k_map, kr_map, p, items, stream)
-             : launch_attn<true, false>(q_map, qr_map, k_map, kr_map, p, items, stream);
+    e = wide ? launch_attn<true, true>(q_map, qr_map, k_map, kr_map, p, ctas, stream)
+             : launch_attn<true, false>(q_map, qr_map, k_map, kr_map, p, ctas, stream);
   else
-    e = wide ? launch_attn<false, true>(q_map, qr_map, k_map, kr_map, p, items, stream)
-             : launch_attn<false, false>(q_map, qr_map, k_map, kr_map, p, items, stream);
+    e = wide ? launch_attn<false, true>(q_map, qr_map, k_map, kr_map, p, ctas, stream)
+             : launch_attn<false, false>(q_map, qr_map, k_map, kr_map, p, ctas, stream);
   if (e != cudaSuccess) return e;
 
   CUtensorMap wuv_map;
   if (!encode_2d(&wuv_map, a.w_uv, bf, 512, static_cast<uint64_t>(H) * 128, 1024, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  return T > 16 ? launch_out<32>(wuv_map, p, a, stream) : launch_out<16>(wuv_map, p, a, stream);
+  return T > 16 ? launch_out<32>(wuv_map, p, a, rows, stream) : launch_out<16>(wuv_map, p, a, rows, stream);
 }
 
 }  // namespace mla

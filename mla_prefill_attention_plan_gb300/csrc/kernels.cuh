@@ -202,8 +202,8 @@ struct DecodeQ8Args {
   const void* w_uv;           // [H][128][512] bf16
   const uint32_t* iro;
   const uint32_t* cache_len;
-  int B, H, T, max_new, max_seq, parts;
-  int part_keys;              // > 0: about this many keys a partition, at most `parts` of them
+  int B, H, T, max_new, max_seq;
+  int pieces;                 // equal parts that the batch's key tiles are cut into
   float scale;
   const int32_t* indices;     // sparse: [B][indices_stride] physical cache rows, or null
   int indices_stride;
@@ -213,10 +213,10 @@ struct DecodeQ8Args {
   int32_t* status;
 };
 struct DecodeQ8Layout {
-  size_t q8, q_scale, o_part, meta, total;
+  size_t head, entries, q8, q_scale, o_part, meta, total;
 };
-DecodeQ8Layout decode_q8_layout(int T, int H, int parts);
-DecodePartitioning decode_q8_partitioning(int B, int H, int max_new, int max_keys);
+DecodeQ8Layout decode_q8_layout(int T, int H, int pieces);
+int decode_q8_pieces(int B, int H, int max_new, int max_keys);
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream);
 
 // Key scores and block selection for sparse decode (index.cu).
