@@ -92,6 +92,16 @@ bool encode_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, const uint64_t (&dims)[4],
+               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, e[4] = {1, 1, 1, 1};
+  return fn(map, dt, 4, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -677,7 +687,7 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
   // Units of the plan (one key tile of an item each, items of 32 rows or more) and CTAs.
   const long long tiles = ((d_indices != nullptr ? indices_stride : max_seq_len) + 127ll) / 128;
   const long long items = total_q_tokens + (rows + 31) / 32;
-  if (items * tiles >= (1ll << 31) || 8ll * pieces >= (1ll << 31) || 512 * (items + pieces) >= (1ll << 31))
+  if (items * tiles >= (1ll << 31) || pieces > (1 << 15) || 512 * (items + pieces) >= (1ll << 31))
     return MLA_ERR_ARG;
   const mla::DecodeQ8Layout L = mla::decode_q8_layout(total_q_tokens, num_heads, pieces);
   if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))

@@ -162,6 +162,7 @@ __device__ void q8_plan(const PlanArgs& a, int tid, int (*scr)[4]) {
   if (tid == 0) {
     a.head->entries = entries;
     a.head->units = units;
+    a.entries[entries].units = units;       // where the last entry's units end
   }
 }
 
@@ -184,7 +185,7 @@ struct QuerySmem {
   int scr[4][4];
 };
 
-__global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
+__global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
     q8_query_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                     const uint16_t* __restrict__ q, uint8_t* __restrict__ q8, float* __restrict__ q_scale, int T,
                     int H, int32_t* status, const PlanArgs plan) {
@@ -216,7 +217,6 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
   const int row = (warp & 3) * 32 + lane;          // epilogue warps 2..5
   const int t = m0 + row;
   const long long grow = static_cast<long long>(t) * H + h;
-  uint32_t xb[128];                                // the row's 128 results, as bits
   float am = 0.f;
   bool ok = work;
   if (work && warp == 0) {
@@ -255,12 +255,14 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
     ok = mbar_wait_warp(smem_u32(&sh->done), 0, status, abort_flag);
     if (ok) {
       tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_ld32(tmem + (uint32_t((warp & 3) * 32) << 16) + c * 32, x);
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        tmem_ld32(tmem + (uint32_t((warp & 3) * 32) << 16) + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xb + 32 * c));
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 128; ++i) am = fmaxf(am, fabsf(__uint_as_float(xb[i])));
+        for (int i = 0; i < 32; ++i) am = fmaxf(am, fabsf(__uint_as_float(x[i])));
+      }
       if (rank == 3 && t < T) {
         const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
 #pragma unroll
@@ -276,7 +278,7 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
   }
   tc_fence_before();
   cluster_sync();
-  if (warp >= 2 && ok && t < T) {
+  if (warp >= 2 && ok) {
     for (uint32_t r = 0; r < 4; ++r) {
       if (static_cast<int>(r) == rank) continue;
       float o;
@@ -286,27 +288,36 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
     const float s = pow2_scale(am);
     const float inv = 1.0f / s;
     // An infinite query has no scale: its scores become NaN.
-    if (rank == 0) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);
+    if (rank == 0 && t < T) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);
     uint8_t* dst = q8 + grow * 1152 + rank * 128;
+    // The results once more from TMEM, 32 columns at a time (few registers, so
+    // that three of these CTAs share an SM).
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[32];
+      tmem_ld32(tmem + (uint32_t((warp & 3) * 32) << 16) + c * 32, x);
+      tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t hi[4], lo[4];
+      for (int i = 0; i < 2; ++i) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[4];
+        for (int k = 0; k < 4; ++k) {
+          float v[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(xb[16 * i + 4 * k + y]);
-        // |v| inv <= 448; the remainder in fp32, so that f16 rounds only it.
-        const uint16_t h0 = pack_e4m3(v[0] * inv, v[1] * inv), h1 = pack_e4m3(v[2] * inv, v[3] * inv);
-        const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
-        hi[k] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
-        lo[k] = static_cast<uint32_t>(pack_e4m3(v[0] * inv - b0.x, v[1] * inv - b0.y)) |
-                (static_cast<uint32_t>(pack_e4m3(v[2] * inv - b1.x, v[3] * inv - b1.y)) << 16);
+          for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(x[16 * i + 4 * k + y]);
+          const uint16_t h0 = pack_e4m3(v[0] * inv, v[1] * inv), h1 = pack_e4m3(v[2] * inv, v[3] * inv);
+          const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
+          hi[k] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
+          lo[k] = static_cast<uint32_t>(pack_e4m3(v[0] * inv - b0.x, v[1] * inv - b0.y)) |
+                  (static_cast<uint32_t>(pack_e4m3(v[2] * inv - b1.x, v[3] * inv - b1.y)) << 16);
+        }
+        if (t < T) {
+          reinterpret_cast<uint4*>(dst)[2 * c + i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          reinterpret_cast<uint4*>(dst + 576)[2 * c + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
-      reinterpret_cast<uint4*>(dst)[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      reinterpret_cast<uint4*>(dst + 576)[i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if (rank == 3) {
+    if (rank == 3 && t < T) {
       const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
       uint32_t* dr = reinterpret_cast<uint32_t*>(q8 + grow * 1152 + 512);
 #pragma unroll
@@ -334,7 +345,38 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 1)
 }
 
 // ============================================================ 2. attention
-constexpr int SLOT = BK * 128;              // one 128-column latent block of a tile, 16 KB
+// The bounded waits of this kernel: one try (which itself waits for some 2700
+// clk) where they stand, the rest out of line.  Inline, the code of a wait that
+// runs out lies between the instructions of the loops, which then do not fit
+// the instruction cache.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, status, abort_flag);
+}
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, status, abort_flag);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, status, abort_flag));
+}
+
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and
+// m = ceil(2^(31 + l) / d), m d exceeds 2^(31 + l) by less than 2^l, so the
+// product's error stays below 2^(31 + l) / d.
+struct FastDiv {
+  uint32_t m;
+  int shift, d;
+};
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.m) >> f.shift);
+}
+
+// A ring slot holds half of a tile's latent columns (two 128-column blocks) in
+// groups of eight keys: [key / 8][block][key % 8][128 bytes], swizzled within
+// the 1 KB of each group and block.  One TMA instruction then loads both blocks
+// of a whole run of keys (a lone lane needs about 130 clk for an instruction,
+// so their number counts), and runs follow each other at the stride of a group.
+constexpr int SLOT = BK * 256;              // 32 KB
+constexpr int GROUP = 2048;                 // eight keys of a slot
 constexpr int ROPE = BK * 64;               // its rope part, 8 KB
 constexpr float kShift = 5.0f;              // weights are kept around 2^5 of e4m3's 448
 constexpr float kGrow = 8.0f;               // and may grow to 2^8 before the reference moves
@@ -351,9 +393,10 @@ constexpr float kGrow = 8.0f;               // and may grow to 2^8 before the re
 template <bool WIDE>
 struct Shape {
   static constexpr int ROWS = WIDE ? 64 : 32;
-  static constexpr int COLS = ROWS / 2;                   // rows of a softmax warpgroup
+  static constexpr int GROUPS = ROWS / 16;                // softmax warpgroups, 16 rows each
+  static constexpr int THREADS = 64 + 128 * GROUPS;       // producer, MMA and softmax warps
   static constexpr int NQ = 2 * ROWS;                     // score columns of a tile
-  static constexpr int SLOTS = WIDE ? 8 : 10;
+  static constexpr int SLOTS = WIDE ? 4 : 5;
   static constexpr int ROPES = WIDE ? 1 : 2;
   static constexpr int QBLOCK = NQ * 128;                 // query operand, 128 columns
   static constexpr int QBYTES = NQ * 576;
@@ -363,16 +406,17 @@ struct Shape {
   static constexpr int AT_Q = AT_ROPE + ROPES * ROPE;
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
-  static constexpr int TOTAL = AT_BAR + 1920 + 1024;
+  static constexpr int TOTAL = AT_BAR + 2048 + 1024;
   static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x 64 columns
   static constexpr uint32_t TM_COLS = 512;
   static_assert(TOTAL <= 227 * 1024 && TM_O + 256 <= TM_COLS, "shared memory, TMEM");
 };
 
 struct AttnSmem {
-  uint64_t k_full[10], k_empty[10];
-  uint64_t r_full[2], r_empty[2];
-  uint64_t q_full, q_free, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
+  uint64_t k_full[5], k_empty[5];     // slots
+  uint64_t r_full[2], r_empty[2];     // rope parts
+  uint64_t fixed;                     // a masked tile's values have been cleaned
+  uint64_t q_full, q_free, s_full[2], s_free[2], p_full, pv_done, o_free, drain, group[4];
   uint32_t tmem;
   int abort;
   alignas(16) float rf[64];   // per query row: factor on the raw score,
@@ -381,8 +425,10 @@ struct AttnSmem {
   alignas(16) float d[64];    // and step of the exponent;
   int top[64];                // largest weight of a row (order-preserving integers)
   int lim[64];                // keys of the segment that the row sees
+  int bad[4][2];              // [group][tile & 1]: a weight of the tile is out of range
+  int run[32], last[16];      // cache rows of the runs that are loaded next, and of the tile before them
 };
-static_assert(sizeof(AttnSmem) <= 1920, "barrier block");
+static_assert(sizeof(AttnSmem) <= 2048, "barrier block");
 
 struct Q8Params {
   const PlanHead* head;
@@ -394,7 +440,8 @@ struct Q8Params {
   const int32_t* indices;
   __half* o_part;          // [slot][members][rows][512], O / (sum of weights * smax)
   float2* meta;            // [slot][members][rows]: LSE in log2, smax (the segment's largest row scale)
-  int indices_stride, num_pages, page_size, max_pages, scale_block;
+  int indices_stride, num_pages, max_pages, cache_rows;
+  FastDiv page, block;     // page size and scale_block
   int H, R, T, pieces, members, box;
   float scale_log2;
   int32_t* status;
@@ -407,9 +454,11 @@ __device__ __forceinline__ PlanEntry load_entry(const PlanEntry* e) {
   r.L = y.x; r.tiles = y.y; r.units = y.z; r.items = y.w;
   return r;
 }
-// First unit of piece g, and the piece of unit u.
+// First unit of piece g, floor(g units / pieces) (pieces <= 2^15, so that the
+// remainders' product has 32 bits), and the piece of unit u.
 __device__ __forceinline__ int piece_begin(int g, int pieces, int units) {
-  return static_cast<int>(static_cast<long long>(g) * units / pieces);
+  const uint32_t q = static_cast<uint32_t>(units) / pieces, r = static_cast<uint32_t>(units) - q * pieces;
+  return static_cast<int>(g * q + g * r / static_cast<uint32_t>(pieces));
 }
 __device__ __forceinline__ int piece_of(int u, int pieces, int units) {
   return static_cast<int>((static_cast<long long>(u + 1) * pieces - 1) / units);
@@ -427,38 +476,37 @@ struct Segment {
 
 // The segments of a piece in order.  Every role of the CTA walks them by itself.
 struct Walk {
-  int u, u1, e, entries, units;
+  int u, u1, e, end;      // next unit, the piece's end, entry, where its units end
   PlanEntry pe;
 };
 __device__ __forceinline__ Walk walk_begin(const Q8Params& p, int piece) {
   Walk w;
-  w.entries = __ldg(&p.head->entries);
-  w.units = __ldg(&p.head->units);
+  const int entries = __ldg(&p.head->entries), units = __ldg(&p.head->units);
   w.e = 0;
   // No more pieces than units, so that none between two others is empty.
-  const int pieces = min(p.pieces, w.units);
+  const int pieces = min(p.pieces, units);
   w.u = w.u1 = 0;
   if (piece >= pieces) return w;
-  w.u = piece_begin(piece, pieces, w.units);
-  w.u1 = piece_begin(piece + 1, pieces, w.units);
-  if (w.u < w.u1) {
-    // Last entry with units <= u that has any (a search over ascending numbers;
-    // entries without units share the next one's number and come before it).
-    int lo = 0, hi = w.entries;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(&p.entries[mid].units) <= w.u) lo = mid; else hi = mid;
-    }
-    w.e = lo;
-    w.pe = load_entry(p.entries + lo);
+  w.u = piece_begin(piece, pieces, units);
+  w.u1 = piece_begin(piece + 1, pieces, units);
+  // Last entry with units <= u that has any (a search over ascending numbers;
+  // entries without units share the next one's number and come before it).
+  int lo = 0, hi = entries;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(&p.entries[mid].units) <= w.u) lo = mid; else hi = mid;
   }
+  w.e = lo;
+  w.pe = load_entry(p.entries + lo);
+  w.end = __ldg(&p.entries[lo + 1].units);
   return w;
 }
 template <int ROWS>
 __device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member, int piece, Segment& s) {
   while (w.u < w.u1) {
-    if (w.u >= w.pe.units + w.pe.tiles * static_cast<int>((static_cast<long long>(w.pe.n) * p.H + p.members * ROWS - 1) / (p.members * ROWS))) {
+    if (w.u >= w.end) {
       w.pe = load_entry(p.entries + ++w.e);          // units remain, so there is one
+      w.end = __ldg(&p.entries[w.e + 1].units);
       continue;
     }
     const int off = w.u - w.pe.units;
@@ -490,37 +538,39 @@ __device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member
 // listed row), then the row or -1 (reported).
 __device__ __forceinline__ int q8_entry(const Q8Params& p, int b, int pos) {
   if (p.indices != nullptr) return __ldg(p.indices + static_cast<long long>(b) * p.indices_stride + pos);
-  const int pi = pos / p.page_size;
+  const int pi = fast_div(pos, p.page);
   return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
 }
 __device__ __forceinline__ int q8_row(const Q8Params& p, int pos, int entry) {
   int row = -1;
   if (p.indices != nullptr) {
-    if (entry >= 0 && entry < p.num_pages * p.page_size) row = entry;
+    if (entry >= 0 && entry < p.cache_rows) row = entry;
   } else if (entry >= 0 && entry < p.num_pages) {
-    row = entry * p.page_size + pos % p.page_size;
+    row = entry * p.page.d + pos - fast_div(pos, p.page) * p.page.d;
   }
   if (row < 0) set_status(p.status, MLA_DEV_BAD_PAGE);
   return row;
 }
 
-// Vote of a softmax warpgroup's four warps: whether any has a weight out of
-// range, and whether any wait of theirs failed.  Both are uniform over the 128
-// threads, so that they leave their loop together.
-__device__ __forceinline__ void softmax_vote(int bar, bool bad, bool fail, bool& any_bad, bool& any_fail) {
-  const int lane = threadIdx.x & 31;
-  const int mine = lane == 0 ? (bad ? 1 : 0) : (lane <= 5 ? (fail ? 1 : 0) : 0);
-  int n;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.popc.aligned.u32 %0, %2, 128, p;\n\t}"
-      : "=r"(n)
-      : "r"(mine), "r"(bar)
-      : "memory");
-  any_fail = n >= 5;
-  any_bad = n % 5 != 0;
+// A softmax warpgroup's barrier, arrived at and waited on apart: its warps
+// go on between the two, and the wait is bounded (a warp that gave up ends the
+// others' waits through the abort flag).
+struct GroupBar {
+  uint32_t bar, phase;
+};
+__device__ __forceinline__ void group_arrive(const GroupBar& g) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(g.bar);
 }
-__device__ __forceinline__ void softmax_sync(int bar) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ bool group_wait(GroupBar& g, int32_t* status, volatile int* abort_flag) {
+  const bool ok = wait_warp(g.bar, g.phase & 1, status, abort_flag);
+  ++g.phase;
+  return ok;
+}
+__device__ __forceinline__ bool group_sync(GroupBar& g, int32_t* status, volatile int* abort_flag) {
+  group_arrive(g);
+  return group_wait(g, status, abort_flag);
+}
 
 // Order-preserving integer of a float (for the integer warp maximum) and back.
 __device__ __forceinline__ int float_order(float x) {
@@ -529,28 +579,43 @@ __device__ __forceinline__ int float_order(float x) {
 }
 __device__ __forceinline__ float order_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_st32(addr, r); else tmem_st16(addr, r);
+// op over the 32 lanes of each of a lane's 16 values; lane l returns value
+// l / 2's.  Lanes exchange halves of their values: 16 shuffles, not 80.
+template <typename Op>
+__device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {
+    const bool up = (lane & (2 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 2 * n));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 constexpr int kSparseProducers = 2;
-constexpr int kAttnThreads = 320;           // producer, MMA, 2 x 4 softmax warps; + 2 copying warps if not DENSE
 
+// A tile's latent blocks are loaded twice, for its scores and again (from L2)
+// for its values, in the order in which the MMAs take them: scores 0, scores 1,
+// values 0, scores 2, values 1, ...  Kept in shared memory through the softmax
+// instead, only two tiles fit, and their loads, MMAs and softmax follow one
+// another: 6000 clk for a tile of 64 rows against 2700 of MMAs.  Streamed, the
+// ring holds nothing but loads in flight, and the softmax of a tile has the time
+// of the MMAs between its scores and its values.
+//
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
-// multiple of 8) two warps copy the rows with cp.async.
+// multiple of 8) warps copy the rows with cp.async.
 template <bool DENSE, bool WIDE>
-__global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSparseProducers, 1)
+__global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSparseProducers), 1)
     q8_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qr_map,
                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
                    const Q8Params p) {
   using C = Shape<WIDE>;
-  constexpr int ROWS = C::ROWS, COLS = C::COLS, SLOTS = C::SLOTS, ROPES = C::ROPES, NQ = C::NQ;
+  constexpr int ROWS = C::ROWS, GROUPS = C::GROUPS, SLOTS = C::SLOTS, ROPES = C::ROPES, NQ = C::NQ;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_COLS = C::TM_COLS;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, NQ, false, false);
   constexpr uint32_t IDESC_PV = idesc_e4m3(128, 64, true, true);
@@ -563,6 +628,7 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
   pdl_enter();
 
   if (threadIdx.x == 0) {
+    // A block's load is counted in bytes (DENSE), or by the copying threads' arrivals.
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(smem_u32(&sh->k_full[s]), DENSE ? 1 : 32 * kSparseProducers);
       mbar_init(smem_u32(&sh->k_empty[s]), 1);
@@ -571,16 +637,21 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
       mbar_init(smem_u32(&sh->r_full[s]), DENSE ? 1 : 32 * kSparseProducers);
       mbar_init(smem_u32(&sh->r_empty[s]), 1);
     }
+    mbar_init(smem_u32(&sh->fixed), 4 * GROUPS);
     mbar_init(smem_u32(&sh->q_full), 1);
     mbar_init(smem_u32(&sh->q_free), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh->s_full[i]), 1);
-      mbar_init(smem_u32(&sh->s_free[i]), 8);
+      mbar_init(smem_u32(&sh->s_free[i]), 4 * GROUPS);
     }
-    mbar_init(smem_u32(&sh->p_full), 8);
+    mbar_init(smem_u32(&sh->p_full), 4 * GROUPS);
     mbar_init(smem_u32(&sh->pv_done), 1);
-    mbar_init(smem_u32(&sh->o_free), 8);
+    mbar_init(smem_u32(&sh->o_free), 4 * GROUPS);
     mbar_init(smem_u32(&sh->drain), 1);
+    for (int i = 0; i < GROUPS; ++i) {
+      mbar_init(smem_u32(&sh->group[i]), 4);
+      sh->bad[i][0] = sh->bad[i][1] = 0;
+    }
     // An earlier kernel timed out: no work (and no plan to read).
     sh->abort = timed_out_before(status) ? 1 : 0;
     fence_mbar_init();
@@ -602,11 +673,17 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
 
   if (warp == 0) {
     // ------------------------------------------------------------ queries, and the keys' TMA loads
-    uint32_t seg = 0, issued = 0, r_issued = 0;
+    // One elected lane waits, counts and issues for a whole tile, in straight
+    // code; the warp only looks up the rows (a warp-wide step for every block
+    // took 700 clk, three times the load itself).
+    uint32_t seg = 0;
+    uint32_t sk = 0, tk = 0, sr = 0, tr = 0;          // slot and turn of the next latent block and rope part
     bool ok = true;
+    const int nbox = BK / p.box;                      // runs of a tile, 16 at most
+    const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
     while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
       auto load_q = [&]() -> bool {
-        if (seg > 0 && !mbar_wait_warp(smem_u32(&sh->q_free), (seg - 1) & 1, status, abort_flag)) return false;
+        if (seg > 0 && !wait_warp(smem_u32(&sh->q_free), (seg - 1) & 1, status, abort_flag)) return false;
         if (elect_one()) {
           const uint32_t qf = smem_u32(&sh->q_full);
           mbar_expect_tx(qf, C::QBYTES);
@@ -625,173 +702,214 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
         return true;
       };
       if constexpr (DENSE) {
-        const int nbox = BK / p.box;                      // runs of a tile, 16 at most
-        const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
         // Lane l has run l % nbox of tile j0 + l / nbox; the next tiles' table
         // entries are read while these are loaded.
+        const int n = sg.n;
         auto entry_of = [&](int j0) -> int {
           const int pos = sg.key0 + j0 * BK + lane * p.box;
           return pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
         };
-        int entry = entry_of(0), row = 0;
+        int entry = entry_of(0);
         // A later segment's queries wait for the scores before them; its first
         // keys need not.
         const bool late = seg > 0;
         if (!late) ok = load_q();
-        for (int j = 0; j < sg.n && ok; ++j) {
-          const int at = j % span;
-          if (at == 0) {
-            const int pos = sg.key0 + j * BK + lane * p.box;
-            row = pos < sg.key1 ? q8_row(p, pos, entry) : 0;
-            if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
-            entry = entry_of(j + span);
-          }
-          const int boxes = min(nbox, (sg.key1 - (sg.key0 + j * BK) + p.box - 1) / p.box);   // runs that hold a key
+        int base = 0, row = 0;                            // first tile of the batch, this lane's run in it
+        auto runs = [&](int j) { return j + 1 < n ? nbox : (sg.key1 - (sg.key0 + j * BK) + p.box - 1) / p.box; };
+        // One elected lane: a tile's two slots, and its rope part.
+        auto blocks = [&](int j, bool rope) -> bool {
+          const int boxes = runs(j);
+          const int* rows = j >= base ? sh->run + (j - base) * nbox : sh->last;
 #pragma unroll
-          for (int c = 0; c < 5; ++c) {
-            const uint32_t s = c < 4 ? issued % SLOTS : r_issued % ROPES;
-            const uint32_t turn = c < 4 ? issued / SLOTS : r_issued / ROPES;
-            const uint32_t empty = smem_u32(c < 4 ? &sh->k_empty[s] : &sh->r_empty[s]);
-            const uint32_t full = smem_u32(c < 4 ? &sh->k_full[s] : &sh->r_full[s]);
-            const uint32_t dst = smem_u32(smem + (c < 4 ? s * SLOT : C::AT_ROPE + s * ROPE));
-            constexpr int W[5] = {128, 128, 128, 128, 64};
-            if (turn > 0 && !(ok = mbar_wait_warp(empty, (turn & 1) ^ 1, status, abort_flag))) break;
-            if (elect_one()) mbar_expect_tx(full, boxes * p.box * W[c]);
-            for (int x = 0; x < boxes; ++x) {
-              const int r = __shfl_sync(0xffffffffu, row, at * nbox + x);
-              if (elect_one()) tma_load_2d(dst + x * p.box * W[c], c < 4 ? &k_map : &kr_map, full, c * 128, r);
+          for (int c = 0; c < 2; ++c) {
+            if (tk > 0 && !wait_one(smem_u32(&sh->k_empty[sk]), (tk & 1) ^ 1, status, abort_flag)) return false;
+            const uint32_t full = smem_u32(&sh->k_full[sk]);
+            mbar_expect_tx(full, boxes * p.box * 256);
+            const uint32_t dst = smem_u32(smem) + sk * SLOT;
+            for (int x = 0; x < boxes; ++x) tma_load_4d(dst + x * p.box * 256, &k_map, full, 0, 0, 2 * c, rows[x] >> 3);
+            if (++sk == SLOTS) {
+              sk = 0;
+              ++tk;
             }
-            if (c < 4) ++issued; else ++r_issued;
           }
-          if (late && j == 0 && ok) ok = load_q();
+          if (rope) {
+            if (tr > 0 && !wait_one(smem_u32(&sh->r_empty[sr]), (tr & 1) ^ 1, status, abort_flag)) return false;
+            const uint32_t full = smem_u32(&sh->r_full[sr]);
+            mbar_expect_tx(full, boxes * p.box * 64);
+            const uint32_t dst = smem_u32(smem + C::AT_ROPE) + sr * ROPE;
+            for (int x = 0; x < boxes; ++x) tma_load_2d(dst + x * p.box * 64, &kr_map, full, 512, rows[x]);
+            if (++sr == ROPES) {
+              sr = 0;
+              ++tr;
+            }
+          }
+          return true;
+        };
+        for (int j0 = 0; j0 < n && ok; j0 += span) {
+          const int pos = sg.key0 + j0 * BK + lane * p.box;
+          // The batch before was full: its last tile's values are still to come.
+          if (lane >= 32 - nbox) sh->last[lane - (32 - nbox)] = row;
+          row = pos < sg.key1 ? q8_row(p, pos, entry) : 0;
+          if (row < 0) row = p.cache_rows;                   // past the end: reads zeros
+          sh->run[lane] = row;
+          base = j0;
+          entry = entry_of(j0 + span);
+          __syncwarp();
+          const int j1 = min(n, j0 + span);
+          bool good = true;
+          if (elect_one()) {
+            for (int j = j0; j < j1 && good; ++j) {
+              if (late && j == 0) break;
+              good = blocks(j, true) && (j == 0 || blocks(j - 1, false));
+            }
+            if (late && j0 == 0) good = blocks(0, true);
+          }
+          ok = __all_sync(0xffffffffu, good);
+          if (late && j0 == 0 && ok && (ok = load_q())) {
+            if (elect_one())
+              for (int j = 1; j < j1 && good; ++j) good = blocks(j, true) && blocks(j - 1, false);
+            ok = __all_sync(0xffffffffu, good);
+          }
+        }
+        if (ok) {
+          bool good = true;
+          if (elect_one()) good = blocks(n - 1, false);
+          ok = __all_sync(0xffffffffu, good);
         }
       } else {
         ok = load_q();
       }
     }
-    // Every load lands before the CTA leaves.
-    volatile int never = 0;
+    // Every load lands before the CTA leaves: the last use of each slot.  (The
+    // elected lane is the same one throughout: it has the counters.)
     if constexpr (DENSE) {
-      for (uint32_t s = 0; s < SLOTS; ++s)
-        if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / SLOTS) & 1, status, &never);
-      for (uint32_t s = 0; s < ROPES; ++s)
-        if (r_issued > s) mbar_wait_warp(smem_u32(&sh->r_full[s]), ((r_issued - 1 - s) / ROPES) & 1, status, &never);
+      if (elect_one()) {
+        volatile int never = 0;
+        for (uint32_t s = 0; s < SLOTS; ++s) {
+          const uint32_t uses = tk + (s < sk ? 1 : 0);
+          if (uses > 0) wait_one(smem_u32(&sh->k_full[s]), (uses - 1) & 1, status, &never);
+        }
+        for (uint32_t s = 0; s < ROPES; ++s) {
+          const uint32_t uses = tr + (s < sr ? 1 : 0);
+          if (uses > 0) wait_one(smem_u32(&sh->r_full[s]), (uses - 1) & 1, status, &never);
+        }
+      }
+      __syncwarp();
     }
-    if (seg > 0) mbar_wait_warp(smem_u32(&sh->q_full), (seg - 1) & 1, status, &never);
+    volatile int never_q = 0;
+    if (seg > 0) wait_warp(smem_u32(&sh->q_full), (seg - 1) & 1, status, &never_q);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // One elected lane, from descriptors that only need an addition (computed
+    // for each MMA they took longer than the MMAs).
     if (elect_one()) {
-      const uint32_t q0 = smem_u32(smem + C::AT_Q);
-      const uint32_t p0 = smem_u32(smem + C::AT_P);
-      // A block of a tile's scores: latent block c, or (c = 4) the rope part.
-      // `g`: the tile's number in the CTA.
-      auto qk_block = [&](uint32_t g, int c, bool last) {
-        const uint32_t d = tmem + TM_S + (g & 1) * NQ;
+      const uint64_t a0 = sdesc(smem_u32(smem), 16, GROUP);                    // slot 0, as keys and as values
+      const uint64_t ar0 = sdesc(smem_u32(smem + C::AT_ROPE), 16, 512, kSwizzle64);
+      const uint64_t b0 = sdesc(smem_u32(smem + C::AT_Q), 16, 1024);
+      const uint64_t br0 = sdesc(smem_u32(smem + C::AT_Q + 4 * C::QBLOCK), 16, 512, kSwizzle64);
+      const uint64_t w0 = sdesc(smem_u32(smem + C::AT_P), 16, 512, kSwizzle64);
+      uint32_t seg = 0, g0 = 0, masked_tiles = 0;      // segments done, tiles before this one's, cleaned tiles
+      uint32_t sk = 0, tk = 0;                         // slot and turn of the next latent block
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_one(smem_u32(bar), parity, status, abort_flag); };
+      auto landed = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (!wait(bar, parity)) return false;
         tc_fence_after();
-        if (!DENSE) fence_async_smem();              // the rows came by cp.async
-        if (c < 4) {
-          const uint32_t a = smem_u32(smem + ((4 * g + c) % SLOTS) * SLOT);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8_ss(d, sdesc(a + kk * 32, 16, 1024), sdesc(q0 + c * C::QBLOCK + kk * 32, 16, 1024), IDESC_QK,
-                      (c | kk) != 0);
-        } else {
-          const uint32_t a = smem_u32(smem + C::AT_ROPE + (g % ROPES) * ROPE);
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            mma_f8_ss(d, sdesc(a + kk * 32, 16, 512, kSwizzle64),
-                      sdesc(q0 + 4 * C::QBLOCK + kk * 32, 16, 512, kSwizzle64), IDESC_QK, 1);
-          tc_commit(smem_u32(&sh->s_full[g & 1]));
-          tc_commit(smem_u32(&sh->r_empty[g % ROPES]));
-          if (last) tc_commit(smem_u32(&sh->q_free));
-        }
+        if (!DENSE) fence_async_smem();                // the rows came by cp.async
+        return true;
       };
-      auto issue_pv = [&](uint32_t g, bool first) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t s = (4 * g + c) % SLOTS;
-          const uint32_t a = smem_u32(smem + s * SLOT);
-          const uint32_t d = tmem + TM_O + c * 64;
+      auto scores = [&](uint32_t g, bool last) -> bool {
+        const uint32_t sb = g & 1, d = tmem + TM_S + sb * NQ;
+        if (g >= 2 && !wait(&sh->s_free[sb], ((g >> 1) & 1) ^ 1)) return false;
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk) {
-            // 32 keys a step: both operands MN-major, groups of 8 keys 1024 (keys) and 512 (weights) bytes apart.
-            const uint64_t ad = sdesc(a + kk * 4096, 16, 1024);
-            mma_f8_ss(d, ad, sdesc(p0 + kk * 2048, 16, 512, kSwizzle64), IDESC_PV, !first || kk != 0);
-            if (WIDE) mma_f8_ss(d, ad, sdesc(p0 + C::PTERM + kk * 2048, 16, 512, kSwizzle64), IDESC_PV, 1);
+        for (int c = 0; c < 2; ++c) {
+          if (!landed(&sh->k_full[sk], tk & 1)) return false;
+          const uint64_t ad = a0 + sk * (SLOT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)                 // blocks 2 c and 2 c + 1, 32 columns a step
+            mma_f8_ss(d, ad + (kk >> 2) * 64 + (kk & 3) * 2, b0 + (2 * c + (kk >> 2)) * (C::QBLOCK >> 4) + (kk & 3) * 2,
+                      IDESC_QK, (c | kk) != 0);
+          tc_commit(smem_u32(&sh->k_empty[sk]));
+          if (++sk == SLOTS) {
+            sk = 0;
+            ++tk;
           }
-          tc_commit(smem_u32(&sh->k_empty[s]));
+        }
+        const uint32_t rs = g % ROPES;
+        if (!landed(&sh->r_full[rs], (g / ROPES) & 1)) return false;
+        const uint64_t ad = ar0 + rs * (ROPE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) mma_f8_ss(d, ad + kk * 2, br0 + kk * 2, IDESC_QK, 1);
+        tc_commit(smem_u32(&sh->s_full[sb]));
+        tc_commit(smem_u32(&sh->r_empty[rs]));
+        if (last) tc_commit(smem_u32(&sh->q_free));
+        return true;
+      };
+      auto values = [&](uint32_t g, bool first, bool masked) -> bool {
+        if (!wait(&sh->p_full, g & 1)) return false;
+        // O is free once the segment before has been read.
+        if (first && seg > 0 && !wait(&sh->o_free, (seg - 1) & 1)) return false;
+        if (masked && !wait(&sh->fixed, masked_tiles++ & 1)) return false;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (!landed(&sh->k_full[sk], tk & 1)) return false;
+          const uint64_t ad = a0 + sk * (SLOT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // Block 2 c + kk / 4, 32 keys a step: both operands MN-major, groups of 8 keys
+            // 2048 (keys) and 512 (weights) bytes apart.
+            const uint64_t av = ad + (kk >> 2) * 64 + (kk & 3) * (4 * GROUP >> 4), wv = w0 + (kk & 3) * 128;
+            const uint32_t d = tmem + TM_O + (2 * c + (kk >> 2)) * 64;
+            mma_f8_ss(d, av, wv, IDESC_PV, !first || (kk & 3) != 0);
+            if (WIDE) mma_f8_ss(d, av, wv + (C::PTERM >> 4), IDESC_PV, 1);
+          }
+          tc_commit(smem_u32(&sh->k_empty[sk]));
+          if (++sk == SLOTS) {
+            sk = 0;
+            ++tk;
+          }
         }
         tc_commit(smem_u32(&sh->pv_done));
+        return true;
       };
-      uint32_t seg = 0, g0 = 0;                        // segments done, tiles before this segment
-      bool ok = true;
       while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
-        if (!(ok = mbar_wait(smem_u32(&sh->q_full), seg & 1, status, abort_flag))) break;
-        // Whichever is ready goes next, P V first (it frees key slots): waiting
-        // for the next tile's keys in front of a ready P V would keep the slots
-        // that those keys need.
-        int jq = 0, cq = 0, jp = 0;                    // next score tile and block, next P V
-        uint32_t idle = 0;
-        uint64_t since = 0;
-        while (ok && jp < sg.n) {
-          bool did = false;
-          if (jp < jq && mbar_test(smem_u32(&sh->p_full), (g0 + jp) & 1)) {
-            // O is free once the segment before has been read.
-            if (jp == 0 && seg > 0 && !(ok = mbar_wait(smem_u32(&sh->o_free), (seg - 1) & 1, status, abort_flag))) break;
-            issue_pv(g0 + jp, jp == 0);
-            ++jp;
-            did = true;
-          } else if (jq < sg.n) {
-            const uint32_t g = g0 + jq, u = 4 * g + cq;
-            const bool have = cq < 4 ? mbar_test(smem_u32(&sh->k_full[u % SLOTS]), (u / SLOTS) & 1)
-                                     : mbar_test(smem_u32(&sh->r_full[g % ROPES]), (g / ROPES) & 1);
-            if (have && (cq > 0 || g < 2 || mbar_test(smem_u32(&sh->s_free[g & 1]), ((g >> 1) & 1) ^ 1))) {
-              qk_block(g, cq, jq == sg.n - 1);
-              if (++cq == 5) {
-                cq = 0;
-                ++jq;
-              }
-              did = true;
-            }
-          }
-          if (did) {
-            idle = 0;
-          } else if ((++idle & 63u) == 0) {            // bounded, as every wait
-            if (*abort_flag) ok = false;
-            if (idle == 64) since = globaltimer();
-            if (ok && globaltimer() - since > kWaitLimitNs) {
-              set_status(status, MLA_DEV_TIMEOUT);
-              raise_abort(abort_flag);
-              ok = false;
-            }
-          }
+        // Tiles that hold a key which some row does not see.
+        int all = sg.key1 - sg.key0;
+        if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
+        ok = wait(&sh->q_full, seg & 1) && scores(g0, sg.n == 1);
+        for (int j = 0; j < sg.n && ok; ++j) {
+          if (j + 1 < sg.n) ok = scores(g0 + j + 1, j + 2 == sg.n);
+          ok = ok && values(g0 + j, j == 0, (j + 1) * BK > all);
         }
         g0 += sg.n;
         ++seg;
       }
       tc_commit(smem_u32(&sh->drain));
       volatile int never = 0;
-      mbar_wait(smem_u32(&sh->drain), 0, status, &never);
+      wait_one(smem_u32(&sh->drain), 0, status, &never);
     }
     __syncwarp();
-  } else if (warp < 10) {
+  } else if (warp < 2 + 4 * GROUPS) {
     // ------------------------------------------------------------ softmax (thread = key), epilogue
-    // Two warpgroups, each with all 128 keys and half of the tile's query rows.
-    const int wg = (warp - 2) >> 2, bar = 1 + wg;
-    const int c0 = wg * COLS;                         // first query row of the group
+    // Warpgroups with all 128 keys and 16 of the tile's query rows each.  The
+    // code of a tile is kept small and there once: with 32 rows a thread and a
+    // second copy for a moving reference it did not fit the instruction cache,
+    // and every warp of the kernel ran at a fifth of its speed.
+    const int wg = (warp - 2) >> 2;
+    GroupBar gb{smem_u32(&sh->group[wg]), 0u};
+    const int c0 = wg * 16;                           // first query row of the group
     const int q4 = warp & 3;
     const int key = q4 * 32 + lane;
     const int tid = (warp - 2 - 4 * wg) * 32 + lane;  // 0..127 in the group
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
     uint8_t* pbuf = smem + C::AT_P;
-    uint32_t seg = 0, g0 = 0;
+    uint32_t seg = 0, g0 = 0;                         // segments done, tiles before this one's
     bool fail = false;
     while (!fail && walk_next<ROWS>(p, wk, member, piece, sg)) {
-      const int mine = min(COLS, sg.nrows - c0);      // rows of this group (none: it only keeps the pace)
+      const int mine = min(16, sg.nrows - c0);        // rows of this group (none: it only keeps the pace)
       const int span = sg.key1 - sg.key0;
       bool seen = false;                              // this thread's row has a reference
-      if (tid < COLS) {
+      if (tid < 16) {
         const int r = c0 + tid;
         float rf = 0.f;
         int lim = 0;
@@ -808,261 +926,321 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
       // Keys that every row of the tile sees.
       int all = span;
       if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
-      softmax_sync(bar);
-      float2 l[COLS / 2];
+      if (!group_sync(gb, status, abort_flag)) {
+        fail = true;
+        break;
+      }
+      float2 l[8];
 #pragma unroll
-      for (int c = 0; c < COLS / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      for (int c = 0; c < 8; ++c) l[c] = make_float2(0.f, 0.f);
       float smax = 0.f;
       // The scale of this thread's key is read one tile ahead, its table entry two.
       auto key_entry = [&](int j) -> int {
         const int pos = sg.key0 + j * BK + key;
         return j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
       };
-      auto key_scale = [&](int j, int entry) -> float {
-        const int pos = sg.key0 + j * BK + key;
-        if (j >= sg.n || pos >= sg.key1) return 1.f;
-        const int row = q8_row(p, pos, entry);
-        return row < 0 ? 1.f : __ldg(p.kv_scales + row / p.scale_block);
-      };
-      int entry = key_entry(1);
-      float next = key_scale(0, key_entry(0));
-      for (int j = 0; j < sg.n; ++j) {
-        const uint32_t g = g0 + j, sb = g & 1;
+      float next = 1.f;
+      int entry = key_entry(0);
+      for (int j = -1; j < sg.n; ++j) {
+        // (Turn -1 only reads the first tile's scale.)
         float ksc = next;
-        next = key_scale(j + 1, entry);
-        entry = key_entry(j + 2);
+        {
+          const int pos = sg.key0 + (j + 1) * BK + key;
+          next = 1.f;
+          if (j + 1 < sg.n && pos < sg.key1) {
+            const int row = q8_row(p, pos, entry);
+            if (row >= 0) next = __ldg(p.kv_scales + fast_div(row, p.block));
+          }
+          entry = key_entry(j + 2);
+        }
+        if (j < 0) continue;
+        const uint32_t g = g0 + j, sb = g & 1;
         const bool valid = sg.key0 + j * BK + key < sg.key1;
         const bool broken = !(fabsf(ksc) < kInf);     // a scale that is no number: the key's scores are NaN
         if (broken) ksc = 1.f;
         if (valid) smax = fmaxf(smax, fabsf(ksc));
         const float lsc = __log2f(fabsf(ksc));
-        const float2 xs = broken ? make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)) : make_float2(ksc, ksc);
-        float2 t[COLS / 2];
-        const bool got = mbar_wait_warp(smem_u32(&sh->s_full[sb]), (g >> 1) & 1, status, abort_flag);
-        fail |= !got;
-        float mx = -kInf;
+        const float xv = broken ? __int_as_float(0x7fc00000) : ksc;
         const bool masked = (j + 1) * BK > all;       // some row does not see every key of the tile
-        if (got && mine > 0) {
-          tc_fence_after();
-          uint32_t hi[COLS], lo[COLS];
-          tmem_ld_n<COLS>(tmem + lane_off + TM_S + sb * NQ + c0, hi);
-          tmem_ld_n<COLS>(tmem + lane_off + TM_S + sb * NQ + ROWS + c0, lo);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < COLS; c += 4) {
-            const float4 rf = *reinterpret_cast<const float4*>(sh->rf + c0 + c);
-            const float4 ry = *reinterpret_cast<const float4*>(sh->ry + c0 + c);
-            const float2 a = __fadd2_rn(make_float2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1])),
-                                        make_float2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1])));
-            const float2 b = __fadd2_rn(make_float2(__uint_as_float(hi[c + 2]), __uint_as_float(hi[c + 3])),
-                                        make_float2(__uint_as_float(lo[c + 2]), __uint_as_float(lo[c + 3])));
-            t[c / 2] = __ffma2_rn(__fmul2_rn(a, xs), make_float2(rf.x, rf.y), make_float2(ry.x, ry.y));
-            t[c / 2 + 1] = __ffma2_rn(__fmul2_rn(b, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
-          }
-          tc_fence_before();
-        } else {
-#pragma unroll
-          for (int c = 0; c < COLS / 2; ++c) t[c] = make_float2(0.f, 0.f);
-        }
-        __syncwarp();
-        if (got && lane == 0) mbar_arrive(smem_u32(&sh->s_free[sb]));
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < COLS / 2; ++c) {
-            t[c].x = j * BK + key < sh->lim[c0 + 2 * c] ? t[c].x : -kInf;
-            t[c].y = j * BK + key < sh->lim[c0 + 2 * c + 1] ? t[c].y : -kInf;
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < COLS / 2; ++c)
-          if (2 * c < mine) mx = fmax3(mx, t[c].x, 2 * c + 1 < mine ? t[c].y : -kInf);
-        bool any_bad, any_fail;
-        softmax_vote(bar, __any_sync(0xffffffffu, mx + lsc > kGrow), fail, any_bad, any_fail);
-        if (any_fail) {
+        if (!wait_warp(smem_u32(&sh->s_full[sb]), (g >> 1) & 1, status, abort_flag)) {
           fail = true;
           break;
         }
-        // The weights' buffer (and O, where the reference moves) is free once
-        // P V of the tile before is done.
-        if (g > 0 && !mbar_wait_warp(smem_u32(&sh->pv_done), (g - 1) & 1, status, abort_flag)) fail = true;
-        if (j == 0 || any_bad) {
-          // ---- move the reference of the rows that need it
-          tc_fence_after();
-          int own = 0;
+        tc_fence_after();
+        // The first tile sets the rows' references; in a later one the weights
+        // are computed against them, and once more if one has to move.
+        bool move = j == 0;
+        if (move && g > 0 && !wait_warp(smem_u32(&sh->pv_done), (g - 1) & 1, status, abort_flag)) {
+          fail = true;
+          break;
+        }
+        float2 t[8];
+        uint32_t hi[4], lo[4];
+        while (true) {
+          // Exponents (log2 units) of the key's weights.
+          {
+            uint32_t a[16], b[16];
+            tmem_ld16(tmem + lane_off + TM_S + sb * NQ + c0, a);
+            tmem_ld16(tmem + lane_off + TM_S + sb * NQ + ROWS + c0, b);
+            tmem_ld_wait();
+            const float2 xs = make_float2(xv, xv);
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            const int v = __reduce_max_sync(0xffffffffu, float_order(fmaxf((c & 1 ? t[c / 2].y : t[c / 2].x) + lsc, -kInf)));
-            if (lane == c) own = v;
+            for (int c = 0; c < 8; c += 2) {
+              const float4 rf = *reinterpret_cast<const float4*>(sh->rf + c0 + 2 * c);
+              const float4 ry = *reinterpret_cast<const float4*>(sh->ry + c0 + 2 * c);
+              const float2 u = __fadd2_rn(make_float2(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])),
+                                          make_float2(__uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1])));
+              const float2 v = __fadd2_rn(make_float2(__uint_as_float(a[2 * c + 2]), __uint_as_float(a[2 * c + 3])),
+                                          make_float2(__uint_as_float(b[2 * c + 2]), __uint_as_float(b[2 * c + 3])));
+              t[c] = __ffma2_rn(__fmul2_rn(u, xs), make_float2(rf.x, rf.y), make_float2(ry.x, ry.y));
+              t[c + 1] = __ffma2_rn(__fmul2_rn(v, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
+            }
           }
-          if (lane < COLS) atomicMax(&sh->top[c0 + lane], own);   // a maximum: the order does not matter
-          softmax_sync(bar);
-          if (tid < COLS) {
-            const float mm = order_float(sh->top[c0 + tid]);
-            sh->top[c0 + tid] = float_order(-kInf);
-            float d = 0.f, f = 1.f;
-            if (mm > -kInf) {
-              if (!seen) {
-                d = kShift - mm;
-                seen = true;
-              } else if (mm > kShift) {
-                d = kShift - mm;
-                f = ex2(d);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              t[c].x = j * BK + key < sh->lim[c0 + 2 * c] ? t[c].x : -kInf;
+              t[c].y = j * BK + key < sh->lim[c0 + 2 * c + 1] ? t[c].y : -kInf;
+            }
+          }
+          if (!move) {
+            // Whether any key of the group has a weight out of range: told to
+            // the others here, looked at when the weights are ready.  (Rows past
+            // the last hold garbage: with less than 16 they are looked at one by one.)
+            float mx = -kInf;
+            if (mine >= 16) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) mx = fmax3(mx, t[c].x, t[c].y);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                if (2 * c < mine) mx = fmaxf(mx, t[c].x);
+                if (2 * c + 1 < mine) mx = fmaxf(mx, t[c].y);
               }
             }
-            sh->ry[c0 + tid] += d;
-            sh->d[c0 + tid] = d;
-            sh->f[c0 + tid] = f;
-          }
-          softmax_sync(bar);
-#pragma unroll
-          for (int c = 0; c < COLS; c += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(sh->d + c0 + c);
-            const float4 f = *reinterpret_cast<const float4*>(sh->f + c0 + c);
-            t[c / 2] = __fadd2_rn(t[c / 2], make_float2(d.x, d.y));
-            t[c / 2 + 1] = __fadd2_rn(t[c / 2 + 1], make_float2(d.z, d.w));
-            l[c / 2] = __fmul2_rn(l[c / 2], make_float2(f.x, f.y));
-            l[c / 2 + 1] = __fmul2_rn(l[c / 2 + 1], make_float2(f.z, f.w));
-          }
-          if (j > 0 && !fail) {
-#pragma unroll 1
-            for (int cb = 0; cb < (WIDE ? 4 : 8); ++cb) {
-              uint32_t r[COLS];
-              const uint32_t ta = tmem + lane_off + TM_O + cb * (WIDE ? 64 : 32) + c0;
-              tmem_ld_n<COLS>(ta, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < COLS; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh->f[c0 + i]);
-              tmem_st_n<COLS>(ta, r);
-            }
-            tmem_st_wait();
-          }
-        }
-        // ---- weights: two e4m3 terms, key-major rows of 64 bytes (64-byte swizzle)
-        if (mine > 0) {
-          uint32_t hi[COLS / 4], lo[COLS / 4];
-          const float2 ks = make_float2(ksc, ksc);
-          // Rounds to four bits: y = x (2^20 + 1) has 24 bits, 20 of which
-          // y - (y - x) cancels.  (The product is an fma with zero so that it
-          // is not merged into the subtractions.)
-          const float2 split = make_float2(1048577.f, 1048577.f);
-#pragma unroll
-          for (int c = 0; c < COLS; c += 4) {
-            uint16_t h[2], w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float2 e = make_float2(ex2(t[c / 2 + i].x), ex2(t[c / 2 + i].y));
-              l[c / 2 + i] = __fadd2_rn(l[c / 2 + i], e);
-              const float2 x = __fmul2_rn(e, ks);
-              const float2 y = __ffma2_rn(x, split, make_float2(0.f, 0.f));
-              const float2 z = __fadd2_rn(y, make_float2(-x.x, -x.y));
-              const float2 a = __fadd2_rn(y, make_float2(-z.x, -z.y));
-              const float2 b = __fadd2_rn(x, make_float2(-a.x, -a.y));
-              h[i] = pack_e4m3(a.x, a.y);
-              w[i] = pack_e4m3(b.x, b.y);
-            }
-            hi[c / 4] = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
-            lo[c / 4] = static_cast<uint32_t>(w[0]) | (static_cast<uint32_t>(w[1]) << 16);
-          }
-          const int sw = (key >> 1) & 3;
-          uint8_t* prow = pbuf + key * 64;
-          if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint8_t* at = prow + (((2 * wg + i) ^ sw) << 4);
-              *reinterpret_cast<uint4*>(at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-              *reinterpret_cast<uint4*>(at + C::PTERM) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-            }
+            if (mx + lsc > kGrow) sh->bad[wg][sb] = 1;
+            group_arrive(gb);
           } else {
-            *reinterpret_cast<uint4*>(prow + ((wg ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(prow + (((2 + wg) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        if (masked && j * BK + key >= all) {
-          // A key that some row does not see: its weight is 0 there, but 0 times
-          // a NaN code is NaN.  Rows past the segment become zeros (they may
-          // hold anything); in the others every NaN code does (a row that sees
-          // such a key has a NaN score, so its result is NaN all the same).
-          // Each group has two of the four latent blocks.
-#pragma unroll 1
-          for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
-            uint4* kr = reinterpret_cast<uint4*>(smem + ((4 * g + c) % SLOTS) * SLOT + key * 128);
-            for (int i = 0; i < 8; ++i) {
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (valid) {
-                v = kr[i];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                for (int x = 0; x < 4; ++x) {
-                  // Bytes equal to 0x7F after clearing the sign.
-                  const uint32_t nan = ((w[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                  w[x] &= ~((nan >> 7) * 0xFFu);
+            // ---- move the reference of the rows that need it
+            float v[16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              v[2 * c] = t[c].x + lsc;
+              v[2 * c + 1] = t[c].y + lsc;
+            }
+            const float m = reduce16(v, [](float x, float y) { return fmaxf(x, y); });
+            if ((lane & 1) == 0) atomicMax(&sh->top[c0 + (lane >> 1)], float_order(m));   // a maximum: in any order
+            if (!group_sync(gb, status, abort_flag)) {
+              fail = true;
+              break;
+            }
+            if (tid < 16) {
+              const float mm = order_float(sh->top[c0 + tid]);
+              sh->top[c0 + tid] = float_order(-kInf);
+              float d = 0.f, f = 1.f;
+              if (mm > -kInf) {
+                if (!seen) {
+                  d = kShift - mm;
+                  seen = true;
+                } else if (mm > kShift) {
+                  d = kShift - mm;
+                  f = ex2(d);
                 }
               }
-              kr[i] = v;
+              sh->ry[c0 + tid] += d;
+              sh->d[c0 + tid] = d;
+              sh->f[c0 + tid] = f;
+            }
+            if (!group_sync(gb, status, abort_flag)) {
+              fail = true;
+              break;
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              t[c] = __fadd2_rn(t[c], *reinterpret_cast<const float2*>(sh->d + c0 + 2 * c));
+              l[c] = __fmul2_rn(l[c], *reinterpret_cast<const float2*>(sh->f + c0 + 2 * c));
+            }
+            if (j > 0) {
+#pragma unroll 1
+              for (int cb = 0; cb < (WIDE ? 4 : 8); ++cb) {
+                uint32_t r[16];
+                const uint32_t ta = tmem + lane_off + TM_O + cb * (WIDE ? 64 : 32) + c0;
+                tmem_ld16(ta, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sh->f[c0 + i]);
+                tmem_st16(ta, r);
+              }
+              tmem_st_wait();
             }
           }
+          // ---- weights, and their two e4m3 terms
+          {
+            const float2 ks = make_float2(ksc, ksc);
+            // Rounds to four bits: y = x (2^20 + 1) has 24 bits, 20 of which
+            // y - (y - x) cancels.  (The product is an fma with zero so that it
+            // is not merged into the subtractions.)
+            const float2 split = make_float2(1048577.f, 1048577.f);
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              uint16_t h[2], w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float2 e = make_float2(ex2(t[c + i].x), ex2(t[c + i].y));
+                t[c + i] = e;
+                const float2 x = __fmul2_rn(e, ks);
+                const float2 y = __ffma2_rn(x, split, make_float2(0.f, 0.f));
+                const float2 z = __fadd2_rn(y, make_float2(-x.x, -x.y));
+                const float2 a = __fadd2_rn(y, make_float2(-z.x, -z.y));
+                const float2 b = __fadd2_rn(x, make_float2(-a.x, -a.y));
+                h[i] = pack_e4m3(a.x, a.y);
+                w[i] = pack_e4m3(b.x, b.y);
+              }
+              hi[c / 2] = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
+              lo[c / 2] = static_cast<uint32_t>(w[0]) | (static_cast<uint32_t>(w[1]) << 16);
+            }
+          }
+          if (move) break;
+          // The weights' buffer (and O, where the reference moves) is free once
+          // P V of the tile before is done.
+          if (!group_wait(gb, status, abort_flag) ||
+              !wait_warp(smem_u32(&sh->pv_done), (g - 1) & 1, status, abort_flag)) {
+            fail = true;
+            break;
+          }
+          // (The other parity's word is cleared for the next tile: all warps
+          // have read it, as they have arrived here after reading it.)
+          move = *reinterpret_cast<volatile int*>(&sh->bad[wg][sb]) != 0;
+          if (tid == 0) sh->bad[wg][sb ^ 1] = 0;
+          if (!move) break;
+          tc_fence_after();
+        }
+        if (fail) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) l[c] = __fadd2_rn(l[c], t[c]);
+        // Key-major rows of 64 bytes (64-byte swizzle): chunk wg, and the second
+        // term in a buffer of its own (wide) or two chunks on.
+        if (mine > 0) {
+          const int sw = (key >> 1) & 3;
+          uint8_t* prow = pbuf + key * 64;
+          *reinterpret_cast<uint4*>(prow + ((wg ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(prow + (WIDE ? C::PTERM + ((wg ^ sw) << 4) : ((2 + wg) ^ sw) << 4)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->p_full));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh->p_full));
+          mbar_arrive(smem_u32(&sh->s_free[sb]));
+        }
+        if (masked) {
+          // A key that some row does not see: its weight is 0 there, but 0 times
+          // a NaN code is NaN.  Rows past the segment become zeros (they may
+          // hold anything); in the others every NaN code does (a row that sees
+          // such a key has a NaN score, so its result is NaN all the same).
+          // The first two warpgroups have one of the tile's two value slots
+          // each, when it lands.
+          if (wg < 2) {
+            const uint32_t u = 4 * g0 + (j + 1 < sg.n ? 4 * j + 4 : 4 * j + 2) + wg;
+            const uint32_t slot = u % SLOTS;
+            if (!wait_warp(smem_u32(&sh->k_full[slot]), (u / SLOTS) & 1, status, abort_flag)) {
+              fail = true;
+              break;
+            }
+            if (j * BK + key >= all) {
+              uint8_t* kr = smem + slot * SLOT + (key >> 3) * GROUP + (key & 7) * 128;
+#pragma unroll 1
+              for (int i = 0; i < 16; ++i) {
+                uint4* at = reinterpret_cast<uint4*>(kr + (i >> 3) * 1024) + (i & 7);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (valid) {
+                  v = *at;
+                  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    // Bytes equal to 0x7F after clearing the sign.
+                    const uint32_t nan = ((w[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    w[x] &= ~((nan >> 7) * 0xFFu);
+                  }
+                }
+                *at = v;
+              }
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->fixed));
+        }
       }
+      if (fail) break;
       g0 += sg.n;
       // ---------------------------------------------------------- epilogue
-      if (!fail && !mbar_wait_warp(smem_u32(&sh->pv_done), (g0 - 1) & 1, status, abort_flag)) fail = true;
+      if (!wait_warp(smem_u32(&sh->pv_done), (g0 - 1) & 1, status, abort_flag) ||
+          !group_sync(gb, status, abort_flag)) {      // every warp is past the row arrays' last use
+        fail = true;
+        break;
+      }
       tc_fence_after();
-      bool any_bad, any_fail;
-      softmax_vote(bar, false, fail, any_bad, any_fail);
-      fail = any_fail;
-      if (!fail && mine > 0) {
-        // Sums over the keys: within each warp by shuffles, then over the four
-        // warps through the row arrays that the segment no longer needs.
-        float own = 0.f;
+      // Sums over the keys: within each warp, then over the four warps through
+      // the row arrays that the segment no longer needs.
+      {
+        float v[16];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-          float v = c & 1 ? l[c / 2].y : l[c / 2].x;
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-          if (lane == c) own = v;
+        for (int c = 0; c < 8; ++c) {
+          v[2 * c] = l[c].x;
+          v[2 * c + 1] = l[c].y;
         }
+        const float sum = reduce16(v, [](float x, float y) { return x + y; });
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
         float* part = q4 == 0 ? sh->rf : (q4 == 1 ? sh->d : (q4 == 2 ? sh->f : reinterpret_cast<float*>(sh->top)));
-        if (lane < COLS) part[c0 + lane] = own;
+        if ((lane & 1) == 0) part[c0 + (lane >> 1)] = sum;
         if (lane == 0) sh->lim[c0 + q4] = __float_as_int(smax);
-        softmax_sync(bar);
-        if (tid < COLS) {
-          const int r = c0 + tid;
-          const float sum = (sh->rf[r] + sh->d[r]) + (sh->f[r] + __int_as_float(sh->top[r]));
-          float s = fmaxf(fmaxf(__int_as_float(sh->lim[c0]), __int_as_float(sh->lim[c0 + 1])),
-                          fmaxf(__int_as_float(sh->lim[c0 + 2]), __int_as_float(sh->lim[c0 + 3])));
-          if (!(s > 0.f)) s = 1.f;
-          sh->f[r] = sum == 0.f ? 0.f : 1.0f / (sum * s);
-          // Weights carry 2^-reference: log2 of the plain sum adds it back.
-          if (tid < mine)
-            p.meta[static_cast<long long>(sg.slot) * ROWS + r] =
-                make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->ry[r], s);
-        }
-        softmax_sync(bar);
-        __half* dst0 = p.o_part + (static_cast<long long>(sg.slot) * ROWS + c0) * 512 + key;
+      }
+      if (!group_sync(gb, status, abort_flag)) {
+        fail = true;
+        break;
+      }
+      if (tid < 16) {
+        const int r = c0 + tid;
+        const float sum = (sh->rf[r] + sh->d[r]) + (sh->f[r] + __int_as_float(sh->top[r]));
+        float s = fmaxf(fmaxf(__int_as_float(sh->lim[c0]), __int_as_float(sh->lim[c0 + 1])),
+                        fmaxf(__int_as_float(sh->lim[c0 + 2]), __int_as_float(sh->lim[c0 + 3])));
+        if (!(s > 0.f)) s = 1.f;
+        sh->f[r] = sum == 0.f ? 0.f : 1.0f / (sum * s);
+        // Weights carry 2^-reference: log2 of the plain sum adds it back.
+        if (tid < mine)
+          p.meta[static_cast<long long>(sg.slot) * ROWS + r] =
+              make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->ry[r], s);
+      }
+      if (!group_sync(gb, status, abort_flag)) {
+        fail = true;
+        break;
+      }
+      if (mine > 0) {
+        __half* dst = p.o_part + (static_cast<long long>(sg.slot) * ROWS + c0) * 512 + key;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[COLS], o2[COLS];
+        for (int c = 0; c < 4; ++c, dst += 128) {
+          uint32_t o[16], o2[16];
           const uint32_t ta = tmem + lane_off + TM_O + c * 64 + c0;
-          tmem_ld_n<COLS>(ta, o);
-          if constexpr (!WIDE) tmem_ld_n<COLS>(ta + 32, o2);
+          tmem_ld16(ta, o);
+          if constexpr (!WIDE) tmem_ld16(ta + 32, o2);
           tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < COLS; ++r) {
+          for (int r = 0; r < 16; ++r) {
             float v = __uint_as_float(o[r]);
             if constexpr (!WIDE) v += __uint_as_float(o2[r]);
             const float f = sh->f[c0 + r];
-            if (r < mine) dst0[r * 512 + c * 128] = __float2half_rn(f == 0.f ? 0.f : v * f);
+            if (r < mine) dst[r * 512] = __float2half_rn(f == 0.f ? 0.f : v * f);
           }
         }
         tc_fence_before();
       }
-      softmax_sync(bar);                              // the row arrays are rewritten by the next segment
-      __syncwarp();
+      if (!group_sync(gb, status, abort_flag)) {      // the row arrays are rewritten by the next segment
+        fail = true;
+        break;
+      }
       if (lane == 0) mbar_arrive(smem_u32(&sh->o_free));
       ++seg;
     }
@@ -1070,11 +1248,11 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
     // ------------------------------------------------------------ listed rows: cp.async
     if constexpr (!DENSE) {
       constexpr int RW = BK / kSparseProducers;       // this warp's keys [RW pw, RW pw + RW) of the tile
-      const int pw = warp - 10;
-      uint32_t issued = 0, r_issued = 0;
+      const int pw = warp - 2 - 4 * GROUPS;
+      uint32_t issued = 0, ropes = 0;
       bool ok = true;
       while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
-        int row[RW / 32], next[RW / 32];              // key 32 x + lane: this tile's row, the next one's table entry
+        int row[RW / 32], prev[RW / 32], next[RW / 32];   // key 32 x + lane: this tile's row, the one before's, the next one's table entry
         auto entries = [&](int j, int (&r)[RW / 32]) {
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
@@ -1082,43 +1260,51 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
             r[x] = j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
           }
         };
+        // A tile's two slots (a chunk of 16 bytes a lane, two rows an
+        // instruction), counted as they land.
+        auto latent = [&](const int (&r)[RW / 32]) -> bool {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t s = issued % SLOTS, turn = issued / SLOTS;
+            if (turn > 0 && !wait_warp(smem_u32(&sh->k_empty[s]), (turn & 1) ^ 1, status, abort_flag)) return false;
+            const uint32_t dst = smem_u32(smem + s * SLOT) + pw * (RW / 8) * GROUP + ((lane >> 3) & 1) * 1024;
+            const uint8_t* src = p.kv_cache + c * 256 + (lane & 15) * 16;
+#pragma unroll
+            for (int i = 0; i < RW / 2; ++i) {
+              const int k = 2 * i + (lane >> 4);
+              const int at = __shfl_sync(0xffffffffu, r[i / 16], k & 31);
+              cp_async16(dst + (k >> 3) * GROUP + (k & 7) * 128 + (((lane & 7) ^ (k & 7)) << 4), src + static_cast<size_t>(at) * 576);
+            }
+            cp_async_arrive(smem_u32(&sh->k_full[s]));
+            ++issued;
+          }
+          return true;
+        };
         entries(0, next);
         for (int j = 0; j < sg.n && ok; ++j) {
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
             const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
+            prev[x] = row[x];
             row[x] = pos < sg.key1 ? q8_row(p, pos, next[x]) : 0;
             if (row[x] < 0) row[x] = 0;               // reported; the result of its rows is not meaningful
           }
           entries(j + 1, next);                       // in flight while the tile is copied
+          if (!(ok = latent(row))) break;
+          const uint32_t s = ropes % ROPES, turn = ropes / ROPES;
+          if (turn > 0 && !(ok = wait_warp(smem_u32(&sh->r_empty[s]), (turn & 1) ^ 1, status, abort_flag))) break;
+          const uint32_t dst = smem_u32(smem + C::AT_ROPE + s * ROPE) + pw * RW * 64;
 #pragma unroll
-          for (int c = 0; c < 5; ++c) {
-            const uint32_t s = c < 4 ? issued % SLOTS : r_issued % ROPES;
-            const uint32_t turn = c < 4 ? issued / SLOTS : r_issued / ROPES;
-            const uint32_t empty = smem_u32(c < 4 ? &sh->k_empty[s] : &sh->r_empty[s]);
-            const uint32_t full = smem_u32(c < 4 ? &sh->k_full[s] : &sh->r_full[s]);
-            if (turn > 0 && !(ok = mbar_wait_warp(empty, (turn & 1) ^ 1, status, abort_flag))) break;
-            if (c < 4) {
-              const uint32_t dst = smem_u32(smem + s * SLOT) + pw * RW * 128;
-#pragma unroll
-              for (int i = 0; i < RW / 4; ++i) {      // four rows of 8 chunks an instruction
-                const int r = 4 * i + (lane >> 3), ch = lane & 7;
-                const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
-                cp_async16(dst + r * 128 + ((ch ^ (r & 7)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + c * 128 + ch * 16);
-              }
-            } else {
-              const uint32_t dst = smem_u32(smem + C::AT_ROPE + s * ROPE) + pw * RW * 64;
-#pragma unroll
-              for (int i = 0; i < RW / 8; ++i) {      // eight rows of 4 chunks
-                const int r = 8 * i + (lane >> 2), ch = lane & 3;
-                const int src = __shfl_sync(0xffffffffu, row[i / 4], r & 31);
-                cp_async16(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), p.kv_cache + static_cast<size_t>(src) * 576 + 512 + ch * 16);
-              }
-            }
-            cp_async_arrive(full);                    // counted as the copies land
-            if (c < 4) ++issued; else ++r_issued;
+          for (int i = 0; i < RW / 8; ++i) {          // eight rows of 4 chunks
+            const int k = 8 * i + (lane >> 2), ch = lane & 3;
+            const int at = __shfl_sync(0xffffffffu, row[i / 4], k & 31);
+            cp_async16(dst + k * 64 + ((ch ^ ((k >> 1) & 3)) << 4), p.kv_cache + static_cast<size_t>(at) * 576 + 512 + ch * 16);
           }
+          cp_async_arrive(smem_u32(&sh->r_full[s]));
+          ++ropes;
+          if (j > 0) ok = latent(prev);
         }
+        ok = ok && latent(row);
       }
       // Every copy lands, and its arrival with it, before the CTA leaves.
       cp_async_commit();
@@ -1126,9 +1312,9 @@ __global__ void __launch_bounds__(DENSE ? kAttnThreads : kAttnThreads + 32 * kSp
       volatile int never = 0;
       if (ok) {
         for (uint32_t s = 0; s < SLOTS; ++s)
-          if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / SLOTS) & 1, status, &never);
+          if (issued > s) wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / SLOTS) & 1, status, &never);
         for (uint32_t s = 0; s < ROPES; ++s)
-          if (r_issued > s) mbar_wait_warp(smem_u32(&sh->r_full[s]), ((r_issued - 1 - s) / ROPES) & 1, status, &never);
+          if (ropes > s) wait_warp(smem_u32(&sh->r_full[s]), ((ropes - 1 - s) / ROPES) & 1, status, &never);
       }
     }
   }
@@ -1349,6 +1535,16 @@ cudaError_t opt_in_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+FastDiv fast_divisor(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  FastDiv f;
+  f.m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+  f.shift = 31 + l;
+  f.d = d;
+  return f;
+}
+
 // Largest power of two, at most 128, that divides the page size.
 int run_rows(int page_size) {
   int g = 1;
@@ -1361,7 +1557,7 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
                         const CUtensorMap& kr_map, const Q8Params& p, long long ctas, cudaStream_t stream) {
   cudaError_t e = opt_in_smem(q8_attn_kernel<DENSE, WIDE>, Shape<WIDE>::TOTAL);
   if (e != cudaSuccess) return e;
-  const int threads = DENSE ? kAttnThreads : kAttnThreads + 32 * kSparseProducers;
+  const int threads = Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSparseProducers);
   return launch_pdl(q8_attn_kernel<DENSE, WIDE>, dim3(static_cast<unsigned>(ctas)), dim3(threads),
                     Shape<WIDE>::TOTAL, stream, q_map, qr_map, k_map, kr_map, p);
 }
@@ -1392,7 +1588,7 @@ DecodeQ8Layout decode_q8_layout(int T, int H, int pieces) {
     return at;
   };
   L.head = take(sizeof(PlanHead));
-  L.entries = take(sizeof(PlanEntry) * static_cast<size_t>(T > 0 ? T : 1));
+  L.entries = take(sizeof(PlanEntry) * (static_cast<size_t>(T) + 1));
   L.q8 = take(R * 1152);
   L.q_scale = take(R * 4);
   // Slots: one for each piece and item.  Items: R / (rows of an item), and one
@@ -1469,9 +1665,10 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   p.meta = reinterpret_cast<float2*>(ws + L.meta);
   p.indices_stride = a.indices_stride;
   p.num_pages = a.num_pages;
-  p.page_size = a.page_size;
   p.max_pages = a.max_pages;
-  p.scale_block = a.scale_block;
+  p.cache_rows = a.num_pages * a.page_size;
+  p.page = fast_divisor(a.page_size);
+  p.block = fast_divisor(a.scale_block);
   p.H = H;
   p.R = static_cast<int>(R);
   p.T = T;
@@ -1486,7 +1683,8 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   CUtensorMap q_map, qr_map, k_map, kr_map;
   if (!encode_2d(&q_map, q8, u8, 1152, R, 1152, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&qr_map, q8, u8, 1152, R, 1152, 64, rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !encode_2d(&k_map, a.kv_cache, u8, 576, cache_rows, 576, 128, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_4d(&k_map, a.kv_cache, u8, {128, 8, 4, cache_rows / 8 > 0 ? cache_rows / 8 : 1}, {576, 128, 8 * 576},
+                 {128, 8, 2, box / 8}, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&kr_map, a.kv_cache, u8, 576, cache_rows, 576, 64, box, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const long long ctas = static_cast<long long>(a.pieces) * members;

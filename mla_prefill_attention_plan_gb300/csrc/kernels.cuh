@@ -256,6 +256,9 @@ cudaError_t launch_bounded_wait_selftest(int32_t* status, long long* elapsed_ns,
 bool encode_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, uint64_t inner,
                uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapSwizzle swizzle);
+// Four dimensions, strides (bytes) of all but the innermost.
+bool encode_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, const uint64_t (&dims)[4],
+               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle);
 int sm_count();
 
 }  // namespace mla
