@@ -394,7 +394,7 @@ template <bool WIDE>
 struct Shape {
   static constexpr int ROWS = WIDE ? 64 : 32;
   static constexpr int GROUPS = ROWS / 16;                // softmax warpgroups, 16 rows each
-  static constexpr int THREADS = 64 + 128 * GROUPS;       // producer, MMA and softmax warps
+  static constexpr int THREADS = 96 + 128 * GROUPS;       // producer, MMA, softmax and scale warps
   static constexpr int NQ = 2 * ROWS;                     // score columns of a tile
   static constexpr int SLOTS = WIDE ? 4 : 5;
   static constexpr int ROPES = WIDE ? 1 : 2;
@@ -406,7 +406,7 @@ struct Shape {
   static constexpr int AT_Q = AT_ROPE + ROPES * ROPE;
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
-  static constexpr int TOTAL = AT_BAR + 2048 + 1024;
+  static constexpr int TOTAL = AT_BAR + 3072;
   static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x 64 columns
   static constexpr uint32_t TM_COLS = 512;
   static_assert(TOTAL <= 227 * 1024 && TM_O + 256 <= TM_COLS, "shared memory, TMEM");
@@ -426,9 +426,10 @@ struct AttnSmem {
   int top[64];                // largest weight of a row (order-preserving integers)
   int lim[64];                // keys of the segment that the row sees
   int bad[4][2];              // [group][tile & 1]: a weight of the tile is out of range
+  float ksc[2][128];          // [tile & 1]: the keys' scales (1 past the segment)
   int run[32], last[16];      // cache rows of the runs that are loaded next, and of the tile before them
 };
-static_assert(sizeof(AttnSmem) <= 2048, "barrier block");
+static_assert(sizeof(AttnSmem) <= 3072, "barrier block");
 
 struct Q8Params {
   const PlanHead* head;
@@ -620,12 +621,16 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, NQ, false, false);
   constexpr uint32_t IDESC_PV = idesc_e4m3(128, 64, true, true);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;   // every byte is used: the base itself is a multiple of 1024 (checked below)
   AttnSmem* sh = reinterpret_cast<AttnSmem*>(smem + C::AT_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int member = blockIdx.x % p.members, piece = blockIdx.x / p.members;
   int32_t* status = p.status;
   pdl_enter();
+  if ((smem_u32(smem_raw) & 1023u) != 0) {           // a launch without that alignment would compute nonsense
+    set_status(status, MLA_DEV_TIMEOUT);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     // A block's load is counted in bytes (DENSE), or by the copying threads' arrivals.
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
     mbar_init(smem_u32(&sh->q_full), 1);
     mbar_init(smem_u32(&sh->q_free), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh->s_full[i]), 1);
+      mbar_init(smem_u32(&sh->s_full[i]), 2);         // the scores, and the keys' scales
       mbar_init(smem_u32(&sh->s_free[i]), 4 * GROUPS);
     }
     mbar_init(smem_u32(&sh->p_full), 4 * GROUPS);
@@ -919,7 +924,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           if (p.indices == nullptr) lim = min(lim, sg.cb + (sg.r0 + r) / p.H + 1 - sg.key0);
         }
         sh->rf[r] = rf;
-        sh->ry[r] = 0.f;
+        sh->ry[r] = tid < mine ? 0.f : -kInf;         // rows past the last: no weight
         sh->lim[r] = lim;
         sh->top[r] = float_order(-kInf);
       }
@@ -934,39 +939,21 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 #pragma unroll
       for (int c = 0; c < 8; ++c) l[c] = make_float2(0.f, 0.f);
       float smax = 0.f;
-      // The scale of this thread's key is read one tile ahead, its table entry two.
-      auto key_entry = [&](int j) -> int {
-        const int pos = sg.key0 + j * BK + key;
-        return j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
-      };
-      float next = 1.f;
-      int entry = key_entry(0);
-      for (int j = -1; j < sg.n; ++j) {
-        // (Turn -1 only reads the first tile's scale.)
-        float ksc = next;
-        {
-          const int pos = sg.key0 + (j + 1) * BK + key;
-          next = 1.f;
-          if (j + 1 < sg.n && pos < sg.key1) {
-            const int row = q8_row(p, pos, entry);
-            if (row >= 0) next = __ldg(p.kv_scales + fast_div(row, p.block));
-          }
-          entry = key_entry(j + 2);
-        }
-        if (j < 0) continue;
+#pragma unroll 1
+      for (int j = 0; j < sg.n; ++j) {
         const uint32_t g = g0 + j, sb = g & 1;
-        const bool valid = sg.key0 + j * BK + key < sg.key1;
-        const bool broken = !(fabsf(ksc) < kInf);     // a scale that is no number: the key's scores are NaN
-        if (broken) ksc = 1.f;
-        if (valid) smax = fmaxf(smax, fabsf(ksc));
-        const float lsc = __log2f(fabsf(ksc));
-        const float xv = broken ? __int_as_float(0x7fc00000) : ksc;
         const bool masked = (j + 1) * BK > all;       // some row does not see every key of the tile
         if (!wait_warp(smem_u32(&sh->s_full[sb]), (g >> 1) & 1, status, abort_flag)) {
           fail = true;
           break;
         }
         tc_fence_after();
+        float ksc = sh->ksc[sb][key];
+        const bool broken = !(fabsf(ksc) < kInf);     // a scale that is no number: the key's scores are NaN
+        if (broken) ksc = 1.f;
+        smax = fmaxf(smax, j * BK + key < span ? fabsf(ksc) : 0.f);
+        const float lsc = __log2f(fabsf(ksc));
+        const float xv = broken ? __int_as_float(0x7fc00000) : ksc;
         // The first tile sets the rows' references; in a later one the weights
         // are computed against them, and once more if one has to move.
         bool move = j == 0;
@@ -996,28 +983,19 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
               t[c + 1] = __ffma2_rn(__fmul2_rn(v, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
             }
           }
-          if (masked) {
+          if (__builtin_expect(masked, 0)) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               t[c].x = j * BK + key < sh->lim[c0 + 2 * c] ? t[c].x : -kInf;
               t[c].y = j * BK + key < sh->lim[c0 + 2 * c + 1] ? t[c].y : -kInf;
             }
           }
-          if (!move) {
+          if (__builtin_expect(!move, 1)) {
             // Whether any key of the group has a weight out of range: told to
-            // the others here, looked at when the weights are ready.  (Rows past
-            // the last hold garbage: with less than 16 they are looked at one by one.)
+            // the others here, looked at when the weights are ready.
             float mx = -kInf;
-            if (mine >= 16) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) mx = fmax3(mx, t[c].x, t[c].y);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                if (2 * c < mine) mx = fmaxf(mx, t[c].x);
-                if (2 * c + 1 < mine) mx = fmaxf(mx, t[c].y);
-              }
-            }
+            for (int c = 0; c < 8; ++c) mx = fmax3(mx, t[c].x, t[c].y);
             if (mx + lsc > kGrow) sh->bad[wg][sb] = 1;
             group_arrive(gb);
           } else {
@@ -1134,7 +1112,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           mbar_arrive(smem_u32(&sh->p_full));
           mbar_arrive(smem_u32(&sh->s_free[sb]));
         }
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           // A key that some row does not see: its weight is 0 there, but 0 times
           // a NaN code is NaN.  Rows past the segment become zeros (they may
           // hold anything); in the others every NaN code does (a row that sees
@@ -1154,7 +1132,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
               for (int i = 0; i < 16; ++i) {
                 uint4* at = reinterpret_cast<uint4*>(kr + (i >> 3) * 1024) + (i & 7);
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (valid) {
+                if (j * BK + key < span) {
                   v = *at;
                   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -1244,11 +1222,44 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
       if (lane == 0) mbar_arrive(smem_u32(&sh->o_free));
       ++seg;
     }
+  } else if (warp == 2 + 4 * GROUPS) {
+    // ------------------------------------------------------------ the keys' scales, a tile ahead
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      const int n = sg.key1 - sg.key0;
+      int entry[4];
+      auto entries = [&](int k0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) entry[x] = k0 + 32 * x + lane < n ? q8_entry(p, sg.b, sg.key0 + k0 + 32 * x + lane) : 0;
+      };
+      entries(0);
+#pragma unroll 1
+      for (int k0 = 0; k0 < n && ok; k0 += BK, ++g) {
+        float v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int k = k0 + 32 * x + lane;
+          v[x] = 1.f;
+          if (k < n) {
+            const int row = q8_row(p, sg.key0 + k, entry[x]);
+            if (row >= 0) v[x] = __ldg(p.kv_scales + fast_div(row, p.block));
+          }
+        }
+        entries(k0 + BK);
+        const uint32_t sb = g & 1;
+        if (g >= 2 && !(ok = wait_warp(smem_u32(&sh->s_free[sb]), ((g >> 1) & 1) ^ 1, status, abort_flag))) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sh->ksc[sb][32 * x + lane] = v[x];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->s_full[sb]));
+      }
+    }
   } else {
     // ------------------------------------------------------------ listed rows: cp.async
     if constexpr (!DENSE) {
       constexpr int RW = BK / kSparseProducers;       // this warp's keys [RW pw, RW pw + RW) of the tile
-      const int pw = warp - 2 - 4 * GROUPS;
+      const int pw = warp - 3 - 4 * GROUPS;
       uint32_t issued = 0, ropes = 0;
       bool ok = true;
       while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
