@@ -674,7 +674,7 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
   if (d_indices == nullptr && (!page_table || max_pages_per_seq < 1)) return MLA_ERR_ARG;
   if (d_indices != nullptr && indices_stride < 1) return MLA_ERR_ARG;
   const long long rows = static_cast<long long>(total_q_tokens) * num_heads;
-  // Launch limits: 65535 heads (or a quarter of them for the query clusters).
+  // (A quarter of the launch limit of 65535 rows of CTAs: two a head are launched.)
   if (rows >= (1ll << 31) / 4 || num_heads > 65535 / 4 ||
       static_cast<long long>(max_new_tokens) * num_heads >= (1ll << 31) / 4 ||
       static_cast<long long>(num_pages) * page_size >= (1ll << 31))

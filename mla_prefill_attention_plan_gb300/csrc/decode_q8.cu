@@ -167,25 +167,36 @@ __device__ void q8_plan(const PlanArgs& a, int tid, int (*scr)[4]) {
 }
 
 // ============================================================ 1. queries
-// One cluster of four CTAs per (128 tokens, head): CTA r computes latent
-// columns [128 r, 128 r + 128) of u for the head's 128 rows; CTA 3 also takes
-// the rope part.  The largest value of a row (over all four CTAs, exchanged
-// through distributed shared memory) sets its scale.  Reads w_uk once (16 MB
-// at 128 heads): memory-bound.
-constexpr int kQThreads = 192;
-constexpr int Q_TILE = 128 * 128;                 // 128 rows of 64 bf16
-constexpr int Q_SMEM_BAR = 4 * Q_TILE;            // two 64-column blocks of A and of B
-constexpr int Q_SMEM_TOTAL = Q_SMEM_BAR + 1024 + 1024;
+// One cluster of two CTAs per (128 tokens, head): CTA r computes latent columns
+// [256 r, 256 r + 256) of u for the head's 128 rows; CTA 1 also takes the rope
+// part.  The largest value of a row (over both CTAs, exchanged through
+// distributed shared memory) sets its scale.  Reads w_uk once (16 MB at 128
+// heads).  Two CTAs a head, two on an SM: 128 heads run in one wave; with four
+// CTAs a head they took two (31 us against 20 for 96 tokens).
+constexpr int kQThreads = 320;                    // TMA, MMA, 8 epilogue warps
+constexpr int Q_A = 128 * 128;                    // 128 rows of 64 bf16
+constexpr int Q_B = 256 * 128;
+constexpr int Q_SMEM_BAR = 2 * (Q_A + Q_B);       // two 64-column blocks of A and of B
+constexpr int Q_SMEM_TOTAL = Q_SMEM_BAR + 2048 + 1024;
 
 struct QuerySmem {
   uint64_t full[2], done;
   uint32_t tmem;
   int abort;
-  float amax[128];
+  float amax[2][128];        // [half of the CTA's columns][row]
   int scr[4][4];
 };
 
-__global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
+// x in two e4m3 terms, four values.
+__device__ __forceinline__ void two_terms(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
+  const uint16_t h0 = pack_e4m3(v[0], v[1]), h1 = pack_e4m3(v[2], v[3]);
+  const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
+  hi = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
+  lo = static_cast<uint32_t>(pack_e4m3(v[0] - b0.x, v[1] - b0.y)) |
+       (static_cast<uint32_t>(pack_e4m3(v[2] - b1.x, v[3] - b1.y)) << 16);
+}
+
+__global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
     q8_query_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                     const uint16_t* __restrict__ q, uint8_t* __restrict__ q8, float* __restrict__ q_scale, int T,
                     int H, int32_t* status, const PlanArgs plan) {
@@ -194,7 +205,7 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
   QuerySmem* sh = reinterpret_cast<QuerySmem*>(smem + Q_SMEM_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int h = blockIdx.y >> 2;
+  const int h = blockIdx.y >> 1;
   const int m0 = blockIdx.x * 128;
   pdl_enter();
   if (threadIdx.x == 0) {
@@ -205,7 +216,7 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sh->tmem), 128);
+    tmem_alloc(smem_u32(&sh->tmem), 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -214,19 +225,22 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
   const bool work = !cluster_any(&sh->abort);
   const uint32_t tmem = sh->tmem;
   volatile int* abort_flag = &sh->abort;
-  const int row = (warp & 3) * 32 + lane;          // epilogue warps 2..5
+  const int half = (warp - 2) >> 2;                // epilogue warps 2..9: columns [128 half, 128 half + 128)
+  const int row = (warp & 3) * 32 + lane;
   const int t = m0 + row;
   const long long grow = static_cast<long long>(t) * H + h;
+  const uint32_t tm = tmem + (uint32_t((warp & 3) * 32) << 16) + half * 128;
   float am = 0.f;
   bool ok = work;
   if (work && warp == 0) {
     if (elect_one()) {
+#pragma unroll 1
       for (int kb = 0; kb < 2; ++kb) {
         const uint32_t full = smem_u32(&sh->full[kb]);
-        const uint32_t a = smem_u32(smem + kb * 2 * Q_TILE);
-        mbar_expect_tx(full, 2 * Q_TILE);
+        const uint32_t a = smem_u32(smem + kb * (Q_A + Q_B));
+        mbar_expect_tx(full, Q_A + Q_B);
         tma_load_2d(a, &a_map, full, h * 192 + kb * 64, m0);
-        tma_load_2d(a + Q_TILE, &b_map, full, kb * 64, h * 512 + rank * 128);
+        tma_load_2d(a + Q_A, &b_map, full, kb * 64, h * 512 + rank * 256);
       }
       volatile int never = 0;
       mbar_wait(smem_u32(&sh->full[0]), 0, status, &never);
@@ -239,11 +253,11 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
       for (int kb = 0; kb < 2 && good; ++kb) {
         if (!(good = mbar_wait(smem_u32(&sh->full[kb]), 0, status, abort_flag))) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + kb * 2 * Q_TILE);
+        const uint32_t a = smem_u32(smem + kb * (Q_A + Q_B));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f16_ss(tmem, sdesc(a + k * 32, 16, 1024), sdesc(a + Q_TILE + k * 32, 16, 1024),
-                     idesc_bf16(128, 128, false, false), (kb | k) != 0);
+          mma_f16_ss(tmem, sdesc(a + k * 32, 16, 1024), sdesc(a + Q_A + k * 32, 16, 1024),
+                     idesc_bf16(128, 256, false, false), (kb | k) != 0);
       }
       tc_commit(smem_u32(&sh->done));
       volatile int never = 0;
@@ -251,19 +265,19 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
     }
     __syncwarp();
   } else if (work) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) q8_plan(plan, threadIdx.x - 64, sh->scr);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && half == 0) q8_plan(plan, threadIdx.x - 64, sh->scr);
     ok = mbar_wait_warp(smem_u32(&sh->done), 0, status, abort_flag);
     if (ok) {
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
-        tmem_ld32(tmem + (uint32_t((warp & 3) * 32) << 16) + c * 32, x);
+        tmem_ld32(tm + c * 32, x);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) am = fmaxf(am, fabsf(__uint_as_float(x[i])));
       }
-      if (rank == 3 && t < T) {
+      if (rank == 1 && half == 1 && t < T) {
         const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -273,29 +287,33 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
           for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf16_lo(u[k])), fabsf(bf16_hi(u[k]))));
         }
       }
-      sh->amax[row] = am;
+      sh->amax[half][row] = am;
     }
   }
   tc_fence_before();
   cluster_sync();
   if (warp >= 2 && ok) {
-    for (uint32_t r = 0; r < 4; ++r) {
-      if (static_cast<int>(r) == rank) continue;
+    am = fmaxf(sh->amax[0][row], sh->amax[1][row]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
       float o;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(smem_u32(&sh->amax[row]), r)) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(o)
+                   : "r"(cluster_addr(smem_u32(&sh->amax[x][row]), rank ^ 1))
+                   : "memory");
       am = fmaxf(am, o);
     }
     const float s = pow2_scale(am);
     const float inv = 1.0f / s;
     // An infinite query has no scale: its scores become NaN.
-    if (rank == 0 && t < T) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);
-    uint8_t* dst = q8 + grow * 1152 + rank * 128;
+    if (rank == 0 && half == 0 && t < T) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);
+    uint8_t* dst = q8 + grow * 1152 + rank * 256 + half * 128;
     // The results once more from TMEM, 32 columns at a time (few registers, so
-    // that three of these CTAs share an SM).
+    // that two of these CTAs share an SM).
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t x[32];
-      tmem_ld32(tmem + (uint32_t((warp & 3) * 32) << 16) + c * 32, x);
+      tmem_ld32(tm + c * 32, x);
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -304,12 +322,8 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
         for (int k = 0; k < 4; ++k) {
           float v[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(x[16 * i + 4 * k + y]);
-          const uint16_t h0 = pack_e4m3(v[0] * inv, v[1] * inv), h1 = pack_e4m3(v[2] * inv, v[3] * inv);
-          const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
-          hi[k] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
-          lo[k] = static_cast<uint32_t>(pack_e4m3(v[0] * inv - b0.x, v[1] * inv - b0.y)) |
-                  (static_cast<uint32_t>(pack_e4m3(v[2] * inv - b1.x, v[3] * inv - b1.y)) << 16);
+          for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(x[16 * i + 4 * k + y]) * inv;
+          two_terms(v, hi[k], lo[k]);
         }
         if (t < T) {
           reinterpret_cast<uint4*>(dst)[2 * c + i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -317,30 +331,26 @@ __global__ void __cluster_dims__(1, 4, 1) __launch_bounds__(kQThreads, 3)
         }
       }
     }
-    if (rank == 3 && t < T) {
+    if (rank == 1 && half == 1 && t < T) {
       const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
-      uint32_t* dr = reinterpret_cast<uint32_t*>(q8 + grow * 1152 + 512);
-#pragma unroll
+      uint2* dr = reinterpret_cast<uint2*>(q8 + grow * 1152 + 512);
+#pragma unroll 1
       for (int i = 0; i < 8; ++i) {
         const uint4 v = __ldg(rp + i);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const float a0 = bf16_lo(u[k]) * inv, a1 = bf16_hi(u[k]) * inv;
-          const float a2 = bf16_lo(u[k + 1]) * inv, a3 = bf16_hi(u[k + 1]) * inv;
-          const uint16_t h0 = pack_e4m3(a0, a1), h1 = pack_e4m3(a2, a3);
-          const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
-          dr[2 * i + k / 2] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
-          dr[144 + 2 * i + k / 2] = static_cast<uint32_t>(pack_e4m3(a0 - b0.x, a1 - b0.y)) |
-                                    (static_cast<uint32_t>(pack_e4m3(a2 - b1.x, a3 - b1.y)) << 16);
-        }
+        const float a[4] = {bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv, bf16_hi(v.y) * inv};
+        const float b[4] = {bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv, bf16_hi(v.w) * inv};
+        uint2 hi, lo;
+        two_terms(a, hi.x, lo.x);
+        two_terms(b, hi.y, lo.y);
+        dr[i] = hi;
+        dr[72 + i] = lo;
       }
     }
   }
   cluster_sync();   // no CTA leaves while another may read its row maxima
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -1339,20 +1349,24 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 }
 
 // ============================================================ 3. merge and w_uv
-// One CTA per (head, NT tokens): the segments' latent results are merged by
-// LSE in fp32 (with the attention sink in the denominator), split into two
+// One CTA per (head, up to NT tokens): the segments' latent results are merged
+// by LSE in fp32 (with the attention sink in the denominator), split into two
 // bf16 terms (their sum within 2^-16) and multiplied by w_uv[h]: D^T [128
-// values, NT tokens] = w_uv[h] [128, 512] . o^T, so that few tokens make a
-// small N.  Reads w_uv[h] once per token tile.
-constexpr int kOutThreads = 256;
+// values, NT tokens] = w_uv[h] [128, 512] . o^T, so that few tokens make a small
+// N.  Reads w_uv[h] once per CTA; its load starts before the attention has
+// ended.  16 warps: with few tokens several of them share one token's segments
+// (a single long sequence has one for every SM) and join through shared memory.
+constexpr int kOutWarps = 16;
 
 template <int NT>
 struct OutShape {
   static constexpr int W = 8 * 16384;                // w_uv[h], eight 64-column blocks
   static constexpr int TERM = 8 * NT * 128;
   static constexpr int AT_O = W;
-  static constexpr int AT_BAR = AT_O + 2 * TERM;
+  static constexpr int AT_JOIN = AT_O + 2 * TERM;    // [warp][512] partial sums, where warps share a token
+  static constexpr int AT_BAR = AT_JOIN + (NT == 16 ? kOutWarps * 2048 : 0);
   static constexpr int TOTAL = AT_BAR + 1024 + 1024;
+  static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 struct OutSmem {
   uint64_t full, done;
@@ -1361,38 +1375,57 @@ struct OutSmem {
   int used[32];      // segments that hold keys of the token; -1: its rows are not written
   int first[32];     // row of the first one's results (in slots), the others `step` apart
   float sink[32];    // log2 units
+  float2 join[kOutWarps];   // a warp's maximum and sum
 };
+static_assert(sizeof(OutSmem) <= 1024, "barrier block");
+
+// Running merge of segments: maximum, sum of weights, weighted sums of 16 latents.
+struct Merge {
+  float mx, tot, o[16];
+};
+__device__ __forceinline__ void merge_scale(Merge& m, float nm) {
+  const float keep = m.mx == -kInf ? 0.f : ex2(m.mx - nm);
+  m.tot *= keep;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m.o[e] *= keep;
+  m.mx = nm;
+}
 
 template <int NT>
-__global__ void __launch_bounds__(kOutThreads, 1)
+__global__ void __launch_bounds__(32 * kOutWarps, 1)
     q8_out_kernel(const __grid_constant__ CUtensorMap w_map, const Q8Params p, const float* __restrict__ sink,
-                  __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T, int rows) {
+                  __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T, int rows, int tokens) {
   using C = OutShape<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   OutSmem* sh = reinterpret_cast<OutSmem*>(smem + C::AT_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * NT, h = blockIdx.y;
-  pdl_enter();
-  if (timed_out_before(p.status)) return;
+  const int t0 = blockIdx.x * tokens, h = blockIdx.y;
+  const int n = min(tokens, T - t0);                 // tokens of this CTA, NT at most
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh->full), 1);
     mbar_init(smem_u32(&sh->done), 1);
     sh->abort = 0;
     fence_mbar_init();
+    // The weights do not come from the kernel before, and whatever wrote them
+    // had completed when that kernel let this one start (it waits for its own
+    // predecessor first).
     const uint32_t full = smem_u32(&sh->full);
     mbar_expect_tx(full, C::W);
+#pragma unroll 1
     for (int kb = 0; kb < 8; ++kb) tma_load_2d(smem_u32(smem + kb * 16384), &w_map, full, kb * 64, h * 128);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh->tmem), 32);
     tmem_relinquish();
   }
+  pdl_enter();
+  const bool dead = timed_out_before(p.status);
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {
     const int i = threadIdx.x - 64, t = t0 + i;
     int used = -1, first = 0;
     float sk = -kInf;
-    if (t < T) {
+    if (i < n && !dead) {
       const int entries = __ldg(&p.head->entries), units = __ldg(&p.head->units);
       int lo = 0, hi = entries;   // last entry with qa <= t
       while (hi - lo > 1) {
@@ -1421,55 +1454,64 @@ __global__ void __launch_bounds__(kOutThreads, 1)
     sh->sink[i] = sk;
   }
   tc_fence_before();
-  __syncthreads();
+  const bool stop = __syncthreads_or(dead ? 1 : 0) != 0;   // an earlier kernel timed out: no work
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
-
-  for (int i = warp; i < NT; i += kOutThreads / 32) {
+  volatile int never = 0;
+  const long long step = static_cast<long long>(p.members) * rows;
+  // Warps of a token: a power of two, so that they divide the 16.
+  int share = 1;
+  while (NT == 16 && 2 * share * n <= kOutWarps) share *= 2;
+  const int part = warp % share;
+  Merge m;
+  // One token's segments part, part + share, ...
+  auto gather = [&](int i) {
     const int used = sh->used[i];
-    const long long first = sh->first[i], step = static_cast<long long>(p.members) * rows;
-    const long long grow = static_cast<long long>(t0 + i) * p.H + h;
-    float o[16];
+    const long long first = sh->first[i];
+    m.mx = -kInf;
+    m.tot = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = 0.f;
-    float mx = -kInf, tot = 0.f;
-    constexpr int KU = 4;                           // segments loaded together
-    for (int k0 = 0; k0 < used; k0 += KU) {
+    for (int e = 0; e < 16; ++e) m.o[e] = 0.f;
+    constexpr int KU = 4;                              // segments loaded together
+#pragma unroll 1
+    for (int k0 = part; k0 < used; k0 += KU * share) {
       uint4 a[KU], c[KU];
       float2 mt[KU];
 #pragma unroll
       for (int x = 0; x < KU; ++x) {
-        const long long at = first + (k0 + x) * step;
-        const bool in = k0 + x < used;
+        const int k = k0 + x * share;
+        const long long at = first + k * step;
+        const bool in = k < used;
         mt[x] = in ? __ldg(p.meta + at) : make_float2(-kInf, 0.f);
         const uint4* src = reinterpret_cast<const uint4*>(p.o_part + at * 512);
         a[x] = in ? __ldg(src + lane) : make_uint4(0u, 0u, 0u, 0u);
         c[x] = in ? __ldg(src + 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
       }
-      float nm = mx;
+      float nm = m.mx;
 #pragma unroll
       for (int x = 0; x < KU; ++x) nm = fmaxf(nm, mt[x].x);
-      const float keep = mx == -kInf ? 0.f : ex2(mx - nm);
-      tot *= keep;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] *= keep;
+      merge_scale(m, nm);
 #pragma unroll
       for (int x = 0; x < KU; ++x) {
         const float w = mt[x].x == -kInf ? 0.f : ex2(mt[x].x - nm);
-        tot += w;
+        m.tot += w;
         const float ws = w * mt[x].y;
         const uint32_t u[8] = {a[x].x, a[x].y, a[x].z, a[x].w, c[x].x, c[x].y, c[x].z, c[x].w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float2 v = f16x2_to_float2(u[e]);
-          o[2 * e] = fmaf(ws, v.x, o[2 * e]);
-          o[2 * e + 1] = fmaf(ws, v.y, o[2 * e + 1]);
+          m.o[2 * e] = fmaf(ws, v.x, m.o[2 * e]);
+          m.o[2 * e + 1] = fmaf(ws, v.y, m.o[2 * e + 1]);
         }
       }
-      mx = nm;
     }
-    float l2 = tot == 0.f ? -kInf : mx + __log2f(tot);
-    float w = tot == 0.f ? 0.f : 1.0f / tot;
+  };
+  // The merged token i into the operand: latents 8 lane .. +7 and 256 + 8 lane ..
+  // +7, that is block of 64 columns lane / 8 (+ 4), 16-byte chunk lane & 7.
+  auto finish = [&](int i) {
+    const int used = sh->used[i];
+    float l2 = m.tot == 0.f ? -kInf : m.mx + __log2f(m.tot);
+    float w = m.tot == 0.f ? 0.f : 1.0f / m.tot;
     const float sk = sh->sink[i];
     if (sink != nullptr && used >= 0) {
       // The sink is one more logit without a value: LSE' = log(e^LSE + e^sink).
@@ -1481,14 +1523,13 @@ __global__ void __launch_bounds__(kOutThreads, 1)
         l2 = l3;
       }
     }
-    if (lse != nullptr && used >= 0 && lane == 0) lse[grow] = l2 * kLn2q;
-    // Latents 8 lane .. +7 and 256 + 8 lane .. +7: block 64 columns, 16-byte chunk lane & 7.
+    if (lse != nullptr && used >= 0 && lane == 0) lse[static_cast<long long>(t0 + i) * p.H + h] = l2 * kLn2q;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = o[8 * half + 2 * e] * w, y = o[8 * half + 2 * e + 1] * w;
+        const float x = m.o[8 * half + 2 * e] * w, y = m.o[8 * half + 2 * e + 1] * w;
         hi[e] = pack_bf16(x, y);
         lo[e] = pack_bf16(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
       }
@@ -1497,14 +1538,49 @@ __global__ void __launch_bounds__(kOutThreads, 1)
       *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(dst + C::TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
+  };
+  if (!stop) {
+    // (Operand rows past the last token hold anything: their results are not stored.)
+    if (share == 1) {
+#pragma unroll 1
+      for (int i = warp; i < n; i += kOutWarps) {
+        gather(i);
+        finish(i);
+      }
+    } else {
+      const int i = warp / share;
+      if (i < n) gather(i);
+      float* join = reinterpret_cast<float*>(smem + C::AT_JOIN) + warp * 512;
+      if (i < n && part > 0) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) join[e * 32 + lane] = m.o[e];
+        if (lane == 0) sh->join[warp] = make_float2(m.mx, m.tot);
+      }
+      __syncthreads();
+      if (i < n && part == 0) {
+#pragma unroll 1
+        for (int x = 1; x < share; ++x) {              // in order: the result does not depend on timing
+          const float2 mt = sh->join[warp + x];
+          const float nm = fmaxf(m.mx, mt.x);
+          if (nm == -kInf) continue;
+          merge_scale(m, nm);
+          const float w = mt.x == -kInf ? 0.f : ex2(mt.x - nm);
+          m.tot = fmaf(w, mt.y, m.tot);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) m.o[e] = fmaf(w, join[x * 512 + e * 32 + lane], m.o[e]);
+        }
+        finish(i);
+      }
+    }
   }
   fence_async_smem();
   __syncthreads();
-  volatile int never = 0;
   if (warp == 0) {
     if (elect_one()) {
-      if (mbar_wait(smem_u32(&sh->full), 0, p.status, &never)) {
+      // (The weights land before the CTA leaves, whether there is work or not.)
+      if (mbar_wait(smem_u32(&sh->full), 0, p.status, &never) && !stop) {
         tc_fence_after();
+#pragma unroll 1
         for (int kb = 0; kb < 8; ++kb) {
           const uint32_t a = smem_u32(smem + kb * 16384);
           const uint32_t o = smem_u32(smem + C::AT_O + kb * NT * 128);
@@ -1531,7 +1607,7 @@ __global__ void __launch_bounds__(kOutThreads, 1)
     __nv_bfloat16* dst = out + (static_cast<long long>(t0) * p.H + h) * 128 + warp * 32 + lane;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      if (sh->used[i] >= 0) dst[static_cast<long long>(i) * p.H * 128] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      if (i < n && sh->used[i] >= 0) dst[static_cast<long long>(i) * p.H * 128] = __float2bfloat16_rn(__uint_as_float(r[i]));
   }
   tc_fence_before();
   __syncthreads();
@@ -1574,12 +1650,13 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
 }
 
 template <int NT>
-cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const DecodeQ8Args& a, int rows,
+cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const DecodeQ8Args& a, int rows, int tokens,
                        cudaStream_t stream) {
   cudaError_t e = opt_in_smem(q8_out_kernel<NT>, OutShape<NT>::TOTAL);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q8_out_kernel<NT>, dim3((a.T + NT - 1) / NT, a.H), dim3(kOutThreads), OutShape<NT>::TOTAL, stream,
-                    w_map, p, a.sink, static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, rows);
+  return launch_pdl(q8_out_kernel<NT>, dim3((a.T + tokens - 1) / tokens, a.H), dim3(32 * kOutWarps),
+                    OutShape<NT>::TOTAL, stream, w_map, p, a.sink, static_cast<__nv_bfloat16*>(a.out), a.lse, a.T,
+                    rows, tokens);
 }
 
 // Query rows of a tile: 64 where a sequence can fill more than 32.
@@ -1641,7 +1718,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   CUtensorMap qa_map, wuk_map;
   if (!encode_2d(&qa_map, a.q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&wuk_map, a.w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 128,
+      !encode_2d(&wuk_map, a.w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 256,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   PlanArgs plan;
@@ -1660,7 +1737,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   plan.status = a.status;
   cudaError_t e = opt_in_smem(q8_query_kernel, Q_SMEM_TOTAL);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(q8_query_kernel, dim3((T + 127) / 128, 4 * H), dim3(kQThreads), Q_SMEM_TOTAL, stream, qa_map, wuk_map,
+  e = launch_pdl(q8_query_kernel, dim3((T + 127) / 128, 2 * H), dim3(kQThreads), Q_SMEM_TOTAL, stream, qa_map, wuk_map,
                  static_cast<const uint16_t*>(a.q), q8, q_scale, T, H, a.status, plan);
   if (e != cudaSuccess) return e;
 
@@ -1710,7 +1787,12 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   CUtensorMap wuv_map;
   if (!encode_2d(&wuv_map, a.w_uv, bf, 512, static_cast<uint64_t>(H) * 128, 1024, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  return T > 16 ? launch_out<32>(wuv_map, p, a, rows, stream) : launch_out<16>(wuv_map, p, a, rows, stream);
+  // Tokens a CTA: as few as one wave of CTAs allows, 16 or 32 where it takes more.
+  int tokens = 1;
+  while (tokens < 16 && static_cast<long long>(H) * ((T + tokens - 1) / tokens) > sm_count()) tokens *= 2;
+  if (static_cast<long long>(H) * ((T + 15) / 16) <= sm_count())
+    return launch_out<16>(wuv_map, p, a, rows, tokens, stream);
+  return launch_out<32>(wuv_map, p, a, rows, 32, stream);
 }
 
 }  // namespace mla
