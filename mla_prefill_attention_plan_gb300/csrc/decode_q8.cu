@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();            // (a wait that runs out raises the flag of the cluster's other CTA too)
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
   volatile int* abort_flag = &sh->abort;
@@ -1342,6 +1342,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();            // neither CTA leaves while the other may still raise its flag
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, TM_COLS);
@@ -1645,8 +1646,24 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
   cudaError_t e = opt_in_smem(q8_attn_kernel<DENSE, WIDE>, Shape<WIDE>::TOTAL);
   if (e != cudaSuccess) return e;
   const int threads = Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSparseProducers);
-  return launch_pdl(q8_attn_kernel<DENSE, WIDE>, dim3(static_cast<unsigned>(ctas)), dim3(threads),
-                    Shape<WIDE>::TOTAL, stream, q_map, qr_map, k_map, kr_map, p);
+  // Members of a piece read the same keys at the same time: as a cluster they
+  // sit on neighbouring SMs, on one die, and share its half of L2 (left to the
+  // order in which SMs became free, 64 x 128 heads took 376 us, not 300).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = Shape<WIDE>::TOTAL;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.members % 2 == 0 ? 2 : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, q8_attn_kernel<DENSE, WIDE>, q_map, qr_map, k_map, kr_map, p);
 }
 
 template <int NT>
