@@ -32,32 +32,34 @@ __device__ __forceinline__ int sequence_of(const uint32_t* __restrict__ iro, int
 }
 
 // ============================================================ scores
-// Keys are the M side of the MMA (128 keys a tile, the heads of one token the
-// N side, K = 128), so a thread of the epilogue holds one key's products with
-// all heads in its own TMEM lane and the weighted sum needs no other thread.
-// One CTA per (sequence, group of its new tokens, range of positions): the
-// group's queries stay in shared memory, key tiles stream through a ring, and
-// two epilogue warpgroups take the (tile, token) units in turn, each with its
-// own TMEM buffer.  With one new token a sequence the call is bound by reading
-// the keys (256 or 128 bytes each, 64 heads: 64 flops a byte); with many it is
-// bound by the epilogue's two instructions a head and pair.
+// Keys are the M side of the MMA (128 keys a tile) and the heads of a batch of
+// tokens the N side (K = 128), so a thread of the epilogue holds one key's
+// products with all of them in its own TMEM lane and the weighted sums need no
+// other thread.  One CTA per (sequence, group of its new tokens, range of
+// positions): the group's queries stay in shared memory, key tiles stream
+// through a ring, and two epilogue warpgroups take the (tile, batch) units in
+// turn, each with its own TMEM buffer of up to 256 columns.
+//
+// With one new token a sequence the call is bound by reading the keys (256 or
+// 128 bytes each; 64 heads: 64 flops a byte); the CTA then needs few buffers
+// and two of them share an SM, one's start under the other's loads.  With many
+// tokens it is bound by the epilogue, three instructions for two products: a
+// batch fills the TMEM buffer, so that an MMA's latency (some 600 clk to its
+// barrier) is paid once for 256 columns.
 constexpr int IT = 128;                             // keys of a tile
-constexpr int I_QMAX = 64 * 1024;                   // query bytes kept at most
-constexpr int I_RING = 128 * 1024;
 constexpr int kScoreThreads = 320;                  // producer, MMA, 2 x 4 epilogue warps
-constexpr int I_MAXG = 16;
-constexpr int I_AT_RING = I_QMAX;
-constexpr int I_AT_W = I_AT_RING + I_RING;          // weights [I_MAXG][128], at most 8 KB
-constexpr int I_AT_BAR = I_AT_W + I_MAXG * 128 * 4;
-constexpr int I_TOTAL = I_AT_BAR + 1024 + 1024;
-static_assert(I_TOTAL <= 227 * 1024, "shared memory");
+constexpr int I_QMAX = 64 * 1024;                   // query bytes kept at most
+constexpr int I_MAXG = 16;                          // tokens of a group at most
+constexpr int I_MAXSTAGES = 8;
 
 struct ScoreSmem {
-  uint64_t k_full[8], k_empty[8], q_full, d_full[2], d_free[2], drain;
+  uint64_t k_full[I_MAXSTAGES], k_empty[I_MAXSTAGES], q_full, d_full[2], d_free[2], drain;
   uint32_t tmem;
   int abort;
-  float part[2][4];
+  float part[2][I_MAXG][4];    // [warpgroup][token][warp]: maxima, for blocks of more than 32 keys
 };
+constexpr int I_BAR = 1024;
+static_assert(sizeof(ScoreSmem) <= I_BAR, "barrier block");
 
 struct ScoreParams {
   float* scores;
@@ -67,7 +69,10 @@ struct ScoreParams {
   const uint32_t* iro;
   const uint32_t* cache_len;
   const int32_t* page_table;
-  int num_pages, page_size, max_pages, block, B, Hi, NP, T, G, groups, splits, span, max_seq, stride, box;
+  int num_pages, page_size, max_pages, block, B, Hi, NP, T, groups, splits, span, max_seq, stride, box;
+  int G, batch;              // tokens of a group and of an MMA
+  int stages, cols;          // ring stages, TMEM columns allocated
+  int at_w, at_ring, at_bar; // shared memory: queries, weights [G][NP], ring, barriers
   int32_t* status;
 };
 
@@ -80,17 +85,16 @@ __device__ __forceinline__ int score_row(const ScoreParams& p, int b, int pos) {
 }
 
 template <bool E8, bool DENSE>
-__global__ void __launch_bounds__(kScoreThreads, 1)
+__global__ void __launch_bounds__(kScoreThreads, 2)
     index_scores_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const ScoreParams p) {
   constexpr int KB = E8 ? 1 : 2;                    // 128-byte blocks of a row
   constexpr int ELT = E8 ? 1 : 2;
   constexpr int STAGE = KB * IT * 128;
-  constexpr int STAGES = E8 ? 8 : 4;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  ScoreSmem* sh = reinterpret_cast<ScoreSmem*>(smem + I_AT_BAR);
-  float* sw = reinterpret_cast<float*>(smem + I_AT_W);
+  ScoreSmem* sh = reinterpret_cast<ScoreSmem*>(smem + p.at_bar);
+  float* sw = reinterpret_cast<float*>(smem + p.at_w);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_enter();
 
@@ -117,241 +121,294 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int tiles = static_cast<int>(min(static_cast<long long>(p.span), tiles_all - tile0));
   const long long base0 = tile0 * IT;
   const int n = base0 > pos_last ? 0 : static_cast<int>(min(static_cast<long long>(tiles), (pos_last - base0) / IT + 1));
+  const int batches = (ng + p.batch - 1) / p.batch;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&sh->k_full[s]), 1);
-      mbar_init(smem_u32(&sh->k_empty[s]), 1);
+  if (n > 0) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(smem_u32(&sh->k_full[s]), 1);
+        mbar_init(smem_u32(&sh->k_empty[s]), 1);
+      }
+      mbar_init(smem_u32(&sh->q_full), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh->d_full[i]), 1);
+        mbar_init(smem_u32(&sh->d_free[i]), 4);
+      }
+      mbar_init(smem_u32(&sh->drain), 1);
+      sh->abort = timed_out_before(p.status) ? 1 : 0;
+      fence_mbar_init();
     }
-    mbar_init(smem_u32(&sh->q_full), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh->d_full[i]), 1);
-      mbar_init(smem_u32(&sh->d_free[i]), 4);
+    if (warp == 1) {
+      tmem_alloc(smem_u32(&sh->tmem), p.cols);
+      tmem_relinquish();
     }
-    mbar_init(smem_u32(&sh->drain), 1);
-    sh->abort = timed_out_before(p.status) ? 1 : 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&sh->tmem), 256);
-    tmem_relinquish();
-  }
-  // The group's weights, heads past the last one zero.
-  for (int i = threadIdx.x; i < ng * p.NP; i += kScoreThreads) {
-    const int gi = i / p.NP, h = i - gi * p.NP;
-    sw[gi * 128 + h] = h < p.Hi ? __ldg(p.w + static_cast<long long>(t0 + gi) * p.Hi + h) : 0.f;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh->tmem;
-  volatile int* abort_flag = &sh->abort;
-  const bool dead = sh->abort != 0;                  // an earlier kernel timed out: no work
+    // The group's weights, heads past the last one zero.
+    for (int i = threadIdx.x; i < ng * p.NP; i += kScoreThreads) {
+      const int gi = i / p.NP, h = i - gi * p.NP;
+      sw[i] = h < p.Hi ? __ldg(p.w + static_cast<long long>(t0 + gi) * p.Hi + h) : 0.f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    volatile int* abort_flag = &sh->abort;
+    const bool dead = sh->abort != 0;                  // an earlier kernel timed out: no work
+    __syncthreads();                                   // the flag may be raised from here on
 
-  if (dead) {
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (n > 0 && elect_one()) {
-      const uint32_t qf = smem_u32(&sh->q_full);
-      mbar_expect_tx(qf, ng * KB * p.NP * 128);
-      for (int i = 0; i < ng; ++i)
-        for (int c = 0; c < KB; ++c)
-          tma_load_2d(smem_u32(smem + (i * KB + c) * p.NP * 128), &q_map, qf, c * (128 / ELT), (t0 + i) * p.Hi);
-    }
-    __syncwarp();
-    bool ok = true;
-    uint32_t issued = 0;
-    int pend = -1;
-    for (int j = 0; j < n && ok; ++j) {
-      const int pos0 = static_cast<int>(base0) + j * IT;
-      const uint32_t s = j % STAGES;
-      const uint32_t full = smem_u32(&sh->k_full[s]);
-      const uint32_t dst = smem_u32(smem + I_AT_RING + s * STAGE);
-      const int have = min(IT, pos_last + 1 - pos0);   // keys that some token sees
-      if constexpr (DENSE) {
-        const int boxes = (have + p.box - 1) / p.box;
-        int row = 0;
-        if (lane < boxes) {
-          row = score_row(p, b, pos0 + lane * p.box);
-          if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
-        }
-        if (j >= STAGES && !(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), ((j / STAGES) & 1) ^ 1, p.status, abort_flag)))
-          break;
-        if (lane == 0) mbar_expect_tx(full, boxes * p.box * 128 * KB);
-        __syncwarp();
-        if (lane < boxes)
-          for (int c = 0; c < KB; ++c)
-            tma_load_2d(dst + c * IT * 128 + lane * p.box * 128, &k_map, full, c * (128 / ELT), row);
-        __syncwarp();
-      } else {
-        int row[4];
+    if (dead) {
+    } else if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (elect_one()) {
+        const uint32_t qf = smem_u32(&sh->q_full);
+        mbar_expect_tx(qf, ng * KB * p.NP * 128);
+#pragma unroll 1
+        for (int i = 0; i < ng; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          row[x] = 32 * x + lane < have ? score_row(p, b, pos0 + 32 * x + lane) : 0;
-          if (row[x] < 0) row[x] = 0;                    // reported
-        }
-        if (j >= STAGES) {
-          // The ring is full: what was copied has to be counted before waiting.
+          for (int c = 0; c < KB; ++c)
+            tma_load_2d(smem_u32(smem) + (c * p.G + i) * p.NP * 128, &q_map, qf, c * (128 / ELT), (t0 + i) * p.Hi);
+      }
+      __syncwarp();
+      bool ok = true;
+      uint32_t issued = 0;
+      int pend = -1;
+      int s = 0, turn = 0;
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        const int pos0 = static_cast<int>(base0) + j * IT;
+        const uint32_t full = smem_u32(&sh->k_full[s]);
+        const uint32_t dst = smem_u32(smem) + p.at_ring + s * STAGE;
+        const int have = min(IT, pos_last + 1 - pos0);   // keys that some token sees
+        if constexpr (DENSE) {
+          const int boxes = (have + p.box - 1) / p.box;
+          int row = 0;
+          if (lane < boxes) {
+            row = score_row(p, b, pos0 + lane * p.box);
+            if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
+          }
+          if (turn > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), (turn & 1) ^ 1, p.status, abort_flag))) break;
+          if (lane == 0) mbar_expect_tx(full, boxes * p.box * 128 * KB);
+          __syncwarp();
+          if (lane < boxes)
+            for (int c = 0; c < KB; ++c)
+              tma_load_2d(dst + c * IT * 128 + lane * p.box * 128, &k_map, full, c * (128 / ELT), row);
+          __syncwarp();
+        } else {
+          int row[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            row[x] = 32 * x + lane < have ? score_row(p, b, pos0 + 32 * x + lane) : 0;
+            if (row[x] < 0) row[x] = 0;                    // reported
+          }
+          if (turn > 0) {
+            // The ring is full: what was copied has to be counted before waiting.
+            if (pend >= 0) {
+              cp_async_wait<0>();
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
+              pend = -1;
+            }
+            if (!(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), (turn & 1) ^ 1, p.status, abort_flag))) break;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int r = 4 * i + (lane >> 3), ch = lane & 7;
+            const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
+#pragma unroll
+            for (int c = 0; c < KB; ++c)
+              cp_async16(dst + c * IT * 128 + r * 128 + ((ch ^ (r & 7)) << 4),
+                         p.keys + static_cast<size_t>(src) * (128 * KB) + c * 128 + ch * 16);
+          }
+          cp_async_commit();
           if (pend >= 0) {
-            cp_async_wait<0>();
+            cp_async_wait<1>();
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
-            pend = -1;
           }
-          if (!(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), ((j / STAGES) & 1) ^ 1, p.status, abort_flag))) break;
+          pend = s;
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int r = 4 * i + (lane >> 3), ch = lane & 7;
-          const int src = __shfl_sync(0xffffffffu, row[i / 8], r & 31);
-#pragma unroll
-          for (int c = 0; c < KB; ++c)
-            cp_async16(dst + c * IT * 128 + r * 128 + ((ch ^ (r & 7)) << 4),
-                       p.keys + static_cast<size_t>(src) * (128 * KB) + c * 128 + ch * 16);
+        ++issued;
+        if (++s == p.stages) {
+          s = 0;
+          ++turn;
         }
-        cp_async_commit();
-        if (pend >= 0) {
-          cp_async_wait<1>();
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
-        }
-        pend = static_cast<int>(s);
       }
-      ++issued;
-    }
-    if constexpr (!DENSE) {
-      cp_async_wait<0>();
-      fence_async_smem();
-      __syncwarp();
-      if (pend >= 0 && lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
-    }
-    volatile int never = 0;
-    if (n > 0) mbar_wait_warp(smem_u32(&sh->q_full), 0, p.status, &never);
-    for (uint32_t s = 0; s < STAGES; ++s)
-      if (issued > s) mbar_wait_warp(smem_u32(&sh->k_full[s]), ((issued - 1 - s) / STAGES) & 1, p.status, &never);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (n > 0 && elect_one()) {
-      const uint32_t idesc = E8 ? idesc_e4m3(128, p.NP, false, false) : idesc_bf16(128, p.NP, false, false);
-      bool ok = mbar_wait(smem_u32(&sh->q_full), 0, p.status, abort_flag);
-      uint32_t u = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t s = j % STAGES;
-        if (!(ok = mbar_wait(smem_u32(&sh->k_full[s]), (j / STAGES) & 1, p.status, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t a = smem_u32(smem + I_AT_RING + s * STAGE);
-        for (int i = 0; i < ng; ++i, ++u) {
-          if (u >= 2 && !(ok = mbar_wait(smem_u32(&sh->d_free[u & 1]), ((u >> 1) & 1) ^ 1, p.status, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t d = tmem + (u & 1) * 128;
-#pragma unroll
-          for (int c = 0; c < KB; ++c) {
-            const uint32_t q = smem_u32(smem + (i * KB + c) * p.NP * 128);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = sdesc(a + c * IT * 128 + kk * 32, 16, 1024), bd = sdesc(q + kk * 32, 16, 1024);
-              if (E8) mma_f8_ss(d, ad, bd, idesc, (c | kk) != 0);
-              else mma_f16_ss(d, ad, bd, idesc, (c | kk) != 0);
-            }
-          }
-          tc_commit(smem_u32(&sh->d_full[u & 1]));
-        }
-        tc_commit(smem_u32(&sh->k_empty[s]));
+      if constexpr (!DENSE) {
+        cp_async_wait<0>();
+        fence_async_smem();
+        __syncwarp();
+        if (pend >= 0 && lane == 0) mbar_arrive(smem_u32(&sh->k_full[pend]));
       }
-      tc_commit(smem_u32(&sh->drain));
       volatile int never = 0;
-      mbar_wait(smem_u32(&sh->drain), 0, p.status, &never);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ weighted sums
-    const int e = (warp - 2) >> 2;                   // epilogue warpgroup: units u with u & 1 == e
-    const int q4 = warp & 3;
-    const int key = q4 * 32 + lane;
-    const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * 128;
-    bool ok = true;
-    uint32_t u = 0, mine = 0;
-    for (int j = 0; j < n && ok; ++j) {
-      const int pos = static_cast<int>(base0) + j * IT + key;
-      float ks = 1.f;
-      if (p.key_scales != nullptr && pos <= pos_last) {
-        const int row = score_row(p, b, pos);
-        if (row >= 0) ks = __ldg(p.key_scales + row);
+      mbar_wait_warp(smem_u32(&sh->q_full), 0, p.status, &never);
+      for (int x = 0; x < p.stages; ++x) {
+        const int uses = turn + (x < s ? 1 : 0);
+        if (uses > 0) mbar_wait_warp(smem_u32(&sh->k_full[x]), (uses - 1) & 1, p.status, &never);
       }
-      for (int i = 0; i < ng; ++i, ++u) {
-        if ((u & 1) != static_cast<uint32_t>(e)) continue;
-        ok = ok && mbar_wait_warp(smem_u32(&sh->d_full[e]), mine & 1, p.status, abort_flag);
-        ++mine;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        if (ok) {
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (elect_one()) {
+        bool ok = mbar_wait(smem_u32(&sh->q_full), 0, p.status, abort_flag);
+        const uint64_t q0 = sdesc(smem_u32(smem), 16, 1024), k0 = sdesc(smem_u32(smem) + p.at_ring, 16, 1024);
+        const uint32_t qblock = static_cast<uint32_t>(p.G * p.NP * 128) >> 4;
+        uint32_t u = 0;
+        int s = 0, turn = 0;
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          if (!(ok = mbar_wait(smem_u32(&sh->k_full[s]), turn & 1, p.status, abort_flag))) break;
           tc_fence_after();
-          const float* w = sw + i * 128;
-          for (int c0 = 0; c0 < p.NP; c0 += 32) {
-            uint32_t x[32];
-            tmem_ld32(ta + c0, x);
-            tmem_ld_wait();
+          const uint64_t ad = k0 + s * (STAGE >> 4);
+#pragma unroll 1
+          for (int i = 0; i < batches; ++i, ++u) {
+            if (u >= 2 && !(ok = mbar_wait(smem_u32(&sh->d_free[u & 1]), ((u >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+            tc_fence_after();
+            const int cols = min(p.batch, ng - i * p.batch) * p.NP;
+            const uint32_t idesc = E8 ? idesc_e4m3(128, cols, false, false) : idesc_bf16(128, cols, false, false);
+            const uint32_t d = tmem + (u & 1) * (p.cols >> 1);
+            const uint64_t bd = q0 + static_cast<uint32_t>(i * p.batch * p.NP * 128 >> 4);
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 wv = *reinterpret_cast<const float4*>(w + c0 + c);
-              if (c0 + c + 4 <= p.Hi) {
-                acc[0] = fmaf(max_nan(__uint_as_float(x[c]), 0.f), wv.x, acc[0]);
-                acc[1] = fmaf(max_nan(__uint_as_float(x[c + 1]), 0.f), wv.y, acc[1]);
-                acc[2] = fmaf(max_nan(__uint_as_float(x[c + 2]), 0.f), wv.z, acc[2]);
-                acc[3] = fmaf(max_nan(__uint_as_float(x[c + 3]), 0.f), wv.w, acc[3]);
-              } else {
-                // Columns past the last head hold the next token's products.
-                if (c0 + c < p.Hi) acc[0] = fmaf(max_nan(__uint_as_float(x[c]), 0.f), wv.x, acc[0]);
-                if (c0 + c + 1 < p.Hi) acc[1] = fmaf(max_nan(__uint_as_float(x[c + 1]), 0.f), wv.y, acc[1]);
-                if (c0 + c + 2 < p.Hi) acc[2] = fmaf(max_nan(__uint_as_float(x[c + 2]), 0.f), wv.z, acc[2]);
+            for (int c = 0; c < KB; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                if (E8) mma_f8_ss(d, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
+                else mma_f16_ss(d, ad + c * (IT * 128 >> 4) + kk * 2, bd + c * qblock + kk * 2, idesc, (c | kk) != 0);
               }
+            tc_commit(smem_u32(&sh->d_full[u & 1]));
+          }
+          tc_commit(smem_u32(&sh->k_empty[s]));
+          if (++s == p.stages) {
+            s = 0;
+            ++turn;
+          }
+        }
+        tc_commit(smem_u32(&sh->drain));
+        volatile int never = 0;
+        mbar_wait(smem_u32(&sh->drain), 0, p.status, &never);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- weighted sums
+      const int e = (warp - 2) >> 2;                   // warpgroup: units u with u & 1 == e
+      const int q4 = warp & 3;
+      const int key = q4 * 32 + lane;
+      const int tid = threadIdx.x - 64 - 128 * e;
+      const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * (p.cols >> 1);
+      const int shift = __ffs(p.block) - 1;
+      uint32_t mine = 0;
+      int j = e / batches, i = e - j * batches;        // tile and batch of the unit
+      // This key's scale in the unit's tile is read a unit ahead, its page id two.
+      auto page_of = [&](int tile) -> int {
+        const int pos = static_cast<int>(base0) + tile * IT + key;
+        if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 0;
+        const int pi = pos / p.page_size;
+        return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
+      };
+      auto scale_of = [&](int tile, int page) -> float {
+        const int pos = static_cast<int>(base0) + tile * IT + key;
+        if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 1.f;
+        if (page >= 0 && page < p.num_pages) return __ldg(p.key_scales + page * p.page_size + pos % p.page_size);
+        set_status(p.status, MLA_DEV_BAD_PAGE);
+        return 1.f;
+      };
+      auto later = [&](int units) { return j + (i + units) / batches; };   // the tile of a unit further on
+      float next = scale_of(j, page_of(j));
+      int page = page_of(later(2));
+#pragma unroll 1
+      while (j < n) {
+        const int pos = static_cast<int>(base0) + j * IT + key;
+        const float ks = next;
+        next = scale_of(later(2), page);
+        page = page_of(later(4));
+        const bool ok = mbar_wait_warp(smem_u32(&sh->d_full[e]), mine & 1, p.status, abort_flag);
+        ++mine;
+        tc_fence_after();
+        const int tok0 = i * p.batch, toks = ok ? min(p.batch, ng - tok0) : 0;
+#pragma unroll 1
+        for (int y = 0; y < toks; ++y) {
+          const float* w = sw + (tok0 + y) * p.NP;
+          float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c0 = 0; c0 < p.Hi; c0 += 16) {
+            uint32_t x[16];
+            tmem_ld16(ta + y * p.NP + c0, x);
+            tmem_ld_wait();
+            if (c0 + 16 > p.Hi) {
+              // Columns past the last head hold the next token's products.
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (c0 + c >= p.Hi) x[c] = 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              const float4 wv = *reinterpret_cast<const float4*>(w + c0 + c);
+              a0 = __ffma2_rn(make_float2(max_nan(__uint_as_float(x[c]), 0.f), max_nan(__uint_as_float(x[c + 1]), 0.f)),
+                              make_float2(wv.x, wv.y), a0);
+              a1 = __ffma2_rn(make_float2(max_nan(__uint_as_float(x[c + 2]), 0.f), max_nan(__uint_as_float(x[c + 3]), 0.f)),
+                              make_float2(wv.z, wv.w), a1);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh->d_free[e]));
-        }
-        float v = ((acc[0] + acc[1]) + (acc[2] + acc[3])) * ks;
-        if (pos > pos_first + i) v = -kInf;          // not visible to the token
-        float* dst = p.scores + static_cast<long long>(t0 + i) * p.stride;
-        if (p.block == 1) {
-          if (ok && pos < p.stride) dst[pos] = v;
-        } else {
-          const int in_warp = min(p.block, 32);
-          for (int d = 1; d < in_warp; d <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
-          if (p.block <= 32) {
-            if (ok && lane % p.block == 0 && pos / p.block < p.stride) dst[pos / p.block] = v;
+          const float2 a = __fadd2_rn(a0, a1);
+          float v = (a.x + a.y) * ks;
+          const int t = tok0 + y;
+          if (pos > pos_first + t) v = -kInf;          // not visible to the token
+          if (p.block == 1) {
+            if (pos < p.stride) p.scores[static_cast<long long>(t0 + t) * p.stride + pos] = v;
           } else {
-            // Blocks of 64 or 128 keys: two or four warps' maxima.  (A failed
-            // wait leaves this loop only at its end, so the barrier is met.)
-            if (lane == 0) sh->part[e][q4] = v;
-            asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
-            const int first = p.block == 64 ? (q4 & 2) : 0;
-            if (lane == 0 && q4 == first) {
-              float m = max_nan(sh->part[e][first], sh->part[e][first + 1]);
-              if (p.block == 128) m = max_nan(m, max_nan(sh->part[e][2], sh->part[e][3]));
-              if (ok && pos / p.block < p.stride) dst[pos / p.block] = m;
+            const int in_warp = min(p.block, 32);
+            for (int d = 1; d < in_warp; d <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
+            if (p.block <= 32) {
+              if ((lane & (p.block - 1)) == 0 && (pos >> shift) < p.stride)
+                p.scores[static_cast<long long>(t0 + t) * p.stride + (pos >> shift)] = v;
+            } else if (lane == 0) {
+              sh->part[e][y][q4] = v;
             }
-            asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(smem_u32(&sh->d_free[e]));
+        if (p.block > 32) {
+          // Blocks of 64 or 128 keys: two or four warps' maxima, a thread for
+          // each token and block.  (Its warps leave this loop together: a wait
+          // that ran out in one of them is known to the others by the barrier.)
+          const int blocks = IT / p.block, warps = 4 / blocks;
+          int bad;
+          asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+                       "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                       : "=r"(bad) : "r"(ok ? 0 : 1), "r"(e + 1) : "memory");
+          const int y = tid / blocks, x = tid - y * blocks;
+          if (y < toks) {
+            float m = sh->part[e][y][x * warps];
+            for (int k = 1; k < warps; ++k) m = max_nan(m, sh->part[e][y][x * warps + k]);
+            const int at = ((static_cast<int>(base0) + j * IT) >> shift) + x;
+            if (at < p.stride) p.scores[static_cast<long long>(t0 + tok0 + y) * p.stride + at] = m;
+          }
+          asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
+          if (bad) break;
+        } else if (!ok) {
+          break;
+        }
+        j = later(2);
+        i = (i + 2) % batches;
       }
     }
-    // Blocks past the group's last key: -infinity.
-    const long long from = (base0 + static_cast<long long>(n) * IT) / p.block;
-    const long long to = min(static_cast<long long>(p.stride), (base0 + static_cast<long long>(tiles) * IT) / p.block);
-    const int tid = threadIdx.x - 64;
-    for (int i = 0; i < ng; ++i)
-      for (long long x = from + tid; x < to; x += 256) p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc(tmem, p.cols);
+    }
+    if (dead) return;
+  } else if (timed_out_before(p.status)) {
+    return;
   }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 256);
-  }
+  // Blocks past the group's last key: -infinity.
+  const long long from = (base0 + static_cast<long long>(n) * IT) / p.block;
+  const long long to = min(static_cast<long long>(p.stride), (base0 + static_cast<long long>(tiles) * IT) / p.block);
+  for (int i = 0; i < ng; ++i)
+    for (long long x = from + threadIdx.x; x < to; x += kScoreThreads)
+      p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
 }
 
 // ============================================================ selection
@@ -587,15 +644,31 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.max_seq = a.max_seq;
   p.stride = a.stride;
   p.status = a.status;
+  const int stage = kb * IT * 128;
+  // Tokens of a group: as many queries as 64 KB hold; of an MMA: 256 columns.
   p.G = std::max(1, std::min({I_MAXG, a.max_new, I_QMAX / (p.NP * 128 * kb)}));
+  p.batch = std::min(p.G, 256 / p.NP);
   p.groups = (a.max_new + p.G - 1) / p.G;
   int box = 1;
   while (box < IT && a.page_size % (2 * box) == 0) box *= 2;
   p.box = box;
-  // Ranges of positions: about two CTAs an SM, at least eight tiles each.
+  p.cols = 32;
+  while (p.cols < 2 * p.batch * p.NP) p.cols *= 2;
+  // Two CTAs an SM where their TMEM allows it, else one with a longer ring.
+  const bool two = p.cols <= 256;
+  const int q_bytes = p.G * p.NP * 128 * kb, w_bytes = (p.G * p.NP * 4 + 1023) / 1024 * 1024;
+  const int room = (two ? 112 : 226) * 1024 - q_bytes - w_bytes - I_BAR - 1024;
+  p.stages = std::max(2, std::min(I_MAXSTAGES, room / stage));
+  p.at_ring = q_bytes;
+  p.at_w = p.at_ring + p.stages * stage;
+  p.at_bar = p.at_w + w_bytes;
+  const int smem = p.at_bar + I_BAR + 1024;
+  // Ranges of positions: CTAs for three rounds of the SMs' places, of at least
+  // eight tiles each (a start costs about three).
   const long long tiles = (static_cast<long long>(a.stride) * a.block + IT - 1) / IT;
   const long long pairs = static_cast<long long>(a.B) * p.groups;
-  long long span = (pairs * tiles + 2 * sm_count() - 1) / (2 * sm_count());
+  const long long places = 3ll * (two ? 2 : 1) * sm_count();
+  long long span = (pairs * tiles + places - 1) / places;
   span = std::min(tiles, std::max(8ll, span));
   p.span = static_cast<int>(span);
   p.splits = static_cast<int>((tiles + span - 1) / span);
@@ -611,9 +684,10 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
                  dense ? box : 8, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   auto go = [&](auto kernel) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I_TOTAL);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kScoreThreads), I_TOTAL, stream, q_map, k_map, p);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kScoreThreads), static_cast<size_t>(smem), stream,
+                      q_map, k_map, p);
   };
   if (e8) return dense ? go(index_scores_kernel<true, true>) : go(index_scores_kernel<true, false>);
   return dense ? go(index_scores_kernel<false, true>) : go(index_scores_kernel<false, false>);
