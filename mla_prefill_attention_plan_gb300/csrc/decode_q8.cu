@@ -369,17 +369,6 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t
   return __all_sync(0xffffffffu, wait_one(bar, parity, status, abort_flag));
 }
 
-// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and
-// m = ceil(2^(31 + l) / d), m d exceeds 2^(31 + l) by less than 2^l, so the
-// product's error stays below 2^(31 + l) / d.
-struct FastDiv {
-  uint32_t m;
-  int shift, d;
-};
-__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
-  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.m) >> f.shift);
-}
-
 // A ring slot holds half of a tile's latent columns (two 128-column blocks) in
 // groups of eight keys: [key / 8][block][key % 8][128 bytes], swizzled within
 // the 1 KB of each group and block.  One TMA instruction then loads both blocks
@@ -1621,16 +1610,6 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
 template <typename K>
 cudaError_t opt_in_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-FastDiv fast_divisor(int d) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;
-  FastDiv f;
-  f.m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
-  f.shift = 31 + l;
-  f.d = d;
-  return f;
 }
 
 // Largest power of two, at most 128, that divides the page size.

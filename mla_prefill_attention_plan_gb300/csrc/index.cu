@@ -21,6 +21,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
   return r;
 }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Largest b with iro[b] <= t (t belongs to b when t < iro[b + 1]).
 __device__ __forceinline__ int sequence_of(const uint32_t* __restrict__ iro, int B, uint32_t t) {
   int lo = 0, hi = B;
@@ -37,18 +49,23 @@ __device__ __forceinline__ int sequence_of(const uint32_t* __restrict__ iro, int
 // products with all of them in its own TMEM lane and the weighted sums need no
 // other thread.  One CTA per (sequence, group of its new tokens, range of
 // positions): the group's queries stay in shared memory, key tiles stream
-// through a ring, and two epilogue warpgroups take the (tile, batch) units in
-// turn, each with its own TMEM buffer of up to 256 columns.
+// through a ring, and the two epilogue warpgroups take the (tile, batch) units
+// in turn, each with its own TMEM buffer of up to 128 columns.  Two CTAs share
+// an SM, one's start under the other's work.
 //
-// With one new token a sequence the call is bound by reading the keys (256 or
-// 128 bytes each; 64 heads: 64 flops a byte); the CTA then needs few buffers
-// and two of them share an SM, one's start under the other's loads.  With many
-// tokens it is bound by the epilogue, three instructions for two products: a
-// batch fills the TMEM buffer, so that an MMA's latency (some 600 clk to its
-// barrier) is paid once for 256 columns.
+// With one new token a sequence the call is bound by reading the keys: 64
+// sequences of 4096 to 16384 keys, 64 heads, bf16, 42 us (4.1 TB/s).  With
+// more it is bound by the epilogue, which takes a maximum and half a packed FMA
+// for every product on the CUDA cores: about 1000 tokens, 32 heads, 8000 8-bit
+// keys, blocks of 64, 106 us (2.3 T products/s, issue slots 54 % taken).  A
+// batch of tokens therefore fills a buffer, so that an MMA's latency (some 600
+// clk to its barrier) is paid once for all of them, and the loop stays small:
+// two chunks in flight in a warp; four ran at 155 us where two ran at 131, and
+// four warpgroups of one CTA an SM at 135.
 constexpr int IT = 128;                             // keys of a tile
-constexpr int kScoreThreads = 320;                  // producer, MMA, 2 x 4 epilogue warps
-constexpr int I_QMAX = 64 * 1024;                   // query bytes kept at most
+constexpr int I_QMAX = 32 * 1024;                   // query bytes of a group with several tokens, at most
+constexpr int GROUPS = 2;                           // epilogue warpgroups and TMEM buffers
+constexpr int kScoreThreads = 64 + 128 * GROUPS;    // producer, MMA and epilogue warps
 constexpr int I_MAXG = 16;                          // tokens of a group at most
 constexpr int I_MAXSTAGES = 8;
 
@@ -56,7 +73,7 @@ struct ScoreSmem {
   uint64_t k_full[I_MAXSTAGES], k_empty[I_MAXSTAGES], q_full, d_full[2], d_free[2], drain;
   uint32_t tmem;
   int abort;
-  float part[2][I_MAXG][4];    // [warpgroup][token][warp]: maxima, for blocks of more than 32 keys
+  float part[2][2][8][4];         // [warpgroup][unit & 1][token][warp]: maxima, for blocks of more than 32 keys
 };
 constexpr int I_BAR = 1024;
 static_assert(sizeof(ScoreSmem) <= I_BAR, "barrier block");
@@ -69,7 +86,8 @@ struct ScoreParams {
   const uint32_t* iro;
   const uint32_t* cache_len;
   const int32_t* page_table;
-  int num_pages, page_size, max_pages, block, B, Hi, NP, T, groups, splits, span, max_seq, stride, box;
+  FastDiv page;
+  int num_pages, max_pages, block, B, Hi, NP, T, groups, splits, span, max_seq, stride, box;
   int G, batch;              // tokens of a group and of an MMA
   int stages, cols;          // ring stages, TMEM columns allocated
   int at_w, at_ring, at_bar; // shared memory: queries, weights [G][NP], ring, barriers
@@ -77,9 +95,9 @@ struct ScoreParams {
 };
 
 __device__ __forceinline__ int score_row(const ScoreParams& p, int b, int pos) {
-  const int pi = pos / p.page_size;
+  const int pi = fast_div(pos, p.page);
   const int page = pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
-  if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - pi * p.page_size);
+  if (page >= 0 && page < p.num_pages) return page * p.page.d + (pos - pi * p.page.d);
   set_status(p.status, MLA_DEV_BAD_PAGE);
   return -1;
 }
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
         mbar_init(smem_u32(&sh->k_empty[s]), 1);
       }
       mbar_init(smem_u32(&sh->q_full), 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < GROUPS; ++i) {
         mbar_init(smem_u32(&sh->d_full[i]), 1);
         mbar_init(smem_u32(&sh->d_free[i]), 4);
       }
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
           int row = 0;
           if (lane < boxes) {
             row = score_row(p, b, pos0 + lane * p.box);
-            if (row < 0) row = p.num_pages * p.page_size;   // past the end: reads zeros
+            if (row < 0) row = p.num_pages * p.page.d;   // past the end: reads zeros
           }
           if (turn > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->k_empty[s]), (turn & 1) ^ 1, p.status, abort_flag))) break;
           if (lane == 0) mbar_expect_tx(full, boxes * p.box * 128 * KB);
@@ -261,11 +279,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
           const uint64_t ad = k0 + s * (STAGE >> 4);
 #pragma unroll 1
           for (int i = 0; i < batches; ++i, ++u) {
-            if (u >= 2 && !(ok = mbar_wait(smem_u32(&sh->d_free[u & 1]), ((u >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+            const uint32_t buf = u % GROUPS;
+            if (u >= GROUPS && !(ok = mbar_wait(smem_u32(&sh->d_free[buf]), ((u / GROUPS) & 1) ^ 1, p.status, abort_flag))) break;
             tc_fence_after();
             const int cols = min(p.batch, ng - i * p.batch) * p.NP;
             const uint32_t idesc = E8 ? idesc_e4m3(128, cols, false, false) : idesc_bf16(128, cols, false, false);
-            const uint32_t d = tmem + (u & 1) * (p.cols >> 1);
+            const uint32_t d = tmem + buf * (p.cols / GROUPS);
             const uint64_t bd = q0 + static_cast<uint32_t>(i * p.batch * p.NP * 128 >> 4);
 #pragma unroll
             for (int c = 0; c < KB; ++c)
@@ -274,7 +293,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                 if (E8) mma_f8_ss(d, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
                 else mma_f16_ss(d, ad + c * (IT * 128 >> 4) + kk * 2, bd + c * qblock + kk * 2, idesc, (c | kk) != 0);
               }
-            tc_commit(smem_u32(&sh->d_full[u & 1]));
+            tc_commit(smem_u32(&sh->d_full[buf]));
           }
           tc_commit(smem_u32(&sh->k_empty[s]));
           if (++s == p.stages) {
@@ -289,81 +308,106 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- weighted sums
-      const int e = (warp - 2) >> 2;                   // warpgroup: units u with u & 1 == e
+      const int e = (warp - 2) >> 2;                   // warpgroup: units u with u % GROUPS == e
       const int q4 = warp & 3;
       const int key = q4 * 32 + lane;
       const int tid = threadIdx.x - 64 - 128 * e;
-      const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * (p.cols >> 1);
+      const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * (p.cols / GROUPS);
       const int shift = __ffs(p.block) - 1;
+      const int tpt = p.Hi <= 16 ? 2 : 1;              // tokens of a turn
       uint32_t mine = 0;
       int j = e / batches, i = e - j * batches;        // tile and batch of the unit
       // This key's scale in the unit's tile is read a unit ahead, its page id two.
       auto page_of = [&](int tile) -> int {
         const int pos = static_cast<int>(base0) + tile * IT + key;
         if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 0;
-        const int pi = pos / p.page_size;
+        const int pi = fast_div(pos, p.page);
         return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
       };
       auto scale_of = [&](int tile, int page) -> float {
         const int pos = static_cast<int>(base0) + tile * IT + key;
         if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 1.f;
-        if (page >= 0 && page < p.num_pages) return __ldg(p.key_scales + page * p.page_size + pos % p.page_size);
+        if (page >= 0 && page < p.num_pages) return __ldg(p.key_scales + page * p.page.d + pos - fast_div(pos, p.page) * p.page.d);
         set_status(p.status, MLA_DEV_BAD_PAGE);
         return 1.f;
       };
-      auto later = [&](int units) { return j + (i + units) / batches; };   // the tile of a unit further on
+      // The tile (and batch) of the warpgroup's next unit.
+      auto step = [&](int& tile, int& batch) {
+        for (batch += GROUPS; batch >= batches; batch -= batches) ++tile;
+      };
       float next = scale_of(j, page_of(j));
-      int page = page_of(later(2));
+      int j1 = j, i1 = i;
+      step(j1, i1);
+      int page = page_of(j1);
 #pragma unroll 1
       while (j < n) {
         const int pos = static_cast<int>(base0) + j * IT + key;
         const float ks = next;
-        next = scale_of(later(2), page);
-        page = page_of(later(4));
+        next = scale_of(j1, page);
+        int j2 = j1, i2 = i1;
+        step(j2, i2);
+        page = page_of(j2);
         const bool ok = mbar_wait_warp(smem_u32(&sh->d_full[e]), mine & 1, p.status, abort_flag);
         ++mine;
         tc_fence_after();
         const int tok0 = i * p.batch, toks = ok ? min(p.batch, ng - tok0) : 0;
+        // Two chunks of 16 columns at a time, of one token or, with up to 16
+        // heads, of two: two chains in flight in each of the warps.
 #pragma unroll 1
-        for (int y = 0; y < toks; ++y) {
-          const float* w = sw + (tok0 + y) * p.NP;
-          float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+        for (int y0 = 0; y0 < toks; y0 += tpt) {
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const int y1 = tpt == 2 ? min(y0 + 1, toks - 1) : y0;
+          const uint32_t col0 = ta + y0 * p.NP, col1 = ta + y1 * p.NP;
+          const uint32_t w0 = smem_u32(sw) + (tok0 + y0) * p.NP * 4, w1 = smem_u32(sw) + (tok0 + y1) * p.NP * 4;
 #pragma unroll 1
-          for (int c0 = 0; c0 < p.Hi; c0 += 16) {
-            uint32_t x[16];
-            tmem_ld16(ta + y * p.NP + c0, x);
+          for (int c = 0; c < p.Hi; c += 16 * (2 / tpt)) {
+            const int second = tpt == 2 ? 0 : min(c + 16, p.NP - 16);
+            uint32_t d[2][16];
+            tmem_ld16(col0 + c, d[0]);
+            tmem_ld16(col1 + second, d[1]);
             tmem_ld_wait();
-            if (c0 + 16 > p.Hi) {
-              // Columns past the last head hold the next token's products.
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (c0 + c >= p.Hi) x[c] = 0u;
-            }
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w = x == 0 ? w0 + 4 * c : w1 + 4 * second;
+              // Heads of the chunk (none: a chunk past the last).
+              const int heads = p.Hi - c - (x == 1 && tpt == 1 ? 16 : 0);
+              if (__builtin_expect(heads < 16, 0)) {
+                if (heads <= 0) break;
+                // Columns past the last head hold the next token's products.
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              const float4 wv = *reinterpret_cast<const float4*>(w + c0 + c);
-              a0 = __ffma2_rn(make_float2(max_nan(__uint_as_float(x[c]), 0.f), max_nan(__uint_as_float(x[c + 1]), 0.f)),
-                              make_float2(wv.x, wv.y), a0);
-              a1 = __ffma2_rn(make_float2(max_nan(__uint_as_float(x[c + 2]), 0.f), max_nan(__uint_as_float(x[c + 3]), 0.f)),
-                              make_float2(wv.z, wv.w), a1);
+                for (int k = 0; k < 16; ++k)
+                  if (k >= heads) d[x][k] = 0u;
+              }
+              float2 a1 = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 wv = ld_shared_f4(w + 4 * k);
+                acc[x] = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[x][k]), 0.f), max_nan(__uint_as_float(d[x][k + 1]), 0.f)),
+                                    make_float2(wv.x, wv.y), acc[x]);
+                a1 = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[x][k + 2]), 0.f), max_nan(__uint_as_float(d[x][k + 3]), 0.f)),
+                                make_float2(wv.z, wv.w), a1);
+              }
+              acc[x] = __fadd2_rn(acc[x], a1);
             }
           }
-          const float2 a = __fadd2_rn(a0, a1);
-          float v = (a.x + a.y) * ks;
-          const int t = tok0 + y;
-          if (pos > pos_first + t) v = -kInf;          // not visible to the token
-          if (p.block == 1) {
-            if (pos < p.stride) p.scores[static_cast<long long>(t0 + t) * p.stride + pos] = v;
-          } else {
-            const int in_warp = min(p.block, 32);
-            for (int d = 1; d < in_warp; d <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
-            if (p.block <= 32) {
-              if ((lane & (p.block - 1)) == 0 && (pos >> shift) < p.stride)
-                p.scores[static_cast<long long>(t0 + t) * p.stride + (pos >> shift)] = v;
-            } else if (lane == 0) {
-              sh->part[e][y][q4] = v;
+          auto finish = [&](float v, int y) {
+            v *= ks;
+            if (pos > pos_first + tok0 + y) v = -kInf;     // not visible to the token
+            if (p.block >= 32) {
+              v = warp_max_nan(v);
+            } else {
+#pragma unroll 1
+              for (int r = 1; r < p.block; r <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, r));
             }
-          }
+            if (p.block > 32) {
+              if (lane == 0) sh->part[e][mine & 1][y][q4] = v;
+            } else if ((lane & (p.block - 1)) == 0 && (pos >> shift) < p.stride) {
+              p.scores[static_cast<long long>(t0 + tok0 + y) * p.stride + (pos >> shift)] = v;
+            }
+          };
+          const float v0 = acc[0].x + acc[0].y, v1 = acc[1].x + acc[1].y;
+          finish(tpt == 1 ? v0 + v1 : v0, y0);
+          if (tpt == 2 && y0 + 1 < toks) finish(v1, y0 + 1);
         }
         tc_fence_before();
         __syncwarp();
@@ -379,18 +423,19 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                        : "=r"(bad) : "r"(ok ? 0 : 1), "r"(e + 1) : "memory");
           const int y = tid / blocks, x = tid - y * blocks;
           if (y < toks) {
-            float m = sh->part[e][y][x * warps];
-            for (int k = 1; k < warps; ++k) m = max_nan(m, sh->part[e][y][x * warps + k]);
+            float m = sh->part[e][mine & 1][y][x * warps];
+            for (int k = 1; k < warps; ++k) m = max_nan(m, sh->part[e][mine & 1][y][x * warps + k]);
             const int at = ((static_cast<int>(base0) + j * IT) >> shift) + x;
             if (at < p.stride) p.scores[static_cast<long long>(t0 + tok0 + y) * p.stride + at] = m;
           }
-          asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(e + 1) : "memory");
           if (bad) break;
         } else if (!ok) {
           break;
         }
-        j = later(2);
-        i = (i + 2) % batches;
+        j = j1;
+        i = i1;
+        j1 = j2;
+        i1 = i2;
       }
     }
     tc_fence_before();
@@ -634,7 +679,7 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.cache_len = a.cache_len;
   p.page_table = a.page_table;
   p.num_pages = a.num_pages;
-  p.page_size = a.page_size;
+  p.page = fast_divisor(a.page_size);
   p.max_pages = a.max_pages;
   p.block = a.block;
   p.B = a.B;
@@ -645,29 +690,27 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.stride = a.stride;
   p.status = a.status;
   const int stage = kb * IT * 128;
-  // Tokens of a group: as many queries as 64 KB hold; of an MMA: 256 columns.
+  // Tokens of a group: as many queries as 32 KB hold; of an MMA: 128 columns, eight at most.
   p.G = std::max(1, std::min({I_MAXG, a.max_new, I_QMAX / (p.NP * 128 * kb)}));
-  p.batch = std::min(p.G, 256 / p.NP);
+  p.batch = std::min({p.G, 8, 128 / p.NP});
   p.groups = (a.max_new + p.G - 1) / p.G;
   int box = 1;
   while (box < IT && a.page_size % (2 * box) == 0) box *= 2;
   p.box = box;
   p.cols = 32;
-  while (p.cols < 2 * p.batch * p.NP) p.cols *= 2;
-  // Two CTAs an SM where their TMEM allows it, else one with a longer ring.
-  const bool two = p.cols <= 256;
+  while (p.cols < GROUPS * p.batch * p.NP) p.cols *= 2;
   const int q_bytes = p.G * p.NP * 128 * kb, w_bytes = (p.G * p.NP * 4 + 1023) / 1024 * 1024;
-  const int room = (two ? 112 : 226) * 1024 - q_bytes - w_bytes - I_BAR - 1024;
+  const int room = 112 * 1024 - q_bytes - w_bytes - I_BAR - 1024;
   p.stages = std::max(2, std::min(I_MAXSTAGES, room / stage));
   p.at_ring = q_bytes;
   p.at_w = p.at_ring + p.stages * stage;
   p.at_bar = p.at_w + w_bytes;
   const int smem = p.at_bar + I_BAR + 1024;
-  // Ranges of positions: CTAs for three rounds of the SMs' places, of at least
+  // Ranges of positions: CTAs for three rounds of the SMs' two places, of at least
   // eight tiles each (a start costs about three).
   const long long tiles = (static_cast<long long>(a.stride) * a.block + IT - 1) / IT;
   const long long pairs = static_cast<long long>(a.B) * p.groups;
-  const long long places = 3ll * (two ? 2 : 1) * sm_count();
+  const long long places = 3ll * 2 * sm_count();
   long long span = (pairs * tiles + places - 1) / places;
   span = std::min(tiles, std::max(8ll, span));
   p.span = static_cast<int>(span);

@@ -29,6 +29,26 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and
+// m = ceil(2^(31 + l) / d), m d exceeds 2^(31 + l) by less than 2^l, so the
+// product's error stays below 2^(31 + l) / d.
+struct FastDiv {
+  uint32_t m;
+  int shift, d;
+};
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.m) >> f.shift);
+}
+inline FastDiv fast_divisor(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  FastDiv f;
+  f.m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+  f.shift = 31 + l;
+  f.d = d;
+  return f;
+}
+
 cudaError_t launch_plan(uint32_t* bro, uint32_t* co, int32_t* bl, const uint32_t* iro,
                         const uint32_t* cache_len, int B, int max_chunks, uint32_t S,
                         int32_t* status, cudaStream_t stream);
