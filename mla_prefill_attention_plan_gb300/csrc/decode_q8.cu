@@ -405,7 +405,7 @@ struct Shape {
   static constexpr int AT_Q = AT_ROPE + ROPES * ROPE;
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
-  static constexpr int TOTAL = AT_BAR + 3072;
+  static constexpr int TOTAL = AT_BAR + 3 * 1024;
   static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x 64 columns
   static constexpr uint32_t TM_COLS = 512;
   static_assert(TOTAL <= 227 * 1024 && TM_O + 256 <= TM_COLS, "shared memory, TMEM");
@@ -424,11 +424,11 @@ struct AttnSmem {
   alignas(16) float d[64];    // and step of the exponent;
   int top[64];                // largest weight of a row (order-preserving integers)
   int lim[64];                // keys of the segment that the row sees
-  int bad[4][2];              // [group][tile & 1]: a weight of the tile is out of range
+  int bad[4][4];              // [group][tile & 3]: a weight of the tile is out of range
   float ksc[2][128];          // [tile & 1]: the keys' scales (1 past the segment)
   int run[32], last[16];      // cache rows of the runs that are loaded next, and of the tile before them
 };
-static_assert(sizeof(AttnSmem) <= 3072, "barrier block");
+static_assert(sizeof(AttnSmem) <= 3 * 1024, "barrier block");
 
 struct Q8Params {
   const PlanHead* head;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
     mbar_init(smem_u32(&sh->drain), 1);
     for (int i = 0; i < GROUPS; ++i) {
       mbar_init(smem_u32(&sh->group[i]), 4);
-      sh->bad[i][0] = sh->bad[i][1] = 0;
+      for (int k = 0; k < 4; ++k) sh->bad[i][k] = 0;
     }
     // An earlier kernel timed out: no work (and no plan to read).
     sh->abort = timed_out_before(status) ? 1 : 0;
@@ -995,7 +995,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
             float mx = -kInf;
 #pragma unroll
             for (int c = 0; c < 8; ++c) mx = fmax3(mx, t[c].x, t[c].y);
-            if (mx + lsc > kGrow) sh->bad[wg][sb] = 1;
+            if (mx + lsc > kGrow) sh->bad[wg][g & 3] = 1;
             group_arrive(gb);
           } else {
             // ---- move the reference of the rows that need it
@@ -1011,6 +1011,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
               fail = true;
               break;
             }
+            if (tid == 0) sh->bad[wg][(g + 2) & 3] = 0;   // as below
             if (tid < 16) {
               const float mm = order_float(sh->top[c0 + tid]);
               sh->top[c0 + tid] = float_order(-kInf);
@@ -1085,10 +1086,11 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
             fail = true;
             break;
           }
-          // (The other parity's word is cleared for the next tile: all warps
-          // have read it, as they have arrived here after reading it.)
-          move = *reinterpret_cast<volatile int*>(&sh->bad[wg][sb]) != 0;
-          if (tid == 0) sh->bad[wg][sb ^ 1] = 0;
+          // The word of two tiles on is cleared: it was last read two tiles
+          // ago, by warps that have arrived here since, and none writes it
+          // before this warp has arrived at the next tile.
+          move = *reinterpret_cast<volatile int*>(&sh->bad[wg][g & 3]) != 0;
+          if (tid == 0) sh->bad[wg][(g + 2) & 3] = 0;
           if (!move) break;
           tc_fence_after();
         }
@@ -1551,8 +1553,8 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
 #pragma unroll 1
         for (int x = 1; x < share; ++x) {              // in order: the result does not depend on timing
           const float2 mt = sh->join[warp + x];
+          if (mt.y == 0.f) continue;                   // no key with a weight
           const float nm = fmaxf(m.mx, mt.x);
-          if (nm == -kInf) continue;
           merge_scale(m, nm);
           const float w = mt.x == -kInf ? 0.f : ex2(mt.x - nm);
           m.tot = fmaf(w, mt.y, m.tot);
