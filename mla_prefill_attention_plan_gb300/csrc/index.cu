@@ -33,16 +33,6 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return r;
 }
 
-// Largest b with iro[b] <= t (t belongs to b when t < iro[b + 1]).
-__device__ __forceinline__ int sequence_of(const uint32_t* __restrict__ iro, int B, uint32_t t) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(iro + mid) <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // ============================================================ scores
 // Keys are the M side of the MMA (128 keys a tile) and the heads of a batch of
 // tokens the N side (K = 128), so a thread of the epilogue holds one key's
@@ -459,18 +449,22 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 // ============================================================ selection
 // A cluster of CTAs per token, each with a contiguous slice of the token's
 // block scores (kept in shared memory where it fits).  The k-th largest score
-// is found digit by digit (11, 11 and 10 bits of an order-preserving integer,
+// is found digit by digit (four of 8 bits of an order-preserving integer,
 // histograms summed over the cluster through distributed shared memory), then
 // the chosen blocks are written in position order: those above it, and as many
 // equal to it as are missing, lowest first.
+//
+// Bound by latency: a chain of barriers, and reads of other CTAs' counters.
+// Digits of 8 bits keep those few: with 2048 counters (three passes) a cluster
+// of eight spent 9000 clk of each pass on reading them.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelMaxCluster = 8;
+constexpr int kSelMaxCluster = 16;
 constexpr int kSelCacheFloats = 40 * 1024;           // slice kept in shared memory, 160 KB
 
 struct SelectSmem {
-  uint32_t hist[3][2048];
-  uint32_t scan[kSelWarps];
+  uint32_t hist[4][256];
+  uint32_t scan[8];
   uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
   uint32_t total[2];           // chosen-for-sure and equal blocks of this CTA
   uint32_t bin, need;
@@ -490,20 +484,29 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank)
 }
 
 __global__ void __launch_bounds__(kSelThreads)
-    index_select_kernel(const IndexSelectArgs a, int cached) {
+    index_select_kernel(const IndexSelectArgs a, const FastDiv page, int cached) {
   extern __shared__ __align__(16) uint32_t cache[];
   __shared__ SelectSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int t = blockIdx.x / C;
+  (&sh.hist[0][0])[tid] = 0u;
   pdl_enter();
+  // The token's sequence: the last b with iro[b] <= t, 1024 probes at a time.
+  int b = 0;
+  for (int end = a.B; end - b > 1;) {
+    const int step = (end - b + kSelThreads - 1) / kSelThreads;
+    const int x = static_cast<int>(min(static_cast<long long>(b) + static_cast<long long>(tid) * step, 0x7FFFFFFFll));
+    const int below = __syncthreads_count(x < end && __ldg(a.iro + x) <= static_cast<uint32_t>(t));
+    b += max(below - 1, 0) * step;
+    end = min(end, b + step);
+  }
   if (tid == 0) {
     int seq = -1, pos = 0;
     if (!timed_out_before(a.status)) {
-      const int b = sequence_of(a.iro, a.B, t);
-      const uint32_t qa = a.iro[b], qe = a.iro[b + 1];
+      const uint32_t qa = __ldg(a.iro + b), qe = __ldg(a.iro + b + 1), cached_tokens = __ldg(a.cache_len + b);
       if (qa <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < qe) {
-        const uint64_t ctx = static_cast<uint64_t>(a.cache_len[b]) + (static_cast<uint32_t>(t) - qa);
+        const uint64_t ctx = static_cast<uint64_t>(cached_tokens) + (static_cast<uint32_t>(t) - qa);
         if (ctx < static_cast<uint64_t>(a.max_seq) && qe <= static_cast<uint32_t>(a.T)) {
           seq = b;
           pos = static_cast<int>(ctx);
@@ -515,7 +518,6 @@ __global__ void __launch_bounds__(kSelThreads)
     sh.seq = seq;
     sh.pos = pos;
   }
-  for (int i = tid; i < 3 * 2048; i += kSelThreads) (&sh.hist[0][0])[i] = 0u;
   cluster_sync();
   // The token's sequence is read from CTA 0, so that all CTAs agree.
   const int seq = static_cast<int>(ld_cluster_u32(&sh.seq, 0)), pos = static_cast<int>(ld_cluster_u32(&sh.pos, 0));
@@ -530,134 +532,194 @@ __global__ void __launch_bounds__(kSelThreads)
   const float* src = a.scores + static_cast<long long>(t) * a.stride + lo;
   const int local_from = nb - a.local - lo;          // slice index of the first always-chosen block
   auto load = [&](int i) -> uint32_t { return i >= local_from ? 0xFFFFFFFFu : select_key(__ldg(src + i)); };
-  auto key = [&](int i) -> uint32_t { return cached ? cache[i] : load(i); };
+  // Keys i .. i + 3 (i is a multiple of 4); 0, below every key, past the slice.
+  auto quad = [&](int i, uint32_t (&u)[4]) {
+    if (cached) {
+      const uint4 v = *reinterpret_cast<const uint4*>(cache + i);
+      u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (i + x >= cnt) u[x] = 0u;
+      else if (!cached) u[x] = load(i + x);
+    }
+  };
 
+  if (cached || k < nb) {
+    // The first digit's counts, and the slice into shared memory.
+    constexpr int U = 4;                             // loads in flight
+    for (int i0 = tid; i0 < cnt; i0 += U * kSelThreads) {
+      uint32_t u[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) u[x] = i0 + x * kSelThreads < cnt ? load(i0 + x * kSelThreads) : 0u;
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        if (i0 + x * kSelThreads < cnt) {
+          if (cached) cache[i0 + x * kSelThreads] = u[x];
+          if (k < nb) atomicAdd(&sh.hist[0][u[x] >> 24], 1u);
+        }
+      }
+    }
+  }
   uint32_t thr = 0u, need = 0u;
   if (k < nb) {
     need = k;
     uint32_t mask = 0u;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
       uint32_t* hist = sh.hist[pass];
-#pragma unroll 4
-      for (int i = tid; i < cnt; i += kSelThreads) {
-        uint32_t u;
-        if (pass == 0) {
-          u = load(i);
-          if (cached) cache[i] = u;
-        } else {
-          u = key(i);
-        }
-        if ((u & mask) == thr) atomicAdd(&hist[(u >> shift) & digits], 1u);
-      }
-      cluster_sync();
-      // Two digits a thread, from the largest down: the cluster's counts and
-      // how many keys have a larger digit.
-      const int d0 = 2047 - 2 * tid;
-      uint32_t c0 = 0, c1 = 0;
-      for (uint32_t r = 0; r < C; ++r) {
-        c0 += ld_cluster_u32(hist + d0, r);
-        c1 += ld_cluster_u32(hist + d0 - 1, r);
-      }
-      uint32_t incl = c0 + c1;
+      if (pass > 0)
+        for (int i = 4 * tid; i < cnt; i += 4 * kSelThreads) {
+          uint32_t u[4];
+          quad(i, u);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - c0 - c1;
-      for (int w = 0; w < warp; ++w) before += sh.scan[w];
-      if (before < need && need <= before + c0) {
-        sh.bin = d0;
-        sh.need = need - before;
-      } else if (before + c0 < need && need <= before + c0 + c1) {
-        sh.bin = d0 - 1;
-        sh.need = need - before - c0;
+          for (int x = 0; x < 4; ++x)
+            if (i + x < cnt && (u[x] & mask) == thr) atomicAdd(&hist[(u[x] >> shift) & 255u], 1u);
+        }
+      cluster_sync();
+      // A digit a thread, from the largest down: the cluster's count of it and
+      // how many keys have a larger one.
+      uint32_t c = 0, before = 0;
+      if (tid < 256) {
+        uint32_t v[kSelMaxCluster];
+#pragma unroll
+        for (uint32_t r = 0; r < kSelMaxCluster; ++r) {
+          v[r] = 0;
+          if (r < C) v[r] = ld_cluster_u32(hist + 255 - tid, r);
+        }
+#pragma unroll
+        for (uint32_t r = 0; r < kSelMaxCluster; ++r) c += v[r];
+        uint32_t incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        if (lane == 31) sh.scan[warp] = incl;
+        before = incl - c;
+        asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+#pragma unroll
+        for (int w = 0; w < 8; ++w) before += w < warp ? sh.scan[w] : 0u;
+        if (before < need && need <= before + c) {
+          sh.bin = 255 - tid;
+          sh.need = need - before;
+        }
       }
       __syncthreads();
       thr |= sh.bin << shift;
       need = sh.need;
-      mask |= digits << shift;
-      __syncthreads();   // bin, need and scan are rewritten by the next pass
+      mask |= 255u << shift;
     }
-  } else if (cached) {
-    for (int i = tid; i < cnt; i += kSelThreads) cache[i] = load(i);
-    __syncthreads();
+  } else {
+    __syncthreads();                                 // the slice is in shared memory
   }
 
   // Chosen and equal blocks before each warp's part of the slice.
-  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
   const int s0 = min(cnt, warp * seg), s1 = min(cnt, s0 + seg);
   uint32_t gt = 0, eq = 0;
-  for (int i = s0; i < s1; i += 32) {
-    const uint32_t u = i + lane < s1 ? key(i + lane) : 0u;
-    const bool in = i + lane < s1;
-    gt += __popc(__ballot_sync(0xffffffffu, in && u > thr));
-    eq += __popc(__ballot_sync(0xffffffffu, in && u == thr));
+  for (int i = s0 + 4 * lane; i < s1; i += 128) {
+    uint32_t u[4];
+    quad(i, u);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      gt += i + x < cnt && u[x] > thr ? 1u : 0u;
+      eq += i + x < cnt && u[x] == thr ? 1u : 0u;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     sh.warp_gt[warp] = gt;
     sh.warp_eq[warp] = eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t x = 0, y = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      x += sh.warp_gt[w];
-      y += sh.warp_eq[w];
+  gt = sh.warp_gt[lane];
+  eq = sh.warp_eq[lane];
+  if (warp == 0) {
+    const uint32_t x = __reduce_add_sync(0xffffffffu, gt), y = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      sh.total[0] = x;
+      sh.total[1] = y;
     }
-    sh.total[0] = x;
-    sh.total[1] = y;
   }
+  gt = __reduce_add_sync(0xffffffffu, lane < warp ? gt : 0u);
+  eq = __reduce_add_sync(0xffffffffu, lane < warp ? eq : 0u);
   cluster_sync();
-  gt = eq = 0;
-  for (uint32_t r = 0; r < rank; ++r) {
-    gt += ld_cluster_u32(&sh.total[0], r);
-    eq += ld_cluster_u32(&sh.total[1], r);
-  }
-  for (int w = 0; w < warp; ++w) {
-    gt += sh.warp_gt[w];
-    eq += sh.warp_eq[w];
+  {
+    const bool other = lane < static_cast<int>(rank);
+    const uint32_t x = other ? ld_cluster_u32(&sh.total[0], lane) : 0u, y = other ? ld_cluster_u32(&sh.total[1], lane) : 0u;
+    gt += __reduce_add_sync(0xffffffffu, x);
+    eq += __reduce_add_sync(0xffffffffu, y);
   }
 
   int32_t* out = a.rows + static_cast<long long>(t) * a.rows_stride;
   const int32_t* table = a.page_table + static_cast<long long>(seq) * a.max_pages;
-  auto row_of = [&](int x) -> int32_t {
-    const int pi = x / a.page_size;
-    const int page = pi < a.max_pages ? __ldg(table + pi) : -1;
-    if (page >= 0 && page < a.num_pages) return page * a.page_size + (x - pi * a.page_size);
+  auto entry_of = [&](int pi) -> int { return pi < a.max_pages ? __ldg(table + pi) : -1; };
+  auto row_of = [&](int x, int pi, int entry) -> int32_t {
+    if (entry >= 0 && entry < a.num_pages) return entry * page.d + (x - pi * page.d);
     set_status(a.status, MLA_DEV_BAD_PAGE);
     return -1;
   };
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i = s0; i < s1; i += 32) {
-    const bool in = i + lane < s1;
-    const uint32_t u = in ? key(i + lane) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, in && u > thr), me = __ballot_sync(0xffffffffu, in && u == thr);
-    const uint32_t my_eq = eq + __popc(me & below);
-    const bool chosen = in && (u > thr || (u == thr && my_eq < need));
-    const uint32_t at = gt + __popc(mg & below) + min(my_eq, need);   // chosen blocks before
-    if (a.block == 1) {
-      if (chosen) out[at] = row_of(lo + i + lane);
-    } else {
-      uint32_t todo = __ballot_sync(0xffffffffu, chosen);
-      while (todo) {
-        const int from = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const long long o = static_cast<long long>(__shfl_sync(0xffffffffu, at, from)) * a.block;
-        const int first = (lo + i + from) * a.block;
-        for (int r = lane; r < a.block; r += 32) out[o + r] = first + r <= pos ? row_of(first + r) : -1;
-      }
+  // Single keys: the page id of a lane's first key is read an iteration ahead.
+  int pi_next = 0, entry_next = -1;
+  auto ahead = [&](int i) {
+    if (a.block == 1 && i < s1) {
+      pi_next = fast_div(lo + i, page);
+      entry_next = entry_of(pi_next);
     }
-    // The last visible block may be cut by the token's position.
-    if (in && lo + i + lane == nb - 1)
-      a.count[t] = chosen ? (k - 1) * a.block + pos % a.block + 1 : k * a.block;
-    gt += __popc(mg);
-    eq += __popc(me);
+  };
+  ahead(s0 + 4 * lane);
+#pragma unroll 1
+  for (int i0 = s0; i0 < s1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const int pi0 = pi_next, entry0 = entry_next;
+    ahead(i + 128);
+    uint32_t u[4];
+    quad(i, u);
+    uint32_t mine = 0;                               // above, and equal << 16
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x < cnt) mine += u[x] > thr ? 1u : (u[x] == thr ? 0x10000u : 0u);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    uint32_t g = gt + ((incl - mine) & 0xFFFFu), e = eq + ((incl - mine) >> 16);
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool in = i + x < cnt, above = in && u[x] > thr, equal = in && u[x] == thr;
+      const bool chosen = above || (equal && e < need);
+      const uint32_t at = g + min(e, need);          // chosen blocks before
+      g += above ? 1 : 0;
+      e += equal ? 1 : 0;
+      if (a.block == 1) {
+        if (chosen) {
+          const int key = lo + i + x, pi = x == 0 ? pi0 : fast_div(key, page);
+          out[at] = row_of(key, pi, pi == pi0 ? entry0 : entry_of(pi));
+        }
+      } else {
+        uint32_t todo = __ballot_sync(0xffffffffu, chosen);
+        while (todo) {
+          const int from = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const long long o = static_cast<long long>(__shfl_sync(0xffffffffu, at, from)) * a.block;
+          const int first = (lo + i0 + 4 * from + x) * a.block;
+          for (int r = lane; r < a.block; r += 32) {
+            const int key = first + r, pi = fast_div(key, page);
+            out[o + r] = key <= pos ? row_of(key, pi, entry_of(pi)) : -1;
+          }
+        }
+      }
+      // The last visible block may be cut by the token's position.
+      if (in && lo + i + x == nb - 1) a.count[t] = chosen ? (k - 1) * a.block + pos % a.block + 1 : k * a.block;
+    }
+    gt += all & 0xFFFFu;
+    eq += all >> 16;
   }
   for (long long x = static_cast<long long>(k) * a.block + rank * kSelThreads + tid; x < a.rows_stride; x += C * kSelThreads)
     out[x] = -1;
@@ -739,30 +801,45 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
 cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   // One CTA a token, or, where the tokens leave SMs idle and the rows are
-  // long, up to eight (at least 4096 scores each).
+  // long, up to 16 (at least 4096 scores each): two tokens of 131000 scores
+  // take 22 us with eight and 19 with 16.
   int C = 1;
   while (C < kSelMaxCluster && static_cast<long long>(a.T) * 2 * C <= sm_count() && a.stride / (2 * C) >= 4096) C *= 2;
-  const long long slice = ((static_cast<long long>(a.stride) + C - 1) / C + 31) / 32 * 32;
-  const int cached = slice <= kSelCacheFloats ? 1 : 0;
-  const size_t smem = cached ? static_cast<size_t>(slice) * 4 : 16;
   cudaError_t e = cudaFuncSetAttribute(index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSelCacheFloats * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(C) * static_cast<unsigned>(a.T));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
   cfg.attrs = attr;
+  auto shape = [&] {
+    const long long slice = ((static_cast<long long>(a.stride) + C - 1) / C + 31) / 32 * 32;
+    cfg.dynamicSmemBytes = slice <= kSelCacheFloats ? static_cast<size_t>(slice) * 4 : 16;
+    cfg.gridDim = dim3(static_cast<unsigned>(C) * static_cast<unsigned>(a.T));
+    attr[0].val.clusterDim.x = C;
+    return slice <= kSelCacheFloats ? 1 : 0;
+  };
+  int cached = shape();
+  if (C == 16) {
+    // Above the portable size; a device (or the part of one) that cannot place
+    // such a cluster gets eight CTAs.
+    e = cudaFuncSetAttribute(index_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&fit, index_select_kernel, &cfg) != cudaSuccess || fit < 1) {
+      cudaGetLastError();
+      C = 8;
+      cached = shape();
+    }
+  }
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, index_select_kernel, a, cached);
+  return cudaLaunchKernelEx(&cfg, index_select_kernel, a, fast_divisor(a.page_size), cached);
 }
 
 }  // namespace mla
