@@ -129,8 +129,10 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
 // writes that block's new rows (one warp a row): first their largest value,
 // then, with the scale known, the codes (the rows are read again, from L1).
 // HBM-bound: per token 1152 bytes of latent read, 576 written, 256 of
-// frequencies, and 4 * 64 * H of queries read and written.
-__global__ void __launch_bounds__(kWriteThreads)
+// frequencies, and 4 * 64 * H of queries read and written.  A thread's first
+// four query pieces (all of them with 128 heads) are read before anything is
+// known of the token, over the chain of reads that finds its position.
+__global__ void __launch_bounds__(kWriteThreads, 3)
     cache_write_q8_kernel(const CacheWriteQ8Args a) {
   __shared__ float s_amax[kWriteWarps];
   __shared__ int s_info[3];   // position (-1: skip), rows to write as leader, first slot of the block
@@ -141,44 +143,61 @@ __global__ void __launch_bounds__(kWriteThreads)
   const uint16_t* latent = static_cast<const uint16_t*>(a.kv_latent);
   uint8_t* cache = static_cast<uint8_t*>(a.kv_cache);
 
+  constexpr int QU = 4;       // query pieces of a thread in flight
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (tid == 0) {
-      int lo = 0, hi = a.B;   // largest b with iro[b] <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.iro[mid] <= static_cast<uint32_t>(t)) lo = mid; else hi = mid;
+    // q: piece m of head h holds rope values 8m .. 8m+7 (pairs 4m .. 4m+3).
+    uint16_t* qt = static_cast<uint16_t*>(a.q) + static_cast<size_t>(t) * a.H * 192 + 128 + 8 * (tid & 7);
+    const int pieces = a.q != nullptr ? 8 * a.H : 0;
+    auto piece = [&](int i) { return reinterpret_cast<uint4*>(qt + static_cast<size_t>(i >> 3) * 192); };
+    uint4 x[QU];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < QU; ++k)
+        if (i0 + k * kWriteThreads < pieces) x[k] = *piece(i0 + k * kWriteThreads);
+    };
+    load(tid);
+    if (warp == 0) {
+      int lo = 0;             // largest b with iro[b] <= t, 32 probes at a time
+      for (int hi = a.B; hi - lo > 1;) {
+        const int step = (hi - lo + 31) / 32;
+        const long long at = lo + static_cast<long long>(tid) * step;
+        const int below = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(a.iro + at) <= static_cast<uint32_t>(t)));
+        lo += max(below - 1, 0) * step;
+        hi = min(hi, lo + step);
       }
-      const uint32_t first = a.iro[lo], end = a.iro[lo + 1];
-      int pos = -1, rows = 0, slot = 0;
-      long long row = -1;
-      if (first <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < end) {
-        const uint64_t p = static_cast<uint64_t>(a.cache_len[lo]) + (static_cast<uint32_t>(t) - first);
-        if (p < static_cast<uint64_t>(a.max_seq_len)) {
-          pos = static_cast<int>(p);
-          slot = pos % a.scale_block;
-          if (slot == 0 || static_cast<uint32_t>(t) == first) {
-            // This block's new rows: up to its end, the sequence's last new
-            // token, the last row of the call and the last position.
-            rows = a.scale_block - slot;
-            rows = static_cast<int>(min(static_cast<uint32_t>(rows), min(end, static_cast<uint32_t>(a.T)) - t));
-            rows = min(rows, a.max_seq_len - pos);
-            const int pidx = pos / a.page_size;
-            const int page = pidx < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + pidx] : -1;
-            if (page >= 0 && page < a.num_pages)
-              row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
-            else
-              set_status(a.status, MLA_DEV_BAD_PAGE);
+      if (tid == 0) {
+        const uint32_t first = a.iro[lo], end = a.iro[lo + 1];
+        int pos = -1, rows = 0, slot = 0;
+        long long row = -1;
+        if (first <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < end) {
+          const uint64_t p = static_cast<uint64_t>(a.cache_len[lo]) + (static_cast<uint32_t>(t) - first);
+          if (p < static_cast<uint64_t>(a.max_seq_len)) {
+            pos = static_cast<int>(p);
+            slot = pos % a.scale_block;
+            if (slot == 0 || static_cast<uint32_t>(t) == first) {
+              // This block's new rows: up to its end, the sequence's last new
+              // token, the last row of the call and the last position.
+              rows = a.scale_block - slot;
+              rows = static_cast<int>(min(static_cast<uint32_t>(rows), min(end, static_cast<uint32_t>(a.T)) - t));
+              rows = min(rows, a.max_seq_len - pos);
+              const int pidx = pos / a.page_size;
+              const int page = pidx < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + pidx] : -1;
+              if (page >= 0 && page < a.num_pages)
+                row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+              else
+                set_status(a.status, MLA_DEV_BAD_PAGE);
+            }
+          } else {
+            set_status(a.status, MLA_DEV_BAD_OFFSETS);
           }
         } else {
           set_status(a.status, MLA_DEV_BAD_OFFSETS);
         }
-      } else {
-        set_status(a.status, MLA_DEV_BAD_OFFSETS);
+        s_info[0] = pos;
+        s_info[1] = row >= 0 ? rows : 0;
+        s_info[2] = slot;
+        s_row = row;
       }
-      s_info[0] = pos;
-      s_info[1] = row >= 0 ? rows : 0;
-      s_info[2] = slot;
-      s_row = row;
     }
     __syncthreads();
     const int pos = s_info[0], rows = s_info[1], slot = s_info[2];
@@ -223,20 +242,24 @@ __global__ void __launch_bounds__(kWriteThreads)
         store_row(cache + static_cast<size_t>(row0 + r) * 576, v, inv);
       }
     }
-    // q: piece m of head h holds rope values 8m .. 8m+7 (pairs 4m .. 4m+3).
-    if (a.q != nullptr && pos >= 0) {
-      const float4* fr = reinterpret_cast<const float4*>(a.freqs + static_cast<size_t>(pos) * 64);
-      uint16_t* qt = static_cast<uint16_t*>(a.q) + static_cast<size_t>(t) * a.H * 192 + 128;
-      for (int i = tid; i < 8 * a.H; i += kWriteThreads) {
-        const int h = i >> 3, m = i & 7;
-        uint4* pq = reinterpret_cast<uint4*>(qt + static_cast<size_t>(h) * 192) + m;
-        const uint4 x = *pq;
-        const float4 fa = __ldg(fr + 2 * m), fb = __ldg(fr + 2 * m + 1);
-        const float2 a0 = rotate2(bf16_lo(x.x), bf16_hi(x.x), fa.x, fa.y);
-        const float2 a1 = rotate2(bf16_lo(x.y), bf16_hi(x.y), fa.z, fa.w);
-        const float2 a2 = rotate2(bf16_lo(x.z), bf16_hi(x.z), fb.x, fb.y);
-        const float2 a3 = rotate2(bf16_lo(x.w), bf16_hi(x.w), fb.z, fb.w);
-        *pq = make_uint4(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y), pack_bf16(a2.x, a2.y), pack_bf16(a3.x, a3.y));
+    if (pos >= 0 && pieces > 0) {
+      const float4* fr = reinterpret_cast<const float4*>(a.freqs + static_cast<size_t>(pos) * 64) + 2 * (tid & 7);
+      const float4 fa = __ldg(fr), fb = __ldg(fr + 1);
+      for (int i0 = tid;;) {
+#pragma unroll
+        for (int k = 0; k < QU; ++k) {
+          if (i0 + k * kWriteThreads < pieces) {
+            const float2 a0 = rotate2(bf16_lo(x[k].x), bf16_hi(x[k].x), fa.x, fa.y);
+            const float2 a1 = rotate2(bf16_lo(x[k].y), bf16_hi(x[k].y), fa.z, fa.w);
+            const float2 a2 = rotate2(bf16_lo(x[k].z), bf16_hi(x[k].z), fb.x, fb.y);
+            const float2 a3 = rotate2(bf16_lo(x[k].w), bf16_hi(x[k].w), fb.z, fb.w);
+            *piece(i0 + k * kWriteThreads) =
+                make_uint4(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y), pack_bf16(a2.x, a2.y), pack_bf16(a3.x, a3.y));
+          }
+        }
+        i0 += QU * kWriteThreads;
+        if (i0 >= pieces) break;
+        load(i0);
       }
     }
     __syncthreads();   // the shared words are rewritten for the next token
