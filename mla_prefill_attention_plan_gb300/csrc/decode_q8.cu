@@ -65,6 +65,23 @@ struct PlanArgs {
 };
 constexpr int BK = 128;                     // keys of a tile
 
+// Position of the last of n ascending numbers, `step` ints apart, that is not
+// above x (0 if none): 32 probes of a warp at a time.
+__device__ __forceinline__ int last_not_above(const int* at, int step, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+#pragma unroll 1
+  for (int hi = n; hi - lo > 1;) {
+    const int d = (hi - lo + 31) / 32;
+    const long long i = lo + static_cast<long long>(lane) * d;
+    const int below = __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(at + i * step) <= x));
+    lo += max(below - 1, 0) * d;
+    hi = min(hi, lo + d);
+  }
+  return lo;
+}
+constexpr int kEntryInts = sizeof(PlanEntry) / 4;
+
 // The plan, by 128 threads (tid) of one CTA: scans over the sequences, 128 at
 // a time.  A sequence is left out if it is empty, ends past the call's tokens,
 // begins before an earlier one ends, or (dense) is longer than max_seq; all but
@@ -176,7 +193,8 @@ __device__ void q8_plan(const PlanArgs& a, int tid, int (*scr)[4]) {
 constexpr int kQThreads = 320;                    // TMA, MMA, 8 epilogue warps
 constexpr int Q_A = 128 * 128;                    // 128 rows of 64 bf16
 constexpr int Q_B = 256 * 128;
-constexpr int Q_SMEM_BAR = 2 * (Q_A + Q_B);       // two 64-column blocks of A and of B
+constexpr int Q_SMEM_BAR = 2 * (Q_A + Q_B);       // two 64-column blocks of A and of B; then the results
+constexpr int Q_OUT = 128 * 128;                  // 128 rows of 128 bytes: [term][half] of codes, the rope part
 constexpr int Q_SMEM_TOTAL = Q_SMEM_BAR + 2048 + 1024;
 
 struct QuerySmem {
@@ -198,6 +216,7 @@ __device__ __forceinline__ void two_terms(const float (&v)[4], uint32_t& hi, uin
 
 __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
     q8_query_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                    const __grid_constant__ CUtensorMap o_map,
                     const uint16_t* __restrict__ q, uint8_t* __restrict__ q8, float* __restrict__ q_scale, int T,
                     int H, int32_t* status, const PlanArgs plan) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -205,9 +224,18 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
   QuerySmem* sh = reinterpret_cast<QuerySmem*>(smem + Q_SMEM_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int h = blockIdx.y >> 1;
+  const int h = static_cast<int>(blockIdx.y >> 1) - 1;
   const int m0 = blockIdx.x * 128;
+  if (threadIdx.x == 0 && h >= 0) {                // w_uk on its way while the kernel before ends
+    tma_prefetch_2d(&b_map, 0, h * 512 + rank * 256);
+    tma_prefetch_2d(&b_map, 64, h * 512 + rank * 256);
+  }
   pdl_enter();
+  if (h < 0) {                                     // the first clusters: one CTA of them writes the plan
+    if (blockIdx.x == 0 && rank == 0 && threadIdx.x < 128 && !timed_out_before(status))
+      q8_plan(plan, threadIdx.x, sh->scr);
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh->full[0]), 1);
     mbar_init(smem_u32(&sh->full[1]), 1);
@@ -265,10 +293,26 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
     }
     __syncwarp();
   } else if (work) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && half == 0) q8_plan(plan, threadIdx.x - 64, sh->scr);
+    // The rope part is read while the operands load, and kept in shared memory
+    // as soon as the MMAs do not need that any more.
+    uint4 rv[8];
+    if (rank == 1 && half == 1) {
+      const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rv[i] = t < T ? __ldg(rp + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
     ok = mbar_wait_warp(smem_u32(&sh->done), 0, status, abort_flag);
     if (ok) {
       tc_fence_after();
+      if (rank == 1 && half == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t u[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf16_lo(u[k])), fabsf(bf16_hi(u[k]))));
+          *reinterpret_cast<uint4*>(smem + 4 * Q_OUT + row * 128 + ((i ^ (row & 7)) << 4)) = rv[i];
+        }
+      }
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
@@ -276,16 +320,6 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) am = fmaxf(am, fabsf(__uint_as_float(x[i])));
-      }
-      if (rank == 1 && half == 1 && t < T) {
-        const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = __ldg(rp + i);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf16_lo(u[k])), fabsf(bf16_hi(u[k]))));
-        }
       }
       sh->amax[half][row] = am;
     }
@@ -307,9 +341,11 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
     const float inv = 1.0f / s;
     // An infinite query has no scale: its scores become NaN.
     if (rank == 0 && half == 0 && t < T) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);
-    uint8_t* dst = q8 + grow * 1152 + rank * 256 + half * 128;
     // The results once more from TMEM, 32 columns at a time (few registers, so
-    // that two of these CTAs share an SM).
+    // that two of these CTAs share an SM), and through shared memory (the
+    // operands are not needed any more) to a bulk store: a row of the result
+    // is H * 1152 bytes on, and 16 bytes of 32 rows at a time took 32 passes.
+    uint8_t* dst = smem + half * Q_OUT + row * 128;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t x[32];
@@ -325,27 +361,37 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
           for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(x[16 * i + 4 * k + y]) * inv;
           two_terms(v, hi[k], lo[k]);
         }
-        if (t < T) {
-          reinterpret_cast<uint4*>(dst)[2 * c + i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          reinterpret_cast<uint4*>(dst + 576)[2 * c + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        uint8_t* at = dst + (((2 * c + i) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + 2 * Q_OUT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+    }
+    fence_async_smem();
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");   // the half's four warps
+    if (threadIdx.x == 64 + 128 * half) {
+#pragma unroll
+      for (int term = 0; term < 2; ++term)         // (rows past the last token are clipped)
+        tma_store_2d(&o_map, smem_u32(smem + (2 * term + half) * Q_OUT), h * 1152 + term * 576 + rank * 256 + half * 128, m0);
+      bulk_commit();
     }
     if (rank == 1 && half == 1 && t < T) {
-      const uint4* rp = reinterpret_cast<const uint4*>(q + grow * 192 + 128);
-      uint2* dr = reinterpret_cast<uint2*>(q8 + grow * 1152 + 512);
+      uint4* dr = reinterpret_cast<uint4*>(q8 + grow * 1152 + 512);
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint4 v = __ldg(rp + i);
-        const float a[4] = {bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv, bf16_hi(v.y) * inv};
-        const float b[4] = {bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv, bf16_hi(v.w) * inv};
-        uint2 hi, lo;
-        two_terms(a, hi.x, lo.x);
-        two_terms(b, hi.y, lo.y);
-        dr[i] = hi;
-        dr[72 + i] = lo;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + 4 * Q_OUT + row * 128 + (((2 * i + k) ^ (row & 7)) << 4));
+          const float a[4] = {bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv, bf16_hi(v.y) * inv};
+          const float b[4] = {bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv, bf16_hi(v.w) * inv};
+          two_terms(a, hi[2 * k], lo[2 * k]);
+          two_terms(b, hi[2 * k + 1], lo[2 * k + 1]);
+        }
+        dr[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        dr[36 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
+    if (threadIdx.x == 64 + 128 * half) bulk_wait<0>();
   }
   cluster_sync();   // no CTA leaves while another may read its row maxima
   if (warp == 1) {
@@ -491,11 +537,7 @@ __device__ __forceinline__ Walk walk_begin(const Q8Params& p, int piece) {
   w.u1 = piece_begin(piece + 1, pieces, units);
   // Last entry with units <= u that has any (a search over ascending numbers;
   // entries without units share the next one's number and come before it).
-  int lo = 0, hi = entries;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(&p.entries[mid].units) <= w.u) lo = mid; else hi = mid;
-  }
+  const int lo = last_not_above(&p.entries[0].units, kEntryInts, entries, w.u);
   w.e = lo;
   w.pe = load_entry(p.entries + lo);
   w.end = __ldg(&p.entries[lo + 1].units);
@@ -1344,18 +1386,22 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 // One CTA per (head, up to NT tokens): the segments' latent results are merged
 // by LSE in fp32 (with the attention sink in the denominator), split into two
 // bf16 terms (their sum within 2^-16) and multiplied by w_uv[h]: D^T [128
-// values, NT tokens] = w_uv[h] [128, 512] . o^T, so that few tokens make a small
-// N.  Reads w_uv[h] once per CTA; its load starts before the attention has
-// ended.  16 warps: with few tokens several of them share one token's segments
-// (a single long sequence has one for every SM) and join through shared memory.
+// values, 2 NT] = w_uv[h] [128, 512] . o^T, both terms of NT tokens side by
+// side, so that few tokens make a small N.  w_uv[h] is loaded once per CTA,
+// from before the attention has ended.  16 warps: with few tokens several of
+// them share one token's segments (a single long sequence has one for every SM)
+// and join through shared memory.
+//
+// The whole of w_uv[h] waits in shared memory: with a ring of two of its blocks
+// and two CTAs an SM, the blocks' latencies one after another took 10000 clk.
 constexpr int kOutWarps = 16;
+constexpr int W_BLOCK = 128 * 128;                   // 128 rows of 64 bf16
 
 template <int NT>
 struct OutShape {
-  static constexpr int W = 8 * 16384;                // w_uv[h], eight 64-column blocks
-  static constexpr int TERM = 8 * NT * 128;
-  static constexpr int AT_O = W;
-  static constexpr int AT_JOIN = AT_O + 2 * TERM;    // [warp][512] partial sums, where warps share a token
+  static constexpr int O_BLOCK = 2 * NT * 128;       // 64 columns of both terms
+  static constexpr int AT_O = 8 * W_BLOCK;
+  static constexpr int AT_JOIN = AT_O + 8 * O_BLOCK; // [warp][512] partial sums, where warps share a token
   static constexpr int AT_BAR = AT_JOIN + (NT == 16 ? kOutWarps * 2048 : 0);
   static constexpr int TOTAL = AT_BAR + 1024 + 1024;
   static_assert(TOTAL <= 227 * 1024, "shared memory");
@@ -1365,7 +1411,7 @@ struct OutSmem {
   uint32_t tmem;
   int abort;
   int used[32];      // segments that hold keys of the token; -1: its rows are not written
-  int first[32];     // row of the first one's results (in slots), the others `step` apart
+  long long first[32];   // row of the first one's results (in slots), the others `step` apart
   float sink[32];    // log2 units
   float2 join[kOutWarps];   // a warp's maximum and sum
 };
@@ -1385,8 +1431,9 @@ __device__ __forceinline__ void merge_scale(Merge& m, float nm) {
 
 template <int NT>
 __global__ void __launch_bounds__(32 * kOutWarps, 1)
-    q8_out_kernel(const __grid_constant__ CUtensorMap w_map, const Q8Params p, const float* __restrict__ sink,
-                  __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T, int rows, int tokens) {
+    q8_out_kernel(const __grid_constant__ CUtensorMap w_map, const Q8Params p, const FastDiv item_rows,
+                  const float* __restrict__ sink, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T,
+                  int tokens) {
   using C = OutShape<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1403,54 +1450,47 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
     // had completed when that kernel let this one start (it waits for its own
     // predecessor first).
     const uint32_t full = smem_u32(&sh->full);
-    mbar_expect_tx(full, C::W);
+    mbar_expect_tx(full, 8 * W_BLOCK);
 #pragma unroll 1
-    for (int kb = 0; kb < 8; ++kb) tma_load_2d(smem_u32(smem + kb * 16384), &w_map, full, kb * 64, h * 128);
+    for (int kb = 0; kb < 8; ++kb) tma_load_2d(smem_u32(smem + kb * W_BLOCK), &w_map, full, kb * 64, h * 128);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sh->tmem), 32);
+    tmem_alloc(smem_u32(&sh->tmem), 2 * NT);
     tmem_relinquish();
   }
   pdl_enter();
-  const bool dead = timed_out_before(p.status);
-  if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {
-    const int i = threadIdx.x - 64, t = t0 + i;
-    int used = -1, first = 0;
+  const bool dead = __any_sync(0xffffffffu, timed_out_before(p.status));   // no work, and no plan to read
+  const int entries = dead ? 0 : __ldg(&p.head->entries), units = dead ? 0 : __ldg(&p.head->units);
+  const long long step = item_rows.d;                // slots between a token's segments
+  // A token, looked up by a warp.
+  auto look_up = [&](int i) {
+    const int t = t0 + i;
+    int used = -1;
+    long long first = 0;
     float sk = -kInf;
-    if (i < n && !dead) {
-      const int entries = __ldg(&p.head->entries), units = __ldg(&p.head->units);
-      int lo = 0, hi = entries;   // last entry with qa <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(&p.entries[mid].qa) <= t) lo = mid; else hi = mid;
-      }
-      if (entries > 0) {
-        const PlanEntry e = load_entry(p.entries + lo);
-        if (e.qa <= t && t < e.qa + e.n) {
-          const int keys = p.indices != nullptr ? e.L : min(e.L, e.cb + (t - e.qa) + 1);
-          const long long r = static_cast<long long>(t - e.qa) * p.H + h;
-          const int item = static_cast<int>(r / (p.members * rows)), in = static_cast<int>(r % (p.members * rows));
-          used = 0;
-          if (keys > 0) {
-            const int u = e.units + item * e.tiles;
-            const int pieces = min(p.pieces, units), g0 = piece_of(u, pieces, units);
-            used = piece_of(u + (keys + BK - 1) / BK - 1, pieces, units) - g0 + 1;
-            first = (g0 + e.items + item) * p.members * rows + in;
-          }
-          if (sink != nullptr) sk = __ldg(sink + e.b) * 1.4426950408889634f;
+    if (entries > 0) {
+      const int e_at = last_not_above(&p.entries[0].qa, kEntryInts, entries, t);
+      const PlanEntry e = load_entry(p.entries + e_at);
+      if (e.qa <= t && t < e.qa + e.n) {
+        const int keys = p.indices != nullptr ? e.L : min(e.L, e.cb + (t - e.qa) + 1);
+        const int r = (t - e.qa) * p.H + h;
+        const int item = fast_div(r, item_rows);
+        used = 0;
+        if (keys > 0) {
+          const int u = e.units + item * e.tiles;
+          const int pieces = min(p.pieces, units), g0 = piece_of(u, pieces, units);
+          used = piece_of(u + (keys + BK - 1) / BK - 1, pieces, units) - g0 + 1;
+          first = static_cast<long long>(g0 + e.items + item) * item_rows.d + (r - item * item_rows.d);
         }
+        if (sink != nullptr) sk = __ldg(sink + e.b) * 1.4426950408889634f;
       }
     }
-    sh->first[i] = first;
-    sh->used[i] = used;
-    sh->sink[i] = sk;
-  }
-  tc_fence_before();
-  const bool stop = __syncthreads_or(dead ? 1 : 0) != 0;   // an earlier kernel timed out: no work
-  tc_fence_after();
-  const uint32_t tmem = sh->tmem;
-  volatile int never = 0;
-  const long long step = static_cast<long long>(p.members) * rows;
+    if (lane == 0) {
+      sh->used[i] = used;
+      sh->first[i] = first;
+      sh->sink[i] = sk;
+    }
+  };
   // Warps of a token: a power of two, so that they divide the 16.
   int share = 1;
   while (NT == 16 && 2 * share * n <= kOutWarps) share *= 2;
@@ -1502,9 +1542,9 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
   // +7, that is block of 64 columns lane / 8 (+ 4), 16-byte chunk lane & 7.
   auto finish = [&](int i) {
     const int used = sh->used[i];
+    const float sk = sh->sink[i];
     float l2 = m.tot == 0.f ? -kInf : m.mx + __log2f(m.tot);
     float w = m.tot == 0.f ? 0.f : 1.0f / m.tot;
-    const float sk = sh->sink[i];
     if (sink != nullptr && used >= 0) {
       // The sink is one more logit without a value: LSE' = log(e^LSE + e^sink).
       const float top = fmaxf(l2, sk);
@@ -1525,23 +1565,21 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
         hi[e] = pack_bf16(x, y);
         lo[e] = pack_bf16(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
       }
-      const int kb = half * 4 + (lane >> 3);
-      uint8_t* dst = smem + C::AT_O + kb * NT * 128 + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+      uint8_t* dst = smem + C::AT_O + (half * 4 + (lane >> 3)) * C::O_BLOCK + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
       *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(dst + C::TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(dst + NT * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   };
-  if (!stop) {
-    // (Operand rows past the last token hold anything: their results are not stored.)
-    if (share == 1) {
+  // (Operand rows past the last token hold anything: their results are not stored.)
+  // (The code of a step is there once, in loops: fetching unrolled copies takes
+  // longer than the chains of reads that they would overlap.)
 #pragma unroll 1
-      for (int i = warp; i < n; i += kOutWarps) {
-        gather(i);
-        finish(i);
-      }
-    } else {
-      const int i = warp / share;
-      if (i < n) gather(i);
+  for (int i = warp / share; i < n; i += kOutWarps / share) look_up(i);
+  __syncwarp();
+#pragma unroll 1
+  for (int i = warp / share;; i += kOutWarps) {
+    if (i < n) gather(i);
+    if (share > 1) {                                   // one turn: share * n <= 16
       float* join = reinterpret_cast<float*>(smem + C::AT_JOIN) + warp * 512;
       if (i < n && part > 0) {
 #pragma unroll
@@ -1554,35 +1592,35 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
         for (int x = 1; x < share; ++x) {              // in order: the result does not depend on timing
           const float2 mt = sh->join[warp + x];
           if (mt.y == 0.f) continue;                   // no key with a weight
-          const float nm = fmaxf(m.mx, mt.x);
-          merge_scale(m, nm);
-          const float w = mt.x == -kInf ? 0.f : ex2(mt.x - nm);
+          merge_scale(m, fmaxf(m.mx, mt.x));
+          const float w = mt.x == -kInf ? 0.f : ex2(mt.x - m.mx);
           m.tot = fmaf(w, mt.y, m.tot);
 #pragma unroll
           for (int e = 0; e < 16; ++e) m.o[e] = fmaf(w, join[x * 512 + e * 32 + lane], m.o[e]);
         }
-        finish(i);
       }
     }
+    if (i < n && part == 0) finish(i);
+    if (share > 1 || i + kOutWarps >= n) break;
   }
   fence_async_smem();
-  __syncthreads();
+  tc_fence_before();
+  const bool stop = __syncthreads_or(dead ? 1 : 0) != 0;   // an earlier kernel timed out
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  volatile int never = 0;
   if (warp == 0) {
     if (elect_one()) {
       // (The weights land before the CTA leaves, whether there is work or not.)
       if (mbar_wait(smem_u32(&sh->full), 0, p.status, &never) && !stop) {
         tc_fence_after();
+        const uint64_t a0 = sdesc(smem_u32(smem), 16, 1024), o0 = sdesc(smem_u32(smem + C::AT_O), 16, 1024);
 #pragma unroll 1
-        for (int kb = 0; kb < 8; ++kb) {
-          const uint32_t a = smem_u32(smem + kb * 16384);
-          const uint32_t o = smem_u32(smem + C::AT_O + kb * NT * 128);
+        for (int kb = 0; kb < 8; ++kb)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = sdesc(a + kk * 32, 16, 1024);
-            mma_f16_ss(tmem, ad, sdesc(o + kk * 32, 16, 1024), idesc_bf16(128, NT, false, false), (kb | kk) != 0);
-            mma_f16_ss(tmem, ad, sdesc(o + C::TERM + kk * 32, 16, 1024), idesc_bf16(128, NT, false, false), 1);
-          }
-        }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(tmem, a0 + kb * (W_BLOCK >> 4) + kk * 2, o0 + kb * (C::O_BLOCK >> 4) + kk * 2,
+                       idesc_bf16(128, 2 * NT, false, false), (kb | kk) != 0);
       } else {
         sh->abort = 1;
       }
@@ -1592,20 +1630,24 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
   }
   const bool ok = mbar_wait_warp(smem_u32(&sh->done), 0, p.status, &never);
   tc_fence_after();
-  if (warp < 4 && ok && *reinterpret_cast<volatile int*>(&sh->abort) == 0) {
-    uint32_t r[32];
-    tmem_ld32(tmem + (uint32_t(warp * 32) << 16), r);   // 32 columns are allocated; NT of them used
+  if (warp < NT / 4 && !stop && ok && *reinterpret_cast<volatile int*>(&sh->abort) == 0) {
+    // Four warps have the 128 values of 16 tokens.
+    const int c = (warp >> 2) * 16, v = (warp & 3) * 32;
+    __nv_bfloat16* dst = out + (static_cast<long long>(t0 + c) * p.H + h) * 128 + v + lane;
+    uint32_t r[16], r2[16];
+    tmem_ld16(tmem + (uint32_t(v) << 16) + c, r);
+    tmem_ld16(tmem + (uint32_t(v) << 16) + NT + c, r2);
     tmem_ld_wait();
-    __nv_bfloat16* dst = out + (static_cast<long long>(t0) * p.H + h) * 128 + warp * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      if (i < n && sh->used[i] >= 0) dst[static_cast<long long>(i) * p.H * 128] = __float2bfloat16_rn(__uint_as_float(r[i]));
+    for (int i = 0; i < 16; ++i)
+      if (c + i < n && sh->used[c + i] >= 0)
+        dst[static_cast<long long>(i) * p.H * 128] = __float2bfloat16_rn(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 32);
+    tmem_dealloc(tmem, 2 * NT);
   }
 }
 
@@ -1653,8 +1695,8 @@ cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const Decode
   cudaError_t e = opt_in_smem(q8_out_kernel<NT>, OutShape<NT>::TOTAL);
   if (e != cudaSuccess) return e;
   return launch_pdl(q8_out_kernel<NT>, dim3((a.T + tokens - 1) / tokens, a.H), dim3(32 * kOutWarps),
-                    OutShape<NT>::TOTAL, stream, w_map, p, a.sink, static_cast<__nv_bfloat16*>(a.out), a.lse, a.T,
-                    rows, tokens);
+                    OutShape<NT>::TOTAL, stream, w_map, p, fast_divisor(p.members * rows), a.sink,
+                    static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, tokens);
 }
 
 // Query rows of a tile: 64 where a sequence can fill more than 32.
@@ -1713,10 +1755,12 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   const int rows = tile_rows(H, a.max_new), members = item_members(H, rows);
   const bool wide = rows == 64;
 
-  CUtensorMap qa_map, wuk_map;
+  CUtensorMap qa_map, wuk_map, u_map;
   if (!encode_2d(&qa_map, a.q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&wuk_map, a.w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 256,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&u_map, q8, u8, static_cast<uint64_t>(H) * 1152, T, static_cast<uint64_t>(H) * 1152, 128, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   PlanArgs plan;
@@ -1735,7 +1779,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   plan.status = a.status;
   cudaError_t e = opt_in_smem(q8_query_kernel, Q_SMEM_TOTAL);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(q8_query_kernel, dim3((T + 127) / 128, 2 * H), dim3(kQThreads), Q_SMEM_TOTAL, stream, qa_map, wuk_map,
+  e = launch_pdl(q8_query_kernel, dim3((T + 127) / 128, 2 * H + 2), dim3(kQThreads), Q_SMEM_TOTAL, stream, qa_map, wuk_map, u_map,
                  static_cast<const uint16_t*>(a.q), q8, q_scale, T, H, a.status, plan);
   if (e != cudaSuccess) return e;
 
