@@ -640,13 +640,15 @@ __device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
 
 constexpr int kSparseProducers = 2;
 
-// A tile's latent blocks are loaded twice, for its scores and again (from L2)
+// TWICE: a tile's latent blocks are loaded for its scores and again (from L2)
 // for its values, in the order in which the MMAs take them: scores 0, scores 1,
-// values 0, scores 2, values 1, ...  Kept in shared memory through the softmax
-// instead, only two tiles fit, and their loads, MMAs and softmax follow one
-// another: 6000 clk for a tile of 64 rows against 2700 of MMAs.  Streamed, the
-// ring holds nothing but loads in flight, and the softmax of a tile has the time
-// of the MMAs between its scores and its values.
+// values 0, scores 2, values 1, ...  The ring then holds nothing but loads in
+// flight.  Otherwise a tile stays in its slots from its scores to its values:
+// half the reads of L2, but a slot is held through the softmax.  32 rows have
+// room for two and a half tiles, and 32 sequences of 16384 to 32768 keys, 16
+// heads, take 113 us so, against 139 with every block loaded twice.  64 rows
+// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, take 311
+// us twice and 322 once; with listed rows, whose copies cost more, 91 and 89.
 //
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
                    const Q8Params p) {
   using C = Shape<WIDE>;
   constexpr int ROWS = C::ROWS, GROUPS = C::GROUPS, SLOTS = C::SLOTS, ROPES = C::ROPES, NQ = C::NQ;
+  constexpr bool TWICE = WIDE && DENSE;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_COLS = C::TM_COLS;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, NQ, false, false);
   constexpr uint32_t IDESC_PV = idesc_e4m3(128, 64, true, true);
@@ -806,18 +809,18 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           if (elect_one()) {
             for (int j = j0; j < j1 && good; ++j) {
               if (late && j == 0) break;
-              good = blocks(j, true) && (j == 0 || blocks(j - 1, false));
+              good = blocks(j, true) && (!TWICE || j == 0 || blocks(j - 1, false));
             }
             if (late && j0 == 0) good = blocks(0, true);
           }
           ok = __all_sync(0xffffffffu, good);
           if (late && j0 == 0 && ok && (ok = load_q())) {
             if (elect_one())
-              for (int j = 1; j < j1 && good; ++j) good = blocks(j, true) && blocks(j - 1, false);
+              for (int j = 1; j < j1 && good; ++j) good = blocks(j, true) && (!TWICE || blocks(j - 1, false));
             ok = __all_sync(0xffffffffu, good);
           }
         }
-        if (ok) {
+        if (TWICE && ok) {
           bool good = true;
           if (elect_one()) good = blocks(n - 1, false);
           ok = __all_sync(0xffffffffu, good);
@@ -856,6 +859,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
       const uint64_t w0 = sdesc(smem_u32(smem + C::AT_P), 16, 512, kSwizzle64);
       uint32_t seg = 0, g0 = 0, masked_tiles = 0;      // segments done, tiles before this one's, cleaned tiles
       uint32_t sk = 0, tk = 0;                         // slot and turn of the next latent block
+      uint32_t vk = 0;                                 // loaded once: slot of the next values
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_one(smem_u32(bar), parity, status, abort_flag); };
       auto landed = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           for (int kk = 0; kk < 8; ++kk)                 // blocks 2 c and 2 c + 1, 32 columns a step
             mma_f8_ss(d, ad + (kk >> 2) * 64 + (kk & 3) * 2, b0 + (2 * c + (kk >> 2)) * (C::QBLOCK >> 4) + (kk & 3) * 2,
                       IDESC_QK, (c | kk) != 0);
-          tc_commit(smem_u32(&sh->k_empty[sk]));
+          if (TWICE) tc_commit(smem_u32(&sh->k_empty[sk]));
           if (++sk == SLOTS) {
             sk = 0;
             ++tk;
@@ -896,10 +900,12 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
         // O is free once the segment before has been read.
         if (first && seg > 0 && !wait(&sh->o_free, (seg - 1) & 1)) return false;
         if (masked && !wait(&sh->fixed, masked_tiles++ & 1)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (!landed(&sh->k_full[sk], tk & 1)) return false;
-          const uint64_t ad = a0 + sk * (SLOT >> 4);
+          if (TWICE && !landed(&sh->k_full[sk], tk & 1)) return false;
+          const uint32_t slot = TWICE ? sk : vk;
+          const uint64_t ad = a0 + slot * (SLOT >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // Block 2 c + kk / 4, 32 keys a step: both operands MN-major, groups of 8 keys
@@ -909,8 +915,10 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
             mma_f8_ss(d, av, wv, IDESC_PV, !first || (kk & 3) != 0);
             if (WIDE) mma_f8_ss(d, av, wv + (C::PTERM >> 4), IDESC_PV, 1);
           }
-          tc_commit(smem_u32(&sh->k_empty[sk]));
-          if (++sk == SLOTS) {
+          tc_commit(smem_u32(&sh->k_empty[slot]));
+          if (!TWICE) {
+            if (++vk == SLOTS) vk = 0;
+          } else if (++sk == SLOTS) {
             sk = 0;
             ++tk;
           }
@@ -1163,7 +1171,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           // The first two warpgroups have one of the tile's two value slots
           // each, when it lands.
           if (wg < 2) {
-            const uint32_t u = 4 * g0 + (j + 1 < sg.n ? 4 * j + 4 : 4 * j + 2) + wg;
+            const uint32_t u = wg + (TWICE ? 4 * g0 + (j + 1 < sg.n ? 4 * j + 4 : 4 * j + 2) : 2 * g);
             const uint32_t slot = u % SLOTS;
             if (!wait_warp(smem_u32(&sh->k_full[slot]), (u / SLOTS) & 1, status, abort_flag)) {
               fail = true;
@@ -1356,9 +1364,9 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           }
           cp_async_arrive(smem_u32(&sh->r_full[s]));
           ++ropes;
-          if (j > 0) ok = latent(prev);
+          if (TWICE && j > 0) ok = latent(prev);
         }
-        ok = ok && latent(row);
+        if (TWICE) ok = ok && latent(row);
       }
       // Every copy lands, and its arrival with it, before the CTA leaves.
       cp_async_commit();
