@@ -32,7 +32,9 @@
  *     projection, attention and decode entry points are programmatic
  *     dependent launches: each may start launching while the kernel before
  *     it on the stream finishes, and waits for that kernel to complete before
- *     it touches memory, so stream order is unchanged.
+ *     it touches memory, so stream order is unchanged.  (The last kernel of
+ *     mla_decode_q8 waits for all that came before the call, not for the
+ *     call's own kernels, before it reads w_uv.)
  *   - Tensors are dense row-major with the leading dimensions written in the
  *     comments.  Integer tables are uint32/int32 as on the pages.
  *   - Geometry is fixed by the pages: q_depth 192 = 128 nope + 64 rope,
@@ -631,13 +633,19 @@ mla_status_t mla_prefill_q8(void* out, float* lse, const void* q, const uint32_t
                             int32_t* d_status, mla_stream_t stream);
 
 /*
- * Partitions a sequence that mla_decode_q8 uses when num_partitions is 0, and
- * the workspace it needs, as mla_decode_partitions and
- * mla_decode_workspace_bytes are for mla_decode (no counterpart on the pages).
+ * Pieces that mla_decode_q8 uses when num_partitions is 0 (no counterpart on
+ * the pages).  Other than mla_decode, it does not split each sequence by
+ * itself: the 128-key tiles of all sequences form one line, which is cut into
+ * num_partitions equal pieces, one for each group of SMs, however the lengths
+ * differ.
  */
 int32_t mla_decode_q8_partitions(int32_t batch_size, int32_t num_heads, int32_t max_new_tokens,
                                  int32_t max_keys);
-/* The pages size no buffer: no counterpart. */
+/*
+ * Workspace for that many pieces (0 for invalid arguments); what
+ * mla_decode_q8_partitions returned for the same arguments serves a call with
+ * num_partitions 0.  The pages size no buffer: no counterpart.
+ */
 size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, int32_t num_partitions);
 
 /*
@@ -657,10 +665,14 @@ size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, 
  * is left out, are not written.
  * max_seq_len bounds the contexts (dense form).
  * Errors: host MLA_ERR_GEOMETRY, MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH
- * as mla_decode, MLA_ERR_ARG for kv_scales or scale_block as above and for more
- * than 16383 heads.  Device MLA_DEV_BAD_OFFSETS (input_row_offsets[b+1] >
- * total_q_tokens, or a dense context longer than max_seq_len: sequence b left
- * out), MLA_DEV_BAD_PAGE (a page id or listed row out of range: the result of
+ * as mla_decode, MLA_ERR_ARG for kv_scales or scale_block as above, for more
+ * than 16383 heads or 32768 pieces and where 32-bit indexes of the work would
+ * not do: total_q_tokens * num_heads or max_new_tokens * num_heads of 2^29 or
+ * more, (total_q_tokens + total_q_tokens * num_heads / 32) times the tiles of
+ * max_seq_len (of indices_stride) of 2^31 or more.  Device MLA_DEV_BAD_OFFSETS
+ * (input_row_offsets[b+1] > total_q_tokens or < input_row_offsets[b], a sequence
+ * that begins before an earlier one ends, or a dense context longer than
+ * max_seq_len: sequence b left out), MLA_DEV_BAD_PAGE (a page id or listed row out of range: the result of
  * the rows that see it is not meaningful), MLA_DEV_TIMEOUT.
  */
 mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,

@@ -124,6 +124,56 @@ def test_scores_status():
     assert np.all(got[1] == FILL) and np.abs(got[0, :11] - ref[0, :11]).max() <= 2.0 ** -15 * mag.max()
 
 
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 64, 128])
+@pytest.mark.parametrize("Hi", [1, 16, 17, 32, 40, 64, 100, 128])
+def test_scores_several_tokens(Hi, block, eight):
+    """Batches of one to eight tokens an MMA, the last ones not full."""
+    check_scores([9, 1, 30], [200, 130, 0], Hi, block, 16, eight, scales=True, seed=Hi)
+
+
+@pytest.mark.parametrize("Hi", [3, 16, 24, 40])
+def test_scores_infinite_weight(Hi):
+    """An infinite weight gives infinity or, where the product is not positive,
+    NaN, in its own token only."""
+    L = 50
+    rng = np.random.default_rng(Hi)
+    table, num = pages([2], [L - 2], 16)
+    k = torch.from_numpy(rng.standard_normal((num, 16, 128))).to(torch.bfloat16)
+    q = torch.from_numpy(rng.standard_normal((2, Hi, 128))).to(torch.bfloat16)
+    w = torch.from_numpy(rng.uniform(0.5, 1, (2, Hi))).float()
+    w[1, Hi - 1] = float("inf")
+    out = torch.zeros(2, L, device=DEV)
+    mla.check(mla.mla_index_scores(out, q.to(DEV), w.to(DEV), k.to(DEV), None, i32([0, 2]), i32([L - 2]), i32(table), num,
+                                   16, table.shape[1], 1, 1, Hi, 2, 2, L, L, mla.MLA_BF16))
+    rows = k.reshape(-1, 128).double()[torch.from_numpy(table[0][np.arange(L) // 16] * 16 + np.arange(L) % 16)]
+    pos = (q[1, Hi - 1].double() @ rows.T > 0).numpy()
+    got = out.cpu().numpy()
+    assert np.isfinite(got[0, :L - 1]).all() and np.isneginf(got[0, L - 1])
+    assert np.all(np.isposinf(got[1][pos])) and np.all(np.isnan(got[1][~pos]))
+
+
+def test_scores_replay_bit_for_bit():
+    rng = np.random.default_rng(0)
+    new, cached, Hi, page = [3, 1], [500, 900], 32, 64
+    table, num = pages(new, cached, page)
+    q, k = (torch.from_numpy(rng.standard_normal(x)).to(torch.bfloat16).to(DEV) for x in ((4, Hi, 128), (num, page, 128)))
+    w, out = torch.from_numpy(rng.standard_normal((4, Hi))).float().to(DEV), torch.zeros(4, 15, device=DEV)
+    args = (out, q, w, k, None, i32(offsets(new)), i32(cached), i32(table), num, page, table.shape[1], 64, 2, Hi, 4, 3, 901,
+            15, mla.MLA_BF16)
+    mla.check(mla.mla_index_scores(*args))
+    torch.cuda.synchronize()
+    ref = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mla.check(mla.mla_index_scores(*args))
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
 # ------------------------------------------------------------------ selection
 
 def check_select(new, cached, block, top, local, page=16, seed=0, scores=None, T_extra=0, extra_stride=0, width=None):
@@ -185,6 +235,12 @@ def test_select_over_a_cluster(cached, scores):
     """Long rows of few tokens: two to eight CTAs a token, and a short row beside
     them whose last CTAs have nothing."""
     check_select([1, 1], [cached, 30], 1, 2048, 1, page=128, scores=scores)
+
+
+def test_select_many_sequences():
+    """More sequences than are probed at once, some of them empty."""
+    new = [0 if b % 7 == 3 else 1 for b in range(1500)]
+    check_select(new, [b % 50 for b in range(1500)], 1, 8, 1, scores=quantised)
 
 
 def test_select_longer_than_shared_memory():

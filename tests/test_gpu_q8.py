@@ -618,3 +618,143 @@ def test_cache_offsets_past_32_bits():
         torch.cuda.synchronize()
         assert st.item() == 0
         compare(out.float().cpu().double().numpy(), lse.cpu().double().numpy(), *ref)
+
+
+# ------------------------------------------------------------------ at the edges of the launch shapes
+
+@pytest.mark.parametrize("H", [65, 192, 256, 320, 576])
+def test_decode_many_heads(H):
+    """Two to eight row tiles walk a piece together (pairs of them as clusters);
+    576 heads are two items a token."""
+    Decode([1, 2], [300, 40], H, 64, 16, seed=H).check(parts=3)
+
+
+@pytest.mark.parametrize("H", [100, 192])
+def test_sparse_decode_many_heads(H):
+    d = Decode([1, 1], [300, 90], H, 24, 8)
+    lists = np.stack([np.resize(d.rows(b, np.arange(91)[::-1]), 150) for b in range(2)])
+    d.check(parts=3, lists=lists, topk=[150, 131])
+
+
+@pytest.mark.parametrize("H", [4, 40])
+def test_decode_one_long_sequence(H):
+    """A piece for every SM and one sequence: 16 warps share a token's pieces."""
+    Decode([1], [40000], H, 128, 64).check()
+
+
+@pytest.mark.parametrize("H,n", [(16, 30), (40, 16), (9, 100), (128, 40)])
+def test_decode_tokens_of_the_last_kernel(H, n):
+    """Two to 32 tokens a CTA of the merge, with one or several warps a token."""
+    rng = np.random.default_rng(H)
+    Decode([1] * n, [int(x) for x in rng.integers(0, 400, n)], H, 16, 4, seed=H).check()
+
+
+def test_decode_many_pieces_of_several_tokens():
+    """Items of two tokens cut into pieces, 128 heads."""
+    Decode([2, 1, 2], [1500, 700, 90], 128, 128, 64).check()
+
+
+def test_decode_mostly_empty_batch():
+    """More sequences than tokens, the plan's scan in several turns."""
+    new, cached = [0] * 400, [int(x) for x in np.random.default_rng(0).integers(0, 200, 400)]
+    for b in (0, 127, 128, 300, 399):
+        new[b] = 1 + b % 2
+    Decode(new, cached, 8, 16, 1).check()
+
+
+def test_decode_max_new_above_every_sequence():
+    d = Decode([1, 2], [300, 140], 8, 128, 8)
+    compare(*d.run(max_new=50), *d.reference())
+
+
+def test_decode_overlapping_and_decreasing_offsets():
+    """Sequence 1 ends before it begins, sequence 2 begins inside sequence 0:
+    both are reported and left out."""
+    d = Decode([2, 1, 2], [100, 30, 60], 4, 16, 1)
+    ref, ref_lse = d.reference()
+    out, lse = d.run(iro=[0, 2, 1, 3], expect=mla.MLA_DEV_BAD_OFFSETS)
+    compare(out[:2], lse[:2], ref[:2], ref_lse[:2])
+    assert np.all(out[2:] == 7.0) and np.all(lse[2:] == 7.0)
+
+
+def test_decode_a_piece_without_weight_beside_one_that_is_no_number():
+    """All scores of the first piece are -infinity, a scale of the second is NaN."""
+    d = Decode([1], [255], 2, 128, 1)
+    d.q[:] = 0
+    d.q[..., 128] = 2.0 ** 60
+    d.codes[:] = 0
+    d.scales[:] = 1.0
+    first = d.rows(0, np.arange(128))
+    d.codes.reshape(-1, 576)[first, 512] = O.e4m3_encode(np.array([-448.0]))[0]
+    d.scales.reshape(-1)[first] = 2.0 ** 100
+    assert np.all(np.isfinite(d.run(2)[0]))
+    d.scales.reshape(-1)[d.rows(0, [200])[0]] = np.nan
+    assert np.all(np.isnan(d.run(2)[0]))
+
+
+def test_decode_two_calls_at_once():
+    """Calls with workspaces of their own on two streams, eager and captured."""
+    a, b = Decode([1, 2], [900, 333], 16, 64, 8), Decode([1], [5000], 40, 128, 64, seed=1)
+    ref = []
+    for d in (a, b):
+        d.run()
+        ref.append((d.out.clone(), d.lse.clone()))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for d, s in zip((a, b), sides):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            d.call()
+        graphs.append(g)
+    for how in ("eager", "captured"):
+        for d in (a, b):
+            d.out.zero_()
+            d.lse.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for d, g, s in zip((a, b), graphs, sides):
+                with torch.cuda.stream(s):
+                    d.call() if how == "eager" else g.replay()
+        torch.cuda.synchronize()
+        for d, (out, lse) in zip((a, b), ref):
+            assert torch.equal(d.out.view(torch.int16), out.view(torch.int16)) and torch.equal(d.lse, lse)
+
+
+@pytest.mark.parametrize("H", [33, 128, 200])
+def test_write_heads(H):
+    """Query pieces that do not fill a turn of the CTA, fill it, and take two."""
+    check_write([2, 5], [9, 60], 16, 4, H)
+
+
+def test_write_many_sequences():
+    """More sequences than 32 * 32, most of them empty."""
+    new = [0] * 1100
+    for b in (0, 5, 31, 32, 500, 1023, 1024, 1099):
+        new[b] = 1 + b % 3
+    check_write(new, [b % 40 for b in range(1100)], 16, 4, 2)
+
+
+def test_write_replays_bit_for_bit():
+    page, n = 32, 70
+    w = scaled(WORKLOADS["tiny_ragged"], H=4)
+    lat, gamma, freqs = make_cache_write_operands(w, n, 100)
+    table, num = pages([n], [10], page)
+    q = torch.randn(n, 4, 192, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).to(DEV)
+    kv, sc, dq = fp8(np.zeros((num, page, 576), np.uint8)), torch.zeros(num, page // 8, device=DEV), q.clone()
+    call = lambda: mla.check(mla.mla_latent_cache_write_q8(kv, sc, dq, *dev, num, page, table.shape[1], 8, 1, 4, n, 100,
+                                                           1e-6))
+    dev = (lat.to(DEV), gamma.to(DEV), freqs.to(DEV), i32([0, n]), i32([10]), i32(table))
+    call()
+    torch.cuda.synchronize()
+    ref = kv.clone(), sc.clone(), dq.clone()
+    dq.copy_(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(2):
+        kv.zero_()
+        sc.zero_()
+        dq.copy_(q)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kv, ref[0]) and torch.equal(sc, ref[1]) and torch.equal(dq.view(torch.int16), ref[2].view(torch.int16))

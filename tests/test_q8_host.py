@@ -76,7 +76,8 @@ def test_decode_refusals(lib):
     for change in (dict(out=None), dict(out=8), dict(q=4), dict(iro=None), dict(cl=None), dict(kv=None), dict(sc=None),
                    dict(pt=None), dict(np=0), dict(ps=0), dict(mp=0), dict(sb=3), dict(sb=0), dict(wuk=8),
                    dict(wuv=None), dict(B=0), dict(T=-1), dict(mn=-1), dict(L=0), dict(parts=-1), dict(scale=0.0),
-                   dict(scale=float("nan")), dict(H=16384), dict(np=1 << 30), dict(T=1 << 28)):
+                   dict(scale=float("nan")), dict(H=16384), dict(np=1 << 30), dict(T=1 << 28),
+                   dict(parts=(1 << 15) + 1)):
         assert call(**change) == mla.MLA_ERR_ARG, change
     assert call() == mla.MLA_ERR_WORKSPACE
     assert call(T=0) == mla.MLA_OK                   # nothing to do
