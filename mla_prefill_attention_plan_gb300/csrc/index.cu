@@ -44,10 +44,10 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // an SM, one's start under the other's work.
 //
 // With one new token a sequence the call is bound by reading the keys: 64
-// sequences of 4096 to 16384 keys, 64 heads, bf16, 42 us (4.1 TB/s).  With
+// sequences of 4096 to 16384 keys, 64 heads, bf16, 36 us (4.8 TB/s).  With
 // more it is bound by the epilogue, which takes a maximum and half a packed FMA
 // for every product on the CUDA cores: about 1000 tokens, 32 heads, 8000 8-bit
-// keys, blocks of 64, 106 us (2.3 T products/s, issue slots 54 % taken).  A
+// keys, blocks of 64, 104 us (2.4 T products/s, issue slots 54 % taken).  A
 // batch of tokens therefore fills a buffer, so that an MMA's latency (some 600
 // clk to its barrier) is paid once for all of them, and the loop stays small:
 // two chunks in flight in a warp; four ran at 155 us where two ran at 131, and
@@ -63,6 +63,8 @@ struct ScoreSmem {
   uint64_t k_full[I_MAXSTAGES], k_empty[I_MAXSTAGES], q_full, d_full[2], d_free[2], drain;
   uint32_t tmem;
   int abort;
+  unsigned long long sum[kScoreThreads / 32];   // the split of the work among the CTAs
+  int scan[kScoreThreads / 32], seq, nth, runs;
   float part[2][2][8][4];         // [warpgroup][unit & 1][token][warp]: maxima, for blocks of more than 32 keys
 };
 constexpr int I_BAR = 1024;
@@ -77,7 +79,7 @@ struct ScoreParams {
   const uint32_t* cache_len;
   const int32_t* page_table;
   FastDiv page;
-  int num_pages, max_pages, block, B, Hi, NP, T, groups, splits, span, max_seq, stride, box;
+  int num_pages, max_pages, block, B, Hi, NP, T, max_new, groups, places, shares, max_seq, stride, box;
   int G, batch;              // tokens of a group and of an MMA
   int stages, cols;          // ring stages, TMEM columns allocated
   int at_w, at_ring, at_bar; // shared memory: queries, weights [G][NP], ring, barriers
@@ -90,6 +92,22 @@ __device__ __forceinline__ int score_row(const ScoreParams& p, int b, int pos) {
   if (page >= 0 && page < p.num_pages) return page * p.page.d + (pos - pi * p.page.d);
   set_status(p.status, MLA_DEV_BAD_PAGE);
   return -1;
+}
+
+// A sequence's groups of new tokens and tiles of keys; none if it is left out.
+struct Scored {
+  int groups, tiles;
+};
+__device__ __forceinline__ Scored scored(const ScoreParams& p, int b, bool report) {
+  const uint32_t qa = __ldg(p.iro + b), qe = __ldg(p.iro + b + 1), cached = __ldg(p.cache_len + b);
+  if (qe <= qa) return {0, 0};
+  const uint64_t ctx = static_cast<uint64_t>(cached) + (qe - qa);
+  if (qe > static_cast<uint32_t>(p.T) || ctx > static_cast<uint64_t>(p.max_seq)) {
+    if (report) set_status(p.status, MLA_DEV_BAD_OFFSETS);
+    return {0, 0};
+  }
+  const int n = static_cast<int>(min(qe - qa, static_cast<uint32_t>(p.max_new)));
+  return {(n + p.G - 1) / p.G, static_cast<int>((ctx + IT - 1) / IT)};
 }
 
 template <bool E8, bool DENSE>
@@ -106,28 +124,71 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_enter();
 
-  const int sp = blockIdx.x % p.splits;
-  const int g = (blockIdx.x / p.splits) % p.groups;
-  const int b = blockIdx.x / p.splits / p.groups;
-  const uint32_t qa = p.iro[b], qe = p.iro[b + 1];
-  if (qe <= qa) return;
-  const uint64_t ctx = static_cast<uint64_t>(p.cache_len[b]) + (qe - qa);
-  if (qe > static_cast<uint32_t>(p.T) || ctx > static_cast<uint64_t>(p.max_seq)) {
-    if (threadIdx.x == 0) set_status(p.status, MLA_DEV_BAD_OFFSETS);
-    return;
+  // ---- this CTA's sequence, group and run of tiles
+  int b, nth = blockIdx.x, runs = 1, span = 0x7FFFFFFF;
+  if (p.places == 0) {                               // many pairs of sequence and group: a CTA each
+    b = nth / p.groups;
+    nth -= b * p.groups;
+    if (nth == 0 && threadIdx.x == 0) scored(p, b, true);
+  } else {
+    unsigned long long total = 0;
+    for (int i = threadIdx.x; i < p.B; i += kScoreThreads) {
+      const Scored w = scored(p, i, blockIdx.x == 0);
+      total += static_cast<unsigned long long>(w.groups) * w.tiles;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane == 0) sh->sum[warp] = total;
+    if (threadIdx.x == 0) sh->seq = -1;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kScoreThreads / 32; ++w) total += sh->sum[w];
+    // Tiles of a run: an equal share, eight at least (a start costs about three).
+    span = static_cast<int>(min(0x7FFFFFFFull, max(8ull, (total + p.shares - 1) / p.shares)));
+    int base = 0;
+    for (int i0 = 0; i0 < p.B && base <= nth; i0 += kScoreThreads) {
+      Scored w = {0, 0};
+      if (i0 + static_cast<int>(threadIdx.x) < p.B) w = scored(p, i0 + threadIdx.x, false);
+      const int each = (w.tiles + span - 1) / span, mine = w.groups * each;
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (lane == 31) sh->scan[warp] = incl;
+      __syncthreads();
+      int before = base;
+      for (int w2 = 0; w2 < kScoreThreads / 32; ++w2) {
+        if (w2 < warp) before += sh->scan[w2];
+        base += sh->scan[w2];
+      }
+      before += incl - mine;
+      if (before <= nth && nth < before + mine) {
+        sh->seq = i0 + threadIdx.x;
+        sh->nth = nth - before;
+        sh->runs = each;
+      }
+      __syncthreads();
+    }
+    b = sh->seq;
+    nth = sh->nth;
+    runs = sh->runs;
+    if (b < 0) return;                               // fewer runs than CTAs
   }
-  const int n_new = static_cast<int>(qe - qa);
+  const Scored work = scored(p, b, false);
+  const int g = nth / runs, sp = nth - g * runs;
+  if (g >= work.groups) return;
+  const int n_new = static_cast<int>(min(p.iro[b + 1] - p.iro[b], static_cast<uint32_t>(p.max_new)));
   const int i0 = g * p.G;
-  if (i0 >= n_new) return;
   const int ng = min(p.G, n_new - i0);
-  const int t0 = static_cast<int>(qa) + i0;
+  const int t0 = static_cast<int>(p.iro[b]) + i0;
   const int pos_first = static_cast<int>(p.cache_len[b]) + i0;   // position of the group's first token
   const int pos_last = pos_first + ng - 1;
-  const long long tiles_all = (static_cast<long long>(p.stride) * p.block + IT - 1) / IT;
-  const long long tile0 = static_cast<long long>(sp) * p.span;
-  if (tile0 >= tiles_all) return;
-  const int tiles = static_cast<int>(min(static_cast<long long>(p.span), tiles_all - tile0));
-  const long long base0 = tile0 * IT;
+  // Runs of a pair differ by one tile at most.
+  const int tile0 = static_cast<int>(static_cast<long long>(work.tiles) * sp / runs);
+  const int tiles = static_cast<int>(static_cast<long long>(work.tiles) * (sp + 1) / runs) - tile0;
+  const long long base0 = static_cast<long long>(tile0) * IT;
   const int n = base0 > pos_last ? 0 : static_cast<int>(min(static_cast<long long>(tiles), (pos_last - base0) / IT + 1));
   const int batches = (ng + p.batch - 1) / p.batch;
 
@@ -438,12 +499,17 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   } else if (timed_out_before(p.status)) {
     return;
   }
-  // Blocks past the group's last key: -infinity.
-  const long long from = (base0 + static_cast<long long>(n) * IT) / p.block;
-  const long long to = min(static_cast<long long>(p.stride), (base0 + static_cast<long long>(tiles) * IT) / p.block);
-  for (int i = 0; i < ng; ++i)
-    for (long long x = from + threadIdx.x; x < to; x += kScoreThreads)
-      p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
+  // Blocks past the run's last key, and a share of those past the sequence's
+  // last tile: -infinity.
+  auto fill = [&](long long from, long long to) {
+    to = min(to, static_cast<long long>(p.stride));
+    for (int i = 0; i < ng; ++i)
+      for (long long x = from + threadIdx.x; x < to; x += kScoreThreads)
+        p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
+  };
+  fill((base0 + static_cast<long long>(n) * IT) / p.block, (base0 + static_cast<long long>(tiles) * IT) / p.block);
+  const long long end = static_cast<long long>(work.tiles) * IT / p.block, rest = max(0ll, p.stride - end);
+  fill(end + rest * sp / runs, end + rest * (sp + 1) / runs);
 }
 
 // ============================================================ selection
@@ -745,6 +811,7 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.max_pages = a.max_pages;
   p.block = a.block;
   p.B = a.B;
+  p.max_new = a.max_new;
   p.Hi = a.Hi;
   p.NP = (a.Hi + 15) / 16 * 16;
   p.T = a.T;
@@ -768,16 +835,19 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.at_w = p.at_ring + p.stages * stage;
   p.at_bar = p.at_w + w_bytes;
   const int smem = p.at_bar + I_BAR + 1024;
-  // Ranges of positions: CTAs for three rounds of the SMs' two places, of at least
-  // eight tiles each (a start costs about three).
-  const long long tiles = (static_cast<long long>(a.stride) * a.block + IT - 1) / IT;
+  // The pairs' tiles in runs of equal length, for the places of one round of
+  // CTAs (two rounds with several tokens): the lengths are only known on the
+  // device, where each CTA finds its run.  Half a run a pair is lost to
+  // rounding, so the share leaves that many places: 304 shares for 64 sequences
+  // made more CTAs than places, and a second round (46 us, not 36).  Ranges cut
+  // on the host by max_seq_len took 41 to 43 us, more where that is far above
+  // the contexts.  Many pairs need no cutting, and finding a run among as many
+  // sequences would take longer than it saves.
   const long long pairs = static_cast<long long>(a.B) * p.groups;
-  const long long places = 3ll * 2 * sm_count();
-  long long span = (pairs * tiles + places - 1) / places;
-  span = std::min(tiles, std::max(8ll, span));
-  p.span = static_cast<int>(span);
-  p.splits = static_cast<int>((tiles + span - 1) / span);
-  const long long items = pairs * p.splits;
+  const long long places = (p.G == 1 ? 2ll : 4ll) * sm_count();
+  p.places = pairs >= 4 * places ? 0 : static_cast<int>(places);
+  p.shares = std::max(p.places / 2, p.places - static_cast<int>(std::min(pairs / 2, places)));
+  const long long items = pairs + p.places;
   if (items >= (1ll << 31)) return cudaErrorInvalidValue;
   const CUtensorMapDataType dt = e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int cols = e8 ? 128 : 64;

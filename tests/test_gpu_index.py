@@ -132,6 +132,21 @@ def test_scores_several_tokens(Hi, block, eight):
     check_scores([9, 1, 30], [200, 130, 0], Hi, block, 16, eight, scales=True, seed=Hi)
 
 
+@pytest.mark.parametrize("B", [700, 1500])
+def test_scores_many_sequences(B):
+    """Runs found among more sequences than a CTA has threads; and, without
+    cutting, a CTA for each.  Some sequences are empty, one is long."""
+    new = [0 if b % 7 == 3 else 1 for b in range(B)]
+    cached = [b % 50 for b in range(B)]
+    cached[B // 2] = 2000
+    check_scores(new, cached, 3, 4, 16, seed=B)
+
+
+def test_scores_max_seq_far_above_the_contexts():
+    check_scores([1, 3], [500, 130], 8, 2, 16, max_seq=40000, extra_stride=3)
+    check_scores([20, 3], [500, 130], 40, 128, 16, max_seq=40000)
+
+
 @pytest.mark.parametrize("Hi", [3, 16, 24, 40])
 def test_scores_infinite_weight(Hi):
     """An infinite weight gives infinity or, where the product is not positive,
