@@ -369,16 +369,19 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       uint32_t mine = 0;
       int j = e / batches, i = e - j * batches;        // tile and batch of the unit
       // This key's scale in the unit's tile is read a unit ahead, its page id two.
-      auto page_of = [&](int tile) -> int {
-        const int pos = static_cast<int>(base0) + tile * IT + key;
-        if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 0;
-        const int pi = fast_div(pos, p.page);
-        return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
+      const int32_t* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+      struct Where {
+        int page, slot;       // slot -1: no key of the call, or no scales
       };
-      auto scale_of = [&](int tile, int page) -> float {
+      auto where = [&](int tile) -> Where {
         const int pos = static_cast<int>(base0) + tile * IT + key;
-        if (p.key_scales == nullptr || tile >= n || pos > pos_last) return 1.f;
-        if (page >= 0 && page < p.num_pages) return __ldg(p.key_scales + page * p.page.d + pos - fast_div(pos, p.page) * p.page.d);
+        if (p.key_scales == nullptr || tile >= n || pos > pos_last) return {0, -1};
+        const int pi = fast_div(pos, p.page);
+        return {pi < p.max_pages ? __ldg(table + pi) : -1, pos - pi * p.page.d};
+      };
+      auto scale_of = [&](const Where& w) -> float {
+        if (w.slot < 0) return 1.f;
+        if (w.page >= 0 && w.page < p.num_pages) return __ldg(p.key_scales + w.page * p.page.d + w.slot);
         set_status(p.status, MLA_DEV_BAD_PAGE);
         return 1.f;
       };
@@ -386,18 +389,18 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       auto step = [&](int& tile, int& batch) {
         for (batch += GROUPS; batch >= batches; batch -= batches) ++tile;
       };
-      float next = scale_of(j, page_of(j));
+      float next = scale_of(where(j));
       int j1 = j, i1 = i;
       step(j1, i1);
-      int page = page_of(j1);
+      Where at = where(j1);
 #pragma unroll 1
       while (j < n) {
         const int pos = static_cast<int>(base0) + j * IT + key;
         const float ks = next;
-        next = scale_of(j1, page);
+        next = scale_of(at);
         int j2 = j1, i2 = i1;
         step(j2, i2);
-        page = page_of(j2);
+        at = where(j2);
         const bool ok = mbar_wait_warp(smem_u32(&sh->d_full[e]), mine & 1, p.status, abort_flag);
         ++mine;
         tc_fence_after();
@@ -467,14 +470,15 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
           // Blocks of 64 or 128 keys: two or four warps' maxima, a thread for
           // each token and block.  (Its warps leave this loop together: a wait
           // that ran out in one of them is known to the others by the barrier.)
-          const int blocks = IT / p.block, warps = 4 / blocks;
+          const int blocks = IT >> shift, warps = p.block >> 5;
           int bad;
           asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
                        "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
                        : "=r"(bad) : "r"(ok ? 0 : 1), "r"(e + 1) : "memory");
-          const int y = tid / blocks, x = tid - y * blocks;
+          const int y = tid >> (7 - shift), x = tid & (blocks - 1);
           if (y < toks) {
             float m = sh->part[e][mine & 1][y][x * warps];
+#pragma unroll 1
             for (int k = 1; k < warps; ++k) m = max_nan(m, sh->part[e][mine & 1][y][x * warps + k]);
             const int at = ((static_cast<int>(base0) + j * IT) >> shift) + x;
             if (at < p.stride) p.scores[static_cast<long long>(t0 + tok0 + y) * p.stride + at] = m;
