@@ -27,6 +27,20 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return v;
 }
 
+// acc += sum over 16 heads of relu(product) * weight.
+__device__ __forceinline__ void weigh(const uint32_t (&d)[16], uint32_t weights, float2& acc) {
+  float2 a1 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    const float4 wv = ld_shared_f4(weights + 4 * k);
+    acc = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[k]), 0.f), max_nan(__uint_as_float(d[k + 1]), 0.f)),
+                     make_float2(wv.x, wv.y), acc);
+    a1 = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[k + 2]), 0.f), max_nan(__uint_as_float(d[k + 3]), 0.f)),
+                    make_float2(wv.z, wv.w), a1);
+  }
+  acc = __fadd2_rn(acc, a1);
+}
+
 __device__ __forceinline__ float warp_max_nan(float v) {
   float r;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       const int tid = threadIdx.x - 64 - 128 * e;
       const uint32_t ta = tmem + (uint32_t(q4 * 32) << 16) + e * (p.cols / GROUPS);
       const int shift = __ffs(p.block) - 1;
-      const int tpt = p.Hi <= 16 ? 2 : 1;              // tokens of a turn
+      const bool pair = p.batch > 1;                   // two tokens a turn
       uint32_t mine = 0;
       int j = e / batches, i = e - j * batches;        // tile and batch of the unit
       // This key's scale in the unit's tile is read a unit ahead, its page id two.
@@ -405,63 +419,60 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
         ++mine;
         tc_fence_after();
         const int tok0 = i * p.batch, toks = ok ? min(p.batch, ng - tok0) : 0;
-        // Two chunks of 16 columns at a time, of one token or, with up to 16
-        // heads, of two: two chains in flight in each of the warps.
+        // Two chunks of 16 columns at a time, of two tokens or, in batches of one,
+        // of the same: two chains in flight in each of the warps.
 #pragma unroll 1
-        for (int y0 = 0; y0 < toks; y0 += tpt) {
+        for (int y0 = 0; y0 < toks; y0 += pair ? 2 : 1) {
+          const int other = pair ? (y0 + 1 < toks ? p.NP : 0) : 16;   // columns to the second chunk
+          const uint32_t col = ta + y0 * p.NP, w = smem_u32(sw) + (tok0 + y0) * p.NP * 4;
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const int y1 = tpt == 2 ? min(y0 + 1, toks - 1) : y0;
-          const uint32_t col0 = ta + y0 * p.NP, col1 = ta + y1 * p.NP;
-          const uint32_t w0 = smem_u32(sw) + (tok0 + y0) * p.NP * 4, w1 = smem_u32(sw) + (tok0 + y1) * p.NP * 4;
 #pragma unroll 1
-          for (int c = 0; c < p.Hi; c += 16 * (2 / tpt)) {
-            const int second = tpt == 2 ? 0 : min(c + 16, p.NP - 16);
+          for (int c = 0; c < p.Hi; c += pair ? 16 : 32) {
+            const bool both = pair || c + 16 < p.Hi;
             uint32_t d[2][16];
-            tmem_ld16(col0 + c, d[0]);
-            tmem_ld16(col1 + second, d[1]);
+            tmem_ld16(col + c, d[0]);
+            tmem_ld16(col + c + (both ? other : 0), d[1]);
             tmem_ld_wait();
+            if (__builtin_expect(p.Hi - c < (pair ? 16 : 32), 0)) {
+              // Columns past the last head hold the next token's products.
+              const int h0 = p.Hi - c, h1 = pair ? h0 : h0 - 16;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t w = x == 0 ? w0 + 4 * c : w1 + 4 * second;
-              // Heads of the chunk (none: a chunk past the last).
-              const int heads = p.Hi - c - (x == 1 && tpt == 1 ? 16 : 0);
-              if (__builtin_expect(heads < 16, 0)) {
-                if (heads <= 0) break;
-                // Columns past the last head hold the next token's products.
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  if (k >= heads) d[x][k] = 0u;
+              for (int k = 0; k < 16; ++k) {
+                if (k >= h0) d[0][k] = 0u;
+                if (k >= h1) d[1][k] = 0u;
               }
-              float2 a1 = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                const float4 wv = ld_shared_f4(w + 4 * k);
-                acc[x] = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[x][k]), 0.f), max_nan(__uint_as_float(d[x][k + 1]), 0.f)),
-                                    make_float2(wv.x, wv.y), acc[x]);
-                a1 = __ffma2_rn(make_float2(max_nan(__uint_as_float(d[x][k + 2]), 0.f), max_nan(__uint_as_float(d[x][k + 3]), 0.f)),
-                                make_float2(wv.z, wv.w), a1);
-              }
-              acc[x] = __fadd2_rn(acc[x], a1);
+            }
+            weigh(d[0], w + 4 * c, acc[0]);
+            if (both) weigh(d[1], w + 4 * (c + other), acc[1]);
+          }
+          float v0 = acc[0].x + acc[0].y, v1 = acc[1].x + acc[1].y;
+          if (!pair) v0 += v1;
+          v0 *= ks;
+          v1 *= ks;
+          const int ahead = pos - (pos_first + tok0 + y0);   // not visible to the token
+          if (ahead > 0) v0 = -kInf;
+          if (ahead > 1) v1 = -kInf;
+          if (p.block >= 32) {
+            v0 = warp_max_nan(v0);
+            if (pair) v1 = warp_max_nan(v1);
+          } else {
+#pragma unroll 1
+            for (int r = 1; r < p.block; r <<= 1) {
+              v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, v0, r));
+              v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, v1, r));
             }
           }
-          auto finish = [&](float v, int y) {
-            v *= ks;
-            if (pos > pos_first + tok0 + y) v = -kInf;     // not visible to the token
-            if (p.block >= 32) {
-              v = warp_max_nan(v);
-            } else {
-#pragma unroll 1
-              for (int r = 1; r < p.block; r <<= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, r));
+          const bool second = pair && y0 + 1 < toks;
+          if (p.block > 32) {
+            if (lane == 0) {
+              sh->part[e][mine & 1][y0][q4] = v0;
+              if (second) sh->part[e][mine & 1][y0 + 1][q4] = v1;
             }
-            if (p.block > 32) {
-              if (lane == 0) sh->part[e][mine & 1][y][q4] = v;
-            } else if ((lane & (p.block - 1)) == 0 && (pos >> shift) < p.stride) {
-              p.scores[static_cast<long long>(t0 + tok0 + y) * p.stride + (pos >> shift)] = v;
-            }
-          };
-          const float v0 = acc[0].x + acc[0].y, v1 = acc[1].x + acc[1].y;
-          finish(tpt == 1 ? v0 + v1 : v0, y0);
-          if (tpt == 2 && y0 + 1 < toks) finish(v1, y0 + 1);
+          } else if ((lane & (p.block - 1)) == 0 && (pos >> shift) < p.stride) {
+            float* dst = p.scores + static_cast<long long>(t0 + tok0 + y0) * p.stride + (pos >> shift);
+            dst[0] = v0;
+            if (second) dst[p.stride] = v1;
+          }
         }
         tc_fence_before();
         __syncwarp();
