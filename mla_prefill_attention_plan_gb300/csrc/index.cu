@@ -58,14 +58,14 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // an SM, one's start under the other's work.
 //
 // With one new token a sequence the call is bound by reading the keys: 64
-// sequences of 4096 to 16384 keys, 64 heads, bf16, 36 us (4.8 TB/s).  With
+// sequences of 4096 to 16384 keys, 64 heads, bf16, 35 us (4.9 TB/s).  With
 // more it is bound by the epilogue, which takes a maximum and half a packed FMA
 // for every product on the CUDA cores: about 1000 tokens, 32 heads, 8000 8-bit
-// keys, blocks of 64, 104 us (2.4 T products/s, issue slots 54 % taken).  A
-// batch of tokens therefore fills a buffer, so that an MMA's latency (some 600
-// clk to its barrier) is paid once for all of them, and the loop stays small:
-// two chunks in flight in a warp; four ran at 155 us where two ran at 131, and
-// four warpgroups of one CTA an SM at 135.
+// keys, blocks of 64, 77 us (3.2 T products/s; 37 us with the epilogue's inner
+// loop taken out).  A batch of tokens therefore fills a buffer, so that an
+// MMA's latency (some 600 clk to its barrier) is paid once for all of them
+// (batches half as large, with two buffers a warpgroup, took 24 % longer), and
+// the loop stays small: four chunks in flight in a warp took 18 % longer than two.
 constexpr int IT = 128;                             // keys of a tile
 constexpr int I_QMAX = 32 * 1024;                   // query bytes of a group with several tokens, at most
 constexpr int GROUPS = 2;                           // epilogue warpgroups and TMEM buffers
@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     total = 0;
     for (int w = 0; w < kScoreThreads / 32; ++w) total += sh->sum[w];
     // Tiles of a run: an equal share, eight at least (a start costs about three).
-    span = static_cast<int>(min(0x7FFFFFFFull, max(8ull, (total + p.shares - 1) / p.shares)));
+    // In fp32, rounded up by one: every CTA gets the same number.
+    span = max(8, static_cast<int>(fminf(__fdividef(static_cast<float>(total), static_cast<float>(p.shares)), 1e9f)) + 1);
     int base = 0;
     for (int i0 = 0; i0 < p.B && base <= nth; i0 += kScoreThreads) {
       Scored w = {0, 0};
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   const int pos_first = static_cast<int>(p.cache_len[b]) + i0;   // position of the group's first token
   const int pos_last = pos_first + ng - 1;
   // Runs of a pair differ by one tile at most.
-  const int tile0 = static_cast<int>(static_cast<long long>(work.tiles) * sp / runs);
-  const int tiles = static_cast<int>(static_cast<long long>(work.tiles) * (sp + 1) / runs) - tile0;
+  const int each = work.tiles / runs, more = work.tiles - each * runs;
+  const int tile0 = each * sp + min(sp, more), tiles = each + (sp < more ? 1 : 0);
   const long long base0 = static_cast<long long>(tile0) * IT;
   const int n = base0 > pos_last ? 0 : static_cast<int>(min(static_cast<long long>(tiles), (pos_last - base0) / IT + 1));
   const int batches = (ng + p.batch - 1) / p.batch;
@@ -226,10 +227,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       tmem_relinquish();
     }
     // The group's weights, heads past the last one zero.
-    for (int i = threadIdx.x; i < ng * p.NP; i += kScoreThreads) {
-      const int gi = i / p.NP, h = i - gi * p.NP;
-      sw[i] = h < p.Hi ? __ldg(p.w + static_cast<long long>(t0 + gi) * p.Hi + h) : 0.f;
-    }
+    for (int i = warp; i < ng; i += kScoreThreads / 32)
+      for (int h = lane; h < p.NP; h += 32)
+        sw[i * p.NP + h] = h < p.Hi ? __ldg(p.w + static_cast<long long>(t0 + i) * p.Hi + h) : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -516,15 +516,18 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   }
   // Blocks past the run's last key, and a share of those past the sequence's
   // last tile: -infinity.
+  const int shift = __ffs(p.block) - 1;
   auto fill = [&](long long from, long long to) {
     to = min(to, static_cast<long long>(p.stride));
-    for (int i = 0; i < ng; ++i)
-      for (long long x = from + threadIdx.x; x < to; x += kScoreThreads)
-        p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
+    for (int i = warp; i < ng; i += kScoreThreads / 32)
+      for (long long x = from + lane; x < to; x += 32) p.scores[static_cast<long long>(t0 + i) * p.stride + x] = -kInf;
   };
-  fill((base0 + static_cast<long long>(n) * IT) / p.block, (base0 + static_cast<long long>(tiles) * IT) / p.block);
-  const long long end = static_cast<long long>(work.tiles) * IT / p.block, rest = max(0ll, p.stride - end);
-  fill(end + rest * sp / runs, end + rest * (sp + 1) / runs);
+  fill((base0 + static_cast<long long>(n) * IT) >> shift, (base0 + static_cast<long long>(tiles) * IT) >> shift);
+  const long long end = static_cast<long long>(work.tiles) * IT >> shift;
+  if (end < p.stride) {
+    const int rest = p.stride - static_cast<int>(end), part = rest / runs + 1;   // (the last shares may be empty)
+    fill(end + static_cast<long long>(part) * sp, end + static_cast<long long>(part) * (sp + 1));
+  }
 }
 
 // ============================================================ selection
