@@ -124,145 +124,197 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
          (static_cast<uint32_t>(pack_e4m3(b.x * ratio, b.y * ratio)) << 16);
 }
 
-// One CTA per new token (grid-stride).  All its threads rotate the token's
-// query heads; the CTA of the first new token of each touched block also
-// writes that block's new rows (one warp a row): first their largest value,
-// then, with the scale known, the codes (the rows are read again, from L1).
-// HBM-bound: per token 1152 bytes of latent read, 576 written, 256 of
-// frequencies, and 4 * 64 * H of queries read and written.  A thread's first
-// four query pieces (all of them with 128 heads) are read before anything is
-// known of the token, over the chain of reads that finds its position.
-__global__ void __launch_bounds__(kWriteThreads, 3)
-    cache_write_q8_kernel(const CacheWriteQ8Args a) {
-  __shared__ float s_amax[kWriteWarps];
-  __shared__ int s_info[3];   // position (-1: skip), rows to write as leader, first slot of the block
-  __shared__ long long s_row; // cache row of the token (-1: no page)
-  pdl_enter();
-  if (timed_out_before(a.status)) return;
+// Position of the last of n ascending offsets that is not above x (0 if none):
+// 32 probes of a warp at a time.
+__device__ __forceinline__ int last_offset(const uint32_t* __restrict__ at, int n, uint32_t x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+#pragma unroll 1
+  for (int hi = n; hi - lo > 1;) {
+    const int step = (hi - lo + 31) / 32;
+    const long long i = lo + static_cast<long long>(lane) * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(at + i) <= x));
+    lo += max(below - 1, 0) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Position of token t in its sequence b's context, or -1 (reported).
+__device__ __forceinline__ int token_position(const CacheWriteQ8Args& a, int t, int b) {
+  const uint32_t first = __ldg(a.iro + b), end = __ldg(a.iro + b + 1), cached = __ldg(a.cache_len + b);
+  if (first <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < end) {
+    const uint64_t p = static_cast<uint64_t>(cached) + (static_cast<uint32_t>(t) - first);
+    if (p < static_cast<uint64_t>(a.max_seq_len)) return static_cast<int>(p);
+  }
+  set_status(a.status, MLA_DEV_BAD_OFFSETS);
+  return -1;
+}
+
+// The first a.row_ctas CTAs write the cache, each the rows of all blocks that
+// begin (or are entered) at one of its a.chunk tokens; the others rotate the
+// query heads, a token at a time.  HBM-bound: per token 1152 bytes of latent
+// read, 576 written, 256 of frequencies, and 4 * 64 * H of queries read and
+// written.
+//
+// Rows: a block's rows are taken by a group of warps (eight, or as many as the
+// block has slots), a row a warp: first their largest value, then, with the
+// scale known, the codes (the rows are read again, from L1).  64 rows take some
+// 25 us that way, bound by latency, so these CTAs come first and run under the
+// others: with the two kinds of work in one CTA per token, 8 prompts of 256 to
+// 2048 tokens, 128 heads, took 75 us, now 57 (5.4 TB/s).
+//
+// Queries: a thread's first four pieces (all of them with 128 heads) are read
+// before anything is known of the token, over the chain of reads that finds its
+// position.
+constexpr int kMaxChunk = 128;   // tokens of a row CTA
+
+struct RowJob {
+  long long row;                 // cache row of the first token
+  int t, pos, slot, rows;        // first token, its position and slot in the block, rows to write
+};
+struct WriteSmem {
+  float amax[kWriteWarps];
+  int jobs, pos;
+  RowJob job[kMaxChunk];
+};
+
+__device__ __forceinline__ void write_rows(const CacheWriteQ8Args& a, WriteSmem& sh, int t0) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint16_t* latent = static_cast<const uint16_t*>(a.kv_latent);
   uint8_t* cache = static_cast<uint8_t*>(a.kv_cache);
-
-  constexpr int QU = 4;       // query pieces of a thread in flight
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    // q: piece m of head h holds rope values 8m .. 8m+7 (pairs 4m .. 4m+3).
-    uint16_t* qt = static_cast<uint16_t*>(a.q) + static_cast<size_t>(t) * a.H * 192 + 128 + 8 * (tid & 7);
-    const int pieces = a.q != nullptr ? 8 * a.H : 0;
-    auto piece = [&](int i) { return reinterpret_cast<uint4*>(qt + static_cast<size_t>(i >> 3) * 192); };
-    uint4 x[QU];
-    auto load = [&](int i0) {
-#pragma unroll
-      for (int k = 0; k < QU; ++k)
-        if (i0 + k * kWriteThreads < pieces) x[k] = *piece(i0 + k * kWriteThreads);
-    };
-    load(tid);
-    if (warp == 0) {
-      int lo = 0;             // largest b with iro[b] <= t, 32 probes at a time
-      for (int hi = a.B; hi - lo > 1;) {
-        const int step = (hi - lo + 31) / 32;
-        const long long at = lo + static_cast<long long>(tid) * step;
-        const int below = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(a.iro + at) <= static_cast<uint32_t>(t)));
-        lo += max(below - 1, 0) * step;
-        hi = min(hi, lo + step);
-      }
-      if (tid == 0) {
-        const uint32_t first = a.iro[lo], end = a.iro[lo + 1];
-        int pos = -1, rows = 0, slot = 0;
-        long long row = -1;
-        if (first <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < end) {
-          const uint64_t p = static_cast<uint64_t>(a.cache_len[lo]) + (static_cast<uint32_t>(t) - first);
-          if (p < static_cast<uint64_t>(a.max_seq_len)) {
-            pos = static_cast<int>(p);
-            slot = pos % a.scale_block;
-            if (slot == 0 || static_cast<uint32_t>(t) == first) {
-              // This block's new rows: up to its end, the sequence's last new
-              // token, the last row of the call and the last position.
-              rows = a.scale_block - slot;
-              rows = static_cast<int>(min(static_cast<uint32_t>(rows), min(end, static_cast<uint32_t>(a.T)) - t));
-              rows = min(rows, a.max_seq_len - pos);
-              const int pidx = pos / a.page_size;
-              const int page = pidx < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + pidx] : -1;
-              if (page >= 0 && page < a.num_pages)
-                row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
-              else
-                set_status(a.status, MLA_DEV_BAD_PAGE);
-            }
-          } else {
-            set_status(a.status, MLA_DEV_BAD_OFFSETS);
-          }
+  if (tid == 0) sh.jobs = 0;
+  __syncthreads();
+  if (32 * warp < a.chunk) {
+    const int t = t0 + tid;
+    int b = last_offset(a.iro, a.B, static_cast<uint32_t>(t0));
+    if (tid < a.chunk && t < a.T) {
+      while (b + 1 < a.B && __ldg(a.iro + b + 1) <= static_cast<uint32_t>(t)) ++b;
+      const int pos = token_position(a, t, b);
+      const int slot = pos < 0 ? 1 : pos % a.scale_block;
+      const uint32_t first = __ldg(a.iro + b), end = __ldg(a.iro + b + 1);
+      if (pos >= 0 && (slot == 0 || static_cast<uint32_t>(t) == first)) {
+        // This block's new rows: up to its end, the sequence's last new
+        // token, the last row of the call and the last position.
+        int rows = a.scale_block - slot;
+        rows = static_cast<int>(min(static_cast<uint32_t>(rows), min(end, static_cast<uint32_t>(a.T)) - t));
+        rows = min(rows, a.max_seq_len - pos);
+        const int pidx = pos / a.page_size;
+        const int page = pidx < a.max_pages ? __ldg(a.page_table + static_cast<size_t>(b) * a.max_pages + pidx) : -1;
+        if (page >= 0 && page < a.num_pages) {
+          RowJob& j = sh.job[atomicAdd(&sh.jobs, 1)];   // (in any order: jobs do not meet)
+          j.row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+          j.t = t;
+          j.pos = pos;
+          j.slot = slot;
+          j.rows = rows;
         } else {
-          set_status(a.status, MLA_DEV_BAD_OFFSETS);
+          set_status(a.status, MLA_DEV_BAD_PAGE);
         }
-        s_info[0] = pos;
-        s_info[1] = row >= 0 ? rows : 0;
-        s_info[2] = slot;
-        s_row = row;
       }
     }
-    __syncthreads();
-    const int pos = s_info[0], rows = s_info[1], slot = s_info[2];
-    const long long row0 = s_row;
-    if (rows > 0) {
-      const uint16_t* src = latent + static_cast<size_t>(t) * 576;
-      RowValues v;
-      float m = 0.f;
-      for (int r = warp; r < rows; r += kWriteWarps) {
-        v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(pos + r) * 64, a.eps);
-        m = fmaxf(m, row_amax(v));
-      }
-      if ((tid & 31) == 0) s_amax[warp] = m;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWriteWarps; ++w) m = fmaxf(m, s_amax[w]);
-      float scale = pow2_scale(m);
-      float* sp = a.kv_scales + row0 / a.scale_block;
-      if (slot > 0) {
-        // Rows before, written by earlier calls under the block's scale.
-        const float was = *sp;
-        if (was > 0.f && was < __int_as_float(0x7f800000)) {
-          if (was >= scale) {
-            scale = was;
-          } else {
-            uint4* old = reinterpret_cast<uint4*>(cache + static_cast<size_t>(row0 - slot) * 576);
-            const float ratio = was / scale;
-            for (int i = tid; i < slot * 36; i += kWriteThreads) {
-              const uint4 c = old[i];
-              old[i] = make_uint4(requantise4(c.x, ratio), requantise4(c.y, ratio), requantise4(c.z, ratio),
-                                  requantise4(c.w, ratio));
-            }
+  }
+  __syncthreads();
+  const int width = a.group_warps, group = warp / width, part = warp - group * width;
+  const int threads = 32 * width, me = tid - group * threads;
+  auto sync = [&] { asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(group + 1), "r"(threads) : "memory"); };
+#pragma unroll 1
+  for (int i = group; i < sh.jobs; i += kWriteWarps / width) {
+    const RowJob j = sh.job[i];
+    const uint16_t* src = latent + static_cast<size_t>(j.t) * 576;
+    RowValues v;
+    float m = 0.f;
+#pragma unroll 1
+    for (int r = part; r < j.rows; r += width) {
+      v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(j.pos + r) * 64, a.eps);
+      m = fmaxf(m, row_amax(v));
+    }
+    if ((tid & 31) == 0) sh.amax[warp] = m;
+    sync();
+    for (int w = 0; w < width; ++w) m = fmaxf(m, sh.amax[group * width + w]);
+    float scale = pow2_scale(m);
+    float* sp = a.kv_scales + j.row / a.scale_block;
+    if (j.slot > 0) {
+      // Rows before, written by earlier calls under the block's scale.
+      const float was = *sp;
+      if (was > 0.f && was < __int_as_float(0x7f800000)) {
+        if (was >= scale) {
+          scale = was;
+        } else {
+          uint4* old = reinterpret_cast<uint4*>(cache + static_cast<size_t>(j.row - j.slot) * 576);
+          const float ratio = was / scale;
+          for (int x = me; x < j.slot * 36; x += threads) {
+            const uint4 c = old[x];
+            old[x] = make_uint4(requantise4(c.x, ratio), requantise4(c.y, ratio), requantise4(c.z, ratio),
+                                requantise4(c.w, ratio));
           }
         }
       }
-      __syncthreads();   // every thread has read the old scale
-      if (tid == 0) *sp = scale;
-      const float inv = 1.0f / scale;   // exact for a power of two
-      for (int r = warp; r < rows; r += kWriteWarps) {
-        if (rows > kWriteWarps)
-          v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(pos + r) * 64, a.eps);
-        store_row(cache + static_cast<size_t>(row0 + r) * 576, v, inv);
-      }
     }
-    if (pos >= 0 && pieces > 0) {
-      const float4* fr = reinterpret_cast<const float4*>(a.freqs + static_cast<size_t>(pos) * 64) + 2 * (tid & 7);
-      const float4 fa = __ldg(fr), fb = __ldg(fr + 1);
-      for (int i0 = tid;;) {
+    sync();                      // every thread has read the old scale (and the maxima)
+    if (me == 0) *sp = scale;
+    const float inv = 1.0f / scale;   // exact for a power of two
+#pragma unroll 1
+    for (int r = part; r < j.rows; r += width) {
+      if (j.rows > width)
+        v = row_values(src + static_cast<size_t>(r) * 576, a.gamma, a.freqs + static_cast<size_t>(j.pos + r) * 64, a.eps);
+      store_row(cache + static_cast<size_t>(j.row + r) * 576, v, inv);
+    }
+  }
+}
+
+__device__ __forceinline__ void rotate_queries(const CacheWriteQ8Args& a, WriteSmem& sh, int t) {
+  constexpr int QU = 4;          // query pieces of a thread in flight
+  const int tid = threadIdx.x;
+  // Piece m of head h holds rope values 8m .. 8m+7 (pairs 4m .. 4m+3).
+  uint16_t* qt = static_cast<uint16_t*>(a.q) + static_cast<size_t>(t) * a.H * 192 + 128 + 8 * (tid & 7);
+  const int pieces = 8 * a.H;
+  auto piece = [&](int i) { return reinterpret_cast<uint4*>(qt + static_cast<size_t>(i >> 3) * 192); };
+  uint4 x[QU];
+  auto load = [&](int i0) {
 #pragma unroll
-        for (int k = 0; k < QU; ++k) {
-          if (i0 + k * kWriteThreads < pieces) {
-            const float2 a0 = rotate2(bf16_lo(x[k].x), bf16_hi(x[k].x), fa.x, fa.y);
-            const float2 a1 = rotate2(bf16_lo(x[k].y), bf16_hi(x[k].y), fa.z, fa.w);
-            const float2 a2 = rotate2(bf16_lo(x[k].z), bf16_hi(x[k].z), fb.x, fb.y);
-            const float2 a3 = rotate2(bf16_lo(x[k].w), bf16_hi(x[k].w), fb.z, fb.w);
-            *piece(i0 + k * kWriteThreads) =
-                make_uint4(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y), pack_bf16(a2.x, a2.y), pack_bf16(a3.x, a3.y));
-          }
+    for (int k = 0; k < QU; ++k)
+      if (i0 + k * kWriteThreads < pieces) x[k] = *piece(i0 + k * kWriteThreads);
+  };
+  load(tid);
+  if (tid < 32) {
+    const int b = last_offset(a.iro, a.B, static_cast<uint32_t>(t));
+    if (tid == 0) sh.pos = token_position(a, t, b);
+  }
+  __syncthreads();
+  const int pos = sh.pos;
+  if (pos >= 0) {
+    const float4* fr = reinterpret_cast<const float4*>(a.freqs + static_cast<size_t>(pos) * 64) + 2 * (tid & 7);
+    const float4 fa = __ldg(fr), fb = __ldg(fr + 1);
+    for (int i0 = tid;;) {
+#pragma unroll
+      for (int k = 0; k < QU; ++k) {
+        if (i0 + k * kWriteThreads < pieces) {
+          const float2 a0 = rotate2(bf16_lo(x[k].x), bf16_hi(x[k].x), fa.x, fa.y);
+          const float2 a1 = rotate2(bf16_lo(x[k].y), bf16_hi(x[k].y), fa.z, fa.w);
+          const float2 a2 = rotate2(bf16_lo(x[k].z), bf16_hi(x[k].z), fb.x, fb.y);
+          const float2 a3 = rotate2(bf16_lo(x[k].w), bf16_hi(x[k].w), fb.z, fb.w);
+          *piece(i0 + k * kWriteThreads) =
+              make_uint4(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y), pack_bf16(a2.x, a2.y), pack_bf16(a3.x, a3.y));
         }
-        i0 += QU * kWriteThreads;
-        if (i0 >= pieces) break;
-        load(i0);
       }
+      i0 += QU * kWriteThreads;
+      if (i0 >= pieces) break;
+      load(i0);
     }
-    __syncthreads();   // the shared words are rewritten for the next token
+  }
+  __syncthreads();               // the position is rewritten for the next token
+}
+
+__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_q8_kernel(const CacheWriteQ8Args a) {
+  __shared__ WriteSmem sh;
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int c = blockIdx.x;
+  if (c < a.row_ctas) {
+    write_rows(a, sh, c * a.chunk);
+  } else {
+    for (int t = c - a.row_ctas; t < a.T; t += gridDim.x - a.row_ctas) rotate_queries(a, sh, t);
   }
 }
 
@@ -344,10 +396,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const GatherQ
 
 }  // namespace
 
-cudaError_t launch_cache_write_q8(const CacheWriteQ8Args& a, cudaStream_t stream) {
-  if (a.T <= 0) return cudaSuccess;
-  const int grid = a.T < 16 * sm_count() ? a.T : 16 * sm_count();
-  return launch_pdl(cache_write_q8_kernel, dim3(grid), dim3(kWriteThreads), 0, stream, a);
+cudaError_t launch_cache_write_q8(const CacheWriteQ8Args& args, cudaStream_t stream) {
+  if (args.T <= 0) return cudaSuccess;
+  CacheWriteQ8Args a = args;
+  // Tokens of a row CTA: a block's, in whole warps, or eight small blocks.
+  a.chunk = a.scale_block > 8 ? (a.scale_block + 31) / 32 * 32 : 8;
+  a.group_warps = 1;
+  while (a.group_warps < kWriteWarps && 2 * a.group_warps <= a.scale_block) a.group_warps *= 2;
+  a.row_ctas = (a.T + a.chunk - 1) / a.chunk;
+  const int rotating = a.q == nullptr ? 0 : (a.T < 16 * sm_count() ? a.T : 16 * sm_count());
+  return launch_pdl(cache_write_q8_kernel, dim3(a.row_ctas + rotating), dim3(kWriteThreads), 0, stream, a);
 }
 
 cudaError_t launch_gather_q8(const GatherQ8Args& a, cudaStream_t stream) {

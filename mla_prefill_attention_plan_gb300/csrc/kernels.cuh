@@ -190,6 +190,8 @@ struct CacheWriteQ8Args {
   int num_pages, page_size, max_pages, scale_block, B, H, T, max_seq_len;
   float eps;
   int32_t* status;
+  // Set by the launch: CTAs that write rows, the tokens of one, warps that share a block.
+  int row_ctas, chunk, group_warps;
 };
 cudaError_t launch_cache_write_q8(const CacheWriteQ8Args& a, cudaStream_t stream);
 
