@@ -672,8 +672,9 @@ size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, 
  * max_seq_len (of indices_stride) of 2^31 or more.  Device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens or < input_row_offsets[b], a sequence
  * that begins before an earlier one ends, or a dense context longer than
- * max_seq_len: sequence b left out), MLA_DEV_BAD_PAGE (a page id or listed row out of range: the result of
- * the rows that see it is not meaningful), MLA_DEV_TIMEOUT.
+ * max_seq_len or 2^31 - 8192: sequence b left out), MLA_DEV_BAD_PAGE (a page id
+ * or listed row out of range: the result of the rows that see it is not
+ * meaningful), MLA_DEV_TIMEOUT.
  */
 mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
                            const uint32_t* cache_lengths, const void* kv_cache, const float* kv_scales,
@@ -716,9 +717,10 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
  * Errors: host MLA_ERR_DTYPE, MLA_ERR_GEOMETRY (num_index_heads outside
  * 1..128), MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens or a context longer than
- * max_seq_len: sequence b left out), MLA_DEV_BAD_PAGE (the block's score is not
- * meaningful), MLA_DEV_TIMEOUT.  Rows of tokens outside every sequence are not
- * written, nor are tokens past max_new_tokens of their sequence.
+ * max_seq_len or 2^31 - 8192: sequence b left out), MLA_DEV_BAD_PAGE (the
+ * block's score is not meaningful), MLA_DEV_TIMEOUT.  Rows of tokens outside
+ * every sequence are not written, nor are tokens past max_new_tokens of their
+ * sequence.
  */
 mla_status_t mla_index_scores(float* scores, const void* index_q, const float* index_w, const void* index_cache,
                               const float* index_scales, const uint32_t* input_row_offsets,

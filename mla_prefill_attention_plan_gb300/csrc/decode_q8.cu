@@ -1780,7 +1780,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   plan.B = a.B;
   plan.H = H;
   plan.T = T;
-  plan.max_seq = a.max_seq;
+  plan.max_seq = std::min(a.max_seq, kMaxContext);
   plan.indices_stride = a.indices_stride;
   plan.sparse = a.indices != nullptr ? 1 : 0;
   plan.item_rows = rows * members;

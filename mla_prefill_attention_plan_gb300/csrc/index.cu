@@ -833,7 +833,7 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   p.Hi = a.Hi;
   p.NP = (a.Hi + 15) / 16 * 16;
   p.T = a.T;
-  p.max_seq = a.max_seq;
+  p.max_seq = std::min(a.max_seq, kMaxContext);
   p.stride = a.stride;
   p.status = a.status;
   const int stage = kb * IT * 128;
@@ -888,6 +888,8 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
+  IndexSelectArgs b = a;
+  b.max_seq = std::min(a.max_seq, kMaxContext);
   // One CTA a token, or, where the tokens leave SMs idle and the rows are
   // long, up to 16 (at least 4096 scores each): two tokens of 131000 scores
   // take 22 us with eight and 19 with 16.
@@ -927,7 +929,7 @@ cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream) {
     }
   }
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, index_select_kernel, a, fast_divisor(a.page_size), cached);
+  return cudaLaunchKernelEx(&cfg, index_select_kernel, b, fast_divisor(a.page_size), cached);
 }
 
 }  // namespace mla

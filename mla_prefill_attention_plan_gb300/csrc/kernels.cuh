@@ -49,6 +49,10 @@ inline FastDiv fast_divisor(int d) {
   return f;
 }
 
+// Longest context of the 8-bit decode, the key scores and the selection: room
+// for a few tiles past it in a 32-bit position.
+constexpr int kMaxContext = 0x7FFFFFFF - 8191;
+
 cudaError_t launch_plan(uint32_t* bro, uint32_t* co, int32_t* bl, const uint32_t* iro,
                         const uint32_t* cache_len, int B, int max_chunks, uint32_t S,
                         int32_t* status, cudaStream_t stream);

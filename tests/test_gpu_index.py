@@ -276,16 +276,17 @@ def test_select_bad_page():
     assert st.item() == mla.MLA_DEV_BAD_PAGE and rows.tolist() == [[-1, -1, -1, -1]] and cnt.item() == 4
 
 
-def test_select_replays_bit_for_bit():
-    n, L = 3, 20000
+@pytest.mark.parametrize("n,L", [(3, 20000), (1, 140000)])
+def test_select_replays_bit_for_bit(n, L):
     s = torch.randn(n, L, generator=torch.Generator().manual_seed(0)).to(DEV)
     rows = torch.zeros(n, 2048, dtype=torch.int32, device=DEV)
     cnt = torch.zeros(n, dtype=torch.int32, device=DEV)
-    args = (rows, cnt, s, i32([0, 1, 2, 3]), i32([L - 1] * 3), i32(np.zeros((3, L // 100 + 1))), 1, 100, L // 100 + 1, 1,
+    args = (rows, cnt, s, i32(range(n + 1)), i32([L - 1] * n), i32(np.zeros((n, L // 100 + 1))), 1, 100, L // 100 + 1, 1,
             2048, 1, n, n, L, L, 2048)
     mla.check(mla.mla_index_select(*args))
     torch.cuda.synchronize()
     ref = rows.clone()
+    assert cnt.tolist() == [2048] * n
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         mla.check(mla.mla_index_select(*args))

@@ -662,6 +662,13 @@ def test_decode_mostly_empty_batch():
     Decode(new, cached, 8, 16, 1).check()
 
 
+def test_decode_without_lse():
+    d = Decode([1, 2], [300, 140], 40, 128, 8)
+    out, lse = d.run(lse=False)
+    assert lse is None
+    compare(out, None, *d.reference())
+
+
 def test_decode_max_new_above_every_sequence():
     d = Decode([1, 2], [300, 140], 8, 128, 8)
     compare(*d.run(max_new=50), *d.reference())
