@@ -668,7 +668,7 @@ size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, 
  * as mla_decode, MLA_ERR_ARG for kv_scales or scale_block as above, for more
  * than 16383 heads or 32768 pieces and where 32-bit indexes of the work would
  * not do: total_q_tokens * num_heads or max_new_tokens * num_heads of 2^29 or
- * more, (total_q_tokens + total_q_tokens * num_heads / 32) times the tiles of
+ * more, (total_q_tokens + total_q_tokens * num_heads / 16) times the tiles of
  * max_seq_len (of indices_stride) of 2^31 or more.  Device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens or < input_row_offsets[b], a sequence
  * that begins before an earlier one ends, or a dense context longer than

@@ -684,9 +684,9 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
   const int pieces = num_partitions > 0
                          ? num_partitions
                          : mla::decode_q8_pieces(batch_size, num_heads, max_new_tokens, max_keys);
-  // Units of the plan (one key tile of an item each, items of 32 rows or more) and CTAs.
+  // Units of the plan (one key tile of an item each, items of 16 rows or more) and CTAs.
   const long long tiles = ((d_indices != nullptr ? indices_stride : max_seq_len) + 127ll) / 128;
-  const long long items = total_q_tokens + (rows + 31) / 32;
+  const long long items = total_q_tokens + (rows + 15) / 16;
   if (items * tiles >= (1ll << 31) || pieces > (1 << 15) || 512 * (items + pieces) >= (1ll << 31))
     return MLA_ERR_ARG;
   const mla::DecodeQ8Layout L = mla::decode_q8_layout(total_q_tokens, num_heads, pieces);

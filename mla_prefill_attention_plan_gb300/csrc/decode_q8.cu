@@ -36,7 +36,7 @@
 // an item leaves a partial result in the slot (piece + item), which no other
 // (piece, item) pair has.
 #include <algorithm>
-#include <mutex>
+#include <type_traits>
 
 #include "kernels.cuh"
 
@@ -426,39 +426,41 @@ constexpr int ROPE = BK * 64;               // its rope part, 8 KB
 constexpr float kShift = 5.0f;              // weights are kept around 2^5 of e4m3's 448
 constexpr float kGrow = 8.0f;               // and may grow to 2^8 before the reference moves
 
-// A tile has 64 (WIDE) or 32 query rows.  The query operand holds both terms,
-// the first terms' rows above the second's, so one MMA of N = 128 or 64 gives
-// both products and the softmax adds them.  The weights' terms: 32 rows lie side
-// by side in one operand of N = 64 and O has two halves, added when it is read;
-// for 64 rows that would fill the whole TMEM with O, so there the terms are two
-// MMAs of N = 64 on the same accumulator.  (An MMA of M = 128 from shared
+// A tile has 64, 32 or 16 query rows.  The query operand holds both terms,
+// the first terms' rows above the second's, so one MMA of N = 128, 64 or 32
+// gives both products and the softmax adds them.  The weights' terms: up to 32
+// rows lie side by side in one operand and O has two halves, added when it is
+// read; for 64 rows that would fill the whole TMEM with O, so there the terms are
+// two MMAs of N = 64 on the same accumulator.  (An MMA of M = 128 from shared
 // memory takes 40, 48, 64 clk at N = 32, 64, 128, measured: half of it at
-// N = 64 is its A operand's 128 bytes a clk.)  The smaller query buffer leaves
-// room for two more key slots.
-template <bool WIDE>
+// N = 64 is its A operand's 128 bytes a clk.)  The smaller the query buffer, the
+// more key slots.
+template <int R>
 struct Shape {
-  static constexpr int ROWS = WIDE ? 64 : 32;
+  static constexpr int ROWS = R;
+  static constexpr bool WIDE = R == 64;
   static constexpr int GROUPS = ROWS / 16;                // softmax warpgroups, 16 rows each
   static constexpr int THREADS = 96 + 128 * GROUPS;       // producer, MMA, softmax and scale warps
   static constexpr int NQ = 2 * ROWS;                     // score columns of a tile
-  static constexpr int SLOTS = WIDE ? 4 : 5;
-  static constexpr int ROPES = WIDE ? 1 : 2;
+  static constexpr int SLOTS = R == 64 ? 4 : (R == 32 ? 5 : 6);
+  static constexpr int ROPES = R == 32 ? 2 : 1;
   static constexpr int QBLOCK = NQ * 128;                 // query operand, 128 columns
   static constexpr int QBYTES = NQ * 576;
-  static constexpr int PTERM = BK * 64;
+  static constexpr int NP = WIDE ? 64 : 2 * ROWS;         // columns of a value MMA, bytes of a key's weights
+  static constexpr int PTERM = BK * NP;
   static constexpr int PBYTES = WIDE ? 2 * PTERM : PTERM;
   static constexpr int AT_ROPE = SLOTS * SLOT;
   static constexpr int AT_Q = AT_ROPE + ROPES * ROPE;
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
   static constexpr int TOTAL = AT_BAR + 3 * 1024;
-  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x 64 columns
-  static constexpr uint32_t TM_COLS = 512;
-  static_assert(TOTAL <= 227 * 1024 && TM_O + 256 <= TM_COLS, "shared memory, TMEM");
+  static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x NP columns
+  static constexpr uint32_t TM_COLS = R == 16 ? 256 : 512;
+  static_assert(TOTAL <= 227 * 1024 && TM_O + 4 * NP <= TM_COLS, "shared memory, TMEM");
 };
 
 struct AttnSmem {
-  uint64_t k_full[5], k_empty[5];     // slots
+  uint64_t k_full[6], k_empty[6];     // slots
   uint64_t r_full[2], r_empty[2];     // rope parts
   uint64_t fixed;                     // a masked tile's values have been cleaned
   uint64_t q_full, q_free, s_full[2], s_free[2], p_full, pv_done, o_free, drain, group[4];
@@ -638,14 +640,14 @@ __device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-constexpr int kSparseProducers = 2;
+constexpr int kSparseProducers = 2;   // warp 0 and another one
 
 // TWICE: a tile's latent blocks are loaded for its scores and again (from L2)
 // for its values, in the order in which the MMAs take them: scores 0, scores 1,
 // values 0, scores 2, values 1, ...  The ring then holds nothing but loads in
 // flight.  Otherwise a tile stays in its slots from its scores to its values:
-// half the reads of L2, but a slot is held through the softmax.  32 rows have
-// room for two and a half tiles, and 32 sequences of 16384 to 32768 keys, 16
+// half the reads of L2, but a slot is held through the softmax.  Tiles of 32
+// rows have room for two and a half, and 32 sequences of 16384 to 32768 keys, 16
 // heads, take 113 us so, against 139 with every block loaded twice.  64 rows
 // have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, take 311
 // us twice and 322 once; with listed rows, whose copies cost more, 91 and 89.
@@ -653,17 +655,17 @@ constexpr int kSparseProducers = 2;
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
 // multiple of 8) warps copy the rows with cp.async.
-template <bool DENSE, bool WIDE>
-__global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSparseProducers), 1)
+template <bool DENSE, int R>
+__global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparseProducers - 1)), 1)
     q8_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qr_map,
                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
                    const Q8Params p) {
-  using C = Shape<WIDE>;
+  using C = Shape<R>;
   constexpr int ROWS = C::ROWS, GROUPS = C::GROUPS, SLOTS = C::SLOTS, ROPES = C::ROPES, NQ = C::NQ;
-  constexpr bool TWICE = WIDE && DENSE;
+  constexpr bool WIDE = C::WIDE, TWICE = WIDE && DENSE;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_COLS = C::TM_COLS;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, NQ, false, false);
-  constexpr uint32_t IDESC_PV = idesc_e4m3(128, 64, true, true);
+  constexpr uint32_t IDESC_PV = idesc_e4m3(128, C::NP, true, true);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;   // every byte is used: the base itself is a multiple of 1024 (checked below)
   AttnSmem* sh = reinterpret_cast<AttnSmem*>(smem + C::AT_BAR);
@@ -720,7 +722,32 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
   Walk wk;
   if (!dead) wk = walk_begin(p, piece); else wk.u = wk.u1 = 0;
 
-  if (warp == 0) {
+  // A segment's queries: warp 0, or, where that copies rows, the scales' warp.
+  auto load_q = [&](const Segment& of, uint32_t seg) -> bool {
+    if (seg > 0 && !wait_warp(smem_u32(&sh->q_free), (seg - 1) & 1, status, abort_flag)) return false;
+    if (elect_one()) {
+      const uint32_t qf = smem_u32(&sh->q_full);
+      mbar_expect_tx(qf, C::QBYTES);
+#pragma unroll
+      for (int term = 0; term < 2; ++term) {
+        // The second term's rows follow the first's.
+        const uint32_t base = smem_u32(smem + C::AT_Q);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tma_load_2d(base + c * C::QBLOCK + term * ROWS * 128, &q_map, qf, term * 576 + c * 128, of.row0);
+        tma_load_2d(base + 4 * C::QBLOCK + term * ROWS * 64, &qr_map, qf, term * 576 + 512, of.row0);
+      }
+    }
+    __syncwarp();
+    return true;
+  };
+  // The last queries land before the CTA leaves.
+  auto drain_q = [&](uint32_t seg) {
+    volatile int never = 0;
+    if (seg > 0) wait_warp(smem_u32(&sh->q_full), (seg - 1) & 1, status, &never);
+  };
+
+  if (DENSE && warp == 0) {
     // ------------------------------------------------------------ queries, and the keys' TMA loads
     // One elected lane waits, counts and issues for a whole tile, in straight
     // code; the warp only looks up the rows (a warp-wide step for every block
@@ -731,25 +758,6 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
     const int nbox = BK / p.box;                      // runs of a tile, 16 at most
     const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
     while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
-      auto load_q = [&]() -> bool {
-        if (seg > 0 && !wait_warp(smem_u32(&sh->q_free), (seg - 1) & 1, status, abort_flag)) return false;
-        if (elect_one()) {
-          const uint32_t qf = smem_u32(&sh->q_full);
-          mbar_expect_tx(qf, C::QBYTES);
-#pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            // The second term's rows follow the first's.
-            const uint32_t base = smem_u32(smem + C::AT_Q);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tma_load_2d(base + c * C::QBLOCK + term * ROWS * 128, &q_map, qf, term * 576 + c * 128, sg.row0);
-            tma_load_2d(base + 4 * C::QBLOCK + term * ROWS * 64, &qr_map, qf, term * 576 + 512, sg.row0);
-          }
-        }
-        __syncwarp();
-        ++seg;
-        return true;
-      };
       if constexpr (DENSE) {
         // Lane l has run l % nbox of tile j0 + l / nbox; the next tiles' table
         // entries are read while these are loaded.
@@ -762,7 +770,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
         // A later segment's queries wait for the scores before them; its first
         // keys need not.
         const bool late = seg > 0;
-        if (!late) ok = load_q();
+        if (!late) ok = load_q(sg, seg++);
         int base = 0, row = 0;                            // first tile of the batch, this lane's run in it
         auto runs = [&](int j) { return j + 1 < n ? nbox : (sg.key1 - (sg.key0 + j * BK) + p.box - 1) / p.box; };
         // One elected lane: a tile's two slots, and its rope part.
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
             if (late && j0 == 0) good = blocks(0, true);
           }
           ok = __all_sync(0xffffffffu, good);
-          if (late && j0 == 0 && ok && (ok = load_q())) {
+          if (late && j0 == 0 && ok && (ok = load_q(sg, seg++))) {
             if (elect_one())
               for (int j = 1; j < j1 && good; ++j) good = blocks(j, true) && (!TWICE || blocks(j - 1, false));
             ok = __all_sync(0xffffffffu, good);
@@ -825,8 +833,6 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           if (elect_one()) good = blocks(n - 1, false);
           ok = __all_sync(0xffffffffu, good);
         }
-      } else {
-        ok = load_q();
       }
     }
     // Every load lands before the CTA leaves: the last use of each slot.  (The
@@ -845,8 +851,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
       }
       __syncwarp();
     }
-    volatile int never_q = 0;
-    if (seg > 0) wait_warp(smem_u32(&sh->q_full), (seg - 1) & 1, status, &never_q);
+    drain_q(seg);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // One elected lane, from descriptors that only need an addition (computed
@@ -856,7 +861,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
       const uint64_t ar0 = sdesc(smem_u32(smem + C::AT_ROPE), 16, 512, kSwizzle64);
       const uint64_t b0 = sdesc(smem_u32(smem + C::AT_Q), 16, 1024);
       const uint64_t br0 = sdesc(smem_u32(smem + C::AT_Q + 4 * C::QBLOCK), 16, 512, kSwizzle64);
-      const uint64_t w0 = sdesc(smem_u32(smem + C::AT_P), 16, 512, kSwizzle64);
+      const uint64_t w0 = sdesc(smem_u32(smem + C::AT_P), 16, 8 * C::NP, C::NP == 64 ? kSwizzle64 : kSwizzle32);
       uint32_t seg = 0, g0 = 0, masked_tiles = 0;      // segments done, tiles before this one's, cleaned tiles
       uint32_t sk = 0, tk = 0;                         // slot and turn of the next latent block
       uint32_t vk = 0;                                 // loaded once: slot of the next values
@@ -909,9 +914,9 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // Block 2 c + kk / 4, 32 keys a step: both operands MN-major, groups of 8 keys
-            // 2048 (keys) and 512 (weights) bytes apart.
-            const uint64_t av = ad + (kk >> 2) * 64 + (kk & 3) * (4 * GROUP >> 4), wv = w0 + (kk & 3) * 128;
-            const uint32_t d = tmem + TM_O + (2 * c + (kk >> 2)) * 64;
+            // 2048 (keys) and 8 NP (weights) bytes apart.
+            const uint64_t av = ad + (kk >> 2) * 64 + (kk & 3) * (4 * GROUP >> 4), wv = w0 + (kk & 3) * (4 * 8 * C::NP >> 4);
+            const uint32_t d = tmem + TM_O + (2 * c + (kk >> 2)) * C::NP;
             mma_f8_ss(d, av, wv, IDESC_PV, !first || (kk & 3) != 0);
             if (WIDE) mma_f8_ss(d, av, wv + (C::PTERM >> 4), IDESC_PV, 1);
           }
@@ -943,7 +948,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
       wait_one(smem_u32(&sh->drain), 0, status, &never);
     }
     __syncwarp();
-  } else if (warp < 2 + 4 * GROUPS) {
+  } else if (warp >= 2 && warp < 2 + 4 * GROUPS) {
     // ------------------------------------------------------------ softmax (thread = key), epilogue
     // Warpgroups with all 128 keys and 16 of the tile's query rows each.  The
     // code of a tile is kept small and there once: with 32 rows a thread and a
@@ -1092,7 +1097,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 #pragma unroll 1
               for (int cb = 0; cb < (WIDE ? 4 : 8); ++cb) {
                 uint32_t r[16];
-                const uint32_t ta = tmem + lane_off + TM_O + cb * (WIDE ? 64 : 32) + c0;
+                const uint32_t ta = tmem + lane_off + TM_O + cb * ROWS + c0;
                 tmem_ld16(ta, r);
                 tmem_ld_wait();
 #pragma unroll
@@ -1147,13 +1152,13 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
         if (fail) break;
 #pragma unroll
         for (int c = 0; c < 8; ++c) l[c] = __fadd2_rn(l[c], t[c]);
-        // Key-major rows of 64 bytes (64-byte swizzle): chunk wg, and the second
-        // term in a buffer of its own (wide) or two chunks on.
+        // Key-major rows of NP bytes (64- or 32-byte swizzle): chunk wg, and the
+        // second term in a buffer of its own (wide) or ROWS bytes on.
         if (mine > 0) {
-          const int sw = (key >> 1) & 3;
-          uint8_t* prow = pbuf + key * 64;
+          const int sw = C::NP == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
+          uint8_t* prow = pbuf + key * C::NP;
           *reinterpret_cast<uint4*>(prow + ((wg ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(prow + (WIDE ? C::PTERM + ((wg ^ sw) << 4) : ((2 + wg) ^ sw) << 4)) =
+          *reinterpret_cast<uint4*>(prow + (WIDE ? C::PTERM + ((wg ^ sw) << 4) : ((ROWS / 16 + wg) ^ sw) << 4)) =
               make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_async_smem();
@@ -1169,9 +1174,10 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
           // hold anything); in the others every NaN code does (a row that sees
           // such a key has a NaN score, so its result is NaN all the same).
           // The first two warpgroups have one of the tile's two value slots
-          // each, when it lands.
-          if (wg < 2) {
-            const uint32_t u = wg + (TWICE ? 4 * g0 + (j + 1 < sg.n ? 4 * j + 4 : 4 * j + 2) : 2 * g);
+          // each, when it lands (a single one has both).
+#pragma unroll 1
+          for (int half = wg; half < 2; half += GROUPS) {
+            const uint32_t u = half + (TWICE ? 4 * g0 + (j + 1 < sg.n ? 4 * j + 4 : 4 * j + 2) : 2 * g);
             const uint32_t slot = u % SLOTS;
             if (!wait_warp(smem_u32(&sh->k_full[slot]), (u / SLOTS) & 1, status, abort_flag)) {
               fail = true;
@@ -1198,6 +1204,7 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
             }
             fence_async_smem();
           }
+          if (fail) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh->fixed));
         }
@@ -1252,9 +1259,9 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
 #pragma unroll 1
         for (int c = 0; c < 4; ++c, dst += 128) {
           uint32_t o[16], o2[16];
-          const uint32_t ta = tmem + lane_off + TM_O + c * 64 + c0;
+          const uint32_t ta = tmem + lane_off + TM_O + c * C::NP + c0;
           tmem_ld16(ta, o);
-          if constexpr (!WIDE) tmem_ld16(ta + 32, o2);
+          if constexpr (!WIDE) tmem_ld16(ta + ROWS, o2);
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
@@ -1275,9 +1282,10 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
     }
   } else if (warp == 2 + 4 * GROUPS) {
     // ------------------------------------------------------------ the keys' scales, a tile ahead
-    uint32_t g = 0;
+    uint32_t g = 0, seg = 0;
     bool ok = true;
     while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      if (!DENSE && !(ok = load_q(sg, seg++))) break;
       const int n = sg.key1 - sg.key0;
       int entry[4];
       auto entries = [&](int k0) {
@@ -1306,11 +1314,12 @@ __global__ void __launch_bounds__(Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSpar
         if (lane == 0) mbar_arrive(smem_u32(&sh->s_full[sb]));
       }
     }
+    if (!DENSE) drain_q(seg);
   } else {
     // ------------------------------------------------------------ listed rows: cp.async
     if constexpr (!DENSE) {
       constexpr int RW = BK / kSparseProducers;       // this warp's keys [RW pw, RW pw + RW) of the tile
-      const int pw = warp - 3 - 4 * GROUPS;
+      const int pw = warp == 0 ? 0 : 1;
       uint32_t issued = 0, ropes = 0;
       bool ok = true;
       while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
@@ -1671,19 +1680,19 @@ int run_rows(int page_size) {
   return g;
 }
 
-template <bool DENSE, bool WIDE>
+template <bool DENSE, int ROWS>
 cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, const CUtensorMap& k_map,
                         const CUtensorMap& kr_map, const Q8Params& p, long long ctas, cudaStream_t stream) {
-  cudaError_t e = opt_in_smem(q8_attn_kernel<DENSE, WIDE>, Shape<WIDE>::TOTAL);
+  cudaError_t e = opt_in_smem(q8_attn_kernel<DENSE, ROWS>, Shape<ROWS>::TOTAL);
   if (e != cudaSuccess) return e;
-  const int threads = Shape<WIDE>::THREADS + (DENSE ? 0 : 32 * kSparseProducers);
+  const int threads = Shape<ROWS>::THREADS + (DENSE ? 0 : 32 * (kSparseProducers - 1));
   // Members of a piece read the same keys at the same time: as a cluster they
   // sit on neighbouring SMs, on one die, and share its half of L2 (left to the
   // order in which SMs became free, 64 x 128 heads took 376 us, not 300).
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = Shape<WIDE>::TOTAL;
+  cfg.dynamicSmemBytes = Shape<ROWS>::TOTAL;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1694,7 +1703,7 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, q8_attn_kernel<DENSE, WIDE>, q_map, qr_map, k_map, kr_map, p);
+  return cudaLaunchKernelEx(&cfg, q8_attn_kernel<DENSE, ROWS>, q_map, qr_map, k_map, kr_map, p);
 }
 
 template <int NT>
@@ -1707,8 +1716,13 @@ cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const Decode
                     static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, tokens);
 }
 
-// Query rows of a tile: 64 where a sequence can fill more than 32.
-int tile_rows(int H, int max_new) { return static_cast<long long>(H) * max_new > 32 ? 64 : 32; }
+// Query rows of a tile: as many as a sequence can fill, 16, 32 or 64.  (16 rows
+// leave room for three key tiles, 32 for two and a half: 32 sequences of 16384
+// to 32768 keys, 16 heads, take 102 us against 113.)
+int tile_rows(int H, int max_new) {
+  const long long rows = static_cast<long long>(H) * max_new;
+  return rows > 32 ? 64 : (rows > 16 ? 32 : 16);
+}
 // Row tiles that walk a piece together: those of one token's heads, eight at most.
 int item_members(int H, int rows) { return std::min(8, (H + rows - 1) / rows); }
 
@@ -1731,7 +1745,7 @@ DecodeQ8Layout decode_q8_layout(int T, int H, int pieces) {
   // more for every sequence whose rows do not fill their last one (T sequences
   // at most).  For either number of rows, as max_new is not known here.
   size_t slot_rows = 0;
-  for (int rows : {32, 64}) {
+  for (int rows : {16, 32, 64}) {
     const size_t item = static_cast<size_t>(rows) * item_members(H, rows);
     const size_t items = (R + item - 1) / item + (H % static_cast<int>(item) == 0 ? 0 : T);
     slot_rows = std::max(slot_rows, (items + pieces) * item);
@@ -1761,7 +1775,6 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   float* q_scale = reinterpret_cast<float*>(ws + L.q_scale);
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const int rows = tile_rows(H, a.max_new), members = item_members(H, rows);
-  const bool wide = rows == 64;
 
   CUtensorMap qa_map, wuk_map, u_map;
   if (!encode_2d(&qa_map, a.q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
@@ -1826,12 +1839,14 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
       !encode_2d(&kr_map, a.kv_cache, u8, 576, cache_rows, 576, 64, box, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const long long ctas = static_cast<long long>(a.pieces) * members;
-  if (dense)
-    e = wide ? launch_attn<true, true>(q_map, qr_map, k_map, kr_map, p, ctas, stream)
-             : launch_attn<true, false>(q_map, qr_map, k_map, kr_map, p, ctas, stream);
-  else
-    e = wide ? launch_attn<false, true>(q_map, qr_map, k_map, kr_map, p, ctas, stream)
-             : launch_attn<false, false>(q_map, qr_map, k_map, kr_map, p, ctas, stream);
+  auto attend = [&](auto rows_of_tile) {
+    constexpr int R = decltype(rows_of_tile)::value;
+    return dense ? launch_attn<true, R>(q_map, qr_map, k_map, kr_map, p, ctas, stream)
+                 : launch_attn<false, R>(q_map, qr_map, k_map, kr_map, p, ctas, stream);
+  };
+  if (rows == 64) e = attend(std::integral_constant<int, 64>());
+  else if (rows == 32) e = attend(std::integral_constant<int, 32>());
+  else e = attend(std::integral_constant<int, 16>());
   if (e != cudaSuccess) return e;
 
   CUtensorMap wuv_map;

@@ -423,7 +423,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
 // stride offset steps between 8-row groups; for an MN-major operand the
 // leading offset steps between 64-element MN blocks and the stride offset
 // between 8-row K groups.
-enum : uint32_t { kSwizzle128 = 2, kSwizzle64 = 4 };
+enum : uint32_t { kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6 };
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
                                           uint32_t layout = kSwizzle128) {
   return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
