@@ -1400,36 +1400,42 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 }
 
 // ============================================================ 3. merge and w_uv
-// One CTA per (head, up to NT tokens): the segments' latent results are merged
+// One CTA per (head, up to 16 tokens): the segments' latent results are merged
 // by LSE in fp32 (with the attention sink in the denominator), split into two
 // bf16 terms (their sum within 2^-16) and multiplied by w_uv[h]: D^T [128
-// values, 2 NT] = w_uv[h] [128, 512] . o^T, both terms of NT tokens side by
-// side, so that few tokens make a small N.  w_uv[h] is loaded once per CTA,
-// from before the attention has ended.  16 warps: with few tokens several of
-// them share one token's segments (a single long sequence has one for every SM)
-// and join through shared memory.
+// values, 32] = w_uv[h] [128, 512] . o^T, both terms of 16 tokens side by side,
+// so that few tokens make a small N.  w_uv[h] is loaded from before the
+// attention has ended.  16 warps: with few tokens several of them share one
+// token's segments (a single long sequence has one for every SM) and join
+// through shared memory.
 //
-// The whole of w_uv[h] waits in shared memory: with a ring of two of its blocks
-// and two CTAs an SM, the blocks' latencies one after another took 10000 clk.
+// RING: blocks of w_uv[h] (of eight) in shared memory.  All of them where one
+// wave of CTAs holds every token; else four, so that two CTAs share an SM, one's
+// chains of reads under the other's: 64 tokens of 128 heads 17.7 us, against 20.9
+// with one CTA an SM, 32 tokens and all blocks.
 constexpr int kOutWarps = 16;
+constexpr int NT = 16;
 constexpr int W_BLOCK = 128 * 128;                   // 128 rows of 64 bf16
+constexpr int O_BLOCK = 2 * NT * 128;                // 64 columns of both terms
 
-template <int NT>
+template <int R>
 struct OutShape {
-  static constexpr int O_BLOCK = 2 * NT * 128;       // 64 columns of both terms
-  static constexpr int AT_O = 8 * W_BLOCK;
+  static constexpr int RING = R;
+  static constexpr int CTAS = RING == 8 ? 1 : 2;     // on an SM
+  static constexpr int KU = RING == 8 ? 4 : 2;       // segments loaded together (registers)
+  static constexpr int AT_O = RING * W_BLOCK;
   static constexpr int AT_JOIN = AT_O + 8 * O_BLOCK; // [warp][512] partial sums, where warps share a token
-  static constexpr int AT_BAR = AT_JOIN + (NT == 16 ? kOutWarps * 2048 : 0);
+  static constexpr int AT_BAR = AT_JOIN + (RING == 8 ? kOutWarps * 2048 : 0);
   static constexpr int TOTAL = AT_BAR + 1024 + 1024;
-  static_assert(TOTAL <= 227 * 1024, "shared memory");
+  static_assert(CTAS * (TOTAL + 1024) <= 228 * 1024, "shared memory");
 };
 struct OutSmem {
-  uint64_t full, done;
+  uint64_t full[8], empty[8], done;
   uint32_t tmem;
   int abort;
-  int used[32];      // segments that hold keys of the token; -1: its rows are not written
-  long long first[32];   // row of the first one's results (in slots), the others `step` apart
-  float sink[32];    // log2 units
+  int used[NT];      // segments that hold keys of the token; -1: its rows are not written
+  long long first[NT];   // row of the first one's results (in slots), the others `step` apart
+  float sink[NT];    // log2 units
   float2 join[kOutWarps];   // a warp's maximum and sum
 };
 static_assert(sizeof(OutSmem) <= 1024, "barrier block");
@@ -1446,30 +1452,36 @@ __device__ __forceinline__ void merge_scale(Merge& m, float nm) {
   m.mx = nm;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(32 * kOutWarps, 1)
+template <int RING>
+__global__ void __launch_bounds__(32 * kOutWarps, OutShape<RING>::CTAS)
     q8_out_kernel(const __grid_constant__ CUtensorMap w_map, const Q8Params p, const FastDiv item_rows,
                   const float* __restrict__ sink, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int T,
                   int tokens) {
-  using C = OutShape<NT>;
+  using C = OutShape<RING>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   OutSmem* sh = reinterpret_cast<OutSmem*>(smem + C::AT_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * tokens, h = blockIdx.y;
   const int n = min(tokens, T - t0);                 // tokens of this CTA, NT at most
+  auto load_w = [&](int kb) {
+    const uint32_t full = smem_u32(&sh->full[kb % RING]);
+    mbar_expect_tx(full, W_BLOCK);
+    tma_load_2d(smem_u32(smem + (kb % RING) * W_BLOCK), &w_map, full, kb * 64, h * 128);
+  };
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&sh->full), 1);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(smem_u32(&sh->full[i]), 1);
+      mbar_init(smem_u32(&sh->empty[i]), 1);
+    }
     mbar_init(smem_u32(&sh->done), 1);
     sh->abort = 0;
     fence_mbar_init();
     // The weights do not come from the kernel before, and whatever wrote them
     // had completed when that kernel let this one start (it waits for its own
     // predecessor first).
-    const uint32_t full = smem_u32(&sh->full);
-    mbar_expect_tx(full, 8 * W_BLOCK);
 #pragma unroll 1
-    for (int kb = 0; kb < 8; ++kb) tma_load_2d(smem_u32(smem + kb * W_BLOCK), &w_map, full, kb * 64, h * 128);
+    for (int kb = 0; kb < RING; ++kb) load_w(kb);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&sh->tmem), 2 * NT);
@@ -1510,7 +1522,7 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
   };
   // Warps of a token: a power of two, so that they divide the 16.
   int share = 1;
-  while (NT == 16 && 2 * share * n <= kOutWarps) share *= 2;
+  while (RING == 8 && 2 * share * n <= kOutWarps) share *= 2;
   const int part = warp % share;
   Merge m;
   // One token's segments part, part + share, ...
@@ -1521,7 +1533,7 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
     m.tot = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) m.o[e] = 0.f;
-    constexpr int KU = 4;                              // segments loaded together
+    constexpr int KU = C::KU;
 #pragma unroll 1
     for (int k0 = part; k0 < used; k0 += KU * share) {
       uint4 a[KU], c[KU];
@@ -1582,7 +1594,7 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
         hi[e] = pack_bf16(x, y);
         lo[e] = pack_bf16(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
       }
-      uint8_t* dst = smem + C::AT_O + (half * 4 + (lane >> 3)) * C::O_BLOCK + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+      uint8_t* dst = smem + C::AT_O + (half * 4 + (lane >> 3)) * O_BLOCK + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
       *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(dst + NT * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
@@ -1628,36 +1640,46 @@ __global__ void __launch_bounds__(32 * kOutWarps, 1)
   volatile int never = 0;
   if (warp == 0) {
     if (elect_one()) {
-      // (The weights land before the CTA leaves, whether there is work or not.)
-      if (mbar_wait(smem_u32(&sh->full), 0, p.status, &never) && !stop) {
-        tc_fence_after();
-        const uint64_t a0 = sdesc(smem_u32(smem), 16, 1024), o0 = sdesc(smem_u32(smem + C::AT_O), 16, 1024);
+      // (What was loaded lands before the CTA leaves, whether there is work or not.)
+      const uint64_t a0 = sdesc(smem_u32(smem), 16, 1024), o0 = sdesc(smem_u32(smem + C::AT_O), 16, 1024);
+      int loaded = RING;
+      bool good = true;
 #pragma unroll 1
-        for (int kb = 0; kb < 8; ++kb)
+      for (int kb = 0; kb < loaded; ++kb) {
+        const int s = kb % RING;
+        good = mbar_wait(smem_u32(&sh->full[s]), (kb / RING) & 1, p.status, &never) && good;
+        if (stop || !good) continue;
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss(tmem, a0 + kb * (W_BLOCK >> 4) + kk * 2, o0 + kb * (C::O_BLOCK >> 4) + kk * 2,
-                       idesc_bf16(128, 2 * NT, false, false), (kb | kk) != 0);
-      } else {
-        sh->abort = 1;
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ss(tmem, a0 + s * (W_BLOCK >> 4) + kk * 2, o0 + kb * (O_BLOCK >> 4) + kk * 2,
+                     idesc_bf16(128, 2 * NT, false, false), (kb | kk) != 0);
+        if (RING < 8) {
+          tc_commit(smem_u32(&sh->empty[s]));
+          // The block before has been multiplied: its place takes the next one.
+          if (kb >= 1 && loaded < 8) {
+            good = mbar_wait(smem_u32(&sh->empty[(kb - 1) % RING]), ((kb - 1) / RING) & 1, p.status, &never);
+            if (good) load_w(loaded++);
+          }
+        }
       }
+      if (!good) sh->abort = 1;
       tc_commit(smem_u32(&sh->done));
     }
     __syncwarp();
   }
   const bool ok = mbar_wait_warp(smem_u32(&sh->done), 0, p.status, &never);
   tc_fence_after();
-  if (warp < NT / 4 && !stop && ok && *reinterpret_cast<volatile int*>(&sh->abort) == 0) {
-    // Four warps have the 128 values of 16 tokens.
-    const int c = (warp >> 2) * 16, v = (warp & 3) * 32;
-    __nv_bfloat16* dst = out + (static_cast<long long>(t0 + c) * p.H + h) * 128 + v + lane;
+  if (warp < 4 && !stop && ok && *reinterpret_cast<volatile int*>(&sh->abort) == 0) {
+    const int v = warp * 32;
+    __nv_bfloat16* dst = out + (static_cast<long long>(t0) * p.H + h) * 128 + v + lane;
     uint32_t r[16], r2[16];
-    tmem_ld16(tmem + (uint32_t(v) << 16) + c, r);
-    tmem_ld16(tmem + (uint32_t(v) << 16) + NT + c, r2);
+    tmem_ld16(tmem + (uint32_t(v) << 16), r);
+    tmem_ld16(tmem + (uint32_t(v) << 16) + NT, r2);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < n && sh->used[c + i] >= 0)
+    for (int i = 0; i < NT; ++i)
+      if (i < n && sh->used[i] >= 0)
         dst[static_cast<long long>(i) * p.H * 128] = __float2bfloat16_rn(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
   }
   tc_fence_before();
@@ -1706,13 +1728,13 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
   return cudaLaunchKernelEx(&cfg, q8_attn_kernel<DENSE, ROWS>, q_map, qr_map, k_map, kr_map, p);
 }
 
-template <int NT>
+template <int RING>
 cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const DecodeQ8Args& a, int rows, int tokens,
                        cudaStream_t stream) {
-  cudaError_t e = opt_in_smem(q8_out_kernel<NT>, OutShape<NT>::TOTAL);
+  cudaError_t e = opt_in_smem(q8_out_kernel<RING>, OutShape<RING>::TOTAL);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q8_out_kernel<NT>, dim3((a.T + tokens - 1) / tokens, a.H), dim3(32 * kOutWarps),
-                    OutShape<NT>::TOTAL, stream, w_map, p, fast_divisor(p.members * rows), a.sink,
+  return launch_pdl(q8_out_kernel<RING>, dim3((a.T + tokens - 1) / tokens, a.H), dim3(32 * kOutWarps),
+                    OutShape<RING>::TOTAL, stream, w_map, p, fast_divisor(p.members * rows), a.sink,
                     static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, tokens);
 }
 
@@ -1852,12 +1874,12 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   CUtensorMap wuv_map;
   if (!encode_2d(&wuv_map, a.w_uv, bf, 512, static_cast<uint64_t>(H) * 128, 1024, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  // Tokens a CTA: as few as one wave of CTAs allows, 16 or 32 where it takes more.
+  // Tokens a CTA: as few as one wave of CTAs allows, 16 where it takes more.
   int tokens = 1;
-  while (tokens < 16 && static_cast<long long>(H) * ((T + tokens - 1) / tokens) > sm_count()) tokens *= 2;
-  if (static_cast<long long>(H) * ((T + 15) / 16) <= sm_count())
-    return launch_out<16>(wuv_map, p, a, rows, tokens, stream);
-  return launch_out<32>(wuv_map, p, a, rows, 32, stream);
+  while (tokens < NT && static_cast<long long>(H) * ((T + tokens - 1) / tokens) > sm_count()) tokens *= 2;
+  if (static_cast<long long>(H) * ((T + tokens - 1) / tokens) <= sm_count())
+    return launch_out<8>(wuv_map, p, a, rows, tokens, stream);
+  return launch_out<4>(wuv_map, p, a, rows, NT, stream);
 }
 
 }  // namespace mla

@@ -551,7 +551,7 @@ struct SelectSmem {
   uint32_t scan[8];
   uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
   uint32_t total[2];           // chosen-for-sure and equal blocks of this CTA
-  uint32_t bin, need;
+  uint32_t bin, need, whole;   // whole: all keys of the digit are chosen
   int seq, pos;
 };
 
@@ -688,12 +688,18 @@ __global__ void __launch_bounds__(kSelThreads)
         if (before < need && need <= before + c) {
           sh.bin = 255 - tid;
           sh.need = need - before;
+          sh.whole = need - before == c ? 1u : 0u;
         }
       }
       __syncthreads();
       thr |= sh.bin << shift;
       need = sh.need;
       mask |= 255u << shift;
+      if (sh.whole != 0u && thr != 0u) {               // nothing to tell apart: the last pass is mostly spared
+        thr -= 1u;
+        need = 0u;
+        break;
+      }
     }
   } else {
     __syncthreads();                                 // the slice is in shared memory
