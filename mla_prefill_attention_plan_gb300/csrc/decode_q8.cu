@@ -1323,7 +1323,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       uint32_t issued = 0, ropes = 0;
       bool ok = true;
       while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
-        int row[RW / 32], prev[RW / 32], next[RW / 32];   // key 32 x + lane: this tile's row, the one before's, the next one's table entry
+        int row[RW / 32], next[RW / 32];              // key 32 x + lane: this tile's row, the next one's table entry
         auto entries = [&](int j, int (&r)[RW / 32]) {
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
@@ -1356,7 +1356,6 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
             const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
-            prev[x] = row[x];
             row[x] = pos < sg.key1 ? q8_row(p, pos, next[x]) : 0;
             if (row[x] < 0) row[x] = 0;               // reported; the result of its rows is not meaningful
           }
@@ -1373,9 +1372,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           }
           cp_async_arrive(smem_u32(&sh->r_full[s]));
           ++ropes;
-          if (TWICE && j > 0) ok = latent(prev);
         }
-        if (TWICE) ok = ok && latent(row);
       }
       // Every copy lands, and its arrival with it, before the CTA leaves.
       cp_async_commit();
