@@ -898,7 +898,7 @@ cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream) {
   b.max_seq = std::min(a.max_seq, kMaxContext);
   // One CTA a token, or, where the tokens leave SMs idle and the rows are
   // long, up to 16 (at least 4096 scores each): two tokens of 131000 scores
-  // take 22 us with eight and 19 with 16.
+  // took 22 us with eight and 19 with 16.
   int C = 1;
   while (C < kSelMaxCluster && static_cast<long long>(a.T) * 2 * C <= sm_count() && a.stride / (2 * C) >= 4096) C *= 2;
   cudaError_t e = cudaFuncSetAttribute(index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
