@@ -21,8 +21,8 @@
 //
 // Three launches:
 //   1. q8_query_kernel   u = w_uk[h] q per head (tcgen05, bf16), a power-of-two
-//      scale for each row, and the two terms: q8 [T*H][hi 576 | lo 576].  Its
-//      first CTA also writes the plan: the batch's work as one line of units.
+//      scale for each row, and the two terms: q8 [T*H][hi 576 | lo 576].  A CTA
+//      of its own writes the plan: the batch's work as one line of units.
 //   2. q8_attn_kernel    one CTA per piece of that line (and row tile).
 //   3. q8_out_kernel     merges the pieces' results by LSE and multiplies by
 //      w_uv[h] (tcgen05, the latent result as two bf16 terms).
@@ -188,8 +188,9 @@ __device__ void q8_plan(const PlanArgs& a, int tid, int (*scr)[4]) {
 // [256 r, 256 r + 256) of u for the head's 128 rows; CTA 1 also takes the rope
 // part.  The largest value of a row (over both CTAs, exchanged through
 // distributed shared memory) sets its scale.  Reads w_uk once (16 MB at 128
-// heads).  Two CTAs a head, two on an SM: 128 heads run in one wave; with four
-// CTAs a head they took two (31 us against 20 for 96 tokens).
+// heads).  Two CTAs a head, two on an SM: 128 heads run in one wave (four CTAs a
+// head, in two waves, took half as long again); 15 us for 96 tokens, of which
+// the operands' loads are a third and the conversion to two terms a quarter.
 constexpr int kQThreads = 320;                    // TMA, MMA, 8 epilogue warps
 constexpr int Q_A = 128 * 128;                    // 128 rows of 64 bf16
 constexpr int Q_B = 256 * 128;
@@ -474,7 +475,7 @@ struct AttnSmem {
   int lim[64];                // keys of the segment that the row sees
   int bad[4][4];              // [group][tile & 3]: a weight of the tile is out of range
   float ksc[2][128];          // [tile & 1]: the keys' scales (1 past the segment)
-  int run[32], last[16];      // cache rows of the runs that are loaded next, and of the tile before them
+  int run[32], last[8];      // cache rows of the runs that are loaded next, and of the tile before them
 };
 static_assert(sizeof(AttnSmem) <= 3 * 1024, "barrier block");
 
@@ -654,7 +655,7 @@ constexpr int kSparseProducers = 2;   // warp 0 and another one
 //
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
-// multiple of 8) warps copy the rows with cp.async.
+// multiple of 16) warps copy the rows with cp.async.
 template <bool DENSE, int R>
 __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparseProducers - 1)), 1)
     q8_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qr_map,
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     uint32_t seg = 0;
     uint32_t sk = 0, tk = 0, sr = 0, tr = 0;          // slot and turn of the next latent block and rope part
     bool ok = true;
-    const int nbox = BK / p.box;                      // runs of a tile, 16 at most
+    const int nbox = BK / p.box;                      // runs of a tile, 8 at most
     const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
     while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
       if constexpr (DENSE) {
@@ -1409,7 +1410,8 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 // RING: blocks of w_uv[h] (of eight) in shared memory.  All of them where one
 // wave of CTAs holds every token; else four, so that two CTAs share an SM, one's
 // chains of reads under the other's: 64 tokens of 128 heads 17.7 us, against 20.9
-// with one CTA an SM, 32 tokens and all blocks.
+// with one CTA an SM, 32 tokens and all blocks.  (In one wave the ring of four
+// makes a decode of 16 heads 1 % longer.)
 constexpr int kOutWarps = 16;
 constexpr int NT = 16;
 constexpr int W_BLOCK = 128 * 128;                   // 128 rows of 64 bf16
@@ -1735,9 +1737,10 @@ cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const Decode
                     static_cast<__nv_bfloat16*>(a.out), a.lse, a.T, tokens);
 }
 
-// Query rows of a tile: as many as a sequence can fill, 16, 32 or 64.  (16 rows
-// leave room for three key tiles, 32 for two and a half: 32 sequences of 16384
-// to 32768 keys, 16 heads, take 102 us against 113.)
+// Query rows of a tile: as many as a sequence can fill, 16, 32 or 64.  (64
+// sequences of 4096 to 16384 keys in tiles of 16, 32 and 64 rows: 99, 108, 151
+// us with 16 heads and one token; 169, 110, 154 with two tokens; 307, 189, 159
+// with four.  128 heads, 1 or 2 tokens: 401 us in 32 rows, 309 in 64.)
 int tile_rows(int H, int max_new) {
   const long long rows = static_cast<long long>(H) * max_new;
   return rows > 32 ? 64 : (rows > 16 ? 32 : 16);
@@ -1847,7 +1850,9 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   p.box = run_rows(a.page_size);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
-  const bool dense = a.indices == nullptr && p.box >= 8;
+  // Runs of 16 rows or more by TMA, shorter ones row by row: pages of 16 took 342
+  // us one way and 359 the other (64 sequences, 128 heads), pages of 8 427 and 361.
+  const bool dense = a.indices == nullptr && p.box >= 16;
   const uint64_t cache_rows = static_cast<uint64_t>(a.num_pages) * a.page_size;
   const uint32_t box = dense ? p.box : 8;
   CUtensorMap q_map, qr_map, k_map, kr_map;

@@ -875,6 +875,8 @@ cudaError_t launch_index_scores(const IndexScoresArgs& a, cudaStream_t stream) {
   if (items >= (1ll << 31)) return cudaErrorInvalidValue;
   const CUtensorMapDataType dt = e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int cols = e8 ? 128 : 64;
+  // Runs of 8 keys or more by TMA, shorter ones key by key (a decode step on pages
+  // of 8: 43 us, against 49).
   const bool dense = box >= 8;
   CUtensorMap q_map, k_map;
   if (!encode_2d(&q_map, a.iq, dt, 128, static_cast<uint64_t>(a.T) * a.Hi, 128 * kb, cols, p.NP,
