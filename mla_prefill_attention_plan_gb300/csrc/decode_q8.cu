@@ -475,7 +475,7 @@ struct AttnSmem {
   int lim[64];                // keys of the segment that the row sees
   int bad[4][4];              // [group][tile & 3]: a weight of the tile is out of range
   float ksc[2][128];          // [tile & 1]: the keys' scales (1 past the segment)
-  int run[32], last[8];      // cache rows of the runs that are loaded next, and of the tile before them
+  int run[32], last[4];      // cache rows of the runs that are loaded next, and of the tile before them
 };
 static_assert(sizeof(AttnSmem) <= 3 * 1024, "barrier block");
 
@@ -649,13 +649,13 @@ constexpr int kSparseProducers = 2;   // warp 0 and another one
 // flight.  Otherwise a tile stays in its slots from its scores to its values:
 // half the reads of L2, but a slot is held through the softmax.  Tiles of 32
 // rows have room for two and a half, and 32 sequences of 16384 to 32768 keys, 16
-// heads, take 113 us so, against 139 with every block loaded twice.  64 rows
-// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, take 311
+// heads, took 113 us so, against 139 with every block loaded twice.  64 rows
+// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, took 311
 // us twice and 322 once; with listed rows, whose copies cost more, 91 and 89.
 //
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
-// multiple of 16) warps copy the rows with cp.async.
+// multiple of 32) warps copy the rows with cp.async.
 template <bool DENSE, int R>
 __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparseProducers - 1)), 1)
     q8_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qr_map,
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     uint32_t seg = 0;
     uint32_t sk = 0, tk = 0, sr = 0, tr = 0;          // slot and turn of the next latent block and rope part
     bool ok = true;
-    const int nbox = BK / p.box;                      // runs of a tile, 8 at most
+    const int nbox = BK / p.box;                      // runs of a tile, 4 at most
     const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
     while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
       if constexpr (DENSE) {
@@ -768,22 +768,20 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           return pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
         };
         int entry = entry_of(0);
-        // A later segment's queries wait for the scores before them; its first
-        // keys need not.
         const bool late = seg > 0;
-        if (!late) ok = load_q(sg, seg++);
         int base = 0, row = 0;                            // first tile of the batch, this lane's run in it
         auto runs = [&](int j) { return j + 1 < n ? nbox : (sg.key1 - (sg.key0 + j * BK) + p.box - 1) / p.box; };
         // One elected lane: a tile's two slots, and its rope part.
         auto blocks = [&](int j, bool rope) -> bool {
           const int boxes = runs(j);
           const int* rows = j >= base ? sh->run + (j - base) * nbox : sh->last;
-#pragma unroll
+#pragma unroll(TWICE ? 2 : 1)   // (measured: 303 us against 315 twice, 96 against 97 once)
           for (int c = 0; c < 2; ++c) {
             if (tk > 0 && !wait_one(smem_u32(&sh->k_empty[sk]), (tk & 1) ^ 1, status, abort_flag)) return false;
             const uint32_t full = smem_u32(&sh->k_full[sk]);
             mbar_expect_tx(full, boxes * p.box * 256);
             const uint32_t dst = smem_u32(smem) + sk * SLOT;
+#pragma unroll 2                                       // (pages of 64, 128 heads: 304 us, against 318 by four and 327 rolled)
             for (int x = 0; x < boxes; ++x) tma_load_4d(dst + x * p.box * 256, &k_map, full, 0, 0, 2 * c, rows[x] >> 3);
             if (++sk == SLOTS) {
               sk = 0;
@@ -813,26 +811,29 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           base = j0;
           entry = entry_of(j0 + span);
           __syncwarp();
-          const int j1 = min(n, j0 + span);
-          bool good = true;
-          if (elect_one()) {
-            for (int j = j0; j < j1 && good; ++j) {
-              if (late && j == 0) break;
-              good = blocks(j, true) && (!TWICE || j == 0 || blocks(j - 1, false));
+          // One place that loads keys, and one for the queries: what is
+          // inlined twice is fetched twice (the instruction cache misses all
+          // the time; this and the MMAs' small loops made both 16 and 128 heads
+          // 7 % faster).  Values a tile behind, the last one's at the end.
+          const int j1 = min(n, j0 + span), end = j1 + (TWICE && j1 == n ? 1 : 0);
+#pragma unroll 1
+          for (int step = j0 == 0 ? 0 : 2; step < 3 && ok; ++step) {
+            // A later segment's queries wait for the scores before them; its
+            // first keys need not.
+            if (step == 1) {
+              ok = load_q(sg, seg++);
+              continue;
             }
-            if (late && j0 == 0) good = blocks(0, true);
-          }
-          ok = __all_sync(0xffffffffu, good);
-          if (late && j0 == 0 && ok && (ok = load_q(sg, seg++))) {
-            if (elect_one())
-              for (int j = 1; j < j1 && good; ++j) good = blocks(j, true) && (!TWICE || blocks(j - 1, false));
+            const int first = step == 0 ? 0 : (late && j0 == 0 ? 1 : j0), stop = step == 0 ? (late ? 1 : 0) : end;
+            bool good = true;
+            if (elect_one()) {
+#pragma unroll 1
+              for (int j = first; j < stop && good; ++j)
+#pragma unroll 1
+                for (int v = j < n ? 0 : 1; v < (TWICE && j > 0 ? 2 : 1) && good; ++v) good = blocks(j - v, v == 0);
+            }
             ok = __all_sync(0xffffffffu, good);
           }
-        }
-        if (TWICE && ok) {
-          bool good = true;
-          if (elect_one()) good = blocks(n - 1, false);
-          ok = __all_sync(0xffffffffu, good);
         }
       }
     }
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       auto scores = [&](uint32_t g, bool last) -> bool {
         const uint32_t sb = g & 1, d = tmem + TM_S + sb * NQ;
         if (g >= 2 && !wait(&sh->s_free[sb], ((g >> 1) & 1) ^ 1)) return false;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           if (!landed(&sh->k_full[sk], tk & 1)) return false;
           const uint64_t ad = a0 + sk * (SLOT >> 4);
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         if (first && seg > 0 && !wait(&sh->o_free, (seg - 1) & 1)) return false;
         if (masked && !wait(&sh->fixed, masked_tiles++ & 1)) return false;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           if (TWICE && !landed(&sh->k_full[sk], tk & 1)) return false;
           const uint32_t slot = TWICE ? sk : vk;
@@ -936,10 +937,11 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         // Tiles that hold a key which some row does not see.
         int all = sg.key1 - sg.key0;
         if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
-        ok = wait(&sh->q_full, seg & 1) && scores(g0, sg.n == 1);
-        for (int j = 0; j < sg.n && ok; ++j) {
-          if (j + 1 < sg.n) ok = scores(g0 + j + 1, j + 2 == sg.n);
-          ok = ok && values(g0 + j, j == 0, (j + 1) * BK > all);
+        ok = wait(&sh->q_full, seg & 1);
+#pragma unroll 1
+        for (int j = 0; j <= sg.n && ok; ++j) {          // scores a tile ahead of values
+          if (j < sg.n) ok = scores(g0 + j, j + 1 == sg.n);
+          if (j > 0) ok = ok && values(g0 + j - 1, j == 1, j * BK > all);
         }
         g0 += sg.n;
         ++seg;
@@ -1850,9 +1852,10 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   p.box = run_rows(a.page_size);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
-  // Runs of 16 rows or more by TMA, shorter ones row by row: pages of 16 took 342
-  // us one way and 359 the other (64 sequences, 128 heads), pages of 8 427 and 361.
-  const bool dense = a.indices == nullptr && p.box >= 16;
+  // Runs of 32 rows or more by TMA, shorter ones row by row: pages of 32 take 343
+  // us one way and 345 the other with 64 sequences and 128 heads, 99 and 103 with
+  // 32 and 16; pages of 16 407 and 346, 108 and 106.
+  const bool dense = a.indices == nullptr && p.box >= 32;
   const uint64_t cache_rows = static_cast<uint64_t>(a.num_pages) * a.page_size;
   const uint32_t box = dense ? p.box : 8;
   CUtensorMap q_map, qr_map, k_map, kr_map;

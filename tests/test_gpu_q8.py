@@ -353,10 +353,10 @@ def compare(out, lse, ref, ref_lse, rel=REL, lse_abs=LSE_ABS):
         assert np.abs(lse[fin] - ref_lse[fin]).max(initial=0.0) <= lse_abs
 
 
-@pytest.mark.parametrize("page,sb", [(128, 64), (64, 1), (48, 16), (16, 16), (24, 8), (100, 4), (7, 7), (1, 1), (256, 128)])
+@pytest.mark.parametrize("page,sb", [(128, 64), (64, 1), (96, 32), (16, 16), (24, 8), (100, 4), (7, 7), (1, 1), (256, 128)])
 @pytest.mark.parametrize("H", [3, 12, 40])
 def test_decode_page_sizes(page, sb, H):
-    """Runs of 128, 64 and 16 rows, and pages whose rows are copied one by one;
+    """Runs of 128, 64 and 32 rows, and pages whose rows are copied one by one;
     the kernels of 16, 32 and 64 rows."""
     Decode([1, 2, 1, 0], [300, 127, 0, 50], H, page, sb, seed=page).check()
 
