@@ -546,7 +546,7 @@ __device__ __forceinline__ Walk walk_begin(const Q8Params& p, int piece) {
   w.end = __ldg(&p.entries[lo + 1].units);
   return w;
 }
-template <int ROWS>
+template <int ROWS, bool DENSE>
 __device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member, int piece, Segment& s) {
   while (w.u < w.u1) {
     if (w.u >= w.end) {
@@ -568,7 +568,7 @@ __device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member
     s.cb = w.pe.cb;
     s.key0 = tile * BK;
     s.key1 = min(w.pe.L, (tile + len) * BK);
-    if (p.indices == nullptr)   // causal: the tile's last token sees keys up to cb + i
+    if (DENSE || p.indices == nullptr)   // causal: the tile's last token sees keys up to cb + i
       s.key1 = min(s.key1, s.cb + (s.r0 + s.nrows - 1) / p.H + 1);
     if (s.key1 <= s.key0) continue;
     s.n = (s.key1 - s.key0 + BK - 1) / BK;
@@ -581,14 +581,16 @@ __device__ __forceinline__ bool walk_next(const Q8Params& p, Walk& w, int member
 // Cache row of key `pos` of sequence b, in two steps, so that the table read can
 // be issued a tile or more before its value is looked at: the page id (or the
 // listed row), then the row or -1 (reported).
+template <bool DENSE>
 __device__ __forceinline__ int q8_entry(const Q8Params& p, int b, int pos) {
-  if (p.indices != nullptr) return __ldg(p.indices + static_cast<long long>(b) * p.indices_stride + pos);
+  if (!DENSE && p.indices != nullptr) return __ldg(p.indices + static_cast<long long>(b) * p.indices_stride + pos);
   const int pi = fast_div(pos, p.page);
   return pi < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pi) : -1;
 }
+template <bool DENSE>
 __device__ __forceinline__ int q8_row(const Q8Params& p, int pos, int entry) {
   int row = -1;
-  if (p.indices != nullptr) {
+  if (!DENSE && p.indices != nullptr) {
     if (entry >= 0 && entry < p.cache_rows) row = entry;
   } else if (entry >= 0 && entry < p.num_pages) {
     row = entry * p.page.d + pos - fast_div(pos, p.page) * p.page.d;
@@ -650,8 +652,9 @@ constexpr int kSparseProducers = 2;   // warp 0 and another one
 // half the reads of L2, but a slot is held through the softmax.  Tiles of 32
 // rows have room for two and a half, and 32 sequences of 16384 to 32768 keys, 16
 // heads, took 113 us so, against 139 with every block loaded twice.  64 rows
-// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, took 311
-// us twice and 322 once; with listed rows, whose copies cost more, 91 and 89.
+// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, take 280
+// us twice and 307 once; with listed rows, whose copies cost more, once is faster
+// (91 and 89 us).
 //
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
@@ -758,14 +761,14 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     bool ok = true;
     const int nbox = BK / p.box;                      // runs of a tile, 4 at most
     const int span = 32 / nbox;                       // tiles whose runs the warp looks up together
-    while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+    while (ok && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
       if constexpr (DENSE) {
         // Lane l has run l % nbox of tile j0 + l / nbox; the next tiles' table
         // entries are read while these are loaded.
         const int n = sg.n;
         auto entry_of = [&](int j0) -> int {
           const int pos = sg.key0 + j0 * BK + lane * p.box;
-          return pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
+          return pos < sg.key1 ? q8_entry<DENSE>(p, sg.b, pos) : 0;
         };
         int entry = entry_of(0);
         const bool late = seg > 0;
@@ -805,7 +808,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           const int pos = sg.key0 + j0 * BK + lane * p.box;
           // The batch before was full: its last tile's values are still to come.
           if (lane >= 32 - nbox) sh->last[lane - (32 - nbox)] = row;
-          row = pos < sg.key1 ? q8_row(p, pos, entry) : 0;
+          row = pos < sg.key1 ? q8_row<DENSE>(p, pos, entry) : 0;
           if (row < 0) row = p.cache_rows;                   // past the end: reads zeros
           sh->run[lane] = row;
           base = j0;
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           if (TWICE && !landed(&sh->k_full[sk], tk & 1)) return false;
           const uint32_t slot = TWICE ? sk : vk;
           const uint64_t ad = a0 + slot * (SLOT >> 4);
-#pragma unroll
+#pragma unroll(TWICE ? 4 : 8)
           for (int kk = 0; kk < 8; ++kk) {
             // Block 2 c + kk / 4, 32 keys a step: both operands MN-major, groups of 8 keys
             // 2048 (keys) and 8 NP (weights) bytes apart.
@@ -933,10 +936,10 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         tc_commit(smem_u32(&sh->pv_done));
         return true;
       };
-      while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      while (ok && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
         // Tiles that hold a key which some row does not see.
         int all = sg.key1 - sg.key0;
-        if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
+        if (DENSE || p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
         ok = wait(&sh->q_full, seg & 1);
 #pragma unroll 1
         for (int j = 0; j <= sg.n && ok; ++j) {          // scores a tile ahead of values
@@ -967,7 +970,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     uint8_t* pbuf = smem + C::AT_P;
     uint32_t seg = 0, g0 = 0;                         // segments done, tiles before this one's
     bool fail = false;
-    while (!fail && walk_next<ROWS>(p, wk, member, piece, sg)) {
+    while (!fail && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
       const int mine = min(16, sg.nrows - c0);        // rows of this group (none: it only keeps the pace)
       const int span = sg.key1 - sg.key0;
       bool seen = false;                              // this thread's row has a reference
@@ -978,7 +981,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         if (tid < mine) {
           rf = p.q_scale[sg.row0 + r] * p.scale_log2;
           lim = span;
-          if (p.indices == nullptr) lim = min(lim, sg.cb + (sg.r0 + r) / p.H + 1 - sg.key0);
+          if (DENSE || p.indices == nullptr) lim = min(lim, sg.cb + (sg.r0 + r) / p.H + 1 - sg.key0);
         }
         sh->rf[r] = rf;
         sh->ry[r] = tid < mine ? 0.f : -kInf;         // rows past the last: no weight
@@ -987,7 +990,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       }
       // Keys that every row of the tile sees.
       int all = span;
-      if (p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
+      if (DENSE || p.indices == nullptr) all = min(all, sg.cb + sg.r0 / p.H + 1 - sg.key0);
       if (!group_sync(gb, status, abort_flag)) {
         fail = true;
         break;
@@ -1287,13 +1290,13 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     // ------------------------------------------------------------ the keys' scales, a tile ahead
     uint32_t g = 0, seg = 0;
     bool ok = true;
-    while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+    while (ok && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
       if (!DENSE && !(ok = load_q(sg, seg++))) break;
       const int n = sg.key1 - sg.key0;
       int entry[4];
       auto entries = [&](int k0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) entry[x] = k0 + 32 * x + lane < n ? q8_entry(p, sg.b, sg.key0 + k0 + 32 * x + lane) : 0;
+        for (int x = 0; x < 4; ++x) entry[x] = k0 + 32 * x + lane < n ? q8_entry<DENSE>(p, sg.b, sg.key0 + k0 + 32 * x + lane) : 0;
       };
       entries(0);
 #pragma unroll 1
@@ -1304,7 +1307,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           const int k = k0 + 32 * x + lane;
           v[x] = 1.f;
           if (k < n) {
-            const int row = q8_row(p, sg.key0 + k, entry[x]);
+            const int row = q8_row<DENSE>(p, sg.key0 + k, entry[x]);
             if (row >= 0) v[x] = __ldg(p.kv_scales + fast_div(row, p.block));
           }
         }
@@ -1325,13 +1328,13 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       const int pw = warp == 0 ? 0 : 1;
       uint32_t issued = 0, ropes = 0;
       bool ok = true;
-      while (ok && walk_next<ROWS>(p, wk, member, piece, sg)) {
+      while (ok && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
         int row[RW / 32], next[RW / 32];              // key 32 x + lane: this tile's row, the next one's table entry
         auto entries = [&](int j, int (&r)[RW / 32]) {
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
             const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
-            r[x] = j < sg.n && pos < sg.key1 ? q8_entry(p, sg.b, pos) : 0;
+            r[x] = j < sg.n && pos < sg.key1 ? q8_entry<DENSE>(p, sg.b, pos) : 0;
           }
         };
         // A tile's two slots (a chunk of 16 bytes a lane, two rows an
@@ -1359,7 +1362,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 #pragma unroll
           for (int x = 0; x < RW / 32; ++x) {
             const int pos = sg.key0 + j * BK + pw * RW + 32 * x + lane;
-            row[x] = pos < sg.key1 ? q8_row(p, pos, next[x]) : 0;
+            row[x] = pos < sg.key1 ? q8_row<DENSE>(p, pos, next[x]) : 0;
             if (row[x] < 0) row[x] = 0;               // reported; the result of its rows is not meaningful
           }
           entries(j + 1, next);                       // in flight while the tile is copied
