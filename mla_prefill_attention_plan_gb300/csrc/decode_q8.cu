@@ -13,11 +13,22 @@
 // The second reads the same shared-memory tile as the first, MN-major.  A few
 // heads then make a small N instead of an M padded to 128, and the fp32 result
 // of up to 64 query rows (4 x 64 TMEM columns) fits beside two score buffers.
-// u and p are not e4m3 values: each is split into two e4m3 terms,
-//   x = e4m3(x) + e4m3(x - e4m3(x)),
-// whose sum is within 2^-8 of x (a bf16 rounding's bound; 0.4 of its mean
-// error), and each MMA is done once for either term.  That costs what one bf16
-// MMA would and needs no widening of the cache in shared memory.
+// u and p are not e4m3 values: each is split into two 8-bit terms,
+//   x = e4m3(x) + (x - e4m3(x)),
+// and each MMA is done once for either term.  That costs what one bf16 MMA
+// would and needs no widening of the cache in shared memory.  The second term of
+// p is e4m3 times 2^5 where the terms have accumulators of their own (0.4 of a
+// bf16 rounding's mean error), and e5m2 where they share one (0.75 of it); the
+// sum is within 2^-8 of x, a bf16 rounding's bound, as long as x is not far below
+// the window's top: 2^8 to 2^8.75 for p, whose error is at least 2^-15 (2^-14, or
+// 1/8 of x) there.  A row's reference therefore follows its keys both ways: it
+// moves when a tile's largest weight leaves 2^-3 .. 2^8 (2^-2 .. 2^8.75), so that
+// an error is at most 2^-12 of the largest weight among the tile's 128 keys or
+// 2^-8 of the weight, and a key far above all others costs only its own tile's
+// keys part of their bits.  (64 sequences of 128 heads: 287 us, against 278 with
+// references that only rise; 328 and 308 where scores spread by 2 nats, not 1.)  The
+// denominator sums the weights before they are split: the terms' errors have
+// either sign, so that their sum's is relatively no larger, and the LSE has none.
 //
 // Three launches:
 //   1. q8_query_kernel   u = w_uk[h] q per head (tcgen05, bf16), a power-of-two
@@ -424,8 +435,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t
 constexpr int SLOT = BK * 256;              // 32 KB
 constexpr int GROUP = 2048;                 // eight keys of a slot
 constexpr int ROPE = BK * 64;               // its rope part, 8 KB
-constexpr float kShift = 5.0f;              // weights are kept around 2^5 of e4m3's 448
-constexpr float kGrow = 8.0f;               // and may grow to 2^8 before the reference moves
+constexpr float kReach = 32.0f;             // how far (log2) a row's reference falls behind its highest
 
 // A tile has 64, 32 or 16 query rows.  The query operand holds both terms,
 // the first terms' rows above the second's, so one MMA of N = 128, 64 or 32
@@ -449,20 +459,30 @@ struct Shape {
   static constexpr int QBYTES = NQ * 576;
   static constexpr int NP = WIDE ? 64 : 2 * ROWS;         // columns of a value MMA, bytes of a key's weights
   static constexpr int PTERM = BK * NP;
+  // Where a tile's largest weight (log2) may lie before the row's reference
+  // moves, and where it is put then: in the first tile, from above and from
+  // below (a larger one leaves room for the next, a smaller one is most often
+  // the lowest of many).
+  static constexpr float HIGH = WIDE ? 8.75f : 8.0f, LOW = WIDE ? -2.0f : -3.0f;
+  static constexpr float FIRST = 5.0f, UP = WIDE ? 7.5f : 7.0f, DOWN = 3.0f;
+  // What a second term is multiplied by where it has its own columns of O; in
+  // the others it is e5m2, whose steps go down to 2^-16.
+  static constexpr float LO = WIDE ? 1.0f : 32.0f;
   static constexpr int PBYTES = WIDE ? 2 * PTERM : PTERM;
   static constexpr int AT_ROPE = SLOTS * SLOT;
   static constexpr int AT_Q = AT_ROPE + ROPES * ROPE;
   static constexpr int AT_P = AT_Q + QBYTES;
   static constexpr int AT_BAR = AT_P + PBYTES;
-  static constexpr int TOTAL = AT_BAR + 3 * 1024;
+  static constexpr int TOTAL = AT_BAR + 3 * 1024 + (WIDE ? 0 : 256);
   static constexpr uint32_t TM_S = 0, TM_O = 2 * NQ;      // TMEM: two score buffers, O^T 4 x NP columns
   static constexpr uint32_t TM_COLS = R == 16 ? 256 : 512;
   static_assert(TOTAL <= 227 * 1024 && TM_O + 4 * NP <= TM_COLS, "shared memory, TMEM");
 };
 
+template <int SLOTS, int ROPES>
 struct AttnSmem {
-  uint64_t k_full[6], k_empty[6];     // slots
-  uint64_t r_full[2], r_empty[2];     // rope parts
+  uint64_t k_full[SLOTS], k_empty[SLOTS];
+  uint64_t r_full[ROPES], r_empty[ROPES];     // rope parts
   uint64_t fixed;                     // a masked tile's values have been cleaned
   uint64_t q_full, q_free, s_full[2], s_free[2], p_full, pv_done, o_free, drain, group[4];
   uint32_t tmem;
@@ -473,11 +493,13 @@ struct AttnSmem {
   alignas(16) float d[64];    // and step of the exponent;
   int top[64];                // largest weight of a row (order-preserving integers)
   int lim[64];                // keys of the segment that the row sees
-  int bad[4][4];              // [group][tile & 3]: a weight of the tile is out of range
+  // [tile & 1][group][warp]: rows without a weight of LOW or more (row r: bit
+  // 15 - r), and bit 16 unless there is one above HIGH.
+  alignas(16) uint32_t range[2][4][4];
+  uint32_t care[4];           // [group]: rows whose reference may fall
   float ksc[2][128];          // [tile & 1]: the keys' scales (1 past the segment)
   int run[32], last[4];      // cache rows of the runs that are loaded next, and of the tile before them
 };
-static_assert(sizeof(AttnSmem) <= 3 * 1024, "barrier block");
 
 struct Q8Params {
   const PlanHead* head;
@@ -619,6 +641,12 @@ __device__ __forceinline__ bool group_sync(GroupBar& g, int32_t* status, volatil
   return group_wait(g, status, abort_flag);
 }
 
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // Order-preserving integer of a float (for the integer warp maximum) and back.
 __device__ __forceinline__ int float_order(float x) {
   const int i = __float_as_int(x);
@@ -672,7 +700,9 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
   constexpr uint32_t IDESC_PV = idesc_e4m3(128, C::NP, true, true);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;   // every byte is used: the base itself is a multiple of 1024 (checked below)
-  AttnSmem* sh = reinterpret_cast<AttnSmem*>(smem + C::AT_BAR);
+  using Smem = AttnSmem<C::SLOTS, C::ROPES>;
+  static_assert(sizeof(Smem) <= C::TOTAL - C::AT_BAR, "barrier block");
+  Smem* sh = reinterpret_cast<Smem*>(smem + C::AT_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int member = blockIdx.x % p.members, piece = blockIdx.x / p.members;
   int32_t* status = p.status;
@@ -705,7 +735,6 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     mbar_init(smem_u32(&sh->drain), 1);
     for (int i = 0; i < GROUPS; ++i) {
       mbar_init(smem_u32(&sh->group[i]), 4);
-      for (int k = 0; k < 4; ++k) sh->bad[i][k] = 0;
     }
     // An earlier kernel timed out: no work (and no plan to read).
     sh->abort = timed_out_before(status) ? 1 : 0;
@@ -923,7 +952,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
             const uint64_t av = ad + (kk >> 2) * 64 + (kk & 3) * (4 * GROUP >> 4), wv = w0 + (kk & 3) * (4 * 8 * C::NP >> 4);
             const uint32_t d = tmem + TM_O + (2 * c + (kk >> 2)) * C::NP;
             mma_f8_ss(d, av, wv, IDESC_PV, !first || (kk & 3) != 0);
-            if (WIDE) mma_f8_ss(d, av, wv + (C::PTERM >> 4), IDESC_PV, 1);
+            if (WIDE) mma_f8_ss(d, av, wv + (C::PTERM >> 4), IDESC_PV | kIdescB_e5m2, 1);
           }
           tc_commit(smem_u32(&sh->k_empty[slot]));
           if (!TWICE) {
@@ -973,7 +1002,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
     while (!fail && walk_next<ROWS, DENSE>(p, wk, member, piece, sg)) {
       const int mine = min(16, sg.nrows - c0);        // rows of this group (none: it only keeps the pace)
       const int span = sg.key1 - sg.key0;
-      bool seen = false;                              // this thread's row has a reference
+      float lowest = kInf;                            // least ry of this thread's row, once it has a reference
       if (tid < 16) {
         const int r = c0 + tid;
         float rf = 0.f;
@@ -1043,20 +1072,35 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
               t[c + 1] = __ffma2_rn(__fmul2_rn(v, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
             }
           }
+          uint32_t rows = 0xFFFFu;                    // that see any key of the tile
           if (__builtin_expect(masked, 0)) {
+            uint32_t some = 0u;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              t[c].x = j * BK + key < sh->lim[c0 + 2 * c] ? t[c].x : -kInf;
-              t[c].y = j * BK + key < sh->lim[c0 + 2 * c + 1] ? t[c].y : -kInf;
+              const int x = sh->lim[c0 + 2 * c] - j * BK, y = sh->lim[c0 + 2 * c + 1] - j * BK;
+              t[c].x = key < x ? t[c].x : -kInf;
+              t[c].y = key < y ? t[c].y : -kInf;
+              some = some << 2 | (x > 0 ? 2u : 0u) | (y > 0 ? 1u : 0u);
             }
+            rows = some;
           }
           if (__builtin_expect(!move, 1)) {
-            // Whether any key of the group has a weight out of range: told to
-            // the others here, looked at when the weights are ready.
+            // Whether a key has a weight above the range, and which rows have
+            // none within it: told to the group's other warps here, looked at
+            // when the weights are ready.
             float mx = -kInf;
 #pragma unroll
             for (int c = 0; c < 8; ++c) mx = fmax3(mx, t[c].x, t[c].y);
-            if (mx + lsc > kGrow) sh->bad[wg][g & 3] = 1;
+            const float2 off = make_float2(lsc - C::LOW, lsc - C::LOW);
+            uint32_t range = mx + lsc > C::HIGH ? 0u : 1u;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {                // the signs, the first row's on top
+              const float2 v = __fadd2_rn(t[c], off);
+              range = __funnelshift_l(__float_as_uint(v.x), range, 1);
+              range = __funnelshift_l(__float_as_uint(v.y), range, 1);
+            }
+            range = __reduce_and_sync(0xffffffffu, range);
+            if (lane == 0) sh->range[g & 1][wg][q4] = range;
             group_arrive(gb);
           } else {
             // ---- move the reference of the rows that need it
@@ -1072,23 +1116,29 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
               fail = true;
               break;
             }
-            if (tid == 0) sh->bad[wg][(g + 2) & 3] = 0;   // as below
             if (tid < 16) {
-              const float mm = order_float(sh->top[c0 + tid]);
+              const float mm = order_float(sh->top[c0 + tid]), ry = sh->ry[c0 + tid];
               sh->top[c0 + tid] = float_order(-kInf);
               float d = 0.f, f = 1.f;
               if (mm > -kInf) {
-                if (!seen) {
-                  d = kShift - mm;
-                  seen = true;
-                } else if (mm > kShift) {
-                  d = kShift - mm;
+                if (lowest == kInf) {
+                  d = C::FIRST - mm;
+                } else if (mm > C::HIGH) {
+                  d = C::UP - mm;
+                  f = ex2(d);
+                } else if (mm < C::LOW) {
+                  // At most so far that the sums' exponents have room; what
+                  // lies that far below the row's largest weights counts for nothing.
+                  d = fmaxf(fminf(C::DOWN - mm, lowest + kReach - ry), 0.f);
                   f = ex2(d);
                 }
+                lowest = fminf(lowest, ry + d);
               }
-              sh->ry[c0 + tid] += d;
+              sh->ry[c0 + tid] = ry + d;
               sh->d[c0 + tid] = d;
               sh->f[c0 + tid] = f;
+              const uint32_t may = __ballot_sync(0xffffu, tid < mine && ry + d < lowest + kReach - 1.f);
+              if (tid == 0) sh->care[wg] = __brev(may) >> 16;
             }
             if (!group_sync(gb, status, abort_flag)) {
               fail = true;
@@ -1113,13 +1163,16 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
               tmem_st_wait();
             }
           }
-          // ---- weights, and their two e4m3 terms
+          // ---- weights, and their two terms
           {
-            const float2 ks = make_float2(ksc, ksc);
-            // Rounds to four bits: y = x (2^20 + 1) has 24 bits, 20 of which
-            // y - (y - x) cancels.  (The product is an fma with zero so that it
-            // is not merged into the subtractions.)
+            const float2 ks = make_float2(ksc * C::LO, ksc * C::LO);
+            // Rounds to four bits (Veltkamp's split): y = x (2^20 + 1) has 24
+            // bits, 20 of which y - (y - x) cancels.  What is added to y keeps
+            // its last bit at 2^-9 of a weight or above, the first term's step
+            // below e4m3's normal range, so that the second term is what is
+            // missing there too.
             const float2 split = make_float2(1048577.f, 1048577.f);
+            const float2 least = make_float2(16384.f * C::LO, 16384.f * C::LO);
 #pragma unroll
             for (int c = 0; c < 8; c += 2) {
               uint16_t h[2], w[2];
@@ -1128,12 +1181,13 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
                 const float2 e = make_float2(ex2(t[c + i].x), ex2(t[c + i].y));
                 t[c + i] = e;
                 const float2 x = __fmul2_rn(e, ks);
-                const float2 y = __ffma2_rn(x, split, make_float2(0.f, 0.f));
+                const float2 y = __ffma2_rn(x, split, least);
                 const float2 z = __fadd2_rn(y, make_float2(-x.x, -x.y));
-                const float2 a = __fadd2_rn(y, make_float2(-z.x, -z.y));
+                float2 a = __fadd2_rn(y, make_float2(-z.x, -z.y));
                 const float2 b = __fadd2_rn(x, make_float2(-a.x, -a.y));
+                if constexpr (!WIDE) a = __fmul2_rn(a, make_float2(1.f / C::LO, 1.f / C::LO));
                 h[i] = pack_e4m3(a.x, a.y);
-                w[i] = pack_e4m3(b.x, b.y);
+                w[i] = WIDE ? pack_e5m2(b.x, b.y) : pack_e4m3(b.x, b.y);
               }
               hi[c / 2] = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
               lo[c / 2] = static_cast<uint32_t>(w[0]) | (static_cast<uint32_t>(w[1]) << 16);
@@ -1147,11 +1201,11 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
             fail = true;
             break;
           }
-          // The word of two tiles on is cleared: it was last read two tiles
-          // ago, by warps that have arrived here since, and none writes it
-          // before this warp has arrived at the next tile.
-          move = *reinterpret_cast<volatile int*>(&sh->bad[wg][g & 3]) != 0;
-          if (tid == 0) sh->bad[wg][(g + 2) & 3] = 0;
+          // (The words are written again two tiles on, by warps that know
+          // all of the group to have arrived at the next tile.)
+          const uint4 word = ld_shared_u4(smem_u32(sh->range[g & 1][wg]));
+          const uint32_t range = (word.x & word.y) & (word.z & word.w);
+          move = range < 0x10000u || (range & rows & *const_cast<const volatile uint32_t*>(&sh->care[wg])) != 0u;
           if (!move) break;
           tc_fence_after();
         }
@@ -1272,7 +1326,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             float v = __uint_as_float(o[r]);
-            if constexpr (!WIDE) v += __uint_as_float(o2[r]);
+            if constexpr (!WIDE) v = fmaf(__uint_as_float(o2[r]), 1.f / C::LO, v);
             const float f = sh->f[c0 + r];
             if (r < mine) dst[r * 512] = __float2half_rn(f == 0.f ? 0.f : v * f);
           }

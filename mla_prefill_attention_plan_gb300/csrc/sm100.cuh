@@ -416,6 +416,8 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return (1u << 4) | (0u << 7) | (0u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
          (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
+// Added to it: B holds e5m2 (kind::f8f6f4 takes the operands' formats apart).
+constexpr uint32_t kIdescB_e5m2 = 1u << 10;
 
 // Shared-memory matrix descriptor: start address, leading- and stride-dimension
 // byte offsets (all >> 4), version 1 at bit 46, layout at bits 61..63
@@ -512,6 +514,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint16_t pack_e5m2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // Two floats -> packed f16x2 (lo in bits 0..15), round to nearest even.

@@ -765,3 +765,82 @@ def test_write_replays_bit_for_bit():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(kv, ref[0]) and torch.equal(sc, ref[1]) and torch.equal(dq.view(torch.int16), ref[2].view(torch.int16))
+
+# ------------------------------------------------------------------ one key far above a long tail
+
+def peaked(n, gap, spread, H, page=128, sb=1, sink_value=0.0, at=0, seed=0):
+    """A sequence of n cached keys, one (position ``at``) `gap` nats above the
+    others, which spread by `spread` nats and whose latents share a mean: with
+    sink_value 0 the result is the others' alone.  Queries are 1 and +-spread in
+    two rope places, so scores are exact and depend on the head's sign."""
+    rng = np.random.default_rng(seed)
+    d = Decode([1], [n], H, page, sb, seed)
+    x = np.zeros((n + 1, 576))
+    x[:, :512] = rng.standard_normal(512) + 0.25 * rng.standard_normal((n + 1, 512))
+    x[:, 513] = rng.standard_normal(n + 1)
+    x[at, :512] = sink_value * rng.standard_normal(512)
+    x[at, 512], x[at, 513] = gap, 0.0
+    d.scales[:] = 2.0 ** -5
+    flat = d.codes.reshape(-1, 576)
+    flat[d.rows(0, np.arange(n + 1))] = O.e4m3_encode(x / 2.0 ** -5)
+    d.q[:] = 0
+    d.q[..., 128] = 1.0
+    d.q[..., 129] = spread * torch.where(torch.arange(H) % 2 == 0, 1.0, -1.0).to(torch.bfloat16)
+    d.scale = 1.0
+    return d
+
+
+def compare_rows(out, ref, rel):
+    """Every token's and head's result by itself."""
+    err = np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert err.max() <= rel, (err.max(), rel)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("H", [4, 16, 20, 48, 64, 128])
+@pytest.mark.parametrize("n,gap,spread,sink_value", [
+    (9000, 10.0, 0.0, 0.0), (9000, 10.0, 0.5, 0.0), (9000, 9.5, 1.0, 1.0), (9000, 13.0, 0.5, 0.0), (30000, 12.0, 1.0, 0.0)])
+def test_decode_one_key_far_above_the_others(n, gap, spread, sink_value, H, listed):
+    """The others keep their share of the result, whatever the largest weight is
+    (one piece, so that they share its reference).
+
+    Per head, in the 2-norm: the output's rounding is at most 2^-8 of each value,
+    sqrt(1/3) of that in the mean of 128; the weights' terms are each within 2^-8
+    of the weight (where all weights are equal, all by the same share); partial
+    results are fp16, 2^-11.  In the tile of the large key, whose weight is put at
+    2^5, the other 127 of n are within 2^-15 (up to 32 heads) or 1/8 of themselves
+    and 2^-17, taken at three spreads below their mean."""
+    d = peaked(n, gap, spread, H, sink_value=sink_value)
+    lists = d.rows(0, np.arange(n + 1))[None] if listed else None
+    out, lse = d.run(1, lists=lists)
+    ref, ref_lse = d.reference(lists=lists)
+    assert np.abs(lse - ref_lse).max() <= LSE_ABS
+    far = np.exp(gap + 3 * spread) / 2.0 ** 5
+    lost = min(1.0, 2.0 ** -15 * far) if H <= 32 else min(1.0, max(1 / 8, 2.0 ** -17 * far))
+    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 127 / n * lost + 2.0 ** -11)
+
+
+@pytest.mark.parametrize("H", [4, 32, 64])
+def test_decode_one_key_far_above_100000(H):
+    d = peaked(100000, 12.0, 1.0, H)
+    out, lse = d.run(1)
+    ref, ref_lse = d.reference()
+    assert np.abs(lse - ref_lse).max() <= LSE_ABS
+    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 2.0 ** -11)
+
+
+@pytest.mark.parametrize("H", [4, 20, 48])
+def test_decode_large_keys_come_and_go(H):
+    """Large keys in every third tile, from the third on: the reference rises and
+    falls many times."""
+    n = 12000
+    d = peaked(n, 11.0, 0.5, H, at=300)
+    flat = d.codes.reshape(-1, 576)
+    for p in range(600, n, 384):
+        flat[d.rows(0, [p])[0]] = flat[d.rows(0, [300])[0]]
+    out, lse = d.run(1)
+    ref, ref_lse = d.reference()
+    assert np.abs(lse - ref_lse).max() <= LSE_ABS
+    # (A third of the tiles hold a large key: their weights are within 1/8 at the
+    # least, 11 nats and three spreads below 2^7.)
+    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 2.0 ** -11 + 1 / 24)
