@@ -509,8 +509,8 @@ struct Q8Params {
   const uint8_t* kv_cache;
   const int32_t* page_table;
   const int32_t* indices;
-  __half* o_part;          // [slot][members][rows][512], O / (sum of weights * smax)
-  float2* meta;            // [slot][members][rows]: LSE in log2, smax (the segment's largest row scale)
+  __half* o_part;          // [slot][members][rows][512], O times a power of two, largest in [2^14, 2^15)
+  float2* meta;            // [slot][members][rows]: LSE in log2, 1 / (that power times the sum of weights)
   int indices_stride, num_pages, max_pages, cache_rows;
   FastDiv page, block;     // page size and scale_block
   int H, R, T, pieces, members, box;
@@ -1027,7 +1027,6 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       float2 l[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) l[c] = make_float2(0.f, 0.f);
-      float smax = 0.f;
 #pragma unroll 1
       for (int j = 0; j < sg.n; ++j) {
         const uint32_t g = g0 + j, sb = g & 1;
@@ -1040,7 +1039,6 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         float ksc = sh->ksc[sb][key];
         const bool broken = !(fabsf(ksc) < kInf);     // a scale that is no number: the key's scores are NaN
         if (broken) ksc = 1.f;
-        smax = fmaxf(smax, j * BK + key < span ? fabsf(ksc) : 0.f);
         const float lsc = __log2f(fabsf(ksc));
         const float xv = broken ? __int_as_float(0x7fc00000) : ksc;
         // The first tile sets the rows' references; in a later one the weights
@@ -1278,8 +1276,39 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         break;
       }
       tc_fence_after();
+      // 128 latent columns of the result, one a thread: the group's rows.
+      auto result = [&](int c, uint32_t (&o)[16]) {
+        const uint32_t ta = tmem + lane_off + TM_O + c * C::NP + c0;
+        tmem_ld16(ta, o);
+        if constexpr (!WIDE) {
+          uint32_t o2[16];
+          tmem_ld16(ta + ROWS, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            o[r] = __float_as_uint(fmaf(__uint_as_float(o2[r]), 1.f / C::LO, __uint_as_float(o[r])));
+        } else {
+          tmem_ld_wait();
+        }
+      };
       // Sums over the keys: within each warp, then over the four warps through
-      // the row arrays that the segment no longer needs.
+      // the row arrays that the segment no longer needs.  And each row's largest
+      // result, whose exponent the row is stored relative to, in fp16: what a row
+      // is made of then does not depend on any key that has no weight in it.
+      if (mine > 0) {
+        float m[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) m[r] = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[16];
+          result(c, o);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) m[r] = fmaxf(m[r], fabsf(__uint_as_float(o[r])));
+        }
+        const float mx = reduce16(m, [](float x, float y) { return fmaxf(x, y); });
+        if ((lane & 1) == 0) atomicMax(&sh->top[c0 + (lane >> 1)], float_order(mx));   // a maximum: in any order
+      }
       {
         float v[16];
 #pragma unroll
@@ -1288,11 +1317,8 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
           v[2 * c + 1] = l[c].y;
         }
         const float sum = reduce16(v, [](float x, float y) { return x + y; });
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-        float* part = q4 == 0 ? sh->rf : (q4 == 1 ? sh->d : (q4 == 2 ? sh->f : reinterpret_cast<float*>(sh->top)));
+        float* part = q4 == 0 ? sh->rf : (q4 == 1 ? sh->d : (q4 == 2 ? sh->f : reinterpret_cast<float*>(sh->lim)));
         if ((lane & 1) == 0) part[c0 + (lane >> 1)] = sum;
-        if (lane == 0) sh->lim[c0 + q4] = __float_as_int(smax);
       }
       if (!group_sync(gb, status, abort_flag)) {
         fail = true;
@@ -1300,15 +1326,15 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
       }
       if (tid < 16) {
         const int r = c0 + tid;
-        const float sum = (sh->rf[r] + sh->d[r]) + (sh->f[r] + __int_as_float(sh->top[r]));
-        float s = fmaxf(fmaxf(__int_as_float(sh->lim[c0]), __int_as_float(sh->lim[c0 + 1])),
-                        fmaxf(__int_as_float(sh->lim[c0 + 2]), __int_as_float(sh->lim[c0 + 3])));
-        if (!(s > 0.f)) s = 1.f;
-        sh->f[r] = sum == 0.f ? 0.f : 1.0f / (sum * s);
+        const float sum = (sh->rf[r] + sh->d[r]) + (sh->f[r] + __int_as_float(sh->lim[r]));
+        // 2^e, which puts the largest in [2^14, 2^15) (an infinite one stays that).
+        const int e = min(14 + 127 - (__float_as_int(order_float(sh->top[r])) >> 23 & 255), 126);
+        sh->f[r] = sum == 0.f ? 0.f : __int_as_float((e + 127) << 23);
         // Weights carry 2^-reference: log2 of the plain sum adds it back.
         if (tid < mine)
           p.meta[static_cast<long long>(sg.slot) * ROWS + r] =
-              make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->ry[r], s);
+              make_float2(sum == 0.f ? -kInf : __log2f(sum) - sh->ry[r],
+                          sum == 0.f ? 0.f : __int_as_float((127 - e) << 23) * (1.0f / sum));
       }
       if (!group_sync(gb, status, abort_flag)) {
         fail = true;
@@ -1318,17 +1344,12 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         __half* dst = p.o_part + (static_cast<long long>(sg.slot) * ROWS + c0) * 512 + key;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c, dst += 128) {
-          uint32_t o[16], o2[16];
-          const uint32_t ta = tmem + lane_off + TM_O + c * C::NP + c0;
-          tmem_ld16(ta, o);
-          if constexpr (!WIDE) tmem_ld16(ta + ROWS, o2);
-          tmem_ld_wait();
+          uint32_t o[16];
+          result(c, o);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            float v = __uint_as_float(o[r]);
-            if constexpr (!WIDE) v = fmaf(__uint_as_float(o2[r]), 1.f / C::LO, v);
             const float f = sh->f[c0 + r];
-            if (r < mine) dst[r * 512] = __float2half_rn(f == 0.f ? 0.f : v * f);
+            if (r < mine) dst[r * 512] = __float2half_rn(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
           }
         }
         tc_fence_before();

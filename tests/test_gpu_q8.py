@@ -844,3 +844,58 @@ def test_decode_large_keys_come_and_go(H):
     # (A third of the tiles hold a large key: their weights are within 1/8 at the
     # least, 11 nats and three spreads below 2^7.)
     compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 2.0 ** -11 + 1 / 24)
+
+
+# ------------------------------------------------------------------ rows of a very large scale
+
+@pytest.mark.parametrize("H", [4, 9, 24, 40, 128])
+def test_decode_a_row_that_is_not_seen_does_not_reach_the_result(H):
+    """The second new token's row has the scale 2^120 (an infinite value's): the
+    first token, in the same row tile up to 32 heads, does not see it."""
+    d = Decode([2], [140], H, 128, 1)
+    ref, ref_lse = d.reference()
+    row = d.rows(0, [141])[0]
+    d.scales.reshape(-1)[row] = 2.0 ** 120
+    d.codes.reshape(-1, 576)[row, :4] = 0x7E
+    out, lse = d.run(1)
+    compare(out[:1], lse[:1], ref[:1], ref_lse[:1])
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("exp", [18, 24, 60, 120])
+@pytest.mark.parametrize("H", [4, 24, 40])
+def test_decode_a_row_without_weight_does_not_reach_the_result(H, exp, listed):
+    """A row whose scale is 2^exp times the others' 2^-6 and whose score is far
+    below theirs (its rope code is the most negative one, the queries positive
+    there): the result is the others', head by head (each within the bound on all
+    of them, and half as much again for the heads' spread)."""
+    d = Decode([1], [300], H, 128, 1, lo=-6, hi=-6)
+    d.q[..., 128:130] = 4.0
+    row = d.rows(0, [170])[0]
+    d.scales.reshape(-1)[row] = 2.0 ** (exp - 6)
+    d.codes.reshape(-1, 576)[row, :512] = O.e4m3_encode(np.random.default_rng(0).standard_normal(512))
+    d.codes.reshape(-1, 576)[row, 512:] = 0
+    d.codes.reshape(-1, 576)[row, 512:514] = 0xFE
+    lists = d.rows(0, np.arange(301))[None] if listed else None
+    out, lse = d.run(1, lists=lists)
+    ref, ref_lse = d.reference(lists=lists)
+    assert np.abs(lse - ref_lse).max() <= LSE_ABS
+    compare_rows(out, ref, REL * 1.5)
+
+
+def test_decode_whole_tiles_without_weight():
+    """The first 128 scores are -infinity, the others near -200, in one piece: no
+    weight may vanish for that."""
+    d = Decode([1], [299], 2, 128, 1)
+    rng = np.random.default_rng(0)
+    d.q[:] = 0
+    d.q[..., 128] = 2.0 ** 60
+    d.scale = 1.0
+    flat, sc = d.codes.reshape(-1, 576), d.scales.reshape(-1)
+    flat[:] = O.e4m3_encode(rng.standard_normal(flat.shape))
+    flat[:, 512] = O.e4m3_encode(np.array([-3.25]))[0]
+    sc[:] = 2.0 ** -54
+    first = d.rows(0, np.arange(128))
+    flat[first, 512] = O.e4m3_encode(np.array([-448.0]))[0]
+    sc[first] = 2.0 ** 100
+    d.check()
