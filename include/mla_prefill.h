@@ -652,8 +652,10 @@ size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, 
  * mla_decode over the 8-bit cache (the decode branch of
  * "mla_prefill_decode_graph_bf16"; its cache is bf16 there): the same
  * definition with c_kv_j and k_rope_j = code * scale of their row.  kv_scales
- * may hold any positive finite numbers.  Arguments, sparse lists, sinks and lse
- * as in mla_decode; q, w_uk, w_uv and out are bf16.
+ * may hold any numbers from 2^-60 to 2^100 (the sums of weights keep the scales
+ * apart from them: smaller scales may make them overflow, and with larger ones,
+ * up to the write's 2^120, small weights are lost).  Arguments, sparse lists,
+ * sinks and lse as in mla_decode; q, w_uk, w_uv and out are bf16.
  * To give every token a list of its own, pass each token as a sequence of one
  * (batch_size = total_q_tokens, input_row_offsets = 0, 1, 2, ...; in the sparse
  * form cache_lengths and page_table are not used).

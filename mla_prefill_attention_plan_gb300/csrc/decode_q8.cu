@@ -349,7 +349,7 @@ __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
                    : "memory");
       am = fmaxf(am, o);
     }
-    const float s = pow2_scale(am);
+    const float s = pow2_scale<-120>(am);   // (queries may be as small as keys are large)
     const float inv = 1.0f / s;
     // An infinite query has no scale: its scores become NaN.
     if (rank == 0 && half == 0 && t < T) q_scale[grow] = am < kInf ? s : __int_as_float(0x7fc00000);

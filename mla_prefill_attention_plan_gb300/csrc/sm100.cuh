@@ -548,12 +548,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 // The smallest power of two s with amax <= 448 s, e4m3's largest value being
-// 448 = 1.75 * 2^8; at least 2^-60 (amax 0 or denormal), at most 2^120 (amax
+// 448 = 1.75 * 2^8; at least 2^MIN (amax 0 or denormal), at most 2^120 (amax
 // infinite).
+template <int MIN = -60>
 __device__ __forceinline__ float pow2_scale(float amax) {
   const uint32_t u = __float_as_uint(amax) & 0x7FFFFFFFu;
   int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = e < -60 ? -60 : (e > 120 ? 120 : e);
+  e = e < MIN ? MIN : (e > 120 ? 120 : e);
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

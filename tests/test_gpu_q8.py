@@ -899,3 +899,24 @@ def test_decode_whole_tiles_without_weight():
     flat[first, 512] = O.e4m3_encode(np.array([-448.0]))[0]
     sc[first] = 2.0 ** 100
     d.check()
+
+
+@pytest.mark.parametrize("lo,hi", [(-60, -58), (97, 100)])
+@pytest.mark.parametrize("H", [8, 24, 40])
+def test_decode_scales_at_the_ends_of_their_range(lo, hi, H):
+    """Queries divided by the largest scale, so that scores stay of order one."""
+    d = Decode([1, 1], [700, 300], H, 128, 4, lo=lo, hi=hi)
+    d.codes = O.e4m3_encode(np.random.default_rng(0).standard_normal(d.codes.shape))
+    d.q = (d.q.float() * 2.0 ** -hi).to(torch.bfloat16)
+    d.check()
+
+
+@pytest.mark.parametrize("H", [8, 24, 40])
+def test_decode_zero_rows_beside_others(H):
+    """Half of the context, whole tiles of it, is zero rows under the smallest
+    scale: they take part in the softmax, and the result is the others'."""
+    d = Decode([1], [1000], H, 128, 1)
+    zero = d.rows(0, np.r_[0:256, 300:310, 512:768])
+    d.codes.reshape(-1, 576)[zero] = 0
+    d.scales.reshape(-1)[zero] = 2.0 ** -60
+    d.check(parts=1)
