@@ -660,10 +660,12 @@ size_t mla_decode_q8_workspace_bytes(int32_t num_heads, int32_t total_q_tokens, 
  * (batch_size = total_q_tokens, input_row_offsets = 0, 1, 2, ...; in the sparse
  * form cache_lengths and page_table are not used).
  * Rounding: the projected query and the softmax weights are each held as the
- * sum of two 8-bit floats: a weight within the largest of 2^-8 of itself (a bf16
- * rounding's bound), 2^-12 of the largest weight of its row among the 128 keys of
- * its tile, and 2^-50 of the row's largest.  Partial results are fp16, the merged
- * latent result two bf16 terms; scores, sums and the merge run in fp32.
+ * sum of two 8-bit floats.  A query value (the rope part's as well) is within
+ * 2^-8 of itself, a bf16 rounding's bound, or 2^-21 of its row's largest; a
+ * weight within 2^-8 of itself, 2^-12 of the largest weight of its row among the
+ * 128 keys of its tile, or 2^-50 of the row's largest; whichever is the larger.
+ * Partial results are fp16 relative to each row's largest, the merged latent
+ * result two bf16 terms; scores, sums and the merge run in fp32.
  * Rows of out (and lse) of tokens outside every sequence, or of a sequence that
  * is left out, are not written.
  * max_seq_len bounds the contexts (dense form).

@@ -217,13 +217,16 @@ struct QuerySmem {
   int scr[4][4];
 };
 
-// x in two e4m3 terms, four values.
+// x in two e4m3 terms, four values.  Rows reach up to 448, where the first term
+// is at most 16 off, so the second is kept 16 times as large: what both leave is
+// 2^-14 at most where x is small, 2^-21 of the row's largest.
+constexpr float kQueryLow = 16.f;
 __device__ __forceinline__ void two_terms(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
   const uint16_t h0 = pack_e4m3(v[0], v[1]), h1 = pack_e4m3(v[2], v[3]);
   const float2 b0 = f16x2_to_float2(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_float2(e4m3x2_to_f16x2(h1));
   hi = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
-  lo = static_cast<uint32_t>(pack_e4m3(v[0] - b0.x, v[1] - b0.y)) |
-       (static_cast<uint32_t>(pack_e4m3(v[2] - b1.x, v[3] - b1.y)) << 16);
+  lo = static_cast<uint32_t>(pack_e4m3((v[0] - b0.x) * kQueryLow, (v[1] - b0.y) * kQueryLow)) |
+       (static_cast<uint32_t>(pack_e4m3((v[2] - b1.x) * kQueryLow, (v[3] - b1.y) * kQueryLow)) << 16);
 }
 
 __global__ void __cluster_dims__(1, 2, 1) __launch_bounds__(kQThreads, 2)
@@ -1057,15 +1060,15 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
             tmem_ld16(tmem + lane_off + TM_S + sb * NQ + c0, a);
             tmem_ld16(tmem + lane_off + TM_S + sb * NQ + ROWS + c0, b);
             tmem_ld_wait();
-            const float2 xs = make_float2(xv, xv);
+            const float2 xs = make_float2(xv, xv), low = make_float2(1.f / kQueryLow, 1.f / kQueryLow);
 #pragma unroll
             for (int c = 0; c < 8; c += 2) {
               const float4 rf = *reinterpret_cast<const float4*>(sh->rf + c0 + 2 * c);
               const float4 ry = *reinterpret_cast<const float4*>(sh->ry + c0 + 2 * c);
-              const float2 u = __fadd2_rn(make_float2(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])),
-                                          make_float2(__uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1])));
-              const float2 v = __fadd2_rn(make_float2(__uint_as_float(a[2 * c + 2]), __uint_as_float(a[2 * c + 3])),
-                                          make_float2(__uint_as_float(b[2 * c + 2]), __uint_as_float(b[2 * c + 3])));
+              const float2 u = __ffma2_rn(make_float2(__uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1])), low,
+                                          make_float2(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])));
+              const float2 v = __ffma2_rn(make_float2(__uint_as_float(b[2 * c + 2]), __uint_as_float(b[2 * c + 3])), low,
+                                          make_float2(__uint_as_float(a[2 * c + 2]), __uint_as_float(a[2 * c + 3])));
               t[c] = __ffma2_rn(__fmul2_rn(u, xs), make_float2(rf.x, rf.y), make_float2(ry.x, ry.y));
               t[c + 1] = __ffma2_rn(__fmul2_rn(v, xs), make_float2(rf.z, rf.w), make_float2(ry.z, ry.w));
             }

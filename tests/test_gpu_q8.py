@@ -920,3 +920,26 @@ def test_decode_zero_rows_beside_others(H):
     d.codes.reshape(-1, 576)[zero] = 0
     d.scales.reshape(-1)[zero] = 2.0 ** -60
     d.check(parts=1)
+
+
+@pytest.mark.parametrize("H", [4, 24, 40])
+def test_decode_queries_small_where_keys_are_large(H):
+    """One rope place of the queries is 2^16 times the others, and zero in the
+    keys; the scores come from the others alone, in places where the keys are
+    large.  A query value is off by at most 2^-21 of its row's largest, 2^-5 of
+    these, evenly spread: scores (of spread 1) by 2^-5 / sqrt(3), which changes a
+    result by no more than sqrt(2) times that."""
+    d = Decode([1], [400], H, 128, 1, lo=-3, hi=-3)
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal(d.codes.shape)
+    x[..., 512] = 0
+    x[..., 513:] *= 8.0
+    d.codes = O.e4m3_encode(x / 2.0 ** -3)
+    d.q[:] = 0
+    d.q[..., 129:] = torch.from_numpy(rng.standard_normal((1, H, 63)) * 2.0 ** -8).to(torch.bfloat16)
+    d.q[..., 128] = 2.0 ** 8
+    d.scale = 2.0 ** 5 / 8.0
+    out, lse = d.run(1)
+    ref, ref_lse = d.reference()
+    assert np.abs(lse - ref_lse).max() <= 2.0 ** -5
+    compare_rows(out, ref, REL + 2.0 ** -5 * (2 / 3) ** 0.5)
