@@ -16,8 +16,10 @@ namespace {
 
 constexpr int kWriteThreads = 256;
 constexpr int kWriteWarps = kWriteThreads / 32;
+constexpr float kInf = __builtin_huge_valf();
 
-// hi + lo += x, keeping the rounding error of the sum in lo.
+// hi + lo += x, keeping the rounding error of the sum in lo (Knuth's two-sum; a
+// hi that overflows leaves lo as NaN).
 __device__ __forceinline__ void add_two(float& hi, float& lo, float x) {
   const float s = hi + x;
   const float b = s - hi;
@@ -25,12 +27,13 @@ __device__ __forceinline__ void add_two(float& hi, float& lo, float x) {
   hi = s;
 }
 
-// a c - b d with one rounding of each product's error taken back (the plain
-// form loses up to three roundings, which moves codes next to a border).
+// a c - b d with one rounding of each product's error taken back (Kahan's; the
+// plain form loses up to three roundings, which moves codes next to a border).
+// An infinite product has no error.
 __device__ __forceinline__ float diff_of_products(float a, float c, float b, float d) {
   const float w = b * d;
-  const float e = fmaf(-b, d, w);
-  return fmaf(a, c, -w) + e;
+  const float e = fmaf(-b, d, w), r = fmaf(a, c, -w);
+  return fabsf(w) < kInf ? r + e : r;
 }
 __device__ __forceinline__ float2 rotate2(float re, float im, float c, float s) {
   return make_float2(diff_of_products(re, c, im, s), diff_of_products(re, s, -im, c));
@@ -52,24 +55,43 @@ __device__ __forceinline__ RowValues row_values(const uint16_t* __restrict__ row
   const float2 f = __ldg(reinterpret_cast<const float2*>(freq) + lane);
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   RowValues v;
-  // Sum of squares in two floats (a bf16 square is exact in fp32).
-  float hi = 0.f, lo = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v.y[2 * i] = bf16_lo(u[i]);
     v.y[2 * i + 1] = bf16_hi(u[i]);
-    add_two(hi, lo, v.y[2 * i] * v.y[2 * i]);
-    add_two(hi, lo, v.y[2 * i + 1] * v.y[2 * i + 1]);
   }
+  float hi, lo;
+  // Once, but for rows whose squares leave fp32's range: those are scaled by a
+  // power of two first, which the norm takes back.
+#pragma unroll 1
+  for (bool once = true;; once = false) {
+    // Sum of squares in two floats (a bf16 square is exact in fp32).
+    hi = 0.f;
+    lo = 0.f;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const float oh = __shfl_xor_sync(0xffffffffu, hi, d), ol = __shfl_xor_sync(0xffffffffu, lo, d);
-    // Both lanes of a pair add the same two numbers in the same order.
-    const bool up = (lane & d) != 0;
-    float h = up ? oh : hi, l = up ? ol : lo;
-    add_two(h, l, up ? hi : oh);
-    hi = h;
-    lo = l + (up ? lo : ol);
+    for (int i = 0; i < 16; ++i) add_two(hi, lo, v.y[i] * v.y[i]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const float oh = __shfl_xor_sync(0xffffffffu, hi, d), ol = __shfl_xor_sync(0xffffffffu, lo, d);
+      // Both lanes of a pair add the same two numbers in the same order.
+      const bool up = (lane & d) != 0;
+      float h = up ? oh : hi, l = up ? ol : lo;
+      add_two(h, l, up ? hi : oh);
+      hi = h;
+      lo = l + (up ? lo : ol);
+    }
+    if (__builtin_expect(!once || (hi >= 0x1p-100f && hi <= 0x1p126f), 1)) break;   // (the same in every lane)
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v.y[i]));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (m == kInf) lo = 0.f;                           // an infinite value: the others become 0, it NaN
+    if (m == kInf || (m < 1.f && eps >= 0x1p-80f)) break;
+    const float k = m < 1.f ? 0x1p100f : 0x1p-80f;
+    eps = eps * k * k;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v.y[i] *= k;
   }
   // 1 / sqrt(mean + eps) as rh + rl: the hardware's approximation and one
   // Newton step whose residual 1 - s rh^2 is formed in two floats.
@@ -78,7 +100,7 @@ __device__ __forceinline__ RowValues row_values(const uint16_t* __restrict__ row
   const float rh = rsqrtf(sh);
   const float th = rh * rh, tl = fmaf(rh, rh, -th);
   const float res = fmaf(-sh, th, 1.0f) - fmaf(sh, tl, sl * th);
-  const float rl = 0.5f * rh * res;
+  const float rl = sh < kInf ? 0.5f * rh * res : 0.f;
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
     const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + (i < 8 ? 0 : 256) + 8 * lane) + ((i & 4) >> 2));

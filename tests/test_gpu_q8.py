@@ -943,3 +943,71 @@ def test_decode_queries_small_where_keys_are_large(H):
     ref, ref_lse = d.reference()
     assert np.abs(lse - ref_lse).max() <= 2.0 ** -5
     compare_rows(out, ref, REL + 2.0 ** -5 * (2 / 3) ** 0.5)
+
+
+# ------------------------------------------------------------------ infinite, very large and very small values
+
+def _extreme_write(lat, eps):
+    """Each row of ``lat`` as a token of one sequence, a scale a slot, angles
+    around the circle, queries with the same rope parts.  Returns the rows'
+    codes, scales, queries' rope parts, and the definition's values in 64 bits."""
+    n = lat.shape[0]
+    gamma = torch.from_numpy(1.0 + 0.1 * np.random.default_rng(1).standard_normal(512)).float()
+    ang = 0.3 + np.arange(n)[:, None] + np.arange(32)[None] * 0.1
+    freqs = torch.from_numpy(np.stack([np.cos(ang), np.sin(ang)], -1).reshape(n, 64)).float()
+    kv, sc = torch.zeros(1, n, 576, dtype=torch.uint8, device=DEV), torch.ones(1, n, device=DEV)
+    q = torch.zeros(n, 1, 192, dtype=torch.bfloat16)
+    q[:, 0, 128:] = lat[:, 512:]
+    dq, st = q.to(DEV), status()
+    mla.check(mla.mla_latent_cache_write_q8(kv, sc, dq, lat.to(DEV), gamma.to(DEV), freqs.to(DEV), i32([0, n]), i32([0]),
+                                            i32([[0]]), 1, n, 1, 1, 1, 1, n, n, eps, st))
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    with np.errstate(all="ignore"):
+        y = q8.new_rows(O.decode(O.codes(lat), "bf16"), gamma.numpy(), freqs.numpy(), [0, n], [0], eps)
+        # (numpy's complex product turns an infinite part into NaN: the real products.)
+        r, f = O.decode(O.codes(lat), "bf16")[:, 512:], freqs.double().numpy()
+        y[:, 512::2] = r[:, ::2] * f[:, ::2] - r[:, 1::2] * f[:, 1::2]
+        y[:, 513::2] = r[:, ::2] * f[:, 1::2] + r[:, 1::2] * f[:, ::2]
+    return kv[0].cpu().numpy(), sc[0].cpu().double().numpy(), dq[:, 0, 128:].float().cpu().double().numpy(), y
+
+
+def _check_codes(codes, scales, y):
+    """Scales equal, NaN for NaN, +-448 for an infinite value, else as check_write."""
+    for c, s, v in zip(codes, scales, y):
+        assert s == q8.block_scale(float(np.nanmax(np.abs(v), initial=0.0)))
+        got, pre = O.e4m3_decode(c), v / s
+        assert np.array_equal(np.isnan(got), np.isnan(pre))
+        inf, fin = np.isinf(pre), np.isfinite(pre)
+        assert np.array_equal(got[inf], 448.0 * np.sign(pre[inf]))
+        a = np.maximum(np.abs(pre[fin]), 2.0 ** -6)
+        assert np.all(np.abs(got[fin] - pre[fin]) <= np.exp2(np.floor(np.log2(a)) - 4) + 2.0 ** -20 * a)
+
+
+def test_write_infinite_values():
+    """An infinite latent makes its row's others zero and itself NaN; infinite
+    rope values, in either half of a pair, keep their signs, the queries' too."""
+    lat = torch.randn(5, 576, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    inf = float("inf")
+    lat[0, 7] = inf
+    lat[1, 300], lat[1, 301] = -inf, inf
+    lat[2, 513], lat[2, 520], lat[2, 575] = inf, -inf, -inf
+    lat[3, 512:514] = inf                        # both halves: NaN where their products cancel
+    codes, scales, q, y = _extreme_write(lat, 1e-6)
+    assert np.isnan(y[0]).sum() == 1 and np.isinf(y[2]).sum() == 6
+    _check_codes(codes, scales, y)
+    assert np.array_equal(np.isnan(q), np.isnan(y[:, 512:])) and np.array_equal(np.isinf(q), np.isinf(y[:, 512:]))
+    fin = np.isfinite(q)
+    assert np.array_equal(q[np.isinf(q)], y[:, 512:][np.isinf(q)])
+    assert np.all(np.abs(q[fin] - y[:, 512:][fin]) <= 2.0 ** -8 * np.abs(y[:, 512:][fin]) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("size,eps", [(1e19, 1e-6), (1e22, 1e-6), (1e37, 1e-6), (1e37, 0.0), (1e-17, 0.0), (1e-22, 0.0),
+                                      (1e-36, 0.0), (1e-30, 1e-35), (1e-20, 1e-6), (0.0, 1e-6)])
+def test_write_latents_whose_squares_leave_the_range(size, eps):
+    """The norm is that of the definition for every size that bf16 has."""
+    x = torch.randn(3, 576, generator=torch.Generator().manual_seed(0), dtype=torch.float64)
+    x[:, :512] *= size
+    x[2, :256] = 0
+    codes, scales, _, y = _extreme_write(x.to(torch.bfloat16), eps)
+    _check_codes(codes, scales, y)
