@@ -721,11 +721,12 @@ mla_status_t mla_decode_q8(void* out, float* lse, const void* q, const uint32_t*
  * index_q and index_cache must be 16-byte aligned.
  * Errors: host MLA_ERR_DTYPE, MLA_ERR_GEOMETRY (num_index_heads outside
  * 1..128), MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS
- * (input_row_offsets[b+1] > total_q_tokens or a context longer than
- * max_seq_len or 2^31 - 8192: sequence b left out), MLA_DEV_BAD_PAGE (the
- * block's score is not meaningful), MLA_DEV_TIMEOUT.  Rows of tokens outside
- * every sequence are not written, nor are tokens past max_new_tokens of their
- * sequence.
+ * (input_row_offsets[b+1] > total_q_tokens or < input_row_offsets[b], or a
+ * context longer than max_seq_len or 2^31 - 8192: sequence b left out; where
+ * offsets decrease, rows of tokens that two sequences claim are not meaningful),
+ * MLA_DEV_BAD_PAGE (the block's score is not meaningful), MLA_DEV_TIMEOUT.
+ * Rows of tokens outside every sequence are not written, nor are tokens past
+ * max_new_tokens of their sequence.
  */
 mla_status_t mla_index_scores(float* scores, const void* index_q, const float* index_w, const void* index_cache,
                               const float* index_scales, const uint32_t* input_row_offsets,

@@ -114,7 +114,10 @@ struct Scored {
 };
 __device__ __forceinline__ Scored scored(const ScoreParams& p, int b, bool report) {
   const uint32_t qa = __ldg(p.iro + b), qe = __ldg(p.iro + b + 1), cached = __ldg(p.cache_len + b);
-  if (qe <= qa) return {0, 0};
+  if (qe <= qa) {
+    if (report && qe < qa) set_status(p.status, MLA_DEV_BAD_OFFSETS);
+    return {0, 0};
+  }
   const uint64_t ctx = static_cast<uint64_t>(cached) + (qe - qa);
   if (qe > static_cast<uint32_t>(p.T) || ctx > static_cast<uint64_t>(p.max_seq)) {
     if (report) set_status(p.status, MLA_DEV_BAD_OFFSETS);
@@ -576,6 +579,10 @@ __global__ void __launch_bounds__(kSelThreads)
   const int t = blockIdx.x / C;
   (&sh.hist[0][0])[tid] = 0u;
   pdl_enter();
+  // Decreasing offsets are reported once (the search below reads the same words).
+  if (blockIdx.x == 0)
+    for (int x = tid; x < a.B; x += kSelThreads)
+      if (__ldg(a.iro + x + 1) < __ldg(a.iro + x)) set_status(a.status, MLA_DEV_BAD_OFFSETS);
   // The token's sequence: the last b with iro[b] <= t, 1024 probes at a time.
   int b = 0;
   for (int end = a.B; end - b > 1;) {

@@ -387,3 +387,31 @@ def test_selected_rows_in_the_bf16_decode():
     ref, _ = d.reference(lists=rows.cpu().numpy(), topk=cnt.cpu().numpy())
     g = out.float().cpu().double().numpy()
     assert np.abs(g - ref).max() <= 2e-2 and np.abs(g - ref).sum() <= 1e-2 * np.abs(ref).sum()
+
+
+@pytest.mark.parametrize("B", [3, 2500])
+def test_scores_decreasing_offsets(B):
+    """The second sequence ends before it begins: reported, the first one scored.
+    (A few sequences, whose work is shared out, and so many that each has a CTA.)"""
+    page, table = 16, np.arange(2 * B).reshape(B, 2)
+    iro = np.concatenate([[0, 4, 2], np.arange(2, B) + 3])            # 4 tokens, -2, 3, then one each
+    T = int(iro[-1])
+    q, w = torch.ones(T, 4, 128, dtype=torch.bfloat16, device=DEV), torch.ones(T, 4, device=DEV)
+    k = torch.ones(2 * B, page, 128, dtype=torch.bfloat16, device=DEV)
+    out, st = torch.full((T, 32), FILL, device=DEV), status()
+    mla.check(mla.mla_index_scores(out, q, w, k, None, i32(iro), i32([9] * B), i32(table), 2 * B, page, 2, 1, B, 4, T, 4,
+                                   32, 32, mla.MLA_BF16, st))
+    torch.cuda.synchronize()
+    assert st.item() == mla.MLA_DEV_BAD_OFFSETS
+    assert torch.all(out[0, :10] == 512.0) and torch.all(out[0, 10:] == float("-inf"))
+    if B > 3:
+        assert torch.all(out[-1, :10] == 512.0) and torch.all(out[-1, 10:] == float("-inf"))
+
+
+def test_select_decreasing_offsets():
+    iro, scores = [0, 4, 2, 5], torch.randn(5, 32, device=DEV)
+    rows, cnt, st = torch.full((5, 8), -7, dtype=torch.int32, device=DEV), torch.zeros(5, dtype=torch.int32, device=DEV), status()
+    mla.check(mla.mla_index_select(rows, cnt, scores, i32(iro), i32([9] * 3), i32([[0, 1], [2, 3], [4, 5]]), 6, 16, 2, 1, 8, 1,
+                                   3, 5, 32, 32, 8, st))
+    torch.cuda.synchronize()
+    assert st.item() == mla.MLA_DEV_BAD_OFFSETS and cnt[0].item() == 8
