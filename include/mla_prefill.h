@@ -756,7 +756,7 @@ mla_status_t mla_index_scores(float* scores, const void* index_q, const float* i
  * num_local: 0 .. top_blocks
  * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS (as
  * above), MLA_DEV_BAD_PAGE (that entry is -1).  Rows of tokens outside every
- * sequence are not written.
+ * sequence, or of a sequence that is left out, are not written.
  */
 mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* scores,
                               const uint32_t* input_row_offsets, const uint32_t* cache_lengths,

@@ -597,10 +597,11 @@ __global__ void __launch_bounds__(kSelThreads)
     if (!timed_out_before(a.status)) {
       const uint32_t qa = __ldg(a.iro + b), qe = __ldg(a.iro + b + 1), cached_tokens = __ldg(a.cache_len + b);
       if (qa <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < qe) {
-        const uint64_t ctx = static_cast<uint64_t>(cached_tokens) + (static_cast<uint32_t>(t) - qa);
-        if (ctx < static_cast<uint64_t>(a.max_seq) && qe <= static_cast<uint32_t>(a.T)) {
+        // (The whole sequence's context: the scores leave it out as one.)
+        const uint64_t ctx = static_cast<uint64_t>(cached_tokens) + (qe - qa);
+        if (ctx <= static_cast<uint64_t>(a.max_seq) && qe <= static_cast<uint32_t>(a.T)) {
           seq = b;
-          pos = static_cast<int>(ctx);
+          pos = static_cast<int>(cached_tokens + (static_cast<uint32_t>(t) - qa));
         } else {
           set_status(a.status, MLA_DEV_BAD_OFFSETS);
         }

@@ -415,3 +415,24 @@ def test_select_decreasing_offsets():
                                    3, 5, 32, 32, 8, st))
     torch.cuda.synchronize()
     assert st.item() == mla.MLA_DEV_BAD_OFFSETS and cnt[0].item() == 8
+
+
+def test_select_leaves_out_what_the_scores_leave_out():
+    """The second sequence's context is one token longer than max_seq_len: none of
+    its tokens has scores, so none is given a list, the first two positions that
+    do exist included."""
+    new, cached, max_seq = [1, 3], [10, 18], 20
+    table, num = pages(new, cached, 16)
+    k = torch.ones(num, 16, 128, dtype=torch.bfloat16, device=DEV)
+    q, w = torch.ones(4, 4, 128, dtype=torch.bfloat16, device=DEV), torch.ones(4, 4, device=DEV)
+    scores, st = torch.full((4, max_seq), FILL, device=DEV), status()
+    iro, cl = i32(offsets(new)), i32(cached)
+    mla.check(mla.mla_index_scores(scores, q, w, k, None, iro, cl, i32(table), num, 16, table.shape[1], 1, 2, 4, 4, 3,
+                                   max_seq, max_seq, mla.MLA_BF16, st))
+    rows, cnt = torch.full((4, 6), -7, dtype=torch.int32, device=DEV), torch.full((4,), -7, dtype=torch.int32, device=DEV)
+    mla.check(mla.mla_index_select(rows, cnt, scores, iro, cl, i32(table), num, 16, table.shape[1], 1, 6, 1, 2, 4, max_seq,
+                                   max_seq, 6, st))
+    torch.cuda.synchronize()
+    assert st.item() == mla.MLA_DEV_BAD_OFFSETS
+    assert torch.all(scores[1:] == FILL) and torch.all(rows[1:] == -7) and torch.all(cnt[1:] == -7)
+    assert cnt[0].item() == 6 and rows[0].min().item() >= 0
