@@ -117,15 +117,18 @@ _current_stream = None
 
 def _stream(stream):
     if stream is None:
-        # The handle of torch's current stream on the current device, without
-        # the Stream object that torch.cuda.current_stream() builds around it
-        # (3 us a call, half of the binding's cost).
+        # The handle of torch's current stream on the current device, where
+        # this torch has it without the Stream object that
+        # torch.cuda.current_stream() builds around it (3 us a call, half of
+        # the binding's cost).
         global _current_stream
         if _current_stream is None:
             import torch
-            device = torch.cuda.current_device
-            raw = torch._C._cuda_getCurrentRawStream
-            _current_stream = lambda: raw(device())  # noqa: E731
+            device, raw = torch.cuda.current_device, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:
+                _current_stream = lambda: raw(device())  # noqa: E731
+            else:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
         return _current_stream()
     if isinstance(stream, int):
         return stream

@@ -209,3 +209,15 @@ def test_oracle_codes_agree_with_torch():
     x = rng.standard_normal(4000) * np.exp(rng.uniform(-8, 8, 4000))
     t = torch.from_numpy(np.clip(x, -448, 448)).to(torch.float32)
     assert np.array_equal(O.e4m3_encode(t.double().numpy()), t.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_stream_of_a_call_without_the_private_function(monkeypatch):
+    """torch's raw stream lookup is not public: without it the public one serves."""
+    monkeypatch.setattr(mla, "_current_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 70 + device, raising=False)
+    assert mla._stream(None) == 73
+    monkeypatch.setattr(mla, "_current_stream", None)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), {"cuda_stream": 5})())
+    assert mla._stream(None) == 5 and mla._stream(9) == 9
