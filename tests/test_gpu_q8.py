@@ -790,6 +790,14 @@ def peaked(n, gap, spread, H, page=128, sb=1, sink_value=0.0, at=0, seed=0):
     return d
 
 
+def far_below(H, gap, spread):
+    """Share of itself by which the weight of a key may be off, `gap` nats and
+    three spreads below one that stands alone in its tile and is put at 2^7.75: it
+    is held to 2^-15 up to 32 heads, else to 2^-14, or 1/8 of itself and 2^-17."""
+    far = np.exp(gap + 3 * spread) / 2.0 ** 7.75
+    return min(1.0, 2.0 ** -15 * far if H <= 32 else min(2.0 ** -14 * far, max(1 / 8, 2.0 ** -17 * far)))
+
+
 def compare_rows(out, ref, rel):
     """Every token's and head's result by itself."""
     err = np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
@@ -807,17 +815,14 @@ def test_decode_one_key_far_above_the_others(n, gap, spread, sink_value, H, list
     Per head, in the 2-norm: the output's rounding is at most 2^-8 of each value,
     sqrt(1/3) of that in the mean of 128; the weights' terms are each within 2^-8
     of the weight (where all weights are equal, all by the same share); partial
-    results are fp16, 2^-11.  In the tile of the large key, whose weight is put at
-    2^5, the other 127 of n are within 2^-15 (up to 32 heads) or 1/8 of themselves
-    and 2^-17, taken at three spreads below their mean."""
+    results are fp16, 2^-11.  In the tile of the large key the other 127 of n are
+    off by what far_below says."""
     d = peaked(n, gap, spread, H, sink_value=sink_value)
     lists = d.rows(0, np.arange(n + 1))[None] if listed else None
     out, lse = d.run(1, lists=lists)
     ref, ref_lse = d.reference(lists=lists)
     assert np.abs(lse - ref_lse).max() <= LSE_ABS
-    far = np.exp(gap + 3 * spread) / 2.0 ** 5
-    lost = min(1.0, 2.0 ** -15 * far) if H <= 32 else min(1.0, max(1 / 8, 2.0 ** -17 * far))
-    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 127 / n * lost + 2.0 ** -11)
+    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + 127 / n * far_below(H, gap, spread) + 2.0 ** -11)
 
 
 @pytest.mark.parametrize("H", [4, 32, 64])
@@ -1011,3 +1016,14 @@ def test_write_latents_whose_squares_leave_the_range(size, eps):
     x[2, :256] = 0
     codes, scales, _, y = _extreme_write(x.to(torch.bfloat16), eps)
     _check_codes(codes, scales, y)
+
+
+@pytest.mark.parametrize("H", [4, 24, 40])
+@pytest.mark.parametrize("n,gap", [(100, 8.0), (100, 12.0), (500, 10.0), (500, 12.0), (500, 13.0), (2000, 14.0)])
+def test_decode_one_key_far_above_a_short_context(n, gap, H):
+    """The large key's tile is a good part of the context, or all of it."""
+    d = peaked(n, gap, 0.25, H)
+    out, lse = d.run(1)
+    ref, ref_lse = d.reference()
+    assert np.abs(lse - ref_lse).max() <= LSE_ABS
+    compare_rows(out, ref, 2.0 ** -8 * 3 ** -0.5 + 2.0 ** -8 + min(1, 127 / n) * far_below(H, gap, 0.25) + 2.0 ** -11)
