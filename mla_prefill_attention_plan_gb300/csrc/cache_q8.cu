@@ -184,7 +184,7 @@ __device__ __forceinline__ int token_position(const CacheWriteQ8Args& a, int t, 
 // scale known, the codes (the rows are read again, from L1).  64 rows take some
 // 25 us that way, bound by latency, so these CTAs come first and run under the
 // others: with the two kinds of work in one CTA per token, 8 prompts of 256 to
-// 2048 tokens, 128 heads, took 75 us, now 57 (5.4 TB/s).
+// 2048 tokens, 128 heads, took 75 us, now 55 (5.6 TB/s).
 //
 // Queries: a thread's first four pieces (all of them with 128 heads) are read
 // before anything is known of the token, over the chain of reads that finds its

@@ -27,7 +27,7 @@
 // 2^-8 of the weight.  A key far above all others costs only its own tile's keys
 // bits, and is put at the window's top, which leaves them most: with 500 keys 14
 // nats below one without value the result is 0.6 % off.  (64 sequences of 128 heads: 287 us, against 278 with
-// references that only rise; 328 and 308 where scores spread by 2 nats, not 1.)  The
+// references that only rise; 330 and 308 where scores spread by 2 nats, not 1.)  The
 // denominator sums the weights before they are split: the terms' errors have
 // either sign, so that their sum's is relatively no larger, and the LSE has none.
 //
@@ -682,12 +682,13 @@ constexpr int kSparseProducers = 2;   // warp 0 and another one
 // for its values, in the order in which the MMAs take them: scores 0, scores 1,
 // values 0, scores 2, values 1, ...  The ring then holds nothing but loads in
 // flight.  Otherwise a tile stays in its slots from its scores to its values:
-// half the reads of L2, but a slot is held through the softmax.  Tiles of 32
-// rows have room for two and a half, and 32 sequences of 16384 to 32768 keys, 16
-// heads, took 113 us so, against 139 with every block loaded twice.  64 rows
-// have room for two: 64 sequences of 4096 to 16384 keys, 128 heads, take 280
-// us twice and 307 once; with listed rows, whose copies cost more, once is faster
-// (91 and 89 us).
+// half the reads of L2, but a slot is held through the softmax.  64 rows leave
+// room for two tiles: 64 sequences of 4096 to 16384 keys, 128 heads, take 284 us
+// twice and 312 once.  16 rows leave room for three: 32 sequences of 16384 to
+// 32768 keys, 16 heads, take 96 us once and 105 twice.  (32 rows, which stay in
+// place too, would be faster twice by now: 96 us against 104, 64 sequences of 32
+// heads, and 108 against 112, 32 long ones; in an earlier state of the loops it was
+// the other way round.)  Listed rows, whose copies cost more, are loaded once.
 //
 // DENSE: a tile's rows come in runs of p.box consecutive rows of one page, each
 // a rectangular TMA load.  Otherwise (listed rows, page sizes that are no
@@ -812,13 +813,13 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
         auto blocks = [&](int j, bool rope) -> bool {
           const int boxes = runs(j);
           const int* rows = j >= base ? sh->run + (j - base) * nbox : sh->last;
-#pragma unroll(TWICE ? 2 : 1)   // (measured: 303 us against 315 twice, 96 against 97 once)
+#pragma unroll(TWICE ? 2 : 1)   // (64 sequences of 128 heads: 284 us, against 298 rolled; 16 heads: 96 either way)
           for (int c = 0; c < 2; ++c) {
             if (tk > 0 && !wait_one(smem_u32(&sh->k_empty[sk]), (tk & 1) ^ 1, status, abort_flag)) return false;
             const uint32_t full = smem_u32(&sh->k_full[sk]);
             mbar_expect_tx(full, boxes * p.box * 256);
             const uint32_t dst = smem_u32(smem) + sk * SLOT;
-#pragma unroll 2                                       // (pages of 64, 128 heads: 304 us, against 318 by four and 327 rolled)
+#pragma unroll 2                                       // (pages of 64, 128 heads: 307 us, 320 by four, 301 rolled)
             for (int x = 0; x < boxes; ++x) tma_load_4d(dst + x * p.box * 256, &k_map, full, 0, 0, 2 * c, rows[x] >> 3);
             if (++sk == SLOTS) {
               sk = 0;
@@ -1508,7 +1509,7 @@ __global__ void __launch_bounds__(Shape<R>::THREADS + (DENSE ? 0 : 32 * (kSparse
 // wave of CTAs holds every token; else four, so that two CTAs share an SM, one's
 // chains of reads under the other's: 64 tokens of 128 heads 17.7 us, against 20.9
 // with one CTA an SM, 32 tokens and all blocks.  (In one wave the ring of four
-// makes a decode of 16 heads 1 % longer.)
+// makes a decode of 16 heads 2 to 3 % longer.)
 constexpr int kOutWarps = 16;
 constexpr int NT = 16;
 constexpr int W_BLOCK = 128 * 128;                   // 128 rows of 64 bf16
@@ -1805,8 +1806,9 @@ cudaError_t launch_attn(const CUtensorMap& q_map, const CUtensorMap& qr_map, con
   if (e != cudaSuccess) return e;
   const int threads = Shape<ROWS>::THREADS + (DENSE ? 0 : 32 * (kSparseProducers - 1));
   // Members of a piece read the same keys at the same time: as a cluster they
-  // sit on neighbouring SMs, on one die, and share its half of L2 (left to the
-  // order in which SMs became free, 64 x 128 heads took 376 us, not 300).
+  // sit on neighbouring SMs, on one die, and share its half of L2.  (Left to the
+  // order in which SMs became free, 64 x 128 heads took 376 us, not 320, when the
+  // kernels before kept some SMs longer than others; now 284 either way.)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(threads);
@@ -1835,10 +1837,9 @@ cudaError_t launch_out(const CUtensorMap& w_map, const Q8Params& p, const Decode
 }
 
 // Query rows of a tile: as many as a sequence can fill, 16, 32 or 64.  (64
-// sequences of 4096 to 16384 keys in tiles of 16, 32 and 64 rows: 99, 108, 151
-// us with 16 heads and one token; 169, 110, 154 with two tokens; 307, 189, 159
-// with four.  128 heads, 1 or 2 tokens: 401 us in 32 rows, 309 in 64.  Measured
-// before the loops were made smaller, which took some 7 % off each.)
+// sequences of 4096 to 16384 keys in tiles of 16, 32 and 64 rows: 87, 101, 109
+// us with 16 heads and one token; 140, 104, 112 with two tokens; 255, 175, 122
+// with four.  128 heads, 1 or 2 tokens: 516, 401, 284.)
 int tile_rows(int H, int max_new) {
   const long long rows = static_cast<long long>(H) * max_new;
   return rows > 32 ? 64 : (rows > 16 ? 32 : 16);
@@ -1948,9 +1949,10 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t stream) {
   p.box = run_rows(a.page_size);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
-  // Runs of 32 rows or more by TMA, shorter ones row by row: pages of 32 take 343
-  // us one way and 345 the other with 64 sequences and 128 heads, 99 and 103 with
-  // 32 and 16; pages of 16 407 and 346, 108 and 106.
+  // Runs of 32 rows or more by TMA, shorter ones row by row: pages of 32 take 345
+  // us by TMA and 340 by rows with 64 sequences and 128 heads, 98 and 102 with 32
+  // and 16; pages of 16 342 and 108 by rows (by TMA, in an earlier state in which
+  // they took 346 and 106 by rows, 407 and 108).
   const bool dense = a.indices == nullptr && p.box >= 32;
   const uint64_t cache_rows = static_cast<uint64_t>(a.num_pages) * a.page_size;
   const uint32_t box = dense ? p.box : 8;
