@@ -80,7 +80,8 @@ enum {
   MLA_DEV_TOO_MANY_CHUNKS = 1, /* the plan needs more than max_chunks rows (truncated) */
   MLA_DEV_BAD_OFFSETS = 2,     /* input_row_offsets[0] != 0, decreasing, or total >= 2^31 */
   MLA_DEV_BAD_PAGE = 3,        /* a page-table entry is negative or >= num_pages */
-  MLA_DEV_TIMEOUT = 4          /* a pipeline wait exceeded its limit; the kernel drained and exited */
+  MLA_DEV_TIMEOUT = 4,         /* a pipeline wait exceeded its limit; the kernel drained and exited */
+  MLA_DEV_NO_PAGES = 5         /* a reservation wants more pages than are free; nothing was changed */
 };
 
 enum { MLA_BF16 = 0, MLA_E4M3 = 1 };
@@ -765,6 +766,183 @@ mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* sc
                               int32_t batch_size, int32_t total_q_tokens, int32_t max_seq_len,
                               int32_t scores_stride, int32_t indices_stride, int32_t* d_status,
                               mla_stream_t stream);
+
+/*
+ * mla_latent_cache_write for drafts ("mla_prefill_decode_graph_bf16", Args:
+ * freqs_cis, kv_norm_gamma, epsilon; kv_collection).  The tokens of a draft
+ * tree sit in consecutive slots behind the context, but a draft's position in
+ * the text is the context plus its depth in the tree: token t is rotated by
+ * freqs_cis[rope_positions[t]] and stored, as above, at context position
+ * cache_lengths[b] + i.
+ *
+ * rope_positions: [total_q_tokens] uint32
+ * Other arguments and errors as mla_latent_cache_write, but that a position is
+ * too large (MLA_DEV_BAD_OFFSETS, the token is skipped) if rope_positions[t] >=
+ * max_seq_len, which is the number of rows of freqs_cis.
+ */
+mla_status_t mla_latent_cache_write_at(void* kv_cache, void* q, const void* kv_latent,
+                                       const float* kv_norm_gamma, const float* freqs_cis,
+                                       const uint32_t* rope_positions,
+                                       const uint32_t* input_row_offsets,
+                                       const uint32_t* cache_lengths, const int32_t* page_table,
+                                       int32_t num_pages, int32_t page_size,
+                                       int32_t max_pages_per_seq, int32_t batch_size,
+                                       int32_t num_heads, int32_t total_q_tokens,
+                                       int32_t max_seq_len, float epsilon, float kv_inv_scale,
+                                       int32_t dtype, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * Bookkeeping of the paged cache.  The pages have no counterpart: they take a
+ * kv_collection whose pages somebody else hands out.
+ *
+ * The pool's state is ref_counts [num_pages] int32: how many table rows hold
+ * the page.  A page is free iff its count is 0; pages are handed out lowest
+ * first.  A table row holds the pages of its entries >= 0; unused entries are
+ * -1.  One table, its lengths and one ref_counts serve every cache that is laid
+ * out by the same page ids (layers, scales, index keys).  Counts, tables and
+ * lists that the calls return depend on their inputs alone.  All calls are
+ * asynchronous; what moves data are mla_pages_copy and mla_cache_keep_rows,
+ * called once for each cache before the moved pages are used.
+ * Arrays of a batch of 0 may be NULL.
+ * Tables whose rows hold a page twice, or counts that are not the number of
+ * rows that hold a page, give tables and counts that mean nothing.
+ *
+ * mla_pages_fork: a new table whose row b continues row parents[b] of the old
+ * one (any number of rows may continue the same one): beam search, several
+ * samples of a prompt, reordering.
+ *   dst_table[b] = src_table[parents[b]], dst_lengths[b] = src_lengths[parents[b]]
+ *   ref_counts[x] += sum over old rows a that hold x of (rows b with parents[b]
+ *   == a) - 1
+ * parents[b] == -1 gives an empty row of length 0.  The old rows end with the
+ * call: those that nobody continues lose their pages.  Pages, the last partly
+ * filled one as well, are shared; mla_pages_reserve makes the copies.
+ *
+ * dst_table [dst_batch][max_pages_per_seq] int32, dst_lengths [dst_batch]
+ *           uint32, outputs; they must not overlap src_table
+ *           [src_batch][max_pages_per_seq] and src_lengths [src_batch]
+ * ref_counts: [num_pages] int32, updated
+ * parents:  [dst_batch] int32
+ * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS (a parent
+ * outside [-1, src_batch): an empty row), MLA_DEV_BAD_PAGE (a page id >=
+ * num_pages: that entry becomes -1).
+ */
+mla_status_t mla_pages_fork(int32_t* dst_table, uint32_t* dst_lengths, const int32_t* src_table,
+                            const uint32_t* src_lengths, int32_t* ref_counts, const int32_t* parents,
+                            int32_t num_pages, int32_t max_pages_per_seq, int32_t dst_batch, int32_t src_batch,
+                            int32_t* d_status, mla_stream_t stream);
+
+/*
+ * Pages given back (no counterpart on the pages).  Sequence b keeps its first
+ * n = min(cache_lengths[b], keep_lengths[b]) tokens: entries from ceil(n /
+ * page_size) on lose a count and become -1, cache_lengths[b] becomes n.
+ * keep_lengths NULL ends every sequence.  keep_lengths may be cache_lengths
+ * itself: pages that were reserved beyond the context are given back.
+ *
+ * page_table [batch_size][max_pages_per_seq], ref_counts, cache_lengths
+ * [batch_size]: updated
+ * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_PAGE (a page id
+ * >= num_pages, or a page whose count is 0 already: the entry becomes -1, the
+ * count stays).
+ */
+mla_status_t mla_pages_free(int32_t* page_table, int32_t* ref_counts, uint32_t* cache_lengths,
+                            const uint32_t* keep_lengths, int32_t num_pages, int32_t page_size,
+                            int32_t max_pages_per_seq, int32_t batch_size, int32_t* d_status,
+                            mla_stream_t stream);
+
+/*
+ * Device memory that mla_pages_reserve and mla_pages_compact work in (256-byte
+ * aligned; its contents mean nothing between calls; one call at a time).  Host
+ * only; 0 for invalid sizes.  The pages have no counterpart.
+ */
+size_t mla_pages_workspace_bytes(int32_t num_pages, int32_t batch_size);
+
+/*
+ * Pages for new_tokens[b] tokens behind the cache_lengths[b] of every sequence
+ * (no counterpart on the pages).  Of the pages that positions [len, len + new)
+ * fall in:
+ *   - a missing one (-1) is taken from the pool;
+ *   - one that other rows hold too is exchanged for a new one, the old one
+ *     loses a count, and if rows before len lie in it the pair (old, new) goes
+ *     on the list of copies.  Where all holders of a page are writers of this
+ *     call, the last of them (largest b) keeps it;
+ *   - any other is kept.
+ * New pages are the lowest free ones in the order of (b, position), with count
+ * 1.  All or nothing: on an error nothing is changed and no copy is listed.
+ * cache_lengths is left to the caller, who knows when the tokens are there.
+ *
+ * new_tokens: [batch_size] uint32, 0 for sequences that take no part
+ * copy_src, copy_dst: [batch_size] int32, outputs in the order of b, -1 behind
+ *             the last; copy_count: [1] int32, output
+ * Errors: host MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH; device
+ * MLA_DEV_NO_PAGES, MLA_DEV_BAD_PAGE (tokens past max_pages_per_seq pages, or a
+ * page id >= num_pages).
+ */
+mla_status_t mla_pages_reserve(int32_t* page_table, int32_t* ref_counts, const uint32_t* cache_lengths,
+                               const uint32_t* new_tokens, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* copy_count, int32_t num_pages, int32_t page_size,
+                               int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
+                               size_t workspace_bytes, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * The live pages moved to the low end of the pool, so that its high end can be
+ * given to somebody else (no counterpart on the pages).  The k-th highest live
+ * page moves to the k-th lowest free page for as long as that is lower, and for
+ * k < max_copies: a small max_copies does a part of the work, the highest pages
+ * first.  Counts move with the pages; page_table's entries are renamed, so it
+ * has to hold every row that refers to the pool.
+ *
+ * page_table [batch_size][max_pages_per_seq], ref_counts: updated
+ * copy_src, copy_dst: [max_copies] int32, outputs, -1 behind the last;
+ * copy_count: [1] int32, output.  No page is both a source and a destination.
+ * Errors: host MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH; device
+ * MLA_DEV_BAD_PAGE (an entry >= num_pages: left as it is).
+ */
+mla_status_t mla_pages_compact(int32_t* page_table, int32_t* ref_counts, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* copy_count, int32_t max_copies, int32_t num_pages,
+                               int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
+                               size_t workspace_bytes, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * The copies that mla_pages_reserve or mla_pages_compact list, in one cache: page
+ * copy_dst[k] becomes page copy_src[k] in every layer, for k <
+ * min(copy_count[0], max_copies).  The pages have no counterpart.
+ *
+ * cache:      num_layers arrays [num_pages][page_bytes], layer_stride bytes apart
+ * page_bytes: a multiple of 4 (576 * 2 * page_size for the bf16 latent cache;
+ *             16-byte multiples of size, stride and address are faster)
+ * copy_count: [1] int32 on the device; max_copies bounds it (sizes the grid)
+ * A destination must not be another copy's source or destination.
+ * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_PAGE (an id
+ * outside [0, num_pages): that copy is left out).
+ */
+mla_status_t mla_pages_copy(void* cache, size_t page_bytes, int32_t num_layers, size_t layer_stride,
+                            const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_count,
+                            int32_t max_copies, int32_t num_pages, int32_t* d_status, mla_stream_t stream);
+
+/*
+ * The rows of accepted drafts moved together behind the context, in every layer
+ * of one cache (no counterpart on the pages): the row at position
+ * cache_lengths[b] + k becomes what the row at cache_lengths[b] + keep[b][k]
+ * was, for k < keep_counts[b].  Drafts written by mla_latent_cache_write_at keep
+ * their rotation: the k-th accepted one has depth k.  cache_lengths is left to
+ * the caller (add keep_counts).
+ *
+ * cache:     num_layers arrays [num_pages][page_size][row_bytes], layer_stride
+ *            bytes apart
+ * row_bytes: a multiple of 4: 1152 for the bf16 latent cache, 576 for 8-bit
+ *            codes and 4 for their scales where each token has its own
+ *            (scale_block 1; rows of a scale shared by several tokens cannot be
+ *            moved without requantising them: not offered)
+ * keep:      [batch_size][keep_stride] int32, strictly ascending from 0 on
+ * Errors: host MLA_ERR_ARG, MLA_ERR_LAUNCH; device MLA_DEV_BAD_OFFSETS (a list
+ * that does not ascend strictly from 0 on or is longer than keep_stride),
+ * MLA_DEV_BAD_PAGE (a position without a page): nothing of that sequence moves.
+ */
+mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_layers, size_t layer_stride,
+                                 const uint32_t* cache_lengths, const int32_t* keep, int32_t keep_stride,
+                                 const int32_t* keep_counts, const int32_t* page_table, int32_t num_pages,
+                                 int32_t page_size, int32_t max_pages_per_seq, int32_t batch_size,
+                                 int32_t* d_status, mla_stream_t stream);
 
 #ifdef __cplusplus
 }

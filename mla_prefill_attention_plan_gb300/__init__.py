@@ -28,6 +28,7 @@ MLA_DEV_TOO_MANY_CHUNKS = 1
 MLA_DEV_BAD_OFFSETS = 2
 MLA_DEV_BAD_PAGE = 3
 MLA_DEV_TIMEOUT = 4
+MLA_DEV_NO_PAGES = 5
 MLA_BF16 = 0
 MLA_E4M3 = 1
 
@@ -79,6 +80,15 @@ SIGNATURES = {
                               _I, _I, _P, _P]),
     "mla_index_select": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                               _P, _P]),
+    "mla_latent_cache_write_at": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                       _I, _F, _F, _I, _P, _P]),
+    "mla_pages_fork": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "mla_pages_free": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "mla_pages_workspace_bytes": (_Z, [_I, _I]),
+    "mla_pages_reserve": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _Z, _P, _P]),
+    "mla_pages_compact": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _Z, _P, _P]),
+    "mla_pages_copy": (_I, [_P, _Z, _I, _Z, _P, _P, _P, _I, _I, _P, _P]),
+    "mla_cache_keep_rows": (_I, [_P, _Z, _I, _Z, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P]),
 }
 
 _lib = None
@@ -386,6 +396,70 @@ def mla_index_select(indices, counts, scores, input_row_offsets, cache_lengths, 
         _ptr(page_table), num_pages, page_size, max_pages_per_seq, block, top_blocks, num_local,
         batch_size, total_q_tokens, max_seq_len, scores_stride, indices_stride, _ptr(d_status),
         _stream(stream))
+
+
+def mla_latent_cache_write_at(kv_cache, q, kv_latent, kv_norm_gamma, freqs_cis, rope_positions,
+                              input_row_offsets, cache_lengths, page_table, num_pages, page_size,
+                              max_pages_per_seq, batch_size, num_heads, total_q_tokens, max_seq_len,
+                              epsilon, kv_inv_scale, dtype, d_status=None, stream=None) -> int:
+    return load().mla_latent_cache_write_at(
+        _ptr(kv_cache), _ptr(q), _ptr(kv_latent), _ptr(kv_norm_gamma), _ptr(freqs_cis),
+        _ptr(rope_positions), _ptr(input_row_offsets), _ptr(cache_lengths), _ptr(page_table),
+        num_pages, page_size, max_pages_per_seq, batch_size, num_heads, total_q_tokens, max_seq_len,
+        epsilon, kv_inv_scale, dtype, _ptr(d_status), _stream(stream))
+
+
+def mla_pages_fork(dst_table, dst_lengths, src_table, src_lengths, ref_counts, parents, num_pages,
+                   max_pages_per_seq, dst_batch, src_batch, d_status=None, stream=None) -> int:
+    return load().mla_pages_fork(
+        _ptr(dst_table), _ptr(dst_lengths), _ptr(src_table), _ptr(src_lengths), _ptr(ref_counts),
+        _ptr(parents), num_pages, max_pages_per_seq, dst_batch, src_batch, _ptr(d_status),
+        _stream(stream))
+
+
+def mla_pages_free(page_table, ref_counts, cache_lengths, keep_lengths, num_pages, page_size,
+                   max_pages_per_seq, batch_size, d_status=None, stream=None) -> int:
+    return load().mla_pages_free(
+        _ptr(page_table), _ptr(ref_counts), _ptr(cache_lengths), _ptr(keep_lengths), num_pages,
+        page_size, max_pages_per_seq, batch_size, _ptr(d_status), _stream(stream))
+
+
+def mla_pages_workspace_bytes(num_pages, batch_size) -> int:
+    return load().mla_pages_workspace_bytes(num_pages, batch_size)
+
+
+def mla_pages_reserve(page_table, ref_counts, cache_lengths, new_tokens, copy_src, copy_dst,
+                      copy_count, num_pages, page_size, max_pages_per_seq, batch_size, workspace=None,
+                      workspace_bytes=0, d_status=None, stream=None) -> int:
+    return load().mla_pages_reserve(
+        _ptr(page_table), _ptr(ref_counts), _ptr(cache_lengths), _ptr(new_tokens), _ptr(copy_src),
+        _ptr(copy_dst), _ptr(copy_count), num_pages, page_size, max_pages_per_seq, batch_size,
+        _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
+
+
+def mla_pages_compact(page_table, ref_counts, copy_src, copy_dst, copy_count, max_copies, num_pages,
+                      max_pages_per_seq, batch_size, workspace=None, workspace_bytes=0,
+                      d_status=None, stream=None) -> int:
+    return load().mla_pages_compact(
+        _ptr(page_table), _ptr(ref_counts), _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count),
+        max_copies, num_pages, max_pages_per_seq, batch_size, _ptr(workspace), workspace_bytes,
+        _ptr(d_status), _stream(stream))
+
+
+def mla_pages_copy(cache, page_bytes, num_layers, layer_stride, copy_src, copy_dst, copy_count,
+                   max_copies, num_pages, d_status=None, stream=None) -> int:
+    return load().mla_pages_copy(
+        _ptr(cache), page_bytes, num_layers, layer_stride, _ptr(copy_src), _ptr(copy_dst),
+        _ptr(copy_count), max_copies, num_pages, _ptr(d_status), _stream(stream))
+
+
+def mla_cache_keep_rows(cache, row_bytes, num_layers, layer_stride, cache_lengths, keep, keep_stride,
+                        keep_counts, page_table, num_pages, page_size, max_pages_per_seq, batch_size,
+                        d_status=None, stream=None) -> int:
+    return load().mla_cache_keep_rows(
+        _ptr(cache), row_bytes, num_layers, layer_stride, _ptr(cache_lengths), _ptr(keep),
+        keep_stride, _ptr(keep_counts), _ptr(page_table), num_pages, page_size, max_pages_per_seq,
+        batch_size, _ptr(d_status), _stream(stream))
 
 
 __all__ = [n for n in SIGNATURES] + ["load", "check", "status_string", "MLAError", "LIB_PATH"]

@@ -132,6 +132,7 @@ const char* mla_status_string(int32_t code) {
     case MLA_DEV_BAD_OFFSETS: return "device: malformed input_row_offsets or lengths";
     case MLA_DEV_BAD_PAGE: return "device: page id out of range";
     case MLA_DEV_TIMEOUT: return "device: pipeline wait timed out";
+    case MLA_DEV_NO_PAGES: return "device: the pool has too few free pages";
     default: return "unknown status";
   }
 }
@@ -155,15 +156,16 @@ mla_status_t mla_selftest_bounded_wait(int32_t* d_status, int64_t* d_elapsed_ns,
                                                      static_cast<cudaStream_t>(stream)));
 }
 
-mla_status_t mla_latent_cache_write(void* kv_cache, void* q, const void* kv_latent,
-                                    const float* kv_norm_gamma, const float* freqs_cis,
-                                    const uint32_t* input_row_offsets,
-                                    const uint32_t* cache_lengths, const int32_t* page_table,
-                                    int32_t num_pages, int32_t page_size,
-                                    int32_t max_pages_per_seq, int32_t batch_size,
-                                    int32_t num_heads, int32_t total_q_tokens,
-                                    int32_t max_seq_len, float epsilon, float kv_inv_scale,
-                                    int32_t dtype, int32_t* d_status, mla_stream_t stream) {
+static mla_status_t cache_write_impl(void* kv_cache, void* q, const void* kv_latent,
+                                     const float* kv_norm_gamma, const float* freqs_cis,
+                                     const uint32_t* input_row_offsets,
+                                     const uint32_t* cache_lengths, const int32_t* page_table,
+                                     int32_t num_pages, int32_t page_size,
+                                     int32_t max_pages_per_seq, int32_t batch_size,
+                                     int32_t num_heads, int32_t total_q_tokens,
+                                     int32_t max_seq_len, float epsilon, float kv_inv_scale,
+                                     const uint32_t* rope_positions, int32_t dtype,
+                                     int32_t* d_status, mla_stream_t stream) {
   if (!dtype_ok(dtype)) return MLA_ERR_DTYPE;
   if (!kv_cache || !kv_latent || !kv_norm_gamma || !freqs_cis || !input_row_offsets ||
       !cache_lengths || !page_table || !aligned16(kv_cache) || !aligned16(kv_latent) ||
@@ -191,8 +193,39 @@ mla_status_t mla_latent_cache_write(void* kv_cache, void* q, const void* kv_late
   a.eps = epsilon;
   a.inv_scale = kv_inv_scale;
   a.elt_bytes = elt_bytes(dtype);
+  a.rope_positions = rope_positions;
   a.status = d_status;
   return from_cuda(mla::launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_latent_cache_write(void* kv_cache, void* q, const void* kv_latent,
+                                    const float* kv_norm_gamma, const float* freqs_cis,
+                                    const uint32_t* input_row_offsets,
+                                    const uint32_t* cache_lengths, const int32_t* page_table,
+                                    int32_t num_pages, int32_t page_size,
+                                    int32_t max_pages_per_seq, int32_t batch_size,
+                                    int32_t num_heads, int32_t total_q_tokens,
+                                    int32_t max_seq_len, float epsilon, float kv_inv_scale,
+                                    int32_t dtype, int32_t* d_status, mla_stream_t stream) {
+  return cache_write_impl(kv_cache, q, kv_latent, kv_norm_gamma, freqs_cis, input_row_offsets, cache_lengths,
+                          page_table, num_pages, page_size, max_pages_per_seq, batch_size, num_heads, total_q_tokens,
+                          max_seq_len, epsilon, kv_inv_scale, nullptr, dtype, d_status, stream);
+}
+
+mla_status_t mla_latent_cache_write_at(void* kv_cache, void* q, const void* kv_latent,
+                                       const float* kv_norm_gamma, const float* freqs_cis,
+                                       const uint32_t* rope_positions,
+                                       const uint32_t* input_row_offsets,
+                                       const uint32_t* cache_lengths, const int32_t* page_table,
+                                       int32_t num_pages, int32_t page_size,
+                                       int32_t max_pages_per_seq, int32_t batch_size,
+                                       int32_t num_heads, int32_t total_q_tokens,
+                                       int32_t max_seq_len, float epsilon, float kv_inv_scale,
+                                       int32_t dtype, int32_t* d_status, mla_stream_t stream) {
+  if (dtype_ok(dtype) && !rope_positions) return MLA_ERR_ARG;
+  return cache_write_impl(kv_cache, q, kv_latent, kv_norm_gamma, freqs_cis, input_row_offsets, cache_lengths,
+                          page_table, num_pages, page_size, max_pages_per_seq, batch_size, num_heads, total_q_tokens,
+                          max_seq_len, epsilon, kv_inv_scale, rope_positions, dtype, d_status, stream);
 }
 
 mla_status_t mla_prefill_plan(uint32_t* buffer_row_offsets, uint32_t* cache_offsets,
@@ -798,6 +831,173 @@ mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* sc
   a.rows_stride = indices_stride;
   a.status = d_status;
   return from_cuda(mla::launch_index_select(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ pages
+mla_status_t mla_pages_fork(int32_t* dst_table, uint32_t* dst_lengths, const int32_t* src_table,
+                            const uint32_t* src_lengths, int32_t* ref_counts, const int32_t* parents,
+                            int32_t num_pages, int32_t max_pages_per_seq, int32_t dst_batch, int32_t src_batch,
+                            int32_t* d_status, mla_stream_t stream) {
+  if (!ref_counts || num_pages < 1 || max_pages_per_seq < 1 || dst_batch < 0 || src_batch < 0 ||
+      static_cast<int64_t>(dst_batch) + src_batch >= (1ll << 31) ||
+      (dst_batch > 0 && (!dst_table || !dst_lengths || !parents)) || (src_batch > 0 && (!src_table || !src_lengths)))
+    return MLA_ERR_ARG;
+  // A row may be read after it has been written: the tables must not overlap.
+  const char *d = reinterpret_cast<const char*>(dst_table), *c = reinterpret_cast<const char*>(src_table);
+  const size_t row = sizeof(int32_t) * static_cast<size_t>(max_pages_per_seq);
+  if (d < c + row * src_batch && c < d + row * dst_batch) return MLA_ERR_ARG;
+  const char *dl = reinterpret_cast<const char*>(dst_lengths), *sl = reinterpret_cast<const char*>(src_lengths);
+  if (dl < sl + 4 * static_cast<size_t>(src_batch) && sl < dl + 4 * static_cast<size_t>(dst_batch)) return MLA_ERR_ARG;
+  mla::PagesForkArgs a;
+  a.dst_table = dst_table;
+  a.dst_lengths = dst_lengths;
+  a.src_table = src_table;
+  a.src_lengths = src_lengths;
+  a.refs = ref_counts;
+  a.parents = parents;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.dst_batch = dst_batch;
+  a.src_batch = src_batch;
+  a.status = d_status;
+  return from_cuda(mla::launch_pages_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_pages_free(int32_t* page_table, int32_t* ref_counts, uint32_t* cache_lengths,
+                            const uint32_t* keep_lengths, int32_t num_pages, int32_t page_size,
+                            int32_t max_pages_per_seq, int32_t batch_size, int32_t* d_status,
+                            mla_stream_t stream) {
+  if (!ref_counts || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      (batch_size > 0 && (!page_table || !cache_lengths)))
+    return MLA_ERR_ARG;
+  mla::PagesFreeArgs a;
+  a.table = page_table;
+  a.refs = ref_counts;
+  a.lengths = cache_lengths;
+  a.keep = keep_lengths;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch_size;
+  a.status = d_status;
+  return from_cuda(mla::launch_pages_free(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_pages_workspace_bytes(int32_t num_pages, int32_t batch_size) {
+  if (num_pages < 1 || batch_size < 0) return 0;
+  return 4 * round_up(sizeof(int32_t) * static_cast<size_t>(num_pages), 256) +
+         round_up(sizeof(int2) * static_cast<size_t>(batch_size), 256);
+}
+
+mla_status_t mla_pages_reserve(int32_t* page_table, int32_t* ref_counts, const uint32_t* cache_lengths,
+                               const uint32_t* new_tokens, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* copy_count, int32_t num_pages, int32_t page_size,
+                               int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
+                               size_t workspace_bytes, int32_t* d_status, mla_stream_t stream) {
+  if (!ref_counts || !copy_count || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      (batch_size > 0 && (!page_table || !cache_lengths || !new_tokens || !copy_src || !copy_dst)))
+    return MLA_ERR_ARG;
+  if (!workspace || workspace_bytes < mla_pages_workspace_bytes(num_pages, batch_size) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return MLA_ERR_WORKSPACE;
+  const size_t step = round_up(sizeof(int32_t) * static_cast<size_t>(num_pages), 256);
+  char* w = static_cast<char*>(workspace);
+  mla::PagesReserveArgs a;
+  a.table = page_table;
+  a.refs = ref_counts;
+  a.lengths = cache_lengths;
+  a.fresh = new_tokens;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_count = copy_count;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch_size;
+  a.before = reinterpret_cast<int32_t*>(w);
+  a.writers = reinterpret_cast<int32_t*>(w + step);
+  a.last = reinterpret_cast<int32_t*>(w + 2 * step);
+  a.free_list = reinterpret_cast<int32_t*>(w + 3 * step);
+  a.want = reinterpret_cast<int2*>(w + 4 * step);
+  a.status = d_status;
+  return from_cuda(mla::launch_pages_reserve(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_pages_compact(int32_t* page_table, int32_t* ref_counts, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* copy_count, int32_t max_copies, int32_t num_pages,
+                               int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
+                               size_t workspace_bytes, int32_t* d_status, mla_stream_t stream) {
+  if (!ref_counts || !copy_count || max_copies < 0 || num_pages < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      (max_copies > 0 && (!copy_src || !copy_dst)) || (batch_size > 0 && !page_table))
+    return MLA_ERR_ARG;
+  if (!workspace || workspace_bytes < mla_pages_workspace_bytes(num_pages, batch_size) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return MLA_ERR_WORKSPACE;
+  mla::PagesCompactArgs a;
+  a.table = page_table;
+  a.refs = ref_counts;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_count = copy_count;
+  a.max_copies = max_copies;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch_size;
+  a.moved = static_cast<int32_t*>(workspace);
+  a.status = d_status;
+  return from_cuda(mla::launch_pages_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_pages_copy(void* cache, size_t page_bytes, int32_t num_layers, size_t layer_stride,
+                            const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_count,
+                            int32_t max_copies, int32_t num_pages, int32_t* d_status, mla_stream_t stream) {
+  if (!cache || page_bytes < 4 || page_bytes % 4 || page_bytes >= (1u << 31) || num_layers < 0 ||
+      (reinterpret_cast<uintptr_t>(cache) & 3u) || layer_stride % 4 || num_pages < 1 ||
+      (num_layers > 1 && layer_stride < page_bytes * static_cast<size_t>(num_pages)) || !copy_count ||
+      max_copies < 0 || (max_copies > 0 && (!copy_src || !copy_dst)))
+    return MLA_ERR_ARG;
+  mla::PagesCopyArgs a;
+  a.cache = static_cast<char*>(cache);
+  a.page_bytes = page_bytes;
+  a.layer_stride = layer_stride;
+  a.layers = num_layers;
+  a.src = copy_src;
+  a.dst = copy_dst;
+  a.count = copy_count;
+  a.max_copies = max_copies;
+  a.num_pages = num_pages;
+  a.status = d_status;
+  return from_cuda(mla::launch_pages_copy(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_layers, size_t layer_stride,
+                                 const uint32_t* cache_lengths, const int32_t* keep, int32_t keep_stride,
+                                 const int32_t* keep_counts, const int32_t* page_table, int32_t num_pages,
+                                 int32_t page_size, int32_t max_pages_per_seq, int32_t batch_size,
+                                 int32_t* d_status, mla_stream_t stream) {
+  if (!cache || row_bytes < 4 || row_bytes % 4 || row_bytes >= (1u << 31) || num_layers < 0 || num_layers > 65535 ||
+      (reinterpret_cast<uintptr_t>(cache) & 3u) || layer_stride % 4 || keep_stride < 1 || num_pages < 1 ||
+      page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      (batch_size > 0 && (!cache_lengths || !keep || !keep_counts || !page_table)) ||
+      static_cast<int64_t>(num_pages) * page_size >= (1ll << 31) ||
+      (num_layers > 1 && layer_stride < row_bytes * static_cast<size_t>(num_pages) * page_size))
+    return MLA_ERR_ARG;
+  mla::KeepRowsArgs a;
+  a.cache = static_cast<char*>(cache);
+  a.row_bytes = row_bytes;
+  a.layer_stride = layer_stride;
+  a.layers = num_layers;
+  a.lengths = cache_lengths;
+  a.keep = keep;
+  a.keep_stride = keep_stride;
+  a.counts = keep_counts;
+  a.table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch_size;
+  a.status = d_status;
+  return from_cuda(mla::launch_keep_rows(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -9,7 +9,9 @@
 // The row, times the cache's inverse scale, is stored at page
 // page_table[b][p / page_size], slot p % page_size, as bf16 or e4m3.  The rope
 // part (last 64 values) of every head of q[row] is rotated in place by the same
-// freqs_cis row.
+// freqs_cis row.  With rope positions given (AT: a draft sits at the next free
+// slot, but its position in the text is its depth in the tree), token t's row
+// of freqs_cis is rope_positions[t] instead of p.
 //
 // One CTA of 128 threads per token (grid-stride over tokens).  Thread j holds
 // latent values 4j..4j+3 (one 8-byte load), so the sum of squares is a warp
@@ -35,14 +37,15 @@ __device__ __forceinline__ float2 rotate(float re, float im, float c, float s) {
   return make_float2(fmaf(re, c, -im * s), fmaf(re, s, im * c));
 }
 
-template <int ELT>
+template <int ELT, bool AT>
 __global__ void __launch_bounds__(kThreads)
     cache_write_kernel(uint8_t* __restrict__ kv_cache, uint16_t* __restrict__ q,
                        const uint16_t* __restrict__ kv_latent, const float* __restrict__ gamma,
                        const float* __restrict__ freqs, const uint32_t* __restrict__ iro,
                        const uint32_t* __restrict__ cache_len, const int32_t* __restrict__ page_table,
                        int num_pages, int page_size, int max_pages, int B, int H, int T,
-                       int max_seq_len, float eps, float inv_scale, int32_t* status) {
+                       int max_seq_len, float eps, float inv_scale, const uint32_t* __restrict__ rope_positions,
+                       int32_t* status) {
   constexpr int kRowBytes = 576 * ELT;
   __shared__ float part[kThreads / 32];
   __shared__ int s_pos;
@@ -64,8 +67,9 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t a = iro[lo], e = iro[lo + 1];
       if (a <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < e) {
         const uint64_t p = static_cast<uint64_t>(cache_len[lo]) + (static_cast<uint32_t>(t) - a);
-        if (p < static_cast<uint64_t>(max_seq_len)) {
-          pos = static_cast<int>(p);
+        const uint64_t at = AT ? rope_positions[t] : p;
+        if (at < static_cast<uint64_t>(max_seq_len)) {
+          pos = static_cast<int>(at);
           const uint64_t pidx = p / static_cast<uint32_t>(page_size);
           const int page = pidx < static_cast<uint64_t>(max_pages)
                                ? page_table[static_cast<size_t>(lo) * max_pages + pidx] : -1;
@@ -150,17 +154,16 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream) {
   if (a.T <= 0) return cudaSuccess;
   const int grid = a.T < 16 * sm_count() ? a.T : 16 * sm_count();
-  if (a.elt_bytes == 2)
-    cache_write_kernel<2><<<grid, kThreads, 0, stream>>>(
+  auto launch = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, stream>>>(
         static_cast<uint8_t*>(a.kv_cache), static_cast<uint16_t*>(a.q), static_cast<const uint16_t*>(a.kv_latent),
         a.gamma, a.freqs, a.iro, a.cache_len, a.page_table, a.num_pages, a.page_size, a.max_pages, a.B, a.H, a.T,
-        a.max_seq_len, a.eps, a.inv_scale, a.status);
-  else
-    cache_write_kernel<1><<<grid, kThreads, 0, stream>>>(
-        static_cast<uint8_t*>(a.kv_cache), static_cast<uint16_t*>(a.q), static_cast<const uint16_t*>(a.kv_latent),
-        a.gamma, a.freqs, a.iro, a.cache_len, a.page_table, a.num_pages, a.page_size, a.max_pages, a.B, a.H, a.T,
-        a.max_seq_len, a.eps, a.inv_scale, a.status);
-  return cudaGetLastError();
+        a.max_seq_len, a.eps, a.inv_scale, a.rope_positions, a.status);
+    return cudaGetLastError();
+  };
+  if (a.rope_positions != nullptr)
+    return a.elt_bytes == 2 ? launch(cache_write_kernel<2, true>) : launch(cache_write_kernel<1, true>);
+  return a.elt_bytes == 2 ? launch(cache_write_kernel<2, false>) : launch(cache_write_kernel<1, false>);
 }
 
 }  // namespace mla

@@ -69,6 +69,7 @@ struct CacheWriteArgs {
   int num_pages, page_size, max_pages, B, H, T, max_seq_len;
   float eps, inv_scale;
   int elt_bytes;            // cache storage: 2 (bf16) or 1 (e4m3)
+  const uint32_t* rope_positions = nullptr;   // [T], or null: the context position
   int32_t* status;
 };
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream);
@@ -272,6 +273,84 @@ struct IndexSelectArgs {
   int32_t* status;
 };
 cudaError_t launch_index_select(const IndexSelectArgs& a, cudaStream_t stream);
+
+// Bookkeeping of the paged cache (pages.cu).
+struct PagesForkArgs {
+  int32_t* dst_table;         // [dst_batch][max_pages]
+  uint32_t* dst_lengths;
+  const int32_t* src_table;   // [src_batch][max_pages]
+  const uint32_t* src_lengths;
+  int32_t* refs;              // [num_pages]
+  const int32_t* parents;     // [dst_batch], -1 for none
+  int num_pages, max_pages, dst_batch, src_batch;
+  int32_t* status;
+};
+cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t stream);
+
+struct PagesFreeArgs {
+  int32_t* table;
+  int32_t* refs;
+  uint32_t* lengths;
+  const uint32_t* keep;       // [batch] or null (nothing is kept)
+  int num_pages, page_size, max_pages, batch;
+  int32_t* status;
+};
+cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t stream);
+
+struct PagesReserveArgs {
+  int32_t* table;
+  int32_t* refs;
+  const uint32_t* lengths;
+  const uint32_t* fresh;      // [batch] tokens to come
+  int32_t* copy_src;          // [batch]
+  int32_t* copy_dst;
+  int32_t* copy_count;
+  int num_pages, page_size, max_pages, batch;
+  // Scratch: of each page its count before the call, its writers and the last
+  // of them; the free pages in order; of each sequence (pages, copies).
+  int32_t *before, *writers, *last, *free_list;
+  int2* want;
+  int32_t* status;
+};
+cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream);
+
+struct PagesCompactArgs {
+  int32_t* table;
+  int32_t* refs;
+  int32_t* copy_src;          // [max_copies]
+  int32_t* copy_dst;
+  int32_t* copy_count;
+  int max_copies, num_pages, max_pages, batch;
+  int32_t* moved;             // scratch [num_pages]: the page's move
+  int32_t* status;
+};
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream);
+
+struct PagesCopyArgs {
+  char* cache;                // [layers] of [num_pages][page_bytes], layer_stride bytes apart
+  size_t page_bytes, layer_stride;
+  int layers;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int max_copies, num_pages;
+  int32_t* status;
+};
+cudaError_t launch_pages_copy(const PagesCopyArgs& a, cudaStream_t stream);
+
+struct KeepRowsArgs {
+  char* cache;                // [layers] of [num_pages * page_size][row_bytes]
+  size_t row_bytes, layer_stride;
+  int layers;
+  const uint32_t* lengths;
+  const int32_t* keep;        // [batch][keep_stride]
+  int keep_stride;
+  const int32_t* counts;
+  const int32_t* table;
+  int num_pages, page_size, max_pages, batch;
+  int32_t* status;
+};
+cudaError_t launch_keep_rows(const KeepRowsArgs& a, cudaStream_t stream);
 
 // Self-test of the bounded waits (selftest.cu): one cluster of `cluster`
 // CTAs waiting on barriers nothing arrives at.

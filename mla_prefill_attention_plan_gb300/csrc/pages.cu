@@ -1,0 +1,595 @@
+// The bookkeeping of the paged cache: page tables and reference counts (fork,
+// reserve, free, compact), and the data that they move (page copies in every
+// layer, accepted rows moved together).  The pages have no counterpart: they
+// take a cache whose pages somebody else hands out ("mla_prefill_decode_graph_bf16",
+// Args: kv_collection).
+//
+// The state of a pool is its reference counts alone: page p is free iff
+// ref[p] == 0, and pages are handed out lowest first.  A result is therefore a
+// function of the inputs, whatever order atomics take: sums commute, and every
+// rank is a prefix sum over page ids or (sequence, page) order.
+//
+// The reserving and compacting kernels are one cluster each: what they compute
+// is a chain of scans (who writes shared pages, how many pages each sequence
+// wants, which pages are free) that other kernels could only share by more
+// launches, and one SM alone reads a pool of 10^5 counts too slowly.  A warp
+// owns a contiguous range of page ids, so a scan costs one barrier, not one a
+// round.
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPoolCtas = 8;        // CTAs of a bookkeeping cluster (the portable most)
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
+
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ int warp_scan(int v, int lane) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ int ld_remote(const int* local, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem_u32(local), rank)) : "memory");
+  return v;
+}
+
+// ============================================================ fork
+// CTAs 0 .. dst_batch - 1 write a row of the new table; CTA dst_batch + a adds
+// (children of row a) - 1 to the counts of the pages that row a holds.
+__global__ void __launch_bounds__(256) fork_kernel(PagesForkArgs a) {
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int t = threadIdx.x;
+  if (blockIdx.x < static_cast<unsigned>(a.dst_batch)) {
+    const int b = blockIdx.x;
+    const int p = a.parents[b];
+    const bool ok = p >= 0 && p < a.src_batch;
+    if (t == 0) {
+      if (!ok && p != -1) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      a.dst_lengths[b] = ok ? a.src_lengths[p] : 0u;
+    }
+    const int32_t* src = a.src_table + static_cast<size_t>(ok ? p : 0) * a.max_pages;
+    int32_t* dst = a.dst_table + static_cast<size_t>(b) * a.max_pages;
+    for (int j = t; j < a.max_pages; j += 256) {
+      int v = ok ? src[j] : -1;
+      if (v >= a.num_pages) {
+        set_status(a.status, MLA_DEV_BAD_PAGE);
+        v = -1;
+      }
+      dst[j] = v < 0 ? -1 : v;
+    }
+    return;
+  }
+  const int row = blockIdx.x - a.dst_batch;
+  int n = 0;
+  for (int b = t; b < a.dst_batch; b += 256) n += a.parents[b] == row;
+  __shared__ int sums[8];
+  n = warp_sum(n);
+  if ((t & 31) == 0) sums[t >> 5] = n;
+  __syncthreads();
+  int more = -1;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) more += sums[w];
+  if (more == 0) return;
+  const int32_t* src = a.src_table + static_cast<size_t>(row) * a.max_pages;
+  for (int j = t; j < a.max_pages; j += 256) {
+    const int v = src[j];
+    if (v >= 0 && v < a.num_pages) atomicAdd(a.refs + v, more);
+  }
+}
+
+// ============================================================ free
+__global__ void __launch_bounds__(256) free_kernel(PagesFreeArgs a) {
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int b = blockIdx.x;
+  const uint32_t len = a.lengths[b];
+  const uint32_t keep = a.keep != nullptr ? min(len, a.keep[b]) : 0u;
+  const uint32_t first = keep / a.page_size + (keep % a.page_size != 0);
+  __syncthreads();                     // every thread has read the length (keep may be the same array)
+  if (threadIdx.x == 0) a.lengths[b] = keep;
+  int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+  for (long long j = static_cast<long long>(first) + threadIdx.x; j < a.max_pages; j += 256) {
+    const int v = row[j];
+    if (v < 0) continue;
+    row[j] = -1;
+    // A count that is already zero stays so.
+    if (v >= a.num_pages || atomicSub(a.refs + v, 1) <= 0) {
+      if (v < a.num_pages) atomicAdd(a.refs + v, 1);
+      set_status(a.status, MLA_DEV_BAD_PAGE);
+    }
+  }
+}
+
+// ============================================================ reserve
+struct PoolSmem {
+  int warp_count[kPoolWarps];     // free (live) pages in the warp's range
+  int tally[4];                   // of this CTA: pages wanted, copies, free pages, flags
+  int scan[kPoolWarps], scan2[kPoolWarps];
+};
+
+// The warp's contiguous range of page ids, a multiple of 128 long (an int4 a
+// lane) so that 16-byte loads of an aligned array stay aligned.
+__device__ __forceinline__ void warp_range(int n, int rank, int warp, int& lo, int& hi) {
+  const int parts = kPoolCtas * kPoolWarps;
+  const long long per = ((static_cast<long long>(n) + parts - 1) / parts + 127) / 128 * 128;
+  const long long at = per * (rank * kPoolWarps + warp);
+  lo = static_cast<int>(min(at, static_cast<long long>(n)));
+  hi = static_cast<int>(min(at + per, static_cast<long long>(n)));
+}
+
+// Four counts from index i on; past the end of the range they read as `past`.
+__device__ __forceinline__ int4 load4(const int32_t* p, int i, int hi, bool wide, int past) {
+  if (wide && i + 4 <= hi) return __ldcg(reinterpret_cast<const int4*>(p + i));
+  int4 v;
+  v.x = i < hi ? __ldcg(p + i) : past;
+  v.y = i + 1 < hi ? __ldcg(p + i + 1) : past;
+  v.z = i + 2 < hi ? __ldcg(p + i + 2) : past;
+  v.w = i + 3 < hi ? __ldcg(p + i + 3) : past;
+  return v;
+}
+
+enum { kBadPage = 1, kShared = 2, kStop = 4 };
+
+// The pages that sequence b writes to: [first, end) of its row, or none.
+struct Touched {
+  int first, end, len;
+  bool part;      // the first of them holds rows that are to be kept
+};
+__device__ __forceinline__ bool touched(const PagesReserveArgs& a, int b, Touched& t) {
+  const uint32_t len = a.lengths[b], n = a.fresh[b];
+  t.first = t.end = 0;
+  if (n == 0) return true;
+  const unsigned long long end = (static_cast<unsigned long long>(len) + n + a.page_size - 1) / a.page_size;
+  if (end > static_cast<unsigned long long>(a.max_pages)) return false;
+  t.first = static_cast<int>(len / a.page_size);
+  t.end = static_cast<int>(end);
+  t.part = len % a.page_size != 0;
+  return true;
+}
+
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
+    reserve_kernel(PagesReserveArgs a) {
+  __shared__ PoolSmem sh;
+  pdl_enter();
+  const bool stop = timed_out_before(a.status);   // the CTAs agree on it below
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const bool wide = (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
+  // Sequences of this CTA; a warp takes every 32nd of them.
+  const int per = (a.batch + kPoolCtas - 1) / kPoolCtas;
+  const int b0 = min(a.batch, rank * per), b1 = min(a.batch, b0 + per);
+  if (t < 4) sh.tally[t] = 0;
+  __syncthreads();
+
+  // The scratch words of the pages that are written to: their count now (the
+  // counts themselves change while others still decide), writers, last writer.
+  int flags = stop ? kStop : 0;
+  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
+    Touched s;
+    if (!touched(a, b, s)) flags |= kBadPage;
+    const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+    for (int j = s.first + lane; j < s.end; j += 32) {
+      const int v = row[j];
+      if (v >= a.num_pages) flags |= kBadPage;
+      else if (v >= 0) {
+        const int r = a.refs[v];
+        a.before[v] = r;
+        a.writers[v] = 0;
+        a.last[v] = -1;
+        if (r > 1) flags |= kShared;
+      }
+    }
+  }
+  int lo, hi, n_free = 0;
+  warp_range(a.num_pages, rank, warp, lo, hi);
+  for (int i = lo + 4 * lane; i < hi; i += 128) {
+    const int4 v = load4(a.refs, i, hi, wide, 1);
+    n_free += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  }
+  n_free = warp_sum(n_free);
+  if (lane == 0) {
+    sh.warp_count[warp] = n_free;
+    atomicAdd(&sh.tally[2], n_free);
+  }
+  if (flags) atomicOr(&sh.tally[3], flags);
+  cluster_sync();
+  int all = 0, free_before = 0, free_total = 0;
+#pragma unroll
+  for (int r = 0; r < kPoolCtas; ++r) {
+    all |= ld_remote(&sh.tally[3], r);
+    const int f = ld_remote(&sh.tally[2], r);
+    free_total += f;
+    if (r < rank) free_before += f;
+  }
+  if (all & kStop) {
+    cluster_sync();    // no CTA leaves while another reads its shared memory
+    return;
+  }
+  if (all & kShared) {
+    for (int b = b0 + warp; b < b1; b += kPoolWarps) {
+      Touched s;
+      if (!touched(a, b, s)) continue;
+      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+      for (int j = s.first + lane; j < s.end; j += 32) {
+        const int v = row[j];
+        if (v >= 0 && v < a.num_pages && __ldcg(a.before + v) > 1) {
+          atomicAdd(a.writers + v, 1);
+          atomicMax(a.last + v, b);
+        }
+      }
+    }
+    cluster_sync();
+  }
+  // A writer of a shared page takes a copy, but for the last one if nobody
+  // else holds the page.
+  auto takes = [&](int v, int b) {
+    const int r = __ldcg(a.before + v);
+    return r > 1 && !(__ldcg(a.writers + v) >= r && __ldcg(a.last + v) == b);
+  };
+  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
+    Touched s;
+    int want = 0, copy = 0;
+    if (touched(a, b, s)) {
+      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+      for (int j = s.first + lane; j < s.end; j += 32) {
+        const int v = row[j];
+        if (v >= a.num_pages) continue;
+        const bool shared = v >= 0 && takes(v, b);
+        want += v < 0 || shared;
+        copy += shared && s.part && j == s.first;
+      }
+    }
+    want = warp_sum(want);
+    copy = warp_sum(copy);
+    if (lane == 0) {
+      a.want[b] = make_int2(want, copy);
+      atomicAdd(&sh.tally[0], want);
+      atomicAdd(&sh.tally[1], copy);
+    }
+  }
+  cluster_sync();
+  int want_before = 0, copy_before = 0, copies = 0;
+  long long want_total = 0;
+#pragma unroll
+  for (int r = 0; r < kPoolCtas; ++r) {
+    const int w = ld_remote(&sh.tally[0], r), c = ld_remote(&sh.tally[1], r);
+    want_total += w;
+    copies += c;
+    if (r < rank) want_before += w, copy_before += c;
+  }
+  const bool ok = !(all & kBadPage) && want_total <= free_total;
+  if (!ok) copies = 0;
+  if (rank == 0 && t == 0) {
+    *a.copy_count = copies;
+    if (!ok) set_status(a.status, (all & kBadPage) ? MLA_DEV_BAD_PAGE : MLA_DEV_NO_PAGES);
+  }
+  for (int i = copies + rank * kPoolThreads + t; i < a.batch; i += kPoolCtas * kPoolThreads)
+    a.copy_src[i] = a.copy_dst[i] = -1;
+  if (ok) {
+    // The free pages in order, as many as are wanted.
+    int at = free_before;
+    for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
+    for (int i = lo; i < hi && at < want_total; i += 128) {
+      const int4 v = load4(a.refs, i + 4 * lane, hi, wide, 1);
+      const int mine = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+      const int upto = warp_scan(mine, lane);
+      int k = at + upto - mine, p = i + 4 * lane;
+      if (v.x == 0 && k < want_total) a.free_list[k] = p;
+      k += v.x == 0;
+      if (v.y == 0 && k < want_total) a.free_list[k] = p + 1;
+      k += v.y == 0;
+      if (v.z == 0 && k < want_total) a.free_list[k] = p + 2;
+      k += v.z == 0;
+      if (v.w == 0 && k < want_total) a.free_list[k] = p + 3;
+      at += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    // Where each sequence's pages and copies begin.
+    for (int base = b0; base < b1; base += kPoolThreads) {
+      const int b = base + t;
+      const int2 w = b < b1 ? __ldcg(a.want + b) : make_int2(0, 0);
+      const int sw = warp_scan(w.x, lane), sc = warp_scan(w.y, lane);
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = sw, sh.scan2[warp] = sc;
+      __syncthreads();
+      int ow = want_before, oc = copy_before, tw = 0, tc = 0;
+      for (int x = 0; x < kPoolWarps; ++x) {
+        if (x < warp) ow += sh.scan[x], oc += sh.scan2[x];
+        tw += sh.scan[x], tc += sh.scan2[x];
+      }
+      if (b < b1) a.want[b] = make_int2(ow + sw - w.x, oc + sc - w.y);
+      want_before += tw;
+      copy_before += tc;
+    }
+  }
+  cluster_sync();      // the last one: no CTA reads another's shared memory behind it
+  if (!ok) return;
+  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
+    Touched s;
+    if (!touched(a, b, s) || s.first == s.end) continue;
+    const int2 base = __ldcg(a.want + b);
+    int at = base.x;
+    int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+    for (int j0 = s.first; j0 < s.end; j0 += 32) {
+      const int j = j0 + lane;
+      const int v = j < s.end ? row[j] : 0;
+      const bool shared = j < s.end && v >= 0 && takes(v, b);
+      const bool want = j < s.end && (v < 0 || shared);
+      const unsigned m = __ballot_sync(0xffffffffu, want);
+      if (want) {
+        const int p = __ldcg(a.free_list + at + __popc(m & ((1u << lane) - 1)));
+        row[j] = p;
+        a.refs[p] = 1;
+        if (shared) atomicSub(a.refs + v, 1);
+        if (shared && s.part && j == s.first) {
+          a.copy_src[base.y] = v;
+          a.copy_dst[base.y] = p;
+        }
+      }
+      at += __popc(m);
+    }
+  }
+}
+
+// ============================================================ compact
+// With L live pages, the k-th highest live page moves to the k-th lowest free
+// one for as long as that is lower, which is for exactly the live pages >= L:
+// as many free pages lie below L.  So each page finds from its own rank
+// whether it takes part.
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
+    compact_kernel(PagesCompactArgs a) {
+  __shared__ PoolSmem sh;
+  pdl_enter();
+  const bool stop = timed_out_before(a.status);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const bool wide = (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
+  if (t < 4) sh.tally[t] = 0;
+  __syncthreads();
+  int lo, hi, n_live = 0;
+  warp_range(a.num_pages, rank, warp, lo, hi);
+  for (int i = lo + 4 * lane; i < hi; i += 128) {
+    const int4 v = load4(a.refs, i, hi, wide, 0);
+    n_live += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+  }
+  n_live = warp_sum(n_live);
+  if (lane == 0) {
+    sh.warp_count[warp] = n_live;
+    atomicAdd(&sh.tally[0], n_live);
+  }
+  if (stop) sh.tally[3] = kStop;
+  cluster_sync();
+  int at = 0, live = 0, all = 0;
+#pragma unroll
+  for (int r = 0; r < kPoolCtas; ++r) {
+    all |= ld_remote(&sh.tally[3], r);
+    const int f = ld_remote(&sh.tally[0], r);
+    live += f;
+    if (r < rank) at += f;
+  }
+  if (all & kStop) {
+    cluster_sync();
+    return;
+  }
+  for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
+  int movers = 0;
+  for (int i = lo; i < hi; i += 128) {
+    const int4 v = load4(a.refs, i + 4 * lane, hi, wide, 0);
+    const int is[4] = {v.x > 0, v.y > 0, v.z > 0, v.w > 0};
+    const int mine = is[0] + is[1] + is[2] + is[3];
+    const int upto = warp_scan(mine, lane);
+    int k = at + upto - mine;                       // live pages below p
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = i + 4 * lane + e;
+      if (p < hi) {
+        if (is[e] && p >= live) {
+          ++movers;
+          if (live - 1 - k < a.max_copies) a.copy_src[live - 1 - k] = p;
+        } else if (!is[e] && p < live && p - k < a.max_copies) {
+          a.copy_dst[p - k] = p;
+        }
+      }
+      k += is[e];
+    }
+    at += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  movers = warp_sum(movers);
+  if (lane == 0 && movers) atomicAdd(&sh.tally[1], movers);
+  cluster_sync();
+  int n = 0;
+#pragma unroll
+  for (int r = 0; r < kPoolCtas; ++r) n += ld_remote(&sh.tally[1], r);
+  n = min(n, a.max_copies);
+  if (rank == 0 && t == 0) *a.copy_count = n;
+  for (int k = rank * kPoolThreads + t; k < a.max_copies; k += kPoolCtas * kPoolThreads) {
+    if (k < n) {
+      const int p = __ldcg(a.copy_src + k), q = __ldcg(a.copy_dst + k);
+      a.refs[q] = a.refs[p];
+      a.refs[p] = 0;
+      a.moved[p] = k;
+    } else {
+      a.copy_src[k] = a.copy_dst[k] = -1;
+    }
+  }
+  cluster_sync();      // no CTA leaves while another reads its shared memory
+}
+
+// Table entries of moved pages.  A page's word of the scratch is only good if
+// the move that it names is that page's.
+__global__ void __launch_bounds__(256) remap_kernel(PagesCompactArgs a) {
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int n = *a.copy_count;
+  if (n == 0) return;
+  const int lowest = a.copy_src[n - 1];            // sources come highest first
+  const long long entries = static_cast<long long>(a.batch) * a.max_pages;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll) {
+    const int v = a.table[i];
+    if (v < lowest) continue;
+    if (v >= a.num_pages) {
+      set_status(a.status, MLA_DEV_BAD_PAGE);
+      continue;
+    }
+    const int k = a.moved[v];
+    if (k >= 0 && k < n && a.copy_src[k] == v) a.table[i] = a.copy_dst[k];
+  }
+}
+
+// ============================================================ copies
+// Page copies in every layer: pieces of kCopyPiece bytes, four vectors a
+// thread in flight before the first is stored.  Bound by HBM: each byte is
+// read and written once.
+constexpr int kCopyThreads = 256, kCopyUnroll = 4;
+
+template <typename V>
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(PagesCopyArgs a) {
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int n = min(*a.count, a.max_copies);
+  const unsigned per_piece = kCopyThreads * kCopyUnroll;
+  const unsigned vecs = static_cast<unsigned>(a.page_bytes / sizeof(V));
+  const unsigned pieces = (vecs + per_piece - 1) / per_piece;
+  const long long units = static_cast<long long>(max(n, 0)) * a.layers * pieces;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const unsigned piece = static_cast<unsigned>(u % pieces);
+    const long long v = u / pieces;
+    const int k = static_cast<int>(v % n), layer = static_cast<int>(v / n);
+    const int src = a.src[k], dst = a.dst[k];
+    if (static_cast<unsigned>(src) >= static_cast<unsigned>(a.num_pages) ||
+        static_cast<unsigned>(dst) >= static_cast<unsigned>(a.num_pages)) {
+      if (threadIdx.x == 0) set_status(a.status, MLA_DEV_BAD_PAGE);
+      continue;
+    }
+    char* base = a.cache + static_cast<size_t>(layer) * a.layer_stride;
+    const V* from = reinterpret_cast<const V*>(base + static_cast<size_t>(src) * a.page_bytes);
+    V* to = reinterpret_cast<V*>(base + static_cast<size_t>(dst) * a.page_bytes);
+    const unsigned i0 = piece * per_piece + threadIdx.x;
+    V x[kCopyUnroll];
+#pragma unroll
+    for (int e = 0; e < kCopyUnroll; ++e)
+      if (i0 + e * kCopyThreads < vecs) x[e] = __ldcs(from + i0 + e * kCopyThreads);
+#pragma unroll
+    for (int e = 0; e < kCopyUnroll; ++e)
+      if (i0 + e * kCopyThreads < vecs) __stcs(to + i0 + e * kCopyThreads, x[e]);
+  }
+}
+
+// Accepted rows of a sequence (blockIdx.x) in a layer (blockIdx.y).  The list
+// ascends strictly, so keep[k] >= k: a round reads rows of the list before any
+// of it is stored, and what it stores lies below all that later rounds read.
+// A thread holds one vector of kKeepUnroll rows.
+constexpr int kKeepThreads = 288, kKeepUnroll = 4;
+
+template <typename V>
+__global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(KeepRowsArgs a) {
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int b = blockIdx.x, t = threadIdx.x;
+  const int n = a.counts[b];
+  if (n <= 0) return;
+  const int32_t* keep = a.keep + static_cast<size_t>(b) * a.keep_stride;
+  const int32_t* pages = a.table + static_cast<size_t>(b) * a.max_pages;
+  const uint32_t len = a.lengths[b];
+  // The row of position len + i, or -1.
+  auto row_of = [&](int i) {
+    const unsigned long long p = static_cast<unsigned long long>(len) + static_cast<unsigned>(i);
+    const unsigned long long j = p / static_cast<unsigned>(a.page_size);
+    if (j >= static_cast<unsigned long long>(a.max_pages)) return -1ll;
+    const int page = pages[j];
+    if (page < 0 || page >= a.num_pages) return -1ll;
+    return static_cast<long long>(page) * a.page_size + static_cast<long long>(p - j * a.page_size);
+  };
+  // The whole list is looked over first: a sequence is moved whole or not at all.
+  int bad = n > a.keep_stride ? 1 : 0;
+  if (!bad)
+    for (int k = t; k < n; k += kKeepThreads) {
+      const int i = keep[k];
+      if (i < 0 || (k > 0 && keep[k - 1] >= i)) bad |= 1;
+      else if (row_of(i) < 0 || row_of(k) < 0) bad |= 2;
+    }
+  const bool bad_list = __syncthreads_or(bad & 1), bad_page = __syncthreads_or(bad & 2);
+  if (bad_list || bad_page) {
+    if (t == 0) set_status(a.status, bad_list ? MLA_DEV_BAD_OFFSETS : MLA_DEV_BAD_PAGE);
+    return;
+  }
+  char* base = a.cache + static_cast<size_t>(blockIdx.y) * a.layer_stride;
+  const int cols = static_cast<int>(a.row_bytes / sizeof(V));
+  const int wide = min(cols, kKeepThreads);             // threads on a row
+  const int lines = kKeepThreads / wide;                // rows side by side
+  const int line = t / wide, col0 = t - line * wide;
+  for (int c0 = 0; c0 < cols; c0 += wide) {
+    const int c = c0 + col0;
+    const bool on = line < lines && c < cols;
+    for (int k0 = 0; k0 < n; k0 += lines * kKeepUnroll) {
+      V x[kKeepUnroll];
+#pragma unroll
+      for (int e = 0; e < kKeepUnroll; ++e) {
+        const int k = k0 + e * lines + line;
+        if (on && k < n && keep[k] != k)
+          x[e] = reinterpret_cast<const V*>(base + row_of(keep[k]) * a.row_bytes)[c];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kKeepUnroll; ++e) {
+        const int k = k0 + e * lines + line;
+        if (on && k < n && keep[k] != k) reinterpret_cast<V*>(base + row_of(k) * a.row_bytes)[c] = x[e];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t stream) {
+  const int grid = a.dst_batch + a.src_batch;
+  if (grid == 0) return cudaSuccess;
+  return launch_pdl(fork_kernel, dim3(grid), dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t stream) {
+  if (a.batch == 0) return cudaSuccess;
+  return launch_pdl(free_kernel, dim3(a.batch), dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream) {
+  return launch_pdl(reserve_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+}
+
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  const long long entries = static_cast<long long>(a.batch) * a.max_pages;
+  if (entries == 0) return cudaSuccess;
+  const int grid = static_cast<int>(std::min<long long>((entries + 255) / 256, 4ll * sm_count()));
+  return launch_pdl(remap_kernel, dim3(grid), dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_pages_copy(const PagesCopyArgs& a, cudaStream_t stream) {
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.cache) | a.page_bytes | a.layer_stride) & 15u) == 0;
+  const long long vecs = a.page_bytes / (wide ? 16 : 4);
+  const long long pieces = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
+  const long long units = std::min<long long>(static_cast<long long>(a.max_copies) * a.layers, 1ll << 40) * pieces;
+  if (units == 0) return cudaSuccess;
+  const int grid = static_cast<int>(std::min<long long>(units, 8ll * sm_count()));
+  return wide ? launch_pdl(pages_copy_kernel<uint4>, dim3(grid), dim3(kCopyThreads), 0, stream, a)
+              : launch_pdl(pages_copy_kernel<unsigned>, dim3(grid), dim3(kCopyThreads), 0, stream, a);
+}
+
+cudaError_t launch_keep_rows(const KeepRowsArgs& a, cudaStream_t stream) {
+  if (a.batch == 0 || a.layers == 0) return cudaSuccess;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.cache) | a.row_bytes | a.layer_stride) & 15u) == 0;
+  const dim3 grid(a.batch, a.layers);
+  return wide ? launch_pdl(keep_rows_kernel<uint4>, grid, dim3(kKeepThreads), 0, stream, a)
+              : launch_pdl(keep_rows_kernel<unsigned>, grid, dim3(kKeepThreads), 0, stream, a);
+}
+
+}  // namespace mla
