@@ -944,6 +944,61 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
                                  int32_t page_size, int32_t max_pages_per_seq, int32_t batch_size,
                                  int32_t* d_status, mla_stream_t stream);
 
+/*
+ * Attention of a chunk of new tokens of every sequence over the paged cache, in
+ * the absorbed form of mla_decode ("mla_prefill_decode_graph_bf16", Args: q,
+ * w_uk, w_uv, scale, attn_sink_ptr; Parameters: mask_str): a draft tree that is
+ * verified, drafts in a row, or the next tokens of a prompt.  The cache holds the
+ * new tokens' rows (mla_latent_cache_write_at).  New token i of sequence b (row t
+ * = input_row_offsets[b] + i) sees all positions j < cache_lengths[b], and the
+ * new token m of its sequence (position cache_lengths[b] + m)
+ *   - with chunk_mask, iff bit m % 32 of chunk_mask[t][m / 32] is set (for a
+ *     tree: its ancestors and itself; bits past the sequence's tokens mean
+ *     nothing);
+ *   - without, iff m <= i.
+ * out and lse are as in mla_decode over those keys: lse natural, attn_sink[b]
+ * one more logit without a value.  A token that sees nothing gets out = 0 and
+ * lse = -infinity (the sink's logit with one).
+ * Longer chunks than about 170 tokens are as right, but mla_prefill then has
+ * less to compute.
+ * Rounding: the projected query and the softmax weights are bf16, the latent
+ * result two bf16 terms; scores, sums and partial results are fp32.  Results do
+ * not change from call to call.
+ *
+ * out:      [total_q_tokens][num_heads][128] bf16, output
+ * lse:      [total_q_tokens][num_heads] fp32 output (of the rounded query), or NULL
+ * q:        [total_q_tokens][num_heads][192] bf16
+ * kv_cache: [num_pages][page_size][576] bf16
+ * w_uk [num_heads][512][128], w_uv [num_heads][128][512] bf16
+ * input_row_offsets [B+1], cache_lengths [B], page_table [B][max_pages_per_seq]
+ * chunk_mask: [total_q_tokens][mask_words] uint32, or NULL with mask_words 0
+ * attn_sink: [B] fp32 or NULL
+ * workspace: device memory of mla_chunk_attention_workspace_bytes(...), 256-byte
+ *            aligned; for one call at a time
+ * Errors: host MLA_ERR_GEOMETRY (num_heads < 1), MLA_ERR_ARG (null or misaligned
+ * pointers, bad sizes, more than 16383 heads, total_q_tokens * num_heads of 2^29
+ * or more), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
+ * (input_row_offsets[b+1] > total_q_tokens, more new tokens than 32 * mask_words
+ * or a context of more than 2^31 - 8192: sequence b is left out; offsets that
+ * decrease or do not begin at 0: all are), MLA_DEV_BAD_PAGE (a missing page or an
+ * id out of range: the result of its sequence is not meaningful),
+ * MLA_DEV_TIMEOUT.  Rows of out and lse of tokens outside every sequence, or of
+ * one that is left out, are not written.
+ */
+mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                                 const uint32_t* cache_lengths, const void* kv_cache, const int32_t* page_table,
+                                 int32_t num_pages, int32_t page_size, int32_t max_pages_per_seq, const void* w_uk,
+                                 const void* w_uv, int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                                 float scale, const uint32_t* chunk_mask, int32_t mask_words,
+                                 const float* attn_sink, void* workspace, size_t workspace_bytes,
+                                 int32_t* d_status, mla_stream_t stream);
+
+/*
+ * Workspace of mla_chunk_attention; 0 for invalid sizes.  Host only.  The pages
+ * size no buffer: no counterpart.
+ */
+size_t mla_chunk_attention_workspace_bytes(int32_t batch_size, int32_t num_heads, int32_t total_q_tokens);
+
 #ifdef __cplusplus
 }
 #endif

@@ -89,6 +89,9 @@ SIGNATURES = {
     "mla_pages_compact": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _Z, _P, _P]),
     "mla_pages_copy": (_I, [_P, _Z, _I, _Z, _P, _P, _P, _I, _I, _P, _P]),
     "mla_cache_keep_rows": (_I, [_P, _Z, _I, _Z, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "mla_chunk_attention": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _F, _P,
+                                 _I, _P, _P, _Z, _P, _P]),
+    "mla_chunk_attention_workspace_bytes": (_Z, [_I, _I, _I]),
 }
 
 _lib = None
@@ -460,6 +463,21 @@ def mla_cache_keep_rows(cache, row_bytes, num_layers, layer_stride, cache_length
         _ptr(cache), row_bytes, num_layers, layer_stride, _ptr(cache_lengths), _ptr(keep),
         keep_stride, _ptr(keep_counts), _ptr(page_table), num_pages, page_size, max_pages_per_seq,
         batch_size, _ptr(d_status), _stream(stream))
+
+
+def mla_chunk_attention_workspace_bytes(batch_size, num_heads, total_q_tokens) -> int:
+    return load().mla_chunk_attention_workspace_bytes(batch_size, num_heads, total_q_tokens)
+
+
+def mla_chunk_attention(out, lse, q, input_row_offsets, cache_lengths, kv_cache, page_table, num_pages,
+                        page_size, max_pages_per_seq, w_uk, w_uv, batch_size, num_heads,
+                        total_q_tokens, scale, chunk_mask=None, mask_words=0, attn_sink=None,
+                        workspace=None, workspace_bytes=0, d_status=None, stream=None) -> int:
+    return load().mla_chunk_attention(
+        _ptr(out), _ptr(lse), _ptr(q), _ptr(input_row_offsets), _ptr(cache_lengths), _ptr(kv_cache),
+        _ptr(page_table), num_pages, page_size, max_pages_per_seq, _ptr(w_uk), _ptr(w_uv), batch_size,
+        num_heads, total_q_tokens, scale, _ptr(chunk_mask), mask_words, _ptr(attn_sink),
+        _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
 
 
 __all__ = [n for n in SIGNATURES] + ["load", "check", "status_string", "MLAError", "LIB_PATH"]

@@ -1000,4 +1000,55 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
   return from_cuda(mla::launch_keep_rows(a, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ chunk attention
+size_t mla_chunk_attention_workspace_bytes(int32_t batch_size, int32_t num_heads, int32_t total_q_tokens) {
+  if (batch_size < 1 || num_heads < 1 || total_q_tokens < 0) return 0;
+  return mla::chunk_attn_workspace(batch_size, num_heads, total_q_tokens);
+}
+
+mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
+                                 const uint32_t* cache_lengths, const void* kv_cache, const int32_t* page_table,
+                                 int32_t num_pages, int32_t page_size, int32_t max_pages_per_seq, const void* w_uk,
+                                 const void* w_uv, int32_t batch_size, int32_t num_heads, int32_t total_q_tokens,
+                                 float scale, const uint32_t* chunk_mask, int32_t mask_words,
+                                 const float* attn_sink, void* workspace, size_t workspace_bytes,
+                                 int32_t* d_status, mla_stream_t stream) {
+  if (num_heads < 1) return MLA_ERR_GEOMETRY;
+  // (Four CTAs a head are launched for the queries: a launch has 65535 rows of them.)
+  if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !page_table || !w_uk || !w_uv ||
+      !aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
+      batch_size < 1 || total_q_tokens < 0 || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+      num_heads > 65535 / 4 || !(scale > 0.0f) || (chunk_mask ? mask_words < 1 : mask_words != 0) ||
+      static_cast<long long>(total_q_tokens) * num_heads >= (1ll << 31) / 4 ||
+      static_cast<long long>(num_pages) * page_size >= (1ll << 31) - 64)
+    return MLA_ERR_ARG;
+  if (total_q_tokens == 0) return MLA_OK;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < mla::chunk_attn_workspace(batch_size, num_heads, total_q_tokens))
+    return MLA_ERR_WORKSPACE;
+  mla::ChunkAttnArgs a;
+  a.out = out;
+  a.lse = lse;
+  a.q = q;
+  a.kv_cache = kv_cache;
+  a.page_table = page_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.w_uk = w_uk;
+  a.w_uv = w_uv;
+  a.iro = input_row_offsets;
+  a.cache_len = cache_lengths;
+  a.mask = chunk_mask;
+  a.mask_words = mask_words;
+  a.sink = attn_sink;
+  a.B = batch_size;
+  a.H = num_heads;
+  a.T = total_q_tokens;
+  a.scale = scale;
+  a.workspace = workspace;
+  a.status = d_status;
+  return from_cuda(mla::launch_chunk_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,859 @@
+// Absorbed MLA attention of a chunk of new tokens of every sequence over the
+// paged cache: a draft tree that is verified, or the next tokens of a prompt
+// ("mla_prefill_decode_graph_bf16", Args w_uk, w_uv; the mask of its Parameters
+// replaced by one among the new tokens).
+//
+//   q_lat = w_uk[h] q_nope;  s_j = scale (q_lat . c_j + q_rope . r_j)
+//   out = w_uv[h] sum_j softmax(s)_j c_j
+//
+// over the cached positions, all of them visible, and the new tokens of the
+// sequence that the mask row names.  For chunks of up to about 170 tokens this
+// is less work than up-projecting the context: 2176 operations for each (row,
+// key) against 262144 for each (head, key) and 640 for each pair.
+//
+// Launches: the query projection; a plan (one CTA); the attention; a merge; the
+// output projection.
+//
+// The attention runs on pairs of SMs.  A pair holds 128 query rows (token,
+// head) of one sequence, 64 in each CTA, and walks 256-key tiles: S = Q K^T and
+// O += P V are two-SM MMAs with M = 128 and N = 256, whose accumulators lie two
+// columns of a row over each other: lanes 0..63 hold the rows' first N / 2
+// columns, lanes 64..127 the rest.  So the fp32 O of 64 rows x 512 columns takes
+// 256 TMEM columns, two score tiles the other 256, and two threads share a row:
+// a thread's softmax has 128 of the 256 keys, against 4352 clk of MMAs a tile.
+// Scores run a tile ahead, so the softmax is hidden entirely.
+//
+// What bounds it: both operands of both products come from shared memory, and K
+// and V are the same bytes needed in different halves (CTA r takes keys 128r..
+// of a tile for S, latent columns 128r.. of each 256 for O), so each CTA reads
+// 147 KB and 131 KB a tile.
+//
+// The batch's (row tile, key tile) units lie on one line, cut into equal pieces,
+// one for each pair.  A row tile that a cut splits leaves (O, max, sum) in
+// fp32, which the merge joins; all others are finished by their pair.
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace mla {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kRescale = 8.0f;             // a row's reference moves when its maximum grows by 2^8
+
+constexpr int kTile = 256;                   // keys of a tile
+constexpr int kRows = 128;                   // query rows of a pair
+constexpr int kStage = 16 * 1024;
+constexpr int kStages = 7;
+constexpr int kQBytes = 9 * 64 * 128;        // 64 rows x 576 columns in blocks of 64
+constexpr int kPBytes = 4 * 64 * 128;        // 64 rows x 256 keys in blocks of 64
+constexpr int kSmemQ = 0;
+constexpr int kSmemP = kSmemQ + kQBytes;
+constexpr int kSmemRing = kSmemP + kPBytes;
+constexpr int kSmemBoxes = kSmemRing + kStages * kStage;      // two tiles' boxes: 4 groups of 64 rows each
+constexpr int kSmemRed = kSmemBoxes + 2 * 4 * 64 * 8;         // row maxima and sums of both halves
+constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
+constexpr int kSmemTotal = kSmemBar + 256 + 1024;
+static_assert(kSmemTotal <= 227 * 1024, "shared memory");
+constexpr int kThreads = 192;                // producer, MMA, 4 softmax warps
+constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
+constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
+constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
+constexpr int kMaxPieces = 76;               // SM pairs
+
+// Boxes of 1, 2, .. 64 rows x 64 columns of the cache: a run of rows that ends
+// anywhere is a few of them.
+struct CacheMaps {
+  CUtensorMap box[7];
+};
+
+struct ChunkSmem {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full, q_free;
+  uint64_t s_full[2], p_full, pv_done, drain;
+  uint64_t swapped[2];       // the two warps that share rows have both written their words
+  uint32_t tmem;
+  int abort;
+  int boxes[2][4];           // boxes of a group of 64 rows
+};
+static_assert(sizeof(ChunkSmem) <= 256, "barrier block");
+
+// A split row tile, noted by the piece in which it ends.
+struct SplitTile {
+  int row0, rows, first_piece, first_slot, seq;
+};
+
+struct ChunkParams {
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const int32_t* page_table;
+  const uint32_t* mask;
+  const float* sink;
+  const int32_t* base;       // [B + 1] units before sequence b
+  __nv_bfloat16* o_lat;      // [R][2][512]
+  float* lse;                // [R] or null
+  float* o_part;             // [2 pieces][128][512]
+  float2* ml_part;           // [2 pieces][128] (max, sum)
+  SplitTile* split;          // [pieces]
+  int num_pages, page_size, max_pages, cache_rows;
+  int B, H, words;
+  float scale_log2;
+  int32_t* status;
+};
+
+// ------------------------------------------------------------------ plan
+// Units of every sequence and their prefix sums, and each token's sequence.
+// A sequence is left out (no units, no tokens) if its rows are not there.
+struct PlanArgs {
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  int32_t* base;
+  int32_t* token_seq;
+  int B, H, T, words, max_pages, page_size;
+  bool masked;
+  SplitTile* split;
+  int pieces;
+  int32_t* status;
+};
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PlanArgs a) {
+  __shared__ long long warp_sum[32];
+  __shared__ int bad;
+  pdl_enter();
+  if (timed_out_before(a.status)) return;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) bad = a.iro[0] != 0;
+  __syncthreads();
+  for (int b = t; b < a.B; b += kPlanThreads)
+    if (a.iro[b + 1] < a.iro[b]) bad = 1;
+  for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
+  if (t < a.pieces) a.split[t].rows = 0;
+  __syncthreads();
+  const bool all_bad = bad;
+  if (all_bad && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + t;
+    long long units = 0;
+    if (b < a.B && !all_bad) {
+      const uint32_t q0 = a.iro[b], q1 = a.iro[b + 1];
+      const long long n = q1 - q0, L = static_cast<long long>(a.cache_len[b]) + n;
+      if (q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
+        set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      } else if (n > 0) {
+        units = (n * a.H + kRows - 1) / kRows * ((L + kTile - 1) / kTile);
+      }
+    }
+    long long s = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += o;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    long long off = before, total = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) off += warp_sum[w];
+      total += warp_sum[w];
+    }
+    if (b < a.B) {
+      // What lies past 2^31 units is left out: no piece reaches it.
+      const long long at = off + s - units;
+      const bool fits = off + s < (1ll << 31);
+      if (!fits && units > 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      a.base[b] = static_cast<int>(min(at, (1ll << 31) - 1));
+      if (b == a.B - 1) a.base[a.B] = static_cast<int>(min(off + s, (1ll << 31) - 1));
+    }
+    before += total;
+    __syncthreads();
+  }
+  __syncthreads();
+  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+    if (a.base[b + 1] == a.base[b]) continue;
+    for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
+  }
+}
+
+// ------------------------------------------------------------------ the line
+struct Segment {
+  int b, row0, r0, rows;      // sequence, first global row, first row within the sequence, valid rows
+  int k0, k1, kt;             // key tiles [k0, k1) of the row tile's kt
+  int tiles;                  // of them, those that a row sees any key of
+  int cached, n, L;
+};
+struct Walk {
+  int x, x1, b;
+};
+
+// The units of piece i are [piece_start(i), piece_start(i + 1)), at least one.
+__device__ __forceinline__ int piece_start(int total, int pieces, int i) {
+  return static_cast<int>(static_cast<long long>(total) * i / pieces);
+}
+
+__device__ __forceinline__ Walk walk_start(const ChunkParams& p, int piece, int total, int pieces) {
+  Walk w;
+  w.x = w.x1 = w.b = 0;
+  if (piece >= pieces) return w;
+  w.x = piece_start(total, pieces, piece);
+  w.x1 = piece_start(total, pieces, piece + 1);
+  int lo = 0, hi = p.B;       // the last sequence with base <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.base[mid] <= w.x) lo = mid;
+    else hi = mid;
+  }
+  w.b = lo;
+  return w;
+}
+
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment& s) {
+  if (w.x >= w.x1) return false;
+  while (p.base[w.b + 1] <= w.x) ++w.b;
+  s.b = w.b;
+  const int q0 = static_cast<int>(p.iro[w.b]);
+  s.n = static_cast<int>(p.iro[w.b + 1]) - q0;
+  s.cached = static_cast<int>(p.cache_len[w.b]);
+  s.L = s.cached + s.n;
+  s.kt = (s.L + kTile - 1) / kTile;
+  const int off = w.x - p.base[w.b];
+  const int m = off / s.kt;
+  s.k0 = off - m * s.kt;
+  s.k1 = static_cast<int>(min(static_cast<long long>(s.kt), static_cast<long long>(s.k0) + (w.x1 - w.x)));
+  w.x += s.k1 - s.k0;
+  const long long rows = static_cast<long long>(s.n) * p.H;
+  s.r0 = m * kRows;
+  s.rows = static_cast<int>(min(static_cast<long long>(kRows), rows - s.r0));
+  s.row0 = static_cast<int>(static_cast<long long>(q0) * p.H + s.r0);
+  int last = s.L;             // causal: the tile's last token sees cached + i + 1 keys
+  if (p.mask == nullptr) last = s.cached + (s.r0 + s.rows - 1) / p.H + 1;
+  s.tiles = max(0, min(s.k1, (last + kTile - 1) / kTile) - s.k0);
+  return true;
+}
+
+// ------------------------------------------------------------------ attention
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CacheMaps maps,
+                      const __grid_constant__ ChunkParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  ChunkSmem* sh = reinterpret_cast<ChunkSmem*>(smem + kSmemBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  int32_t* const status = p.status;
+  pdl_enter();
+  const int total = p.base[p.B];                 // units of the line
+  const int piece = blockIdx.x >> 1, pieces = min(static_cast<int>(gridDim.x >> 1), total);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), rank == 0 ? 2 : 1);   // CTA 0: its own bytes and CTA 1's word
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh->q_full), rank == 0 ? 2 : 1);
+    mbar_init(smem_u32(&sh->q_free), 1);
+    mbar_init(smem_u32(&sh->s_full[0]), 1);
+    mbar_init(smem_u32(&sh->s_full[1]), 1);
+    mbar_init(smem_u32(&sh->p_full), 8);
+    mbar_init(smem_u32(&sh->pv_done), 1);
+    mbar_init(smem_u32(&sh->drain), 1);
+    mbar_init(smem_u32(&sh->swapped[0]), 2);
+    mbar_init(smem_u32(&sh->swapped[1]), 2);
+    sh->abort = timed_out_before(status) ? 1 : 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&sh->tmem), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  volatile int* const abort_flag = &sh->abort;
+  const bool stop = cluster_any(abort_flag);     // an earlier kernel timed out: no work
+  const uint32_t ring = smem_u32(smem + kSmemRing);
+  volatile int never = 0;
+
+  if (stop) {
+    // (the barriers below are passed by all)
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    // (cache row, first row << 8 | log2 rows)
+    int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
+    Walk w = walk_start(p, piece, total, pieces);
+    Segment s;
+    uint32_t stage = 0, phase = 0, segments = 0;
+    uint32_t used = 0;
+    bool ok = true;
+    // The boxes of a tile: each run of consecutive cache rows in a group of 64
+    // is cut into powers of two, largest first.  Rows past the context, or
+    // without a page, are boxes behind the cache's end, which read as zeros: no
+    // row that nobody has written can reach a product.
+    auto look_up = [&](const Segment& sg, int tile, int slot) {
+      int row[kTile / 32];
+#pragma unroll
+      for (int e = 0; e < kTile / 32; ++e) {
+        const int pos = tile * kTile + e * 32 + lane;
+        row[e] = -1;
+        if (pos < sg.L) {
+          const int j = pos / p.page_size;
+          const int page = j < p.max_pages ? p.page_table[static_cast<size_t>(sg.b) * p.max_pages + j] : -1;
+          if (page >= 0 && page < p.num_pages) row[e] = page * p.page_size + (pos - j * p.page_size);
+          else set_status(status, MLA_DEV_BAD_PAGE);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // Bit i: row i of the group does not continue row i - 1.
+        unsigned long long cuts = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          int before = __shfl_up_sync(0xffffffffu, row[2 * g + u], 1);
+          const int other = __shfl_sync(0xffffffffu, row[2 * g], 31);
+          if (lane == 0) before = other;
+          const bool cut = (u == 0 && lane == 0) ||
+                           (row[2 * g + u] < 0 ? before >= 0 : before < 0 || row[2 * g + u] != before + 1);
+          cuts |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, cut)) << (32 * u);
+        }
+        int count = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int i = 32 * u + lane;
+          const unsigned long long upto = cuts & (~0ull >> (63 - i)), past = i == 63 ? 0 : cuts >> (i + 1);
+          const int at = i - (63 - __clzll(upto));                       // within its run
+          const int left = past ? __ffsll(past) : 64 - i;                // rows of the run from here on
+          const bool starts = at == 0 || left < (at & -at);
+          const unsigned m = __ballot_sync(0xffffffffu, starts);
+          if (starts)
+            boxes[(slot * 4 + g) * 64 + count + __popc(m & ((1u << lane) - 1))] =
+                make_int2(row[2 * g + u] < 0 ? p.cache_rows : row[2 * g + u], i << 8 | (31 - __clz(left)));
+          count += __popc(m);
+        }
+        if (lane == 0) sh->boxes[slot][g] = count;
+      }
+      __syncwarp();
+    };
+    auto load_group = [&](int slot, int g, uint32_t dst, uint32_t bar, int col) {
+      const int n = sh->boxes[slot][g];
+      for (int i = lane; i < n; i += 32) {
+        const int2 b = boxes[(slot * 4 + g) * 64 + i];
+        tma_load_2d(dst + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, col, b.x);
+      }
+    };
+    auto acquire = [&]() {
+      if (used >= kStages && !mbar_wait_warp(smem_u32(&sh->empty[stage]), phase ^ 1, status, abort_flag)) return ok = false;
+      if (lane == 0) mbar_expect_tx(smem_u32(&sh->full[stage]), kStage);
+      __syncwarp();
+      return true;
+    };
+    auto advance = [&]() {
+      __syncwarp();
+      ++used;
+      if (++stage == kStages) stage = 0, phase ^= 1;
+    };
+    auto load_k = [&](int slot) {
+      for (int c = 0; c < 9; ++c) {
+        if (!acquire()) return;
+        const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
+        load_group(slot, 2 * rank, dst, bar, c * 64);
+        load_group(slot, 2 * rank + 1, dst + 8192, bar, c * 64);
+        advance();
+      }
+    };
+    auto load_v = [&](int slot) {
+      for (int i = 0; i < 8; ++i) {
+        if (!acquire()) return;
+        const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
+        const int col = 256 * (i & 1) + 128 * static_cast<int>(rank);
+        load_group(slot, i >> 1, dst, bar, col);
+        load_group(slot, i >> 1, dst + 8192, bar, col + 64);
+        advance();
+      }
+    };
+    while (ok && walk_next(p, w, s)) {
+      if (s.tiles == 0) continue;
+      look_up(s, s.k0, 0);
+      if (segments > 0 && !mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        const uint32_t bar = smem_u32(&sh->q_full);
+        mbar_expect_tx(bar, kQBytes);
+        for (int c = 0; c < 9; ++c)
+          tma_load_2d(smem_u32(smem + kSmemQ) + c * 8192, &q_map, bar, c * 64, s.row0 + 64 * static_cast<int>(rank));
+      }
+      __syncwarp();
+      ++segments;
+      load_k(0);
+      for (int j = 0; j < s.tiles && ok; ++j) {
+        if (j + 1 < s.tiles) {
+          look_up(s, s.k0 + j + 1, (j + 1) & 1);
+          load_k((j + 1) & 1);
+        }
+        if (ok) load_v(j & 1);
+      }
+    }
+    // Nothing may be on its way into this CTA when it leaves: the loads (if the
+    // MMAs did not get to wait for them) and the releases of the stages.
+    if (elect_one()) {
+      const uint32_t n = min(used, static_cast<uint32_t>(kStages));
+      for (uint32_t i = 0; i < n && ok; ++i) {
+        const uint32_t u = used - 1 - i;
+        ok = mbar_wait(smem_u32(&sh->empty[u % kStages]), (u / kStages) & 1, status, abort_flag);
+      }
+      if (segments > 0) ok = ok && mbar_wait(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag);
+      if (!ok) {      // (CTA 0's words of CTA 1 may be missing: a short limit)
+        for (uint32_t i = 0; i < n; ++i) {
+          const uint32_t u = used - 1 - i;
+          mbar_wait(smem_u32(&sh->full[u % kStages]), (u / kStages) & 1, status, &never, 10000000ull);
+        }
+        if (segments > 0) mbar_wait(smem_u32(&sh->q_full), (segments - 1) & 1, status, &never, 10000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (elect_one()) {
+      Walk w = walk_start(p, piece, total, pieces);
+      Segment s;
+      uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
+      bool ok = true;
+      if (rank == 0) {
+        const uint32_t sq = smem_u32(smem + kSmemQ), sp = smem_u32(smem + kSmemP);
+        auto take = [&]() {
+          ok = ok && mbar_wait(smem_u32(&sh->full[stage]), phase, status, abort_flag);
+          tc_fence_after();
+          return ok;
+        };
+        auto give = [&]() {
+          tc_commit_pair(smem_u32(&sh->empty[stage]), 3);
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        };
+        auto scores = [&](uint32_t buf) {
+          for (int c = 0; c < 9; ++c) {
+            if (!take()) return;
+            const uint32_t k = ring + stage * kStage;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma_f16_ss_pair(tmem + buf * 128, sdesc(sq + c * 8192 + e * 32, 16, 1024), sdesc(k + e * 32, 16, 1024),
+                              kIdescS, (c | e) != 0);
+            give();
+          }
+          tc_commit_pair(smem_u32(&sh->s_full[buf]), 3);
+        };
+        while (ok && walk_next(p, w, s)) {
+          if (s.tiles == 0) continue;
+          if (!(ok = mbar_wait(smem_u32(&sh->q_full), segments & 1, status, abort_flag))) break;
+          ++segments;
+          tc_fence_after();
+          scores(tile & 1);
+          if (s.tiles == 1 && ok) tc_commit_pair(smem_u32(&sh->q_free), 3);
+          for (int j = 0; j < s.tiles && ok; ++j) {
+            if (j + 1 < s.tiles) {
+              scores((tile + 1) & 1);
+              if (j + 2 == s.tiles && ok) tc_commit_pair(smem_u32(&sh->q_free), 3);
+            }
+            if (!ok || !(ok = mbar_wait(smem_u32(&sh->p_full), p_phase, status, abort_flag))) break;
+            p_phase ^= 1;
+            tc_fence_after();
+            for (int g = 0; g < 4; ++g) {
+              for (int m = 0; m < 2; ++m) {
+                if (!take()) break;
+                const uint32_t v = ring + stage * kStage;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  mma_f16_ss_pair(tmem + kTmO + m * 128, sdesc(sp + g * 8192 + e * 32, 16, 1024),
+                                  sdesc(v + e * 2048, 8192, 1024), kIdescO, (j | g | e) != 0);
+                give();
+              }
+            }
+            if (ok) tc_commit_pair(smem_u32(&sh->pv_done), 3);
+            ++tile;
+          }
+        }
+        // The last arrival of this CTA's commits in either CTA.
+        tc_commit_pair(smem_u32(&sh->drain), 3);
+      } else {
+        // CTA 1's loads have landed: a word to CTA 0, in the order of use.
+        uint32_t bars[kStages];
+        for (int i = 0; i < kStages; ++i) bars[i] = cluster_addr(smem_u32(&sh->full[i]), 0);
+        const uint32_t q_bar = cluster_addr(smem_u32(&sh->q_full), 0);
+        while (ok && walk_next(p, w, s)) {
+          if (s.tiles == 0) continue;
+          if (!(ok = mbar_wait(smem_u32(&sh->q_full), segments & 1, status, abort_flag))) break;
+          mbar_arrive_cluster(q_bar);
+          ++segments;
+          for (int i = 0; i < 17 * s.tiles && ok; ++i) {
+            if (!(ok = mbar_wait(smem_u32(&sh->full[stage]), phase, status, abort_flag))) break;
+            mbar_arrive_cluster(cluster_addr(smem_u32(&sh->full[stage]), 0));
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+        }
+      }
+      mbar_wait(smem_u32(&sh->drain), 0, status, &never);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int quarter = warp & 3;
+    const int tl = quarter * 32 + lane;          // TMEM lane
+    const int row = tl & 63, half = tl >> 6;     // row of this CTA; which columns of it
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][128]
+    const uint32_t sp = smem_u32(smem + kSmemP);
+    const uint32_t p_bar = cluster_addr(smem_u32(&sh->p_full), 0);
+    Walk w = walk_start(p, piece, total, pieces);
+    Segment s;
+    uint32_t tile = 0, swaps = 0;
+    bool ok = true;
+    // The word of the thread with the other columns of the row (two sets of
+    // words: a set is written again only after the other has been swapped).
+    auto swap = [&](float v, float& other) {
+      float* const words = red + (swaps & 1) * 128;
+      words[tl] = v;
+      __syncwarp();
+      const uint32_t bar = smem_u32(&sh->swapped[quarter & 1]);
+      if (lane == 0) mbar_arrive(bar);
+      if (!mbar_wait_warp(bar, swaps & 1, status, abort_flag)) return false;
+      ++swaps;
+      other = words[tl ^ 64];
+      return true;
+    };
+    while (ok && walk_next(p, w, s)) {
+      const int local = static_cast<int>(rank) * 64 + row;            // row of the pair's tile
+      const bool live = local < s.rows;
+      const int token = live ? (s.r0 + local) / p.H : 0;              // within the sequence
+      const uint32_t* mask_row =
+          p.mask != nullptr ? p.mask + static_cast<size_t>(p.iro[s.b] + token) * p.words : nullptr;
+      float ref = kNegInf, sum = 0.0f;
+      for (int j = 0; j < s.tiles; ++j, ++tile) {
+        const uint32_t buf = tile & 1;
+        if (!(ok = mbar_wait_warp(smem_u32(&sh->s_full[buf]), (tile >> 1) & 1, status, abort_flag))) break;
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld32(tmem + lane_off + buf * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+        tmem_ld_wait();
+        // Keys that the row does not see.
+        const int k0 = (s.k0 + j) * kTile + half * 128;
+        if (k0 + 128 > s.cached) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = k0 + c * 32 - s.cached;                     // new token of the first key
+            uint32_t see = 0xffffffffu;
+            if (i + 32 > 0) {
+              if (mask_row != nullptr) {
+                const int wi = i >> 5, sh_ = i & 31;                  // floor for i < 0, too
+                const uint32_t lo = wi >= 0 && wi < p.words ? mask_row[wi] : 0u;
+                const uint32_t hi = wi + 1 >= 0 && wi + 1 < p.words ? mask_row[wi + 1] : 0u;
+                see = sh_ ? (lo >> sh_) | (hi << (32 - sh_)) : lo;
+                if (i < 0) see |= (1u << -i) - 1u;                    // cached keys (i > -32)
+              } else {
+                const int n = token + 1 - i;                          // keys from the first on
+                see = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+              }
+              const int n = s.n - i;                                  // keys that there are
+              see &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1)) x[c * 32 + e] = __float_as_uint(kNegInf);
+          }
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        float other;
+        if (!(ok = swap(top, other))) break;
+        top = fmaxf(top, other) * p.scale_log2;
+        float factor = 1.0f;
+        if (top > ref + kRescale || (ref == kNegInf && top > kNegInf)) {
+          factor = ref == kNegInf ? 0.0f : ex2(ref - top);
+          ref = top;
+          sum *= factor;
+        }
+        // P of the tile before is read, O holds its product.
+        if (tile > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->pv_done), (tile - 1) & 1, status, abort_flag))) break;
+        tc_fence_after();
+        if (j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = factor == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * factor);
+            tmem_st32(tmem + lane_off + kTmO + c * 32, o);
+          }
+          tmem_st_wait();
+        }
+        const float shift = ref == kNegInf ? 0.0f : ref;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = ex2(fmaf(__uint_as_float(x[c * 8 + 2 * e]), p.scale_log2, -shift));
+            const float b = ex2(fmaf(__uint_as_float(x[c * 8 + 2 * e + 1]), p.scale_log2, -shift));
+            sum += a + b;
+            pk[e] = pack_bf16(a, b);
+          }
+          const uint32_t dst = sp + (half * 2 + (c >> 3)) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]),
+                       "r"(pk[3])
+                       : "memory");
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_bar);
+      }
+      if (!ok) break;
+      if (s.tiles > 0) {
+        if (!(ok = mbar_wait_warp(smem_u32(&sh->pv_done), (tile - 1) & 1, status, abort_flag))) break;
+        tc_fence_after();
+      }
+      float other;
+      if (!(ok = swap(sum, other))) break;
+      sum += other;
+      const bool none = sum == 0.0f;                 // the row saw nothing
+      const bool starts = s.k0 == 0, ends = s.k1 == s.kt;
+      if (starts && ends) {
+        if (p.sink != nullptr) {
+          const float sk = p.sink[s.b] * kLog2e;
+          const float m = fmaxf(ref, sk), f = ref == kNegInf ? 0.0f : ex2(ref - m);
+          const float add = sk == kNegInf ? 0.0f : ex2(sk - m);
+          if (p.lse != nullptr && live && half == 0)
+            p.lse[s.row0 + local] = m == kNegInf ? kNegInf : (m + log2f(fmaf(sum, f, add))) * kLn2;
+          sum = fmaf(sum, f, add);
+          sum = f == 0.0f ? __builtin_huge_valf() : sum / f;
+        } else if (p.lse != nullptr && live && half == 0) {
+          p.lse[s.row0 + local] = sum == 0.0f ? kNegInf : (ref + log2f(sum)) * kLn2;
+        }
+        const float inv = 1.0f / sum;
+        __nv_bfloat16* dst = p.o_lat + static_cast<size_t>(s.row0 + local) * 1024 + half * 128;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
+          tmem_ld_wait();
+          if (live) {
+            uint4* const hi4 = reinterpret_cast<uint4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
+            uint4* const lo4 = reinterpret_cast<uint4*>(dst + 512 + (c >> 2) * 256 + (c & 3) * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t h[4], l[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i]) * inv;
+                const float b = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i + 1]) * inv;
+                h[i] = pack_bf16(a, b);
+                l[i] = pack_bf16(a - bf16_lo(h[i]), b - bf16_hi(h[i]));
+              }
+              hi4[e] = make_uint4(h[0], h[1], h[2], h[3]);
+              lo4[e] = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+          }
+        }
+      } else {
+        // Slots of a piece: its first segment, its last one.
+        const bool leads = w.x - (s.k1 - s.k0) == piece_start(total, pieces, piece);
+        const int slot = 2 * piece + (leads ? 0 : 1);
+        if (half == 0) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
+        if (s.tiles > 0) {
+          float* dst = p.o_part + (static_cast<size_t>(slot) * kRows + local) * 512 + half * 128;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
+            tmem_ld_wait();
+            float4* d4 = reinterpret_cast<float4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              d4[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                  __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
+        }
+        if (ends && tl == 0 && rank == 0) {
+          // The unit at which the row tile begins, the piece that holds it, and
+          // whether it is that piece's first.
+          const int x0 = w.x - s.kt;
+          int fp = static_cast<int>(static_cast<long long>(x0) * pieces / total);
+          while (piece_start(total, pieces, fp) > x0) --fp;
+          while (piece_start(total, pieces, fp + 1) <= x0) ++fp;
+          SplitTile t;
+          t.row0 = s.row0;
+          t.rows = s.rows;
+          t.first_piece = fp;
+          t.first_slot = 2 * fp + (piece_start(total, pieces, fp) == x0 ? 0 : 1);
+          t.seq = s.b;
+          p.split[piece] = t;
+        }
+      }
+      tc_fence_before();
+      // (The next segment's first product is ordered behind these reads by the
+      // arrival on p_full.)
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ merge
+// Split row tiles: blockIdx.x is the piece in which one ends, blockIdx.y a
+// slice of its rows; a warp takes a row at a time.
+constexpr int kMergeSlices = 8, kMergeWarps = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pieces) {
+  pdl_enter();
+  if (timed_out_before(p.status)) return;
+  const int piece = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SplitTile t = p.split[piece];
+  if (t.rows <= 0) return;
+  const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
+  for (int r = blockIdx.y * kMergeWarps + warp; r < t.rows; r += kMergeSlices * kMergeWarps) {
+    float top = sink;
+    for (int q = t.first_piece; q <= piece; ++q) {
+      const int slot = q == t.first_piece ? t.first_slot : 2 * q;
+      top = fmaxf(top, p.ml_part[slot * kRows + r].x);
+    }
+    float sum = sink == kNegInf ? 0.0f : ex2(sink - top);
+    float4 o[4] = {};
+    for (int q = t.first_piece; q <= piece; ++q) {
+      const int slot = q == t.first_piece ? t.first_slot : 2 * q;
+      const float2 ml = p.ml_part[slot * kRows + r];
+      if (ml.y == 0.0f) continue;      // (the segment saw nothing; it may have stored no rows)
+      const float f = ex2(ml.x - top);
+      sum = fmaf(ml.y, f, sum);
+      const float4* src = reinterpret_cast<const float4*>(p.o_part + (static_cast<size_t>(slot) * kRows + r) * 512);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldcs(src + i * 32 + lane);
+        o[i].x = fmaf(v.x, f, o[i].x);
+        o[i].y = fmaf(v.y, f, o[i].y);
+        o[i].z = fmaf(v.z, f, o[i].z);
+        o[i].w = fmaf(v.w, f, o[i].w);
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint2* hi = reinterpret_cast<uint2*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024);
+    uint2* lo = hi + 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = o[i].x * inv, b = o[i].y * inv, c = o[i].z * inv, d = o[i].w * inv;
+      const uint32_t h0 = pack_bf16(a, b), h1 = pack_bf16(c, d);
+      hi[i * 32 + lane] = make_uint2(h0, h1);
+      lo[i * 32 + lane] = make_uint2(pack_bf16(a - bf16_lo(h0), b - bf16_hi(h0)),
+                                     pack_bf16(c - bf16_lo(h1), d - bf16_hi(h1)));
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
+  }
+}
+
+struct Layout {
+  size_t q_full, o_lat, base, token_seq, o_part, ml_part, split, total;
+};
+Layout layout(int B, int H, int T) {
+  const size_t R = static_cast<size_t>(T) * H;
+  Layout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  L.q_full = take(R * 1152);
+  L.o_lat = take(R * 2048);
+  L.base = take(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+  L.token_seq = take(sizeof(int32_t) * static_cast<size_t>(T));
+  L.o_part = take(static_cast<size_t>(2 * kMaxPieces) * kRows * 512 * sizeof(float));
+  L.ml_part = take(static_cast<size_t>(2 * kMaxPieces) * kRows * sizeof(float2));
+  L.split = take(kMaxPieces * sizeof(SplitTile));
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+size_t chunk_attn_workspace(int B, int H, int T) { return layout(B, H, T).total; }
+
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
+  if (a.T == 0) return cudaSuccess;
+  const size_t R = static_cast<size_t>(a.T) * a.H;
+  const Layout L = layout(a.B, a.H, a.T);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  __nv_bfloat16* q_full = reinterpret_cast<__nv_bfloat16*>(ws + L.q_full);
+  const int pieces = std::max(1, std::min(kMaxPieces, sm_count() / 2));
+
+  ChunkParams p;
+  p.iro = a.iro;
+  p.cache_len = a.cache_len;
+  p.page_table = a.page_table;
+  p.mask = a.mask;
+  p.sink = a.sink;
+  p.base = reinterpret_cast<int32_t*>(ws + L.base);
+  p.o_lat = reinterpret_cast<__nv_bfloat16*>(ws + L.o_lat);
+  p.lse = a.lse;
+  p.o_part = reinterpret_cast<float*>(ws + L.o_part);
+  p.ml_part = reinterpret_cast<float2*>(ws + L.ml_part);
+  p.split = reinterpret_cast<SplitTile*>(ws + L.split);
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.cache_rows = a.num_pages * a.page_size;
+  p.B = a.B;
+  p.H = a.H;
+  p.words = a.mask_words;
+  p.scale_log2 = a.scale * kLog2e;
+  p.status = a.status;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap q_map;
+  CacheMaps maps;
+  if (!encode_2d(&q_map, q_full, bf, 576, R, 1152, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  for (int e = 0; e < 8; ++e)
+    if (!encode_2d(&maps.box[e], a.kv_cache, bf, 576, static_cast<uint64_t>(p.cache_rows), 1152, 64, 1u << e,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+
+  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, a.T, a.H, a.status, stream);
+  if (e != cudaSuccess) return e;
+  PlanArgs pa;
+  pa.iro = a.iro;
+  pa.cache_len = a.cache_len;
+  pa.base = reinterpret_cast<int32_t*>(ws + L.base);
+  pa.token_seq = reinterpret_cast<int32_t*>(ws + L.token_seq);
+  pa.B = a.B;
+  pa.H = a.H;
+  pa.T = a.T;
+  pa.words = a.mask_words;
+  pa.max_pages = a.max_pages;
+  pa.page_size = a.page_size;
+  pa.masked = a.mask != nullptr;
+  pa.split = p.split;
+  pa.pieces = pieces;
+  pa.status = a.status;
+  if ((e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pa)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) !=
+      cudaSuccess)
+    return e;
+  if ((e = launch_pdl(chunk_attn_kernel, dim3(2 * pieces), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
+      cudaSuccess)
+    return e;
+  if ((e = launch_pdl(chunk_merge_kernel, dim3(pieces, kMergeSlices), dim3(kMergeWarps * 32), 0, stream, p, pieces)) !=
+      cudaSuccess)
+    return e;
+  return launch_project_outputs(p.o_lat, true, a.w_uv, a.out, a.T, a.H, pa.token_seq, a.status, stream);
+}
+
+}  // namespace mla

@@ -53,6 +53,8 @@ constexpr float kRescaleLog2 = 8.0f;
 // bf16 result at out + row * out_ld + h * out_hstride.  With rope_src set,
 // the 64 values at rope_src + row * rope_ld + h * rope_hstride are copied
 // after the N results (the query's rope part next to its latent part).
+// With TERMS > 1, A is the sum of TERMS matrices side by side, K columns each,
+// that share B_h.  With row_seq set, row r is written only if row_seq[r] >= 0.
 template <int N, int K, int STAGES>
 struct HeadGemm {
   static constexpr int KB = K / 64;             // 64-column (128-byte) k-blocks
@@ -69,12 +71,12 @@ struct HeadGemm {
 
 // SPLIT > 1: the head's N * SPLIT output columns are shared by SPLIT CTAs
 // (grid.y = H * SPLIT), N each, so that a small M still fills the GPU.
-template <int N, int K, int STAGES, int SPLIT>
+template <int N, int K, int STAGES, int SPLIT, int TERMS>
 __global__ void __launch_bounds__(192, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                      int a_col0, int a_hstride, __nv_bfloat16* __restrict__ out, long long out_ld,
                      int out_hstride, const __nv_bfloat16* __restrict__ rope_src, long long rope_ld,
-                     int rope_hstride, int M, int32_t* status) {
+                     int rope_hstride, int M, const int32_t* __restrict__ row_seq, int32_t* status) {
   using C = HeadGemm<N, K, STAGES>;
   struct Bars {
     uint64_t full[STAGES], empty[STAGES], done;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(192, 1)
       prefetch_tmap(&b_map);
       int last[STAGES];
       for (int s = 0; s < STAGES; ++s) last[s] = -1;
-      for (int kb = 0; kb < C::KB; ++kb) {
+      for (int kb = 0; kb < C::KB * TERMS; ++kb) {
         const int s = kb % STAGES;
         if (kb >= STAGES && !mbar_wait(smem_u32(&sh->empty[s]), ((kb / STAGES) & 1) ^ 1, status, abort_flag))
           break;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(192, 1)
         tma_load_2d(a, &a_map, full, a_col0 + h * a_hstride + kb * 64, m0);
 #pragma unroll
         for (int nb = 0; nb < N; nb += C::NB)
-          tma_load_2d(a + C::A_BYTES + nb * 128, &b_map, full, kb * 64, (h * SPLIT + nc) * N + nb);
+          tma_load_2d(a + C::A_BYTES + nb * 128, &b_map, full, kb % C::KB * 64, (h * SPLIT + nc) * N + nb);
         last[s] = (kb / STAGES) & 1;
       }
       volatile int never = 0;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(192, 1)
   } else if (warp == 1) {
     if (elect_one()) {
       bool ok = true;
-      for (int kb = 0; kb < C::KB && ok; ++kb) {
+      for (int kb = 0; kb < C::KB * TERMS && ok; ++kb) {
         const int s = kb % STAGES;
         if (!(ok = mbar_wait(smem_u32(&sh->full[s]), (kb / STAGES) & 1, status, abort_flag))) break;
         tc_fence_after();
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(192, 1)
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
     if (mbar_wait_warp(smem_u32(&sh->done), 0, status, abort_flag)) {
       tc_fence_after();
-      const bool row_ok = m0 + row < M;
+      const bool row_ok = m0 + row < M && (row_seq == nullptr || row_seq[m0 + row] >= 0);
       __nv_bfloat16* dst =
           out + static_cast<long long>(m0 + row) * out_ld + static_cast<long long>(h) * out_hstride + nc * N;
 #pragma unroll 1
@@ -1051,21 +1053,54 @@ int decode_clusters(int device) {
   return cached[device];
 }
 
-template <int N, int K, int STAGES, int SPLIT = 1>
+template <int N, int K, int STAGES, int SPLIT = 1, int TERMS = 1>
 cudaError_t launch_head_gemm(const CUtensorMap& a_map, const CUtensorMap& b_map, int a_col0, int a_hstride,
                              __nv_bfloat16* out, long long out_ld, int out_hstride, const __nv_bfloat16* rope_src,
-                             long long rope_ld, int rope_hstride, int M, int H, int32_t* status,
-                             cudaStream_t stream) {
+                             long long rope_ld, int rope_hstride, int M, int H, const int32_t* row_seq,
+                             int32_t* status, cudaStream_t stream) {
   using C = HeadGemm<N, K, STAGES>;
-  cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT>,
+  cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
   if (e != cudaSuccess) return e;
   const dim3 grid((M + 127) / 128, H * SPLIT);
-  return launch_pdl(head_gemm_kernel<N, K, STAGES, SPLIT>, grid, dim3(192), C::SMEM_TOTAL, stream, a_map, b_map,
-                    a_col0, a_hstride, out, out_ld, out_hstride, rope_src, rope_ld, rope_hstride, M, status);
+  return launch_pdl(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS>, grid, dim3(192), C::SMEM_TOTAL, stream, a_map,
+                    b_map, a_col0, a_hstride, out, out_ld, out_hstride, rope_src, rope_ld, rope_hstride, M, row_seq,
+                    status);
 }
 
 }  // namespace
+
+cudaError_t launch_project_queries(const void* q, const void* w_uk, __nv_bfloat16* q_full, int T, int H,
+                                   int32_t* status, cudaStream_t stream) {
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap qa_map, wuk_map;
+  if (!encode_2d(&qa_map, q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&wuk_map, w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  // Four CTAs a head, 128 latent columns each: a decode batch has few rows.
+  return launch_head_gemm<128, 128, 2, 4>(qa_map, wuk_map, 0, 192, q_full, static_cast<long long>(H) * 576, 576,
+                                          static_cast<const __nv_bfloat16*>(q) + 128,
+                                          static_cast<long long>(H) * 192, 192, T, H, nullptr, status, stream);
+}
+
+cudaError_t launch_project_outputs(const __nv_bfloat16* o_lat, bool two_terms, const void* w_uv, void* out, int T,
+                                   int H, const int32_t* row_seq, int32_t* status, cudaStream_t stream) {
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t width = static_cast<uint64_t>(H) * (two_terms ? 1024 : 512);
+  CUtensorMap ol_map, wuv_map;
+  if (!encode_2d(&ol_map, o_lat, bf, width, T, 2 * width, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&wuv_map, w_uv, bf, 512, static_cast<uint64_t>(H) * 128, 1024, 64, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  const long long ld = static_cast<long long>(H) * 128;
+  return two_terms ? launch_head_gemm<128, 512, 4, 1, 2>(ol_map, wuv_map, 0, 1024, o, ld, 128, nullptr, 0, 0, T, H,
+                                                         row_seq, status, stream)
+                   : launch_head_gemm<128, 512, 4>(ol_map, wuv_map, 0, 512, o, ld, 128, nullptr, 0, 0, T, H, row_seq,
+                                                   status, stream);
+}
 
 DecodeLayout decode_layout(int T, int H, int parts) {
   const size_t R = static_cast<size_t>(T) * H;
@@ -1114,17 +1149,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
   // 1. q_lat = w_uk[h] q_nope, with the rope part alongside: q_full [T*H, 576].
-  CUtensorMap qa_map, wuk_map;
-  if (!encode_2d(&qa_map, a.q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&wuk_map, a.w_uk, bf, 128, static_cast<uint64_t>(H) * 512, 256, 64, 128,
-                 CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  // Four CTAs a head, 128 latent columns each: a decode batch has few rows.
-  cudaError_t e = launch_head_gemm<128, 128, 2, 4>(qa_map, wuk_map, 0, 192, q_full,
-                                                   static_cast<long long>(H) * 576, 576,
-                                                   static_cast<const __nv_bfloat16*>(a.q) + 128,
-                                                   static_cast<long long>(H) * 192, 192, T, H, a.status, stream);
+  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, T, H, a.status, stream);
   if (e != cudaSuccess) return e;
 
   // 2. Latent attention over the key partitions.
@@ -1182,14 +1207,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     return e;
 
   // 4. out = w_uv[h] o_lat.
-  CUtensorMap ol_map, wuv_map;
-  if (!encode_2d(&ol_map, o_lat, bf, static_cast<uint64_t>(H) * 512, T, static_cast<uint64_t>(H) * 1024, 64, 128,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&wuv_map, a.w_uv, bf, 512, static_cast<uint64_t>(H) * 128, 1024, 64, 128,
-                 CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  return launch_head_gemm<128, 512, 4>(ol_map, wuv_map, 0, 512, static_cast<__nv_bfloat16*>(a.out),
-                                       static_cast<long long>(H) * 128, 128, nullptr, 0, 0, T, H, a.status, stream);
+  return launch_project_outputs(o_lat, false, a.w_uv, a.out, T, H, nullptr, a.status, stream);
 }
 
 }  // namespace mla

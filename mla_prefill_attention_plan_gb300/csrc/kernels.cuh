@@ -179,6 +179,38 @@ struct DecodePartitioning {
 DecodePartitioning decode_partitioning(int B, int H, int max_new, int max_keys);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
+// The decode's per-head projections (decode.cu), for other absorbed attentions:
+// q_full [T*H][576] = (w_uk[h] q_nope, q_rope); out[t][h] = w_uv[h] o_lat[t][h]
+// with o_lat [T*H][512], or (two_terms) the sum of [T*H][2][512].  Rows t with
+// row_seq[t] < 0 are not written (row_seq may be null).
+cudaError_t launch_project_queries(const void* q, const void* w_uk, __nv_bfloat16* q_full, int T, int H,
+                                   int32_t* status, cudaStream_t stream);
+cudaError_t launch_project_outputs(const __nv_bfloat16* o_lat, bool two_terms, const void* w_uv, void* out, int T,
+                                   int H, const int32_t* row_seq, int32_t* status, cudaStream_t stream);
+
+// Absorbed attention of chunks of new tokens over the paged cache (chunk_attn.cu).
+struct ChunkAttnArgs {
+  void* out;                  // [T][H][128] bf16
+  float* lse;                 // [T][H] or null
+  const void* q;              // [T][H][192] bf16
+  const void* kv_cache;       // [num_pages][page_size][576] bf16
+  const int32_t* page_table;  // [B][max_pages]
+  int num_pages, page_size, max_pages;
+  const void* w_uk;           // [H][512][128] bf16
+  const void* w_uv;           // [H][128][512] bf16
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  const uint32_t* mask;       // [T][mask_words] or null (causal)
+  int mask_words;
+  const float* sink;          // [B] or null
+  int B, H, T;
+  float scale;
+  void* workspace;
+  int32_t* status;
+};
+size_t chunk_attn_workspace(int B, int H, int T);
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream);
+
 // The 8-bit latent cache (cache_q8.cu): e4m3 rows, one power-of-two scale for
 // each block of scale_block slots of a page (scale_block divides page_size,
 // so cache row r has scale r / scale_block).

@@ -1,0 +1,464 @@
+"""GPU tests of chunk attention against the float64 oracle.
+
+Tolerance.  A bf16 rounding is off by at most 2^-8 of the value, on average over
+the significand by 0.42 * 2^-8 = 0.00165 (root mean square).  On random rows
+three of them reach an output, independent of each other: its own, the weights',
+and the projected query's, which moves a score of spread sigma by 0.00165 sigma
+(sigma is 1 here).  Together 0.00165 * sqrt(3) = 0.0029 of the output's 2-norm;
+twice that is allowed for a whole result, four times for a row of 128 values.
+The lse is off by no more than the worst score: 2^-8 of scale * sum |q_lat c|
+(the oracle's slack), and fp32's part of it."""
+import numpy as np
+import pytest
+import torch
+
+import mla_prefill_attention_plan_gb300 as mla
+import oracle as O
+from oracle import chunk_oracle as C
+from oracle import pages_oracle as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FILL = 3.5
+WHOLE, ROW = 2 * 0.0029, 4 * 0.0029
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from mla_prefill_attention_plan_gb300 import build
+    build.build()
+    mla.load()
+
+
+def dev(x, kind=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(x).astype(kind))).to(DEV)
+
+
+def bf16(x):
+    """(device tensor, the values it holds)."""
+    t = torch.from_numpy(np.asarray(x, dtype=np.float32)).to(torch.bfloat16)
+    return t.to(DEV), t.double().numpy()
+
+
+def tree(rng, n):
+    seen = []
+    for i in range(n):
+        up = int(rng.integers(-1, i)) if i else -1
+        seen.append(1 << i | (seen[up] if up >= 0 else 0))
+    return seen
+
+
+def words_of(rows, words):
+    return np.array([[r >> 32 * w & 0xffffffff for w in range(words)] for r in rows], dtype=np.uint32).view(np.int32)
+
+
+class Case:
+    """Inputs of ragged sequences on shuffled pages; rows that no sequence sees are NaN."""
+
+    def __init__(self, new, cached, H, page, seed=0, mask="tree", sink=False, extra=0, words=None, spread=1.0):
+        rng = np.random.default_rng(seed)
+        self.new, self.cached, self.H, self.page, self.B = new, cached, H, page, len(new)
+        held = [-(-(n + c) // page) for n, c in zip(new, cached)]
+        self.num, self.most = sum(held) + 1, max(held) + 1
+        order, at = rng.permutation(self.num), 0
+        self.table = np.full((self.B, self.most), -1, np.int32)
+        for b, k in enumerate(held):
+            self.table[b, :k] = order[at: at + k]
+            at += k
+        self.iro = np.concatenate([[0], np.cumsum(new)])
+        self.T = int(self.iro[-1]) + extra
+        rows = np.full((self.num * page, 576), np.nan)
+        for b in range(self.B):
+            j = np.arange(new[b] + cached[b])
+            rows[self.table[b, j // page] * page + j % page] = rng.standard_normal((len(j), 576))
+        self.kv_d, self.kv = bf16(rows)
+        self.q_d, self.q = bf16(rng.standard_normal((self.T, H, 192)) * spread)
+        self.uk_d, self.uk = bf16(rng.standard_normal((H, 512, 128)) * 512 ** -0.5)
+        self.uv_d, self.uv = bf16(rng.standard_normal((H, 128, 512)) * 512 ** -0.5)
+        self.mask = None
+        if mask == "tree":
+            self.mask = sum((tree(rng, n) for n in new), [])
+        elif mask == "any":
+            self.mask = [int(rng.integers(0, 2)) and int.from_bytes(rng.bytes(32), "little") for _ in range(self.T)]
+        elif isinstance(mask, list):
+            self.mask = mask
+        self.words = 0
+        if self.mask is not None:
+            self.words = words or max(1, -(-max(new) // 32))
+            self.mask = (self.mask + [0] * self.T)[:self.T]
+        self.sink = rng.standard_normal(self.B).astype(np.float32) if sink else None
+        self.scale = 192 ** -0.5
+        self.make_buffers()
+
+    def make_buffers(self):
+        self.out = torch.full((self.T, self.H, 128), FILL, dtype=torch.bfloat16, device=DEV)
+        self.lse = torch.full((self.T, self.H), FILL, device=DEV)
+        self.st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.bytes = mla.mla_chunk_attention_workspace_bytes(self.B, self.H, self.T)
+        self.ws = torch.randint(0, 256, (self.bytes,), dtype=torch.uint8, device=DEV)
+        self.ints = [dev(self.iro), dev(self.cached), dev(self.table)]
+        self.mask_d = None if self.mask is None else dev(words_of(self.mask, self.words))
+        self.sink_d = None if self.sink is None else torch.from_numpy(self.sink).to(DEV)
+
+    def call(self, lse=True, stream=None, **kw):
+        iro, cached, table = self.ints
+        a = dict(chunk_mask=self.mask_d, mask_words=self.words, attn_sink=self.sink_d, workspace=self.ws,
+                 workspace_bytes=self.bytes, d_status=self.st, stream=stream)
+        a.update(kw)
+        return mla.mla_chunk_attention(self.out, self.lse if lse else None, self.q_d, iro, cached, self.kv_d, table,
+                                       self.num, self.page, self.most, self.uk_d, self.uv_d, self.B, self.H, self.T,
+                                       self.scale, **a)
+
+    def oracle(self):
+        return C.chunk_attention(self.q, self.kv, self.table, self.page, self.uk, self.uv, self.iro, self.cached,
+                                 self.scale, self.mask, self.sink)
+
+    def check(self, **kw):
+        mla.check(self.call(**kw))
+        torch.cuda.synchronize()
+        assert self.st.item() == 0
+        self.compare(*self.oracle())
+
+    def compare(self, out, lse, slack):
+        got, got_lse = self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
+        outside = np.isnan(lse)
+        assert (got[outside] == FILL).all() and (got_lse[outside] == FILL).all()
+        got, got_lse, out, lse, slack = (x[~outside] for x in (got, got_lse, out, lse, slack))
+        blank = np.isneginf(lse)
+        assert np.isneginf(got_lse[blank]).all() and not got[blank].any()
+        got, got_lse, out, lse, slack = (x[~blank] for x in (got, got_lse, out, lse, slack))
+        if not len(out):
+            return
+        assert np.isfinite(got).all()
+        off, size = np.linalg.norm(got - out, axis=-1), np.linalg.norm(out, axis=-1)
+        assert np.linalg.norm(off) <= WHOLE * np.linalg.norm(size), np.linalg.norm(off) / np.linalg.norm(size)
+        assert (off <= ROW * size + 1e-6).all(), (off / size).max()
+        worst = 2.0 ** -8 * slack + 2.0 ** -20 * (1 + np.abs(lse))
+        assert (np.abs(got_lse - lse) <= worst).all(), (np.abs(got_lse - lse) / worst).max()
+
+
+@pytest.mark.parametrize("page", [128, 256, 64, 16, 24, 100, 7, 1])
+def test_pages(page):
+    Case([3, 1, 5], [300, 255, 40], 4, page, seed=page).check()
+
+
+@pytest.mark.parametrize("H", [1, 2, 16, 21, 64, 128])
+def test_heads(H):
+    Case([2, 3], [70, 400], H, 16, seed=H).check()
+
+
+@pytest.mark.parametrize("cached", [0, 1, 126, 127, 128, 129, 253, 254, 255, 256, 257, 511, 512, 600])
+def test_context_lengths_at_the_tiles_edges(cached):
+    """New tokens on both sides of a half tile's and a tile's edge."""
+    Case([3], [cached], 8, 32, seed=cached).check()
+
+
+@pytest.mark.parametrize("mask", ["causal", "tree", "any"])
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 64, 65, 100, 128])
+def test_chunk_lengths(n, mask):
+    Case([n, 1], [90, 3], 3, 16, seed=n, mask=mask).check()
+
+
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+def test_long_chunks(mask):
+    """More new tokens than a tile has keys, rows of several tiles a token."""
+    Case([300, 2], [5, 200], 2, 64, mask=mask, words=16 if mask == "tree" else None).check()
+
+
+def test_no_new_tokens_and_single_ones():
+    Case([0, 1, 0, 1, 0], [10, 0, 0, 700, 3], 16, 16).check()
+
+
+def test_many_short_sequences():
+    """Several row tiles a piece, sequences shorter than one key tile."""
+    rng = np.random.default_rng(5)
+    Case(list(rng.integers(0, 6, 200)), list(rng.integers(0, 60, 200)), 4, 16, mask="any").check()
+
+
+@pytest.mark.parametrize("mask", ["causal", "any"])
+def test_one_long_sequence_cut_into_many_pieces(mask):
+    Case([4], [22000], 4, 128, mask=mask).check()
+
+
+@pytest.mark.parametrize("sink", [True, False])
+def test_rows_that_see_nothing(sink):
+    Case([4, 2, 1], [0, 0, 9], 5, 16, mask=[0, 1, 0, 6, 0, 2, 0], sink=sink).check()
+
+
+def test_rows_that_see_nothing_in_a_split_tile():
+    """No cached keys, thousands of new ones, of which most rows see few."""
+    rng = np.random.default_rng(1)
+    n = 3500
+    mask = [0 if i % 3 == 0 else 1 << int(rng.integers(n)) | 1 << int(rng.integers(n)) for i in range(n)]
+    c = Case([n], [0], 1, 128, mask=mask, words=-(-n // 32))
+    c.check()
+
+
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+def test_sinks(mask):
+    Case([5, 40, 1], [0, 300, 2000], 16, 64, mask=mask, sink=True).check()
+
+
+def test_a_sink_that_is_no_logit():
+    c = Case([2, 2], [30, 0], 4, 16, sink=True)
+    c.sink[:] = [-np.inf, 80.0]
+    c.make_buffers()
+    c.check()
+
+
+def test_rows_behind_the_last_sequence_stay():
+    Case([3, 2], [50, 10], 4, 16, extra=4).check()
+
+
+def test_spread_scores():
+    """Scores whose maximum moves from tile to tile: references that follow it.
+    (sigma is 6: the query's rounding counts six times, so that bound only.)"""
+    c = Case([4], [3000], 4, 64, spread=6.0)
+    mla.check(c.call())
+    out, lse, slack = c.oracle()
+    got = c.out.double().cpu().numpy()
+    assert np.linalg.norm(got - out) <= 2 * 0.00165 * np.sqrt(2 + 36) * np.linalg.norm(out)
+    assert (np.abs(c.lse.double().cpu().numpy() - lse) <= 2.0 ** -8 * slack + 2.0 ** -20 * (1 + np.abs(lse))).all()
+
+
+def test_a_maximum_that_grows_and_one_far_above():
+    """Keys whose scores rise along the context by far more than a reference
+    bears, and one key that takes all the weight."""
+    c = Case([1], [2000], 1, 64, mask="causal")
+    rows = c.kv.copy()
+    lat = c.uk[0] @ c.q[0, 0, :128]
+    j = np.arange(2001)
+    at = c.table[0, j // 64] * 64 + j % 64
+    rows[at, :512] += np.outer(np.linspace(-3, 3, 2001), lat / np.linalg.norm(lat)) * 60
+    c.kv_d, c.kv = bf16(rows)
+    mla.check(c.call())
+    out, lse, slack = c.oracle()
+    got = c.out.double().cpu().numpy()
+    # The scores' error is bounded by the slack; what it does to a softmax by twice that, relative.
+    assert np.linalg.norm(got - out) <= (2 * 0.00165 * slack.max() + 2 * 0.0029) * np.linalg.norm(out)
+    assert np.abs(c.lse.item() - lse.item()) <= 2.0 ** -8 * slack.max() + 2.0 ** -20 * (1 + abs(lse.item()))
+
+
+def test_one_key_is_its_own_result():
+    """A token that sees itself alone: out = w_uv c, lse = its score."""
+    Case([6, 1], [0, 0], 8, 16, mask=[1 << i for i in range(6)] + [1]).check()
+
+
+def test_causal_equals_the_mask_that_says_so():
+    c = Case([7, 33, 2], [100, 255, 0], 16, 16, mask="causal")
+    mla.check(c.call())
+    d = Case([7, 33, 2], [100, 255, 0], 16, 16, mask=[(2 << i) - 1 for n in (7, 33, 2) for i in range(n)])
+    mla.check(d.call())
+    assert torch.equal(c.out, d.out) and torch.equal(c.lse, d.lse)
+
+
+def test_bits_past_the_chunk_mean_nothing():
+    c = Case([3, 2], [20, 0], 4, 16, mask=[1, 3, 5, 1, 2])
+    mla.check(c.call())
+    d = Case([3, 2], [20, 0], 4, 16, mask=[1 | 8 << 20, 3 | 16, 5 | 1 << 60, 1 | 12, 2 | 1 << 33], words=3)
+    mla.check(d.call())
+    assert torch.equal(c.out, d.out) and torch.equal(c.lse, d.lse)
+
+
+def test_equal_to_decode_on_single_tokens():
+    """mla_decode's result within both calls' roundings."""
+    c = Case([1] * 5, [500, 3, 64, 1000, 128], 16, 64, mask="causal", sink=True)
+    mla.check(c.call())
+    out, lse = torch.zeros_like(c.out), torch.zeros_like(c.lse)
+    iro, cached, table = c.ints
+    parts = mla.mla_decode_partitions(c.B, c.H, 1, 1001)
+    n = mla.mla_decode_workspace_bytes(c.H, c.T, parts)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    kv = torch.nan_to_num(c.kv_d)                    # the decode reads whole tiles
+    mla.check(mla.mla_decode(out, lse, c.q_d, iro, cached, kv, table, c.num, c.page, c.most, c.uk_d, c.uv_d, c.B, c.H,
+                             c.T, 1, 1001, 0, c.scale, attn_sink=c.sink_d, workspace=ws, workspace_bytes=n,
+                             d_status=c.st))
+    assert c.st.item() == 0
+    a, b = c.out.double(), out.double()
+    assert ((a - b).norm() / b.norm()).item() <= 2 * WHOLE and (c.lse - lse).abs().max().item() <= 5e-3
+
+
+def test_without_lse_and_repeated_calls_are_the_same_bits():
+    c = Case([9, 3, 20], [3000, 10, 700], 16, 64)
+    c.check()
+    out = c.out.clone()
+    for _ in range(3):
+        c.out.fill_(FILL)
+        mla.check(c.call(lse=False))
+        assert torch.equal(c.out, out)
+
+
+def test_captured_replayed_and_on_two_streams():
+    """A graph replayed on other inputs, and two calls at once with workspaces of their own."""
+    a, b = Case([5, 8], [900, 60], 8, 32, seed=1), Case([6, 7], [80, 1200], 8, 32, seed=2)
+    a.check(), b.check()
+    want = a.out.clone(), b.out.clone()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c in (a, b):
+        c.out.fill_(FILL)
+    torch.cuda.synchronize()
+    mla.check(a.call(stream=s)), mla.check(b.call(stream=t))
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mla.check(a.call())
+    for scale in (1.0, 0.5):
+        a.q_d.mul_(scale)
+        a.q = a.q_d.double().cpu().numpy()
+        a.out.fill_(FILL)
+        g.replay()
+        torch.cuda.synchronize()
+        a.compare(*a.oracle())
+
+
+def test_left_out_sequences():
+    """Offsets past the tokens, more tokens than the mask has bits: those rows stay."""
+    c = Case([3, 40, 2], [20, 30, 5], 4, 16, words=1)
+    mla.check(c.call())
+    assert c.st.item() == mla.MLA_DEV_BAD_OFFSETS
+    out, lse, slack = c.oracle()
+    lse[3:43] = np.nan
+    c.compare(out, lse, slack)
+    c = Case([3, 4], [20, 30], 4, 16)
+    c.T -= 1
+    mla.check(c.call())
+    assert c.st.item() == mla.MLA_DEV_BAD_OFFSETS
+    out, lse, slack = c.oracle()
+    lse[3:] = np.nan
+    c.compare(out, lse, slack)
+
+
+@pytest.mark.parametrize("iro", [[0, 5, 3, 7], [1, 3, 5, 7], [0, 3, 7, 1 << 31]])
+def test_offsets_that_are_none(iro):
+    c = Case([3, 2, 2], [20, 30, 40], 4, 16)
+    c.ints[0] = dev(np.array(iro, dtype=np.int64).astype(np.uint32).view(np.int32))
+    mla.check(c.call())
+    assert c.st.item() == mla.MLA_DEV_BAD_OFFSETS
+    if iro[0] == 0 and iro[2] == 7:
+        assert (c.out != FILL).any()
+    else:
+        assert (c.out == FILL).all() and (c.lse == FILL).all()
+
+
+def test_a_missing_page_is_reported_and_harms_no_other_sequence():
+    c = Case([3, 2], [100, 100], 4, 16)
+    out, lse, slack = c.oracle()
+    for entry in (-1, c.num, 1 << 30):
+        table = c.table.copy()
+        table[0, 2] = entry
+        c.ints[2] = dev(table)
+        c.st.zero_(), c.out.fill_(FILL), c.lse.fill_(FILL)
+        mla.check(c.call())
+        assert c.st.item() == mla.MLA_DEV_BAD_PAGE
+        c.out[:3], c.lse[:3] = FILL, FILL
+        lse[:3] = np.nan
+        c.compare(out, lse, slack)
+
+
+def test_a_nan_key_is_nan_for_those_who_see_it():
+    c = Case([4], [40], 4, 16, mask=[1, 2, 4, 8])
+    j = 42                                         # new token 2
+    c.kv_d[int(c.table[0, j // 16]) * 16 + j % 16, 530] = float("nan")
+    mla.check(c.call())
+    nan = torch.isnan(c.out).any(-1).any(-1).tolist()
+    assert nan[2] and torch.isnan(c.out[2]).all()
+
+
+def test_a_timeout_before_stops_the_call():
+    c = Case([4], [40], 4, 16)
+    c.st.fill_(mla.MLA_DEV_TIMEOUT)
+    mla.check(c.call())
+    assert (c.out == FILL).all() and (c.lse == FILL).all()
+
+
+def test_a_speculative_step():
+    """The calls of one step in a row: two prompts are continued twice each, drafts are written at their depths,
+    attend as trees, the accepted ones move together, what was reserved for the others is given back, the pool is
+    compacted, and the next token decodes: as the same tokens do in caches of their own."""
+    rng = np.random.default_rng(11)
+    page, H, most, pool, B = 8, 4, 8, 40, 4
+    L0, parents, n_draft = [19, 24], [0, 0, 1, 1], 6
+    up = [-1, 0, 0, 1, 3, 2]
+    depth, mask = [], []
+    for i, u in enumerate(up):
+        depth.append(0 if u < 0 else depth[u] + 1)
+        mask.append(1 << i | (mask[u] if u >= 0 else 0))
+    kept = [[0, 1, 3], [0, 2, 5], [0], [0, 1, 3, 4]]                      # paths from the root
+    ang = np.arange(64)[:, None] * 10000.0 ** (-np.arange(32) / 32)
+    freqs = torch.from_numpy(np.stack([np.cos(ang), np.sin(ang)], -1).reshape(64, 64)).float().to(DEV)
+    gamma = torch.ones(512, device=DEV)
+    kv = torch.full((pool * page, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    uk, uv = bf16(rng.standard_normal((H, 512, 128)) * 512 ** -0.5), bf16(rng.standard_normal((H, 128, 512)) * 512 ** -0.5)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table, refs, lengths = dev(np.full((2, most), -1)), dev(np.zeros(pool)), dev([0, 0])
+    src, dst, cnt = dev(np.zeros(pool)), dev(np.zeros(pool)), dev([0])
+    size = mla.mla_pages_workspace_bytes(pool, B)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+
+    def reserve(t, n, new, b):
+        mla.check(mla.mla_pages_reserve(t, refs, n, dev(new), src, dst, cnt, pool, page, most, b, ws, size, st))
+        mla.check(mla.mla_pages_copy(kv, page * 1152, 1, 0, src, dst, cnt, pool, pool, st))
+
+    def write(t, n, lat, iro, b, q=None, positions=None):
+        rest = (dev(iro), n, t, pool, page, most, b, H, len(lat), 64, 1e-6, 1.0, mla.MLA_BF16, st)
+        if positions is None:
+            mla.check(mla.mla_latent_cache_write(kv, q, lat, gamma, freqs, *rest))
+        else:
+            mla.check(mla.mla_latent_cache_write_at(kv, q, lat, gamma, freqs, dev(positions), *rest))
+
+    prompt = bf16(rng.standard_normal((sum(L0), 576)))[0]
+    reserve(table, lengths, L0, 2)
+    write(table, lengths, prompt, [0, L0[0], sum(L0)], 2)
+    lengths = dev(L0)
+    t2, n2 = dev(np.zeros((B, most))), dev(np.zeros(B))
+    mla.check(mla.mla_pages_fork(t2, n2, table, lengths, refs, dev(parents), pool, most, B, 2, st))
+    reserve(t2, n2, [n_draft] * B, B)
+    iro = np.arange(B + 1) * n_draft
+    drafts = bf16(rng.standard_normal((B * n_draft, 576)))[0]
+    q_raw = bf16(rng.standard_normal((B * n_draft, H, 192)))[0]
+    q = q_raw.clone()
+    at = np.concatenate([[L0[p] + d for d in depth] for p in parents])
+    write(t2, n2, drafts, iro, B, q, at)
+    words = dev(np.array(mask * B)[:, None])
+    out, lse = torch.zeros(B * n_draft, H, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(B * n_draft, H, device=DEV)
+    nb = mla.mla_chunk_attention_workspace_bytes(B, H, B * n_draft)
+    cws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+
+    def attend(qq, t, n, i, o, l, m=None):
+        mla.check(mla.mla_chunk_attention(o, l, qq, dev(i), n, kv, t, pool, page, most, uk[0], uv[0], len(i) - 1, H, len(qq),
+                                          192 ** -0.5, chunk_mask=m, mask_words=0 if m is None else 1, workspace=cws,
+                                          workspace_bytes=nb, d_status=st))
+    attend(q, t2, n2, iro, out, lse, words)
+    # The accepted rows, the rest given back, the pool compacted.
+    width = max(map(len, kept))
+    pad = dev([k + [-1] * (width - len(k)) for k in kept])
+    counts = dev([len(k) for k in kept])
+    mla.check(mla.mla_cache_keep_rows(kv, 1152, 1, 0, n2, pad, width, counts, t2, pool, page, most, B, st))
+    n2 += counts
+    mla.check(mla.mla_pages_free(t2, refs, n2, n2, pool, page, most, B, st))
+    mla.check(mla.mla_pages_compact(t2, refs, src, dst, cnt, pool, pool, most, B, ws, size, st))
+    mla.check(mla.mla_pages_copy(kv, page * 1152, 1, 0, src, dst, cnt, pool, pool, st))
+    assert st.item() == 0
+    live = int((refs > 0).sum())
+    assert (refs[:live] > 0).all() and np.array_equal(np.bincount(t2[t2 >= 0].cpu(), minlength=pool), refs.cpu())
+    # Each sequence's rows are those of its text written in a row.
+    for b in range(B):
+        p = parents[b]
+        L = L0[p] + len(kept[b])
+        lat = torch.cat([prompt[L0[0] * p: L0[0] * p + L0[p]], drafts[[b * n_draft + k for k in kept[b]]]])
+        own = torch.zeros(8 * page, 576, dtype=torch.bfloat16, device=DEV)
+        mla.check(mla.mla_latent_cache_write(own, None, lat, gamma, freqs, dev([0, L]), dev([0]), dev([np.arange(8)]), 8, page,
+                                             8, 1, H, L, 64, 1e-6, 1.0, mla.MLA_BF16, st))
+        j = np.arange(L)
+        rows = t2[b].cpu().numpy()[j // page] * page + j % page
+        assert torch.equal(kv[rows], own[:L])
+        # Each accepted draft saw the prompt and the path behind it: the causal chunk of the kept rows.
+        qk = q[[b * n_draft + k for k in kept[b]]].contiguous()
+        o, l = torch.zeros(len(kept[b]), H, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(len(kept[b]), H, device=DEV)
+        attend(qk, t2[b: b + 1].contiguous(), dev([L0[p]]), [0, len(kept[b])], o, l)
+        want = out[[b * n_draft + k for k in kept[b]]].double()
+        assert ((o.double() - want).norm() / want.norm()).item() <= 2 * WHOLE
+        assert (l - lse[[b * n_draft + k for k in kept[b]]]).abs().max().item() <= 1e-5
+    assert st.item() == 0
