@@ -52,12 +52,13 @@ constexpr int kPBytes = 4 * 64 * 128;        // 64 rows x 256 keys in blocks of 
 constexpr int kSmemQ = 0;
 constexpr int kSmemP = kSmemQ + kQBytes;
 constexpr int kSmemRing = kSmemP + kPBytes;
-constexpr int kSmemBoxes = kSmemRing + kStages * kStage;      // two tiles' boxes: 4 groups of 64 rows each
-constexpr int kSmemRed = kSmemBoxes + 2 * 4 * 64 * 8;         // row maxima and sums of both halves
+constexpr int kFound = 4;                    // tiles whose rows have been looked up
+constexpr int kSmemBoxes = kSmemRing + kStages * kStage;      // their boxes: 4 groups of 64 rows each
+constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // row maxima and sums of both halves
 constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
-constexpr int kSmemTotal = kSmemBar + 256 + 1024;
+constexpr int kSmemTotal = kSmemBar + 512 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
-constexpr int kThreads = 192;                // producer, MMA, 4 softmax warps
+constexpr int kThreads = 224;                // producer, MMA, 4 softmax warps, row lookup
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
@@ -76,9 +77,11 @@ struct ChunkSmem {
   uint64_t swapped[2];       // the two warps that share rows have both written their words
   uint32_t tmem;
   int abort;
-  int boxes[2][4];           // boxes of a group of 64 rows
+  uint64_t found[kFound], taken[kFound];
+  int row[kFound][4];        // first cache row of a group of 64 consecutive ones, or -1:
+  int boxes[kFound][4];      // it is this many boxes
 };
-static_assert(sizeof(ChunkSmem) <= 256, "barrier block");
+static_assert(sizeof(ChunkSmem) <= 512, "barrier block");
 
 // A split row tile, noted by the piece in which it ends.
 struct SplitTile {
@@ -260,6 +263,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh->p_full), 8);
     mbar_init(smem_u32(&sh->pv_done), 1);
     mbar_init(smem_u32(&sh->drain), 1);
+    for (int s = 0; s < kFound; ++s) {
+      mbar_init(smem_u32(&sh->found[s]), 1);
+      mbar_init(smem_u32(&sh->taken[s]), 1);
+    }
     mbar_init(smem_u32(&sh->swapped[0]), 2);
     mbar_init(smem_u32(&sh->swapped[1]), 2);
     sh->abort = timed_out_before(status) ? 1 : 0;
@@ -282,105 +289,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (the barriers below are passed by all)
   } else if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    // (cache row, first row << 8 | log2 rows)
-    int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
+    const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
     Walk w = walk_start(p, piece, total, pieces);
     Segment s;
-    uint32_t stage = 0, phase = 0, segments = 0;
-    uint32_t used = 0;
+    uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
     bool ok = true;
-    // The boxes of a tile: each run of consecutive cache rows in a group of 64
-    // is cut into powers of two, largest first.  Rows past the context, or
-    // without a page, are boxes behind the cache's end, which read as zeros: no
-    // row that nobody has written can reach a product.
-    auto look_up = [&](const Segment& sg, int tile, int slot) {
-      int row[kTile / 32];
-#pragma unroll
-      for (int e = 0; e < kTile / 32; ++e) {
-        const int pos = tile * kTile + e * 32 + lane;
-        row[e] = -1;
-        if (pos < sg.L) {
-          const int j = pos / p.page_size;
-          const int page = j < p.max_pages ? p.page_table[static_cast<size_t>(sg.b) * p.max_pages + j] : -1;
-          if (page >= 0 && page < p.num_pages) row[e] = page * p.page_size + (pos - j * p.page_size);
-          else set_status(status, MLA_DEV_BAD_PAGE);
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        // Bit i: row i of the group does not continue row i - 1.
-        unsigned long long cuts = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          int before = __shfl_up_sync(0xffffffffu, row[2 * g + u], 1);
-          const int other = __shfl_sync(0xffffffffu, row[2 * g], 31);
-          if (lane == 0) before = other;
-          const bool cut = (u == 0 && lane == 0) ||
-                           (row[2 * g + u] < 0 ? before >= 0 : before < 0 || row[2 * g + u] != before + 1);
-          cuts |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, cut)) << (32 * u);
-        }
-        int count = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = 32 * u + lane;
-          const unsigned long long upto = cuts & (~0ull >> (63 - i)), past = i == 63 ? 0 : cuts >> (i + 1);
-          const int at = i - (63 - __clzll(upto));                       // within its run
-          const int left = past ? __ffsll(past) : 64 - i;                // rows of the run from here on
-          const bool starts = at == 0 || left < (at & -at);
-          const unsigned m = __ballot_sync(0xffffffffu, starts);
-          if (starts)
-            boxes[(slot * 4 + g) * 64 + count + __popc(m & ((1u << lane) - 1))] =
-                make_int2(row[2 * g + u] < 0 ? p.cache_rows : row[2 * g + u], i << 8 | (31 - __clz(left)));
-          count += __popc(m);
-        }
-        if (lane == 0) sh->boxes[slot][g] = count;
-      }
-      __syncwarp();
-    };
-    auto load_group = [&](int slot, int g, uint32_t dst, uint32_t bar, int col) {
-      const int n = sh->boxes[slot][g];
-      for (int i = lane; i < n; i += 32) {
-        const int2 b = boxes[(slot * 4 + g) * 64 + i];
-        tma_load_2d(dst + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, col, b.x);
-      }
-    };
-    auto acquire = [&]() {
+    // One stage: two groups of 64 rows x 64 columns.
+    auto load = [&](int slot, int g0, int g1, int col0, int col1) {
       if (used >= kStages && !mbar_wait_warp(smem_u32(&sh->empty[stage]), phase ^ 1, status, abort_flag)) return ok = false;
-      if (lane == 0) mbar_expect_tx(smem_u32(&sh->full[stage]), kStage);
-      __syncwarp();
-      return true;
-    };
-    auto advance = [&]() {
+      const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
+      const int y0 = sh->row[slot][g0], y1 = sh->row[slot][g1];
+      if ((y0 | y1) >= 0) {
+        if (elect_one()) {
+          mbar_expect_tx(bar, kStage);
+          tma_load_2d(dst, &maps.box[6], bar, col0, y0);
+          tma_load_2d(dst + 8192, &maps.box[6], bar, col1, y1);
+        }
+      } else {
+        if (lane == 0) mbar_expect_tx(bar, kStage);
+        __syncwarp();
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          const int g = u ? g1 : g0, y = u ? y1 : y0, n = y >= 0 ? 1 : sh->boxes[slot][g];
+          for (int i = lane; i < n; i += 32) {
+            const int2 b = y >= 0 ? make_int2(y, 6) : boxes[(slot * 4 + g) * 64 + i];
+            tma_load_2d(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
+          }
+        }
+      }
       __syncwarp();
       ++used;
       if (++stage == kStages) stage = 0, phase ^= 1;
+      return true;
     };
-    auto load_k = [&](int slot) {
-      for (int c = 0; c < 9; ++c) {
-        if (!acquire()) return;
-        const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
-        load_group(slot, 2 * rank, dst, bar, c * 64);
-        load_group(slot, 2 * rank + 1, dst + 8192, bar, c * 64);
-        advance();
-      }
-    };
-    auto load_v = [&](int slot) {
-      for (int i = 0; i < 8; ++i) {
-        if (!acquire()) return;
-        const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
-        const int col = 256 * (i & 1) + 128 * static_cast<int>(rank);
-        load_group(slot, i >> 1, dst, bar, col);
-        load_group(slot, i >> 1, dst + 8192, bar, col + 64);
-        advance();
-      }
-    };
+    // K of tile j, V of the tile before, in the order of use.
     while (ok && walk_next(p, w, s)) {
       if (s.tiles == 0) continue;
-      look_up(s, s.k0, 0);
-      if (segments > 0 && !mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag)) {
-        ok = false;
-        break;
-      }
+      if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
       if (elect_one()) {
         const uint32_t bar = smem_u32(&sh->q_full);
         mbar_expect_tx(bar, kQBytes);
@@ -389,14 +334,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++segments;
-      load_k(0);
-      for (int j = 0; j < s.tiles && ok; ++j) {
-        if (j + 1 < s.tiles) {
-          look_up(s, s.k0 + j + 1, (j + 1) & 1);
-          load_k((j + 1) & 1);
+#pragma unroll 1
+      for (int j = 0; j <= s.tiles && ok; ++j) {
+        if (j < s.tiles) {
+          const int slot = (tile + j) % kFound;
+          if (!(ok = mbar_wait_warp(smem_u32(&sh->found[slot]), ((tile + j) / kFound) & 1, status, abort_flag))) break;
+#pragma unroll 1
+          for (int c = 0; c < 9 && ok; ++c) load(slot, 2 * rank, 2 * rank + 1, c * 64, c * 64);
         }
-        if (ok) load_v(j & 1);
+        if (j > 0) {
+          const int slot = (tile + j - 1) % kFound;
+#pragma unroll 1
+          for (int i = 0; i < 8 && ok; ++i) {
+            const int col = 256 * (i & 1) + 128 * static_cast<int>(rank);
+            load(slot, i >> 1, i >> 1, col, col + 64);
+          }
+          if (lane == 0) mbar_arrive(smem_u32(&sh->taken[slot]));
+        }
       }
+      tile += s.tiles;
     }
     // Nothing may be on its way into this CTA when it leaves: the loads (if the
     // MMAs did not get to wait for them) and the releases of the stages.
@@ -498,6 +454,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&sh->drain), 0, status, &never);
     }
     __syncwarp();
+  } else if (warp == 6) {
+    // ---------------------------------------------------------------- row lookup
+    // Where a tile's rows are in the cache.  Four groups of 64 that each are
+    // consecutive rows need a row each; any other group is a list of boxes
+    // (cache row, first row << 8 | log2 rows): every run of consecutive rows is
+    // cut into powers of two, largest first.  Rows past the context, or without
+    // a page, are boxes behind the cache's end, which read as zeros: no row that
+    // nobody has written reaches a product.
+    int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
+    Walk w = walk_start(p, piece, total, pieces);
+    Segment s;
+    uint32_t tile = 0;
+    bool ok = true;
+    const bool aligned = p.page_size % 64 == 0;
+    while (ok && walk_next(p, w, s)) {
+      const int32_t* const pages = p.page_table + static_cast<size_t>(s.b) * p.max_pages;
+#pragma unroll 1
+      for (int j = 0; j < s.tiles; ++j, ++tile) {
+        const int slot = tile % kFound;
+        const int first = (s.k0 + j) * kTile;
+        auto row_of = [&](int pos) {
+          if (pos >= s.L) return -1;
+          const int i = pos / p.page_size;
+          const int page = i < p.max_pages ? pages[i] : -1;
+          if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - i * p.page_size);
+          set_status(status, MLA_DEV_BAD_PAGE);
+          return -1;
+        };
+        int whole = -1;                                   // lane g < 4: group g
+        if (aligned && lane < 4 && first + 64 * lane + 64 <= s.L) whole = row_of(first + 64 * lane);
+        const unsigned parts = __ballot_sync(0xffffffffu, whole < 0) & 15u;
+        if (tile >= kFound &&
+            !(ok = mbar_wait_warp(smem_u32(&sh->taken[slot]), ((tile / kFound) & 1) ^ 1, status, abort_flag)))
+          break;
+        if (lane < 4) sh->row[slot][lane] = whole;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          if (!(parts >> g & 1)) continue;
+          const int pos = first + 64 * g + lane;
+          const int row0 = row_of(pos), row1 = row_of(pos + 32);
+          // Bit i: row i of the group does not continue row i - 1.
+          const int last0 = __shfl_sync(0xffffffffu, row0, 31);
+          int before0 = __shfl_up_sync(0xffffffffu, row0, 1), before1 = __shfl_up_sync(0xffffffffu, row1, 1);
+          if (lane == 0) before1 = last0;
+          auto cut = [](int row, int before) { return row < 0 ? before >= 0 : before < 0 || row != before + 1; };
+          const unsigned lo = __ballot_sync(0xffffffffu, lane == 0 || cut(row0, before0));
+          const unsigned hi = __ballot_sync(0xffffffffu, cut(row1, before1));
+          const unsigned long long cuts = static_cast<unsigned long long>(hi) << 32 | lo;
+          int count = 0;
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            const int i = 32 * u + lane, row = u ? row1 : row0;
+            const unsigned long long upto = cuts & (~0ull >> (63 - i)), past = i == 63 ? 0 : cuts >> (i + 1);
+            const int at = i - (63 - __clzll(upto));                       // within its run
+            const int left = past ? __ffsll(past) : 64 - i;                // rows of the run from here on
+            const bool starts = at == 0 || left < (at & -at);
+            const unsigned m = __ballot_sync(0xffffffffu, starts);
+            if (starts)
+              boxes[(slot * 4 + g) * 64 + count + __popc(m & ((1u << lane) - 1))] =
+                  make_int2(row < 0 ? p.cache_rows : row, i << 8 | (31 - __clz(left)));
+            count += __popc(m);
+          }
+          if (lane == 0) sh->boxes[slot][g] = count;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->found[slot]));
+      }
+    }
   } else {
     // ---------------------------------------------------------------- softmax
     const int quarter = warp & 3;
