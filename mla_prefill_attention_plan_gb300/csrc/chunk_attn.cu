@@ -78,7 +78,7 @@ struct ChunkSmem {
   uint32_t tmem;
   int abort;
   uint64_t found[kFound], taken[kFound];
-  int row[kFound][4];        // first cache row of a group of 64 consecutive ones, or -1:
+  alignas(16) int row[kFound][4];   // first cache row of a group of 64 consecutive ones, or -1:
   int boxes[kFound][4];      // it is this many boxes
 };
 static_assert(sizeof(ChunkSmem) <= 512, "barrier block");
@@ -292,37 +292,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
     Walk w = walk_start(p, piece, total, pieces);
     Segment s;
-    uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
+    uint32_t stage = 0, phase = 0, segments = 0, used = 0, last = 0, tile = 0;
     bool ok = true;
-    // One stage: two groups of 64 rows x 64 columns.
-    auto load = [&](int slot, int g0, int g1, int col0, int col1) {
-      if (used >= kStages && !mbar_wait_warp(smem_u32(&sh->empty[stage]), phase ^ 1, status, abort_flag)) return ok = false;
-      const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
-      const int y0 = sh->row[slot][g0], y1 = sh->row[slot][g1];
-      if ((y0 | y1) >= 0) {
-        if (elect_one()) {
+    // Stage `used`, when its last reader is through with it.
+    auto ready = [&](uint32_t st, uint32_t ph, uint32_t n) {
+      return n < kStages || mbar_wait(smem_u32(&sh->empty[st]), ph ^ 1, status, abort_flag);
+    };
+    auto advance = [&](uint32_t n) {
+      used += n;
+      stage += n;
+      while (stage >= kStages) stage -= kStages, phase ^= 1;
+    };
+    // n stages of two boxes each that lie whole in the cache, issued by one lane
+    // (what the loop costs for each stage is what bounds the loads: with a warp's
+    // votes and the rows read for each stage, 495 clk).
+    auto load_whole = [&](uint32_t n, auto box) {
+      if (elect_one()) {
+        uint32_t st = stage, ph = phase;
+        for (uint32_t i = 0; i < n; ++i) {
+          if (!(ok = ready(st, ph, used + i))) break;
+          const uint32_t bar = smem_u32(&sh->full[st]), dst = ring + st * kStage;
           mbar_expect_tx(bar, kStage);
-          tma_load_2d(dst, &maps.box[6], bar, col0, y0);
-          tma_load_2d(dst + 8192, &maps.box[6], bar, col1, y1);
-        }
-      } else {
-        if (lane == 0) mbar_expect_tx(bar, kStage);
-        __syncwarp();
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          const int g = u ? g1 : g0, y = u ? y1 : y0, n = y >= 0 ? 1 : sh->boxes[slot][g];
-          for (int i = lane; i < n; i += 32) {
-            const int2 b = y >= 0 ? make_int2(y, 6) : boxes[(slot * 4 + g) * 64 + i];
-            tma_load_2d(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
-          }
+          box(i, dst, bar);
+          if (++st == kStages) st = 0, ph ^= 1;
+          last = used + i + 1;
         }
       }
       __syncwarp();
-      ++used;
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      return true;
+      ok = __all_sync(0xffffffffu, ok);
+      advance(n);
+    };
+    // One stage of two groups of 64 rows x 64 columns, any boxes.
+    auto load = [&](int slot, int g0, int g1, int col0, int col1) {
+      ok = __all_sync(0xffffffffu, ready(stage, phase, used));
+      if (!ok) return;
+      const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
+      if (lane == 0) mbar_expect_tx(bar, kStage);
+      __syncwarp();
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        const int g = u ? g1 : g0, y = sh->row[slot][g], n = y >= 0 ? 1 : sh->boxes[slot][g];
+        for (int i = lane; i < n; i += 32) {
+          const int2 b = y >= 0 ? make_int2(y, 6) : boxes[(slot * 4 + g) * 64 + i];
+          tma_load_2d(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
+        }
+      }
+      __syncwarp();
+      last = used + 1;
+      advance(1);
     };
     // K of tile j, V of the tile before, in the order of use.
+    const int vcol = 128 * static_cast<int>(rank);
     while (ok && walk_next(p, w, s)) {
       if (s.tiles == 0) continue;
       if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
@@ -339,21 +359,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (j < s.tiles) {
           const int slot = (tile + j) % kFound;
           if (!(ok = mbar_wait_warp(smem_u32(&sh->found[slot]), ((tile + j) / kFound) & 1, status, abort_flag))) break;
+          const int y0 = sh->row[slot][2 * rank], y1 = sh->row[slot][2 * rank + 1];
+          if ((y0 | y1) >= 0) {
+            load_whole(9, [&](int c, uint32_t dst, uint32_t bar) {
+              tma_load_2d(dst, &maps.box[6], bar, c * 64, y0);
+              tma_load_2d(dst + 8192, &maps.box[6], bar, c * 64, y1);
+            });
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < 9 && ok; ++c) load(slot, 2 * rank, 2 * rank + 1, c * 64, c * 64);
+            for (int c = 0; c < 9 && ok; ++c) load(slot, 2 * rank, 2 * rank + 1, c * 64, c * 64);
+          }
         }
-        if (j > 0) {
+        if (j > 0 && ok) {
           const int slot = (tile + j - 1) % kFound;
+          const int4 y = *reinterpret_cast<const int4*>(sh->row[slot]);
+          if ((y.x | y.y | y.z | y.w) >= 0) {
+            load_whole(8, [&](int i, uint32_t dst, uint32_t bar) {
+              const int g = i >> 1, col = 256 * (i & 1) + vcol;
+              const int row = g == 0 ? y.x : g == 1 ? y.y : g == 2 ? y.z : y.w;
+              tma_load_2d(dst, &maps.box[6], bar, col, row);
+              tma_load_2d(dst + 8192, &maps.box[6], bar, col + 64, row);
+            });
+          } else {
 #pragma unroll 1
-          for (int i = 0; i < 8 && ok; ++i) {
-            const int col = 256 * (i & 1) + 128 * static_cast<int>(rank);
-            load(slot, i >> 1, i >> 1, col, col + 64);
+            for (int i = 0; i < 8 && ok; ++i) {
+              const int col = 256 * (i & 1) + vcol;
+              load(slot, i >> 1, i >> 1, col, col + 64);
+            }
           }
           if (lane == 0) mbar_arrive(smem_u32(&sh->taken[slot]));
         }
       }
       tile += s.tiles;
     }
+    used = __reduce_max_sync(0xffffffffu, last);      // stages that were loaded
     // Nothing may be on its way into this CTA when it leaves: the loads (if the
     // MMAs did not get to wait for them) and the releases of the stages.
     if (elect_one()) {
