@@ -253,10 +253,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sh->full[s]), rank == 0 ? 2 : 1);   // CTA 0: its own bytes and CTA 1's word
+      mbar_init(smem_u32(&sh->full[s]), 1);    // (CTA 0's counts both CTAs' bytes)
       mbar_init(smem_u32(&sh->empty[s]), 1);
     }
-    mbar_init(smem_u32(&sh->q_full), rank == 0 ? 2 : 1);
+    mbar_init(smem_u32(&sh->q_full), 1);
     mbar_init(smem_u32(&sh->q_free), 1);
     mbar_init(smem_u32(&sh->s_full[0]), 1);
     mbar_init(smem_u32(&sh->s_full[1]), 1);
@@ -294,6 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Segment s;
     uint32_t stage = 0, phase = 0, segments = 0, used = 0, last = 0, tile = 0;
     bool ok = true;
+    // Both CTAs' loads count at CTA 0's barriers, whose MMAs wait for them.
+    const uint32_t full0 = cluster_addr(smem_u32(&sh->full[0]), 0);
     // Stage `used`, when its last reader is through with it.
     auto ready = [&](uint32_t st, uint32_t ph, uint32_t n) {
       return n < kStages || mbar_wait(smem_u32(&sh->empty[st]), ph ^ 1, status, abort_flag);
@@ -311,9 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t st = stage, ph = phase;
         for (uint32_t i = 0; i < n; ++i) {
           if (!(ok = ready(st, ph, used + i))) break;
-          const uint32_t bar = smem_u32(&sh->full[st]), dst = ring + st * kStage;
-          mbar_expect_tx(bar, kStage);
-          box(i, dst, bar);
+          if (rank == 0) mbar_expect_tx(smem_u32(&sh->full[st]), 2 * kStage);
+          box(i, ring + st * kStage, full0 + st * 8);
           if (++st == kStages) st = 0, ph ^= 1;
           last = used + i + 1;
         }
@@ -326,15 +327,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto load = [&](int slot, int g0, int g1, int col0, int col1) {
       ok = __all_sync(0xffffffffu, ready(stage, phase, used));
       if (!ok) return;
-      const uint32_t bar = smem_u32(&sh->full[stage]), dst = ring + stage * kStage;
-      if (lane == 0) mbar_expect_tx(bar, kStage);
+      const uint32_t bar = full0 + stage * 8, dst = ring + stage * kStage;
+      if (rank == 0 && lane == 0) mbar_expect_tx(smem_u32(&sh->full[stage]), 2 * kStage);
       __syncwarp();
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         const int g = u ? g1 : g0, y = sh->row[slot][g], n = y >= 0 ? 1 : sh->boxes[slot][g];
         for (int i = lane; i < n; i += 32) {
           const int2 b = y >= 0 ? make_int2(y, 6) : boxes[(slot * 4 + g) * 64 + i];
-          tma_load_2d(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
+          tma_load_2d_pair(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
         }
       }
       __syncwarp();
@@ -347,10 +348,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (s.tiles == 0) continue;
       if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
       if (elect_one()) {
-        const uint32_t bar = smem_u32(&sh->q_full);
-        mbar_expect_tx(bar, kQBytes);
+        if (rank == 0) mbar_expect_tx(smem_u32(&sh->q_full), 2 * kQBytes);
+        const uint32_t bar = cluster_addr(smem_u32(&sh->q_full), 0);
         for (int c = 0; c < 9; ++c)
-          tma_load_2d(smem_u32(smem + kSmemQ) + c * 8192, &q_map, bar, c * 64, s.row0 + 64 * static_cast<int>(rank));
+          tma_load_2d_pair(smem_u32(smem + kSmemQ) + c * 8192, &q_map, bar, c * 64, s.row0 + 64 * static_cast<int>(rank));
       }
       __syncwarp();
       ++segments;
@@ -362,8 +363,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int y0 = sh->row[slot][2 * rank], y1 = sh->row[slot][2 * rank + 1];
           if ((y0 | y1) >= 0) {
             load_whole(9, [&](int c, uint32_t dst, uint32_t bar) {
-              tma_load_2d(dst, &maps.box[6], bar, c * 64, y0);
-              tma_load_2d(dst + 8192, &maps.box[6], bar, c * 64, y1);
+              tma_load_2d_pair(dst, &maps.box[6], bar, c * 64, y0);
+              tma_load_2d_pair(dst + 8192, &maps.box[6], bar, c * 64, y1);
             });
           } else {
 #pragma unroll 1
@@ -377,8 +378,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_whole(8, [&](int i, uint32_t dst, uint32_t bar) {
               const int g = i >> 1, col = 256 * (i & 1) + vcol;
               const int row = g == 0 ? y.x : g == 1 ? y.y : g == 2 ? y.z : y.w;
-              tma_load_2d(dst, &maps.box[6], bar, col, row);
-              tma_load_2d(dst + 8192, &maps.box[6], bar, col + 64, row);
+              tma_load_2d_pair(dst, &maps.box[6], bar, col, row);
+              tma_load_2d_pair(dst + 8192, &maps.box[6], bar, col + 64, row);
             });
           } else {
 #pragma unroll 1
@@ -402,23 +403,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = mbar_wait(smem_u32(&sh->empty[u % kStages]), (u / kStages) & 1, status, abort_flag);
       }
       if (segments > 0) ok = ok && mbar_wait(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag);
-      if (!ok) {      // (CTA 0's words of CTA 1 may be missing: a short limit)
-        for (uint32_t i = 0; i < n; ++i) {
-          const uint32_t u = used - 1 - i;
-          mbar_wait(smem_u32(&sh->full[u % kStages]), (u / kStages) & 1, status, &never, 10000000ull);
+      if (!ok) {      // loads that nobody waits for land long before this ends
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
         }
-        if (segments > 0) mbar_wait(smem_u32(&sh->q_full), (segments - 1) & 1, status, &never, 10000000ull);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {
-      Walk w = walk_start(p, piece, total, pieces);
-      Segment s;
-      uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
-      bool ok = true;
       if (rank == 0) {
+        Walk w = walk_start(p, piece, total, pieces);
+        Segment s;
+        uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
+        bool ok = true;
         const uint32_t sq = smem_u32(smem + kSmemQ), sp = smem_u32(smem + kSmemP);
         auto take = [&]() {
           ok = ok && mbar_wait(smem_u32(&sh->full[stage]), phase, status, abort_flag);
@@ -473,22 +472,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // The last arrival of this CTA's commits in either CTA.
         tc_commit_pair(smem_u32(&sh->drain), 3);
-      } else {
-        // CTA 1's loads have landed: a word to CTA 0, in the order of use.
-        uint32_t bars[kStages];
-        for (int i = 0; i < kStages; ++i) bars[i] = cluster_addr(smem_u32(&sh->full[i]), 0);
-        const uint32_t q_bar = cluster_addr(smem_u32(&sh->q_full), 0);
-        while (ok && walk_next(p, w, s)) {
-          if (s.tiles == 0) continue;
-          if (!(ok = mbar_wait(smem_u32(&sh->q_full), segments & 1, status, abort_flag))) break;
-          mbar_arrive_cluster(q_bar);
-          ++segments;
-          for (int i = 0; i < 17 * s.tiles && ok; ++i) {
-            if (!(ok = mbar_wait(smem_u32(&sh->full[stage]), phase, status, abort_flag))) break;
-            mbar_arrive_cluster(cluster_addr(smem_u32(&sh->full[stage]), 0));
-            if (++stage == kStages) stage = 0, phase ^= 1;
-          }
-        }
       }
       mbar_wait(smem_u32(&sh->drain), 0, status, &never);
     }
