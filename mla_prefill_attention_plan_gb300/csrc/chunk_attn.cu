@@ -28,8 +28,13 @@
 // of a tile for S, latent columns 128r.. of each 256 for O), so each CTA reads
 // 147 KB and 131 KB a tile.
 //
-// The batch's (row tile, key tile) units lie on one line, cut into equal pieces,
-// one for each pair.  A row tile that a cut splits leaves (O, max, sum) in
+// Who does what, found on the device from the lengths: the row tiles of a
+// sequence, two by two, are items that two pairs work at side by side (class
+// 0), a last odd one is an item of a single pair (class 1).  Of each class,
+// workers first take whole items in turn, so that the 76 pairs are at the same
+// few sequences at any time and HBM is read once or twice, not once a row tile;
+// what is left is a line of key tiles that is cut so that all workers end
+// with the same load.  A row tile that a cut splits leaves (O, max, sum) in
 // fp32, which the merge joins; all others are finished by their pair.
 #include <algorithm>
 
@@ -62,7 +67,7 @@ constexpr int kThreads = 224;                // producer, MMA, 4 softmax warps, 
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
-constexpr int kMaxPieces = 76;               // SM pairs
+constexpr int kMaxPairs = 76;                // SM pairs
 
 // Boxes of 1, 2, .. 64 rows x 64 columns of the cache: a run of rows that ends
 // anywhere is a few of them.
@@ -83,9 +88,21 @@ struct ChunkSmem {
 };
 static_assert(sizeof(ChunkSmem) <= 512, "barrier block");
 
-// A split row tile, noted by the piece in which it ends.
+// A split row tile, noted by the worker in whose part of the line it ends.
 struct SplitTile {
-  int row0, rows, first_piece, first_slot, seq;
+  int row0, rows, seq;
+  int first, slot;      // the worker in whose part it begins, and its slot there
+};
+
+// Items of class c have workers(c) workers: groups of two pairs, or pairs.
+__host__ __device__ constexpr int workers_of(int pairs, int c) { return c == 0 ? pairs / 2 : pairs; }
+struct Schedule {
+  int whole[2];                          // items that each worker takes whole, in turn
+  int tail[2][kMaxPairs + 1];            // then [tail[w], tail[w + 1]) of the class's line of key tiles
+};
+// Before sequence b: items and key tiles of them, of class 0 and 1.
+struct Base {
+  int items[2], units[2];
 };
 
 struct ChunkParams {
@@ -94,12 +111,13 @@ struct ChunkParams {
   const int32_t* page_table;
   const uint32_t* mask;
   const float* sink;
-  const int32_t* base;       // [B + 1] units before sequence b
+  const Base* base;          // [B + 1]
+  const Schedule* schedule;
   __nv_bfloat16* o_lat;      // [R][2][512]
   float* lse;                // [R] or null
-  float* o_part;             // [2 pieces][128][512]
-  float2* ml_part;           // [2 pieces][128] (max, sum)
-  SplitTile* split;          // [pieces]
+  float* o_part;             // [4 pairs][128][512]: a pair's first and last segment of each line
+  float2* ml_part;           // [4 pairs][128] (max, sum)
+  SplitTile* split;          // [2][pairs]
   int num_pages, page_size, max_pages, cache_rows;
   int B, H, words;
   float scale_log2;
@@ -107,127 +125,217 @@ struct ChunkParams {
 };
 
 // ------------------------------------------------------------------ plan
-// Units of every sequence and their prefix sums, and each token's sequence.
-// A sequence is left out (no units, no tokens) if its rows are not there.
+// Items of every sequence, their prefix sums, the workers' shares, and each
+// token's sequence.  A sequence is left out (no items, no tokens) if its rows
+// are not there.
 struct PlanArgs {
   const uint32_t* iro;
   const uint32_t* cache_len;
-  int32_t* base;
+  Base* base;
+  Schedule* schedule;
   int32_t* token_seq;
-  int B, H, T, words, max_pages, page_size;
-  bool masked;
   SplitTile* split;
-  int pieces;
+  int B, H, T, words, pairs;
+  bool masked;
   int32_t* status;
 };
 constexpr int kPlanThreads = 1024;
 
+// The sequence of item (or unit) i of class c: the last one with base <= i.
+template <bool UNITS>
+__device__ __forceinline__ int sequence_of(const Base* base, int B, int c, int i) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((UNITS ? base[mid].units[c] : base[mid].items[c]) <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PlanArgs a) {
-  __shared__ long long warp_sum[32];
-  __shared__ int bad;
+  __shared__ int4 warp_sum[32];
+  __shared__ int bad, whole[2], rest[2][kMaxPairs];
   pdl_enter();
   if (timed_out_before(a.status)) return;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) bad = a.iro[0] != 0;
+  if (t == 0) {
+    bad = a.iro[0] != 0;
+    whole[0] = whole[1] = 0x7FFFFFFF;
+  }
   __syncthreads();
   for (int b = t; b < a.B; b += kPlanThreads)
     if (a.iro[b + 1] < a.iro[b]) bad = 1;
   for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
-  if (t < a.pieces) a.split[t].rows = 0;
+  for (int i = t; i < 2 * a.pairs; i += kPlanThreads) a.split[i].rows = 0;
   __syncthreads();
   const bool all_bad = bad;
   if (all_bad && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
-  long long before = 0;
+  int4 before = make_int4(0, 0, 0, 0);          // items of class 0 and 1, units of class 0 and 1
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + t;
-    long long units = 0;
+    int4 own = make_int4(0, 0, 0, 0);
     if (b < a.B && !all_bad) {
       const uint32_t q0 = a.iro[b], q1 = a.iro[b + 1];
       const long long n = q1 - q0, L = static_cast<long long>(a.cache_len[b]) + n;
       if (q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
         set_status(a.status, MLA_DEV_BAD_OFFSETS);
       } else if (n > 0) {
-        units = (n * a.H + kRows - 1) / kRows * ((L + kTile - 1) / kTile);
+        const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
+        own.x = static_cast<int>(tiles / 2);
+        own.y = static_cast<int>(tiles & 1);
+        // (2^31 units would be a day's work; positions saturate, see below.)
+        own.z = static_cast<int>(min(tiles / 2 * kt, 0x7FFFFFFFll));
+        own.w = own.y ? static_cast<int>(kt) : 0;
       }
     }
-    long long s = units;
+    // Sums that would not fit stay at the largest number.
+    auto add = [](int x, int y) { return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), 0x7FFFFFFFu)); };
+    int4 s = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += o;
+      const int x = __shfl_up_sync(0xffffffffu, s.x, d), y = __shfl_up_sync(0xffffffffu, s.y, d);
+      const int z = __shfl_up_sync(0xffffffffu, s.z, d), w = __shfl_up_sync(0xffffffffu, s.w, d);
+      if (lane >= d) s.x += x, s.y += y, s.z = add(s.z, z), s.w = add(s.w, w);
     }
     if (lane == 31) warp_sum[warp] = s;
     __syncthreads();
-    long long off = before, total = 0;
+    int4 off = before;
     for (int w = 0; w < 32; ++w) {
-      if (w < warp) off += warp_sum[w];
-      total += warp_sum[w];
+      const int4 v = warp_sum[w];
+      if (w < warp) off.x += v.x, off.y += v.y, off.z = add(off.z, v.z), off.w = add(off.w, v.w);
+      before.x += v.x, before.y += v.y, before.z = add(before.z, v.z), before.w = add(before.w, v.w);
     }
     if (b < a.B) {
-      // What lies past 2^31 units is left out: no piece reaches it.
-      const long long at = off + s - units;
-      const bool fits = off + s < (1ll << 31);
-      if (!fits && units > 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
-      a.base[b] = static_cast<int>(min(at, (1ll << 31) - 1));
-      if (b == a.B - 1) a.base[a.B] = static_cast<int>(min(off + s, (1ll << 31) - 1));
+      const int4 upto = make_int4(off.x + s.x, off.y + s.y, add(off.z, s.z), add(off.w, s.w));
+      Base v;
+      v.items[0] = upto.x, v.items[1] = upto.y, v.units[0] = upto.z, v.units[1] = upto.w;
+      a.base[b + 1] = v;
     }
-    before += total;
     __syncthreads();
   }
+  if (t == 0) a.base[0] = Base{};
+  const bool over = before.z == 0x7FFFFFFF || before.w == 0x7FFFFFFF;
+  if (over && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
   __syncthreads();
+  // Threads 0 .. and 128 .. are the workers of class 0 and 1.
+  const int c = t >> 7, w = t & 127;
+  const int n = c < 2 ? workers_of(a.pairs, c) : 0;
+  const bool worker = c < 2 && w < n;
+  const int items = c == 0 ? before.x : before.y, units = over ? 0 : c == 0 ? before.z : before.w;
+  auto length = [&](int item) {
+    const int b = sequence_of<false>(a.base, a.B, c, item);
+    return (a.base[b + 1].units[c] - a.base[b].units[c]) / (a.base[b + 1].items[c] - a.base[b].items[c]);
+  };
+  int mine = 0;
+  if (worker) {
+    // Whole items, as many as no worker is overloaded by.
+    int load = 0, k = 0;
+    for (; !over && w + static_cast<long long>(k) * n < items; ++k) {
+      load += length(w + k * n);
+      if (load > units / n) break;
+    }
+    atomicMin(&whole[c], k);
+  }
+  __syncthreads();
+  if (worker) {
+    for (int k = 0; k < whole[c]; ++k) mine += length(w + k * n);
+    const long long total = units;
+    mine = static_cast<int>(total * (w + 1) / n - total * w / n) - mine;
+    rest[c][w] = mine;
+    if (w == 0) a.schedule->whole[c] = whole[c];
+  }
+  __syncthreads();
+  if (worker) {
+    const int first = whole[c] * n;                 // the first item on the line
+    int at = units;
+    if (first < items && !over) {
+      const int b = sequence_of<false>(a.base, a.B, c, first);
+      at = a.base[b].units[c] + (first - a.base[b].items[c]) * length(first);
+    }
+    for (int v = 0; v < w; ++v) at += rest[c][v];
+    a.schedule->tail[c][w] = at;
+    if (w == n - 1) a.schedule->tail[c][n] = at + mine;
+  }
+  if (over) return;                                 // nobody has work: no token has a result
   for (int b = warp; b < a.B; b += kPlanThreads / 32) {
-    if (a.base[b + 1] == a.base[b]) continue;
+    const Base v0 = a.base[b], v1 = a.base[b + 1];
+    if (v0.items[0] == v1.items[0] && v0.items[1] == v1.items[1]) continue;
     for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
   }
 }
 
-// ------------------------------------------------------------------ the line
+// ------------------------------------------------------------------ segments
 struct Segment {
   int b, row0, r0, rows;      // sequence, first global row, first row within the sequence, valid rows
   int k0, k1, kt;             // key tiles [k0, k1) of the row tile's kt
   int tiles;                  // of them, those that a row sees any key of
   int cached, n, L;
+  int c, x;                   // class; the position of k0 on the class's line (-1: a whole item taken in turn)
 };
 struct Walk {
-  int x, x1, b;
+  int c, pair, pairs, b;
+  int item, left;             // whole items: the next one, how many more
+  int x, x1;                  // this worker's part of the line
+  bool begun;
 };
 
-// The units of piece i are [piece_start(i), piece_start(i + 1)), at least one.
-__device__ __forceinline__ int piece_start(int total, int pieces, int i) {
-  return static_cast<int>(static_cast<long long>(total) * i / pieces);
-}
-
-__device__ __forceinline__ Walk walk_start(const ChunkParams& p, int piece, int total, int pieces) {
+__device__ __forceinline__ Walk walk_start(int pair, int pairs) {
   Walk w;
-  w.x = w.x1 = w.b = 0;
-  if (piece >= pieces) return w;
-  w.x = piece_start(total, pieces, piece);
-  w.x1 = piece_start(total, pieces, piece + 1);
-  int lo = 0, hi = p.B;       // the last sequence with base <= x
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.base[mid] <= w.x) lo = mid;
-    else hi = mid;
-  }
-  w.b = lo;
+  w.c = -1;
+  w.pair = pair;
+  w.pairs = pairs;
+  w.left = w.x = w.x1 = w.item = w.b = 0;
+  w.begun = false;
   return w;
 }
 
 __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment& s) {
-  if (w.x >= w.x1) return false;
-  while (p.base[w.b + 1] <= w.x) ++w.b;
+  while (w.left == 0 && w.x >= w.x1) {
+    if (w.c == 1) return false;
+    ++w.c;
+    const int worker = w.c == 0 ? w.pair >> 1 : w.pair;
+    if (worker >= workers_of(w.pairs, w.c)) continue;
+    w.item = worker;
+    w.left = p.schedule->whole[w.c];
+    w.x = p.schedule->tail[w.c][worker];
+    w.x1 = p.schedule->tail[w.c][worker + 1];
+    w.begun = false;
+  }
+  const int c = w.c;
+  int i;                       // item within the sequence
+  if (w.left > 0) {
+    w.b = sequence_of<false>(p.base, p.B, c, w.item);
+    i = w.item - p.base[w.b].items[c];
+    w.item += workers_of(w.pairs, c);
+    --w.left;
+  } else {
+    if (!w.begun) w.b = sequence_of<true>(p.base, p.B, c, w.x);
+    w.begun = true;
+    while (p.base[w.b + 1].units[c] <= w.x) ++w.b;
+    i = -1;
+  }
+  s.c = c;
   s.b = w.b;
   const int q0 = static_cast<int>(p.iro[w.b]);
   s.n = static_cast<int>(p.iro[w.b + 1]) - q0;
   s.cached = static_cast<int>(p.cache_len[w.b]);
   s.L = s.cached + s.n;
   s.kt = (s.L + kTile - 1) / kTile;
-  const int off = w.x - p.base[w.b];
-  const int m = off / s.kt;
-  s.k0 = off - m * s.kt;
-  s.k1 = static_cast<int>(min(static_cast<long long>(s.kt), static_cast<long long>(s.k0) + (w.x1 - w.x)));
-  w.x += s.k1 - s.k0;
+  if (i >= 0) {
+    s.k0 = 0;
+    s.k1 = s.kt;
+    s.x = -1;
+  } else {
+    const int off = w.x - p.base[w.b].units[c];
+    i = off / s.kt;
+    s.k0 = off - i * s.kt;
+    s.k1 = static_cast<int>(min(static_cast<long long>(s.kt), static_cast<long long>(s.k0) + (w.x1 - w.x)));
+    s.x = w.x;
+    w.x += s.k1 - s.k0;
+  }
   const long long rows = static_cast<long long>(s.n) * p.H;
+  const int m = c == 0 ? 2 * i + (w.pair & 1) : static_cast<int>((rows - 1) / kRows);
   s.r0 = m * kRows;
   s.rows = static_cast<int>(min(static_cast<long long>(kRows), rows - s.r0));
   s.row0 = static_cast<int>(static_cast<long long>(q0) * p.H + s.r0);
@@ -248,8 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   int32_t* const status = p.status;
   pdl_enter();
-  const int total = p.base[p.B];                 // units of the line
-  const int piece = blockIdx.x >> 1, pieces = min(static_cast<int>(gridDim.x >> 1), total);
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -290,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 0) {
     // ---------------------------------------------------------------- producer
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(p, piece, total, pieces);
+    Walk w = walk_start(pair, pairs);
     Segment s;
     uint32_t stage = 0, phase = 0, segments = 0, used = 0, last = 0, tile = 0;
     bool ok = true;
@@ -414,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {
       if (rank == 0) {
-        Walk w = walk_start(p, piece, total, pieces);
+        Walk w = walk_start(pair, pairs);
         Segment s;
         uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
         bool ok = true;
@@ -485,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a page, are boxes behind the cache's end, which read as zeros: no row that
     // nobody has written reaches a product.
     int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(p, piece, total, pieces);
+    Walk w = walk_start(pair, pairs);
     Segment s;
     uint32_t tile = 0;
     bool ok = true;
@@ -553,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][128]
     const uint32_t sp = smem_u32(smem + kSmemP);
     const uint32_t p_bar = cluster_addr(smem_u32(&sh->p_full), 0);
-    Walk w = walk_start(p, piece, total, pieces);
+    Walk w = walk_start(pair, pairs);
     Segment s;
     uint32_t tile = 0, swaps = 0;
     bool ok = true;
@@ -709,9 +816,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        // Slots of a piece: its first segment, its last one.
-        const bool leads = w.x - (s.k1 - s.k0) == piece_start(total, pieces, piece);
-        const int slot = 2 * piece + (leads ? 0 : 1);
+        const int worker = s.c == 0 ? pair >> 1 : pair;
+        const int* const tail = p.schedule->tail[s.c];
+        const int slot = 4 * pair + 2 * s.c + (s.x == tail[worker] ? 0 : 1);
         if (half == 0) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
         if (s.tiles > 0) {
           float* dst = p.o_part + (static_cast<size_t>(slot) * kRows + local) * 512 + half * 128;
@@ -728,19 +835,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (ends && tl == 0 && rank == 0) {
-          // The unit at which the row tile begins, the piece that holds it, and
-          // whether it is that piece's first.
-          const int x0 = w.x - s.kt;
-          int fp = static_cast<int>(static_cast<long long>(x0) * pieces / total);
-          while (piece_start(total, pieces, fp) > x0) --fp;
-          while (piece_start(total, pieces, fp + 1) <= x0) ++fp;
+          // The worker in whose part of the line the row tile begins.
+          const int x0 = s.x - s.k0;
+          int first = worker;
+          while (tail[first] > x0) --first;
           SplitTile t;
           t.row0 = s.row0;
           t.rows = s.rows;
-          t.first_piece = fp;
-          t.first_slot = 2 * fp + (piece_start(total, pieces, fp) == x0 ? 0 : 1);
           t.seq = s.b;
-          p.split[piece] = t;
+          t.first = first;
+          t.slot = tail[first] == x0 ? 0 : 1;
+          p.split[s.c * pairs + pair] = t;
         }
       }
       tc_fence_before();
@@ -756,27 +861,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Split row tiles: blockIdx.x is the piece in which one ends, blockIdx.y a
-// slice of its rows; a warp takes a row at a time.
+// Split row tiles: blockIdx.x is the (class, pair) in whose part one ends,
+// blockIdx.y a slice of its rows; a warp takes a row at a time.
 constexpr int kMergeSlices = 8, kMergeWarps = 8;
 
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pieces) {
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pairs) {
   pdl_enter();
   if (timed_out_before(p.status)) return;
-  const int piece = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const SplitTile t = p.split[piece];
+  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SplitTile t = p.split[blockIdx.x];
   if (t.rows <= 0) return;
+  const int worker = c == 0 ? pair >> 1 : pair;
+  const int* const tail = p.schedule->tail[c];
+  // Worker q's slot of this row tile, or -1 (an empty part of the line).
+  auto slot_of = [&](int q) {
+    if (tail[q] == tail[q + 1]) return -1;
+    return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
+  };
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
   for (int r = blockIdx.y * kMergeWarps + warp; r < t.rows; r += kMergeSlices * kMergeWarps) {
     float top = sink;
-    for (int q = t.first_piece; q <= piece; ++q) {
-      const int slot = q == t.first_piece ? t.first_slot : 2 * q;
-      top = fmaxf(top, p.ml_part[slot * kRows + r].x);
+    for (int q = t.first; q <= worker; ++q) {
+      const int slot = slot_of(q);
+      if (slot >= 0) top = fmaxf(top, p.ml_part[slot * kRows + r].x);
     }
     float sum = sink == kNegInf ? 0.0f : ex2(sink - top);
     float4 o[4] = {};
-    for (int q = t.first_piece; q <= piece; ++q) {
-      const int slot = q == t.first_piece ? t.first_slot : 2 * q;
+    for (int q = t.first; q <= worker; ++q) {
+      const int slot = slot_of(q);
+      if (slot < 0) continue;
       const float2 ml = p.ml_part[slot * kRows + r];
       if (ml.y == 0.0f) continue;      // (the segment saw nothing; it may have stored no rows)
       const float f = ex2(ml.x - top);
@@ -808,7 +921,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 }
 
 struct Layout {
-  size_t q_full, o_lat, base, token_seq, o_part, ml_part, split, total;
+  size_t q_full, o_lat, base, schedule, token_seq, o_part, ml_part, split, total;
 };
 Layout layout(int B, int H, int T) {
   const size_t R = static_cast<size_t>(T) * H;
@@ -821,11 +934,12 @@ Layout layout(int B, int H, int T) {
   };
   L.q_full = take(R * 1152);
   L.o_lat = take(R * 2048);
-  L.base = take(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+  L.base = take(sizeof(Base) * (static_cast<size_t>(B) + 1));
+  L.schedule = take(sizeof(Schedule));
   L.token_seq = take(sizeof(int32_t) * static_cast<size_t>(T));
-  L.o_part = take(static_cast<size_t>(2 * kMaxPieces) * kRows * 512 * sizeof(float));
-  L.ml_part = take(static_cast<size_t>(2 * kMaxPieces) * kRows * sizeof(float2));
-  L.split = take(kMaxPieces * sizeof(SplitTile));
+  L.o_part = take(static_cast<size_t>(4 * kMaxPairs) * kRows * 512 * sizeof(float));
+  L.ml_part = take(static_cast<size_t>(4 * kMaxPairs) * kRows * sizeof(float2));
+  L.split = take(2 * kMaxPairs * sizeof(SplitTile));
   L.total = off;
   return L;
 }
@@ -840,7 +954,7 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   const Layout L = layout(a.B, a.H, a.T);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   __nv_bfloat16* q_full = reinterpret_cast<__nv_bfloat16*>(ws + L.q_full);
-  const int pieces = std::max(1, std::min(kMaxPieces, sm_count() / 2));
+  const int pairs = std::max(2, std::min(kMaxPairs, sm_count() / 2));
 
   ChunkParams p;
   p.iro = a.iro;
@@ -848,7 +962,8 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.page_table = a.page_table;
   p.mask = a.mask;
   p.sink = a.sink;
-  p.base = reinterpret_cast<int32_t*>(ws + L.base);
+  p.base = reinterpret_cast<const Base*>(ws + L.base);
+  p.schedule = reinterpret_cast<const Schedule*>(ws + L.schedule);
   p.o_lat = reinterpret_cast<__nv_bfloat16*>(ws + L.o_lat);
   p.lse = a.lse;
   p.o_part = reinterpret_cast<float*>(ws + L.o_part);
@@ -877,26 +992,25 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   PlanArgs pa;
   pa.iro = a.iro;
   pa.cache_len = a.cache_len;
-  pa.base = reinterpret_cast<int32_t*>(ws + L.base);
+  pa.base = reinterpret_cast<Base*>(ws + L.base);
+  pa.schedule = reinterpret_cast<Schedule*>(ws + L.schedule);
   pa.token_seq = reinterpret_cast<int32_t*>(ws + L.token_seq);
   pa.B = a.B;
   pa.H = a.H;
   pa.T = a.T;
   pa.words = a.mask_words;
-  pa.max_pages = a.max_pages;
-  pa.page_size = a.page_size;
   pa.masked = a.mask != nullptr;
   pa.split = p.split;
-  pa.pieces = pieces;
+  pa.pairs = pairs;
   pa.status = a.status;
   if ((e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pa)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) !=
       cudaSuccess)
     return e;
-  if ((e = launch_pdl(chunk_attn_kernel, dim3(2 * pieces), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
+  if ((e = launch_pdl(chunk_attn_kernel, dim3(2 * pairs), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
       cudaSuccess)
     return e;
-  if ((e = launch_pdl(chunk_merge_kernel, dim3(pieces, kMergeSlices), dim3(kMergeWarps * 32), 0, stream, p, pieces)) !=
+  if ((e = launch_pdl(chunk_merge_kernel, dim3(2 * pairs, kMergeSlices), dim3(kMergeWarps * 32), 0, stream, p, pairs)) !=
       cudaSuccess)
     return e;
   return launch_project_outputs(p.o_lat, true, a.w_uv, a.out, a.T, a.H, pa.token_seq, a.status, stream);
