@@ -63,16 +63,16 @@ constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // row maxima and 
 constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
 constexpr int kSmemTotal = kSmemBar + 512 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
-constexpr int kThreads = 224;                // producer, MMA, 4 softmax warps, row lookup
+constexpr int kThreads = 256;                // producer, MMA, 4 softmax warps, row lookup, producer
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
 constexpr int kMaxPairs = 76;                // SM pairs
 
-// Boxes of 1, 2, .. 64 rows x 64 columns of the cache: a run of rows that ends
-// anywhere is a few of them.
+// Boxes of 1, 2, .. 128 rows x 64 columns of the cache: a run of rows that ends
+// anywhere is a few of them.  wide: 64 rows x 2 blocks of 64 columns.
 struct CacheMaps {
-  CUtensorMap box[7];
+  CUtensorMap box[8], wide;
 };
 
 struct ChunkSmem {
@@ -372,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh->drain), 1);
     for (int s = 0; s < kFound; ++s) {
       mbar_init(smem_u32(&sh->found[s]), 1);
-      mbar_init(smem_u32(&sh->taken[s]), 1);
+      mbar_init(smem_u32(&sh->taken[s]), 2);
     }
     mbar_init(smem_u32(&sh->swapped[0]), 2);
     mbar_init(smem_u32(&sh->swapped[1]), 2);
@@ -394,12 +394,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (stop) {
     // (the barriers below are passed by all)
-  } else if (warp == 0) {
-    // ---------------------------------------------------------------- producer
+  } else if (warp == 0 || warp == 7) {
+    // ---------------------------------------------------------------- producers
+    // Two warps, each every other stage: one lane's loop takes about 60 clk an
+    // operation and 200 a stage, too slow for the 256 clk of a stage's MMAs.
+    const uint32_t odd = warp == 7;
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
     Walk w = walk_start(pair, pairs);
     Segment s;
-    uint32_t stage = 0, phase = 0, segments = 0, used = 0, last = 0, tile = 0;
+    uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
     bool ok = true;
     // Both CTAs' loads count at CTA 0's barriers, whose MMAs wait for them.
     const uint32_t full0 = cluster_addr(smem_u32(&sh->full[0]), 0);
@@ -412,49 +415,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       stage += n;
       while (stage >= kStages) stage -= kStages, phase ^= 1;
     };
-    // n stages of two boxes each that lie whole in the cache, issued by one lane
-    // (what the loop costs for each stage is what bounds the loads: with a warp's
-    // votes and the rows read for each stage, 495 clk).
-    auto load_whole = [&](uint32_t n, auto box) {
+    // n stages, issued by one lane (what the loop costs for each stage bounds the
+    // loads: with a warp's votes and the rows read for each stage, 495 clk).
+    auto load = [&](uint32_t n, auto boxes_of) {
       if (elect_one()) {
         uint32_t st = stage, ph = phase;
-        for (uint32_t i = 0; i < n; ++i) {
+        uint32_t i = (used ^ odd) & 1;
+        if (i && ++st == kStages) st = 0, ph ^= 1;
+        for (; i < n; i += 2) {
           if (!(ok = ready(st, ph, used + i))) break;
           if (rank == 0) mbar_expect_tx(smem_u32(&sh->full[st]), 2 * kStage);
-          box(i, ring + st * kStage, full0 + st * 8);
-          if (++st == kStages) st = 0, ph ^= 1;
-          last = used + i + 1;
+          boxes_of(i, ring + st * kStage, full0 + st * 8);
+          if ((st += 2) >= kStages) st -= kStages, ph ^= 1;
         }
       }
       __syncwarp();
       ok = __all_sync(0xffffffffu, ok);
-      advance(n);
+      used += n;
+      stage += n;
+      while (stage >= kStages) stage -= kStages, phase ^= 1;
     };
-    // One stage of two groups of 64 rows x 64 columns, any boxes.
-    auto load = [&](int slot, int g0, int g1, int col0, int col1) {
-      ok = __all_sync(0xffffffffu, ready(stage, phase, used));
-      if (!ok) return;
-      const uint32_t bar = full0 + stage * 8, dst = ring + stage * kStage;
-      if (rank == 0 && lane == 0) mbar_expect_tx(smem_u32(&sh->full[stage]), 2 * kStage);
-      __syncwarp();
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        const int g = u ? g1 : g0, y = sh->row[slot][g], n = y >= 0 ? 1 : sh->boxes[slot][g];
-        for (int i = lane; i < n; i += 32) {
-          const int2 b = y >= 0 ? make_int2(y, 6) : boxes[(slot * 4 + g) * 64 + i];
-          tma_load_2d_pair(dst + u * 8192 + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, u ? col1 : col0, b.x);
-        }
+    // The boxes of group g.
+    auto group = [&](int slot, int g, uint32_t dst, uint32_t bar, int col) {
+      const int y = sh->row[slot][g];
+      if (y >= 0) {
+        tma_load_2d_pair(dst, &maps.box[6], bar, col, y);
+        return;
       }
-      __syncwarp();
-      last = used + 1;
-      advance(1);
+      const int n = sh->boxes[slot][g];
+      const int2* const list = boxes + (slot * 4 + g) * 64;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int2 b = list[i];
+        tma_load_2d_pair(dst + (b.y >> 8) * 128, &maps.box[b.y & 255], bar, col, b.x);
+      }
     };
     // K of tile j, V of the tile before, in the order of use.
     const int vcol = 128 * static_cast<int>(rank);
     while (ok && walk_next(p, w, s)) {
       if (s.tiles == 0) continue;
       if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
-      if (elect_one()) {
+      if (!odd && elect_one()) {
         if (rank == 0) mbar_expect_tx(smem_u32(&sh->q_full), 2 * kQBytes);
         const uint32_t bar = cluster_addr(smem_u32(&sh->q_full), 0);
         for (int c = 0; c < 9; ++c)
@@ -468,39 +469,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int slot = (tile + j) % kFound;
           if (!(ok = mbar_wait_warp(smem_u32(&sh->found[slot]), ((tile + j) / kFound) & 1, status, abort_flag))) break;
           const int y0 = sh->row[slot][2 * rank], y1 = sh->row[slot][2 * rank + 1];
-          if ((y0 | y1) >= 0) {
-            load_whole(9, [&](int c, uint32_t dst, uint32_t bar) {
+          if (y0 >= 0 && y1 == y0 + 64) {
+            load(9, [&](int c, uint32_t dst, uint32_t bar) {
+              tma_load_2d_pair(dst, &maps.box[7], bar, c * 64, y0);
+            });
+          } else if ((y0 | y1) >= 0) {
+            load(9, [&](int c, uint32_t dst, uint32_t bar) {
               tma_load_2d_pair(dst, &maps.box[6], bar, c * 64, y0);
               tma_load_2d_pair(dst + 8192, &maps.box[6], bar, c * 64, y1);
             });
           } else {
-#pragma unroll 1
-            for (int c = 0; c < 9 && ok; ++c) load(slot, 2 * rank, 2 * rank + 1, c * 64, c * 64);
+            load(9, [&](int c, uint32_t dst, uint32_t bar) {
+              group(slot, 2 * rank, dst, bar, c * 64);
+              group(slot, 2 * rank + 1, dst + 8192, bar, c * 64);
+            });
           }
         }
         if (j > 0 && ok) {
           const int slot = (tile + j - 1) % kFound;
           const int4 y = *reinterpret_cast<const int4*>(sh->row[slot]);
           if ((y.x | y.y | y.z | y.w) >= 0) {
-            load_whole(8, [&](int i, uint32_t dst, uint32_t bar) {
-              const int g = i >> 1, col = 256 * (i & 1) + vcol;
+            load(8, [&](int i, uint32_t dst, uint32_t bar) {
+              const int g = i >> 1;
               const int row = g == 0 ? y.x : g == 1 ? y.y : g == 2 ? y.z : y.w;
-              tma_load_2d_pair(dst, &maps.box[6], bar, col, row);
-              tma_load_2d_pair(dst + 8192, &maps.box[6], bar, col + 64, row);
+              tma_load_3d_pair(dst, &maps.wide, bar, 0, row, 4 * (i & 1) + 2 * static_cast<int>(rank));
             });
           } else {
-#pragma unroll 1
-            for (int i = 0; i < 8 && ok; ++i) {
+            load(8, [&](int i, uint32_t dst, uint32_t bar) {
               const int col = 256 * (i & 1) + vcol;
-              load(slot, i >> 1, i >> 1, col, col + 64);
-            }
+              group(slot, i >> 1, dst, bar, col);
+              group(slot, i >> 1, dst + 8192, bar, col + 64);
+            });
           }
           if (lane == 0) mbar_arrive(smem_u32(&sh->taken[slot]));
         }
       }
       tile += s.tiles;
     }
-    used = __reduce_max_sync(0xffffffffu, last);      // stages that were loaded
     // Nothing may be on its way into this CTA when it leaves: the loads (if the
     // MMAs did not get to wait for them) and the releases of the stages.
     if (elect_one()) {
@@ -982,8 +987,11 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   CUtensorMap q_map;
   CacheMaps maps;
   if (!encode_2d(&q_map, q_full, bf, 576, R, 1152, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  const uint64_t rows = static_cast<uint64_t>(p.cache_rows);
+  if (!encode_3d(&maps.wide, a.kv_cache, bf, {64, rows, 9}, {1152, 128}, {64, 64, 2}, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   for (int e = 0; e < 8; ++e)
-    if (!encode_2d(&maps.box[e], a.kv_cache, bf, 576, static_cast<uint64_t>(p.cache_rows), 1152, 64, 1u << e,
+    if (!encode_2d(&maps.box[e], a.kv_cache, bf, 576, rows, 1152, 64, 1u << e,
                    CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
 
