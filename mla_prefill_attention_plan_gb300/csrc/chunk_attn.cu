@@ -11,8 +11,8 @@
 // is less work than up-projecting the context: 2176 operations for each (row,
 // key) against 262144 for each (head, key) and 640 for each pair.
 //
-// Launches: the query projection; a plan (one CTA); the attention; a merge; the
-// output projection.
+// Launches: the query projection with the plan in a CTA of its own; the
+// attention; a merge; the output projection.
 //
 // The attention runs on pairs of SMs.  A pair holds 128 query rows (token,
 // head) of one sequence, 64 in each CTA, and walks 256-key tiles: S = Q K^T and
@@ -38,18 +38,18 @@
 // fp32, which the merge joins; all others are finished by their pair.
 #include <algorithm>
 
+#include "chunk_plan.cuh"
 #include "kernels.cuh"
 
 namespace mla {
 namespace {
+using namespace chunk;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescale = 8.0f;             // a row's reference moves when its maximum grows by 2^8
 
-constexpr int kTile = 256;                   // keys of a tile
-constexpr int kRows = 128;                   // query rows of a pair
 constexpr int kStage = 16 * 1024;
 constexpr int kStages = 7;
 constexpr int kQBytes = 9 * 64 * 128;        // 64 rows x 576 columns in blocks of 64
@@ -67,7 +67,6 @@ constexpr int kThreads = 256;                // producer, MMA, 4 softmax warps, 
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
-constexpr int kMaxPairs = 76;                // SM pairs
 
 // Boxes of 1, 2, .. 128 rows x 64 columns of the cache: a run of rows that ends
 // anywhere is a few of them.  wide: 64 rows x 2 blocks of 64 columns.
@@ -88,23 +87,6 @@ struct ChunkSmem {
 };
 static_assert(sizeof(ChunkSmem) <= 512, "barrier block");
 
-// A split row tile, noted by the worker in whose part of the line it ends.
-struct SplitTile {
-  int row0, rows, seq;
-  int first, slot;      // the worker in whose part it begins, and its slot there
-};
-
-// Items of class c have workers(c) workers: groups of two pairs, or pairs.
-__host__ __device__ constexpr int workers_of(int pairs, int c) { return c == 0 ? pairs / 2 : pairs; }
-struct Schedule {
-  int whole[2];                          // items that each worker takes whole, in turn
-  int tail[2][kMaxPairs + 1];            // then [tail[w], tail[w + 1]) of the class's line of key tiles
-};
-// Before sequence b: items and key tiles of them, of class 0 and 1.
-struct Base {
-  int items[2], units[2];
-};
-
 struct ChunkParams {
   const uint32_t* iro;
   const uint32_t* cache_len;
@@ -124,147 +106,6 @@ struct ChunkParams {
   int32_t* status;
 };
 
-// ------------------------------------------------------------------ plan
-// Items of every sequence, their prefix sums, the workers' shares, and each
-// token's sequence.  A sequence is left out (no items, no tokens) if its rows
-// are not there.
-struct PlanArgs {
-  const uint32_t* iro;
-  const uint32_t* cache_len;
-  Base* base;
-  Schedule* schedule;
-  int32_t* token_seq;
-  SplitTile* split;
-  int B, H, T, words, pairs;
-  bool masked;
-  int32_t* status;
-};
-constexpr int kPlanThreads = 1024;
-
-// The sequence of item (or unit) i of class c: the last one with base <= i.
-template <bool UNITS>
-__device__ __forceinline__ int sequence_of(const Base* base, int B, int c, int i) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((UNITS ? base[mid].units[c] : base[mid].items[c]) <= i) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PlanArgs a) {
-  __shared__ int4 warp_sum[32];
-  __shared__ int bad, whole[2], rest[2][kMaxPairs];
-  pdl_enter();
-  if (timed_out_before(a.status)) return;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) {
-    bad = a.iro[0] != 0;
-    whole[0] = whole[1] = 0x7FFFFFFF;
-  }
-  __syncthreads();
-  for (int b = t; b < a.B; b += kPlanThreads)
-    if (a.iro[b + 1] < a.iro[b]) bad = 1;
-  for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
-  for (int i = t; i < 2 * a.pairs; i += kPlanThreads) a.split[i].rows = 0;
-  __syncthreads();
-  const bool all_bad = bad;
-  if (all_bad && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
-  int4 before = make_int4(0, 0, 0, 0);          // items of class 0 and 1, units of class 0 and 1
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + t;
-    int4 own = make_int4(0, 0, 0, 0);
-    if (b < a.B && !all_bad) {
-      const uint32_t q0 = a.iro[b], q1 = a.iro[b + 1];
-      const long long n = q1 - q0, L = static_cast<long long>(a.cache_len[b]) + n;
-      if (q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
-        set_status(a.status, MLA_DEV_BAD_OFFSETS);
-      } else if (n > 0) {
-        const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
-        own.x = static_cast<int>(tiles / 2);
-        own.y = static_cast<int>(tiles & 1);
-        // (2^31 units would be a day's work; positions saturate, see below.)
-        own.z = static_cast<int>(min(tiles / 2 * kt, 0x7FFFFFFFll));
-        own.w = own.y ? static_cast<int>(kt) : 0;
-      }
-    }
-    // Sums that would not fit stay at the largest number.
-    auto add = [](int x, int y) { return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), 0x7FFFFFFFu)); };
-    int4 s = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, s.x, d), y = __shfl_up_sync(0xffffffffu, s.y, d);
-      const int z = __shfl_up_sync(0xffffffffu, s.z, d), w = __shfl_up_sync(0xffffffffu, s.w, d);
-      if (lane >= d) s.x += x, s.y += y, s.z = add(s.z, z), s.w = add(s.w, w);
-    }
-    if (lane == 31) warp_sum[warp] = s;
-    __syncthreads();
-    int4 off = before;
-    for (int w = 0; w < 32; ++w) {
-      const int4 v = warp_sum[w];
-      if (w < warp) off.x += v.x, off.y += v.y, off.z = add(off.z, v.z), off.w = add(off.w, v.w);
-      before.x += v.x, before.y += v.y, before.z = add(before.z, v.z), before.w = add(before.w, v.w);
-    }
-    if (b < a.B) {
-      const int4 upto = make_int4(off.x + s.x, off.y + s.y, add(off.z, s.z), add(off.w, s.w));
-      Base v;
-      v.items[0] = upto.x, v.items[1] = upto.y, v.units[0] = upto.z, v.units[1] = upto.w;
-      a.base[b + 1] = v;
-    }
-    __syncthreads();
-  }
-  if (t == 0) a.base[0] = Base{};
-  const bool over = before.z == 0x7FFFFFFF || before.w == 0x7FFFFFFF;
-  if (over && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
-  __syncthreads();
-  // Threads 0 .. and 128 .. are the workers of class 0 and 1.
-  const int c = t >> 7, w = t & 127;
-  const int n = c < 2 ? workers_of(a.pairs, c) : 0;
-  const bool worker = c < 2 && w < n;
-  const int items = c == 0 ? before.x : before.y, units = over ? 0 : c == 0 ? before.z : before.w;
-  auto length = [&](int item) {
-    const int b = sequence_of<false>(a.base, a.B, c, item);
-    return (a.base[b + 1].units[c] - a.base[b].units[c]) / (a.base[b + 1].items[c] - a.base[b].items[c]);
-  };
-  int mine = 0;
-  if (worker) {
-    // Whole items, as many as no worker is overloaded by.
-    int load = 0, k = 0;
-    for (; !over && w + static_cast<long long>(k) * n < items; ++k) {
-      load += length(w + k * n);
-      if (load > units / n) break;
-    }
-    atomicMin(&whole[c], k);
-  }
-  __syncthreads();
-  if (worker) {
-    for (int k = 0; k < whole[c]; ++k) mine += length(w + k * n);
-    const long long total = units;
-    mine = static_cast<int>(total * (w + 1) / n - total * w / n) - mine;
-    rest[c][w] = mine;
-    if (w == 0) a.schedule->whole[c] = whole[c];
-  }
-  __syncthreads();
-  if (worker) {
-    const int first = whole[c] * n;                 // the first item on the line
-    int at = units;
-    if (first < items && !over) {
-      const int b = sequence_of<false>(a.base, a.B, c, first);
-      at = a.base[b].units[c] + (first - a.base[b].items[c]) * length(first);
-    }
-    for (int v = 0; v < w; ++v) at += rest[c][v];
-    a.schedule->tail[c][w] = at;
-    if (w == n - 1) a.schedule->tail[c][n] = at + mine;
-  }
-  if (over) return;                                 // nobody has work: no token has a result
-  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
-    const Base v0 = a.base[b], v1 = a.base[b + 1];
-    if (v0.items[0] == v1.items[0] && v0.items[1] == v1.items[1]) continue;
-    for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
-  }
-}
-
 // ------------------------------------------------------------------ segments
 struct Segment {
   int b, row0, r0, rows;      // sequence, first global row, first row within the sequence, valid rows
@@ -274,17 +115,16 @@ struct Segment {
   int c, x;                   // class; the position of k0 on the class's line (-1: a whole item taken in turn)
 };
 struct Walk {
-  int c, pair, pairs, b;
+  int c, pair, b;
   int item, left;             // whole items: the next one, how many more
   int x, x1;                  // this worker's part of the line
   bool begun;
 };
 
-__device__ __forceinline__ Walk walk_start(int pair, int pairs) {
+__device__ __forceinline__ Walk walk_start(int pair) {
   Walk w;
   w.c = -1;
   w.pair = pair;
-  w.pairs = pairs;
   w.left = w.x = w.x1 = w.item = w.b = 0;
   w.begun = false;
   return w;
@@ -295,7 +135,7 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
     if (w.c == 1) return false;
     ++w.c;
     const int worker = w.c == 0 ? w.pair >> 1 : w.pair;
-    if (worker >= workers_of(w.pairs, w.c)) continue;
+    if (worker >= p.schedule->workers[w.c]) continue;
     w.item = worker;
     w.left = p.schedule->whole[w.c];
     w.x = p.schedule->tail[w.c][worker];
@@ -307,7 +147,7 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
   if (w.left > 0) {
     w.b = sequence_of<false>(p.base, p.B, c, w.item);
     i = w.item - p.base[w.b].items[c];
-    w.item += workers_of(w.pairs, c);
+    w.item += p.schedule->workers[c];
     --w.left;
   } else {
     if (!w.begun) w.b = sequence_of<true>(p.base, p.B, c, w.x);
@@ -400,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // operation and 200 a stage, too slow for the 256 clk of a stage's MMAs.
     const uint32_t odd = warp == 7;
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(pair, pairs);
+    Walk w = walk_start(pair);
     Segment s;
     uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
     bool ok = true;
@@ -409,11 +249,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Stage `used`, when its last reader is through with it.
     auto ready = [&](uint32_t st, uint32_t ph, uint32_t n) {
       return n < kStages || mbar_wait(smem_u32(&sh->empty[st]), ph ^ 1, status, abort_flag);
-    };
-    auto advance = [&](uint32_t n) {
-      used += n;
-      stage += n;
-      while (stage >= kStages) stage -= kStages, phase ^= 1;
     };
     // n stages, issued by one lane (what the loop costs for each stage bounds the
     // loads: with a warp's votes and the rows read for each stage, 495 clk).
@@ -526,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {
       if (rank == 0) {
-        Walk w = walk_start(pair, pairs);
+        Walk w = walk_start(pair);
         Segment s;
         uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
         bool ok = true;
@@ -597,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a page, are boxes behind the cache's end, which read as zeros: no row that
     // nobody has written reaches a product.
     int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(pair, pairs);
+    Walk w = walk_start(pair);
     Segment s;
     uint32_t tile = 0;
     bool ok = true;
@@ -665,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][128]
     const uint32_t sp = smem_u32(smem + kSmemP);
     const uint32_t p_bar = cluster_addr(smem_u32(&sh->p_full), 0);
-    Walk w = walk_start(pair, pairs);
+    Walk w = walk_start(pair);
     Segment s;
     uint32_t tile = 0, swaps = 0;
     bool ok = true;
@@ -995,23 +830,22 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
                    CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
 
-  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, a.T, a.H, a.status, stream);
-  if (e != cudaSuccess) return e;
-  PlanArgs pa;
+  ChunkPlanArgs pa;
   pa.iro = a.iro;
   pa.cache_len = a.cache_len;
   pa.base = reinterpret_cast<Base*>(ws + L.base);
   pa.schedule = reinterpret_cast<Schedule*>(ws + L.schedule);
   pa.token_seq = reinterpret_cast<int32_t*>(ws + L.token_seq);
+  pa.split = p.split;
   pa.B = a.B;
   pa.H = a.H;
   pa.T = a.T;
   pa.words = a.mask_words;
-  pa.masked = a.mask != nullptr;
-  pa.split = p.split;
   pa.pairs = pairs;
+  pa.masked = a.mask != nullptr;
   pa.status = a.status;
-  if ((e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pa)) != cudaSuccess) return e;
+  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, a.T, a.H, &pa, a.status, stream);
+  if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) !=
       cudaSuccess)
     return e;

@@ -1,0 +1,175 @@
+// Who does what in chunk attention (chunk_attn.cu), found on the device from the
+// sequences' lengths.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace mla {
+
+namespace chunk {
+constexpr int kTile = 256;                   // keys of a tile
+constexpr int kRows = 128;                   // query rows of a pair of SMs
+constexpr int kMaxPairs = 76;
+
+// A split row tile, noted by the worker in whose part of the line it ends.
+struct SplitTile {
+  int row0, rows, seq;
+  int first, slot;      // the worker in whose part it begins, and its slot there
+};
+
+// Items of class c have workers(c) workers: groups of two pairs, or pairs.
+__host__ __device__ constexpr int workers_of(int pairs, int c) { return c == 0 ? pairs / 2 : pairs; }
+struct Schedule {
+  int workers[2];                        // that have any work
+  int whole[2];                          // items that each worker takes whole, in turn
+  int tail[2][kMaxPairs + 1];            // then [tail[w], tail[w + 1]) of the class's line of key tiles
+};
+// Before sequence b: items and key tiles of them, of class 0 and 1.
+struct Base {
+  int items[2], units[2];
+};
+
+// Items of every sequence, their prefix sums, the workers' shares, and each
+// token's sequence.  A sequence is left out (no items, no tokens) if its rows
+// are not there.
+struct ChunkPlanArgs {
+  const uint32_t* iro;
+  const uint32_t* cache_len;
+  Base* base;
+  Schedule* schedule;
+  int32_t* token_seq;
+  SplitTile* split;
+  int B, H, T, words, pairs;
+  bool masked;
+  int32_t* status;
+};
+
+// The sequence of item (or unit) i of class c: the last one with base <= i.
+template <bool UNITS>
+__device__ __forceinline__ int sequence_of(const Base* base, int B, int c, int i) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((UNITS ? base[mid].units[c] : base[mid].items[c]) <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// By one CTA of kPlanThreads.
+template <int kPlanThreads>
+__device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
+  constexpr int kWarps = kPlanThreads / 32;
+  static_assert(kPlanThreads >= 64 + kMaxPairs, "a thread for each worker");
+  __shared__ int4 warp_sum[kWarps];
+  __shared__ int bad, whole[2], rest[2][kMaxPairs];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) {
+    bad = a.iro[0] != 0;
+    whole[0] = whole[1] = 0x7FFFFFFF;
+  }
+  __syncthreads();
+  for (int b = t; b < a.B; b += kPlanThreads)
+    if (a.iro[b + 1] < a.iro[b]) bad = 1;
+  for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
+  for (int i = t; i < 2 * a.pairs; i += kPlanThreads) a.split[i].rows = 0;
+  __syncthreads();
+  const bool all_bad = bad;
+  if (all_bad && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+  int4 before = make_int4(0, 0, 0, 0);          // items of class 0 and 1, units of class 0 and 1
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + t;
+    int4 own = make_int4(0, 0, 0, 0);
+    if (b < a.B && !all_bad) {
+      const uint32_t q0 = a.iro[b], q1 = a.iro[b + 1];
+      const long long n = q1 - q0, L = static_cast<long long>(a.cache_len[b]) + n;
+      if (q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
+        set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      } else if (n > 0) {
+        const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
+        own.x = static_cast<int>(tiles / 2);
+        own.y = static_cast<int>(tiles & 1);
+        // (2^31 units would be a day's work; positions saturate, see below.)
+        own.z = static_cast<int>(min(tiles / 2 * kt, 0x7FFFFFFFll));
+        own.w = own.y ? static_cast<int>(kt) : 0;
+      }
+    }
+    // Sums that would not fit stay at the largest number.
+    auto add = [](int x, int y) { return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), 0x7FFFFFFFu)); };
+    int4 s = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, s.x, d), y = __shfl_up_sync(0xffffffffu, s.y, d);
+      const int z = __shfl_up_sync(0xffffffffu, s.z, d), w = __shfl_up_sync(0xffffffffu, s.w, d);
+      if (lane >= d) s.x += x, s.y += y, s.z = add(s.z, z), s.w = add(s.w, w);
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    int4 off = before;
+    for (int w = 0; w < kWarps; ++w) {
+      const int4 v = warp_sum[w];
+      if (w < warp) off.x += v.x, off.y += v.y, off.z = add(off.z, v.z), off.w = add(off.w, v.w);
+      before.x += v.x, before.y += v.y, before.z = add(before.z, v.z), before.w = add(before.w, v.w);
+    }
+    if (b < a.B) {
+      const int4 upto = make_int4(off.x + s.x, off.y + s.y, add(off.z, s.z), add(off.w, s.w));
+      Base v;
+      v.items[0] = upto.x, v.items[1] = upto.y, v.units[0] = upto.z, v.units[1] = upto.w;
+      a.base[b + 1] = v;
+    }
+    __syncthreads();
+  }
+  if (t == 0) a.base[0] = Base{};
+  const bool over = before.z == 0x7FFFFFFF || before.w == 0x7FFFFFFF;
+  if (over && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
+  __syncthreads();
+  // Threads 0 .. and 64 .. are the workers of class 0 and 1 (no more of them than
+  // there are units, so that no part of a short line is empty).
+  const int c = t >= 64, w = c ? t - 64 : t;
+  const int items = c == 0 ? before.x : before.y, units = over ? 0 : c == 0 ? before.z : before.w;
+  const int n = max(1, min(workers_of(a.pairs, c), units));
+  const bool worker = w < n;
+  auto length = [&](int item) {
+    const int b = sequence_of<false>(a.base, a.B, c, item);
+    return (a.base[b + 1].units[c] - a.base[b].units[c]) / (a.base[b + 1].items[c] - a.base[b].items[c]);
+  };
+  int mine = 0;
+  if (worker) {
+    // Whole items, as many as no worker is overloaded by.
+    int load = 0, k = 0;
+    for (; !over && w + static_cast<long long>(k) * n < items; ++k) {
+      load += length(w + k * n);
+      if (load > units / n) break;
+    }
+    atomicMin(&whole[c], k);
+  }
+  __syncthreads();
+  if (worker) {
+    for (int k = 0; k < whole[c]; ++k) mine += length(w + k * n);
+    const long long total = units;
+    mine = static_cast<int>(total * (w + 1) / n - total * w / n) - mine;
+    rest[c][w] = mine;
+    if (w == 0) a.schedule->whole[c] = whole[c], a.schedule->workers[c] = n;
+  }
+  __syncthreads();
+  if (worker) {
+    const int first = whole[c] * n;                 // the first item on the line
+    int at = units;
+    if (first < items && !over) {
+      const int b = sequence_of<false>(a.base, a.B, c, first);
+      at = a.base[b].units[c] + (first - a.base[b].items[c]) * length(first);
+    }
+    for (int v = 0; v < w; ++v) at += rest[c][v];
+    a.schedule->tail[c][w] = at;
+    if (w == n - 1) a.schedule->tail[c][n] = at + mine;
+  }
+  if (over) return;                                 // nobody has work: no token has a result
+  for (int b = warp; b < a.B; b += kWarps) {
+    const Base v0 = a.base[b], v1 = a.base[b + 1];
+    if (v0.items[0] == v1.items[0] && v0.items[1] == v1.items[1]) continue;
+    for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
+  }
+}
+
+}  // namespace chunk
+}  // namespace mla

@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "chunk_plan.cuh"
 #include "kernels.cuh"
 
 namespace mla {
@@ -71,12 +72,14 @@ struct HeadGemm {
 
 // SPLIT > 1: the head's N * SPLIT output columns are shared by SPLIT CTAs
 // (grid.y = H * SPLIT), N each, so that a small M still fills the GPU.
-template <int N, int K, int STAGES, int SPLIT, int TERMS>
+// PLAN: one more CTA (the last of grid.y) finds chunk attention's schedule.
+template <int N, int K, int STAGES, int SPLIT, int TERMS, bool PLAN>
 __global__ void __launch_bounds__(192, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                      int a_col0, int a_hstride, __nv_bfloat16* __restrict__ out, long long out_ld,
                      int out_hstride, const __nv_bfloat16* __restrict__ rope_src, long long rope_ld,
-                     int rope_hstride, int M, const int32_t* __restrict__ row_seq, int32_t* status) {
+                     int rope_hstride, int M, const int32_t* __restrict__ row_seq, int32_t* status,
+                     const chunk::ChunkPlanArgs plan) {
   using C = HeadGemm<N, K, STAGES>;
   struct Bars {
     uint64_t full[STAGES], empty[STAGES], done;
@@ -92,6 +95,10 @@ __global__ void __launch_bounds__(192, 1)
   const int m0 = blockIdx.x * 128;
   pdl_enter();
   if (timed_out_before(status)) return;   // an earlier kernel timed out: no work
+  if (PLAN && blockIdx.y == gridDim.y - 1) {
+    if (blockIdx.x == 0) chunk::chunk_plan<192>(plan);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -1053,25 +1060,26 @@ int decode_clusters(int device) {
   return cached[device];
 }
 
-template <int N, int K, int STAGES, int SPLIT = 1, int TERMS = 1>
+template <int N, int K, int STAGES, int SPLIT = 1, int TERMS = 1, bool PLAN = false>
 cudaError_t launch_head_gemm(const CUtensorMap& a_map, const CUtensorMap& b_map, int a_col0, int a_hstride,
                              __nv_bfloat16* out, long long out_ld, int out_hstride, const __nv_bfloat16* rope_src,
                              long long rope_ld, int rope_hstride, int M, int H, const int32_t* row_seq,
-                             int32_t* status, cudaStream_t stream) {
+                             int32_t* status, cudaStream_t stream,
+                             const chunk::ChunkPlanArgs& plan = chunk::ChunkPlanArgs{}) {
   using C = HeadGemm<N, K, STAGES>;
-  cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS>,
+  cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS, PLAN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
   if (e != cudaSuccess) return e;
-  const dim3 grid((M + 127) / 128, H * SPLIT);
-  return launch_pdl(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS>, grid, dim3(192), C::SMEM_TOTAL, stream, a_map,
+  const dim3 grid((M + 127) / 128, H * SPLIT + (PLAN ? 1 : 0));
+  return launch_pdl(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS, PLAN>, grid, dim3(192), C::SMEM_TOTAL, stream, a_map,
                     b_map, a_col0, a_hstride, out, out_ld, out_hstride, rope_src, rope_ld, rope_hstride, M, row_seq,
-                    status);
+                    status, plan);
 }
 
 }  // namespace
 
 cudaError_t launch_project_queries(const void* q, const void* w_uk, __nv_bfloat16* q_full, int T, int H,
-                                   int32_t* status, cudaStream_t stream) {
+                                   const chunk::ChunkPlanArgs* plan, int32_t* status, cudaStream_t stream) {
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qa_map, wuk_map;
   if (!encode_2d(&qa_map, q, bf, static_cast<uint64_t>(H) * 192, T, static_cast<uint64_t>(H) * 384, 64, 128,
@@ -1080,9 +1088,12 @@ cudaError_t launch_project_queries(const void* q, const void* w_uk, __nv_bfloat1
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   // Four CTAs a head, 128 latent columns each: a decode batch has few rows.
-  return launch_head_gemm<128, 128, 2, 4>(qa_map, wuk_map, 0, 192, q_full, static_cast<long long>(H) * 576, 576,
-                                          static_cast<const __nv_bfloat16*>(q) + 128,
-                                          static_cast<long long>(H) * 192, 192, T, H, nullptr, status, stream);
+  const __nv_bfloat16* rope = static_cast<const __nv_bfloat16*>(q) + 128;
+  const long long ld = static_cast<long long>(H) * 576, rope_ld = static_cast<long long>(H) * 192;
+  return plan != nullptr ? launch_head_gemm<128, 128, 2, 4, 1, true>(qa_map, wuk_map, 0, 192, q_full, ld, 576, rope,
+                                                                     rope_ld, 192, T, H, nullptr, status, stream, *plan)
+                         : launch_head_gemm<128, 128, 2, 4>(qa_map, wuk_map, 0, 192, q_full, ld, 576, rope, rope_ld,
+                                                            192, T, H, nullptr, status, stream);
 }
 
 cudaError_t launch_project_outputs(const __nv_bfloat16* o_lat, bool two_terms, const void* w_uv, void* out, int T,
@@ -1149,7 +1160,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
   // 1. q_lat = w_uk[h] q_nope, with the rope part alongside: q_full [T*H, 576].
-  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, T, H, a.status, stream);
+  cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, T, H, nullptr, a.status, stream);
   if (e != cudaSuccess) return e;
 
   // 2. Latent attention over the key partitions.

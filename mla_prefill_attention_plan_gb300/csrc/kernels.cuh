@@ -182,9 +182,13 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // The decode's per-head projections (decode.cu), for other absorbed attentions:
 // q_full [T*H][576] = (w_uk[h] q_nope, q_rope); out[t][h] = w_uv[h] o_lat[t][h]
 // with o_lat [T*H][512], or (two_terms) the sum of [T*H][2][512].  Rows t with
-// row_seq[t] < 0 are not written (row_seq may be null).
+// row_seq[t] < 0 are not written (row_seq may be null).  With plan given, the
+// same launch finds chunk attention's schedule (chunk_plan.cuh).
+namespace chunk {
+struct ChunkPlanArgs;
+}
 cudaError_t launch_project_queries(const void* q, const void* w_uk, __nv_bfloat16* q_full, int T, int H,
-                                   int32_t* status, cudaStream_t stream);
+                                   const chunk::ChunkPlanArgs* plan, int32_t* status, cudaStream_t stream);
 cudaError_t launch_project_outputs(const __nv_bfloat16* o_lat, bool two_terms, const void* w_uv, void* out, int T,
                                    int H, const int32_t* row_seq, int32_t* status, cudaStream_t stream);
 
