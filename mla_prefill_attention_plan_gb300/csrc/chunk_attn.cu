@@ -528,16 +528,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t buf = tile & 1;
         if (!(ok = mbar_wait_warp(smem_u32(&sh->s_full[buf]), (tile >> 1) & 1, status, abort_flag))) break;
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(tmem + lane_off + buf * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
-        tmem_ld_wait();
-        // Keys that the row does not see.
+        // Two passes over the scores, 32 at a time (a tile's 128 unrolled are 20 KB of
+        // code, which a short context fetches from L2 for one use): the maximum,
+        // then the weights.  In a tile that the row does not see all of, the first
+        // pass stores the scores back with -infinity in them.
+        const uint32_t sc = tmem + lane_off + buf * 128;
         const int k0 = (s.k0 + j) * kTile + half * 128;
-        if (k0 + 128 > s.cached) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+        const bool partly = k0 + 128 > s.cached;
+        float top = kNegInf;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          tmem_ld32(sc + c * 32, x);
+          tmem_ld_wait();
+          if (partly) {
             const int i = k0 + c * 32 - s.cached;                     // new token of the first key
             uint32_t see = 0xffffffffu;
             if (i + 32 > 0) {
@@ -556,12 +560,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(see >> e & 1)) x[c * 32 + e] = __float_as_uint(kNegInf);
+              if (!(see >> e & 1)) x[e] = __float_as_uint(kNegInf);
+            tmem_st32(sc + c * 32, x);
           }
-        }
-        float top = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        }
+        if (partly) tmem_st_wait();
         float other;
         if (!(ok = swap(top, other))) break;
         top = fmaxf(top, other) * p.scale_log2;
@@ -588,20 +593,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         }
         const float shift = ref == kNegInf ? 0.0f : ref;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          tmem_ld32(sc + c * 32, x);
+          tmem_ld_wait();
+          // Chunks of 8 keys (16 bytes) of the row, in the 128-byte swizzle.
+          const uint32_t dst = sp + (half * 2 + (c >> 1)) * 8192 + row * 128;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          uint32_t pk[4];
+          for (int u = 0; u < 4; ++u) {
+            uint32_t pk[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = ex2(fmaf(__uint_as_float(x[c * 8 + 2 * e]), p.scale_log2, -shift));
-            const float b = ex2(fmaf(__uint_as_float(x[c * 8 + 2 * e + 1]), p.scale_log2, -shift));
-            sum += a + b;
-            pk[e] = pack_bf16(a, b);
+            for (int e = 0; e < 4; ++e) {
+              const float a = ex2(fmaf(__uint_as_float(x[u * 8 + 2 * e]), p.scale_log2, -shift));
+              const float b = ex2(fmaf(__uint_as_float(x[u * 8 + 2 * e + 1]), p.scale_log2, -shift));
+              sum += a + b;
+              pk[e] = pack_bf16(a, b);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((((c & 1) * 4 + u) ^ (row & 7)) << 4)),
+                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                         : "memory");
           }
-          const uint32_t dst = sp + (half * 2 + (c >> 3)) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]),
-                       "r"(pk[3])
-                       : "memory");
         }
         fence_async_smem();
         tc_fence_before();
@@ -713,37 +725,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
   if (t.rows <= 0) return;
   const int worker = c == 0 ? pair >> 1 : pair;
   const int* const tail = p.schedule->tail[c];
-  // Worker q's slot of this row tile, or -1 (an empty part of the line).
-  auto slot_of = [&](int q) {
-    if (tail[q] == tail[q + 1]) return -1;
-    return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
-  };
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
   for (int r = blockIdx.y * kMergeWarps + warp; r < t.rows; r += kMergeSlices * kMergeWarps) {
-    float top = sink;
-    for (int q = t.first; q <= worker; ++q) {
-      const int slot = slot_of(q);
-      if (slot >= 0) top = fmaxf(top, p.ml_part[slot * kRows + r].x);
-    }
-    float sum = sink == kNegInf ? 0.0f : ex2(sink - top);
+    float top = sink, sum = 0.0f;
     float4 o[4] = {};
-    for (int q = t.first; q <= worker; ++q) {
-      const int slot = slot_of(q);
-      if (slot < 0) continue;
-      const float2 ml = p.ml_part[slot * kRows + r];
-      if (ml.y == 0.0f) continue;      // (the segment saw nothing; it may have stored no rows)
-      const float f = ex2(ml.x - top);
-      sum = fmaf(ml.y, f, sum);
-      const float4* src = reinterpret_cast<const float4*>(p.o_part + (static_cast<size_t>(slot) * kRows + r) * 512);
+    // A lane looks after one part; 32 parts at a time, the sums so far kept
+    // relative to the largest maximum.
+    for (int q0 = t.first; q0 <= worker; q0 += 32) {
+      const int q = q0 + lane;
+      int slot = -1;                            // (-1: an empty part of the line)
+      if (q <= worker && tail[q] != tail[q + 1])
+        slot = 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
+      float2 ml = make_float2(kNegInf, 0.0f);
+      if (slot >= 0) ml = p.ml_part[slot * kRows + r];
+      float most = ml.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldcs(src + i * 32 + lane);
-        o[i].x = fmaf(v.x, f, o[i].x);
-        o[i].y = fmaf(v.y, f, o[i].y);
-        o[i].z = fmaf(v.z, f, o[i].z);
-        o[i].w = fmaf(v.w, f, o[i].w);
+      for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      most = fmaxf(most, top);
+      const float keep = top == kNegInf ? 0.0f : ex2(top - most);
+      top = most;
+      sum *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
+      // (A part that saw nothing may have stored no rows.)
+      const unsigned parts = __ballot_sync(0xffffffffu, ml.y != 0.0f);
+      const float weight = ml.x == kNegInf ? ml.y * 0.0f : ex2(ml.x - top);
+      const float mass = ml.y * weight;
+      for (unsigned m = parts; m != 0; m &= m - 1) {
+        const int src_lane = __ffs(m) - 1;
+        const float f = __shfl_sync(0xffffffffu, weight, src_lane);
+        sum += __shfl_sync(0xffffffffu, mass, src_lane);
+        const int from = __shfl_sync(0xffffffffu, slot, src_lane);
+        const float4* src = reinterpret_cast<const float4*>(p.o_part + (static_cast<size_t>(from) * kRows + r) * 512);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = __ldcs(src + i * 32 + lane);
+          o[i].x = fmaf(v.x, f, o[i].x);
+          o[i].y = fmaf(v.y, f, o[i].y);
+          o[i].z = fmaf(v.z, f, o[i].z);
+          o[i].w = fmaf(v.w, f, o[i].w);
+        }
       }
     }
+    if (sink != kNegInf) sum += ex2(sink - top);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint2* hi = reinterpret_cast<uint2*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024);
     uint2* lo = hi + 128;
