@@ -97,7 +97,7 @@ struct ChunkParams {
   const Schedule* schedule;
   __nv_bfloat16* o_lat;      // [R][2][512]
   float* lse;                // [R] or null
-  float* o_part;             // [4 pairs][128][512]: a pair's first and last segment of each line
+  float4* o_part;            // [4 pairs][2][64][128]: a pair's first and last segment of each line
   float2* ml_part;           // [4 pairs][128] (max, sum)
   SplitTile* split;          // [2][pairs]
   int num_pages, page_size, max_pages, cache_rows;
@@ -116,38 +116,53 @@ struct Segment {
 };
 struct Walk {
   int c, pair, b;
-  int item, left;             // whole items: the next one, how many more
+  int item, left, stride;     // whole items: the next one, how many more
   int x, x1;                  // this worker's part of the line
+  int left1, stride1, tail1, end1;   // the same for class 1, while at class 0
   bool begun;
 };
 
-__device__ __forceinline__ Walk walk_start(int pair) {
+// (All that the schedule says of a pair is loaded at once: one latency.)
+__device__ __forceinline__ Walk walk_start(const ChunkParams& p, int pair) {
+  const Schedule& sc = *p.schedule;
+  const int g = pair >> 1;
   Walk w;
-  w.c = -1;
+  w.c = 0;
   w.pair = pair;
-  w.left = w.x = w.x1 = w.item = w.b = 0;
+  w.b = 0;
   w.begun = false;
+  w.item = g;
+  w.stride = sc.workers[0];
+  w.left = sc.whole[0];
+  w.x = sc.tail[0][g];
+  w.x1 = sc.tail[0][g + 1];
+  w.stride1 = sc.workers[1];
+  w.left1 = sc.whole[1];
+  w.tail1 = sc.tail[1][pair];
+  w.end1 = sc.tail[1][pair + 1];
+  if (g >= w.stride) w.left = w.x = w.x1 = 0;
+  if (pair >= w.stride1) w.left1 = w.tail1 = w.end1 = 0;
   return w;
 }
 
 __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment& s) {
-  while (w.left == 0 && w.x >= w.x1) {
+  if (w.left == 0 && w.x >= w.x1) {
     if (w.c == 1) return false;
-    ++w.c;
-    const int worker = w.c == 0 ? w.pair >> 1 : w.pair;
-    if (worker >= p.schedule->workers[w.c]) continue;
-    w.item = worker;
-    w.left = p.schedule->whole[w.c];
-    w.x = p.schedule->tail[w.c][worker];
-    w.x1 = p.schedule->tail[w.c][worker + 1];
+    w.c = 1;
+    w.item = w.pair;
+    w.left = w.left1;
+    w.stride = w.stride1;
+    w.x = w.tail1;
+    w.x1 = w.end1;
     w.begun = false;
+    if (w.left == 0 && w.x >= w.x1) return false;
   }
   const int c = w.c;
   int i;                       // item within the sequence
   if (w.left > 0) {
     w.b = sequence_of<false>(p.base, p.B, c, w.item);
     i = w.item - p.base[w.b].items[c];
-    w.item += p.schedule->workers[c];
+    w.item += w.stride;
     --w.left;
   } else {
     if (!w.begun) w.b = sequence_of<true>(p.base, p.B, c, w.x);
@@ -195,7 +210,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   int32_t* const status = p.status;
-  pdl_enter();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -216,13 +230,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&sh->swapped[0]), 2);
     mbar_init(smem_u32(&sh->swapped[1]), 2);
-    sh->abort = timed_out_before(status) ? 1 : 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&sh->tmem), 512);
     tmem_relinquish_pair();
   }
+  pdl_enter();               // (what comes before reads nothing of earlier kernels)
+  if (threadIdx.x == 0) sh->abort = timed_out_before(status) ? 1 : 0;
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -240,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // operation and 200 a stage, too slow for the 256 clk of a stage's MMAs.
     const uint32_t odd = warp == 7;
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(pair);
+    Walk w = walk_start(p, pair);
     Segment s;
     uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
     bool ok = true;
@@ -361,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {
       if (rank == 0) {
-        Walk w = walk_start(pair);
+        Walk w = walk_start(p, pair);
         Segment s;
         uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
         bool ok = true;
@@ -432,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a page, are boxes behind the cache's end, which read as zeros: no row that
     // nobody has written reaches a product.
     int2* const boxes = reinterpret_cast<int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(pair);
+    Walk w = walk_start(p, pair);
     Segment s;
     uint32_t tile = 0;
     bool ok = true;
@@ -458,11 +473,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             !(ok = mbar_wait_warp(smem_u32(&sh->taken[slot]), ((tile / kFound) & 1) ^ 1, status, abort_flag)))
           break;
         if (lane < 4) sh->row[slot][lane] = whole;
+        if (parts != 0) {                                 // all lookups in flight together
+          int* const rows = reinterpret_cast<int*>(boxes + slot * 256);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rows[(e >> 1) * 128 + (e & 1) * 32 + lane] = row_of(first + 32 * e + lane);
+        }
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
           if (!(parts >> g & 1)) continue;
-          const int pos = first + 64 * g + lane;
-          const int row0 = row_of(pos), row1 = row_of(pos + 32);
+          const int* const rows = reinterpret_cast<const int*>(boxes + (slot * 4 + g) * 64);
+          const int row0 = rows[lane], row1 = rows[32 + lane];
+          __syncwarp();                                   // the list takes their place
           // Bit i: row i of the group does not continue row i - 1.
           const int last0 = __shfl_sync(0xffffffffu, row0, 31);
           int before0 = __shfl_up_sync(0xffffffffu, row0, 1), before1 = __shfl_up_sync(0xffffffffu, row1, 1);
@@ -500,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][128]
     const uint32_t sp = smem_u32(smem + kSmemP);
     const uint32_t p_bar = cluster_addr(smem_u32(&sh->p_full), 0);
-    Walk w = walk_start(pair);
+    Walk w = walk_start(p, pair);
     Segment s;
     uint32_t tile = 0, swaps = 0;
     bool ok = true;
@@ -526,6 +547,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float ref = kNegInf, sum = 0.0f;
       for (int j = 0; j < s.tiles; ++j, ++tile) {
         const uint32_t buf = tile & 1;
+        const int k0 = (s.k0 + j) * kTile + half * 128;
+        const bool partly = k0 + 128 > s.cached;
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (partly) {
+          // Which of the thread's keys the row sees, a bit each (loaded while the
+          // scores are computed).
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = k0 + c * 32 - s.cached;                     // new token of the first key
+            if (i + 32 <= 0) continue;
+            if (mask_row != nullptr) {
+              const int wi = i >> 5, by = i & 31;                     // floor for i < 0, too
+              const uint32_t lo = wi >= 0 && wi < p.words ? mask_row[wi] : 0u;
+              const uint32_t hi = wi + 1 >= 0 && wi + 1 < p.words ? mask_row[wi + 1] : 0u;
+              see[c] = by ? (lo >> by) | (hi << (32 - by)) : lo;
+              if (i < 0) see[c] |= (1u << -i) - 1u;                   // cached keys (i > -32)
+            } else {
+              const int n = token + 1 - i;                            // keys from the first on
+              see[c] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+            }
+            const int n = s.n - i;                                    // keys that there are
+            see[c] &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+          }
+        }
         if (!(ok = mbar_wait_warp(smem_u32(&sh->s_full[buf]), (tile >> 1) & 1, status, abort_flag))) break;
         tc_fence_after();
         // Two passes over the scores, 32 at a time (a tile's 128 unrolled are 20 KB of
@@ -533,8 +578,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // then the weights.  In a tile that the row does not see all of, the first
         // pass stores the scores back with -infinity in them.
         const uint32_t sc = tmem + lane_off + buf * 128;
-        const int k0 = (s.k0 + j) * kTile + half * 128;
-        const bool partly = k0 + 128 > s.cached;
         float top = kNegInf;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -542,25 +585,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld32(sc + c * 32, x);
           tmem_ld_wait();
           if (partly) {
-            const int i = k0 + c * 32 - s.cached;                     // new token of the first key
-            uint32_t see = 0xffffffffu;
-            if (i + 32 > 0) {
-              if (mask_row != nullptr) {
-                const int wi = i >> 5, sh_ = i & 31;                  // floor for i < 0, too
-                const uint32_t lo = wi >= 0 && wi < p.words ? mask_row[wi] : 0u;
-                const uint32_t hi = wi + 1 >= 0 && wi + 1 < p.words ? mask_row[wi + 1] : 0u;
-                see = sh_ ? (lo >> sh_) | (hi << (32 - sh_)) : lo;
-                if (i < 0) see |= (1u << -i) - 1u;                    // cached keys (i > -32)
-              } else {
-                const int n = token + 1 - i;                          // keys from the first on
-                see = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-              }
-              const int n = s.n - i;                                  // keys that there are
-              see &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-            }
+            const uint32_t m = c & 2 ? (c & 1 ? see[3] : see[2]) : c & 1 ? see[1] : see[0];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(see >> e & 1)) x[e] = __float_as_uint(kNegInf);
+              if (!(m >> e & 1)) x[e] = __float_as_uint(kNegInf);
             tmem_st32(sc + c * 32, x);
           }
 #pragma unroll
@@ -643,47 +671,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.lse[s.row0 + local] = sum == 0.0f ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
         const float inv = 1.0f / sum;
-        __nv_bfloat16* dst = p.o_lat + static_cast<size_t>(s.row0 + local) * 1024 + half * 128;
+        const float unit = none ? 0.0f : inv;
+        // Both terms of 128 columns a time through the warp's own part of P (32 rows
+        // x 256 bytes), so that rows leave in whole lines.
+        const int row0 = tl & 32;                                     // the warp's first row
+        const uint32_t mine = sp + half * 2 * 8192 + row0 * 128;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
-          tmem_ld_wait();
-          if (live) {
-            uint4* const hi4 = reinterpret_cast<uint4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
-            uint4* const lo4 = reinterpret_cast<uint4*>(dst + 512 + (c >> 2) * 256 + (c & 3) * 32);
+        for (int u = 0; u < 4; ++u) {                                 // (256 columns, term)
+          const int m = u >> 1;
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + kTmO + m * 128 + c * 32, o);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint32_t h[4], l[4];
+              uint32_t h[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float a = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i]) * inv;
-                const float b = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i + 1]) * inv;
+                const float a = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i]) * unit;
+                const float b = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i + 1]) * unit;
                 h[i] = pack_bf16(a, b);
-                l[i] = pack_bf16(a - bf16_lo(h[i]), b - bf16_hi(h[i]));
+                if (u & 1) h[i] = pack_bf16(a - bf16_lo(h[i]), b - bf16_hi(h[i]));
               }
-              hi4[e] = make_uint4(h[0], h[1], h[2], h[3]);
-              lo4[e] = make_uint4(l[0], l[1], l[2], l[3]);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               mine + (c >> 1) * 8192 + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)),
+                           "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                           : "memory");
             }
           }
+          __syncwarp();
+          const int chunk = lane & 15;
+#pragma unroll 4
+          for (int i = lane >> 4; i < 32; i += 2) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(mine + (chunk >> 3) * 8192 + i * 128 + (((chunk & 7) ^ (i & 7)) << 4))
+                         : "memory");
+            const int to = static_cast<int>(rank) * 64 + row0 + i;
+            if (to < s.rows)
+              *reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(s.row0 + to) * 1024 + (u & 1) * 512 + m * 256 +
+                                        half * 128 + chunk * 8) = v;
+          }
         }
+        __syncwarp();
       } else {
         const int worker = s.c == 0 ? pair >> 1 : pair;
         const int* const tail = p.schedule->tail[s.c];
         const int slot = 4 * pair + 2 * s.c + (s.x == tail[worker] ? 0 : 1);
         if (half == 0) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
         if (s.tiles > 0) {
-          float* dst = p.o_part + (static_cast<size_t>(slot) * kRows + local) * 512 + half * 128;
+          // Laid out as the threads hold it: [CTA][column / 4 of the 256][thread].
+          float4* dst = p.o_part + (static_cast<size_t>(slot) * 2 + rank) * 64 * 128 + tl;
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
             tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
             tmem_ld_wait();
-            float4* d4 = reinterpret_cast<float4*>(dst + (c >> 2) * 256 + (c & 3) * 32);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              d4[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                  __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+              dst[(c * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
         if (ends && tl == 0 && rank == 0) {
@@ -713,75 +763,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Split row tiles: blockIdx.x is the (class, pair) in whose part one ends,
-// blockIdx.y a slice of its rows; a warp takes a row at a time.
+// Split row tiles: blockIdx.x is the (class, pair) in whose part one ends.  A
+// warp takes 32 of the attention's threads' rows and 32 of their 256 columns.
 constexpr int kMergeSlices = 8, kMergeWarps = 8;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pairs) {
   pdl_enter();
   if (timed_out_before(p.status)) return;
-  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs;
   const SplitTile t = p.split[blockIdx.x];
   if (t.rows <= 0) return;
+  const int unit = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int rank = unit >> 5, quarter = unit >> 3 & 3, part = unit & 7;     // CTA, its rows, their columns
+  const int tl = quarter * 32 + lane, half = tl >> 6;
+  const int r = rank * 64 + (tl & 63);
   const int worker = c == 0 ? pair >> 1 : pair;
   const int* const tail = p.schedule->tail[c];
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
-  for (int r = blockIdx.y * kMergeWarps + warp; r < t.rows; r += kMergeSlices * kMergeWarps) {
-    float top = sink, sum = 0.0f;
-    float4 o[4] = {};
-    // A lane looks after one part; 32 parts at a time, the sums so far kept
-    // relative to the largest maximum.
-    for (int q0 = t.first; q0 <= worker; q0 += 32) {
-      const int q = q0 + lane;
-      int slot = -1;                            // (-1: an empty part of the line)
-      if (q <= worker && tail[q] != tail[q + 1])
-        slot = 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
-      float2 ml = make_float2(kNegInf, 0.0f);
-      if (slot >= 0) ml = p.ml_part[slot * kRows + r];
-      float most = ml.x;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      most = fmaxf(most, top);
-      const float keep = top == kNegInf ? 0.0f : ex2(top - most);
-      top = most;
-      sum *= keep;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
+  // Worker q's slot, or -1 (an empty part of the line): a lane looks it up for
+  // one of 32 workers at a time.
+  auto slots = [&](int q0) {
+    const int q = q0 + lane;
+    if (q > worker || tail[q] == tail[q + 1]) return -1;
+    return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
+  };
+  float top = sink;
+  for (int q0 = t.first; q0 <= worker; q0 += 32) {
+    const int mine = slots(q0);
+    for (unsigned m = __ballot_sync(0xffffffffu, mine >= 0); m != 0; m &= m - 1) {
+      const int slot = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1);
+      top = fmaxf(top, p.ml_part[slot * kRows + r].x);
+    }
+  }
+  float sum = sink == kNegInf ? 0.0f : ex2(sink - top);
+  float4 o[8] = {};
+  for (int q0 = t.first; q0 <= worker; q0 += 32) {
+    const int mine = slots(q0);
+    for (unsigned m = __ballot_sync(0xffffffffu, mine >= 0); m != 0; m &= m - 1) {
+      const int slot = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1);
+      const float2 ml = p.ml_part[slot * kRows + r];
       // (A part that saw nothing may have stored no rows.)
-      const unsigned parts = __ballot_sync(0xffffffffu, ml.y != 0.0f);
-      const float weight = ml.x == kNegInf ? ml.y * 0.0f : ex2(ml.x - top);
-      const float mass = ml.y * weight;
-      for (unsigned m = parts; m != 0; m &= m - 1) {
-        const int src_lane = __ffs(m) - 1;
-        const float f = __shfl_sync(0xffffffffu, weight, src_lane);
-        sum += __shfl_sync(0xffffffffu, mass, src_lane);
-        const int from = __shfl_sync(0xffffffffu, slot, src_lane);
-        const float4* src = reinterpret_cast<const float4*>(p.o_part + (static_cast<size_t>(from) * kRows + r) * 512);
+      const bool any = ml.y != 0.0f;
+      const float f = ml.x == kNegInf ? ml.y * 0.0f : ex2(ml.x - top);
+      if (any) sum = fmaf(ml.y, f, sum);
+      const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * 8) * 128 + tl;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = __ldcs(src + i * 32 + lane);
-          o[i].x = fmaf(v.x, f, o[i].x);
-          o[i].y = fmaf(v.y, f, o[i].y);
-          o[i].z = fmaf(v.z, f, o[i].z);
-          o[i].w = fmaf(v.w, f, o[i].w);
+      for (int e = 0; e < 8; ++e) {
+        const float4 v = __ldcs(src + e * 128);
+        if (any) {
+          o[e].x = fmaf(v.x, f, o[e].x);
+          o[e].y = fmaf(v.y, f, o[e].y);
+          o[e].z = fmaf(v.z, f, o[e].z);
+          o[e].w = fmaf(v.w, f, o[e].w);
         }
       }
     }
-    if (sink != kNegInf) sum += ex2(sink - top);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint2* hi = reinterpret_cast<uint2*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024);
-    uint2* lo = hi + 128;
+  }
+  if (r >= t.rows) return;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint4* hi = reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (part >> 2) * 256 + half * 128 +
+                                       (part & 3) * 32);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float v[8] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv,
+                        o[e + 1].x * inv, o[e + 1].y * inv, o[e + 1].z * inv, o[e + 1].w * inv};
+    uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = o[i].x * inv, b = o[i].y * inv, c = o[i].z * inv, d = o[i].w * inv;
-      const uint32_t h0 = pack_bf16(a, b), h1 = pack_bf16(c, d);
-      hi[i * 32 + lane] = make_uint2(h0, h1);
-      lo[i * 32 + lane] = make_uint2(pack_bf16(a - bf16_lo(h0), b - bf16_hi(h0)),
-                                     pack_bf16(c - bf16_lo(h1), d - bf16_hi(h1)));
+      h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      l[i] = pack_bf16(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
     }
-    if (p.lse != nullptr && lane == 0)
-      p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
+    hi[e >> 1] = make_uint4(h[0], h[1], h[2], h[3]);
+    hi[64 + (e >> 1)] = make_uint4(l[0], l[1], l[2], l[3]);
   }
+  if (p.lse != nullptr && part == 0 && half == 0)
+    p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
 }
 
 struct Layout {
@@ -830,7 +887,7 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.schedule = reinterpret_cast<const Schedule*>(ws + L.schedule);
   p.o_lat = reinterpret_cast<__nv_bfloat16*>(ws + L.o_lat);
   p.lse = a.lse;
-  p.o_part = reinterpret_cast<float*>(ws + L.o_part);
+  p.o_part = reinterpret_cast<float4*>(ws + L.o_part);
   p.ml_part = reinterpret_cast<float2*>(ws + L.ml_part);
   p.split = reinterpret_cast<SplitTile*>(ws + L.split);
   p.num_pages = a.num_pages;
