@@ -22,11 +22,15 @@
 namespace mla {
 namespace {
 
-constexpr int kPoolCtas = 8;        // CTAs of a bookkeeping cluster (the portable most)
+constexpr int kPoolCtas = 16;       // CTAs of a bookkeeping cluster (the most there can be)
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ long long warp_sum64(int v) {     // of values >= 0
+  return static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) >> 16)) * 65536 +
+         __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) & 0xFFFFu);
+}
 __device__ __forceinline__ int warp_scan(int v, int lane) {   // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -112,7 +116,8 @@ __global__ void __launch_bounds__(256) free_kernel(PagesFreeArgs a) {
 // ============================================================ reserve
 struct PoolSmem {
   int warp_count[kPoolWarps];     // free (live) pages in the warp's range
-  int tally[4];                   // of this CTA: pages wanted, copies, free pages, flags
+  int tally[4];                   // of this CTA: pages wanted (live), movers, free pages, flags
+  int shared_tally[2];            // pages wanted and copies once the sharers are known
   int scan[kPoolWarps], scan2[kPoolWarps];
 };
 
@@ -137,6 +142,8 @@ __device__ __forceinline__ int4 load4(const int32_t* p, int i, int hi, bool wide
   return v;
 }
 
+constexpr int kRowUnroll = 8;         // table entries that a lane has in flight
+constexpr int kNoEntry = -0x7FFFFFFF - 1;   // (past the range; an entry below 0 is a missing page)
 enum { kBadPage = 1, kShared = 2, kStop = 4 };
 
 // The pages that sequence b writes to: [first, end) of its row, or none.
@@ -168,52 +175,84 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   const int per = (a.batch + kPoolCtas - 1) / kPoolCtas;
   const int b0 = min(a.batch, rank * per), b1 = min(a.batch, b0 + per);
   if (t < 4) sh.tally[t] = 0;
+  if (t < 2) sh.shared_tally[t] = 0;
   __syncthreads();
 
-  // The scratch words of the pages that are written to: their count now (the
-  // counts themselves change while others still decide), writers, last writer.
-  int flags = stop ? kStop : 0;
+  // First look: missing pages are counted.  The scratch words of pages that are
+  // there: their count now (the counts themselves change while others still
+  // decide), writers, last writer.
+  int flags = stop ? kStop : 0, wants = 0;
   for (int b = b0 + warp; b < b1; b += kPoolWarps) {
     Touched s;
     if (!touched(a, b, s)) flags |= kBadPage;
     const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-    for (int j = s.first + lane; j < s.end; j += 32) {
-      const int v = row[j];
-      if (v >= a.num_pages) flags |= kBadPage;
-      else if (v >= 0) {
-        const int r = a.refs[v];
-        a.before[v] = r;
-        a.writers[v] = 0;
-        a.last[v] = -1;
-        if (r > 1) flags |= kShared;
+    int missing = 0;
+    for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
+      int v[kRowUnroll];
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) {
+        const int j = j0 + e * 32 + lane;
+        v[e] = j < s.end ? row[j] : kNoEntry;
+      }
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) {
+        if (v[e] < 0) {
+          missing += v[e] != kNoEntry;
+        } else if (v[e] >= a.num_pages) {
+          flags |= kBadPage;
+        } else {
+          const int r = a.refs[v[e]];
+          a.before[v[e]] = r;
+          a.writers[v[e]] = 0;
+          a.last[v[e]] = -1;
+          if (r > 1) flags |= kShared;
+        }
       }
     }
+    missing = warp_sum(missing);
+    if (lane == 0) a.want[b] = make_int2(missing, 0);
+    wants += missing;
   }
   int lo, hi, n_free = 0;
   warp_range(a.num_pages, rank, warp, lo, hi);
-  for (int i = lo + 4 * lane; i < hi; i += 128) {
-    const int4 v = load4(a.refs, i, hi, wide, 1);
-    n_free += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  for (int i = lo + 4 * lane; i < hi; i += 128 * 4) {
+    int4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = load4(a.refs, i + 128 * e, hi, wide, 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n_free += (v[e].x == 0) + (v[e].y == 0) + (v[e].z == 0) + (v[e].w == 0);
   }
   n_free = warp_sum(n_free);
+  flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0) {
     sh.warp_count[warp] = n_free;
     atomicAdd(&sh.tally[2], n_free);
+    if (wants) atomicAdd(&sh.tally[0], wants);
+    if (flags) atomicOr(&sh.tally[3], flags);
   }
-  if (flags) atomicOr(&sh.tally[3], flags);
   cluster_sync();
-  int all = 0, free_before = 0, free_total = 0;
-#pragma unroll
-  for (int r = 0; r < kPoolCtas; ++r) {
-    all |= ld_remote(&sh.tally[3], r);
-    const int f = ld_remote(&sh.tally[2], r);
-    free_total += f;
-    if (r < rank) free_before += f;
+  // What the CTAs found: sums of all of them and of those before this one.
+  int all = 0, free_before = 0, want_before = 0, copy_before = 0, copies = 0;
+  long long want_total = 0, free_total = 0;
+  {
+    const bool on = lane < kPoolCtas;
+    const int w = on ? ld_remote(&sh.tally[0], lane) : 0, f = on ? ld_remote(&sh.tally[2], lane) : 0;
+    all = __reduce_or_sync(0xffffffffu, on ? ld_remote(&sh.tally[3], lane) : 0);
+    free_total = warp_sum(f);
+    free_before = warp_sum(lane < rank ? f : 0);
+    want_total = warp_sum64(w);
+    want_before = warp_sum(lane < rank ? w : 0);
   }
   if (all & kStop) {
     cluster_sync();    // no CTA leaves while another reads its shared memory
     return;
   }
+  // A writer of a shared page takes a copy, but for the last one if nobody
+  // else holds the page.
+  auto takes = [&](int v, int b) {
+    const int r = __ldcg(a.before + v);
+    return r > 1 && !(__ldcg(a.writers + v) >= r && __ldcg(a.last + v) == b);
+  };
   if (all & kShared) {
     for (int b = b0 + warp; b < b1; b += kPoolWarps) {
       Touched s;
@@ -228,43 +267,34 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       }
     }
     cluster_sync();
-  }
-  // A writer of a shared page takes a copy, but for the last one if nobody
-  // else holds the page.
-  auto takes = [&](int v, int b) {
-    const int r = __ldcg(a.before + v);
-    return r > 1 && !(__ldcg(a.writers + v) >= r && __ldcg(a.last + v) == b);
-  };
-  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
-    Touched s;
-    int want = 0, copy = 0;
-    if (touched(a, b, s)) {
-      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-      for (int j = s.first + lane; j < s.end; j += 32) {
-        const int v = row[j];
-        if (v >= a.num_pages) continue;
-        const bool shared = v >= 0 && takes(v, b);
-        want += v < 0 || shared;
-        copy += shared && s.part && j == s.first;
+    for (int b = b0 + warp; b < b1; b += kPoolWarps) {
+      Touched s;
+      int want = 0, copy = 0;
+      if (touched(a, b, s)) {
+        const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+        for (int j = s.first + lane; j < s.end; j += 32) {
+          const int v = row[j];
+          if (v >= a.num_pages) continue;
+          const bool shared = v >= 0 && takes(v, b);
+          want += v < 0 || shared;
+          copy += shared && s.part && j == s.first;
+        }
+      }
+      want = warp_sum(want);
+      copy = warp_sum(copy);
+      if (lane == 0) {
+        atomicAdd(&sh.shared_tally[0], want);
+        atomicAdd(&sh.shared_tally[1], copy);
+        a.want[b] = make_int2(want, copy);
       }
     }
-    want = warp_sum(want);
-    copy = warp_sum(copy);
-    if (lane == 0) {
-      a.want[b] = make_int2(want, copy);
-      atomicAdd(&sh.tally[0], want);
-      atomicAdd(&sh.tally[1], copy);
-    }
-  }
-  cluster_sync();
-  int want_before = 0, copy_before = 0, copies = 0;
-  long long want_total = 0;
-#pragma unroll
-  for (int r = 0; r < kPoolCtas; ++r) {
-    const int w = ld_remote(&sh.tally[0], r), c = ld_remote(&sh.tally[1], r);
-    want_total += w;
-    copies += c;
-    if (r < rank) want_before += w, copy_before += c;
+    cluster_sync();
+    const bool on = lane < kPoolCtas;
+    const int w = on ? ld_remote(&sh.shared_tally[0], lane) : 0, c = on ? ld_remote(&sh.shared_tally[1], lane) : 0;
+    want_total = warp_sum64(w);
+    want_before = warp_sum(lane < rank ? w : 0);
+    copies = warp_sum(c);
+    copy_before = warp_sum(lane < rank ? c : 0);
   }
   const bool ok = !(all & kBadPage) && want_total <= free_total;
   if (!ok) copies = 0;
@@ -277,20 +307,24 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   if (ok) {
     // The free pages in order, as many as are wanted.
     int at = free_before;
-    for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
-    for (int i = lo; i < hi && at < want_total; i += 128) {
-      const int4 v = load4(a.refs, i + 4 * lane, hi, wide, 1);
-      const int mine = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
-      const int upto = warp_scan(mine, lane);
-      int k = at + upto - mine, p = i + 4 * lane;
-      if (v.x == 0 && k < want_total) a.free_list[k] = p;
-      k += v.x == 0;
-      if (v.y == 0 && k < want_total) a.free_list[k] = p + 1;
-      k += v.y == 0;
-      if (v.z == 0 && k < want_total) a.free_list[k] = p + 2;
-      k += v.z == 0;
-      if (v.w == 0 && k < want_total) a.free_list[k] = p + 3;
-      at += __shfl_sync(0xffffffffu, upto, 31);
+    at += warp_sum(lane < warp ? sh.warp_count[lane] : 0);
+    for (int i = lo; i < hi && at < want_total; i += 128 * 2) {
+      int4 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) v[e] = load4(a.refs, i + 128 * e + 4 * lane, hi, wide, 1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int f[4] = {v[e].x == 0, v[e].y == 0, v[e].z == 0, v[e].w == 0};
+        const int mine = f[0] + f[1] + f[2] + f[3];
+        const int upto = warp_scan(mine, lane);
+        int k = at + upto - mine;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (f[u] && k < want_total) a.free_list[k] = i + 128 * e + 4 * lane + u;
+          k += f[u];
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
+      }
     }
     // Where each sequence's pages and copies begin.
     for (int base = b0; base < b1; base += kPoolThreads) {
@@ -300,14 +334,11 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       __syncthreads();
       if (lane == 31) sh.scan[warp] = sw, sh.scan2[warp] = sc;
       __syncthreads();
-      int ow = want_before, oc = copy_before, tw = 0, tc = 0;
-      for (int x = 0; x < kPoolWarps; ++x) {
-        if (x < warp) ow += sh.scan[x], oc += sh.scan2[x];
-        tw += sh.scan[x], tc += sh.scan2[x];
-      }
-      if (b < b1) a.want[b] = make_int2(ow + sw - w.x, oc + sc - w.y);
-      want_before += tw;
-      copy_before += tc;
+      const int ow = sh.scan[lane], oc = sh.scan2[lane];      // (as many warps as lanes)
+      const int bw = warp_sum(lane < warp ? ow : 0), bc = warp_sum(lane < warp ? oc : 0);
+      if (b < b1) a.want[b] = make_int2(want_before + bw + sw - w.x, copy_before + bc + sc - w.y);
+      want_before += warp_sum(ow);
+      copy_before += warp_sum(oc);
     }
   }
   cluster_sync();      // the last one: no CTA reads another's shared memory behind it
@@ -318,23 +349,38 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int2 base = __ldcg(a.want + b);
     int at = base.x;
     int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-    for (int j0 = s.first; j0 < s.end; j0 += 32) {
-      const int j = j0 + lane;
-      const int v = j < s.end ? row[j] : 0;
-      const bool shared = j < s.end && v >= 0 && takes(v, b);
-      const bool want = j < s.end && (v < 0 || shared);
-      const unsigned m = __ballot_sync(0xffffffffu, want);
-      if (want) {
-        const int p = __ldcg(a.free_list + at + __popc(m & ((1u << lane) - 1)));
-        row[j] = p;
-        a.refs[p] = 1;
-        if (shared) atomicSub(a.refs + v, 1);
-        if (shared && s.part && j == s.first) {
-          a.copy_src[base.y] = v;
-          a.copy_dst[base.y] = p;
+    for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
+      int v[kRowUnroll], rank_of[kRowUnroll], page[kRowUnroll];
+      bool shared[kRowUnroll];
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) {
+        const int j = j0 + e * 32 + lane;
+        v[e] = j < s.end ? row[j] : kNoEntry;
+      }
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) {
+        shared[e] = (all & kShared) && v[e] >= 0 && takes(v[e], b);
+        const bool want = (v[e] < 0 && v[e] != kNoEntry) || shared[e];
+        const unsigned m = __ballot_sync(0xffffffffu, want);
+        rank_of[e] = want ? at + __popc(m & ((1u << lane) - 1)) : -1;
+        at += __popc(m);
+      }
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) page[e] = rank_of[e] >= 0 ? __ldcg(a.free_list + rank_of[e]) : -1;
+#pragma unroll
+      for (int e = 0; e < kRowUnroll; ++e) {
+        if (rank_of[e] < 0) continue;
+        const int j = j0 + e * 32 + lane;
+        row[j] = page[e];
+        a.refs[page[e]] = 1;
+        if (shared[e]) {
+          atomicSub(a.refs + v[e], 1);
+          if (s.part && j == s.first) {
+            a.copy_src[base.y] = v[e];
+            a.copy_dst[base.y] = page[e];
+          }
         }
       }
-      at += __popc(m);
     }
   }
 }
@@ -356,9 +402,12 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   __syncthreads();
   int lo, hi, n_live = 0;
   warp_range(a.num_pages, rank, warp, lo, hi);
-  for (int i = lo + 4 * lane; i < hi; i += 128) {
-    const int4 v = load4(a.refs, i, hi, wide, 0);
-    n_live += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+  for (int i = lo + 4 * lane; i < hi; i += 128 * 4) {
+    int4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = load4(a.refs, i + 128 * e, hi, wide, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n_live += (v[e].x > 0) + (v[e].y > 0) + (v[e].z > 0) + (v[e].w > 0);
   }
   n_live = warp_sum(n_live);
   if (lane == 0) {
@@ -367,19 +416,16 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
   if (stop) sh.tally[3] = kStop;
   cluster_sync();
-  int at = 0, live = 0, all = 0;
-#pragma unroll
-  for (int r = 0; r < kPoolCtas; ++r) {
-    all |= ld_remote(&sh.tally[3], r);
-    const int f = ld_remote(&sh.tally[0], r);
-    live += f;
-    if (r < rank) at += f;
-  }
+  const bool on = lane < kPoolCtas;
+  const int found = on ? ld_remote(&sh.tally[0], lane) : 0;
+  const int all = __reduce_or_sync(0xffffffffu, on ? ld_remote(&sh.tally[3], lane) : 0);
+  const int live = warp_sum(found);
+  int at = warp_sum(lane < rank ? found : 0);
   if (all & kStop) {
     cluster_sync();
     return;
   }
-  for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
+  at += warp_sum(lane < warp ? sh.warp_count[lane] : 0);
   int movers = 0;
   for (int i = lo; i < hi; i += 128) {
     const int4 v = load4(a.refs, i + 4 * lane, hi, wide, 0);
@@ -405,10 +451,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   movers = warp_sum(movers);
   if (lane == 0 && movers) atomicAdd(&sh.tally[1], movers);
   cluster_sync();
-  int n = 0;
-#pragma unroll
-  for (int r = 0; r < kPoolCtas; ++r) n += ld_remote(&sh.tally[1], r);
-  n = min(n, a.max_copies);
+  const int n = min(warp_sum(on ? ld_remote(&sh.tally[1], lane) : 0), a.max_copies);
   if (rank == 0 && t == 0) *a.copy_count = n;
   for (int k = rank * kPoolThreads + t; k < a.max_copies; k += kPoolCtas * kPoolThreads) {
     if (k < n) {
@@ -483,14 +526,16 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(PagesCopyArgs 
   }
 }
 
-// Accepted rows of a sequence (blockIdx.x) in a layer (blockIdx.y).  The list
-// ascends strictly, so keep[k] >= k: a round reads rows of the list before any
-// of it is stored, and what it stores lies below all that later rounds read.
-// A thread holds one vector of kKeepUnroll rows.
-constexpr int kKeepThreads = 288, kKeepUnroll = 4;
+// Accepted rows of a sequence (blockIdx.x) in layers blockIdx.y, + gridDim.y, ..
+// The list ascends strictly, so keep[k] >= k: a round reads rows of the list
+// before any of it is stored, and what it stores lies below all that later
+// rounds read.  Where the rows are is found once for all layers.  A thread holds
+// one vector of kKeepUnroll rows.
+constexpr int kKeepThreads = 288, kKeepUnroll = 4, kKeepRound = 1024;
 
 template <typename V>
 __global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(KeepRowsArgs a) {
+  __shared__ int from[kKeepRound], to[kKeepRound];
   pdl_enter();
   if (timed_out_before(a.status)) return;
   const int b = blockIdx.x, t = threadIdx.x;
@@ -503,45 +548,58 @@ __global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(KeepRowsArgs a)
   auto row_of = [&](int i) {
     const unsigned long long p = static_cast<unsigned long long>(len) + static_cast<unsigned>(i);
     const unsigned long long j = p / static_cast<unsigned>(a.page_size);
-    if (j >= static_cast<unsigned long long>(a.max_pages)) return -1ll;
+    if (j >= static_cast<unsigned long long>(a.max_pages)) return -1;
     const int page = pages[j];
-    if (page < 0 || page >= a.num_pages) return -1ll;
-    return static_cast<long long>(page) * a.page_size + static_cast<long long>(p - j * a.page_size);
+    if (page < 0 || page >= a.num_pages) return -1;
+    return page * a.page_size + static_cast<int>(p - j * a.page_size);
   };
   // The whole list is looked over first: a sequence is moved whole or not at all.
   int bad = n > a.keep_stride ? 1 : 0;
   if (!bad)
     for (int k = t; k < n; k += kKeepThreads) {
-      const int i = keep[k];
-      if (i < 0 || (k > 0 && keep[k - 1] >= i)) bad |= 1;
-      else if (row_of(i) < 0 || row_of(k) < 0) bad |= 2;
+      const int i = keep[k], before = k > 0 ? keep[k - 1] : -1;
+      int src = -1, dst = -1;
+      if (i < 0 || before >= i) bad |= 1;
+      else if ((src = row_of(i)) < 0 || (dst = row_of(k)) < 0) bad |= 2;
+      if (k < kKeepRound) from[k] = src, to[k] = dst;
     }
   const bool bad_list = __syncthreads_or(bad & 1), bad_page = __syncthreads_or(bad & 2);
   if (bad_list || bad_page) {
     if (t == 0) set_status(a.status, bad_list ? MLA_DEV_BAD_OFFSETS : MLA_DEV_BAD_PAGE);
     return;
   }
-  char* base = a.cache + static_cast<size_t>(blockIdx.y) * a.layer_stride;
   const int cols = static_cast<int>(a.row_bytes / sizeof(V));
   const int wide = min(cols, kKeepThreads);             // threads on a row
   const int lines = kKeepThreads / wide;                // rows side by side
   const int line = t / wide, col0 = t - line * wide;
-  for (int c0 = 0; c0 < cols; c0 += wide) {
-    const int c = c0 + col0;
-    const bool on = line < lines && c < cols;
-    for (int k0 = 0; k0 < n; k0 += lines * kKeepUnroll) {
-      V x[kKeepUnroll];
-#pragma unroll
-      for (int e = 0; e < kKeepUnroll; ++e) {
-        const int k = k0 + e * lines + line;
-        if (on && k < n && keep[k] != k)
-          x[e] = reinterpret_cast<const V*>(base + row_of(keep[k]) * a.row_bytes)[c];
-      }
+  for (int first = 0; first < n; first += kKeepRound) {
+    const int m = min(n - first, kKeepRound);
+    if (first > 0) {                                    // (the first of them are there already)
       __syncthreads();
+      for (int k = t; k < m; k += kKeepThreads) from[k] = row_of(keep[first + k]), to[k] = row_of(first + k);
+      __syncthreads();
+    }
+    for (int layer = blockIdx.y; layer < a.layers; layer += gridDim.y) {
+      char* base = a.cache + static_cast<size_t>(layer) * a.layer_stride;
+      for (int c0 = 0; c0 < cols; c0 += wide) {
+        const int c = c0 + col0;
+        const bool on = line < lines && c < cols;
+        for (int k0 = 0; k0 < m; k0 += lines * kKeepUnroll) {
+          V x[kKeepUnroll];
 #pragma unroll
-      for (int e = 0; e < kKeepUnroll; ++e) {
-        const int k = k0 + e * lines + line;
-        if (on && k < n && keep[k] != k) reinterpret_cast<V*>(base + row_of(k) * a.row_bytes)[c] = x[e];
+          for (int e = 0; e < kKeepUnroll; ++e) {
+            const int k = k0 + e * lines + line;
+            if (on && k < m && from[k] != to[k])
+              x[e] = reinterpret_cast<const V*>(base + static_cast<size_t>(from[k]) * a.row_bytes)[c];
+          }
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < kKeepUnroll; ++e) {
+            const int k = k0 + e * lines + line;
+            if (on && k < m && from[k] != to[k])
+              reinterpret_cast<V*>(base + static_cast<size_t>(to[k]) * a.row_bytes)[c] = x[e];
+          }
+        }
       }
     }
   }
@@ -561,11 +619,15 @@ cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   return launch_pdl(reserve_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  cudaError_t e = cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
   const long long entries = static_cast<long long>(a.batch) * a.max_pages;
   if (entries == 0) return cudaSuccess;
@@ -587,7 +649,9 @@ cudaError_t launch_pages_copy(const PagesCopyArgs& a, cudaStream_t stream) {
 cudaError_t launch_keep_rows(const KeepRowsArgs& a, cudaStream_t stream) {
   if (a.batch == 0 || a.layers == 0) return cudaSuccess;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.cache) | a.row_bytes | a.layer_stride) & 15u) == 0;
-  const dim3 grid(a.batch, a.layers);
+  // One wave of CTAs (7 fit an SM), each for several layers where there are many.
+  const int most = std::max(1, 7 * sm_count() / a.batch);
+  const dim3 grid(a.batch, std::min(a.layers, most));
   return wide ? launch_pdl(keep_rows_kernel<uint4>, grid, dim3(kKeepThreads), 0, stream, a)
               : launch_pdl(keep_rows_kernel<unsigned>, grid, dim3(kKeepThreads), 0, stream, a);
 }
