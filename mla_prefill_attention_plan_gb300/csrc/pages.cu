@@ -22,7 +22,7 @@
 namespace mla {
 namespace {
 
-constexpr int kPoolCtas = 16;       // CTAs of a bookkeeping cluster (the most there can be)
+constexpr int kPoolCtas = 16;       // CTAs of a bookkeeping cluster (the most there can be), or one
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
@@ -38,6 +38,12 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {   // inclusive
     if (lane >= d) v += o;
   }
   return v;
+}
+// All threads of the CTAs that share the work.
+template <int CTAS>
+__device__ __forceinline__ void pool_sync() {
+  if (CTAS > 1) cluster_sync();
+  else __syncthreads();
 }
 __device__ __forceinline__ int ld_remote(const int* local, uint32_t rank) {
   int v;
@@ -123,8 +129,9 @@ struct PoolSmem {
 
 // The warp's contiguous range of page ids, a multiple of 128 long (an int4 a
 // lane) so that 16-byte loads of an aligned array stay aligned.
+template <int CTAS>
 __device__ __forceinline__ void warp_range(int n, int rank, int warp, int& lo, int& hi) {
-  const int parts = kPoolCtas * kPoolWarps;
+  const int parts = CTAS * kPoolWarps;
   const long long per = ((static_cast<long long>(n) + parts - 1) / parts + 127) / 128 * 128;
   const long long at = per * (rank * kPoolWarps + warp);
   lo = static_cast<int>(min(at, static_cast<long long>(n)));
@@ -163,16 +170,16 @@ __device__ __forceinline__ bool touched(const PagesReserveArgs& a, int b, Touche
   return true;
 }
 
-__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
-    reserve_kernel(PagesReserveArgs a) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) reserve_kernel(PagesReserveArgs a) {
   __shared__ PoolSmem sh;
   pdl_enter();
   const bool stop = timed_out_before(a.status);   // the CTAs agree on it below
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int rank = static_cast<int>(cluster_rank());
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
   const bool wide = (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
   // Sequences of this CTA; a warp takes every 32nd of them.
-  const int per = (a.batch + kPoolCtas - 1) / kPoolCtas;
+  const int per = (a.batch + CTAS - 1) / CTAS;
   const int b0 = min(a.batch, rank * per), b1 = min(a.batch, b0 + per);
   if (t < 4) sh.tally[t] = 0;
   if (t < 2) sh.shared_tally[t] = 0;
@@ -214,7 +221,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     wants += missing;
   }
   int lo, hi, n_free = 0;
-  warp_range(a.num_pages, rank, warp, lo, hi);
+  warp_range<CTAS>(a.num_pages, rank, warp, lo, hi);
   for (int i = lo + 4 * lane; i < hi; i += 128 * 4) {
     int4 v[4];
 #pragma unroll
@@ -230,12 +237,12 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     if (wants) atomicAdd(&sh.tally[0], wants);
     if (flags) atomicOr(&sh.tally[3], flags);
   }
-  cluster_sync();
+  pool_sync<CTAS>();
   // What the CTAs found: sums of all of them and of those before this one.
   int all = 0, free_before = 0, want_before = 0, copy_before = 0, copies = 0;
   long long want_total = 0, free_total = 0;
   {
-    const bool on = lane < kPoolCtas;
+    const bool on = lane < CTAS;
     const int w = on ? ld_remote(&sh.tally[0], lane) : 0, f = on ? ld_remote(&sh.tally[2], lane) : 0;
     all = __reduce_or_sync(0xffffffffu, on ? ld_remote(&sh.tally[3], lane) : 0);
     free_total = warp_sum(f);
@@ -244,7 +251,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     want_before = warp_sum(lane < rank ? w : 0);
   }
   if (all & kStop) {
-    cluster_sync();    // no CTA leaves while another reads its shared memory
+    pool_sync<CTAS>();    // no CTA leaves while another reads its shared memory
     return;
   }
   // A writer of a shared page takes a copy, but for the last one if nobody
@@ -266,7 +273,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
         }
       }
     }
-    cluster_sync();
+    pool_sync<CTAS>();
     for (int b = b0 + warp; b < b1; b += kPoolWarps) {
       Touched s;
       int want = 0, copy = 0;
@@ -288,8 +295,8 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
         a.want[b] = make_int2(want, copy);
       }
     }
-    cluster_sync();
-    const bool on = lane < kPoolCtas;
+    pool_sync<CTAS>();
+    const bool on = lane < CTAS;
     const int w = on ? ld_remote(&sh.shared_tally[0], lane) : 0, c = on ? ld_remote(&sh.shared_tally[1], lane) : 0;
     want_total = warp_sum64(w);
     want_before = warp_sum(lane < rank ? w : 0);
@@ -302,7 +309,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     *a.copy_count = copies;
     if (!ok) set_status(a.status, (all & kBadPage) ? MLA_DEV_BAD_PAGE : MLA_DEV_NO_PAGES);
   }
-  for (int i = copies + rank * kPoolThreads + t; i < a.batch; i += kPoolCtas * kPoolThreads)
+  for (int i = copies + rank * kPoolThreads + t; i < a.batch; i += CTAS * kPoolThreads)
     a.copy_src[i] = a.copy_dst[i] = -1;
   if (ok) {
     // The free pages in order, as many as are wanted.
@@ -341,7 +348,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       copy_before += warp_sum(oc);
     }
   }
-  cluster_sync();      // the last one: no CTA reads another's shared memory behind it
+  pool_sync<CTAS>();      // the last one: no CTA reads another's shared memory behind it
   if (!ok) return;
   for (int b = b0 + warp; b < b1; b += kPoolWarps) {
     Touched s;
@@ -390,18 +397,18 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
 // one for as long as that is lower, which is for exactly the live pages >= L:
 // as many free pages lie below L.  So each page finds from its own rank
 // whether it takes part.
-__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
-    compact_kernel(PagesCompactArgs a) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) compact_kernel(PagesCompactArgs a) {
   __shared__ PoolSmem sh;
   pdl_enter();
   const bool stop = timed_out_before(a.status);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int rank = static_cast<int>(cluster_rank());
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
   const bool wide = (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
   if (t < 4) sh.tally[t] = 0;
   __syncthreads();
   int lo, hi, n_live = 0;
-  warp_range(a.num_pages, rank, warp, lo, hi);
+  warp_range<CTAS>(a.num_pages, rank, warp, lo, hi);
   for (int i = lo + 4 * lane; i < hi; i += 128 * 4) {
     int4 v[4];
 #pragma unroll
@@ -415,14 +422,14 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     atomicAdd(&sh.tally[0], n_live);
   }
   if (stop) sh.tally[3] = kStop;
-  cluster_sync();
-  const bool on = lane < kPoolCtas;
+  pool_sync<CTAS>();
+  const bool on = lane < CTAS;
   const int found = on ? ld_remote(&sh.tally[0], lane) : 0;
   const int all = __reduce_or_sync(0xffffffffu, on ? ld_remote(&sh.tally[3], lane) : 0);
   const int live = warp_sum(found);
   int at = warp_sum(lane < rank ? found : 0);
   if (all & kStop) {
-    cluster_sync();
+    pool_sync<CTAS>();
     return;
   }
   at += warp_sum(lane < warp ? sh.warp_count[lane] : 0);
@@ -450,10 +457,10 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
   movers = warp_sum(movers);
   if (lane == 0 && movers) atomicAdd(&sh.tally[1], movers);
-  cluster_sync();
+  pool_sync<CTAS>();
   const int n = min(warp_sum(on ? ld_remote(&sh.tally[1], lane) : 0), a.max_copies);
   if (rank == 0 && t == 0) *a.copy_count = n;
-  for (int k = rank * kPoolThreads + t; k < a.max_copies; k += kPoolCtas * kPoolThreads) {
+  for (int k = rank * kPoolThreads + t; k < a.max_copies; k += CTAS * kPoolThreads) {
     if (k < n) {
       const int p = __ldcg(a.copy_src + k), q = __ldcg(a.copy_dst + k);
       a.refs[q] = a.refs[p];
@@ -463,7 +470,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       a.copy_src[k] = a.copy_dst[k] = -1;
     }
   }
-  cluster_sync();      // no CTA leaves while another reads its shared memory
+  pool_sync<CTAS>();      // no CTA leaves while another reads its shared memory
 }
 
 // Table entries of moved pages.  A page's word of the scratch is only good if
@@ -618,16 +625,40 @@ cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t stream) {
   return launch_pdl(free_kernel, dim3(a.batch), dim3(256), 0, stream, a);
 }
 
+// One CTA where there is little to look at: it has no cluster barriers to wait
+// at.  (64 sequences, 10301 pages, 1 to 8 tokens each: 13.9 us with 16 CTAs.)
+static bool one_cta(int num_pages, int batch) { return num_pages <= 32768 && batch <= 128; }
+
+// Clusters of more than 8 CTAs have to be allowed, once a device and kernel.
+// (Two threads may both do it: it is the same call.)
+static cudaError_t allow_big_clusters(const void* kernel, bool (&allowed)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && allowed[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+  return e;
+}
+
 cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (one_cta(a.num_pages, a.batch))
+    return launch_pdl(reserve_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
+  static bool allowed[64];
+  cudaError_t e = allow_big_clusters(reinterpret_cast<const void*>(reserve_kernel<kPoolCtas>), allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(reserve_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  return launch_pdl(reserve_kernel<kPoolCtas>, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  cudaError_t e;
+  if (one_cta(a.num_pages, 0)) {
+    e = launch_pdl(compact_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
+  } else {
+    static bool allowed[64];
+    if ((e = allow_big_clusters(reinterpret_cast<const void*>(compact_kernel<kPoolCtas>), allowed)) != cudaSuccess)
+      return e;
+    e = launch_pdl(compact_kernel<kPoolCtas>, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  }
   if (e != cudaSuccess) return e;
   const long long entries = static_cast<long long>(a.batch) * a.max_pages;
   if (entries == 0) return cudaSuccess;
