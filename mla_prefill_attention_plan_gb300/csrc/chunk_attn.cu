@@ -63,7 +63,8 @@ constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // row maxima and 
 constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
 constexpr int kSmemTotal = kSmemBar + 512 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
-constexpr int kThreads = 256;                // producer, MMA, 4 softmax warps, row lookup, producer
+constexpr int kProducers = 4;                // warps 0, 7, 8, 9
+constexpr int kThreads = 224 + 32 * (kProducers - 1);   // with MMA, 4 softmax warps, row lookup
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
@@ -226,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh->drain), 1);
     for (int s = 0; s < kFound; ++s) {
       mbar_init(smem_u32(&sh->found[s]), 1);
-      mbar_init(smem_u32(&sh->taken[s]), 2);
+      mbar_init(smem_u32(&sh->taken[s]), kProducers);
     }
     mbar_init(smem_u32(&sh->swapped[0]), 2);
     mbar_init(smem_u32(&sh->swapped[1]), 2);
@@ -249,11 +250,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (stop) {
     // (the barriers below are passed by all)
-  } else if (warp == 0 || warp == 7) {
+  } else if (warp == 0 || warp >= 7) {
     // ---------------------------------------------------------------- producers
-    // Two warps, each every other stage: one lane's loop takes about 60 clk an
+    // Warps that take stages in turn: one lane's loop takes about 60 clk an
     // operation and 200 a stage, too slow for the 256 clk of a stage's MMAs.
-    const uint32_t odd = warp == 7;
+    const uint32_t turn = warp == 0 ? 0 : warp - 6;
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
     Walk w = walk_start(p, pair);
     Segment s;
@@ -269,14 +270,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // loads: with a warp's votes and the rows read for each stage, 495 clk).
     auto load = [&](uint32_t n, auto boxes_of) {
       if (elect_one()) {
-        uint32_t st = stage, ph = phase;
-        uint32_t i = (used ^ odd) & 1;
-        if (i && ++st == kStages) st = 0, ph ^= 1;
-        for (; i < n; i += 2) {
+        // The first stage from `used` on that is this warp's.
+        uint32_t i = (turn - used) % kProducers;
+        uint32_t st = stage + i, ph = phase;
+        if (st >= kStages) st -= kStages, ph ^= 1;
+        for (; i < n; i += kProducers) {
           if (!(ok = ready(st, ph, used + i))) break;
           if (rank == 0) mbar_expect_tx(smem_u32(&sh->full[st]), 2 * kStage);
           boxes_of(i, ring + st * kStage, full0 + st * 8);
-          if ((st += 2) >= kStages) st -= kStages, ph ^= 1;
+          if ((st += kProducers) >= kStages) st -= kStages, ph ^= 1;
         }
       }
       __syncwarp();
@@ -305,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && walk_next(p, w, s)) {
       if (s.tiles == 0) continue;
       if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
-      if (!odd && elect_one()) {
+      if (turn == 0 && elect_one()) {
         if (rank == 0) mbar_expect_tx(smem_u32(&sh->q_full), 2 * kQBytes);
         const uint32_t bar = cluster_addr(smem_u32(&sh->q_full), 0);
         for (int c = 0; c < 9; ++c)
