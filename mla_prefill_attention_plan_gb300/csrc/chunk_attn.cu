@@ -65,6 +65,7 @@ constexpr int kSmemTotal = kSmemBar + 512 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
 constexpr int kProducers = 4;                // warps 0, 7, 8, 9
 constexpr int kThreads = 224 + 32 * (kProducers - 1);   // with MMA, 4 softmax warps, row lookup
+static_assert((kProducers & (kProducers - 1)) == 0, "whose stage it is: a difference modulo 2^32");
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
 constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
