@@ -958,7 +958,9 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  *   - without, iff m <= i.
  * out and lse are as in mla_decode over those keys: lse natural, attn_sink[b]
  * one more logit without a value.  A token that sees nothing gets out = 0 and
- * lse = -infinity (the sink's logit with one).
+ * lse = -infinity (the sink's logit with one).  A key that a token does not see
+ * has no part in its result, whatever it holds; one that it sees and that has an
+ * infinite or NaN latent value makes the token's out and lse NaN.
  * Longer chunks than about 170 tokens are as right, but mla_prefill then has
  * less to compute.
  * Rounding: the projected query and the softmax weights are bf16, the latent
@@ -976,7 +978,7 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  * workspace: device memory of mla_chunk_attention_workspace_bytes(...), 256-byte
  *            aligned; for one call at a time
  * Errors: host MLA_ERR_GEOMETRY (num_heads < 1), MLA_ERR_ARG (null or misaligned
- * pointers, bad sizes, more than 16383 heads, total_q_tokens * num_heads of 2^29
+ * pointers, bad sizes, more than 16379 heads, total_q_tokens * num_heads of 2^29
  * or more), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens, more new tokens than 32 * mask_words
  * or a context of more than 2^31 - 8192: sequence b is left out; offsets that

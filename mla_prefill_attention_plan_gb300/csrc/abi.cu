@@ -1024,11 +1024,11 @@ mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uin
                                  const float* attn_sink, void* workspace, size_t workspace_bytes,
                                  int32_t* d_status, mla_stream_t stream) {
   if (num_heads < 1) return MLA_ERR_GEOMETRY;
-  // (Four CTAs a head are launched for the queries: a launch has 65535 rows of them.)
+  // (Four CTAs a head and 17 more are launched first: a launch has 65535 rows of them.)
   if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !page_table || !w_uk || !w_uv ||
       !aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
       batch_size < 1 || total_q_tokens < 0 || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
-      num_heads > 65535 / 4 || !(scale > 0.0f) || (chunk_mask ? mask_words < 1 : mask_words != 0) ||
+      num_heads > 16379 || !(scale > 0.0f) || (chunk_mask ? mask_words < 1 : mask_words != 0) ||
       static_cast<long long>(total_q_tokens) * num_heads >= (1ll << 31) / 4 ||
       static_cast<long long>(num_pages) * page_size >= (1ll << 31) - 64)
     return MLA_ERR_ARG;

@@ -102,8 +102,9 @@ struct ChunkParams {
   float4* o_part;            // [4 pairs][2][64][128]: a pair's first and last segment of each line
   float2* ml_part;           // [4 pairs][128] (max, sum)
   SplitTile* split;          // [2][pairs]
+  const uint32_t* odd_rows;  // [(T + 31) / 32]: tokens whose rows hold an infinity or NaN
   int num_pages, page_size, max_pages, cache_rows;
-  int B, H, words;
+  int B, H, T, words;
   float scale_log2;
   int32_t* status;
 };
@@ -200,6 +201,13 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
   if (p.mask == nullptr) last = s.cached + (s.r0 + s.rows - 1) / p.H + 1;
   s.tiles = max(0, min(s.k1, (last + kTile - 1) / kTile) - s.k0);
   return true;
+}
+
+// The bits of 32 new tokens from token t on (of T).
+__device__ __forceinline__ uint32_t odd_bits(const ChunkParams& p, int t) {
+  const int words = (p.T + 31) / 32, w = t >> 5, by = t & 31;
+  const uint32_t lo = w < words ? p.odd_rows[w] : 0u, hi = w + 1 < words ? p.odd_rows[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, by);
 }
 
 // ------------------------------------------------------------------ attention
@@ -461,8 +469,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < s.tiles; ++j, ++tile) {
         const int slot = tile % kFound;
         const int first = (s.k0 + j) * kTile;
+        const int token0 = static_cast<int>(p.iro[s.b]) - s.cached;     // a new token's number less its position
         auto row_of = [&](int pos) {
-          if (pos >= s.L) return -1;
+          if (pos >= s.L || (pos >= s.cached && (odd_bits(p, token0 + pos) & 1u))) return -1;
           const int i = pos / p.page_size;
           const int page = i < p.max_pages ? pages[i] : -1;
           if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - i * p.page_size);
@@ -470,7 +479,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return -1;
         };
         int whole = -1;                                   // lane g < 4: group g
-        if (aligned && lane < 4 && first + 64 * lane + 64 <= s.L) whole = row_of(first + 64 * lane);
+        const int at = first + 64 * lane, to = at + 64;
+        if (aligned && lane < 4 && to <= s.L) {
+          // (Rows of new tokens before bit 0 of a word are others': a group that is
+          // taken for odd by them is only taken apart.)
+          const bool odd = to > s.cached && (odd_bits(p, token0 + max(at, s.cached)) | odd_bits(p, token0 + max(to - 32, s.cached)));
+          if (!odd) whole = row_of(at);
+        }
         const unsigned parts = __ballot_sync(0xffffffffu, whole < 0) & 15u;
         if (tile >= kFound &&
             !(ok = mbar_wait_warp(smem_u32(&sh->taken[slot]), ((tile / kFound) & 1) ^ 1, status, abort_flag)))
@@ -572,6 +587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const int n = s.n - i;                                    // keys that there are
             see[c] &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+            // New tokens among them that are no finite numbers.
+            const int first = static_cast<int>(p.iro[s.b]) + max(i, 0);
+            if (n > 0 && (see[c] >> max(-i, 0) & odd_bits(p, first)) != 0) sum = __int_as_float(0x7FC00000);
           }
         }
         if (!(ok = mbar_wait_warp(smem_u32(&sh->s_full[buf]), (tile >> 1) & 1, status, abort_flag))) break;
@@ -845,7 +863,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 }
 
 struct Layout {
-  size_t q_full, o_lat, base, schedule, token_seq, o_part, ml_part, split, total;
+  size_t q_full, o_lat, base, schedule, token_seq, odd_rows, o_part, ml_part, split, total;
 };
 Layout layout(int B, int H, int T) {
   const size_t R = static_cast<size_t>(T) * H;
@@ -861,6 +879,7 @@ Layout layout(int B, int H, int T) {
   L.base = take(sizeof(Base) * (static_cast<size_t>(B) + 1));
   L.schedule = take(sizeof(Schedule));
   L.token_seq = take(sizeof(int32_t) * static_cast<size_t>(T));
+  L.odd_rows = take(sizeof(uint32_t) * ((static_cast<size_t>(T) + 31) / 32));
   L.o_part = take(static_cast<size_t>(4 * kMaxPairs) * kRows * 512 * sizeof(float));
   L.ml_part = take(static_cast<size_t>(4 * kMaxPairs) * kRows * sizeof(float2));
   L.split = take(2 * kMaxPairs * sizeof(SplitTile));
@@ -893,12 +912,14 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.o_part = reinterpret_cast<float4*>(ws + L.o_part);
   p.ml_part = reinterpret_cast<float2*>(ws + L.ml_part);
   p.split = reinterpret_cast<SplitTile*>(ws + L.split);
+  p.odd_rows = reinterpret_cast<const uint32_t*>(ws + L.odd_rows);
   p.num_pages = a.num_pages;
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.cache_rows = a.num_pages * a.page_size;
   p.B = a.B;
   p.H = a.H;
+  p.T = a.T;
   p.words = a.mask_words;
   p.scale_log2 = a.scale * kLog2e;
   p.status = a.status;
@@ -928,6 +949,12 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   pa.pairs = pairs;
   pa.masked = a.mask != nullptr;
   pa.status = a.status;
+  pa.kv_cache = a.kv_cache;
+  pa.page_table = a.page_table;
+  pa.num_pages = a.num_pages;
+  pa.page_size = a.page_size;
+  pa.max_pages = a.max_pages;
+  pa.odd_rows = ws + L.odd_rows;
   cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, a.T, a.H, &pa, a.status, stream);
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) !=

@@ -42,6 +42,12 @@ struct ChunkPlanArgs {
   int B, H, T, words, pairs;
   bool masked;
   int32_t* status;
+  // The new tokens' cache rows, and where those with a value that is no finite
+  // number among their 512 latent ones are noted, a bit a token.
+  const void* kv_cache;      // bf16 [num_pages * page_size][576]
+  const int32_t* page_table;
+  int num_pages, page_size, max_pages;
+  uint8_t* odd_rows;         // [(T + 7) / 8]
 };
 
 // The sequence of item (or unit) i of class c: the last one with base <= i.
@@ -169,6 +175,46 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
     if (v0.items[0] == v1.items[0] && v0.items[1] == v1.items[1]) continue;
     for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
   }
+}
+
+// Bits of the tokens [8 group, 8 group + 8), by one CTA.  A key that a row does
+// not see has weight 0, and 0 times infinity or NaN is NaN: rows with such values
+// are left out of the products (a row of zeros is loaded instead), and who sees
+// one gets NaN.  Only new tokens can be hidden from a row of their sequence.
+template <int kThreads>
+__device__ __forceinline__ void find_odd_rows(const ChunkPlanArgs& a, int group) {
+  __shared__ unsigned bits;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) bits = 0;
+  __syncthreads();
+  for (int i = warp; i < 8; i += kThreads / 32) {
+    const int t = 8 * group + i;
+    if (t >= a.T) continue;
+    int lo = 0, hi = a.B;                        // the last sequence that begins at t or before
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.iro[mid] <= static_cast<uint32_t>(t)) lo = mid;
+      else hi = mid;
+    }
+    if (a.iro[lo] > static_cast<uint32_t>(t) || a.iro[lo + 1] <= static_cast<uint32_t>(t)) continue;
+    const long long pos = static_cast<long long>(a.cache_len[lo]) + (t - static_cast<long long>(a.iro[lo]));
+    const long long j = pos / a.page_size;
+    const int page = j < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + j] : -1;
+    if (page < 0 || page >= a.num_pages) continue;
+    const size_t row = static_cast<size_t>(page) * a.page_size + static_cast<size_t>(pos - j * a.page_size);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv_cache) + row * 1152);
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint4 v = src[e * 32 + lane];
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) odd |= (x[u] & 0x7F80u) == 0x7F80u || (x[u] & 0x7F800000u) == 0x7F800000u;
+    }
+    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&bits, 1u << i);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && 8 * group < a.T) a.odd_rows[group] = static_cast<uint8_t>(bits);
 }
 
 }  // namespace chunk

@@ -72,7 +72,9 @@ struct HeadGemm {
 
 // SPLIT > 1: the head's N * SPLIT output columns are shared by SPLIT CTAs
 // (grid.y = H * SPLIT), N each, so that a small M still fills the GPU.
-// PLAN: one more CTA (the last of grid.y) finds chunk attention's schedule.
+// PLAN: more CTAs (the last kPlanRows of grid.y) find chunk attention's schedule
+// and look its new tokens' rows over, 8 of the row tile's 128 tokens each.
+constexpr int kPlanRows = 17;
 template <int N, int K, int STAGES, int SPLIT, int TERMS, bool PLAN>
 __global__ void __launch_bounds__(192, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
@@ -95,8 +97,10 @@ __global__ void __launch_bounds__(192, 1)
   const int m0 = blockIdx.x * 128;
   pdl_enter();
   if (timed_out_before(status)) return;   // an earlier kernel timed out: no work
-  if (PLAN && blockIdx.y == gridDim.y - 1) {
-    if (blockIdx.x == 0) chunk::chunk_plan<192>(plan);
+  if (PLAN && blockIdx.y + kPlanRows >= gridDim.y) {
+    const int y = gridDim.y - 1 - blockIdx.y;
+    if (y > 0) chunk::find_odd_rows<192>(plan, blockIdx.x * (kPlanRows - 1) + y - 1);
+    else if (blockIdx.x == 0) chunk::chunk_plan<192>(plan);
     return;
   }
 
@@ -1070,7 +1074,7 @@ cudaError_t launch_head_gemm(const CUtensorMap& a_map, const CUtensorMap& b_map,
   cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS, PLAN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
   if (e != cudaSuccess) return e;
-  const dim3 grid((M + 127) / 128, H * SPLIT + (PLAN ? 1 : 0));
+  const dim3 grid((M + 127) / 128, H * SPLIT + (PLAN ? kPlanRows : 0));
   return launch_pdl(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS, PLAN>, grid, dim3(192), C::SMEM_TOTAL, stream, a_map,
                     b_map, a_col0, a_hstride, out, out_ld, out_hstride, rope_src, rope_ld, rope_hstride, M, row_seq,
                     status, plan);

@@ -30,7 +30,7 @@ def call(chunk_mask=16, mask_words=1, workspace=256, workspace_bytes=1 << 40, **
 @pytest.mark.parametrize("change", [
     dict(out=None), dict(out=8), dict(q=None), dict(q=24), dict(iro=None), dict(cl=None), dict(kv=None), dict(kv=2),
     dict(pt=None), dict(np=0), dict(ps=0), dict(mp=0), dict(uk=None), dict(uk=8), dict(uv=None), dict(uv=4), dict(B=0),
-    dict(T=-1), dict(scale=0.0), dict(scale=float("nan")), dict(H=16384), dict(T=1 << 22, H=128),
+    dict(T=-1), dict(scale=0.0), dict(scale=float("nan")), dict(H=16380), dict(T=1 << 22, H=128),
     dict(np=1 << 20, ps=1 << 11), dict(mask_words=0), dict(mask_words=-1), dict(chunk_mask=None, mask_words=2)])
 def test_refusals(lib, change):
     assert call(**change) == mla.MLA_ERR_ARG

@@ -462,3 +462,60 @@ def test_a_speculative_step():
         assert ((o.double() - want).norm() / want.norm()).item() <= 2 * WHOLE
         assert (l - lse[[b * n_draft + k for k in kept[b]]]).abs().max().item() <= 1e-5
     assert st.item() == 0
+
+
+def poisoned(c, j, columns, value):
+    """Context position j of sequence 0 with a value that is no finite number in some columns."""
+    row = int(c.table[0, j // c.page]) * c.page + j % c.page
+    c.kv_d[row, columns] = value
+
+
+@pytest.mark.parametrize("page", [64, 16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("columns", [slice(0, 512), slice(7, 8), slice(511, 512), slice(512, 576), slice(575, 576)])
+@pytest.mark.parametrize("mask", ["tree", "causal"])
+def test_a_key_that_is_no_number_does_not_reach_who_does_not_see_it(mask, columns, value, page):
+    """New token 5 of 9, hidden from the tokens before it and (tree) from its siblings' branches; everything else as
+    without it."""
+    c = Case([9, 2], [190, 300], 4, page, mask=mask, seed=3)
+    out, lse, slack = c.oracle()
+    poisoned(c, 195, columns, value)
+    mla.check(c.call())
+    sees = [i >= 5 if c.mask is None else bool(c.mask[i] >> 5 & 1) for i in range(9)]
+    assert any(sees) and not all(sees)
+    got, l = c.out.clone(), c.lse.clone()
+    for i in range(9):
+        if sees[i]:
+            if columns.stop <= 512:
+                assert torch.isnan(got[i]).all() and torch.isnan(l[i]).all()
+            c.out[i], c.lse[i] = FILL, FILL
+            lse[i] = np.nan
+    c.compare(out, lse, slack)
+
+
+def test_keys_that_are_no_numbers_in_a_long_chunk():
+    """Among 200 new tokens over several groups of 64, each seen by itself alone."""
+    n = 200
+    c = Case([3, n], [40, 77], 2, 64, mask=[1, 2, 4] + [1 << i for i in range(n)], words=7)
+    out, lse, slack = c.oracle()
+    odd = [0, 1, 31, 32, 50, 63, 64, 120, 179, 180, 199]
+    for m in odd:
+        j = 77 + m
+        c.kv_d[int(c.table[1, j // 64]) * 64 + j % 64, m % 512] = float("nan") if m % 2 else float("inf")
+    mla.check(c.call())
+    for m in odd:
+        assert torch.isnan(c.out[3 + m]).all() and torch.isnan(c.lse[3 + m]).all()
+        c.out[3 + m], c.lse[3 + m] = FILL, FILL
+        lse[3 + m] = np.nan
+    c.compare(out, lse, slack)
+
+
+def test_the_largest_numbers_are_numbers():
+    """The largest bf16 among a hidden row's values: no part of it reaches the others."""
+    c = Case([4], [100], 2, 16, mask=[1, 2, 4, 8])
+    out, lse, slack = c.oracle()
+    poisoned(c, 102, slice(0, 512), 3.3895e38)
+    mla.check(c.call())
+    c.out[2], c.lse[2] = FILL, FILL
+    lse[2] = np.nan
+    c.compare(out, lse, slack)
