@@ -59,12 +59,12 @@ constexpr int kSmemP = kSmemQ + kQBytes;
 constexpr int kSmemRing = kSmemP + kPBytes;
 constexpr int kFound = 4;                    // tiles whose rows have been looked up
 constexpr int kSmemBoxes = kSmemRing + kStages * kStage;      // their boxes: 4 groups of 64 rows each
-constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // row maxima and sums of both halves
+constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // a row's maxima and sums of both threads
 constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
-constexpr int kSmemTotal = kSmemBar + 512 + 1024;
+constexpr int kSmemTotal = kSmemBar + 1024 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
 constexpr int kProducers = 4;                // warps 0, 7, 8, 9
-constexpr int kThreads = 224 + 32 * (kProducers - 1);   // with MMA, 4 softmax warps, row lookup
+constexpr int kThreads = 192 + 32 * kProducers;   // with MMA (1), softmax (2 .. 5), row lookup (6)
 static_assert((kProducers & (kProducers - 1)) == 0, "whose stage it is: a difference modulo 2^32");
 constexpr uint32_t kTmO = 256;               // TMEM: S 2 x 128, O 2 x 128 columns
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kTile, false, false);
@@ -75,19 +75,6 @@ constexpr uint32_t kIdescO = idesc_bf16(kRows, 256, false, true);
 struct CacheMaps {
   CUtensorMap box[8], wide;
 };
-
-struct ChunkSmem {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, q_free;
-  uint64_t s_full[2], p_full, pv_done, drain;
-  uint64_t swapped[2];       // the two warps that share rows have both written their words
-  uint32_t tmem;
-  int abort;
-  uint64_t found[kFound], taken[kFound];
-  alignas(16) int row[kFound][4];   // first cache row of a group of 64 consecutive ones, or -1:
-  int boxes[kFound][4];      // it is this many boxes
-};
-static_assert(sizeof(ChunkSmem) <= 512, "barrier block");
 
 struct ChunkParams {
   const uint32_t* iro;
@@ -113,7 +100,7 @@ struct ChunkParams {
 struct Segment {
   int b, row0, r0, rows;      // sequence, first global row, first row within the sequence, valid rows
   int k0, k1, kt;             // key tiles [k0, k1) of the row tile's kt
-  int tiles;                  // of them, those that a row sees any key of
+  int tiles;                  // of them, those that a row sees any key of (-1: no more segments)
   int cached, n, L;
   int c, x;                   // class; the position of k0 on the class's line (-1: a whole item taken in turn)
 };
@@ -203,6 +190,23 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
   return true;
 }
 
+constexpr int kSegments = 4;     // segments that the lookup warp is ahead by
+
+struct ChunkSmem {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full, q_free;
+  uint64_t s_full[2], p_full, pv_done, drain;
+  uint64_t swapped[2];       // the two warps that share rows have both written their words
+  uint32_t tmem;
+  int abort;
+  uint64_t found[kFound], taken[kFound];
+  alignas(16) int row[kFound][4];   // first cache row of a group of 64 consecutive ones, or -1:
+  int boxes[kFound][4];      // it is this many boxes
+  uint64_t seg_full[kSegments], seg_free[kSegments];
+  Segment segment[kSegments];
+};
+static_assert(sizeof(ChunkSmem) <= 1024, "barrier block");
+
 // The bits of 32 new tokens from token t on (of T).
 __device__ __forceinline__ uint32_t odd_bits(const ChunkParams& p, int t) {
   const int words = (p.T + 31) / 32, w = t >> 5, by = t & 31;
@@ -238,6 +242,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh->found[s]), 1);
       mbar_init(smem_u32(&sh->taken[s]), kProducers);
     }
+    for (int s = 0; s < kSegments; ++s) {
+      mbar_init(smem_u32(&sh->seg_full[s]), 1);
+      mbar_init(smem_u32(&sh->seg_free[s]), kProducers + 4 + (rank == 0));
+    }
     mbar_init(smem_u32(&sh->swapped[0]), 2);
     mbar_init(smem_u32(&sh->swapped[1]), 2);
     fence_mbar_init();
@@ -256,16 +264,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool stop = cluster_any(abort_flag);     // an earlier kernel timed out: no work
   const uint32_t ring = smem_u32(smem + kSmemRing);
   volatile int never = 0;
+  // The next segment that the lookup warp has found (by a warp; by one lane of the
+  // MMA warp).
+  uint32_t seg = 0;
+  auto next_segment = [&](Segment& s, bool alone) {
+    const uint32_t i = seg % kSegments, full = smem_u32(&sh->seg_full[i]), parity = (seg / kSegments) & 1;
+    if (alone) {
+      if (!mbar_wait(full, parity, status, abort_flag)) return false;
+    } else if (!mbar_wait_warp(full, parity, status, abort_flag)) {
+      return false;
+    }
+    s = sh->segment[i];
+    if (!alone) __syncwarp();
+    if (alone || lane == 0) mbar_arrive(smem_u32(&sh->seg_free[i]));
+    ++seg;
+    return s.tiles >= 0;
+  };
 
   if (stop) {
     // (the barriers below are passed by all)
-  } else if (warp == 0 || warp >= 7) {
+  } else if (warp == 0 || (warp >= 7 && warp < 6 + kProducers)) {
     // ---------------------------------------------------------------- producers
     // Warps that take stages in turn: one lane's loop takes about 60 clk an
     // operation and 200 a stage, too slow for the 256 clk of a stage's MMAs.
     const uint32_t turn = warp == 0 ? 0 : warp - 6;
     const int2* const boxes = reinterpret_cast<const int2*>(smem + kSmemBoxes);
-    Walk w = walk_start(p, pair);
     Segment s;
     uint32_t stage = 0, phase = 0, segments = 0, used = 0, tile = 0;
     bool ok = true;
@@ -313,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // K of tile j, V of the tile before, in the order of use.
     const int vcol = 128 * static_cast<int>(rank);
-    while (ok && walk_next(p, w, s)) {
+    while (ok && next_segment(s, false)) {
       if (s.tiles == 0) continue;
       if (segments > 0 && !(ok = mbar_wait_warp(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag))) break;
       if (turn == 0 && elect_one()) {
@@ -387,7 +410,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {
       if (rank == 0) {
-        Walk w = walk_start(p, pair);
         Segment s;
         uint32_t stage = 0, phase = 0, segments = 0, tile = 0, p_phase = 0;
         bool ok = true;
@@ -413,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tc_commit_pair(smem_u32(&sh->s_full[buf]), 3);
         };
-        while (ok && walk_next(p, w, s)) {
+        while (ok && next_segment(s, true)) {
           if (s.tiles == 0) continue;
           if (!(ok = mbar_wait(smem_u32(&sh->q_full), segments & 1, status, abort_flag))) break;
           ++segments;
@@ -451,6 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 6) {
     // ---------------------------------------------------------------- row lookup
+    // The segments in order, for all roles (a walk is a chain of loads), and:
     // Where a tile's rows are in the cache.  Four groups of 64 that each are
     // consecutive rows need a row each; any other group is a list of boxes
     // (cache row, first row << 8 | log2 rows): every run of consecutive rows is
@@ -463,7 +486,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t tile = 0;
     bool ok = true;
     const bool aligned = p.page_size % 64 == 0;
-    while (ok && walk_next(p, w, s)) {
+    for (bool more = true; ok && more;) {
+      more = walk_next(p, w, s);
+      if (!more) s.tiles = -1;
+      const uint32_t i = seg % kSegments;
+      if (seg >= kSegments &&
+          !(ok = mbar_wait_warp(smem_u32(&sh->seg_free[i]), ((seg / kSegments) & 1) ^ 1, status, abort_flag)))
+        break;
+      if (lane == 0) {
+        sh->segment[i] = s;
+        mbar_arrive(smem_u32(&sh->seg_full[i]));
+      }
+      ++seg;
       const int32_t* const pages = p.page_table + static_cast<size_t>(s.b) * p.max_pages;
 #pragma unroll 1
       for (int j = 0; j < s.tiles; ++j, ++tile) {
@@ -532,47 +566,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    // Two threads share a row: half of a tile's keys and of O's columns each, as
+    // its two TMEM lanes hold them.  (Two warps for each quarter of the lanes take
+    // as long: the softmax is not what a tile waits for.)
+    constexpr int kChunks = 4;                   // of 32 keys
     const int quarter = warp & 3;
     const int tl = quarter * 32 + lane;          // TMEM lane
     const int row = tl & 63, half = tl >> 6;     // row of this CTA; which columns of it
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][128]
-    const uint32_t sp = smem_u32(smem + kSmemP);
+    const uint32_t o_at = tmem + lane_off + kTmO;
+    float* const red = reinterpret_cast<float*>(smem + kSmemRed);     // [2][2][64]
+    // The warp's part of P: 32 rows of two blocks of 64 keys.
+    const uint32_t mine = smem_u32(smem + kSmemP) + half * 2 * 8192 + (tl & 32) * 128;
     const uint32_t p_bar = cluster_addr(smem_u32(&sh->p_full), 0);
-    Walk w = walk_start(p, pair);
     Segment s;
     uint32_t tile = 0, swaps = 0;
     bool ok = true;
-    // The word of the thread with the other columns of the row (two sets of
-    // words: a set is written again only after the other has been swapped).
-    auto swap = [&](float v, float& other) {
+    // The words of the row's two threads (two sets: a set is written again only
+    // after the other has been swapped).
+    auto swap = [&](float v, float (&all)[2]) {
       float* const words = red + (swaps & 1) * 128;
-      words[tl] = v;
+      words[(half) * 64 + row] = v;
       __syncwarp();
       const uint32_t bar = smem_u32(&sh->swapped[quarter & 1]);
       if (lane == 0) mbar_arrive(bar);
       if (!mbar_wait_warp(bar, swaps & 1, status, abort_flag)) return false;
       ++swaps;
-      other = words[tl ^ 64];
+      all[0] = words[row], all[1] = words[64 + row];
       return true;
     };
-    while (ok && walk_next(p, w, s)) {
+    while (ok && next_segment(s, false)) {
       const int local = static_cast<int>(rank) * 64 + row;            // row of the pair's tile
       const bool live = local < s.rows;
       const int token = live ? (s.r0 + local) / p.H : 0;              // within the sequence
-      const uint32_t* mask_row =
-          p.mask != nullptr ? p.mask + static_cast<size_t>(p.iro[s.b] + token) * p.words : nullptr;
+      const int token0 = static_cast<int>(p.iro[s.b]);
+      const uint32_t* mask_row = p.mask != nullptr ? p.mask + static_cast<size_t>(token0 + token) * p.words : nullptr;
       float ref = kNegInf, sum = 0.0f;
       for (int j = 0; j < s.tiles; ++j, ++tile) {
         const uint32_t buf = tile & 1;
         const int k0 = (s.k0 + j) * kTile + half * 128;
-        const bool partly = k0 + 128 > s.cached;
-        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        const bool partly = k0 + 32 * kChunks > s.cached;
+        uint32_t see[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) see[c] = 0xffffffffu;
         if (partly) {
           // Which of the thread's keys the row sees, a bit each (loaded while the
           // scores are computed).
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             const int i = k0 + c * 32 - s.cached;                     // new token of the first key
             if (i + 32 <= 0) continue;
             if (mask_row != nullptr) {
@@ -588,20 +629,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int n = s.n - i;                                    // keys that there are
             see[c] &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
             // New tokens among them that are no finite numbers.
-            const int first = static_cast<int>(p.iro[s.b]) + max(i, 0);
-            if (n > 0 && (see[c] >> max(-i, 0) & odd_bits(p, first)) != 0) sum = __int_as_float(0x7FC00000);
+            if (n > 0 && (see[c] >> max(-i, 0) & odd_bits(p, token0 + max(i, 0))) != 0)
+              sum = __int_as_float(0x7FC00000);
           }
         }
         if (!(ok = mbar_wait_warp(smem_u32(&sh->s_full[buf]), (tile >> 1) & 1, status, abort_flag))) break;
         tc_fence_after();
-        // Two passes over the scores, 32 at a time (a tile's 128 unrolled are 20 KB of
-        // code, which a short context fetches from L2 for one use): the maximum,
-        // then the weights.  In a tile that the row does not see all of, the first
-        // pass stores the scores back with -infinity in them.
+        // Two passes over the scores, 32 at a time (unrolled further they are code
+        // that a short context fetches from L2 for one use): the maximum, then the
+        // weights.  In a tile that the row does not see all of, the first pass
+        // stores the scores back with -infinity in them.
         const uint32_t sc = tmem + lane_off + buf * 128;
         float top = kNegInf;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t x[32];
           tmem_ld32(sc + c * 32, x);
           tmem_ld_wait();
@@ -616,9 +657,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         }
         if (partly) tmem_st_wait();
-        float other;
-        if (!(ok = swap(top, other))) break;
-        top = fmaxf(top, other) * p.scale_log2;
+        float all[2];
+        if (!(ok = swap(top, all))) break;
+        top = fmaxf(all[0], all[1]) * p.scale_log2;
         float factor = 1.0f;
         if (top > ref + kRescale || (ref == kNegInf && top > kNegInf)) {
           factor = ref == kNegInf ? 0.0f : ex2(ref - top);
@@ -632,23 +673,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
+            tmem_ld32(o_at + c * 32, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               o[e] = factor == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * factor);
-            tmem_st32(tmem + lane_off + kTmO + c * 32, o);
+            tmem_st32(o_at + c * 32, o);
           }
           tmem_st_wait();
         }
         const float shift = ref == kNegInf ? 0.0f : ref;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t x[32];
           tmem_ld32(sc + c * 32, x);
           tmem_ld_wait();
           // Chunks of 8 keys (16 bytes) of the row, in the 128-byte swizzle.
-          const uint32_t dst = sp + (half * 2 + (c >> 1)) * 8192 + row * 128;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t pk[4];
@@ -659,7 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               sum += a + b;
               pk[e] = pack_bf16(a, b);
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((((c & 1) * 4 + u) ^ (row & 7)) << 4)),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (c >> 1) * 8192 + lane * 128 + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4)),
                          "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
                          : "memory");
           }
@@ -674,67 +714,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait_warp(smem_u32(&sh->pv_done), (tile - 1) & 1, status, abort_flag))) break;
         tc_fence_after();
       }
-      float other;
-      if (!(ok = swap(sum, other))) break;
-      sum += other;
+      float all[2];
+      if (!(ok = swap(sum, all))) break;
+      sum = all[0] + all[1];
       const bool none = sum == 0.0f;                 // the row saw nothing
-      const bool starts = s.k0 == 0, ends = s.k1 == s.kt;
+      const bool starts = s.k0 == 0, ends = s.k1 == s.kt, first = half == 0;
       if (starts && ends) {
         if (p.sink != nullptr) {
           const float sk = p.sink[s.b] * kLog2e;
           const float m = fmaxf(ref, sk), f = ref == kNegInf ? 0.0f : ex2(ref - m);
           const float add = sk == kNegInf ? 0.0f : ex2(sk - m);
-          if (p.lse != nullptr && live && half == 0)
-            p.lse[s.row0 + local] = m == kNegInf ? kNegInf : (m + log2f(fmaf(sum, f, add))) * kLn2;
+          if (p.lse != nullptr && live && first)
+            p.lse[s.row0 + local] = m == kNegInf && none ? kNegInf : (m + log2f(fmaf(sum, f, add))) * kLn2;
           sum = fmaf(sum, f, add);
-          sum = f == 0.0f ? __builtin_huge_valf() : sum / f;
-        } else if (p.lse != nullptr && live && half == 0) {
-          p.lse[s.row0 + local] = sum == 0.0f ? kNegInf : (ref + log2f(sum)) * kLn2;
+          sum = f == 0.0f && none ? __builtin_huge_valf() : sum / f;
+        } else if (p.lse != nullptr && live && first) {
+          p.lse[s.row0 + local] = none ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
-        const float inv = 1.0f / sum;
-        const float unit = none ? 0.0f : inv;
-        // Both terms of 128 columns a time through the warp's own part of P (32 rows
-        // x 256 bytes), so that rows leave in whole lines.
-        const int row0 = tl & 32;                                     // the warp's first row
-        const uint32_t mine = sp + half * 2 * 8192 + row0 * 128;
+        // (A row that saw nothing has zeros in O: no key of its sequence is there
+        // but finite ones with weight 0.)
+        const float unit = none ? 0.0f : 1.0f / sum;
+        // 32 columns at a time through the warp's part of P (32 rows x 128 bytes):
+        // the first term, the upper halves of the floats, then the second, what is
+        // left of them, so that rows leave in whole sectors.
 #pragma unroll 1
-        for (int u = 0; u < 4; ++u) {                                 // (256 columns, term)
-          const int m = u >> 1;
+        for (int u = 0; u < 8; ++u) {
+          uint32_t o[32];
+          tmem_ld32(o_at + u * 32, o);
+          tmem_ld_wait();
           __syncwarp();
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kTmO + m * 128 + c * 32, o);
-            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t h[4];
+          for (int e = 0; e < 4; ++e) {
+            uint32_t h[4], l[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i]) * unit;
-                const float b = none ? 0.0f : __uint_as_float(o[e * 8 + 2 * i + 1]) * unit;
-                h[i] = pack_bf16(a, b);
-                if (u & 1) h[i] = pack_bf16(a - bf16_lo(h[i]), b - bf16_hi(h[i]));
-              }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               mine + (c >> 1) * 8192 + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)),
-                           "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                           : "memory");
+            for (int i = 0; i < 4; ++i) {
+              const float a = __uint_as_float(o[e * 8 + 2 * i]) * unit, b = __uint_as_float(o[e * 8 + 2 * i + 1]) * unit;
+              h[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+              l[i] = pack_bf16(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                               b - __uint_as_float(__float_as_uint(b) & 0xFFFF0000u));
             }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((e ^ (lane & 7)) << 4)),
+                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + (((4 + e) ^ (lane & 7)) << 4)),
+                         "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3])
+                         : "memory");
           }
           __syncwarp();
-          const int chunk = lane & 15;
-#pragma unroll 4
-          for (int i = lane >> 4; i < 32; i += 2) {
+          const int chunk = lane & 7;
+          __nv_bfloat16* const dst =
+              p.o_lat + (chunk >> 2) * 512 + (u >> 2) * 256 + half * 128 + (u & 3) * 32 + (chunk & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
             uint4 v;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(mine + (chunk >> 3) * 8192 + i * 128 + (((chunk & 7) ^ (i & 7)) << 4))
+                         : "r"(mine + r * 128 + ((chunk ^ (r & 7)) << 4))
                          : "memory");
-            const int to = static_cast<int>(rank) * 64 + row0 + i;
-            if (to < s.rows)
-              *reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(s.row0 + to) * 1024 + (u & 1) * 512 + m * 256 +
-                                        half * 128 + chunk * 8) = v;
+            const int to = static_cast<int>(rank) * 64 + (tl & 32) + r;
+            if (to < s.rows) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(s.row0 + to) * 1024) = v;
           }
         }
         __syncwarp();
@@ -742,14 +781,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int worker = s.c == 0 ? pair >> 1 : pair;
         const int* const tail = p.schedule->tail[s.c];
         const int slot = 4 * pair + 2 * s.c + (s.x == tail[worker] ? 0 : 1);
-        if (half == 0) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
+        if (first) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
         if (s.tiles > 0) {
-          // Laid out as the threads hold it: [CTA][column / 4 of the 256][thread].
-          float4* dst = p.o_part + (static_cast<size_t>(slot) * 2 + rank) * 64 * 128 + tl;
+          // Laid out as the threads hold it: [CTA][column / 4 of the 256][TMEM lane].
+          float4* dst = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64) * 128 + tl;
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kTmO + c * 32, o);
+            tmem_ld32(o_at + c * 32, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -760,14 +799,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ends && tl == 0 && rank == 0) {
           // The worker in whose part of the line the row tile begins.
           const int x0 = s.x - s.k0;
-          int first = worker;
-          while (tail[first] > x0) --first;
+          int from = worker;
+          while (tail[from] > x0) --from;
           SplitTile t;
           t.row0 = s.row0;
           t.rows = s.rows;
           t.seq = s.b;
-          t.first = first;
-          t.slot = tail[first] == x0 ? 0 : 1;
+          t.first = from;
+          t.slot = tail[from] == x0 ? 0 : 1;
           p.split[s.c * pairs + pair] = t;
         }
       }
