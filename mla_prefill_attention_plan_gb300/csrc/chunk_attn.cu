@@ -504,21 +504,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int slot = tile % kFound;
         const int first = (s.k0 + j) * kTile;
         const int token0 = static_cast<int>(p.iro[s.b]) - s.cached;     // a new token's number less its position
-        auto row_of = [&](int pos) {
-          if (pos >= s.L || (pos >= s.cached && (odd_bits(p, token0 + pos) & 1u))) return -1;
+        // The page of a position (-1: none there), and its row.
+        auto page_of = [&](int pos) {
           const int i = pos / p.page_size;
-          const int page = i < p.max_pages ? pages[i] : -1;
-          if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - i * p.page_size);
+          return pos < s.L && i < p.max_pages ? pages[i] : -1;
+        };
+        auto row_of = [&](int pos, int page) {
+          if (pos >= s.L) return -1;
+          if (page >= 0 && page < p.num_pages) return page * p.page_size + pos % p.page_size;
           set_status(status, MLA_DEV_BAD_PAGE);
           return -1;
         };
         int whole = -1;                                   // lane g < 4: group g
         const int at = first + 64 * lane, to = at + 64;
         if (aligned && lane < 4 && to <= s.L) {
+          const int page = page_of(at);
           // (Rows of new tokens before bit 0 of a word are others': a group that is
           // taken for odd by them is only taken apart.)
           const bool odd = to > s.cached && (odd_bits(p, token0 + max(at, s.cached)) | odd_bits(p, token0 + max(to - 32, s.cached)));
-          if (!odd) whole = row_of(at);
+          if (!odd) whole = row_of(at, page);
         }
         const unsigned parts = __ballot_sync(0xffffffffu, whole < 0) & 15u;
         if (tile >= kFound &&
@@ -527,8 +531,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane < 4) sh->row[slot][lane] = whole;
         if (parts != 0) {                                 // all lookups in flight together
           int* const rows = reinterpret_cast<int*>(boxes + slot * 256);
+          int page[8];
+          bool odd[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rows[(e >> 1) * 128 + (e & 1) * 32 + lane] = row_of(first + 32 * e + lane);
+          for (int e = 0; e < 8; ++e) page[e] = page_of(first + 32 * e + lane);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int pos = first + 32 * e + lane;
+            odd[e] = pos >= s.cached && pos < s.L && (odd_bits(p, token0 + pos) & 1u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = row_of(first + 32 * e + lane, page[e]);
+            rows[(e >> 1) * 128 + (e & 1) * 32 + lane] = odd[e] ? -1 : row;
+          }
         }
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
@@ -807,6 +823,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           t.seq = s.b;
           t.first = from;
           t.slot = tail[from] == x0 ? 0 : 1;
+          t.parts[0] = t.parts[1] = t.parts[2] = 0;
+          for (int q = from; q <= worker; ++q)           // (parts of the line may be empty)
+            if (tail[q] != tail[q + 1]) t.parts[(q - from) >> 5] |= 1u << ((q - from) & 31);
           p.split[s.c * pairs + pair] = t;
         }
       }
@@ -824,81 +843,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ merge
 // Split row tiles: blockIdx.x is the (class, pair) in whose part one ends.  A
-// warp takes 32 of the attention's threads' rows and 32 of their 256 columns.
-constexpr int kMergeSlices = 8, kMergeWarps = 8;
+// warp takes 32 of the attention's threads' rows and 32 of their 256 columns,
+// kMergeTurns times.  What a short context waits for here are chains of loads, so
+// the sums and the rows of two parts are asked for at once, as soon as the tile's
+// record is there.
+constexpr int kMergeSlices = 4, kMergeWarps = 8, kMergeTurns = 64 / (kMergeSlices * kMergeWarps);
 
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pairs) {
   pdl_enter();
-  if (timed_out_before(p.status)) return;
   const int lane = threadIdx.x & 31;
-  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs;
   const SplitTile t = p.split[blockIdx.x];
-  if (t.rows <= 0) return;
-  const int unit = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const int rank = unit >> 5, quarter = unit >> 3 & 3, part = unit & 7;     // CTA, its rows, their columns
-  const int tl = quarter * 32 + lane, half = tl >> 6;
-  const int r = rank * 64 + (tl & 63);
-  const int worker = c == 0 ? pair >> 1 : pair;
-  const int* const tail = p.schedule->tail[c];
+  if (timed_out_before(p.status) || t.rows <= 0) return;
+  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs;
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
-  // Worker q's slot, or -1 (an empty part of the line): a lane looks it up for
-  // one of 32 workers at a time.
-  auto slots = [&](int q0) {
-    const int q = q0 + lane;
-    if (q > worker || tail[q] == tail[q + 1]) return -1;
-    return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
-  };
-  float top = sink;
-  for (int q0 = t.first; q0 <= worker; q0 += 32) {
-    const int mine = slots(q0);
-    for (unsigned m = __ballot_sync(0xffffffffu, mine >= 0); m != 0; m &= m - 1) {
-      const int slot = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1);
-      top = fmaxf(top, p.ml_part[slot * kRows + r].x);
-    }
-  }
-  float sum = sink == kNegInf ? 0.0f : ex2(sink - top);
-  float4 o[8] = {};
-  for (int q0 = t.first; q0 <= worker; q0 += 32) {
-    const int mine = slots(q0);
-    for (unsigned m = __ballot_sync(0xffffffffu, mine >= 0); m != 0; m &= m - 1) {
-      const int slot = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1);
-      const float2 ml = p.ml_part[slot * kRows + r];
-      // (A part that saw nothing may have stored no rows.)
-      const bool any = ml.y != 0.0f;
-      const float f = ml.x == kNegInf ? ml.y * 0.0f : ex2(ml.x - top);
-      if (any) sum = fmaf(ml.y, f, sum);
-      const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * 8) * 128 + tl;
+#pragma unroll 1
+  for (int turn = 0; turn < kMergeTurns; ++turn) {
+    const int unit = (turn * kMergeSlices + blockIdx.y) * kMergeWarps + (threadIdx.x >> 5);
+    const int rank = unit >> 5, quarter = unit >> 3 & 3, part = unit & 7;     // CTA, its rows, their columns
+    const int tl = quarter * 32 + lane, half = tl >> 6;
+    const int r = rank * 64 + (tl & 63);
+    uint32_t left[3] = {t.parts[0], t.parts[1], t.parts[2]};
+    auto next_slot = [&]() {                      // of the next part, or -1
+      const int w = left[0] ? 0 : left[1] ? 1 : 2;
+      const uint32_t m = w == 0 ? left[0] : w == 1 ? left[1] : left[2];
+      if (m == 0) return -1;
+      const int q = t.first + 32 * w + __ffs(m) - 1;
+      if (w == 0) left[0] &= m - 1;
+      else if (w == 1) left[1] &= m - 1;
+      else left[2] &= m - 1;
+      return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
+    };
+    float top = sink, sum = sink == kNegInf ? 0.0f : 1.0f;
+    float4 o[8] = {};
+    for (int s0 = next_slot(); s0 >= 0; s0 = next_slot()) {
+      const int s1 = next_slot();
+      float4 v[2][8];
+      float2 ml[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float4 v = __ldcs(src + e * 128);
-        if (any) {
-          o[e].x = fmaf(v.x, f, o[e].x);
-          o[e].y = fmaf(v.y, f, o[e].y);
-          o[e].z = fmaf(v.z, f, o[e].z);
-          o[e].w = fmaf(v.w, f, o[e].w);
+      for (int u = 0; u < 2; ++u) {
+        const int slot = u == 0 || s1 < 0 ? s0 : s1;
+        ml[u] = p.ml_part[slot * kRows + r];
+        const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * 8) * 128 + tl;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = __ldcs(src + e * 128);
+      }
+      if (s1 < 0) ml[1] = make_float2(kNegInf, 0.0f);
+      const float most = fmaxf(top, fmaxf(ml[0].x, ml[1].x));
+      const float keep = top == kNegInf ? 0.0f : ex2(top - most);
+      top = most;
+      sum *= keep;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (ml[u].y == 0.0f) continue;           // it saw nothing; it may have stored no rows
+        const float f = ml[u].x == kNegInf ? ml[u].y * 0.0f : ex2(ml[u].x - top);
+        sum = fmaf(ml[u].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e].x = fmaf(v[u][e].x, f, o[e].x);
+          o[e].y = fmaf(v[u][e].y, f, o[e].y);
+          o[e].z = fmaf(v[u][e].z, f, o[e].z);
+          o[e].w = fmaf(v[u][e].w, f, o[e].w);
         }
       }
     }
-  }
-  if (r >= t.rows) return;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint4* hi = reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (part >> 2) * 256 + half * 128 +
-                                       (part & 3) * 32);
+    if (r >= t.rows) continue;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint4* hi = reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (part >> 2) * 256 +
+                                         half * 128 + (part & 3) * 32);
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float v[8] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv,
-                        o[e + 1].x * inv, o[e + 1].y * inv, o[e + 1].z * inv, o[e + 1].w * inv};
-    uint32_t h[4], l[4];
+    for (int e = 0; e < 8; e += 2) {
+      const float x[8] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv,
+                          o[e + 1].x * inv, o[e + 1].y * inv, o[e + 1].z * inv, o[e + 1].w * inv};
+      uint32_t h[4], l[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-      l[i] = pack_bf16(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
+      for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        l[i] = pack_bf16(x[2 * i] - bf16_lo(h[i]), x[2 * i + 1] - bf16_hi(h[i]));
+      }
+      hi[e >> 1] = make_uint4(h[0], h[1], h[2], h[3]);
+      hi[64 + (e >> 1)] = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    hi[e >> 1] = make_uint4(h[0], h[1], h[2], h[3]);
-    hi[64 + (e >> 1)] = make_uint4(l[0], l[1], l[2], l[3]);
+    if (p.lse != nullptr && part == 0 && half == 0)
+      p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
   }
-  if (p.lse != nullptr && part == 0 && half == 0)
-    p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
 }
 
 struct Layout {

@@ -10,11 +10,13 @@ namespace chunk {
 constexpr int kTile = 256;                   // keys of a tile
 constexpr int kRows = 128;                   // query rows of a pair of SMs
 constexpr int kMaxPairs = 76;
+static_assert(kMaxPairs <= 96, "bits of SplitTile::parts");
 
 // A split row tile, noted by the worker in whose part of the line it ends.
 struct SplitTile {
   int row0, rows, seq;
   int first, slot;      // the worker in whose part it begins, and its slot there
+  uint32_t parts[3];    // bit q: worker first + q holds a part of it
 };
 
 // Items of class c have workers(c) workers: groups of two pairs, or pairs.
