@@ -847,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // kMergeTurns times.  What a short context waits for here are chains of loads, so
 // the sums and the rows of two parts are asked for at once, as soon as the tile's
 // record is there.
-constexpr int kMergeSlices = 4, kMergeWarps = 8, kMergeTurns = 64 / (kMergeSlices * kMergeWarps);
+constexpr int kMergeSlices = 8, kMergeWarps = 8, kMergeTurns = 64 / (kMergeSlices * kMergeWarps);
 
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pairs) {
   pdl_enter();
