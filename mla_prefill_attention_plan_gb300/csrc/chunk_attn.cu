@@ -91,6 +91,7 @@ struct ChunkParams {
   SplitTile* split;          // [2][pairs]
   const uint32_t* odd_rows;  // [(T + 31) / 32]: tokens whose rows hold an infinity or NaN
   int num_pages, page_size, max_pages, cache_rows;
+  FastDiv by_page;
   int B, H, T, words;
   float scale_log2;
   int32_t* status;
@@ -506,12 +507,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int token0 = static_cast<int>(p.iro[s.b]) - s.cached;     // a new token's number less its position
         // The page of a position (-1: none there), and its row.
         auto page_of = [&](int pos) {
-          const int i = pos / p.page_size;
+          const int i = fast_div(pos, p.by_page);
           return pos < s.L && i < p.max_pages ? pages[i] : -1;
         };
         auto row_of = [&](int pos, int page) {
           if (pos >= s.L) return -1;
-          if (page >= 0 && page < p.num_pages) return page * p.page_size + pos % p.page_size;
+          if (page >= 0 && page < p.num_pages) return page * p.page_size + (pos - fast_div(pos, p.by_page) * p.page_size);
           set_status(status, MLA_DEV_BAD_PAGE);
           return -1;
         };
@@ -984,6 +985,7 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.num_pages = a.num_pages;
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
+  p.by_page = fast_divisor(a.page_size);
   p.cache_rows = a.num_pages * a.page_size;
   p.B = a.B;
   p.H = a.H;
