@@ -125,6 +125,7 @@ struct PoolSmem {
   int tally[4];                   // of this CTA: pages wanted (live), movers, free pages, flags
   int shared_tally[2];            // pages wanted and copies once the sharers are known
   int scan[kPoolWarps], scan2[kPoolWarps];
+  int n_long, long_ones[kPoolThreads];
 };
 
 // The warp's contiguous range of page ids, a multiple of 128 long (an int4 a
@@ -170,6 +171,32 @@ __device__ __forceinline__ bool touched(const PagesReserveArgs& a, int b, Touche
   return true;
 }
 
+// Sequences [b0, b1) of a CTA, 1024 at a time: those that write to few pages by
+// a thread each (one_thread(b, pages)), the others by a warp each (one_warp).
+constexpr int kFewPages = 4;
+template <typename Thread, typename Warp>
+__device__ __forceinline__ void for_sequences(const PagesReserveArgs& a, int b0, int b1, PoolSmem& sh, Thread one_thread,
+                                              Warp one_warp) {
+  for (int base = b0; base < b1; base += kPoolThreads) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n_long = 0;
+    __syncthreads();
+    const int b = base + threadIdx.x;
+    if (b < b1) {
+      Touched s;
+      const bool fits = touched(a, b, s);
+      if (s.end - s.first <= kFewPages) one_thread(b, s, fits);
+      else sh.long_ones[atomicAdd(&sh.n_long, 1)] = b;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < sh.n_long; i += kPoolWarps) {
+      Touched s;
+      touched(a, sh.long_ones[i], s);
+      one_warp(sh.long_ones[i], s);
+    }
+  }
+}
+
 template <int CTAS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) reserve_kernel(PagesReserveArgs a) {
   __shared__ PoolSmem sh;
@@ -178,7 +205,6 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
   const bool wide = (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
-  // Sequences of this CTA; a warp takes every 32nd of them.
   const int per = (a.batch + CTAS - 1) / CTAS;
   const int b0 = min(a.batch, rank * per), b1 = min(a.batch, b0 + per);
   if (t < 4) sh.tally[t] = 0;
@@ -189,37 +215,48 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
   // there: their count now (the counts themselves change while others still
   // decide), writers, last writer.
   int flags = stop ? kStop : 0, wants = 0;
-  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
-    Touched s;
-    if (!touched(a, b, s)) flags |= kBadPage;
-    const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-    int missing = 0;
-    for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
-      int v[kRowUnroll];
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) {
-        const int j = j0 + e * 32 + lane;
-        v[e] = j < s.end ? row[j] : kNoEntry;
-      }
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) {
-        if (v[e] < 0) {
-          missing += v[e] != kNoEntry;
-        } else if (v[e] >= a.num_pages) {
-          flags |= kBadPage;
-        } else {
-          const int r = a.refs[v[e]];
-          a.before[v[e]] = r;
-          a.writers[v[e]] = 0;
-          a.last[v[e]] = -1;
-          if (r > 1) flags |= kShared;
-        }
-      }
+  auto look = [&](int v) {
+    if (v < 0) return 1;
+    if (v >= a.num_pages) {
+      flags |= kBadPage;
+    } else {
+      const int r = a.refs[v];
+      a.before[v] = r;
+      a.writers[v] = 0;
+      a.last[v] = -1;
+      if (r > 1) flags |= kShared;
     }
-    missing = warp_sum(missing);
-    if (lane == 0) a.want[b] = make_int2(missing, 0);
-    wants += missing;
-  }
+    return 0;
+  };
+  for_sequences(a, b0, b1, sh,
+                [&](int b, const Touched& s, bool fits) {
+                  if (!fits) flags |= kBadPage;
+                  const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+                  int missing = 0;
+                  for (int j = s.first; j < s.end; ++j) missing += look(row[j]);
+                  a.want[b] = make_int2(missing, 0);
+                  wants += missing;
+                },
+                [&](int b, const Touched& s) {
+                  const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+                  int missing = 0;
+                  for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
+                    int v[kRowUnroll];
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e) {
+                      const int j = j0 + e * 32 + lane;
+                      v[e] = j < s.end ? row[j] : kNoEntry;
+                    }
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e)
+                      if (v[e] != kNoEntry) missing += look(v[e]);
+                  }
+                  missing = warp_sum(missing);
+                  if (lane == 0) {
+                    a.want[b] = make_int2(missing, 0);
+                    wants += missing;
+                  }
+                });
   int lo, hi, n_free = 0;
   warp_range<CTAS>(a.num_pages, rank, warp, lo, hi);
   for (int i = lo + 4 * lane; i < hi; i += 128 * 4) {
@@ -230,6 +267,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
     for (int e = 0; e < 4; ++e) n_free += (v[e].x == 0) + (v[e].y == 0) + (v[e].z == 0) + (v[e].w == 0);
   }
   n_free = warp_sum(n_free);
+  wants = warp_sum(wants);
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0) {
     sh.warp_count[warp] = n_free;
@@ -257,43 +295,62 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
   // A writer of a shared page takes a copy, but for the last one if nobody
   // else holds the page.
   auto takes = [&](int v, int b) {
-    const int r = __ldcg(a.before + v);
-    return r > 1 && !(__ldcg(a.writers + v) >= r && __ldcg(a.last + v) == b);
+    const int r = __ldcg(a.before + v), w = __ldcg(a.writers + v), l = __ldcg(a.last + v);
+    return r > 1 && !(w >= r && l == b);
   };
   if (all & kShared) {
-    for (int b = b0 + warp; b < b1; b += kPoolWarps) {
-      Touched s;
-      if (!touched(a, b, s)) continue;
-      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-      for (int j = s.first + lane; j < s.end; j += 32) {
-        const int v = row[j];
-        if (v >= 0 && v < a.num_pages && __ldcg(a.before + v) > 1) {
-          atomicAdd(a.writers + v, 1);
-          atomicMax(a.last + v, b);
-        }
+    auto count = [&](int v, int b) {
+      if (v >= 0 && v < a.num_pages && __ldcg(a.before + v) > 1) {
+        atomicAdd(a.writers + v, 1);
+        atomicMax(a.last + v, b);
       }
-    }
+    };
+    for_sequences(a, b0, b1, sh,
+                  [&](int b, const Touched& s, bool) {
+                    for (int j = s.first; j < s.end; ++j) count(a.table[static_cast<size_t>(b) * a.max_pages + j], b);
+                  },
+                  [&](int b, const Touched& s) {
+                    for (int j = s.first + lane; j < s.end; j += 32)
+                      count(a.table[static_cast<size_t>(b) * a.max_pages + j], b);
+                  });
     pool_sync<CTAS>();
-    for (int b = b0 + warp; b < b1; b += kPoolWarps) {
-      Touched s;
-      int want = 0, copy = 0;
-      if (touched(a, b, s)) {
-        const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-        for (int j = s.first + lane; j < s.end; j += 32) {
-          const int v = row[j];
-          if (v >= a.num_pages) continue;
-          const bool shared = v >= 0 && takes(v, b);
-          want += v < 0 || shared;
-          copy += shared && s.part && j == s.first;
-        }
-      }
-      want = warp_sum(want);
-      copy = warp_sum(copy);
-      if (lane == 0) {
-        atomicAdd(&sh.shared_tally[0], want);
-        atomicAdd(&sh.shared_tally[1], copy);
-        a.want[b] = make_int2(want, copy);
-      }
+    int want_sum = 0, copy_sum = 0;
+    for_sequences(a, b0, b1, sh,
+                  [&](int b, const Touched& s, bool) {
+                    int want = 0, copy = 0;
+                    for (int j = s.first; j < s.end; ++j) {
+                      const int v = a.table[static_cast<size_t>(b) * a.max_pages + j];
+                      if (v >= a.num_pages) continue;
+                      const bool shared = v >= 0 && takes(v, b);
+                      want += v < 0 || shared;
+                      copy += shared && s.part && j == s.first;
+                    }
+                    a.want[b] = make_int2(want, copy);
+                    want_sum += want;
+                    copy_sum += copy;
+                  },
+                  [&](int b, const Touched& s) {
+                    int want = 0, copy = 0;
+                    for (int j = s.first + lane; j < s.end; j += 32) {
+                      const int v = a.table[static_cast<size_t>(b) * a.max_pages + j];
+                      if (v >= a.num_pages) continue;
+                      const bool shared = v >= 0 && takes(v, b);
+                      want += v < 0 || shared;
+                      copy += shared && s.part && j == s.first;
+                    }
+                    want = warp_sum(want);
+                    copy = warp_sum(copy);
+                    if (lane == 0) {
+                      a.want[b] = make_int2(want, copy);
+                      want_sum += want;
+                      copy_sum += copy;
+                    }
+                  });
+    want_sum = warp_sum(want_sum);
+    copy_sum = warp_sum(copy_sum);
+    if (lane == 0) {
+      if (want_sum) atomicAdd(&sh.shared_tally[0], want_sum);
+      if (copy_sum) atomicAdd(&sh.shared_tally[1], copy_sum);
     }
     pool_sync<CTAS>();
     const bool on = lane < CTAS;
@@ -350,46 +407,57 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
   }
   pool_sync<CTAS>();      // the last one: no CTA reads another's shared memory behind it
   if (!ok) return;
-  for (int b = b0 + warp; b < b1; b += kPoolWarps) {
-    Touched s;
-    if (!touched(a, b, s) || s.first == s.end) continue;
-    const int2 base = __ldcg(a.want + b);
-    int at = base.x;
-    int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-    for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
-      int v[kRowUnroll], rank_of[kRowUnroll], page[kRowUnroll];
-      bool shared[kRowUnroll];
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) {
-        const int j = j0 + e * 32 + lane;
-        v[e] = j < s.end ? row[j] : kNoEntry;
-      }
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) {
-        shared[e] = (all & kShared) && v[e] >= 0 && takes(v[e], b);
-        const bool want = (v[e] < 0 && v[e] != kNoEntry) || shared[e];
-        const unsigned m = __ballot_sync(0xffffffffu, want);
-        rank_of[e] = want ? at + __popc(m & ((1u << lane) - 1)) : -1;
-        at += __popc(m);
-      }
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) page[e] = rank_of[e] >= 0 ? __ldcg(a.free_list + rank_of[e]) : -1;
-#pragma unroll
-      for (int e = 0; e < kRowUnroll; ++e) {
-        if (rank_of[e] < 0) continue;
-        const int j = j0 + e * 32 + lane;
-        row[j] = page[e];
-        a.refs[page[e]] = 1;
-        if (shared[e]) {
-          atomicSub(a.refs + v[e], 1);
-          if (s.part && j == s.first) {
-            a.copy_src[base.y] = v[e];
-            a.copy_dst[base.y] = page[e];
-          }
-        }
+  auto put = [&](int32_t* row, int j, int v, bool shared, int page, const Touched& s, int copy) {
+    row[j] = page;
+    a.refs[page] = 1;
+    if (shared) {
+      atomicSub(a.refs + v, 1);
+      if (s.part && j == s.first) {
+        a.copy_src[copy] = v;
+        a.copy_dst[copy] = page;
       }
     }
-  }
+  };
+  for_sequences(a, b0, b1, sh,
+                [&](int b, const Touched& s, bool) {
+                  if (s.first == s.end) return;
+                  const int2 base = __ldcg(a.want + b);
+                  int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+                  int at = base.x;
+                  for (int j = s.first; j < s.end; ++j) {
+                    const int v = row[j];
+                    const bool shared = (all & kShared) && v >= 0 && takes(v, b);
+                    if (v < 0 || shared) put(row, j, v, shared, __ldcg(a.free_list + at++), s, base.y);
+                  }
+                },
+                [&](int b, const Touched& s) {
+                  const int2 base = __ldcg(a.want + b);
+                  int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+                  int at = base.x;
+                  for (int j0 = s.first; j0 < s.end; j0 += 32 * kRowUnroll) {
+                    int v[kRowUnroll], rank_of[kRowUnroll], page[kRowUnroll];
+                    bool shared[kRowUnroll];
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e) {
+                      const int j = j0 + e * 32 + lane;
+                      v[e] = j < s.end ? row[j] : kNoEntry;
+                    }
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e) {
+                      shared[e] = (all & kShared) && v[e] >= 0 && takes(v[e], b);
+                      const bool want = (v[e] < 0 && v[e] != kNoEntry) || shared[e];
+                      const unsigned m = __ballot_sync(0xffffffffu, want);
+                      rank_of[e] = want ? at + __popc(m & ((1u << lane) - 1)) : -1;
+                      at += __popc(m);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e)
+                      page[e] = rank_of[e] >= 0 ? __ldcg(a.free_list + rank_of[e]) : -1;
+#pragma unroll
+                    for (int e = 0; e < kRowUnroll; ++e)
+                      if (rank_of[e] >= 0) put(row, j0 + e * 32 + lane, v[e], shared[e], page[e], s, base.y);
+                  }
+                });
 }
 
 // ============================================================ compact
@@ -625,9 +693,14 @@ cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t stream) {
   return launch_pdl(free_kernel, dim3(a.batch), dim3(256), 0, stream, a);
 }
 
-// One CTA where there is little to look at: it has no cluster barriers to wait
-// at.  (64 sequences, 10301 pages, 1 to 8 tokens each: 13.9 us with 16 CTAs.)
-static bool one_cta(int num_pages, int batch) { return num_pages <= 32768 && batch <= 128; }
+// One CTA where there is little to look at (a pool's counts, the tables'
+// entries): it has no cluster barriers to wait at, nor atomics on words that
+// other SMs hold.  (256 samples of 16 prompts, their copies included: 68 us with
+// one CTA, 79 with 16.  512 prompts in 171386 pages have 16: 28 us; the counts
+// alone are 670 KB.)
+static bool one_cta(int num_pages, int batch, int max_pages) {
+  return num_pages <= 32768 && batch <= kPoolThreads && static_cast<long long>(batch) * max_pages <= 65536;
+}
 
 // Clusters of more than 8 CTAs have to be allowed, once a device and kernel.
 // (Two threads may both do it: it is the same call.)
@@ -641,7 +714,7 @@ static cudaError_t allow_big_clusters(const void* kernel, bool (&allowed)[64]) {
 }
 
 cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream) {
-  if (one_cta(a.num_pages, a.batch))
+  if (one_cta(a.num_pages, a.batch, a.max_pages))
     return launch_pdl(reserve_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
   static bool allowed[64];
   cudaError_t e = allow_big_clusters(reinterpret_cast<const void*>(reserve_kernel<kPoolCtas>), allowed);
@@ -651,7 +724,7 @@ cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream)
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream) {
   cudaError_t e;
-  if (one_cta(a.num_pages, 0)) {
+  if (one_cta(a.num_pages, 0, 0)) {
     e = launch_pdl(compact_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
   } else {
     static bool allowed[64];
