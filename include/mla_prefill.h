@@ -925,7 +925,8 @@ mla_status_t mla_pages_copy(void* cache, size_t page_bytes, int32_t num_layers, 
  * cache_lengths[b] + k becomes what the row at cache_lengths[b] + keep[b][k]
  * was, for k < keep_counts[b].  Drafts written by mla_latent_cache_write_at keep
  * their rotation: the k-th accepted one has depth k.  cache_lengths is left to
- * the caller (add keep_counts).
+ * the caller (add keep_counts).  The pages of these rows have to be the
+ * sequence's own, as mla_pages_reserve makes them.
  *
  * cache:     num_layers arrays [num_pages][page_size][row_bytes], layer_stride
  *            bytes apart

@@ -1011,8 +1011,15 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
 }
 
 // ------------------------------------------------------------------ chunk attention
+// Rows (token, head) are counted in 32 bits; and four CTAs a head and 17 more are
+// launched first, where a launch has 65535 rows of them.
+static bool chunk_sizes_ok(int32_t num_heads, int32_t total_q_tokens) {
+  return num_heads >= 1 && num_heads <= 16379 && total_q_tokens >= 0 &&
+         static_cast<long long>(total_q_tokens) * num_heads < (1ll << 31) / 4;
+}
+
 size_t mla_chunk_attention_workspace_bytes(int32_t batch_size, int32_t num_heads, int32_t total_q_tokens) {
-  if (batch_size < 1 || num_heads < 1 || total_q_tokens < 0) return 0;
+  if (batch_size < 1 || !chunk_sizes_ok(num_heads, total_q_tokens)) return 0;
   return mla::chunk_attn_workspace(batch_size, num_heads, total_q_tokens);
 }
 
@@ -1024,12 +1031,11 @@ mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uin
                                  const float* attn_sink, void* workspace, size_t workspace_bytes,
                                  int32_t* d_status, mla_stream_t stream) {
   if (num_heads < 1) return MLA_ERR_GEOMETRY;
-  // (Four CTAs a head and 17 more are launched first: a launch has 65535 rows of them.)
   if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !page_table || !w_uk || !w_uv ||
       !aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
-      batch_size < 1 || total_q_tokens < 0 || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
-      num_heads > 16379 || !(scale > 0.0f) || (chunk_mask ? mask_words < 1 : mask_words != 0) ||
-      static_cast<long long>(total_q_tokens) * num_heads >= (1ll << 31) / 4 ||
+      batch_size < 1 || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+      !chunk_sizes_ok(num_heads, total_q_tokens) || !(scale > 0.0f) ||
+      (chunk_mask ? mask_words < 1 : mask_words != 0) ||
       static_cast<long long>(num_pages) * page_size >= (1ll << 31) - 64)
     return MLA_ERR_ARG;
   if (total_q_tokens == 0) return MLA_OK;

@@ -63,6 +63,14 @@ def inputs(new, cached, H, page, seed=0):
                 w_uv=rng.standard_normal((H, 128, 512)) * 512 ** -0.5, iro=iro, cached=cached, scale=192 ** -0.5)
 
 
+def test_no_workspace_for_sizes_that_are_refused(lib):
+    most = (1 << 29) - 1
+    for heads, tokens in [(16380, 1), (2, 1 << 28), (16, 1 << 25), (16379, 1 << 30), (1, 1 << 29)]:
+        assert mla.mla_chunk_attention_workspace_bytes(1, heads, tokens) == 0
+        assert call(H=heads, T=tokens) == mla.MLA_ERR_ARG
+    assert mla.mla_chunk_attention_workspace_bytes(1, 1, most) >= most * 3200
+
+
 def test_causal_oracle_is_the_decode_oracle():
     x = inputs([2, 1, 3], [9, 0, 30], 3, 8)
     out, lse, _ = C.chunk_attention(**x)
