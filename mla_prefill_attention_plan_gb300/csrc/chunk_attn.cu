@@ -136,6 +136,7 @@ __device__ __forceinline__ Walk walk_start(const ChunkParams& p, int pair) {
   return w;
 }
 
+// By a warp.
 __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment& s) {
   if (w.left == 0 && w.x >= w.x1) {
     if (w.c == 1) return false;
@@ -151,12 +152,12 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
   const int c = w.c;
   int i;                       // item within the sequence
   if (w.left > 0) {
-    w.b = sequence_of<false>(p.base, p.B, c, w.item);
+    w.b = last_of(p.B, [&](int b) { return p.base[b].items[c] <= w.item; });
     i = w.item - p.base[w.b].items[c];
     w.item += w.stride;
     --w.left;
   } else {
-    if (!w.begun) w.b = sequence_of<true>(p.base, p.B, c, w.x);
+    if (!w.begun) w.b = last_of(p.B, [&](int b) { return p.base[b].units[c] <= w.x; });
     w.begun = true;
     while (p.base[w.b + 1].units[c] <= w.x) ++w.b;
     i = -1;

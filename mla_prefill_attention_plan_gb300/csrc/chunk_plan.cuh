@@ -52,46 +52,65 @@ struct ChunkPlanArgs {
   uint8_t* odd_rows;         // [(T + 7) / 8]
 };
 
-// The sequence of item (or unit) i of class c: the last one with base <= i.
-template <bool UNITS>
+// The sequence of item i of class c: the last one with base <= i.
 __device__ __forceinline__ int sequence_of(const Base* base, int B, int c, int i) {
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((UNITS ? base[mid].units[c] : base[mid].items[c]) <= i) lo = mid;
+    if (base[mid].items[c] <= i) lo = mid;
     else hi = mid;
   }
   return lo;
 }
 
-// By one CTA of kPlanThreads.
-template <int kPlanThreads>
-__device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
+// The last b of [0, B) that is 0 or has before(b), which holds up to some b, by a
+// warp: 32 of them are looked at in one step of what is a chain of loads.
+template <typename F>
+__device__ __forceinline__ int last_of(int B, F before) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    lo += step * __popc(__ballot_sync(0xffffffffu, at < hi && before(at)));
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// By one CTA of kPlanThreads, with kKeepBases Base of shared memory: the bases are
+// searched there if they fit (76 sequences: 9 us from global memory, which is
+// longer than the projection beside it).
+template <int kPlanThreads, int kKeepBases>
+__device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a, Base* kept) {
   constexpr int kWarps = kPlanThreads / 32;
   static_assert(kPlanThreads >= 64 + kMaxPairs, "a thread for each worker");
   __shared__ int4 warp_sum[kWarps];
-  __shared__ int bad, whole[2], rest[2][kMaxPairs];
+  __shared__ int whole[2], rest[2][kMaxPairs];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) {
-    bad = a.iro[0] != 0;
-    whole[0] = whole[1] = 0x7FFFFFFF;
-  }
-  __syncthreads();
-  for (int b = t; b < a.B; b += kPlanThreads)
-    if (a.iro[b + 1] < a.iro[b]) bad = 1;
+  struct Lengths {
+    uint32_t q0, q1, cached;
+  };
+  auto lengths = [&](int b) { return b < a.B ? Lengths{a.iro[b], a.iro[b + 1], a.cache_len[b]} : Lengths{}; };
+  Lengths next = lengths(t);
+  bool bad = t == 0 && a.iro[0] != 0;
+  for (int b = t; b < a.B; b += kPlanThreads) bad |= a.iro[b + 1] < a.iro[b];
+  if (t < 2) whole[t] = 0x7FFFFFFF;
   for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
   for (int i = t; i < 2 * a.pairs; i += kPlanThreads) a.split[i].rows = 0;
-  __syncthreads();
-  const bool all_bad = bad;
+  const bool all_bad = __syncthreads_or(bad);
+  const bool keep = a.B < kKeepBases;
+  const Base* const base = keep ? kept : a.base;
   if (all_bad && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
   int4 before = make_int4(0, 0, 0, 0);          // items of class 0 and 1, units of class 0 and 1
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + t;
     int4 own = make_int4(0, 0, 0, 0);
+    int token0 = 0, tokens = 0;
+    const Lengths at = next;
+    next = lengths(b + kPlanThreads);
     if (b < a.B && !all_bad) {
-      const uint32_t q0 = a.iro[b], q1 = a.iro[b + 1];
-      const long long n = q1 - q0, L = static_cast<long long>(a.cache_len[b]) + n;
-      if (q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
+      const long long n = at.q1 - at.q0, L = static_cast<long long>(at.cached) + n;
+      if (at.q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
         set_status(a.status, MLA_DEV_BAD_OFFSETS);
       } else if (n > 0) {
         const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
@@ -100,7 +119,20 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
         // (2^31 units would be a day's work; positions saturate, see below.)
         own.z = static_cast<int>(min(tiles / 2 * kt, 0x7FFFFFFFll));
         own.w = own.y ? static_cast<int>(kt) : 0;
+        token0 = static_cast<int>(at.q0);
+        tokens = static_cast<int>(n);
       }
+    }
+    // A sequence's first tokens by its thread, more of them by the warp.  (All by the
+    // warp: 5 us for 32 sequences, one after the other.)
+    constexpr int kFew = 32;
+#pragma unroll 1
+    for (int i = 0; i < min(tokens, kFew); ++i) a.token_seq[token0 + i] = b;
+    for (unsigned m = __ballot_sync(0xffffffffu, tokens > kFew); m != 0; m &= m - 1) {
+      const int from = __ffs(m) - 1;
+      const int first = __shfl_sync(0xffffffffu, token0, from), n = __shfl_sync(0xffffffffu, tokens, from);
+#pragma unroll 1
+      for (int i = kFew + lane; i < n; i += 32) a.token_seq[first + i] = b - lane + from;
     }
     // Sums that would not fit stay at the largest number.
     auto add = [](int x, int y) { return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), 0x7FFFFFFFu)); };
@@ -124,10 +156,14 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
       Base v;
       v.items[0] = upto.x, v.items[1] = upto.y, v.units[0] = upto.z, v.units[1] = upto.w;
       a.base[b + 1] = v;
+      if (keep) kept[b + 1] = v;
     }
     __syncthreads();
   }
-  if (t == 0) a.base[0] = Base{};
+  if (t == 0) {
+    a.base[0] = Base{};
+    if (keep) kept[0] = Base{};
+  }
   const bool over = before.z == 0x7FFFFFFF || before.w == 0x7FFFFFFF;
   if (over && t == 0) set_status(a.status, MLA_DEV_BAD_OFFSETS);
   __syncthreads();
@@ -138,8 +174,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
   const int n = max(1, min(workers_of(a.pairs, c), units));
   const bool worker = w < n;
   auto length = [&](int item) {
-    const int b = sequence_of<false>(a.base, a.B, c, item);
-    return (a.base[b + 1].units[c] - a.base[b].units[c]) / (a.base[b + 1].items[c] - a.base[b].items[c]);
+    const int b = sequence_of(base, a.B, c, item);
+    return (base[b + 1].units[c] - base[b].units[c]) / (base[b + 1].items[c] - base[b].items[c]);
   };
   int mine = 0;
   if (worker) {
@@ -154,8 +190,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
   __syncthreads();
   if (worker) {
     for (int k = 0; k < whole[c]; ++k) mine += length(w + k * n);
-    const long long total = units;
-    mine = static_cast<int>(total * (w + 1) / n - total * w / n) - mine;
+    // units (w + 1) / n - units w / n, rounded down both
+    const int each = units / n, more = units - each * n;
+    mine = each + more * (w + 1) / n - more * w / n - mine;
     rest[c][w] = mine;
     if (w == 0) a.schedule->whole[c] = whole[c], a.schedule->workers[c] = n;
   }
@@ -164,19 +201,15 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a) {
     const int first = whole[c] * n;                 // the first item on the line
     int at = units;
     if (first < items && !over) {
-      const int b = sequence_of<false>(a.base, a.B, c, first);
-      at = a.base[b].units[c] + (first - a.base[b].items[c]) * length(first);
+      const int b = sequence_of(base, a.B, c, first);
+      at = base[b].units[c] + (first - base[b].items[c]) * length(first);
     }
     for (int v = 0; v < w; ++v) at += rest[c][v];
     a.schedule->tail[c][w] = at;
     if (w == n - 1) a.schedule->tail[c][n] = at + mine;
   }
-  if (over) return;                                 // nobody has work: no token has a result
-  for (int b = warp; b < a.B; b += kWarps) {
-    const Base v0 = a.base[b], v1 = a.base[b + 1];
-    if (v0.items[0] == v1.items[0] && v0.items[1] == v1.items[1]) continue;
-    for (uint32_t i = a.iro[b] + lane; i < a.iro[b + 1]; i += 32) a.token_seq[i] = b;
-  }
+  if (over)                                         // nobody has work: no token has a result
+    for (int i = t; i < a.T; i += kPlanThreads) a.token_seq[i] = -1;
 }
 
 // Bits of the tokens [8 group, 8 group + 8), by one CTA.  A key that a row does
@@ -189,34 +222,50 @@ __device__ __forceinline__ void find_odd_rows(const ChunkPlanArgs& a, int group)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) bits = 0;
   __syncthreads();
-  for (int i = warp; i < 8; i += kThreads / 32) {
-    const int t = 8 * group + i;
-    if (t >= a.T) continue;
-    int lo = 0, hi = a.B;                        // the last sequence that begins at t or before
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.iro[mid] <= static_cast<uint32_t>(t)) lo = mid;
-      else hi = mid;
+  // Every warp finds the rows of all eight tokens, token i in lane i: the sequence
+  // of the first by a search, those of the others among the next 32.
+  const int t0 = 8 * group, t = t0 + lane;
+  const int first = last_of(a.B, [&](int b) { return a.iro[b] <= static_cast<uint32_t>(t0); });
+  const int begins = first + 1 + lane;
+  const uint32_t begin = begins < a.B ? a.iro[begins] : 0xFFFFFFFFu;
+  int lo = first;
+  for (int i = 0; i < 8; ++i) {
+    const int more = __popc(__ballot_sync(0xffffffffu, begin <= static_cast<uint32_t>(t0 + i)));
+    const int b = more < 32 ? first + more : last_of(a.B, [&](int b) { return a.iro[b] <= static_cast<uint32_t>(t0 + i); });
+    if (lane == i) lo = b;
+  }
+  long long row = -1;
+  if (lane < 8 && t < a.T) {
+    const uint32_t q0 = a.iro[lo], q1 = a.iro[lo + 1], cached = a.cache_len[lo];
+    if (q0 <= static_cast<uint32_t>(t) && static_cast<uint32_t>(t) < q1) {
+      const long long pos = static_cast<long long>(cached) + (t - static_cast<long long>(q0)), j = pos / a.page_size;
+      const int page = j < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + j] : -1;
+      if (page >= 0 && page < a.num_pages) row = static_cast<long long>(page) * a.page_size + (pos - j * a.page_size);
     }
-    if (a.iro[lo] > static_cast<uint32_t>(t) || a.iro[lo + 1] <= static_cast<uint32_t>(t)) continue;
-    const long long pos = static_cast<long long>(a.cache_len[lo]) + (t - static_cast<long long>(a.iro[lo]));
-    const long long j = pos / a.page_size;
-    const int page = j < a.max_pages ? a.page_table[static_cast<size_t>(lo) * a.max_pages + j] : -1;
-    if (page < 0 || page >= a.num_pages) continue;
-    const size_t row = static_cast<size_t>(page) * a.page_size + static_cast<size_t>(pos - j * a.page_size);
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv_cache) + row * 1152);
+  }
+  constexpr int kWarps = kThreads / 32, kEach = (8 + kWarps - 1) / kWarps;
+  uint4 v[kEach][2] = {};
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int i = warp + u * kWarps;
+    const long long r = __shfl_sync(0xffffffffu, row, i & 7);
+    if (i >= 8 || r < 0) continue;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv_cache) + r * 1152);
+    v[u][0] = src[lane], v[u][1] = src[32 + lane];
+  }
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
     bool odd = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint4 v = src[e * 32 + lane];
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t x[4] = {v[u][e].x, v[u][e].y, v[u][e].z, v[u][e].w};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) odd |= (x[u] & 0x7F80u) == 0x7F80u || (x[u] & 0x7F800000u) == 0x7F800000u;
+      for (int k = 0; k < 4; ++k) odd |= (x[k] & 0x7F80u) == 0x7F80u || (x[k] & 0x7F800000u) == 0x7F800000u;
     }
-    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&bits, 1u << i);
+    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&bits, 1u << (warp + u * kWarps));
   }
   __syncthreads();
-  if (threadIdx.x == 0 && 8 * group < a.T) a.odd_rows[group] = static_cast<uint8_t>(bits);
+  if (threadIdx.x == 0 && t0 < a.T) a.odd_rows[group] = static_cast<uint8_t>(bits);
 }
 
 }  // namespace chunk

@@ -72,7 +72,7 @@ struct HeadGemm {
 
 // SPLIT > 1: the head's N * SPLIT output columns are shared by SPLIT CTAs
 // (grid.y = H * SPLIT), N each, so that a small M still fills the GPU.
-// PLAN: more CTAs (the last kPlanRows of grid.y) find chunk attention's schedule
+// PLAN: more CTAs (the first kPlanRows of grid.y) find chunk attention's schedule
 // and look its new tokens' rows over, 8 of the row tile's 128 tokens each.
 constexpr int kPlanRows = 17;
 template <int N, int K, int STAGES, int SPLIT, int TERMS, bool PLAN>
@@ -92,15 +92,17 @@ __global__ void __launch_bounds__(192, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* sh = reinterpret_cast<Bars*>(smem + C::SMEM_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y / SPLIT;
-  const int nc = blockIdx.y % SPLIT;   // this CTA's N-column block of the head
+  const int y = static_cast<int>(blockIdx.y) - (PLAN ? kPlanRows : 0);
+  const int h = y / SPLIT;
+  const int nc = y % SPLIT;            // this CTA's N-column block of the head
   const int m0 = blockIdx.x * 128;
   pdl_enter();
   if (timed_out_before(status)) return;   // an earlier kernel timed out: no work
-  if (PLAN && blockIdx.y + kPlanRows >= gridDim.y) {
-    const int y = gridDim.y - 1 - blockIdx.y;
-    if (y > 0) chunk::find_odd_rows<192>(plan, blockIdx.x * (kPlanRows - 1) + y - 1);
-    else if (blockIdx.x == 0) chunk::chunk_plan<192>(plan);
+  if (PLAN && y < 0) {
+    if (blockIdx.y > 0)
+      chunk::find_odd_rows<192>(plan, blockIdx.x * (kPlanRows - 1) + blockIdx.y - 1);
+    else if (blockIdx.x == 0)
+      chunk::chunk_plan<192, C::SMEM_BAR / sizeof(chunk::Base)>(plan, reinterpret_cast<chunk::Base*>(smem));
     return;
   }
 
