@@ -964,9 +964,10 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  * infinite or NaN latent value makes the token's out and lse NaN.
  * Longer chunks than about 170 tokens are as right, but mla_prefill then has
  * less to compute.
- * Rounding: the projected query and the softmax weights are bf16, the latent
- * result two bf16 terms; scores, sums and partial results are fp32.  Results do
- * not change from call to call.
+ * Rounding: the projected query and the softmax weights are bf16 (the weights two
+ * bf16 terms in calls whose tokens, heads and page table's width make for little
+ * work), the latent result two bf16 terms; scores, sums and partial results are
+ * fp32.  Results do not change from call to call.
  *
  * out:      [total_q_tokens][num_heads][128] bf16, output
  * lse:      [total_q_tokens][num_heads] fp32 output (of the rounded query), or NULL

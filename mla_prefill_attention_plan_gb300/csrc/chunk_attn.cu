@@ -25,8 +25,15 @@
 //
 // What bounds it: both operands of both products come from shared memory, and K
 // and V are the same bytes needed in different halves (CTA r takes keys 128r..
-// of a tile for S, latent columns 128r.. of each 256 for O), so each CTA reads
-// 147 KB and 131 KB a tile.
+// of a tile for S, latent columns 128r.. of each 256 for O), so each CTA writes
+// and reads 147 KB and 131 KB a tile, and reads 74 KB of Q and twice 32 KB of P:
+// 5600 clk at 128 bytes a clk.  Measured: 64 tokens over 65536 keys, 128 heads, 775
+// us, 1510 TFLOP/s, 7050 clk a tile (a ring of 5, 6, 7 stages: 864, 804, 777 us).
+// Where a row tile is alone with its context, HBM's latency and the second read of
+// a tile from L2 come on top: 32 sequences of 8 tokens over 20000 keys, 16 heads,
+// 205 us for 740 MB, 4.6 us a tile; on pages of 16, whose tiles are 16 boxes, the
+// loads' issue (10 tokens: 284 us on pages of 64, 372 on pages of 16).  A short
+// context is chains of dependent loads: 35 us for one tree over 1000 keys.
 //
 // Who does what, found on the device from the lengths: the row tiles of a
 // sequence, two by two, are items that two pairs work at side by side (class
@@ -51,18 +58,27 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescale = 8.0f;             // a row's reference moves when its maximum grows by 2^8
 
 constexpr int kStage = 16 * 1024;
-constexpr int kStages = 7;
+// Small calls (launch_chunk_attn has the rule) hold the softmax weights in two bf16
+// terms.  Results over 300 to 2500 keys are 0.0025 off in the 2-norm with one term
+// and 0.0022 with two, of which the output's own rounding is 0.0017 and the
+// projected query's 0.0014.  A small call waits for chains of loads, not for MMAs,
+// and is as fast on a ring of 5 stages, which leaves room for the second term: one
+// tree of 6 over 1000 keys, 16 heads, 33.5 us with one and 35.3 with two.  Of larger
+// calls the products are what bounds them: 8 chunks of 64 over 2000 keys, 128 heads,
+// took 340 us with one and 499 with two.
+__host__ __device__ constexpr int ring_stages(bool two) { return two ? 5 : 7; }
 constexpr int kQBytes = 9 * 64 * 128;        // 64 rows x 576 columns in blocks of 64
 constexpr int kPBytes = 4 * 64 * 128;        // 64 rows x 256 keys in blocks of 64
 constexpr int kSmemQ = 0;
 constexpr int kSmemP = kSmemQ + kQBytes;
-constexpr int kSmemRing = kSmemP + kPBytes;
+__host__ __device__ constexpr int smem_ring(bool two) { return kSmemP + (two ? 2 : 1) * kPBytes; }
 constexpr int kFound = 4;                    // tiles whose rows have been looked up
-constexpr int kSmemBoxes = kSmemRing + kStages * kStage;      // their boxes: 4 groups of 64 rows each
+constexpr int kSmemBoxes = smem_ring(false) + ring_stages(false) * kStage;      // their boxes: 4 groups of 64 rows each
 constexpr int kSmemRed = kSmemBoxes + kFound * 4 * 64 * 8;    // a row's maxima and sums of both threads
 constexpr int kSmemBar = kSmemRed + 2 * 128 * 4;
 constexpr int kSmemTotal = kSmemBar + 1024 + 1024;
 static_assert(kSmemTotal <= 227 * 1024, "shared memory");
+static_assert(smem_ring(true) + ring_stages(true) * kStage <= kSmemBoxes, "shared memory");
 constexpr int kProducers = 4;                // warps 0, 7, 8, 9
 constexpr int kThreads = 192 + 32 * kProducers;   // with MMA (1), softmax (2 .. 5), row lookup (6)
 static_assert((kProducers & (kProducers - 1)) == 0, "whose stage it is: a difference modulo 2^32");
@@ -195,7 +211,7 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment
 constexpr int kSegments = 4;     // segments that the lookup warp is ahead by
 
 struct ChunkSmem {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[ring_stages(false)], empty[ring_stages(false)];
   uint64_t q_full, q_free;
   uint64_t s_full[2], p_full, pv_done, drain;
   uint64_t swapped[2];       // the two warps that share rows have both written their words
@@ -217,9 +233,11 @@ __device__ __forceinline__ uint32_t odd_bits(const ChunkParams& p, int t) {
 }
 
 // ------------------------------------------------------------------ attention
+template <bool TWO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CacheMaps maps,
                       const __grid_constant__ ChunkParams p) {
+  constexpr int kStages = ring_stages(TWO);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   ChunkSmem* sh = reinterpret_cast<ChunkSmem*>(smem + kSmemBar);
@@ -264,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh->tmem;
   volatile int* const abort_flag = &sh->abort;
   const bool stop = cluster_any(abort_flag);     // an earlier kernel timed out: no work
-  const uint32_t ring = smem_u32(smem + kSmemRing);
+  const uint32_t ring = smem_u32(smem + smem_ring(TWO));
   volatile int never = 0;
   // The next segment that the lookup warp has found (by a warp; by one lane of the
   // MMA warp).
@@ -457,9 +475,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!take()) break;
                 const uint32_t v = ring + stage * kStage;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  mma_f16_ss_pair(tmem + kTmO + m * 128, sdesc(sp + g * 8192 + e * 32, 16, 1024),
-                                  sdesc(v + e * 2048, 8192, 1024), kIdescO, (j | g | e) != 0);
+                for (int e = 0; e < (TWO ? 8 : 4); ++e)              // (term, 16 keys)
+                  mma_f16_ss_pair(tmem + kTmO + m * 128,
+                                  sdesc(sp + (e >> 2) * kPBytes + g * 8192 + (e & 3) * 32, 16, 1024),
+                                  sdesc(v + (e & 3) * 2048, 8192, 1024), kIdescO, (j | g | e) != 0);
                 give();
               }
             }
@@ -709,17 +728,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // Chunks of 8 keys (16 bytes) of the row, in the 128-byte swizzle.
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            uint32_t pk[4];
+            uint32_t pk[4], rest[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float a = ex2(fmaf(__uint_as_float(x[u * 8 + 2 * e]), p.scale_log2, -shift));
               const float b = ex2(fmaf(__uint_as_float(x[u * 8 + 2 * e + 1]), p.scale_log2, -shift));
               sum += a + b;
               pk[e] = pack_bf16(a, b);
+              if (TWO) rest[e] = pack_bf16(a - bf16_lo(pk[e]), b - bf16_hi(pk[e]));
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (c >> 1) * 8192 + lane * 128 + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4)),
-                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+            const uint32_t at = mine + (c >> 1) * 8192 + lane * 128 + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
                          : "memory");
+            if (TWO)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kPBytes), "r"(rest[0]), "r"(rest[1]),
+                           "r"(rest[2]), "r"(rest[3])
+                           : "memory");
           }
         }
         fence_async_smem();
@@ -1028,10 +1052,15 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   pa.odd_rows = ws + L.odd_rows;
   cudaError_t e = launch_project_queries(a.q, a.w_uk, q_full, a.T, a.H, &pa, a.status, stream);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) !=
-      cudaSuccess)
+  // Two terms where a pair has one tile or two at most, by what the host knows: the
+  // row tiles that there can be, and the tiles of the longest context that the page
+  // table holds.
+  const long long row_tiles = static_cast<long long>(R) / kRows + a.B;
+  const long long key_tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
+  const auto kernel = row_tiles * key_tiles <= 2 * pairs ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) != cudaSuccess)
     return e;
-  if ((e = launch_pdl(chunk_attn_kernel, dim3(2 * pairs), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
+  if ((e = launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
       cudaSuccess)
     return e;
   if ((e = launch_pdl(chunk_merge_kernel, dim3(2 * pairs, kMergeSlices), dim3(kMergeWarps * 32), 0, stream, p, pairs)) !=

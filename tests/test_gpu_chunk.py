@@ -5,7 +5,8 @@ the significand by 0.42 * 2^-8 = 0.00165 (root mean square).  On random rows
 three of them reach an output, independent of each other: its own, the weights',
 and the projected query's, which moves a score of spread sigma by 0.00165 sigma
 (sigma is 1 here).  Together 0.00165 * sqrt(3) = 0.0029 of the output's 2-norm;
-twice that is allowed for a whole result, four times for a row of 128 values.
+twice that is allowed for a whole result, four times for a row of 128 values.  (Small calls have the weights
+in two terms; the bound stays.)
 The lse is off by no more than the worst score: 2^-8 of scale * sum |q_lat c|
 (the oracle's slack), and fp32's part of it."""
 import numpy as np
@@ -52,14 +53,22 @@ def words_of(rows, words):
     return np.array([[r >> 32 * w & 0xffffffff for w in range(words)] for r in rows], dtype=np.uint32).view(np.int32)
 
 
+@pytest.fixture(params=["small", "any"], autouse=True)
+def size(request):
+    """Calls whose page table holds few tiles have their weights in two terms."""
+    Case.reach = 0 if request.param == "small" else 40000
+
+
 class Case:
     """Inputs of ragged sequences on shuffled pages; rows that no sequence sees are NaN."""
+
+    reach = 0              # positions that the page table has entries for, at least
 
     def __init__(self, new, cached, H, page, seed=0, mask="tree", sink=False, extra=0, words=None, spread=1.0):
         rng = np.random.default_rng(seed)
         self.new, self.cached, self.H, self.page, self.B = new, cached, H, page, len(new)
         held = [-(-(n + c) // page) for n, c in zip(new, cached)]
-        self.num, self.most = sum(held) + 1, max(held) + 1
+        self.num, self.most = sum(held) + 1, max(held + [self.reach // page]) + 1
         order, at = rng.permutation(self.num), 0
         self.table = np.full((self.B, self.most), -1, np.int32)
         for b, k in enumerate(held):
@@ -135,6 +144,18 @@ class Case:
         assert (off <= ROW * size + 1e-6).all(), (off / size).max()
         worst = 2.0 ** -8 * slack + 2.0 ** -20 * (1 + np.abs(lse))
         assert (np.abs(got_lse - lse) <= worst).all(), (np.abs(got_lse - lse) / worst).max()
+
+
+def test_small_calls_are_closer():
+    """At most 0.00165 sqrt(2) = 0.0023 without the weights' rounding, 0.0029 with it:
+    over 10^5 values a result is far from the middle of them."""
+    off = []
+    for Case.reach in (0, 40000):
+        c = Case([20], [1000], 64, 64)
+        mla.check(c.call())
+        out = c.oracle()[0]
+        off.append(np.linalg.norm(c.out.double().cpu().numpy() - out) / np.linalg.norm(out))
+    assert off[0] < 0.0026 and off[0] < 0.95 * off[1], off
 
 
 @pytest.mark.parametrize("page", [128, 256, 64, 16, 24, 100, 7, 1])
