@@ -1056,7 +1056,8 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   // row tiles that there can be, and the tiles of the longest context that the page
   // table holds.
   const long long row_tiles = static_cast<long long>(R) / kRows + a.B;
-  const long long key_tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
+  const long long key_tiles = std::min((static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile,
+                                       static_cast<long long>(kMaxContext));
   const auto kernel = row_tiles * key_tiles <= 2 * pairs ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal)) != cudaSuccess)
     return e;
