@@ -540,3 +540,27 @@ def test_the_largest_numbers_are_numbers():
     c.out[2], c.lse[2] = FILL, FILL
     lse[2] = np.nan
     c.compare(out, lse, slack)
+
+
+def test_thousands_of_sequences():
+    """More than the plan holds in shared memory, most of them without new tokens."""
+    rng = np.random.default_rng(8)
+    Case(list((rng.random(5000) < 0.3).astype(int) * rng.integers(1, 4, 5000)), list(rng.integers(0, 20, 5000)), 2, 16,
+         mask="any").check()
+
+
+@pytest.mark.parametrize("empty", [30, 31, 32, 33, 200])
+def test_odd_keys_behind_sequences_without_tokens(empty):
+    """Tokens 3 and 4 are neighbours in the batch with many sequences between them."""
+    new = [4] + [0] * empty + [3, 0, 2]
+    c = Case(new, [20] + [1] * empty + [30, 5, 40], 3, 16, mask=[1, 2, 4, 8] + [1, 2, 4] + [1, 2])
+    out, lse, slack = c.oracle()
+    for b, m, t in ((0, 3, 3), (empty + 1, 1, 5), (empty + 3, 0, 7)):
+        j = c.cached[b] + m
+        c.kv_d[int(c.table[b, j // 16]) * 16 + j % 16, 5] = float("nan")
+        lse[t] = np.nan
+    mla.check(c.call())
+    for t in (3, 5, 7):
+        assert torch.isnan(c.out[t]).all() and torch.isnan(c.lse[t]).all()
+        c.out[t], c.lse[t] = FILL, FILL
+    c.compare(out, lse, slack)
