@@ -54,12 +54,13 @@ constexpr float kRescaleLog2 = 8.0f;
 // bf16 result at out + row * out_ld + h * out_hstride.  With rope_src set,
 // the 64 values at rope_src + row * rope_ld + h * rope_hstride are copied
 // after the N results (the query's rope part next to its latent part).
-// With TERMS > 1, A is the sum of TERMS matrices side by side, K columns each,
-// that share B_h.  With row_seq set, row r is written only if row_seq[r] >= 0.
-template <int N, int K, int STAGES>
+// With TERMS > 1, A is the sum of TERMS matrices side by side, K columns each; a
+// stage of the ring holds the same columns of all of them and B_h's once.  With row_seq set, row r is written only if row_seq[r] >= 0.
+template <int N, int K, int STAGES, int TERMS>
 struct HeadGemm {
   static constexpr int KB = K / 64;             // 64-column (128-byte) k-blocks
-  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int A_TERM = 128 * 128;
+  static constexpr int A_BYTES = TERMS * A_TERM;
   static constexpr int B_BYTES = N * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int SMEM_BAR = STAGES * STAGE;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(192, 1)
                      int out_hstride, const __nv_bfloat16* __restrict__ rope_src, long long rope_ld,
                      int rope_hstride, int M, const int32_t* __restrict__ row_seq, int32_t* status,
                      const chunk::ChunkPlanArgs plan) {
-  using C = HeadGemm<N, K, STAGES>;
+  using C = HeadGemm<N, K, STAGES, TERMS>;
   struct Bars {
     uint64_t full[STAGES], empty[STAGES], done;
     uint32_t tmem;
@@ -131,17 +132,19 @@ __global__ void __launch_bounds__(192, 1)
       prefetch_tmap(&b_map);
       int last[STAGES];
       for (int s = 0; s < STAGES; ++s) last[s] = -1;
-      for (int kb = 0; kb < C::KB * TERMS; ++kb) {
+      for (int kb = 0; kb < C::KB; ++kb) {
         const int s = kb % STAGES;
         if (kb >= STAGES && !mbar_wait(smem_u32(&sh->empty[s]), ((kb / STAGES) & 1) ^ 1, status, abort_flag))
           break;
         const uint32_t full = smem_u32(&sh->full[s]);
         const uint32_t a = smem_u32(smem + s * C::STAGE);
         mbar_expect_tx(full, C::STAGE);
-        tma_load_2d(a, &a_map, full, a_col0 + h * a_hstride + kb * 64, m0);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+          tma_load_2d(a + term * C::A_TERM, &a_map, full, a_col0 + h * a_hstride + term * K + kb * 64, m0);
 #pragma unroll
         for (int nb = 0; nb < N; nb += C::NB)
-          tma_load_2d(a + C::A_BYTES + nb * 128, &b_map, full, kb % C::KB * 64, (h * SPLIT + nc) * N + nb);
+          tma_load_2d(a + C::A_BYTES + nb * 128, &b_map, full, kb * 64, (h * SPLIT + nc) * N + nb);
         last[s] = (kb / STAGES) & 1;
       }
       volatile int never = 0;
@@ -152,17 +155,18 @@ __global__ void __launch_bounds__(192, 1)
   } else if (warp == 1) {
     if (elect_one()) {
       bool ok = true;
-      for (int kb = 0; kb < C::KB * TERMS && ok; ++kb) {
+      for (int kb = 0; kb < C::KB && ok; ++kb) {
         const int s = kb % STAGES;
         if (!(ok = mbar_wait(smem_u32(&sh->full[s]), (kb / STAGES) & 1, status, abort_flag))) break;
         tc_fence_after();
         const uint32_t a = smem_u32(smem + s * C::STAGE);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t ad = sdesc(a + k * 32, 16, 1024);
+        for (int k = 0; k < 4 * TERMS; ++k) {                 // (term, 16 columns)
+          const int col = k % 4 * 32;
+          const uint64_t ad = sdesc(a + k / 4 * C::A_TERM + col, 16, 1024);
 #pragma unroll
           for (int nb = 0; nb < N; nb += C::NB)
-            mma_f16_ss(tmem + nb, ad, sdesc(a + C::A_BYTES + nb * 128 + k * 32, 16, 1024), C::IDESC,
+            mma_f16_ss(tmem + nb, ad, sdesc(a + C::A_BYTES + nb * 128 + col, 16, 1024), C::IDESC,
                        (kb | k) != 0);
         }
         tc_commit(smem_u32(&sh->empty[s]));
@@ -1072,7 +1076,7 @@ cudaError_t launch_head_gemm(const CUtensorMap& a_map, const CUtensorMap& b_map,
                              long long rope_ld, int rope_hstride, int M, int H, const int32_t* row_seq,
                              int32_t* status, cudaStream_t stream,
                              const chunk::ChunkPlanArgs& plan = chunk::ChunkPlanArgs{}) {
-  using C = HeadGemm<N, K, STAGES>;
+  using C = HeadGemm<N, K, STAGES, TERMS>;
   cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<N, K, STAGES, SPLIT, TERMS, PLAN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
   if (e != cudaSuccess) return e;
@@ -1113,9 +1117,16 @@ cudaError_t launch_project_outputs(const __nv_bfloat16* o_lat, bool two_terms, c
     return cudaErrorInvalidValue;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
   const long long ld = static_cast<long long>(H) * 128;
-  return two_terms ? launch_head_gemm<128, 512, 4, 1, 2>(ol_map, wuv_map, 0, 1024, o, ld, 128, nullptr, 0, 0, T, H,
-                                                         row_seq, status, stream)
-                   : launch_head_gemm<128, 512, 4>(ol_map, wuv_map, 0, 512, o, ld, 128, nullptr, 0, 0, T, H, row_seq,
+  if (!two_terms)
+    return launch_head_gemm<128, 512, 4>(ol_map, wuv_map, 0, 512, o, ld, 128, nullptr, 0, 0, T, H, row_seq, status,
+                                         stream);
+  // A CTA that is alone on its SM has more stages; of more CTAs than SMs, two fit
+  // one with two stages.  (Whole calls of chunk attention: 16 CTAs, 34.6 us with four
+  // stages, 35.6 with two; 1024 CTAs, 327 and 322.)
+  return static_cast<long long>((T + 127) / 128) * H <= sm_count()
+             ? launch_head_gemm<128, 512, 4, 1, 2>(ol_map, wuv_map, 0, 1024, o, ld, 128, nullptr, 0, 0, T, H, row_seq,
+                                                   status, stream)
+             : launch_head_gemm<128, 512, 2, 1, 2>(ol_map, wuv_map, 0, 1024, o, ld, 128, nullptr, 0, 0, T, H, row_seq,
                                                    status, stream);
 }
 
