@@ -104,7 +104,8 @@ struct ChunkParams {
   float* lse;                // [R] or null
   float4* o_part;            // [4 pairs][2][64][128]: a pair's first and last segment of each line
   float2* ml_part;           // [4 pairs][128] (max, sum)
-  SplitTile* split;          // [2][pairs]
+  SplitTile* split;          // [2 pairs]
+  bool by_tile;              // a row tile's place there is its number
   const uint32_t* odd_rows;  // [(T + 31) / 32]: tokens whose rows hold an infinity or NaN
   int num_pages, page_size, max_pages, cache_rows;
   FastDiv by_page;
@@ -847,12 +848,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           t.row0 = s.row0;
           t.rows = s.rows;
           t.seq = s.b;
+          t.c = s.c;
+          t.odd = pair & 1;
           t.first = from;
           t.slot = tail[from] == x0 ? 0 : 1;
           t.parts[0] = t.parts[1] = t.parts[2] = 0;
           for (int q = from; q <= worker; ++q)           // (parts of the line may be empty)
             if (tail[q] != tail[q + 1]) t.parts[(q - from) >> 5] |= 1u << ((q - from) & 31);
-          p.split[s.c * pairs + pair] = t;
+          const Base before = p.base[s.b];
+          p.split[p.by_tile ? 2 * before.items[0] + before.items[1] + s.r0 / kRows : s.c * pairs + pair] = t;
         }
       }
       tc_fence_before();
@@ -868,92 +872,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Split row tiles: blockIdx.x is the (class, pair) in whose part one ends.  A
-// warp takes 32 of the attention's threads' rows and 32 of their 256 columns,
-// kMergeTurns times.  What a short context waits for here are chains of loads, so
-// the sums and the rows of two parts are asked for at once, as soon as the tile's
-// record is there.
-constexpr int kMergeSlices = 8, kMergeWarps = 8, kMergeTurns = 64 / (kMergeSlices * kMergeWarps);
+// Split row tiles, blockIdx.x.  A warp takes 32 of the attention's threads' rows and
+// COLS of their 256 columns.  What is waited for here are chains of loads, so the
+// sums and the rows of PARTS parts are asked for at once, as soon as the tile's
+// record is there.  A few row tiles have many parts each and would leave SMs idle:
+// up to 8 of them take fewer columns a warp and more parts.  (Whole calls of 4 tokens:
+// over 40000 keys, 16 heads, one row tile of 76 parts, 68 us with 16 columns and 4
+// parts, 56 with 4 and 16; over 20000 keys, 128 heads, 54 and 50; but 12 tokens, 12 row
+// tiles, 78 and 82.)
+constexpr int kMergeWarps = 8;
+constexpr int merge_slices(int cols) { return 8 * 256 / cols / kMergeWarps; }
 
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p, int pairs) {
+template <int COLS, int PARTS>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const SplitTile t = p.split[blockIdx.x];
-  if (timed_out_before(p.status) || t.rows <= 0) return;
-  const int c = blockIdx.x / pairs, pair = blockIdx.x - c * pairs;
+  constexpr int kBlocks = 256 / COLS, kVecs = COLS / 4;
+  const int unit = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int part = unit % kBlocks, quarter = unit / kBlocks & 3, rank = unit / kBlocks >> 2;   // columns; rows, CTA
+  const int tl = quarter * 32 + lane, half = tl >> 6;
+  const int r = rank * 64 + (tl & 63);
+  if (timed_out_before(p.status) || r >= t.rows) return;
+  const int c = t.c;
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
-#pragma unroll 1
-  for (int turn = 0; turn < kMergeTurns; ++turn) {
-    const int unit = (turn * kMergeSlices + blockIdx.y) * kMergeWarps + (threadIdx.x >> 5);
-    const int rank = unit >> 5, quarter = unit >> 3 & 3, part = unit & 7;     // CTA, its rows, their columns
-    const int tl = quarter * 32 + lane, half = tl >> 6;
-    const int r = rank * 64 + (tl & 63);
-    uint32_t left[3] = {t.parts[0], t.parts[1], t.parts[2]};
-    auto next_slot = [&]() {                      // of the next part, or -1
-      const int w = left[0] ? 0 : left[1] ? 1 : 2;
-      const uint32_t m = w == 0 ? left[0] : w == 1 ? left[1] : left[2];
-      if (m == 0) return -1;
-      const int q = t.first + 32 * w + __ffs(m) - 1;
-      if (w == 0) left[0] &= m - 1;
-      else if (w == 1) left[1] &= m - 1;
-      else left[2] &= m - 1;
-      return 4 * (c == 0 ? 2 * q + (pair & 1) : q) + 2 * c + (q == t.first ? t.slot : 0);
-    };
-    float top = sink, sum = sink == kNegInf ? 0.0f : 1.0f;
-    float4 o[8] = {};
-    for (int s0 = next_slot(); s0 >= 0; s0 = next_slot()) {
-      const int s1 = next_slot();
-      float4 v[2][8];
-      float2 ml[2];
+  uint32_t left[3] = {t.parts[0], t.parts[1], t.parts[2]};
+  auto next_slot = [&]() {                      // of the next part, or -1
+    const int w = left[0] ? 0 : left[1] ? 1 : 2;
+    const uint32_t m = w == 0 ? left[0] : w == 1 ? left[1] : left[2];
+    if (m == 0) return -1;
+    const int q = t.first + 32 * w + __ffs(m) - 1;
+    if (w == 0) left[0] &= m - 1;
+    else if (w == 1) left[1] &= m - 1;
+    else left[2] &= m - 1;
+    return 4 * (c == 0 ? 2 * q + t.odd : q) + 2 * c + (q == t.first ? t.slot : 0);
+  };
+  float top = sink, sum = sink == kNegInf ? 0.0f : 1.0f;
+  float4 o[kVecs] = {};
+  for (int slot = next_slot(); slot >= 0; slot = next_slot()) {
+    float4 v[PARTS][kVecs];
+    float2 ml[PARTS];
+    float most = top;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int slot = u == 0 || s1 < 0 ? s0 : s1;
-        ml[u] = p.ml_part[slot * kRows + r];
-        const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * 8) * 128 + tl;
+    for (int u = 0; u < PARTS; ++u) {
+      if (u > 0 && slot >= 0) slot = next_slot();
+      ml[u] = make_float2(kNegInf, 0.0f);
+      if (slot < 0) continue;
+      ml[u] = p.ml_part[slot * kRows + r];
+      const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * kVecs) * 128 + tl;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = __ldcs(src + e * 128);
-      }
-      if (s1 < 0) ml[1] = make_float2(kNegInf, 0.0f);
-      const float most = fmaxf(top, fmaxf(ml[0].x, ml[1].x));
-      const float keep = top == kNegInf ? 0.0f : ex2(top - most);
-      top = most;
-      sum *= keep;
+      for (int e = 0; e < kVecs; ++e) v[u][e] = __ldcs(src + e * 128);
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
+    for (int u = 0; u < PARTS; ++u) most = fmaxf(most, ml[u].x);
+    const float keep = top == kNegInf ? 0.0f : ex2(top - most);
+    top = most;
+    sum *= keep;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (ml[u].y == 0.0f) continue;           // it saw nothing; it may have stored no rows
-        const float f = ml[u].x == kNegInf ? ml[u].y * 0.0f : ex2(ml[u].x - top);
-        sum = fmaf(ml[u].y, f, sum);
+    for (int e = 0; e < kVecs; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[e].x = fmaf(v[u][e].x, f, o[e].x);
-          o[e].y = fmaf(v[u][e].y, f, o[e].y);
-          o[e].z = fmaf(v[u][e].z, f, o[e].z);
-          o[e].w = fmaf(v[u][e].w, f, o[e].w);
-        }
+    for (int u = 0; u < PARTS; ++u) {
+      if (ml[u].y == 0.0f) continue;           // it saw nothing; it may have stored no rows
+      const float f = ml[u].x == kNegInf ? ml[u].y * 0.0f : ex2(ml[u].x - top);
+      sum = fmaf(ml[u].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < kVecs; ++e) {
+        o[e].x = fmaf(v[u][e].x, f, o[e].x);
+        o[e].y = fmaf(v[u][e].y, f, o[e].y);
+        o[e].z = fmaf(v[u][e].z, f, o[e].z);
+        o[e].w = fmaf(v[u][e].w, f, o[e].w);
       }
     }
-    if (r >= t.rows) continue;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint4* hi = reinterpret_cast<uint4*>(p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (part >> 2) * 256 +
-                                         half * 128 + (part & 3) * 32);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float x[8] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv,
-                          o[e + 1].x * inv, o[e + 1].y * inv, o[e + 1].z * inv, o[e + 1].w * inv};
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        l[i] = pack_bf16(x[2 * i] - bf16_lo(h[i]), x[2 * i + 1] - bf16_hi(h[i]));
-      }
-      hi[e >> 1] = make_uint4(h[0], h[1], h[2], h[3]);
-      hi[64 + (e >> 1)] = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-    if (p.lse != nullptr && part == 0 && half == 0)
-      p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
+    if (slot < 0) break;
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int col = part * COLS;           // of the 256: 128 of each half of the 512
+  __nv_bfloat16* hi = p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (col >> 7) * 256 + half * 128 + (col & 127);
+#pragma unroll
+  for (int e = 0; e < kVecs; ++e) {
+    const float x[4] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv};
+    const uint32_t h0 = pack_bf16(x[0], x[1]), h1 = pack_bf16(x[2], x[3]);
+    const uint32_t l0 = pack_bf16(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)), l1 = pack_bf16(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1));
+    *reinterpret_cast<uint2*>(hi + 4 * e) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>(hi + 512 + 4 * e) = make_uint2(l0, l1);
+  }
+  if (p.lse != nullptr && part == 0 && half == 0)
+    p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
 }
 
 struct Layout {
@@ -992,6 +996,8 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   __nv_bfloat16* q_full = reinterpret_cast<__nv_bfloat16*>(ws + L.q_full);
   const int pairs = std::max(2, std::min(kMaxPairs, sm_count() / 2));
+  const long long row_tiles = static_cast<long long>(R) / kRows + a.B;      // at most
+  const bool few_tiles = row_tiles <= 8;
 
   ChunkParams p;
   p.iro = a.iro;
@@ -1006,6 +1012,7 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.o_part = reinterpret_cast<float4*>(ws + L.o_part);
   p.ml_part = reinterpret_cast<float2*>(ws + L.ml_part);
   p.split = reinterpret_cast<SplitTile*>(ws + L.split);
+  p.by_tile = row_tiles <= 2 * pairs;
   p.odd_rows = reinterpret_cast<const uint32_t*>(ws + L.odd_rows);
   p.num_pages = a.num_pages;
   p.page_size = a.page_size;
@@ -1055,7 +1062,6 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   // Two terms where a pair has one tile or two at most, by what the host knows: the
   // row tiles that there can be, and the tiles of the longest context that the page
   // table holds.
-  const long long row_tiles = static_cast<long long>(R) / kRows + a.B;
   const long long key_tiles = std::min((static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile,
                                        static_cast<long long>(kMaxContext));
   const auto kernel = row_tiles * key_tiles <= 2 * pairs ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
@@ -1064,9 +1070,9 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   if ((e = launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
       cudaSuccess)
     return e;
-  if ((e = launch_pdl(chunk_merge_kernel, dim3(2 * pairs, kMergeSlices), dim3(kMergeWarps * 32), 0, stream, p, pairs)) !=
-      cudaSuccess)
-    return e;
+  const auto merge = few_tiles ? chunk_merge_kernel<4, 16> : chunk_merge_kernel<16, 4>;
+  const dim3 merge_grid(p.by_tile ? static_cast<int>(row_tiles) : 2 * pairs, merge_slices(few_tiles ? 4 : 16));
+  if ((e = launch_pdl(merge, merge_grid, dim3(kMergeWarps * 32), 0, stream, p)) != cudaSuccess) return e;
   return launch_project_outputs(p.o_lat, true, a.w_uv, a.out, a.T, a.H, pa.token_seq, a.status, stream);
 }
 

@@ -12,9 +12,12 @@ constexpr int kRows = 128;                   // query rows of a pair of SMs
 constexpr int kMaxPairs = 76;
 static_assert(kMaxPairs <= 96, "bits of SplitTile::parts");
 
-// A split row tile, noted by the worker in whose part of the line it ends.
+// A split row tile, noted by the worker in whose part of the line it ends: in the
+// place of the row tile, where there are no more of them than 2 pairs, else in the
+// worker's.
 struct SplitTile {
   int row0, rows, seq;
+  int c, odd;           // class; which pair of a group
   int first, slot;      // the worker in whose part it begins, and its slot there
   uint32_t parts[3];    // bit q: worker first + q holds a part of it
 };
