@@ -824,7 +824,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int worker = s.c == 0 ? pair >> 1 : pair;
         const int* const tail = p.schedule->tail[s.c];
         const int slot = 4 * pair + 2 * s.c + (s.x == tail[worker] ? 0 : 1);
-        if (first) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
+        if (first && live) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
         if (s.tiles > 0) {
           // Laid out as the threads hold it: [CTA][column / 4 of the 256][TMEM lane].
           float4* dst = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64) * 128 + tl;
@@ -833,6 +833,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t o[32];
             tmem_ld32(o_at + c * 32, o);
             tmem_ld_wait();
+            if (!live) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[(c * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
