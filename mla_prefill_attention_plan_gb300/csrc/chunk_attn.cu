@@ -876,11 +876,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Split row tiles, blockIdx.x.  A warp takes 32 of the attention's threads' rows and
 // COLS of their 256 columns.  What is waited for here are chains of loads, so the
 // sums and the rows of PARTS parts are asked for at once, as soon as the tile's
-// record is there.  A few row tiles have many parts each and would leave SMs idle:
-// up to 8 of them take fewer columns a warp and more parts.  (Whole calls of 4 tokens:
-// over 40000 keys, 16 heads, one row tile of 76 parts, 68 us with 16 columns and 4
-// parts, 56 with 4 and 16; over 20000 keys, 128 heads, 54 and 50; but 12 tokens, 12 row
-// tiles, 78 and 82.)
+// record is there.  The fewer row tiles there are, the more parts they have and the
+// more warps it takes to keep the SMs busy; with many of them warps cost more than
+// they bring.  (Whole calls.  4 tokens over 40000 keys, 16 heads, one row tile of 76
+// parts: 87 us with 32 columns and 2 parts, 68 with 16 and 4, 56 with 4 and 16.  12
+// tokens over 20000, 128 heads, 12 row tiles: 83, 78, 82.  76 sequences of 8 tokens over
+// 2000, 16 heads, 76 row tiles that nothing splits: 83 with 32, 85 with 16.)
 constexpr int kMergeWarps = 8;
 constexpr int merge_slices(int cols) { return 8 * 256 / cols / kMergeWarps; }
 
@@ -998,7 +999,6 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   __nv_bfloat16* q_full = reinterpret_cast<__nv_bfloat16*>(ws + L.q_full);
   const int pairs = std::max(2, std::min(kMaxPairs, sm_count() / 2));
   const long long row_tiles = static_cast<long long>(R) / kRows + a.B;      // at most
-  const bool few_tiles = row_tiles <= 8;
 
   ChunkParams p;
   p.iro = a.iro;
@@ -1071,8 +1071,9 @@ cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream) {
   if ((e = launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), kSmemTotal, stream, q_map, maps, p)) !=
       cudaSuccess)
     return e;
-  const auto merge = few_tiles ? chunk_merge_kernel<4, 16> : chunk_merge_kernel<16, 4>;
-  const dim3 merge_grid(p.by_tile ? static_cast<int>(row_tiles) : 2 * pairs, merge_slices(few_tiles ? 4 : 16));
+  const int cols = row_tiles <= 8 ? 4 : row_tiles <= pairs / 2 ? 16 : 32;
+  const auto merge = cols == 4 ? chunk_merge_kernel<4, 16> : cols == 16 ? chunk_merge_kernel<16, 4> : chunk_merge_kernel<32, 2>;
+  const dim3 merge_grid(p.by_tile ? static_cast<int>(row_tiles) : 2 * pairs, merge_slices(cols));
   if ((e = launch_pdl(merge, merge_grid, dim3(kMergeWarps * 32), 0, stream, p)) != cudaSuccess) return e;
   return launch_project_outputs(p.o_lat, true, a.w_uv, a.out, a.T, a.H, pa.token_seq, a.status, stream);
 }

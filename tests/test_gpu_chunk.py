@@ -564,3 +564,12 @@ def test_odd_keys_behind_sequences_without_tokens(empty):
         assert torch.isnan(c.out[t]).all() and torch.isnan(c.lse[t]).all()
         c.out[t], c.lse[t] = FILL, FILL
     c.compare(out, lse, slack)
+
+
+@pytest.mark.parametrize("B", [1, 4, 20, 60, 250])
+def test_a_long_sequence_among_short_ones(B):
+    """Row tiles of many parts, of one and of none, however many row tiles there are."""
+    rng = np.random.default_rng(B)
+    cached = list(rng.integers(0, 400, B))
+    cached[B // 2] = 9000
+    Case(list(rng.integers(1, 30, B)), cached, 8, 64, seed=B, sink=True).check()
