@@ -950,13 +950,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int col = part * COLS;           // of the 256: 128 of each half of the 512
   __nv_bfloat16* hi = p.o_lat + static_cast<size_t>(t.row0 + r) * 1024 + (col >> 7) * 256 + half * 128 + (col & 127);
+  uint2 h[kVecs], l[kVecs];
 #pragma unroll
   for (int e = 0; e < kVecs; ++e) {
     const float x[4] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv};
-    const uint32_t h0 = pack_bf16(x[0], x[1]), h1 = pack_bf16(x[2], x[3]);
-    const uint32_t l0 = pack_bf16(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)), l1 = pack_bf16(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1));
-    *reinterpret_cast<uint2*>(hi + 4 * e) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>(hi + 512 + 4 * e) = make_uint2(l0, l1);
+    h[e] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    l[e] = make_uint2(pack_bf16(x[0] - bf16_lo(h[e].x), x[1] - bf16_hi(h[e].x)),
+                      pack_bf16(x[2] - bf16_lo(h[e].y), x[3] - bf16_hi(h[e].y)));
+  }
+  if constexpr (kVecs == 1) {
+    *reinterpret_cast<uint2*>(hi) = h[0];
+    *reinterpret_cast<uint2*>(hi + 512) = l[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVecs; e += 2) {
+      *reinterpret_cast<uint4*>(hi + 4 * e) = make_uint4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
+      *reinterpret_cast<uint4*>(hi + 512 + 4 * e) = make_uint4(l[e].x, l[e].y, l[e + 1].x, l[e + 1].y);
+    }
   }
   if (p.lse != nullptr && part == 0 && half == 0)
     p.lse[t.row0 + r] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kLn2;
