@@ -895,31 +895,34 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
   const int part = unit % kBlocks, quarter = unit / kBlocks & 3, rank = unit / kBlocks >> 2;   // columns; rows, CTA
   const int tl = quarter * 32 + lane, half = tl >> 6;
   const int r = rank * 64 + (tl & 63);
-  if (timed_out_before(p.status) || r >= t.rows) return;
-  const int c = t.c;
+  if (timed_out_before(p.status) || t.rows <= 0) return;
+  // The slots of the parts, in order (found one after the other they took as long as
+  // the loads).
+  __shared__ int slots[kMergeWarps][96];
+  int* const slot_of = slots[threadIdx.x >> 5];
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    const int q = t.first + 32 * w + lane;
+    if (t.parts[w] >> lane & 1)
+      slot_of[n + __popc(t.parts[w] & ((1u << lane) - 1))] =
+          4 * (t.c == 0 ? 2 * q + t.odd : q) + 2 * t.c + (q == t.first ? t.slot : 0);
+    n += __popc(t.parts[w]);
+  }
+  __syncwarp();
+  if (r >= t.rows) return;
   const float sink = p.sink != nullptr ? p.sink[t.seq] * kLog2e : kNegInf;
-  uint32_t left[3] = {t.parts[0], t.parts[1], t.parts[2]};
-  auto next_slot = [&]() {                      // of the next part, or -1
-    const int w = left[0] ? 0 : left[1] ? 1 : 2;
-    const uint32_t m = w == 0 ? left[0] : w == 1 ? left[1] : left[2];
-    if (m == 0) return -1;
-    const int q = t.first + 32 * w + __ffs(m) - 1;
-    if (w == 0) left[0] &= m - 1;
-    else if (w == 1) left[1] &= m - 1;
-    else left[2] &= m - 1;
-    return 4 * (c == 0 ? 2 * q + t.odd : q) + 2 * c + (q == t.first ? t.slot : 0);
-  };
   float top = sink, sum = sink == kNegInf ? 0.0f : 1.0f;
   float4 o[kVecs] = {};
-  for (int slot = next_slot(); slot >= 0; slot = next_slot()) {
+  for (int k = 0; k < n; k += PARTS) {
     float4 v[PARTS][kVecs];
     float2 ml[PARTS];
     float most = top;
 #pragma unroll
     for (int u = 0; u < PARTS; ++u) {
-      if (u > 0 && slot >= 0) slot = next_slot();
       ml[u] = make_float2(kNegInf, 0.0f);
-      if (slot < 0) continue;
+      if (k + u >= n) continue;
+      const int slot = slot_of[k + u];
       ml[u] = p.ml_part[slot * kRows + r];
       const float4* src = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64 + part * kVecs) * 128 + tl;
 #pragma unroll
@@ -945,7 +948,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
         o[e].w = fmaf(v[u][e].w, f, o[e].w);
       }
     }
-    if (slot < 0) break;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int col = part * COLS;           // of the 256: 128 of each half of the 512
