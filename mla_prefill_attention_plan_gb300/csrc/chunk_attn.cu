@@ -31,9 +31,9 @@
 // us, 1510 TFLOP/s, 7050 clk a tile (a ring of 5, 6, 7 stages: 864, 804, 777 us).
 // Where a row tile is alone with its context, HBM's latency and the second read of
 // a tile from L2 come on top: 32 sequences of 8 tokens over 20000 keys, 16 heads,
-// 205 us for 740 MB, 4.6 us a tile; on pages of 16, whose tiles are 16 boxes, the
-// loads' issue (10 tokens: 284 us on pages of 64, 372 on pages of 16).  A short
-// context is chains of dependent loads: 35 us for one tree over 1000 keys.
+// 203 us for 740 MB, 4.6 us a tile; on pages of 16, whose tiles are 16 boxes, the
+// loads' issue (10 tokens: 277 us on pages of 64, 368 on pages of 16).  A short
+// context is chains of dependent loads: 32 us for one tree over 1000 keys.
 //
 // Who does what, found on the device from the lengths: the row tiles of a
 // sequence, two by two, are items that two pairs work at side by side (class
@@ -63,7 +63,7 @@ constexpr int kStage = 16 * 1024;
 // and 0.0022 with two, of which the output's own rounding is 0.0017 and the
 // projected query's 0.0014.  A small call waits for chains of loads, not for MMAs,
 // and is as fast on a ring of 5 stages, which leaves room for the second term: one
-// tree of 6 over 1000 keys, 16 heads, 33.5 us with one and 35.3 with two.  Of larger
+// tree of 6 over 1000 keys, 16 heads, 30.0 us with one and 31.7 with two.  Of larger
 // calls the products are what bounds them: 8 chunks of 64 over 2000 keys, 128 heads,
 // took 340 us with one and 499 with two.
 __host__ __device__ constexpr int ring_stages(bool two) { return two ? 5 : 7; }
@@ -878,10 +878,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // sums and the rows of PARTS parts are asked for at once, as soon as the tile's
 // record is there.  The fewer row tiles there are, the more parts they have and the
 // more warps it takes to keep the SMs busy; with many of them warps cost more than
-// they bring.  (Whole calls.  4 tokens over 40000 keys, 16 heads, one row tile of 76
-// parts: 87 us with 32 columns and 2 parts, 68 with 16 and 4, 56 with 4 and 16.  12
-// tokens over 20000, 128 heads, 12 row tiles: 83, 78, 82.  76 sequences of 8 tokens over
-// 2000, 16 heads, 76 row tiles that nothing splits: 83 with 32, 85 with 16.)
+// they bring.  (Whole calls with 4, 16, 32 columns: 4 tokens over 40000 keys, 16
+// heads, one row tile of 76 parts, 50, 67, 92 us; 12 tokens over 20000, 128 heads, 12
+// row tiles, 80, 78, 82; 76 sequences of 8 tokens over 2000, 16 heads, 76 row tiles
+// that nothing splits, 100, 85, 83.)
 constexpr int kMergeWarps = 8;
 constexpr int merge_slices(int cols) { return 8 * 256 / cols / kMergeWarps; }
 
