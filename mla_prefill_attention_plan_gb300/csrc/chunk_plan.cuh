@@ -81,8 +81,8 @@ __device__ __forceinline__ int last_of(int B, F before) {
 }
 
 // By one CTA of kPlanThreads, with kKeepBases Base of shared memory: the bases are
-// searched there if they fit (76 sequences: 9 us from global memory, which is
-// longer than the projection beside it).
+// searched there if they fit.  (500 sequences of 3 tokens over 600 keys, 16 heads: a
+// call takes 182 us with that and the pairs' searches by warps, 203 without.)
 template <int kPlanThreads, int kKeepBases>
 __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a, Base* kept) {
   constexpr int kWarps = kPlanThreads / 32;
