@@ -65,7 +65,7 @@ constexpr int kStage = 16 * 1024;
 // and is as fast on a ring of 5 stages, which leaves room for the second term: one
 // tree of 6 over 1000 keys, 16 heads, 30.0 us with one and 31.7 with two.  Of larger
 // calls the products are what bounds them: 8 chunks of 64 over 2000 keys, 128 heads,
-// took 340 us with one and 499 with two.
+// took 340 us with one and 499 with two (on seven stages, a tile in two steps).
 __host__ __device__ constexpr int ring_stages(bool two) { return two ? 5 : 7; }
 constexpr int kQBytes = 9 * 64 * 128;        // 64 rows x 576 columns in blocks of 64
 constexpr int kPBytes = 4 * 64 * 128;        // 64 rows x 256 keys in blocks of 64
