@@ -487,10 +487,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++tile;
           }
         }
-        // The last arrival of this CTA's commits in either CTA.
+        // The last arrival of this CTA's commits in either CTA.  (The other CTA waits
+        // for it when its softmax is through: a wait is for one step of the pipeline,
+        // never for as long as the call takes.)
         tc_commit_pair(smem_u32(&sh->drain), 3);
+        mbar_wait(smem_u32(&sh->drain), 0, status, &never);
       }
-      mbar_wait(smem_u32(&sh->drain), 0, status, &never);
     }
     __syncwarp();
   } else if (warp == 6) {
@@ -864,6 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (The next segment's first product is ordered behind these reads by the
       // arrival on p_full.)
     }
+    if (rank == 1 && warp == 2) mbar_wait_warp(smem_u32(&sh->drain), 0, status, &never);
   }
 
   tc_fence_before();

@@ -573,3 +573,44 @@ def test_a_long_sequence_among_short_ones(B):
     cached = list(rng.integers(0, 400, B))
     cached[B // 2] = 9000
     Case(list(rng.integers(1, 30, B)), cached, 8, 64, seed=B, sink=True).check()
+
+
+@pytest.mark.parametrize("size", ["any"], indirect=True)
+def test_a_call_that_takes_longer_than_a_wait_may(size):
+    """Waits are limited to two seconds each, calls are not: 4096 tokens over a context of small pages, which hold the
+    same few rows again and again.  out is as over those rows once, with how often each is seen as its weight.
+    The products are added up in fp32, at most 2^-23 off each of the 16 steps of a tile; the sums of the weights,
+    128 a tile and thread, by half of that to either side, of which eight times the root mean square is allowed."""
+    rng = np.random.default_rng(4)
+    H, T, pool, cached = 128, 4096, 4096, 800000
+    kv_d, kv = bf16(rng.standard_normal((pool, 576)))
+    q_d = torch.randn(T, H, 192, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(torch.bfloat16)
+    uk_d, uk = bf16(rng.standard_normal((H, 512, 128)) * 512 ** -0.5)
+    uv_d, uv = bf16(rng.standard_normal((H, 128, 512)) * 512 ** -0.5)
+    table = dev(rng.permutation(pool)[np.arange(cached + T) % pool][None])
+    iro, lengths, st = dev([0, T]), dev([cached]), dev([0])
+    out, lse = torch.full((T, H, 128), FILL, dtype=torch.bfloat16, device=DEV), torch.full((T, H), FILL, device=DEV)
+    size = mla.mla_chunk_attention_workspace_bytes(1, H, T)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    mla.check(mla.mla_chunk_attention(out, lse, q_d, iro, lengths, kv_d, table, pool, 1, cached + T, uk_d, uv_d, 1, H, T,
+                                      192 ** -0.5, workspace=ws, workspace_bytes=size, d_status=st))
+    end.record()
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert begin.elapsed_time(end) > 2000, "the call no longer takes as long as this test needs it to"
+    order = table[0, :pool].cpu().numpy()
+    for t, h in ((0, 0), (0, 77), (1777, 5), (T - 1, 127)):
+        q, seen = q_d[t, h].double().cpu().numpy(), cached + t + 1
+        times = np.empty(pool)
+        times[order] = seen // pool + (np.arange(pool) < seen % pool)
+        lat = uk[h] @ q[:128]
+        s = 192 ** -0.5 * (kv[:, :512] @ lat + kv[:, 512:] @ q[128:])
+        w = times * np.exp(s - s.max())
+        want = uv[h] @ (w @ kv[:, :512] / w.sum())
+        got = out[t, h].double().cpu().numpy()
+        assert np.linalg.norm(got - want) <= (ROW + 16 * (seen / 256 + 1) * 2.0 ** -23) * np.linalg.norm(want)
+        slack = 192 ** -0.5 * (np.abs(kv[:, :512]) @ np.abs(lat)).max()
+        assert abs(lse[t, h].item() - (s.max() + np.log(w.sum()))) <= (
+            2.0 ** -8 * slack + 8 * np.sqrt(seen / 2) * 2.0 ** -24)
