@@ -961,7 +961,9 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  * one more logit without a value.  A token that sees nothing gets out = 0 and
  * lse = -infinity (the sink's logit with one).  A key that a token does not see
  * has no part in its result, whatever it holds; one that it sees and that has an
- * infinite or NaN latent value makes the token's out and lse NaN.
+ * infinite or NaN latent value makes the token's out and lse NaN.  (Its lse stays
+ * a number if the key is a cached one and its logit is -infinity: nothing is added
+ * to the sum.)
  * Longer chunks than about 170 tokens are as right, but mla_prefill then has
  * less to compute.
  * Rounding: the projected query and the softmax weights are bf16 (the weights two

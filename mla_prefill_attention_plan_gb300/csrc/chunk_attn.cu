@@ -716,8 +716,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld32(o_at + c * 32, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = factor == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * factor);
+            for (int e = 0; e < 32; ++e) {
+              // (No part of the sum is left at a factor of 0, but a NaN that a key of
+              // weight 0 with an infinite value has brought.)
+              const float v = __uint_as_float(o[e]);
+              o[e] = __float_as_uint(factor != 0.0f ? v * factor : v == v ? 0.0f : v);
+            }
             tmem_st32(o_at + c * 32, o);
           }
           tmem_st_wait();
@@ -776,8 +780,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else if (p.lse != nullptr && live && first) {
           p.lse[s.row0 + local] = none ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
-        // (A row that saw nothing has zeros in O: no key of its sequence is there
-        // but finite ones with weight 0.)
+        // (A row that saw nothing has zeros in O: what it does not see is finite.
+        // Logits of -infinity alone, of keys with infinite values, leave NaN there.)
         const float unit = none ? 0.0f : 1.0f / sum;
         // 32 columns at a time through the warp's part of P (32 rows x 128 bytes):
         // the first term, the upper halves of the floats, then the second, what is
@@ -826,7 +830,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int worker = s.c == 0 ? pair >> 1 : pair;
         const int* const tail = p.schedule->tail[s.c];
         const int slot = 4 * pair + 2 * s.c + (s.x == tail[worker] ? 0 : 1);
-        if (first && live) p.ml_part[slot * kRows + local] = make_float2(ref, sum);
+        // (A sum below 0 says that there is no O.)
+        if (first && live) p.ml_part[slot * kRows + local] = make_float2(ref, s.tiles > 0 ? sum : -1.0f);
         if (s.tiles > 0) {
           // Laid out as the threads hold it: [CTA][column / 4 of the 256][TMEM lane].
           float4* dst = p.o_part + ((static_cast<size_t>(slot) * 2 + rank) * 64) * 128 + tl;
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
     float most = top;
 #pragma unroll
     for (int u = 0; u < PARTS; ++u) {
-      ml[u] = make_float2(kNegInf, 0.0f);
+      ml[u] = make_float2(kNegInf, -1.0f);
       if (k + u >= n) continue;
       const int slot = slot_of[k + u];
       ml[u] = p.ml_part[slot * kRows + r];
@@ -940,7 +945,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
     for (int e = 0; e < kVecs; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
 #pragma unroll
     for (int u = 0; u < PARTS; ++u) {
-      if (ml[u].y == 0.0f) continue;           // it saw nothing; it may have stored no rows
+      if (ml[u].y < 0.0f) continue;            // it had no tiles and stored no rows
       const float f = ml[u].x == kNegInf ? ml[u].y * 0.0f : ex2(ml[u].x - top);
       sum = fmaf(ml[u].y, f, sum);
 #pragma unroll

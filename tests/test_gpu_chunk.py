@@ -614,3 +614,63 @@ def test_a_call_that_takes_longer_than_a_wait_may(size):
         slack = 192 ** -0.5 * (np.abs(kv[:, :512]) @ np.abs(lat)).max()
         assert abs(lse[t, h].item() - (s.max() + np.log(w.sum()))) <= (
             2.0 ** -8 * slack + 8 * np.sqrt(seen / 2) * 2.0 ** -24)
+
+
+def infinite_keys(c, js, column, logit):
+    """Cached positions js of the only token, head 0, with an infinite value in a latent column, so that their logits
+    are logit (+-infinity); (out, lse) of what is left."""
+    lat = c.uk[0] @ c.q[0, 0, :128]
+    for j in js:
+        poisoned(c, j, slice(column, column + 1), float(np.sign(lat[column])) * logit)
+    rest = np.setdiff1d(np.arange(c.cached[0] + 1), js)
+    at = c.table[0, rest // c.page] * c.page + rest % c.page
+    s = c.scale * (c.kv[at, :512] @ lat + c.kv[at, 512:] @ c.q[0, 0, 128:])
+    slack = c.scale * (np.abs(c.kv[at, :512]) @ np.abs(lat)).max()
+    return s.max() + np.log(np.exp(s - s.max()).sum()), slack
+
+
+@pytest.mark.parametrize("logit", [-np.inf, np.inf])
+@pytest.mark.parametrize("column", [0, 200, 511])
+@pytest.mark.parametrize("cached,js", [
+    (700, [3]), (700, [699]), (700, range(256)), (700, range(128)), (700, range(256, 512)), (700, range(512, 700)),
+    (20000, range(256)), (20000, range(128, 256)), (20000, range(512, 1024)), (20000, [19000]), (20000, range(20000))])
+def test_a_cached_key_with_an_infinite_value_is_nan_for_all(cached, js, column, logit):
+    """Also where its logit, -infinity, is all that a tile or a part of the line has: softmax of it is 0, and 0 times
+    infinity is no number."""
+    c = Case([1, 1], [cached, 9], 1, 64, mask="causal", seed=cached + column)
+    want, slack = infinite_keys(c, js, column, logit)
+    mla.check(c.call())
+    assert c.st.item() == 0
+    assert torch.isnan(c.out[0]).all() and torch.isfinite(c.out[1]).all() and torch.isfinite(c.lse[1]).all()
+    if logit > 0:
+        assert torch.isnan(c.lse[0]).all()
+    else:
+        assert abs(c.lse[0].item() - want) <= 2.0 ** -8 * slack + 2.0 ** -20 * (1 + abs(want))
+
+
+@pytest.mark.parametrize("B", [1, 160])
+def test_no_number_is_forgotten_when_the_maximum_jumps(B):
+    """A key of weight 0 with an infinite value, then keys that are above all before them by more than 2^-126 leaves."""
+    c = Case([1] * B, [700] * B, 1, 64, mask="causal", seed=2)
+    lat = c.uk[0] @ c.q[0, 0, :128]
+    j = np.arange(300, 701)
+    at = c.table[0, j // 64] * 64 + j % 64
+    rows = c.kv.copy()
+    rows[at, :512] += 250 / c.scale * lat / (lat @ lat)
+    c.kv_d, c.kv = bf16(rows)
+    infinite_keys(c, [5], 17, -np.inf)
+    mla.check(c.call())
+    assert torch.isnan(c.out[0]).all() and torch.isfinite(c.out[1:]).all() and torch.isfinite(c.lse).all()
+
+
+def test_a_key_that_is_cached_and_no_number():
+    """NaN in a latent or rope column, of one sequence's context: nobody else's."""
+    for column in (0, 511, 512, 575):
+        c = Case([3, 2, 1], [500, 300, 40], 8, 16, sink=True)
+        out, lse, slack = c.oracle()
+        poisoned(c, 77, slice(column, column + 1), float("nan"))
+        mla.check(c.call())
+        assert torch.isnan(c.out[:3]).all() and torch.isnan(c.lse[:3]).all()
+        c.out[:3], c.lse[:3] = FILL, FILL
+        lse[:3] = np.nan
+        c.compare(out, lse, slack)
