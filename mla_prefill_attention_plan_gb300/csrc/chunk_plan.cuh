@@ -36,7 +36,8 @@ struct Base {
 
 // Items of every sequence, their prefix sums, the workers' shares, and each
 // token's sequence.  A sequence is left out (no items, no tokens) if its rows
-// are not there.
+// are not there, or if its context is longer than its row of the page table: a
+// wrong length costs the other sequences nothing.
 struct ChunkPlanArgs {
   const uint32_t* iro;
   const uint32_t* cache_len;
@@ -115,6 +116,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a, Base* kept) {
       const long long n = at.q1 - at.q0, L = static_cast<long long>(at.cached) + n;
       if (at.q1 > static_cast<uint32_t>(a.T) || (a.masked && n > 32ll * a.words) || L > kMaxContext) {
         set_status(a.status, MLA_DEV_BAD_OFFSETS);
+      } else if (n > 0 && L > static_cast<long long>(a.max_pages) * a.page_size) {
+        set_status(a.status, MLA_DEV_BAD_PAGE);
       } else if (n > 0) {
         const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
         own.x = static_cast<int>(tiles / 2);

@@ -674,3 +674,24 @@ def test_a_key_that_is_cached_and_no_number():
         c.out[:3], c.lse[:3] = FILL, FILL
         lse[:3] = np.nan
         c.compare(out, lse, slack)
+
+
+@pytest.mark.parametrize("sink", [True, False])
+@pytest.mark.parametrize("long", [0, 1, 1 << 20, 1 << 30])
+def test_a_context_longer_than_its_pages_is_left_out(long, sink):
+    """A wrong length beside good ones: its rows stay, theirs are right.  (At 0 the context
+    ends with the last page of the row.)"""
+    c = Case([3, 2, 4], [100, 100, 3], 4, 16, sink=sink)
+    out, lse, slack = c.oracle()
+    cached = list(c.cached)
+    cached[1] = c.most * c.page - 2 + long
+    c.ints[1] = dev(cached)
+    mla.check(c.call())
+    assert c.st.item() == mla.MLA_DEV_BAD_PAGE
+    if long:
+        assert (c.out[3:5] == FILL).all() and (c.lse[3:5] == FILL).all()
+    else:
+        assert (c.out[3:5] != FILL).any()            # (pages are missing, but there is room for them)
+        c.out[3:5], c.lse[3:5] = FILL, FILL
+    lse[3:5] = np.nan
+    c.compare(out, lse, slack)
