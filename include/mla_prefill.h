@@ -986,7 +986,9 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  * or more), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens, more new tokens than 32 * mask_words
  * or a context of more than 2^31 - 8192: sequence b is left out; offsets that
- * decrease or do not begin at 0: all are), MLA_DEV_BAD_PAGE (a context longer than
+ * decrease or do not begin at 0: all are, and so are those of a call of 2^31 - 1 or
+ * more tiles of 256 (token, head) rows of a sequence by 256 keys, or as many of the
+ * up to 128 rows that a sequence has left over), MLA_DEV_BAD_PAGE (a context longer than
  * max_pages_per_seq pages: its sequence is left out; a missing page or an id out of
  * range: the result of its sequence is not meaningful), MLA_DEV_TIMEOUT.  Rows of out and lse of tokens outside every sequence, or of
  * one that is left out, are not written.

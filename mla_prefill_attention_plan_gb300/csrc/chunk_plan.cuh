@@ -122,7 +122,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkPlanArgs& a, Base* kept) {
         const long long tiles = (n * a.H + kRows - 1) / kRows, kt = (L + kTile - 1) / kTile;
         own.x = static_cast<int>(tiles / 2);
         own.y = static_cast<int>(tiles & 1);
-        // (2^31 units would be a day's work; positions saturate, see below.)
+        // (2^31 units are some 100 to 200 s of work, at 3.6 us a tile; sums saturate and
+        // the call is refused, see below.)
         own.z = static_cast<int>(min(tiles / 2 * kt, 0x7FFFFFFFll));
         own.w = own.y ? static_cast<int>(kt) : 0;
         token0 = static_cast<int>(at.q0);

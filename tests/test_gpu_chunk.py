@@ -695,3 +695,26 @@ def test_a_context_longer_than_its_pages_is_left_out(long, sink):
         c.out[3:5], c.lse[3:5] = FILL, FILL
     lse[3:5] = np.nan
     c.compare(out, lse, slack)
+
+
+@pytest.mark.parametrize("size", ["any"], indirect=True)
+@pytest.mark.parametrize("H,many", [(128, 600), (1, 300)])
+def test_more_tiles_than_are_counted(H, many):
+    """Contexts of 2^31 keys on one page again and again: for 300 pairs of row tiles of one sequence, and for the one
+    row tile of each of 300 sequences, the tiles do not fit 31 bits.  Nothing is worked at, and all rows stay."""
+    one = H > 1
+    new, page, most = [many] if one else [1] * many, 1 << 16, 1 << 15
+    c = Case([2], [30], H, 16, mask="causal")
+    T = sum(new)
+    iro, cached = dev(np.concatenate([[0], np.cumsum(new)])), dev([(1 << 31) - 8192 - n for n in new])
+    kv, table = torch.zeros(page, 576, dtype=torch.bfloat16, device=DEV), dev(np.zeros((len(new), most)))
+    q = torch.zeros(T, H, 192, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.full((T, H, 128), FILL, dtype=torch.bfloat16, device=DEV), torch.full((T, H), FILL, device=DEV)
+    size = mla.mla_chunk_attention_workspace_bytes(len(new), H, T)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    mla.check(mla.mla_chunk_attention(out, lse, q, iro, cached, kv, table, 1, page, most, c.uk_d, c.uv_d, len(new), H, T,
+                                      1.0, workspace=ws, workspace_bytes=size, d_status=c.st))
+    assert c.st.item() == mla.MLA_DEV_BAD_OFFSETS
+    assert (out == FILL).all() and (lse == FILL).all()
+    c.st.zero_()
+    c.check()
