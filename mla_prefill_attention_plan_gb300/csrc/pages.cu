@@ -541,14 +541,14 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPoolThreads, 1) 
   pool_sync<CTAS>();      // no CTA leaves while another reads its shared memory
 }
 
-// Table entries of moved pages.  A page's word of the scratch is only good if
-// the move that it names is that page's.
+// Table entries of moved pages; bad entries are reported whether any page moves or
+// not.  A page's word of the scratch is only good if the move that it names is that
+// page's.
 __global__ void __launch_bounds__(256) remap_kernel(PagesCompactArgs a) {
   pdl_enter();
   if (timed_out_before(a.status)) return;
   const int n = *a.copy_count;
-  if (n == 0) return;
-  const int lowest = a.copy_src[n - 1];            // sources come highest first
+  const int lowest = n > 0 ? a.copy_src[n - 1] : a.num_pages;     // sources come highest first
   const long long entries = static_cast<long long>(a.batch) * a.max_pages;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll) {
     const int v = a.table[i];

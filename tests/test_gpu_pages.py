@@ -341,3 +341,18 @@ def test_write_at_rotates_by_the_given_positions(dtype):
     skipped = write(bad, expect=mla.MLA_DEV_BAD_OFFSETS)
     assert not skipped[0].view(sum(held), page, -1)[int(table[0, 15 // page]), 15 % page].any()
     assert torch.equal(skipped[1][2], q0.view(torch.int16)[2])
+
+
+@pytest.mark.parametrize("refs,limit", [([1, 1, 1, 0, 0], 9), ([1, 0, 1, 1, 0], 0), ([0, 0, 1, 1, 1], 9)])
+@pytest.mark.parametrize("bad", [5, 1 << 30, 0x7FFFFFFF])
+def test_compact_reports_bad_pages(refs, limit, bad):
+    """Whether pages move or not; the entry stays, what is good is done."""
+    refs = np.array(refs, np.int32)
+    table = np.concatenate([np.flatnonzero(refs), [-1, bad]])[None].astype(np.int32)
+    t, r, st = dev(table), dev(refs), status()
+    src, dst, n = dev(np.full(limit + 1, FILL)), dev(np.full(limit + 1, FILL)), dev([FILL])
+    ws, size = workspace(len(refs), 1)
+    mla.check(mla.mla_pages_compact(t, r, src, dst, n, limit, len(refs), 5, 1, ws, size, st))
+    moves = P.compact(table, refs, limit)
+    assert st.item() == mla.MLA_DEV_BAD_PAGE and n.item() == len(moves)
+    assert np.array_equal(t.cpu(), table) and np.array_equal(r.cpu(), refs)
