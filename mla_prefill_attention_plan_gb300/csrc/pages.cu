@@ -16,6 +16,7 @@
 // owns a contiguous range of page ids, so a scan costs one barrier, not one a
 // round.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 
@@ -704,19 +705,20 @@ static bool one_cta(int num_pages, int batch, int max_pages) {
 
 // Clusters of more than 8 CTAs have to be allowed, once a device and kernel.
 // (Two threads may both do it: it is the same call.)
-static cudaError_t allow_big_clusters(const void* kernel, bool (&allowed)[64]) {
+using DeviceFlags = std::atomic<bool>[64];
+static cudaError_t allow_big_clusters(const void* kernel, DeviceFlags& allowed) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && allowed[dev])) return e;
+  if (e != cudaSuccess || (dev < 64 && allowed[dev].load(std::memory_order_acquire))) return e;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+  if (e == cudaSuccess && dev < 64) allowed[dev].store(true, std::memory_order_release);
   return e;
 }
 
 cudaError_t launch_pages_reserve(const PagesReserveArgs& a, cudaStream_t stream) {
   if (one_cta(a.num_pages, a.batch, a.max_pages))
     return launch_pdl(reserve_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
-  static bool allowed[64];
+  static DeviceFlags allowed;
   cudaError_t e = allow_big_clusters(reinterpret_cast<const void*>(reserve_kernel<kPoolCtas>), allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(reserve_kernel<kPoolCtas>, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
@@ -727,7 +729,7 @@ cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t stream)
   if (one_cta(a.num_pages, 0, 0)) {
     e = launch_pdl(compact_kernel<1>, dim3(1), dim3(kPoolThreads), 0, stream, a);
   } else {
-    static bool allowed[64];
+    static DeviceFlags allowed;
     if ((e = allow_big_clusters(reinterpret_cast<const void*>(compact_kernel<kPoolCtas>), allowed)) != cudaSuccess)
       return e;
     e = launch_pdl(compact_kernel<kPoolCtas>, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);

@@ -356,3 +356,29 @@ def test_compact_reports_bad_pages(refs, limit, bad):
     moves = P.compact(table, refs, limit)
     assert st.item() == mla.MLA_DEV_BAD_PAGE and n.item() == len(moves)
     assert np.array_equal(t.cpu(), table) and np.array_equal(r.cpu(), refs)
+
+
+def test_calls_from_several_threads():
+    """Reservations and compactions of large pools (clusters of 16), each thread on a stream and a pool of its own."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    def one(i):
+        table, refs, lengths = state(9, 16, 8, 40000 + i, 70 + i, share=0.5)
+        lengths = lengths // 2
+        new = np.full(9, 20 + i)
+        new = np.minimum(new, 16 * 8 - lengths)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = run_reserve(table, refs, lengths, new, 16)
+            copies = P.reserve(table, refs, lengths, new, 16)
+            assert got[2] == copies and np.array_equal(got[0], table) and np.array_equal(got[1], refs)
+            t, r, st = dev(table), dev(refs), status()
+            src, dst, n = dev(np.full(99, FILL)), dev(np.full(99, FILL)), dev([FILL])
+            ws, size = workspace(len(refs), 9)
+            mla.check(mla.mla_pages_compact(t, r, src, dst, n, 99, len(refs), 8, 9, ws, size, st))
+            moves = P.compact(table, refs, 99)
+            assert st.item() == 0 and list(zip(src.tolist(), dst.tolist()))[:n.item()] == moves
+            assert np.array_equal(t.cpu(), table) and np.array_equal(r.cpu(), refs)
+        return i
+
+    with ThreadPoolExecutor(8) as threads:
+        assert list(threads.map(one, range(16))) == list(range(16))
