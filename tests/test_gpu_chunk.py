@@ -718,3 +718,128 @@ def test_more_tiles_than_are_counted(H, many):
     assert (out == FILL).all() and (lse == FILL).all()
     c.st.zero_()
     c.check()
+
+
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+def test_a_sink_that_is_no_number(value):
+    """No weights can be told: NaN, as in the definition, whether a row tile is split (the long context) or not."""
+    c = Case([2, 3] + [1] * 160, [20000, 9] + [40] * 160, 4, 64, sink=True)
+    c.sink[[0, 1, 50]] = value
+    c.make_buffers()
+    out, lse, slack = c.oracle()
+    mla.check(c.call())
+    bad = [0, 1, 2, 3, 4, 5 + 48]
+    assert np.isnan(out[bad]).all() and torch.isnan(c.out[bad]).all() and torch.isnan(c.lse[bad]).all()
+    c.out[bad], c.lse[bad] = FILL, FILL
+    lse[bad] = np.nan
+    c.compare(out, lse, slack)
+
+
+def exact_queries(H):
+    """(w_uk, projected): every latent column takes one of the 128 query values, with a sign, so that the projected
+    query is a bf16 number and no rounding of it is in a result."""
+    uk = np.zeros((H, 512, 128))
+    k = np.arange(512)
+    uk[:, k, k % 128] = np.where(k // 128 % 2, -1.0, 1.0)
+    return bf16(uk)
+
+
+class Ranked:
+    """Sequences of one token each that share their pages, in orders of their own: the keys' logits rise (or fall, or
+    go up and down by pages) by far more than a reference bears, many times within the tiles that a pair walks.
+
+    Logits are scale * q . (noise + at[j] u): the queries have u's direction in common.  The projected query is exact
+    (exact_queries), so that no rounding of it moves a logit; what is left are the weights' and the output's."""
+
+    def __init__(self, B, L, H, order, reach=40, page=64, seed=0, spikes=0.0):
+        rng = np.random.default_rng(seed)
+        self.B, self.L, self.H, self.page = B, L, H, page
+        pages = -(-(L + 1) // page)
+        base = rng.standard_normal(128)
+        lat = np.concatenate([base, -base, base, -base])
+        noise = rng.standard_normal((pages * page, 576))
+        at = np.linspace(-1, 1, pages * page) * reach / 192 ** -0.5 / np.linalg.norm(lat)
+        if spikes:
+            at[:] = 0.0
+            at[rng.choice(len(at), 6, replace=False)] = spikes * (1 - 0.1 * np.arange(6)) / 192 ** -0.5 / np.linalg.norm(lat)
+        noise[:, :512] += at[:, None] * lat / np.linalg.norm(lat)
+        self.kv_d, self.kv = bf16(noise)
+        rows = np.arange(pages)
+        self.table = np.stack([{"up": rows, "down": rows[::-1], "mixed": rng.permutation(pages)}[order] for _ in range(B)])
+        self.cached = rng.integers(L // 2, L + 1, B)
+        self.cached[0] = L
+        q = rng.standard_normal((B, H, 192)) * 0.1
+        q[..., :128] += base
+        self.q_d, self.q = bf16(q)
+        self.uk_d, self.uk = exact_queries(H)
+        self.uv_d, self.uv = bf16(rng.standard_normal((H, 128, 512)) * 512 ** -0.5)
+
+    def check(self):
+        B, H, scale = self.B, self.H, 192 ** -0.5
+        out = torch.full((B, H, 128), FILL, dtype=torch.bfloat16, device=DEV)
+        lse, st = torch.full((B, H), FILL, device=DEV), dev([0])
+        size = mla.mla_chunk_attention_workspace_bytes(B, H, B)
+        ws = torch.randint(0, 256, (size,), dtype=torch.uint8, device=DEV)
+        mla.check(mla.mla_chunk_attention(out, lse, self.q_d, dev(np.arange(B + 1)), dev(self.cached), self.kv_d,
+                                          dev(self.table), len(self.kv) // self.page, self.page, self.table.shape[1],
+                                          self.uk_d, self.uv_d, B, H, B, scale, workspace=ws, workspace_bytes=size,
+                                          d_status=st))
+        assert st.item() == 0
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        off, whole, heaviest = 0.0, 0.0, []
+        for b in range(B):
+            j = np.arange(self.cached[b] + 1)
+            c = self.kv[self.table[b, j // self.page] * self.page + j % self.page]
+            for h in range(H):
+                lat = self.uk[h] @ self.q[b, h, :128]
+                assert np.array_equal(lat, bf16(lat)[1])
+                s = scale * (c[:, :512] @ lat + c[:, 512:] @ self.q[b, h, 128:])
+                p = np.exp(s - s.max())
+                total = p.sum()
+                mix = p @ c[:, :512] / total
+                want = self.uv[h] @ mix
+                # Weights and output are off by 0.00165 each, independent of each other (see above); a weight's
+                # part goes by its own key.  A logit is off by at most fp32's 2^-23 of the terms' sizes in each of
+                # 36 steps of 16, and a quarter of that again in the exponent.
+                each = 0.00165 * np.sqrt(((p[:, None] * (c[:, :512] - mix)) ** 2).sum()) / total
+                fp32 = 45 * 2.0 ** -23 * scale * (np.abs(c[:, :512]) @ np.abs(lat)).max()
+                moved = fp32 * (p @ np.abs(c[:, :512] - mix)) / total
+                bound = 4 * (each + 0.00165 * np.linalg.norm(want)) + 2 * np.linalg.norm(moved)
+                miss = np.linalg.norm(out[b, h] - want)
+                assert miss <= bound, (b, h, miss, bound)
+                assert abs(lse[b, h] - s.max() - np.log(total)) <= fp32 + 2.0 ** -20 * (1 + abs(lse[b, h]))
+                off, whole = off + miss ** 2, whole + want @ want
+                heaviest.append(1 / total)
+        return np.sqrt(off / whole), np.array(heaviest)
+
+
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+@pytest.mark.parametrize("B,L", [(160, 2500), (80, 5000), (1, 40000)])
+def test_references_that_move_many_times(B, L, order):
+    """Whole row tiles that a pair walks alone, and one cut into many parts: no key is lost on the way."""
+    off, heaviest = Ranked(B, L, 2, order, reach=40 * max(1.0, L / 10000), seed=L).check()
+    assert off <= WHOLE and heaviest.max() < 0.9
+
+
+@pytest.mark.parametrize("order", ["up", "mixed"])
+@pytest.mark.parametrize("B,L", [(160, 2500), (1, 40000)])
+def test_a_key_that_takes_all_the_weight(B, L, order):
+    """A few keys 100 to 200 above all others and 20 apart: what comes before and behind the highest has no part in
+    the result."""
+    off, heaviest = Ranked(B, L, 2, order, seed=L, spikes=200.0).check()
+    assert off <= WHOLE and (heaviest > 0.999).all()
+
+
+@pytest.mark.parametrize("H", [129, 160, 256])
+def test_more_heads_than_a_row_tile_has_rows(H):
+    """A token's heads lie in two or three row tiles."""
+    Case([2, 3], [70, 400], H, 16, seed=H, sink=True).check()
+
+
+@pytest.mark.parametrize("mask", ["tree", "causal"])
+def test_contexts_on_shared_pages(mask):
+    """Samples of one prompt: 12 sequences hold its 47 full pages in common and one page of their own."""
+    c = Case([6] * 12, [3010] * 12, 16, 64, mask=mask)
+    c.table[:, :47] = c.table[0, :47]
+    c.make_buffers()
+    c.check()
