@@ -382,3 +382,94 @@ def test_calls_from_several_threads():
 
     with ThreadPoolExecutor(8) as threads:
         assert list(threads.map(one, range(16))) == list(range(16))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_a_walk_of_all_calls(seed):
+    """The pool under random calls in a row, each on what the one before left: tables, counts, lengths, lists and a
+    cache of two layers are the oracle's after every one, and each sequence's rows hold the tokens of its text."""
+    rng = np.random.default_rng(seed)
+    B, page, most = [(6, 4, 10), (24, 16, 7), (6, 1, 30), (40, 8, 12)][seed % 4]
+    pool = int(B * most * [0.4, 0.9][seed // 4]) + (40000 if seed == 5 else 0)        # (a pool that 16 CTAs look after)
+    table, refs, lengths = np.full((B, most), -1, np.int32), np.zeros(pool, np.int32), np.zeros(B, np.int64)
+    cache, text, word = np.zeros((2, pool * page), np.int32), [[] for _ in range(B)], 1
+    t, r, n, x, st = dev(table), dev(refs), dev(lengths), dev(cache), status()
+    src, dst, cnt = dev(np.zeros(pool)), dev(np.zeros(pool)), dev([0])
+    ws, size = workspace(pool, B)
+
+    def moved():
+        k = cnt.item()
+        return list(zip(src[:k].tolist(), dst[:k].tolist()))
+
+    def copies(limit):
+        mla.check(mla.mla_pages_copy(x, 4 * page, 2, 4 * page * pool, src, dst, cnt, limit, pool, st))
+
+    done = set()
+    for _ in range(40):
+        op = ["fork", "free", "compact", "reserve", "reserve", "draft", "draft"][rng.integers(7)]
+        expect = 0
+        if op == "fork":
+            parents = rng.integers(-1, B, B)
+            t2, n2 = dev(np.zeros((B, most))), dev(np.zeros(B))
+            mla.check(mla.mla_pages_fork(t2, n2, t, n, r, dev(parents), pool, most, B, B, st))
+            t, n = t2, n2
+            table, lengths = P.fork(table, lengths, refs, parents)
+            text = [list(text[p]) if p >= 0 else [] for p in parents]
+        elif op == "free":
+            keep = rng.integers(0, page * most, B)
+            mla.check(mla.mla_pages_free(t, r, n, dev(keep), pool, page, most, B, st))
+            P.free(table, refs, lengths, keep, page)
+            text = [w[:int(k)] for w, k in zip(text, lengths)]
+        elif op == "compact":
+            limit = int(rng.integers(0, 20))
+            mla.check(mla.mla_pages_compact(t, r, src, dst, cnt, limit, pool, most, B, ws, size, st))
+            copies(limit)
+            moves = P.compact(table, refs, limit)
+            P.copy(cache.reshape(2, pool, page), moves)
+            assert moved() == moves
+        else:
+            new = np.minimum(rng.integers(0, 9, B), page * most - lengths)
+            mla.check(mla.mla_pages_reserve(t, r, n, dev(new), src, dst, cnt, pool, page, most, B, ws, size, st))
+            copies(B)
+            moves = P.reserve(table, refs, lengths, new, page)
+            if moves is None:
+                expect, op = mla.MLA_DEV_NO_PAGES, "refused"
+                assert cnt.item() == 0
+            else:
+                P.copy(cache.reshape(2, pool, page), moves)
+                assert moved() == moves
+                # New tokens are written behind each sequence; of drafts, some are kept and what was reserved for the
+                # others goes back.
+                kept = []
+                for b in range(B):
+                    words = np.arange(word, word + new[b])
+                    word += int(new[b])
+                    at = lengths[b] + np.arange(new[b])
+                    cache[:, table[b, at // page] * page + at % page] = [words, -words]
+                    keeps = sorted(rng.choice(new[b], rng.integers(0, new[b] + 1), replace=False)) if op == "draft" else range(new[b])
+                    kept.append(list(keeps))
+                    text[b] += [int(words[k]) for k in keeps]
+                x.copy_(dev(cache))
+                counts = np.array([len(k) for k in kept])
+                if op == "draft":
+                    pad = np.full((B, 9), -1)
+                    for b, k in enumerate(kept):
+                        pad[b, :len(k)] = k
+                    mla.check(mla.mla_cache_keep_rows(x, 4, 2, 4 * page * pool, n, dev(pad), 9, dev(counts), t, pool, page,
+                                                      most, B, st))
+                    P.keep_rows(cache, lengths, kept, table, page)
+                n += dev(counts)
+                lengths = lengths + counts
+                if op == "draft":
+                    mla.check(mla.mla_pages_free(t, r, n, n, pool, page, most, B, st))
+                    P.free(table, refs, lengths, lengths, page)
+        done.add(op)
+        assert st.item() == expect
+        st.zero_()
+        assert np.array_equal(t.cpu(), table) and np.array_equal(r.cpu(), refs) and np.array_equal(n.cpu(), lengths)
+        assert np.array_equal(x.cpu(), cache)
+        for b in range(B):
+            at = np.arange(len(text[b]))
+            rows = table[b, at // page] * page + at % page
+            assert cache[0, rows].tolist() == text[b] and (cache[1, rows] == -cache[0, rows]).all()
+    assert {"fork", "free", "compact", "reserve", "draft"} <= done
