@@ -804,6 +804,9 @@ mla_status_t mla_latent_cache_write_at(void* kv_cache, void* q, const void* kv_l
  * asynchronous; what moves data are mla_pages_copy and mla_cache_keep_rows,
  * called once for each cache before the moved pages are used.
  * Arrays of a batch of 0 may be NULL.
+ * Sizes (pages, entries of a row, sequences, lengths of lists) of more than 2^31 -
+ * 65536 are MLA_ERR_ARG, for mla_pages_reserve also batch_size * max_pages_per_seq of
+ * 2^31 or more.
  * Tables whose rows hold a page twice, or counts that are not the number of
  * rows that hold a page, give tables and counts that mean nothing.
  *
@@ -983,7 +986,7 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  *            aligned; for one call at a time
  * Errors: host MLA_ERR_GEOMETRY (num_heads < 1), MLA_ERR_ARG (null or misaligned
  * pointers, bad sizes, more than 16379 heads, total_q_tokens * num_heads of 2^29
- * or more), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
+ * or more, more than 2^31 - 65536 sequences), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
  * (input_row_offsets[b+1] > total_q_tokens, more new tokens than 32 * mask_words
  * or a context of more than 2^31 - 8192: sequence b is left out; offsets that
  * decrease or do not begin at 0: all are, and so are those of a call of 2^31 - 1 or

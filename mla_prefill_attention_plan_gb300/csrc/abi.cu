@@ -3,6 +3,7 @@
 // point allocates memory or synchronises the stream.
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "kernels.cuh"
@@ -844,11 +845,20 @@ mla_status_t mla_index_select(int32_t* indices, int32_t* counts, const float* sc
 }
 
 // ------------------------------------------------------------------ pages
+// Loops over pages, entries, sequences and lists count in 32 bits and step past
+// their ends by up to 16 CTAs of threads.
+static bool counts_ok(std::initializer_list<int32_t> sizes) {
+  for (int32_t n : sizes)
+    if (n > 0x7FFFFFFF - 65535) return false;
+  return true;
+}
+
 mla_status_t mla_pages_fork(int32_t* dst_table, uint32_t* dst_lengths, const int32_t* src_table,
                             const uint32_t* src_lengths, int32_t* ref_counts, const int32_t* parents,
                             int32_t num_pages, int32_t max_pages_per_seq, int32_t dst_batch, int32_t src_batch,
                             int32_t* d_status, mla_stream_t stream) {
   if (!ref_counts || num_pages < 1 || max_pages_per_seq < 1 || dst_batch < 0 || src_batch < 0 ||
+      !counts_ok({num_pages, max_pages_per_seq, dst_batch, src_batch}) ||
       static_cast<int64_t>(dst_batch) + src_batch >= (1ll << 31) ||
       (dst_batch > 0 && (!dst_table || !dst_lengths || !parents)) || (src_batch > 0 && (!src_table || !src_lengths)))
     return MLA_ERR_ARG;
@@ -878,6 +888,7 @@ mla_status_t mla_pages_free(int32_t* page_table, int32_t* ref_counts, uint32_t* 
                             int32_t max_pages_per_seq, int32_t batch_size, int32_t* d_status,
                             mla_stream_t stream) {
   if (!ref_counts || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      !counts_ok({num_pages, max_pages_per_seq, batch_size}) ||
       (batch_size > 0 && (!page_table || !cache_lengths)))
     return MLA_ERR_ARG;
   mla::PagesFreeArgs a;
@@ -894,7 +905,7 @@ mla_status_t mla_pages_free(int32_t* page_table, int32_t* ref_counts, uint32_t* 
 }
 
 size_t mla_pages_workspace_bytes(int32_t num_pages, int32_t batch_size) {
-  if (num_pages < 1 || batch_size < 0) return 0;
+  if (num_pages < 1 || batch_size < 0 || !counts_ok({num_pages, batch_size})) return 0;
   return 4 * round_up(sizeof(int32_t) * static_cast<size_t>(num_pages), 256) +
          round_up(sizeof(int2) * static_cast<size_t>(batch_size), 256);
 }
@@ -904,7 +915,10 @@ mla_status_t mla_pages_reserve(int32_t* page_table, int32_t* ref_counts, const u
                                int32_t* copy_count, int32_t num_pages, int32_t page_size,
                                int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
                                size_t workspace_bytes, int32_t* d_status, mla_stream_t stream) {
+  // (The pages that are wanted, at most the table's entries, are counted in 32 bits.)
   if (!ref_counts || !copy_count || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      !counts_ok({num_pages, max_pages_per_seq, batch_size}) ||
+      static_cast<int64_t>(batch_size) * max_pages_per_seq >= (1ll << 31) ||
       (batch_size > 0 && (!page_table || !cache_lengths || !new_tokens || !copy_src || !copy_dst)))
     return MLA_ERR_ARG;
   if (!workspace || workspace_bytes < mla_pages_workspace_bytes(num_pages, batch_size) ||
@@ -938,6 +952,7 @@ mla_status_t mla_pages_compact(int32_t* page_table, int32_t* ref_counts, int32_t
                                int32_t max_pages_per_seq, int32_t batch_size, void* workspace,
                                size_t workspace_bytes, int32_t* d_status, mla_stream_t stream) {
   if (!ref_counts || !copy_count || max_copies < 0 || num_pages < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      !counts_ok({max_copies, num_pages, max_pages_per_seq, batch_size}) ||
       (max_copies > 0 && (!copy_src || !copy_dst)) || (batch_size > 0 && !page_table))
     return MLA_ERR_ARG;
   if (!workspace || workspace_bytes < mla_pages_workspace_bytes(num_pages, batch_size) ||
@@ -987,7 +1002,7 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
                                  int32_t* d_status, mla_stream_t stream) {
   if (!cache || row_bytes < 4 || row_bytes % 4 || row_bytes >= (1u << 31) || num_layers < 0 || num_layers > 65535 ||
       (reinterpret_cast<uintptr_t>(cache) & 3u) || layer_stride % 4 || keep_stride < 1 || num_pages < 1 ||
-      page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 ||
+      page_size < 1 || max_pages_per_seq < 1 || batch_size < 0 || !counts_ok({keep_stride, batch_size}) ||
       (batch_size > 0 && (!cache_lengths || !keep || !keep_counts || !page_table)) ||
       static_cast<int64_t>(num_pages) * page_size >= (1ll << 31) ||
       (num_layers > 1 && layer_stride < row_bytes * static_cast<size_t>(num_pages) * page_size))
@@ -1013,13 +1028,13 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
 // ------------------------------------------------------------------ chunk attention
 // Rows (token, head) are counted in 32 bits; and four CTAs a head and 17 more are
 // launched first, where a launch has 65535 rows of them.
-static bool chunk_sizes_ok(int32_t num_heads, int32_t total_q_tokens) {
-  return num_heads >= 1 && num_heads <= 16379 && total_q_tokens >= 0 &&
+static bool chunk_sizes_ok(int32_t batch_size, int32_t num_heads, int32_t total_q_tokens) {
+  return batch_size >= 1 && counts_ok({batch_size}) && num_heads >= 1 && num_heads <= 16379 && total_q_tokens >= 0 &&
          static_cast<long long>(total_q_tokens) * num_heads < (1ll << 31) / 4;
 }
 
 size_t mla_chunk_attention_workspace_bytes(int32_t batch_size, int32_t num_heads, int32_t total_q_tokens) {
-  if (batch_size < 1 || !chunk_sizes_ok(num_heads, total_q_tokens)) return 0;
+  if (!chunk_sizes_ok(batch_size, num_heads, total_q_tokens)) return 0;
   return mla::chunk_attn_workspace(batch_size, num_heads, total_q_tokens);
 }
 
@@ -1033,8 +1048,8 @@ mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uin
   if (num_heads < 1) return MLA_ERR_GEOMETRY;
   if (!out || !q || !input_row_offsets || !cache_lengths || !kv_cache || !page_table || !w_uk || !w_uv ||
       !aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
-      batch_size < 1 || num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
-      !chunk_sizes_ok(num_heads, total_q_tokens) || !(scale > 0.0f) ||
+      num_pages < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+      !chunk_sizes_ok(batch_size, num_heads, total_q_tokens) || !(scale > 0.0f) ||
       (chunk_mask ? mask_words < 1 : mask_words != 0) ||
       static_cast<long long>(num_pages) * page_size >= (1ll << 31) - 64)
     return MLA_ERR_ARG;

@@ -113,3 +113,9 @@ def test_closed_forms():
     np.testing.assert_allclose(out[1], x["w_uv"] @ c[:512])
     out, lse, _ = C.chunk_attention(**x, mask=[0, 2], sink=[0.25])
     assert not out[0].any() and np.allclose(lse[0], 0.25)
+
+
+def test_more_sequences_than_32_bits_step_over(lib):
+    for B in ((1 << 31) - 65535, (1 << 31) - 1):
+        assert call(B=B) == mla.MLA_ERR_ARG and mla.mla_chunk_attention_workspace_bytes(B, 4, 6) == 0
+    assert mla.mla_chunk_attention_workspace_bytes((1 << 31) - 65536, 4, 6) > 0

@@ -176,3 +176,26 @@ def test_oracle_keep_rows():
     P.keep_rows(cache, [5], [[0, 2, 3, 6]], np.array([[1, 0, 3]]), 8)
     # positions 5, 6, 7, 8 become what 5, 7, 8, 11 were: rows 13, 15, 0, 3
     assert cache[0, [13, 14, 15, 0]].tolist() == [13, 15, 0, 3]
+
+
+HUGE = (1 << 31) - 65535       # one more than a count may be: the kernels' loops step past their ends
+
+
+def test_sizes_that_32_bits_are_too_few_for(lib):
+    fork = _caller(mla.mla_pages_fork, "dt dl st sl rc par np mp db sb",
+                   [1 << 16, 1 << 17, 1 << 50, 1 << 51, 1 << 22, 1 << 23, 8, 8, 2, 3])
+    free = _caller(mla.mla_pages_free, "pt rc cl keep np ps mp b", [16, 16, 16, None, 8, 16, 4, 2])
+    reserve = _caller(mla.mla_pages_reserve, "pt rc cl new cs cd cc np ps mp b",
+                      [16, 16, 16, 16, 16, 16, 16, 8, 16, 4, 2], workspace=256, workspace_bytes=1 << 50)
+    compact = _caller(mla.mla_pages_compact, "pt rc cs cd cc most np mp b", [16, 16, 16, 16, 16, 8, 8, 4, 2],
+                      workspace=256, workspace_bytes=1 << 50)
+    keep = _caller(mla.mla_cache_keep_rows, "kv bytes layers stride cl keep ks kc pt np ps mp b",
+                   [16, 16, 2, 512, 16, 16, 4, 16, 16, 8, 4, 2, 2])
+    for call, names in ((fork, "np mp db sb"), (free, "np mp b"), (reserve, "np mp b"), (compact, "most np mp b"),
+                        (keep, "ks b")):
+        for name in names.split():
+            for size in (HUGE, (1 << 31) - 1):
+                assert call(**{name: size}) == mla.MLA_ERR_ARG, (call, name)
+    assert reserve(mp=1 << 20, b=1 << 11) == mla.MLA_ERR_ARG         # entries, and so the pages that may be wanted
+    assert mla.mla_pages_workspace_bytes(HUGE, 1) == 0 and mla.mla_pages_workspace_bytes(1, HUGE) == 0
+    assert mla.mla_pages_workspace_bytes(HUGE - 1, HUGE - 1) > 0
