@@ -420,6 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = mbar_wait(smem_u32(&sh->empty[u % kStages]), (u / kStages) & 1, status, abort_flag);
       }
       if (segments > 0) ok = ok && mbar_wait(smem_u32(&sh->q_free), (segments - 1) & 1, status, abort_flag);
+      if (rank == 1 && turn == 0) mbar_wait(smem_u32(&sh->drain), 0, status, &never);
       if (!ok) {      // loads that nobody waits for land long before this ends
         const uint64_t t0 = globaltimer();
         while (globaltimer() - t0 < 1000000ull) {
@@ -487,9 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++tile;
           }
         }
-        // The last arrival of this CTA's commits in either CTA.  (The other CTA waits
-        // for it when its softmax is through: a wait is for one step of the pipeline,
-        // never for as long as the call takes.)
+        // The last arrival of this CTA's commits in either CTA.  (A producer of the
+        // other CTA waits for it when it is through: a wait is for one step of the
+        // pipeline, never for as long as the call takes.)
         tc_commit_pair(smem_u32(&sh->drain), 3);
         mbar_wait(smem_u32(&sh->drain), 0, status, &never);
       }
@@ -871,7 +872,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (The next segment's first product is ordered behind these reads by the
       // arrival on p_full.)
     }
-    if (rank == 1 && warp == 2) mbar_wait_warp(smem_u32(&sh->drain), 0, status, &never);
   }
 
   tc_fence_before();
