@@ -27,8 +27,10 @@
 // and V are the same bytes needed in different halves (CTA r takes keys 128r..
 // of a tile for S, latent columns 128r.. of each 256 for O), so each CTA writes
 // and reads 147 KB and 131 KB a tile, and reads 74 KB of Q and twice 32 KB of P:
-// 5600 clk at 128 bytes a clk.  Measured: 64 tokens over 65536 keys, 128 heads, 775
-// us, 1510 TFLOP/s, 7050 clk a tile (a ring of 5, 6, 7 stages: 864, 804, 777 us).
+// 5600 clk at 128 bytes a clk.  Measured: 64 tokens over 65536 keys, 128 heads, 750
+// us, 1560 TFLOP/s, 6900 clk a tile (with a ring of 5 and 6 stages 11 and 3 % more);
+// 805 to 835 us in thousands of such calls, which run at the card's power limit and
+// 1700 to 1870 MHz.
 // Where a row tile is alone with its context, HBM's latency and the second read of
 // a tile from L2 come on top: 32 sequences of 8 tokens over 20000 keys, 16 heads,
 // 203 us for 740 MB, 4.6 us a tile; on pages of 16, whose tiles are 16 boxes, the
