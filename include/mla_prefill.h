@@ -985,16 +985,17 @@ mla_status_t mla_cache_keep_rows(void* cache, size_t row_bytes, int32_t num_laye
  * workspace: device memory of mla_chunk_attention_workspace_bytes(...), 256-byte
  *            aligned; for one call at a time
  * Errors: host MLA_ERR_GEOMETRY (num_heads < 1), MLA_ERR_ARG (null or misaligned
- * pointers, bad sizes, more than 16379 heads, total_q_tokens * num_heads of 2^29
- * or more, more than 2^31 - 65536 sequences), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.  Device MLA_DEV_BAD_OFFSETS
- * (input_row_offsets[b+1] > total_q_tokens, more new tokens than 32 * mask_words
- * or a context of more than 2^31 - 8192: sequence b is left out; offsets that
- * decrease or do not begin at 0: all are, and so are those of a call of 2^31 - 1 or
- * more tiles of 256 (token, head) rows of a sequence by 256 keys, or as many of the
- * up to 128 rows that a sequence has left over), MLA_DEV_BAD_PAGE (a context longer than
- * max_pages_per_seq pages: its sequence is left out; a missing page or an id out of
- * range: the result of its sequence is not meaningful), MLA_DEV_TIMEOUT.  Rows of out and lse of tokens outside every sequence, or of
- * one that is left out, are not written.
+ * pointers, bad sizes, more than 16379 heads, total_q_tokens * num_heads of 2^29 or
+ * more, more than 2^31 - 65536 sequences), MLA_ERR_WORKSPACE, MLA_ERR_LAUNCH.
+ * Device MLA_DEV_BAD_OFFSETS (input_row_offsets[b+1] > total_q_tokens, more new
+ * tokens than 32 * mask_words or a context of more than 2^31 - 8192: sequence b is
+ * left out; offsets that decrease or do not begin at 0: all are, and so are those
+ * of a call of 2^31 - 1 or more tiles of 256 (token, head) rows of a sequence by
+ * 256 keys, or as many of the up to 128 rows that a sequence has left over),
+ * MLA_DEV_BAD_PAGE (a context longer than max_pages_per_seq pages: its sequence is
+ * left out; a missing page or an id out of range: the result of its sequence is not
+ * meaningful), MLA_DEV_TIMEOUT. Rows of out and lse of tokens outside every
+ * sequence, or of one that is left out, are not written.
  */
 mla_status_t mla_chunk_attention(void* out, float* lse, const void* q, const uint32_t* input_row_offsets,
                                  const uint32_t* cache_lengths, const void* kv_cache, const int32_t* page_table,
